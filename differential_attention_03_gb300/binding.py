@@ -10,6 +10,7 @@ module raises on first use: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -123,6 +124,31 @@ def lib() -> ctypes.CDLL:
             L.diffattn_v2_layer_workspace.restype = ctypes.c_size_t
             L.diffattn_v2_layer_forward.argtypes = [i, i, i, i, i, i, vp, vp, vp, i, vp, vp, ctypes.c_size_t, vp]
             L.diffattn_v2_layer_forward.restype = i
+            d_ = ctypes.c_double
+            L.diffattn_rope_init.argtypes = [vp, i, i, d_, i, d_, i, d_, d_]
+            L.diffattn_rope_init.restype = i
+            L.diffattn_rope_from_frequencies.argtypes = [vp, i, i, vp, f]
+            L.diffattn_rope_from_frequencies.restype = i
+            L.diffattn_rope.argtypes = [i, i, i, i, i, vp, vp, vp, vp, i, vp, vp]
+            L.diffattn_rope.restype = i
+            L.diffattn_cache_append.argtypes = [i, i, i, i, i, i] + [vp] * 14 + [f, f] + [vp] * 4
+            L.diffattn_cache_append.restype = i
+            L.diffattn_v2_cache_append.argtypes = [i, i, i, i, i, i, i] + [vp] * 10 + [f] + [vp] * 3
+            L.diffattn_v2_cache_append.restype = i
+            L.diffattn_cache_keep.argtypes = [i, i, i, i, i, i] + [vp] * 11
+            L.diffattn_cache_keep.restype = i
+            L.diffattn_v2_cache_keep.argtypes = [i, i, i, i, i, i] + [vp] * 9
+            L.diffattn_v2_cache_keep.restype = i
+            L.diffattn_tree_decode_workspace.argtypes = [i, i, i, i]
+            L.diffattn_tree_decode_workspace.restype = sz
+            L.diffattn_tree_decode.argtypes = [i, i, i, i, i, i, vp, vp, vp, vp, f, f, vp, vp, vp, vp, vp, vp, vp, ll,
+                                               vp, f, vp, f, vp, vp, sz, vp]
+            L.diffattn_tree_decode.restype = i
+            L.diffattn_v2_tree_decode_workspace.argtypes = [i, i, i, i, i]
+            L.diffattn_v2_tree_decode_workspace.restype = sz
+            L.diffattn_v2_tree_decode.argtypes = [i, i, i, i, i, i, i, vp, vp, f, vp, vp, vp, vp, vp, vp, ll, vp, ll,
+                                                  ll, f, vp, vp, sz, vp]
+            L.diffattn_v2_tree_decode.restype = i
             L.diffattn_device_status.argtypes = [vp]
             L.diffattn_device_status.restype = i
             L.diffattn_bounds_checked.argtypes = []
@@ -826,6 +852,357 @@ def v2_layer_forward(x, w_qkvl, w_o, Hq: int, Hkv: int, causal: bool = True, out
     wp, wn = _ws_args(workspace, need)
     _check(lib().diffattn_v2_layer_forward(B, n, D, Hq, Hkv, d, _ptr(x), _ptr(w_qkvl), _ptr(w_o),
                                            1 if causal else 0, _ptr(out), wp, wn, _stream(stream)))
+    return out
+
+
+# ----------------------------------------------------------------------------- positions and caches
+class RopeSpec(ctypes.Structure):
+    """A rotation, as rope_spec or rope_from_frequencies makes it (immutable: they are shared)."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("mult", ctypes.c_float),
+                ("turns", ctypes.c_ulonglong * 64)]
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+@functools.lru_cache(maxsize=256)
+def rope_spec(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_context: int = 0, beta_fast: float = 32.0,
+              beta_slow: float = 1.0) -> RopeSpec:
+    """Rotary positions on the first rot_dim channels of a head: theta_i = base^(-2i / rot_dim), scaled.
+
+    interleaved: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2).  scaling: "none", "linear"
+    (theta / factor), "ntk" (base factor^(rot_dim / (rot_dim - 2))) or "yarn" (between the two, by the
+    turns a pair makes over original_context positions; the rotated values times 0.1 ln(factor) + 1).
+    Host only.
+    """
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    spec = RopeSpec()
+    _check(lib().diffattn_rope_init(ctypes.byref(spec), rot_dim, 1 if interleaved else 0, base, ROPE_SCALINGS[scaling],
+                                    factor, original_context, beta_fast, beta_slow))
+    return spec
+
+
+def rope_from_frequencies(frequencies, interleaved: bool = False, mult: float = 1.0) -> RopeSpec:
+    """A rotation of 2 len(frequencies) channels by frequencies of the caller's own (radians per position)."""
+    fr = [float(x) for x in frequencies]
+    spec = RopeSpec()
+    _check(lib().diffattn_rope_from_frequencies(ctypes.byref(spec), 2 * len(fr), 1 if interleaved else 0,
+                                                (ctypes.c_double * max(1, len(fr)))(*fr), mult))
+    return spec
+
+
+def _on(t, name, dtype, shape, dev):
+    """_need, on the device `dev` (an index), which has to be the current one."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, dtype, shape)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+
+
+def _current(t, name) -> int:
+    """The device index of t, which has to be the current device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def rope(tensors, spec: RopeSpec, positions=None, inverse: bool = False, out=None, stream=None) -> list:
+    """Rotary positions on up to four tensors [B, n, heads, d] (bf16 or fp32, d <= 128) in one kernel.
+
+    positions: int32 [B, n] or None (token t at position t).  inverse: the rotation by the negative
+    angles, which is also the backward pass: the gradients of the unrotated tensors from those of the
+    rotated ones.  out: None or tensors like the inputs, each allowed to be its own input (in place).
+    Returns the list of rotated tensors.
+    """
+    xs = list(tensors)
+    if not xs:
+        return []
+    if len(xs) > 4:
+        raise ValueError(f"at most 4 tensors a call, got {len(xs)}")
+    dev = _current(xs[0], "tensors[0]")
+    B, n, _, d = xs[0].shape
+    dt = xs[0].dtype
+    for k, x in enumerate(xs):
+        _on(x, f"tensors[{k}]", dt, (B, n, x.shape[2] if x.dim() == 4 else -1, d), dev)
+    if positions is not None:
+        _on(positions, "positions", torch.int32, (B, n), dev)
+    if out is None:
+        out = [torch.empty_like(x) for x in xs]
+    else:
+        out = list(out)
+        if len(out) != len(xs):
+            raise ValueError(f"out must hold {len(xs)} tensors, got {len(out)}")
+        for k, (x, o) in enumerate(zip(xs, out)):
+            _on(o, f"out[{k}]", dt, x.shape, dev)
+    m = len(xs)
+    _check(lib().diffattn_rope(_dt(xs[0]), B, n, d, m, (ctypes.c_void_p * m)(*[x.data_ptr() for x in xs]),
+                               (ctypes.c_int * m)(*[x.shape[2] for x in xs]), ctypes.byref(spec), _ptr(positions),
+                               1 if inverse else 0, (ctypes.c_void_p * m)(*[o.data_ptr() for o in out]),
+                               _stream(stream)))
+    return out
+
+
+CACHE_FORMATS = {"bf16": 0, "fp8k": 1, "fp8": 2}
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class KVCache:
+    """A key/value cache: V1 (k1, k2 [B, n, H, d], v [B, n, H, 2d]) or, with k2 None, V2 (k1, v [B, n, Hkv, d]).
+
+    fmt: "bf16"; "fp8k" (e4m3 keys, one scale a tensor: k1_scale, k2_scale; bf16 values); "fp8" (e4m3
+    keys and values, fp32 scales a row: k1_scales, k2_scales, v_scales [B, H, n]).  e4m3 tensors are
+    torch.float8_e4m3fn or their bytes as torch.uint8.  cache_v1 and cache_v2 allocate one.
+    """
+
+    __slots__ = ("fmt", "code", "k1", "k2", "v", "k1_scale", "k2_scale", "k1_scales", "k2_scales", "v_scales", "B", "n",
+                 "H", "d", "dev")
+
+    def __init__(self, fmt, k1, k2, v, k1_scale: float = 1.0, k2_scale: float = 1.0, k1_scales=None, k2_scales=None,
+                 v_scales=None):
+        if fmt not in CACHE_FORMATS:
+            raise ValueError(f"the cache format must be one of {sorted(CACHE_FORMATS)}, got {fmt!r}")
+        if not k1.is_cuda:
+            raise ValueError("k1 must be a CUDA tensor")
+        self.fmt, self.code = fmt, CACHE_FORMATS[fmt]
+        self.B, self.n, self.H, self.d = B, n, H, d = k1.shape
+        self.dev = dev = k1.get_device()
+        kt, vt = (torch.bfloat16 if fmt == "bf16" else k1.dtype), (v.dtype if fmt == "fp8" else torch.bfloat16)
+        if (fmt != "bf16" and kt not in _CODES) or (fmt == "fp8" and vt not in _CODES):
+            raise ValueError("e4m3 tensors must be torch.float8_e4m3fn or torch.uint8")
+        _on(k1, "k1", kt, (B, n, H, d), dev)
+        if k2 is not None:
+            _on(k2, "k2", kt, (B, n, H, d), dev)
+        _on(v, "v", vt, (B, n, H, d if k2 is None else 2 * d), dev)
+        if fmt == "fp8":
+            for name, x, want in (("k1_scales", k1_scales, True), ("k2_scales", k2_scales, k2 is not None),
+                                  ("v_scales", v_scales, True)):
+                if want:
+                    if x is None:
+                        raise ValueError(f"an fp8 cache needs {name}")
+                    _on(x, name, torch.float32, (B, H, n), dev)
+        self.k1, self.k2, self.v = k1, k2, v
+        self.k1_scale, self.k2_scale = float(k1_scale), float(k2_scale)
+        self.k1_scales, self.k2_scales, self.v_scales = k1_scales, k2_scales, v_scales
+
+
+def _new_cache(B, n, H, d, dv, two, fmt, device, scales):
+    if fmt not in CACHE_FORMATS:
+        raise ValueError(f"the cache format must be one of {sorted(CACHE_FORMATS)}, got {fmt!r}")
+    kt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    vt = torch.float8_e4m3fn if fmt == "fp8" else torch.bfloat16
+
+    def sc(want=True):
+        return torch.zeros((B, H, n), device=device, dtype=torch.float32) if fmt == "fp8" and want else None
+    return KVCache(fmt, torch.zeros((B, n, H, d), device=device, dtype=kt),
+                   torch.zeros((B, n, H, d), device=device, dtype=kt) if two else None,
+                   torch.zeros((B, n, H, dv), device=device, dtype=vt), *scales, sc(), sc(two), sc())
+
+
+def cache_v1(B: int, n: int, H: int, d: int, fmt: str = "bf16", device="cuda", k1_scale: float = 1.0,
+             k2_scale: float = 1.0) -> KVCache:
+    """An empty V1 cache of n tokens a sequence."""
+    return _new_cache(B, n, H, d, 2 * d, True, fmt, device, (k1_scale, k2_scale))
+
+
+def cache_v2(B: int, n: int, Hkv: int, d: int, fmt: str = "bf16", device="cuda", k_scale: float = 1.0) -> KVCache:
+    """An empty V2 cache of n tokens a sequence."""
+    return _new_cache(B, n, Hkv, d, d, False, fmt, device, (k_scale, 1.0))
+
+
+def _need_kind(cache, two):
+    if (cache.k2 is not None) != two:
+        raise ValueError("a V1 cache (k1 and k2) is needed" if two else "a V2 cache (one key tensor) is needed")
+    if cache.dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on device {cache.dev}, the current device is {torch.cuda.current_device()}")
+
+
+def _int32(t, name, shape, dev):
+    if t is None:
+        return None
+    _on(t, name, torch.int32, shape, dev)
+    return t.data_ptr()
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def cache_append(cache: KVCache, k1, k2, v, q1=None, q2=None, rope=None, positions=None, lens=None, ntok=None,
+                 q1_out=None, q2_out=None, stream=None):
+    """Write T new tokens a sequence into a V1 cache: keys rotated and quantised, values quantised, queries rotated.
+
+    k1, k2 (and q1, q2, or both None): bf16 [B, T, H, d]; v: [B, T, H, 2d].  rope: a RopeSpec or None;
+    positions: int32 [B, T] or None (the cache row).  lens: int32 [B], the first row written (None: 0);
+    ntok: int32 [B] tokens a sequence (None: T; later ones leave the cache as it is and give zero
+    queries).  Returns (q1_out, q2_out), the rotated queries (None without queries).
+    """
+    _need_kind(cache, True)
+    B, T, H, d = k1.shape
+    dev, bf = cache.dev, torch.bfloat16
+    if (B, H, d) != (cache.B, cache.H, cache.d):
+        raise ValueError(f"keys {tuple(k1.shape)} do not fit a cache of B={cache.B}, H={cache.H}, d={cache.d}")
+    shp = (B, T, H, d)
+    _on(k1, "k1", bf, shp, dev)
+    _on(k2, "k2", bf, shp, dev)
+    _on(v, "v", bf, (B, T, H, 2 * d), dev)
+    if (q1 is None) != (q2 is None):
+        raise ValueError("q1 and q2 come together")
+    if q1 is not None:
+        _on(q1, "q1", bf, shp, dev)
+        _on(q2, "q2", bf, shp, dev)
+        q1_out = torch.empty_like(q1) if q1_out is None else q1_out
+        q2_out = torch.empty_like(q2) if q2_out is None else q2_out
+        _on(q1_out, "q1_out", bf, shp, dev)
+        _on(q2_out, "q2_out", bf, shp, dev)
+    _check(lib().diffattn_cache_append(
+        cache.code, B, T, H, cache.n, d, _addr(q1), _addr(q2), k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
+        None if rope is None else ctypes.byref(rope), _int32(positions, "positions", (B, T), dev),
+        _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(q1_out), _addr(q2_out),
+        cache.k1.data_ptr(), cache.k2.data_ptr(), cache.v.data_ptr(), cache.k1_scale, cache.k2_scale,
+        _addr(cache.k1_scales), _addr(cache.k2_scales), _addr(cache.v_scales), _stream(stream)))
+    return None if q1 is None else (q1_out, q2_out)
+
+
+def v2_cache_append(cache: KVCache, k, v, q=None, rope=None, positions=None, lens=None, ntok=None, q_out=None,
+                    stream=None):
+    """cache_append for a V2 cache: k, v bf16 [B, T, Hkv, d]; q [B, T, Hq, d] or None.  Returns q_out."""
+    _need_kind(cache, False)
+    B, T, H, d = k.shape
+    dev, bf = cache.dev, torch.bfloat16
+    if (B, H, d) != (cache.B, cache.H, cache.d):
+        raise ValueError(f"keys {tuple(k.shape)} do not fit a cache of B={cache.B}, Hkv={cache.H}, d={cache.d}")
+    _on(k, "k", bf, (B, T, H, d), dev)
+    _on(v, "v", bf, (B, T, H, d), dev)
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[2]
+        _on(q, "q", bf, (B, T, Hq, d), dev)
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _on(q_out, "q_out", bf, (B, T, Hq, d), dev)
+    _check(lib().diffattn_v2_cache_append(
+        cache.code, B, T, Hq, H, cache.n, d, _addr(q), k.data_ptr(), v.data_ptr(),
+        None if rope is None else ctypes.byref(rope), _int32(positions, "positions", (B, T), dev),
+        _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(q_out), cache.k1.data_ptr(),
+        cache.v.data_ptr(), cache.k1_scale, _addr(cache.k1_scales), _addr(cache.v_scales), _stream(stream)))
+    return None if q is None else q_out
+
+
+def cache_keep(cache: KVCache, lens, path, nkeep, new_lens=None, stream=None) -> torch.Tensor:
+    """Move the rows of each accepted path's nodes to the front of the drafted rows, in place.
+
+    Row lens[b] + path[b, i] moves to row lens[b] + i for i < nkeep[b]; path: int32 [B, A], ascending
+    node numbers, A <= 64; lens, nkeep: int32 [B].  Works on V1 and V2 caches.  Returns new_lens,
+    int32 [B]: lens plus the nodes kept.
+    """
+    _need_kind(cache, cache.k2 is not None)
+    B, dev = cache.B, cache.dev
+    if path.dim() != 2:
+        raise ValueError(f"path must be [B, A], got {tuple(path.shape)}")
+    A = path.shape[1]
+    if new_lens is None:
+        new_lens = torch.empty_like(lens)
+    a = (_int32(lens, "lens", (B,), dev), _int32(path, "path", (B, A), dev), _int32(nkeep, "nkeep", (B,), dev),
+         _int32(new_lens, "new_lens", (B,), dev), _stream(stream))
+    if cache.k2 is not None:
+        _check(lib().diffattn_cache_keep(
+            cache.code, B, A, cache.H, cache.n, cache.d, cache.k1.data_ptr(), cache.k2.data_ptr(), cache.v.data_ptr(),
+            _addr(cache.k1_scales), _addr(cache.k2_scales), _addr(cache.v_scales), *a))
+    else:
+        _check(lib().diffattn_v2_cache_keep(
+            cache.code, B, A, cache.H, cache.n, cache.d, cache.k1.data_ptr(), cache.v.data_ptr(),
+            _addr(cache.k1_scales), _addr(cache.v_scales), *a))
+    return new_lens
+
+
+def tree_decode_workspace_bytes(B: int, T: int, H: int, d: int) -> int:
+    """Device workspace of tree_decode (partial softmax states)."""
+    return int(lib().diffattn_tree_decode_workspace(B, T, H, d))
+
+
+def v2_tree_decode_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().diffattn_v2_tree_decode_workspace(B, T, Hq, Hkv, d))
+
+
+def _tree_args(lens, ntok, mask, B, T, dev):
+    sb = 0
+    if mask is not None:
+        if mask.dim() == 2:
+            _on(mask, "mask", torch.int64, (B, T), dev)
+            sb = T
+        else:
+            _on(mask, "mask", torch.int64, (T,), dev)
+    return _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(mask), sb
+
+
+def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=None, eps: float = 1e-5, lens=None,
+                ntok=None, mask=None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """DIFF V1 attention of T <= 64 drafted tokens a sequence over a cache that already holds their keys and values.
+
+    q1, q2: bf16 [B, T, H, d].  lens: int32 [B] keys before the drafts (None: n - T), which every
+    token sees; the drafts are rows lens[b] .. lens[b] + ntok[b] - 1 (ntok: int32 [B] or None: T).
+    mask: int64 words [B, T] or [T], bit u of word t: token t sees draft u; None: a chain (u <= t).
+    T = 1 is a plain decode step.  lam, gamma, eps: as for diffattn_decode.  workspace: a device tensor
+    of tree_decode_workspace_bytes(B, T, H, d) bytes (allocated here if None).  Returns out
+    [B, T, H, 2d] bf16; tokens from ntok[b] on, and tokens that see nothing, are zeros.
+    """
+    _need_kind(cache, True)
+    B, T, H, d = q1.shape
+    dev, bf = cache.dev, torch.bfloat16
+    if (B, H, d) != (cache.B, cache.H, cache.d):
+        raise ValueError(f"queries {tuple(q1.shape)} do not fit a cache of B={cache.B}, H={cache.H}, d={cache.d}")
+    _on(q1, "q1", bf, (B, T, H, d), dev)
+    _on(q2, "q2", bf, (B, T, H, d), dev)
+    _on(lam, "lambda", torch.float32, (1,), dev)
+    if gamma is not None:
+        _on(gamma, "gamma", torch.float32, (2 * d,), dev)
+    a = _tree_args(lens, ntok, mask, B, T, dev)
+    if out is None:
+        out = torch.empty((B, T, H, 2 * d), device=q1.device, dtype=bf)
+    _on(out, "out", bf, (B, T, H, 2 * d), dev)
+    need = tree_decode_workspace_bytes(B, T, H, d)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q1.device)
+    wp, wn = _ws_args(workspace, need)
+    _check(lib().diffattn_tree_decode(
+        cache.code, B, T, H, cache.n, d, q1.data_ptr(), q2.data_ptr(), cache.k1.data_ptr(), cache.k2.data_ptr(),
+        cache.k1_scale, cache.k2_scale, _addr(cache.k1_scales), _addr(cache.k2_scales), cache.v.data_ptr(),
+        _addr(cache.v_scales), *a, lam.data_ptr(), lambda_init_value, _addr(gamma), eps, out.data_ptr(), wp, wn,
+        _stream(stream)))
+    return out
+
+
+def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=None, softmax_scale: float = 0.0,
+                   out=None, workspace=None, stream=None) -> torch.Tensor:
+    """tree_decode for DIFF V2: q bf16 [B, T, Hq, d]; lam_logits fp32 [B, T, Hq/2], [B, Hq/2] or [Hq/2].
+
+    workspace: v2_tree_decode_workspace_bytes(B, T, Hq, Hkv, d) bytes.  Returns out [B, T, Hq/2, d].
+    """
+    _need_kind(cache, False)
+    B, T, Hq, d = q.shape
+    dev, bf, G = cache.dev, torch.bfloat16, Hq // 2
+    if (B, d) != (cache.B, cache.d):
+        raise ValueError(f"queries {tuple(q.shape)} do not fit a cache of B={cache.B}, d={cache.d}")
+    _on(q, "q", bf, (B, T, Hq, d), dev)
+    sb, st = (T * G, G) if lam_logits.dim() == 3 else (G, 0) if lam_logits.dim() == 2 else (0, 0)
+    _on(lam_logits, "lam_logits", torch.float32, ((B, T, G), (B, G), (G,))[3 - lam_logits.dim()]
+        if 1 <= lam_logits.dim() <= 3 else (B, T, G), dev)
+    a = _tree_args(lens, ntok, mask, B, T, dev)
+    if out is None:
+        out = torch.empty((B, T, G, d), device=q.device, dtype=bf)
+    _on(out, "out", bf, (B, T, G, d), dev)
+    need = v2_tree_decode_workspace_bytes(B, T, Hq, cache.H, d)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    wp, wn = _ws_args(workspace, need)
+    _check(lib().diffattn_v2_tree_decode(
+        cache.code, B, T, Hq, cache.H, cache.n, d, q.data_ptr(), cache.k1.data_ptr(), cache.k1_scale,
+        _addr(cache.k1_scales), cache.v.data_ptr(), _addr(cache.v_scales), *a, lam_logits.data_ptr(), sb, st,
+        float(softmax_scale), out.data_ptr(), wp, wn, _stream(stream)))
     return out
 
 

@@ -22,6 +22,7 @@
 #include "decode.cuh"
 #include "gemm_params.h"
 #include "diffattn.h"
+#include "host.h"
 #include "launch.h"
 
 // Device status word (one per device that loads the library).  Kernels record
@@ -2145,3 +2146,15 @@ diffattn_status diffattn_debug_wait_timeout(long long budget_ns, void* stream) {
 long long diffattn_launch_count(void) { return g_launches.load(); }
 
 }  // extern "C"
+
+// What other translation units' entry points use of this one.
+namespace da {
+namespace host {
+diffattn_status error(diffattn_status s, const char* msg) { return fail(s, "%s", msg); }
+diffattn_status success() { return ok(); }
+diffattn_status status_address(int** out) { return status_word(out); }
+int sms() { return sm_count(); }
+void count_launches(int k) { g_launches.fetch_add(k); }
+diffattn_status encoder(EncodeTiled* fn) { return get_encoder(fn); }
+}  // namespace host
+}  // namespace da

@@ -1,0 +1,923 @@
+// Attention of drafted tokens over a key/value cache (tcgen05 tensor cores,
+// TMA, mbarriers; sm_103a): up to 64 new tokens of a sequence, the nodes of a
+// draft tree, against its cached keys.
+//
+// What it computes, for sequence b with L = lens[b] committed keys and the
+// keys of its nt drafted tokens in cache rows L .. L + nt - 1:
+//   token t sees key j  iff  j < L, or j = L + u with u < nt and bit u of its mask word
+//   O_r = sum_j softmax_j(q_r . k_r[j] / sqrt d) v[j] over the keys it sees,   r = 1, 2
+//   V1: out = (1 - lambda_init) gamma (O_1 - lambda O_2) / rms(O_1 - lambda O_2)
+//   V2: out = O_1 - sigmoid(logit) O_2   (q_1, q_2 the query heads of a pair over one key head)
+// A token that sees no key, or t >= nt, gets zeros.  One token is nt = 1.
+//
+// Rows.  A work unit is (sequence, key head, row tile); its 128 MMA rows are
+// map 1's rows 0 .. 63 and map 2's 64 .. 127 (row = pair * T + token, pairs of
+// a key head packed while they fit).  V1's maps have their own keys: the
+// score tile is the sum of two MMAs whose A operands are [Q_1; 0] and
+// [0; Q_2], windows of one shared buffer Q_1 | zeros | Q_2, so both maps'
+// scores land stacked in one accumulator and one P V MMA serves both maps:
+// each key and value byte is read once.  The half of the score MMAs that
+// multiplies zeros is free, as HBM bounds the kernel: 128 keys of bf16 V1 at
+// d = 128 are 128 KB, 5600 cycles of this SM's share of HBM, against 3072
+// cycles of MMA.
+//
+// Formats.  bf16; FP8K: e4m3 keys with one scale a tensor, bf16 values; FP8:
+// e4m3 keys and values with an fp32 scale a row.  8-bit operands are not
+// converted: the query row is scaled by a power of two and split into two e4m3
+// terms (hi + lo holds a bf16 value's eight bits), and so is P, at twice the
+// MMA rate.  A key's scale multiplies its scores; a value row's scale is
+// folded into P before the split, and the reference maximum is that of score
+// + log2(value scale), so that the largest contribution, not the largest
+// weight, sits at the top of e4m3's range (a key with a large weight and a
+// small value row would otherwise push every other weight towards e4m3's
+// absolute floor).
+//
+// Split.  The key tiles (128 keys) of all units form one line that is dealt
+// out evenly, a contiguous range to each CTA, from the lengths on the device;
+// a CTA writes one partial state (maximum, sum, unnormalised O) a unit it
+// touches, and tree_combine_kernel merges a unit's states and finishes the
+// rows.  So a ragged batch, one long sequence and many short ones all keep
+// every SM streaming.
+//
+// Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 score
+// MMAs; warp 2 P V MMAs; warp 3 value and key scales (FP8); warps 4-11
+// softmax, two warps per lane quarter, each half of a tile's key columns
+// (quarters without rows sleep).  TMEM: O, then two score tiles, in which P
+// replaces the scores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "cache_params.h"
+#include "ptx.cuh"
+
+#undef DA_BOUNDS_FILE
+#define DA_BOUNDS_FILE 12
+
+namespace da {
+
+template <int D, bool V2, int FMT>
+struct TreeCfg {
+  static constexpr bool K8 = FMT != kCacheBf16, V8 = FMT == kCacheFp8;
+  static constexpr int BN = 128;              // keys of a tile
+  static constexpr int DV = V2 ? D : 2 * D;
+  static constexpr int NMAP_K = V2 ? 1 : 2;   // key tensors
+  static constexpr int NTERM = K8 ? 2 : 1;    // terms of a query row
+  static constexpr int KROW = D * (K8 ? 1 : 2);         // bytes of a key row
+  static constexpr int KBOXB = KROW < 128 ? KROW : 128;  // bytes of a key box row (its swizzle width)
+  static constexpr int KBOX = KROW / KBOXB;
+  static constexpr int VROW = DV * (V8 ? 1 : 2);
+  static constexpr int VBOX = VROW / 128;
+  static constexpr int VKEYS = 64;  // keys of a value slot
+  static constexpr int K_SLOT = BN * KROW, V_SLOT = VKEYS * VROW;
+  static constexpr int QROWS = V2 ? 128 : 192;          // Q_even | Q_odd, or Q_1 | zeros | Q_2
+  static constexpr int Q_TERM = QROWS * KROW;
+  static constexpr int Q_BYTES = NTERM * Q_TERM;
+  // Rings: about 160-176 KB in flight, split between keys and values.
+  static constexpr int NK = (!V2 && D == 128) ? (K8 ? 4 : 2) : (!V2) ? (K8 ? (V8 ? 10 : 8) : 5) : (K8 ? 5 : 3);
+  static constexpr int NV = (!V2 && D == 128) ? (V8 ? 6 : 3) : (!V2) ? (V8 ? 12 : (K8 ? 7 : 6)) : (V8 ? 11 : (K8 ? 6 : 5));
+  static constexpr int NS = 4;  // scale buffers (FP8)
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = Q_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * K_SLOT;
+  static constexpr int OFF_SC = OFF_V + NV * V_SLOT;           // float [NS][4][128]: key scales 1, 2, value scales, log2 of them
+  static constexpr int OFF_XM = OFF_SC + (V8 ? NS * 4 * 128 * 4 : 0);  // float [2 tiles][2 halves][128]
+  static constexpr int OFF_XL = OFF_XM + 4 * 128 * 4;          // float [2 segments][128] row sums of half 1
+  static constexpr int OFF_QI = OFF_XL + 2 * 128 * 4;          // float [128]: inverse of the query row's power of two
+  static constexpr int OFF_BARS = OFF_QI + 128 * 4;
+  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NS + 2 + 2 + 2 + 1 + 2;
+  static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 256 + 1024;
+  static constexpr uint32_t TM_O = 0, TM_S = DV;  // two score tiles of BN columns
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr int QK_STEPS = KROW / 32;
+  static constexpr uint32_t IDESC_QK = K8 ? idesc_e4m3(128, BN) : idesc_bf16(128, BN, false, false);
+  static constexpr uint32_t IDESC_PV = V8 ? (idesc_e4m3(128, DV) | (1u << 16)) : idesc_bf16(128, DV, false, true);
+  static constexpr int NTHREADS = 384;
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+  static_assert(DV + 2 * BN <= 512, "tensor memory");
+  static_assert(K_SLOT % 1024 == 0 && V_SLOT % 1024 == 0 && Q_TERM % 1024 == 0, "swizzled boxes start on 1 KB");
+};
+
+constexpr float kTreeRescaleLog2 = 8.f;   // bf16 P: how far a score may exceed the reference maximum
+constexpr float kTreeTopLog2 = 7.f;       // e4m3 P: the reference maximum sits at 2^7 (e4m3 ends at 448) ...
+constexpr float kTreeRescale8Log2 = 1.f;  // ... and may be exceeded by a factor of two
+
+// A sequence's committed keys, its drafted tokens, the end of its keys and its tiles.
+struct TreeLen {
+  int L, nt, end, tiles;
+};
+__device__ __forceinline__ TreeLen tree_len(const TreeParams& p, int b) {
+  TreeLen x;
+  x.L = max(0, min(p.lens ? p.lens[b] : p.n - p.T, p.n));
+  x.nt = max(0, min(p.ntok ? p.ntok[b] : p.T, p.T));
+  x.end = min(p.n, x.L + x.nt);
+  x.tiles = (x.end + 127) >> 7;
+  return x;
+}
+
+// Tiles of all sequences before `upto` and of all of them, per unit of a
+// sequence (each has the same units), by the whole CTA; scratch of 2 * 32 + 2
+// long longs.  Every thread returns with (before, total).
+__device__ __forceinline__ void tree_prefix(const TreeParams& p, int upto, long long* scratch, long long& before,
+                                            long long& total) {
+  long long a = 0, t = 0;
+  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+    const int x = tree_len(p, b).tiles;
+    t += x;
+    if (b < upto) a += x;
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, x);
+    t += __shfl_xor_sync(0xffffffffu, t, x);
+  }
+  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    scratch[warp] = a;
+    scratch[32 + warp] = t;
+  }
+  __syncthreads();
+  before = total = 0;
+  for (int w = 0; w < nw; ++w) {
+    before += scratch[w];
+    total += scratch[32 + w];
+  }
+  __syncthreads();
+}
+
+// Shared-memory matrix descriptor, 64-byte swizzle.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(4) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void mma_ts_f8_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  if (!DA_MMA_OK(d_tmem, idesc) || !DA_TMEM_A_OK(a_tmem)) return;
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Two floats as e4m3 codes (a in the low byte) and what the codes stand for.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
+}
+
+template <int D, bool V2, int FMT>
+__global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = TreeCfg<D, V2, FMT>;
+  constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* kfull = bars;
+  uint64_t* kempty = kfull + NK;
+  uint64_t* vfull = kempty + NK;
+  uint64_t* vempty = vfull + NV;
+  uint64_t* sc_full = vempty + NV;
+  uint64_t* sc_free = sc_full + NS;
+  uint64_t* s_full = sc_free + NS;   // [2] scores of the tile in buffer s
+  uint64_t* p_ready = s_full + 2;    // [2] P of the tile written over them
+  uint64_t* pv_done = p_ready + 2;   // [2] its P V completed
+  uint64_t* q_full = pv_done + 2;    // the segment's queries written
+  uint64_t* drained = q_full + 1;    // [2] every MMA of an MMA warp completed (abort)
+  uint8_t* misc = smem + C::OFF_MISC;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  int* start = reinterpret_cast<int*>(misc + 16);  // b, unit of the sequence, tile
+  unsigned long long* poison = reinterpret_cast<unsigned long long*>(misc + 32);  // [3] by segment
+  long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_XM);
+
+  // Softmax warps with rows: quarter 0 (and 1) of map 1, quarter 2 (and 3) of map 2.
+  const bool wide = p.R > 32;
+  const int nact = wide ? 8 : 4;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NK; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&sc_full[s], 32);
+      mbar_init(&sc_free[s], nact);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_ready[s], nact);
+      mbar_init(&pv_done[s], 1);
+      mbar_init(&drained[s], 1);
+    }
+    mbar_init(q_full, nact);
+    *abort_flag = 0;
+    poison[0] = poison[1] = poison[2] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (rows without a query, and V1's zeros)
+    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+
+  // ---- this CTA's range of the line of tiles
+  const int HM = p.H * p.mt;
+  long long before, total;
+  tree_prefix(p, 0, scratch, before, total);
+  const long long W = total * HM;
+  const long long G = min(static_cast<long long>(p.grid), max(W, 1ll));  // no CTA between two with tiles is without
+  const long long lo = W * blockIdx.x / G, hi = W * (blockIdx.x + 1) / G;
+  const int count = blockIdx.x < G ? static_cast<int>(hi - lo) : 0;
+  if (warp == 0 && count > 0) {  // the sequence that tile `lo` falls in: 32 sequences a step
+    long long base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const long long mine = (b0 + lane < p.B) ? static_cast<long long>(tree_len(p, b0 + lane).tiles) * HM : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += y;
+      }
+      const long long excl = base + incl - mine;
+      const bool here = lo >= excl && lo < excl + mine;
+      if (here) {
+        const int tiles = static_cast<int>(mine / HM);
+        start[0] = b0 + lane;
+        start[1] = static_cast<int>((lo - excl) / tiles);
+        start[2] = static_cast<int>((lo - excl) % tiles);
+      }
+      if (__any_sync(0xffffffffu, here)) break;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const AbortState ab{abort_flag, p.status};
+
+  // Every role walks the same segments: the CTA's tiles of one unit each.
+  struct Walk {
+    int b, hm, t, rem;
+    TreeLen len;
+  };
+  auto walk_begin = [&]() {
+    Walk w;
+    w.rem = count;
+    w.b = count > 0 ? start[0] : 0;
+    w.hm = count > 0 ? start[1] : 0;
+    w.t = count > 0 ? start[2] : 0;
+    if (count > 0) w.len = tree_len(p, w.b);
+    return w;
+  };
+  auto walk_seg = [&](const Walk& w) { return min(w.rem, w.len.tiles - w.t); };
+  auto walk_next = [&](Walk& w, int seg) {
+    w.rem -= seg;
+    w.t = 0;
+    if (w.rem <= 0) return;
+    if (++w.hm == HM) {
+      w.hm = 0;
+      do {
+        ++w.b;
+        w.len = tree_len(p, w.b);
+      } while (w.len.tiles == 0 && w.b + 1 < p.B);
+    }
+  };
+
+  if (warp == 0) {
+    // =============================================================== producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tm_k1);
+      if (!V2) tma_prefetch_desc(&p.tm_k2);
+      tma_prefetch_desc(&p.tm_v);
+      int kf = 0, vf = 0;
+      bool ok = true;
+      auto load_k = [&](const CUtensorMap* map, int b, int h, int key0) {
+        const int s = kf % NK;
+        const uint32_t use = static_cast<uint32_t>(kf / NK);
+        if (use > 0 && !mbar_wait(&kempty[s], (use - 1) & 1u, ab)) return false;
+        ++kf;
+        mbar_arrive_expect_tx(&kfull[s], C::K_SLOT);
+        uint8_t* dst = smem + C::OFF_K + s * C::K_SLOT;
+        if (DA_BOUNDS_V(key0 < p.n && b < p.B && h < p.H, key0))
+          for (int bx = 0; bx < C::KBOX; ++bx) tma_load_4d(dst + bx * BN * C::KBOXB, map, &kfull[s], bx * 64, h, key0, b);
+        return true;
+      };
+      auto load_v = [&](int b, int h, int key0) {
+        for (int part = 0; part < 2; ++part) {
+          const int s = vf % NV;
+          const uint32_t use = static_cast<uint32_t>(vf / NV);
+          if (use > 0 && !mbar_wait(&vempty[s], (use - 1) & 1u, ab)) return false;
+          ++vf;
+          mbar_arrive_expect_tx(&vfull[s], C::V_SLOT);
+          uint8_t* dst = smem + C::OFF_V + s * C::V_SLOT;
+          if (DA_BOUNDS_V(b < p.B && h < p.H, key0))  // (a box past n reads zeros)
+            for (int bx = 0; bx < C::VBOX; ++bx)
+              tma_load_4d(dst + bx * C::VKEYS * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
+                          key0 + part * C::VKEYS, b);
+        }
+        return true;
+      };
+      int pb = 0, ph = 0, pk = -1;  // the tile whose values come after the next tile's keys
+      Walk w = walk_begin();
+      while (ok && w.rem > 0) {
+        const int seg = walk_seg(w);
+        const int h = w.hm / p.mt;
+        for (int i = 0; ok && i < seg; ++i) {
+          const int key0 = (w.t + i) * BN;
+          ok = load_k(&p.tm_k1, w.b, h, key0) && (V2 || load_k(&p.tm_k2, w.b, h, key0));
+          if (ok && pk >= 0) ok = load_v(pb, ph, pk);
+          pb = w.b;
+          ph = h;
+          pk = key0;
+        }
+        walk_next(w, seg);
+      }
+      if (ok && pk >= 0) load_v(pb, ph, pk);
+      if (*ab.flag) {  // aborted: let the copies already issued land before the CTA exits
+        for (int f = (kf > NK ? kf - NK : 0); f < kf; ++f)
+          mbar_wait_drain(&kfull[f % NK], static_cast<uint32_t>(f / NK) & 1u, kWaitBudgetCycles);
+        for (int f = (vf > NV ? vf - NV : 0); f < vf; ++f)
+          mbar_wait_drain(&vfull[f % NV], static_cast<uint32_t>(f / NV) & 1u, kWaitBudgetCycles);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // =============================================================== MMA issuers
+    auto waitp = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool v = __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+      tc_fence_after();
+      return v;
+    };
+    bool ok = true;
+    uint32_t g = 0;  // tiles so far
+    int fill = 0;
+    Walk w = walk_begin();
+    for (uint32_t k = 0; ok && w.rem > 0; ++k) {
+      const int seg = walk_seg(w);
+      if (warp == 1) {
+        ok = waitp(q_full, k & 1u);
+        for (int i = 0; ok && i < seg; ++i, ++g) {
+          const uint32_t s = g & 1u;
+          if (g >= 2 && !waitp(&pv_done[s], ((g - 2) >> 1) & 1u)) ok = false;
+#pragma unroll
+          for (int m = 0; m < C::NMAP_K; ++m) {
+            const int slot = fill % NK;
+            if (ok && !waitp(&kfull[slot], static_cast<uint32_t>(fill / NK) & 1u)) ok = false;
+            if (!ok) break;
+            ++fill;
+            const uint32_t qa = smem_u32(smem + C::OFF_Q) + m * 64 * C::KBOXB;  // rows 0-127 or 64-191
+            const uint32_t ka = smem_u32(smem + C::OFF_K + slot * C::K_SLOT);
+            const uint64_t dk = (C::KBOXB == 128) ? sdesc_sw128(ka, 16, 1024) : sdesc_sw64(ka, 16, 512);
+#pragma unroll
+            for (int term = 0; term < C::NTERM; ++term) {
+              const uint32_t qt = qa + term * C::Q_TERM;
+              const uint64_t dq = (C::KBOXB == 128) ? sdesc_sw128(qt, 16, 1024) : sdesc_sw64(qt, 16, 512);
+#pragma unroll
+              for (int st = 0; st < C::QK_STEPS; ++st) {
+                const uint64_t a = dq + static_cast<uint64_t>((((st >> 2) * (C::QROWS * 128)) + (st & 3) * 32) >> 4);
+                const uint64_t bd = dk + static_cast<uint64_t>((((st >> 2) * (BN * 128)) + (st & 3) * 32) >> 4);
+                const uint32_t acc = (m > 0 || term > 0 || st > 0) ? 1u : 0u;
+                if constexpr (C::K8)
+                  mma_ss_f8_elect(tmem + C::TM_S + s * BN, a, bd, C::IDESC_QK, acc);
+                else
+                  mma_ss_elect(tmem + C::TM_S + s * BN, a, bd, C::IDESC_QK, acc);
+              }
+            }
+            tc_commit_elect(&kempty[slot]);
+          }
+          if (ok) tc_commit_elect(&s_full[s]);
+        }
+      } else {
+        for (int i = 0; ok && i < seg; ++i, ++g) {
+          const uint32_t s = g & 1u;
+          if (!waitp(&p_ready[s], (g >> 1) & 1u)) ok = false;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const int slot = fill % NV;
+            if (ok && !waitp(&vfull[slot], static_cast<uint32_t>(fill / NV) & 1u)) ok = false;
+            if (!ok) break;
+            ++fill;
+            const uint64_t dv =
+                sdesc_sw128(smem_u32(smem + C::OFF_V + slot * C::V_SLOT), C::VKEYS * 128, 1024);
+            constexpr int KS = C::V8 ? 32 : 16;  // keys of an MMA
+#pragma unroll
+            for (int kk = 0; kk < C::VKEYS / KS; ++kk) {
+              const uint64_t b = dv + static_cast<uint64_t>((kk * KS * 128) >> 4);
+              const uint32_t col = tmem + C::TM_S + s * BN + 8u * (part * (C::VKEYS / KS) + kk);
+              const uint32_t acc = (i > 0 || part > 0 || kk > 0) ? 1u : 0u;
+              if constexpr (C::V8) {
+                mma_ts_f8_elect(tmem + C::TM_O, col, b, C::IDESC_PV, acc);
+                mma_ts_f8_elect(tmem + C::TM_O, col + 32u, b, C::IDESC_PV, 1u);
+              } else {
+                mma_ts_elect(tmem + C::TM_O, col, b, C::IDESC_PV, acc);
+              }
+            }
+            tc_commit_elect(&vempty[slot]);
+          }
+          if (ok) tc_commit_elect(&pv_done[s]);
+        }
+      }
+      walk_next(w, seg);
+    }
+    tc_commit_elect(&drained[warp - 1]);
+    if (*ab.flag) mbar_wait_drain(&drained[warp - 1], 0, kWaitBudgetCycles);
+    __syncwarp();
+  } else if (warp == 3) {
+    // =============================================================== row scales (FP8)
+    if constexpr (C::V8) {
+      uint32_t g = 0;
+      bool ok = true;
+      Walk w = walk_begin();
+      for (uint32_t k = 0; ok && w.rem > 0; ++k) {
+        const int seg = walk_seg(w);
+        const size_t row = (static_cast<size_t>(w.b) * p.H + w.hm / p.mt) * p.n;
+        for (int i = 0; ok && i < seg; ++i, ++g) {
+          const uint32_t s = g % NS, use = g / NS;
+          float x[3][4];  // the loads do not wait for the buffer
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = (w.t + i) * BN + 32 * e + lane;
+            const bool in = j < w.len.end;
+            x[0][e] = in ? p.k1_scales[row + j] : 0.f;
+            x[1][e] = (!V2 && in) ? p.k2_scales[row + j] : 0.f;
+            x[2][e] = in ? p.v_scales[row + j] : 0.f;
+          }
+          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[s], (use - 1) & 1u, ab));
+          float* dst = reinterpret_cast<float*>(smem + C::OFF_SC) + s * 512;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 32 * e + lane;
+            dst[j] = x[0][e];
+            dst[128 + j] = x[1][e];
+            // The scale, at the top of the range, and the log2 that the reference maximum goes
+            // by: at least 2^-100, so that the sum of weights stays far below fp32's end.
+            dst[256 + j] = x[2][e] * exp2f(kTreeTopLog2);
+            dst[384 + j] = fmaxf(log2f(x[2][e]), -100.f);
+          }
+          mbar_arrive(&sc_full[s]);
+        }
+        walk_next(w, seg);
+      }
+    }
+  } else {
+    // =============================================================== softmax
+    const int wq = warp & 3, half = (warp - 4) >> 2;
+    const int map = wq >> 1;
+    if ((wq & 1) == 0 || wide) {
+      const int r = (wq & 1) * 32 + lane;    // row of the map
+      const bool valid = r < p.R;
+      const int row = wq * 32 + lane;        // MMA row
+      const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+      const int pr = r / p.T, tok = r - pr * p.T;
+      // index among the threads of the softmax warps with rows
+      const int ti = (half * (wide ? 4 : 2) + (wide ? wq : (wq >> 1))) * 32 + lane;
+      const int nth = nact * 32;
+      float* xm = reinterpret_cast<float*>(smem + C::OFF_XM);
+      float* xl = reinterpret_cast<float*>(smem + C::OFF_XL);
+      float* qi = reinterpret_cast<float*>(smem + C::OFF_QI);
+      const float top = C::V8 ? kTreeRescale8Log2 : kTreeRescaleLog2;
+      uint32_t g = 0;
+      Walk w = walk_begin();
+      // (an aborted CTA walks on: every wait then returns at once, and no warp misses a named barrier)
+      for (uint32_t k = 0; w.rem > 0; ++k) {
+        const int seg = walk_seg(w);
+        const int h = w.hm / p.mt, mtile = w.hm - h * p.mt;
+        // ---- the segment's queries (the previous segment's score MMAs have completed: every warp
+        // here has seen its last s_full)
+        const int pair0 = mtile * p.ppt, npair = min(p.ppt, p.pairs - pair0);
+        constexpr int NCH = D / 8;  // 16-byte chunks of a bf16 query row
+        for (int i0 = 0; i0 < 2 * p.R * NCH; i0 += nth) {
+          const int i = i0 + ti;
+          const int ch = i % NCH, rr = i / NCH;
+          const int m = rr >= p.R, r2 = rr - m * p.R;
+          const int pj = r2 / p.T, tj = r2 - pj * p.T;
+          const bool in = i < 2 * p.R * NCH;
+          const bool have = in && pj < npair;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (have) {
+            const size_t at = static_cast<size_t>(w.b) * p.T + tj;
+            const __nv_bfloat16* src =
+                V2 ? p.q1 + (at * (2 * p.pairs * p.H) + 2 * (h * p.pairs + pair0 + pj) + m) * D
+                   : (m ? p.q2 : p.q1) + (at * p.H + h) * D;
+            x = reinterpret_cast<const uint4*>(src)[ch];
+          }
+          const int qr = (V2 ? 64 : 128) * m + r2;  // row of the shared buffer
+          uint8_t* q = smem + C::OFF_Q;
+          if constexpr (!C::K8) {
+            if (in)
+              *reinterpret_cast<uint4*>(q + (ch >> 3) * (C::QROWS * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = x;
+          } else {
+            // The row scaled by a power of two that puts its largest magnitude in [128, 256), in
+            // two e4m3 terms: exact for every element down to 2^-10 of the largest.
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+            float f[8], amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              f[2 * e] = __uint_as_float(u[e] << 16);
+              f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+              amax = fmaxf(amax, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+            }
+#pragma unroll
+            for (int o = 1; o < NCH; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int bexp = (__float_as_int(amax) >> 23) & 0xff;
+            const int sh = (amax > 0.f) ? max(-100, min(100, 134 - bexp)) : 0;
+            const float mul = __int_as_float((127 + sh) << 23);
+            uint32_t hi[2], lo8[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t a[2], b[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const float v0 = f[4 * e + 2 * z] * mul, v1 = f[4 * e + 2 * z + 1] * mul;
+                a[z] = e4m3x2(v0, v1);
+                const float2 back = e4m3x2_value(a[z]);
+                b[z] = e4m3x2(v0 - back.x, v1 - back.y);
+              }
+              hi[e] = a[0] | (a[1] << 16);
+              lo8[e] = b[0] | (b[1] << 16);
+            }
+            if (in) {
+              const int c16 = ch >> 1;  // 16-byte chunk of the code row
+              const int sw = (C::KBOXB == 128) ? (c16 ^ (qr & 7)) : (c16 ^ ((qr >> 1) & 3));
+              uint8_t* dst = q + qr * C::KROW + (sw << 4) + 8 * (ch & 1);
+              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(dst + C::Q_TERM) = make_uint2(lo8[0], lo8[1]);
+              if (ch == 0) qi[64 * m + r2] = __int_as_float((127 - sh) << 23);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        if (C::K8) named_bar_sync(5, nth);  // (every row's scale is written)
+        float rc = p.scale_log2;
+        if (C::K8) rc *= valid ? qi[64 * map + r] : 0.f;
+        if (FMT == kCacheFp8k) rc *= (map && !V2) ? p.k2_scale : p.k1_scale;
+        // ---- what the row sees of the drafted tokens
+        const int nt = w.len.end - w.len.L;
+        unsigned long long see = 0;
+        if (valid) see = p.mask ? p.mask[w.b * p.mask_sb + tok] : ((2ull << tok) - 1ull);
+        if (nt < 64) see &= (1ull << nt) - 1ull;
+
+        float m_used = -INFINITY, l = 0.f;
+        for (int i = 0; i < seg; ++i, ++g) {
+          const uint32_t s = g & 1u;
+          const int key0 = (w.t + i) * BN;
+          const uint32_t tS = tl + C::TM_S + s * BN;
+          mbar_wait(&s_full[s], (g >> 1) & 1u, ab);
+          __syncwarp();
+          tc_fence_after();
+          uint32_t x[2][32];
+          tmem_ld32(tS + 64u * half, x[0]);
+          tmem_ld32(tS + 64u * half + 32u, x[1]);
+          const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + 64 * half;
+          if constexpr (C::V8) {
+            mbar_wait(&sc_full[g % NS], (g / NS) & 1u, ab);
+            __syncwarp();
+          }
+          tmem_ld_wait2(x[0], x[1]);
+          // ---- scores in the log2 domain
+          const bool special = key0 + BN > w.len.L;  // the tile reaches into the drafted keys or past them
+          unsigned long long vis = ~0ull;
+          if (special) {
+            const int rel = key0 + 64 * half - w.len.L;  // drafted token of the first column
+            vis = rel >= 64 ? 0ull : rel >= 0 ? see >> rel : rel <= -64 ? ~0ull : (see << -rel) | ((1ull << -rel) - 1ull);
+          }
+          float pm = -INFINITY;
+          if constexpr (C::V8) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 ks = *reinterpret_cast<const float4*>(sc + 128 * ((map && !V2) ? 1 : 0) + 32 * q + c);
+                const float4 lv = *reinterpret_cast<const float4*>(sc + 384 + 32 * q + c);
+                const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, ll[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float v = __uint_as_float(x[q][c + e]) * rc * kk[e];
+                  if (special && !((vis >> (32 * q + c + e)) & 1ull)) v = -INFINITY;
+                  x[q][c + e] = __float_as_uint(v);
+                  pm = fmaxf(pm, v + ll[e]);
+                }
+              }
+          } else {
+            if (special) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!((vis >> (32 * q + c)) & 1ull)) x[q][c] = __float_as_uint(-INFINITY);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int c = 0; c < 32; c += 2)
+                pm = max3(pm, __uint_as_float(x[q][c]), __uint_as_float(x[q][c + 1]));
+            pm *= rc;
+          }
+          // ---- the row's maximum over both halves of the tile
+          float* xg = xm + (g & 1u) * 256;
+          xg[half * 128 + row] = pm;
+          named_bar_sync(1 + wq, 64);
+          pm = fmaxf(pm, xg[(half ^ 1) * 128 + row]);
+          const float m_new = fmaxf(m_used, pm);
+          const bool rescale = __any_sync(0xffffffffu, m_new > m_used + top);
+          if (rescale) {
+            const float f = (m_used == m_new) ? 1.f : ex2(m_used - m_new);
+            l *= f;
+            m_used = m_new;
+            if (i > 0) {  // (the first P V of a segment overwrites O)
+              mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
+              __syncwarp();
+              tc_fence_after();
+#pragma unroll
+              for (int q = 0; q < DV / 64; ++q) {
+                uint32_t o[32];
+                tmem_ld32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                tmem_st32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+              }
+            }
+          }
+          const float ref = (m_used == -INFINITY) ? 0.f : m_used;
+          // ---- weights, in place of the scores
+          if constexpr (C::V8) {
+            float l0 = 0.f, l1 = 0.f;
+            uint32_t hi[16], lo8[16];
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float4 vs4 = *reinterpret_cast<const float4*>(sc + 256 + 32 * q + c);
+                const float vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+                float pw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pw[e] = ex2(__uint_as_float(x[q][c + e]) - ref);
+                l0 += pw[0] + pw[1];
+                l1 += pw[2] + pw[3];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  pw[e] *= vs[e];
+                  // (a hidden row's scale may be anything)
+                  if (special && !((vis >> (32 * q + c + e)) & 1ull)) pw[e] = 0.f;
+                }
+                const uint32_t a = e4m3x2(pw[0], pw[1]), b = e4m3x2(pw[2], pw[3]);
+                const float2 fa = e4m3x2_value(a), fb = e4m3x2_value(b);
+                hi[(32 * q + c) >> 2] = a | (b << 16);
+                lo8[(32 * q + c) >> 2] = e4m3x2(pw[0] - fa.x, pw[1] - fa.y) | (e4m3x2(pw[2] - fb.x, pw[3] - fb.y) << 16);
+              }
+            l += l0 + l1;
+            tmem_st16(tS + 16u * half, hi);
+            tmem_st16(tS + 32u + 16u * half, lo8);
+          } else {
+            const uint64_t rc2 = f2pack(rc, rc), nb2 = f2pack(-ref, -ref);
+            uint64_t acc[2] = {0, 0};
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float a0, a1;
+                f2unpack(fma2(f2pack(__uint_as_float(x[q][c]), __uint_as_float(x[q][c + 1])), rc2, nb2), a0, a1);
+                const float p0 = ex2(a0), p1 = ex2(a1);
+                acc[q] = add2(acc[q], f2pack(p0, p1));
+                x[q][c >> 1] = pack_bf16x2(p0, p1);
+              }
+            float s0, s1;
+            f2unpack(add2(acc[0], acc[1]), s0, s1);
+            l += s0 + s1;
+            tmem_st16(tS + 32u * half, reinterpret_cast<const uint32_t(&)[16]>(x[0]));
+            tmem_st16(tS + 32u * half + 16u, reinterpret_cast<const uint32_t(&)[16]>(x[1]));
+          }
+          if (special) {
+            // Value rows that some token must not see: rows past the drafted ones hold whatever the
+            // cache held (zeroed here), and a drafted row with a NaN or an infinity is zeroed and
+            // remembered, so that it reaches only the tokens that see it.
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const uint32_t f = 2 * g + part;
+              const int kp = key0 + part * C::VKEYS;
+              const int r0 = max(0, w.len.L - kp);  // first drafted row of the slot
+              if (r0 >= C::VKEYS) continue;
+              mbar_wait(&vfull[f % NV], (f / NV) & 1u, ab);
+              __syncwarp();
+              uint8_t* slot = smem + C::OFF_V + (f % NV) * C::V_SLOT;
+              constexpr int RCH = C::VROW / 16;  // 16-byte chunks of a value row
+              for (int i2 = ti; i2 < (C::VKEYS - r0) * RCH; i2 += nth) {
+                const int vr = r0 + i2 / RCH, vc = i2 % RCH;
+                uint4* at = reinterpret_cast<uint4*>(slot + (vc >> 3) * (C::VKEYS * 128) + vr * 128 + ((vc & 7) << 4));
+                bool zero = kp + vr >= w.len.end;
+                if (!zero) {
+                  const uint4 u = *at;
+                  const uint32_t v4[4] = {u.x, u.y, u.z, u.w};
+                  bool bad = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if constexpr (C::V8) {  // e4m3: 0x7f, 0xff
+                      const uint32_t t7 = (v4[e] & 0x7f7f7f7fu) + 0x01010101u;
+                      bad |= (t7 & 0x80808080u) != 0;
+                    } else {
+                      bad |= (v4[e] & 0x7f80u) == 0x7f80u || (v4[e] & 0x7f800000u) == 0x7f800000u;
+                    }
+                  }
+                  if (bad) {
+                    atomicOr(&poison[k % 3], 1ull << (kp + vr - w.len.L));
+                    zero = true;
+                  }
+                }
+                if (zero) *at = make_uint4(0, 0, 0, 0);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&p_ready[s]);
+            if (C::V8) mbar_arrive(&sc_free[g % NS]);
+          }
+          __syncwarp();
+        }
+        // ---- the segment's partial state
+        mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
+        __syncwarp();
+        tc_fence_after();
+        if (half == 1) xl[(k & 1u) * 128 + row] = l;
+        named_bar_sync(1 + wq, 64);
+        if (ti == 0) poison[(k + 2) % 3] = 0;
+        const size_t unit = static_cast<size_t>(w.b) * HM + w.hm;
+        float* piece = p.ws + (unit + blockIdx.x) * tree_state_floats(p.R, DV);
+        if (half == 0 && valid) {
+          l += xl[(k & 1u) * 128 + row];
+          if (see & poison[k % 3]) l = __uint_as_float(0x7fffffffu);
+          if (DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM && r < kTreeRows, r))
+            reinterpret_cast<float2*>(piece)[map * p.R + r] = make_float2(m_used, l);
+        }
+        float4* o4 = reinterpret_cast<float4*>(piece + 4 * p.R) + (static_cast<size_t>(map) * (DV / 4) + (DV / 8) * half) * p.R;
+#pragma unroll
+        for (int q = 0; q < DV / 64; ++q) {
+          uint32_t o[32];
+          tmem_ld32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+          tmem_ld_wait(o);
+          if (valid && DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM, r)) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              o4[(8 * q + c) * p.R + r] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                                      __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        walk_next(w, seg);
+      }
+    }
+  }
+
+  // ---- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Merges the partial states of a unit and finishes four of its rows a CTA:
+// thread = (row of the four, 4 channels); DV threads.
+template <int DV, bool V2>
+__global__ void __launch_bounds__(DV) tree_combine_kernel(const __grid_constant__ TreeParams p, float o_mult) {
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  __shared__ long long scratch[64];
+  __shared__ float red[DV / 32][4];
+  const int HM = p.H * p.mt;
+  const int groups = (p.R + 3) >> 2;
+  const int unit = static_cast<int>(blockIdx.x / groups), rg = static_cast<int>(blockIdx.x % groups);
+  const int b = unit / HM, hm = unit - b * HM;
+  const int h = hm / p.mt, mtile = hm - h * p.mt;
+  long long before, total;
+  tree_prefix(p, b, scratch, before, total);
+  const TreeLen len = tree_len(p, b);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = 4 * rg + (threadIdx.x & 3), c4 = threadIdx.x >> 2;
+  const int pj = r / p.T, t = r - pj * p.T;
+  const int pair = mtile * p.ppt + pj;
+  const bool have = r < p.R && pair < p.pairs;
+  float y[4] = {0.f, 0.f, 0.f, 0.f};
+  float ss = 0.f;
+  if (have && len.tiles > 0 && t < len.nt) {
+    const long long W = total * HM;
+    const long long s = before * HM + static_cast<long long>(hm) * len.tiles, e = s + len.tiles - 1;
+    const long long G = min(static_cast<long long>(p.grid), W);
+    const int c0 = static_cast<int>(((s + 1) * G - 1) / W), c1 = static_cast<int>(((e + 1) * G - 1) / W);
+    const size_t pf = tree_state_floats(p.R, DV);
+    const float* src = p.ws + (static_cast<size_t>(unit) + c0) * pf;
+    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, acc[2][4] = {};
+    for (int c = c0; c <= c1; ++c, src += pf) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float2 ml = reinterpret_cast<const float2*>(src)[m * p.R + r];
+        const float4 o = reinterpret_cast<const float4*>(src + 4 * p.R)[(static_cast<size_t>(m) * (DV / 4) + c4) * p.R + r];
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen in this state
+        const float mn = fmaxf(M[m], ml.x);
+        const float fo = (M[m] == mn) ? 1.f : ex2(M[m] - mn), fn = (ml.x == mn) ? 1.f : ex2(ml.x - mn);
+        M[m] = mn;
+        L[m] = L[m] * fo + ml.y * fn;
+        acc[m][0] = acc[m][0] * fo + o.x * fn;
+        acc[m][1] = acc[m][1] * fo + o.y * fn;
+        acc[m][2] = acc[m][2] * fo + o.z * fn;
+        acc[m][3] = acc[m][3] * fo + o.w * fn;
+      }
+    }
+    const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
+    const float a1 = (L[0] == 0.f) ? 0.f : o_mult / L[0], a2 = (L[1] == 0.f) ? 0.f : -coef * o_mult / L[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = acc[0][i] * a1 + acc[1][i] * a2;
+      ss = fmaf(y[i], y[i], ss);
+    }
+  }
+  float rinv = 1.f;
+  if (!V2) {
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+    if (lane < 4) red[warp][lane] = ss;
+    __syncthreads();
+    float tot = 0.f;
+#pragma unroll
+    for (int w = 0; w < DV / 32; ++w) tot += red[w][threadIdx.x & 3];
+    rinv = p.norm_mult * rsqrtf(tot * (1.f / DV) + p.eps);
+  }
+  if (have) {
+    float g[4] = {1.f, 1.f, 1.f, 1.f};
+    if (!V2 && p.gamma) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = p.gamma[4 * c4 + i];
+    }
+    const size_t orow = V2 ? (static_cast<size_t>(b) * p.T + t) * (p.H * p.pairs) + h * p.pairs + pair
+                           : (static_cast<size_t>(b) * p.T + t) * p.H + h;
+    if (DA_BOUNDS_V(b < p.B && t < p.T && h < p.H, t))
+      *reinterpret_cast<uint2*>(p.out + orow * DV + 4 * c4) =
+          make_uint2(pack_bf16x2(y[0] * rinv * g[0], y[1] * rinv * g[1]),
+                     pack_bf16x2(y[2] * rinv * g[2], y[3] * rinv * g[3]));
+  }
+}
+
+template <int D, bool V2, int FMT>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+  using C = TreeCfg<D, V2, FMT>;
+  auto kern = tree_kernel<D, V2, FMT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
+  cfg.blockDim = dim3(C::NTHREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cc = {};
+  const long long ctas = static_cast<long long>(p.B) * p.H * p.mt * ((p.R + 3) / 4);
+  cc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cc.blockDim = dim3(C::DV, 1, 1);
+  cc.stream = s;
+  cc.attrs = attr;
+  cc.numAttrs = 1;
+  return cudaLaunchKernelEx(&cc, tree_combine_kernel<C::DV, V2>, p, C::V8 ? 1.f / 128.f : 1.f);
+}
+
+}  // namespace da

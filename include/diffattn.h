@@ -580,6 +580,189 @@ diffattn_status lambda_reparam_backward(const float* lq1, const float* lk1, cons
                                         void* stream);
 
 /*
+ * Rotary positions: y = mult R(pos theta) x on the first rot_dim channels of
+ * each head, the others unchanged.  Channel pair i turns by pos theta_i; pairs
+ * are (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved:
+ *   y_a = mult (x_a cos - x_b sin),   y_b = mult (x_b cos + x_a sin).
+ * The pages leave positions to the model around the operator; these calls
+ * put them on the queries and keys that diffattn_forward, diffattn_backward
+ * and the decode calls take.
+ *
+ * diffattn_rope_spec is filled on the host by one of the two calls below and
+ * passed by pointer; a call copies it into its launch.  turns[i] is theta_i as
+ * a fraction of a turn per position, 2^64 to the turn, so that pos * turns[i]
+ * modulo 2^64 is the exact phase however far the position.
+ */
+typedef struct {
+    int rot_dim;                  /* rotated channels: even, 2 .. 128, at most d */
+    int interleaved;              /* 0: pairs of halves; else adjacent pairs     */
+    float mult;                   /* factor on the rotated channels              */
+    unsigned long long turns[64]; /* rot_dim / 2 of them                         */
+} diffattn_rope_spec;
+
+typedef enum {
+    DIFFATTN_ROPE_NONE = 0,   /* theta_i = base^(-2 i / rot_dim)                          */
+    DIFFATTN_ROPE_LINEAR = 1, /* theta_i / factor                                         */
+    DIFFATTN_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in base's place  */
+    DIFFATTN_ROPE_YARN = 3    /* theta_i (1 - w_i) + theta_i / factor w_i, with w_i rising
+                                 from 0 to 1 between the pairs that make beta_fast and
+                                 beta_slow turns over original_context positions (rounded
+                                 down and up); mult = 0.1 ln(factor) + 1                  */
+} diffattn_rope_scaling;
+
+/*
+ * Host only.  base > 1; factor >= 1 (unused without scaling); original_context
+ * and the betas (usually 32 and 1) for YARN only.  NULL -> ERR_NULL, an
+ * unknown scaling -> ERR_DTYPE, sizes or values out of range -> ERR_SHAPE.
+ */
+diffattn_status diffattn_rope_init(diffattn_rope_spec* rope, int rot_dim, int interleaved, double base,
+                                   diffattn_rope_scaling scaling, double factor, int original_context,
+                                   double beta_fast, double beta_slow);
+
+/* Host only: rot_dim / 2 frequencies of the caller's own (radians per position, finite). */
+diffattn_status diffattn_rope_from_frequencies(diffattn_rope_spec* rope, int rot_dim, int interleaved,
+                                               const double* frequencies, float mult);
+
+/*
+ * Rotates up to four tensors (e.g. q1, q2, k1, k2) by the same positions in
+ * one kernel.
+ *   dt        : DIFFATTN_BF16 or DIFFATTN_F32, for all; arithmetic in fp32,
+ *               rounded once.
+ *   x, out    : host arrays of `count` device pointers, x[i] and out[i]
+ *               [B, n, heads[i], d] contiguous; d <= 128; bf16 16-byte aligned
+ *               (else ERR_ALIGN).  out[i] may be x[i]; any other overlap ->
+ *               ERR_SHAPE.  heads : host array.
+ *   positions : device int32 [B, n], or NULL: token t at position t.
+ *   inverse   : non-zero: the rotation by the negative angles with the same
+ *               mult, which is the transpose, so also the backward pass: the
+ *               gradient of x given that of y (the fp32 gradients of
+ *               diffattn_backward).
+ * count > 4 or d > 128 -> ERR_UNSUPPORTED.  Asynchronous on `stream`.
+ */
+diffattn_status diffattn_rope(diffattn_dtype dt, int B, int n, int d, int count, const void* const* x,
+                              const int* heads, const diffattn_rope_spec* rope, const int* positions, int inverse,
+                              void* const* out, void* stream);
+
+/*
+ * Formats of a key/value cache; tensors [B, n, H, d] (keys) and [B, n, H, 2d]
+ * (V1 values; V2: [B, n, Hkv, d]) as the decode calls take them.
+ */
+typedef enum {
+    DIFFATTN_CACHE_BF16 = 0, /* keys and values bf16 (diffattn_decode)                           */
+    DIFFATTN_CACHE_FP8K = 1, /* e4m3 keys, one scale a tensor (a host float), bf16 values
+                                (diffattn_decode_fp8k): code = e4m3(k / scale), saturating       */
+    DIFFATTN_CACHE_FP8 = 2   /* e4m3 keys and values with an fp32 scale a row (token and head),
+                                scales [B, H, n]: scale = amax / 448, code = e4m3(x 448 / amax);
+                                a row of zeros has scale 0, a row with a NaN or an infinity
+                                reads as NaN; scales are never negative                          */
+} diffattn_cache_format;
+
+/*
+ * Writes T new tokens a sequence into a V1 cache: keys rotated (rope, or NULL
+ * for none), quantised from fp32 and stored at rows lens[b] .. of the
+ * sequence, values likewise without the rotation, and the queries rotated
+ * into q1_out, q2_out: a decode step's or a prefill's work between the
+ * projections and the attention, in one kernel.
+ *   q1, q2    : bf16 [B, T, H, d], or both NULL (no queries); q1_out, q2_out
+ *               the same shape, not overlapping q1 or q2 (ERR_SHAPE).
+ *   k1, k2, v : bf16 [B, T, H, d], [B, T, H, 2d]; d in {64, 128}.
+ *   positions : device int32 [B, T] (e.g. the depths in a draft tree), or
+ *               NULL: the cache row.
+ *   lens      : device int32 [B], the first row written; NULL: 0.
+ *   ntok      : device int32 [B], tokens of each sequence; NULL: T.  A token
+ *               t >= ntok[b] leaves the cache as it is and gives zero queries;
+ *               rows outside [0, n) are not written.
+ *   k1_scale, k2_scale : FP8K only, finite and positive (else ERR_SHAPE).
+ *   k1_scales, k2_scales, v_scales : FP8 only, device fp32 [B, H, n].
+ * An unknown format -> ERR_DTYPE.  Tensors 16-byte aligned.  Asynchronous on
+ * `stream`.  The V2 form has one key tensor and Hq query heads (d = 128).
+ */
+diffattn_status diffattn_cache_append(diffattn_cache_format fmt, int B, int T, int H, int n, int d, const void* q1,
+                                      const void* q2, const void* k1, const void* k2, const void* v,
+                                      const diffattn_rope_spec* rope, const int* positions, const int* lens,
+                                      const int* ntok, void* q1_out, void* q2_out, void* k1_cache, void* k2_cache,
+                                      void* v_cache, float k1_scale, float k2_scale, float* k1_scales,
+                                      float* k2_scales, float* v_scales, void* stream);
+
+diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T, int Hq, int Hkv, int n, int d,
+                                         const void* q, const void* k, const void* v, const diffattn_rope_spec* rope,
+                                         const int* positions, const int* lens, const int* ntok, void* q_out,
+                                         void* k_cache, void* v_cache, float k_scale, float* k_scales,
+                                         float* v_scales, void* stream);
+
+/*
+ * Attention of up to 64 drafted tokens a sequence over a cache of any format:
+ * diffattn_decode (diffattn_v2_decode) for the nodes of a draft tree.  The
+ * drafted tokens' keys and values are in the cache already, at rows lens[b] ..
+ * lens[b] + ntok[b] - 1 (diffattn_cache_append).  Token t of sequence b sees
+ * the keys j < lens[b], and drafted token u iff bit u of its mask word is set
+ * (its own bit included, where it is to see itself).
+ *   q1, q2    : bf16 [B, T, H, d] (V2: q [B, T, Hq, d]); T <= 64, else
+ *               ERR_UNSUPPORTED; d in {64, 128} (V2 128).  T = 1 is a plain
+ *               decode step, also over the FP8 format.
+ *   k1, k2, v, scales : the cache (k1_scale, k2_scale for FP8K, the row scales
+ *               for FP8).  What lies behind the drafted rows is not read into
+ *               any result.
+ *   lens      : device int32 [B], clamped to [0, n]; NULL: n - T.
+ *   ntok      : device int32 [B], clamped to [0, T]; NULL: T.  Tokens t >=
+ *               ntok[b], and tokens that see no key, give zeros.  Drafted rows
+ *               that do not fit below n are not seen.
+ *   mask      : device words, that of (b, t) at mask[b * mask_sb + t] (mask_sb
+ *               = 0: one tree for all); NULL: a chain (token t sees u <= t).
+ *   lambda, lambda_init, gamma, eps, out [B, T, H, 2d] : as for
+ *               diffattn_decode.  V2: lam_logits at b * sb + t * st + pair,
+ *               softmax_scale <= 0 selects 1/sqrt(d), out [B, T, Hq/2, d].
+ *   workspace : required, at least the workspace call's bytes, 16-byte
+ *               aligned; partial states, nothing kept between calls.  Calls
+ *               that can overlap need their own.
+ * A drafted key or value row with a NaN or an infinity makes the tokens that
+ * see it NaN, and no others.  Two kernels; results do not depend on the
+ * order in which they run (the same inputs give the same bits on the same
+ * GPU).  Errors as for diffattn_decode; an unknown format -> ERR_DTYPE.
+ */
+size_t diffattn_tree_decode_workspace(int B, int T, int H, int d);
+
+diffattn_status diffattn_tree_decode(diffattn_cache_format fmt, int B, int T, int H, int n, int d, const void* q1,
+                                     const void* q2, const void* k1, const void* k2, float k1_scale, float k2_scale,
+                                     const float* k1_scales, const float* k2_scales, const void* v,
+                                     const float* v_scales, const int* lens, const int* ntok,
+                                     const unsigned long long* mask, long long mask_sb, const float* lambda,
+                                     float lambda_init, const float* gamma, float eps, void* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+size_t diffattn_v2_tree_decode_workspace(int B, int T, int Hq, int Hkv, int d);
+
+diffattn_status diffattn_v2_tree_decode(diffattn_cache_format fmt, int B, int T, int Hq, int Hkv, int n, int d,
+                                        const void* q, const void* k, float k_scale, const float* k_scales,
+                                        const void* v, const float* v_scales, const int* lens, const int* ntok,
+                                        const unsigned long long* mask, long long mask_sb, const float* lam_logits,
+                                        long long sb, long long st, float softmax_scale, void* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * After the drafts are judged: moves the rows of the accepted path's nodes to
+ * the front of the drafted rows, row lens[b] + path[b][i] to row lens[b] + i
+ * for i < nkeep[b], in place, keys, values and row scales.
+ *   path     : device int32 [B, A], node numbers in ascending order (a child
+ *              follows its parent in the draft); A <= 64, else ERR_UNSUPPORTED.
+ *              An entry that does not ascend, is not in [0, 64) or whose row is
+ *              not in the cache ends the sequence's path there.
+ *   nkeep    : device int32 [B], clamped to [0, A].
+ *   lens     : device int32 [B], required.
+ *   new_lens : device int32 [B] or NULL, receives lens[b] plus the nodes kept;
+ *              may not overlap lens (ERR_SHAPE).
+ * Other rows are left as they are.  Asynchronous on `stream`.
+ */
+diffattn_status diffattn_cache_keep(diffattn_cache_format fmt, int B, int A, int H, int n, int d, void* k1_cache,
+                                    void* k2_cache, void* v_cache, float* k1_scales, float* k2_scales,
+                                    float* v_scales, const int* lens, const int* path, const int* nkeep,
+                                    int* new_lens, void* stream);
+
+diffattn_status diffattn_v2_cache_keep(diffattn_cache_format fmt, int B, int A, int Hkv, int n, int d, void* k_cache,
+                                       void* v_cache, float* k_scales, float* v_scales, const int* lens,
+                                       const int* path, const int* nkeep, int* new_lens, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device status
  * word on the current device.  Returns DIFFATTN_OK, DIFFATTN_ERR_TIMEOUT if a
  * bounded in-kernel wait ran out since the last call, DIFFATTN_ERR_BOUNDS (the
