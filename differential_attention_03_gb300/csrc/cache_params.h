@@ -95,9 +95,10 @@ struct TreeParams {
 
 constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree decode
 
-// Floats of one partial state of the tree decode: (maximum, sum) and O of R rows of both maps.
+// Floats of one partial state of the tree decode: (maximum, sum) and O of R rows of both maps, twice
+// (each half of the keys its own) where the rows leave room.
 __host__ __device__ __forceinline__ size_t tree_state_floats(int R, int dv) {
-  return 2 * static_cast<size_t>(R) * (dv + 2);
+  return 2 * static_cast<size_t>(R > kTreeRows / 2 ? R : 2 * R) * (dv + 2);
 }
 
 cudaError_t launch_rope(const RopeParams& p, bool f32, bool vec, int grid_x, int grid_y, cudaStream_t s);

@@ -78,31 +78,36 @@ struct TreeCfg {
   // Rings: about 160-176 KB in flight, split between keys and values.
   static constexpr int NK = (!V2 && D == 128) ? (K8 ? 4 : 2) : (!V2) ? (K8 ? (V8 ? 10 : 8) : 5) : (K8 ? 5 : 3);
   static constexpr int NV = (!V2 && D == 128) ? (V8 ? 6 : 3) : (!V2) ? (V8 ? 12 : (K8 ? 7 : 6)) : (V8 ? 11 : (K8 ? 6 : 5));
-  static constexpr int NS = 4;  // scale buffers (FP8)
+  static constexpr int NS = 6;  // scale buffers (FP8)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = Q_BYTES;
   static constexpr int OFF_V = OFF_K + NK * K_SLOT;
   static constexpr int OFF_SC = OFF_V + NV * V_SLOT;           // float [NS][4][128]: key scales 1, 2, value scales, log2 of them
-  static constexpr int OFF_XM = OFF_SC + (V8 ? NS * 4 * 128 * 4 : 0);  // float [2 tiles][2 halves][128]
-  static constexpr int OFF_XL = OFF_XM + 4 * 128 * 4;          // float [2 segments][128] row sums of half 1
-  static constexpr int OFF_QI = OFF_XL + 2 * 128 * 4;          // float [128]: inverse of the query row's power of two
+  static constexpr int OFF_XM = OFF_SC + (V8 ? NS * 4 * 128 * 4 : 0);  // float [2 tiles][4 warps][128]: maxima (at a segment's end: sums)
+  static constexpr int OFF_QI = OFF_XM + 8 * 128 * 4;          // float [128]: inverse of the query row's power of two
   static constexpr int OFF_BARS = OFF_QI + 128 * 4;
-  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NS + 2 + 2 + 2 + 1 + 2;
+  static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NS + 2 + 2 + 2 + 2 + 1 + 2;
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 256 + 1024;
-  static constexpr uint32_t TM_O = 0, TM_S = DV;  // two score tiles of BN columns
+  // Tensor memory: O, two score tiles, and, where O leaves the room (DV = 128), two P tiles of 64
+  // columns; else P takes the place of its scores.
+  static constexpr bool PSEP = DV == 128;
+  static constexpr uint32_t TM_O = 0, TM_S = DV;
+  static constexpr uint32_t TM_P = PSEP ? TM_S + 2 * BN : TM_S, P_STEP = PSEP ? 64 : BN;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int QK_STEPS = KROW / 32;
   static constexpr uint32_t IDESC_QK = K8 ? idesc_e4m3(128, BN) : idesc_bf16(128, BN, false, false);
   static constexpr uint32_t IDESC_PV = V8 ? (idesc_e4m3(128, DV) | (1u << 16)) : idesc_bf16(128, DV, false, true);
-  static constexpr int NTHREADS = 384;
+  static constexpr int NACT = 16;  // softmax warps: four a lane quarter
+  static constexpr int NTHREADS = (4 + NACT) * 32;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
-  static_assert(DV + 2 * BN <= 512, "tensor memory");
+  static_assert(DV + 2 * BN + (PSEP ? 128 : 0) <= 512, "tensor memory");
   static_assert(K_SLOT % 1024 == 0 && V_SLOT % 1024 == 0 && Q_TERM % 1024 == 0, "swizzled boxes start on 1 KB");
 };
 
 constexpr float kTreeRescaleLog2 = 8.f;   // bf16 P: how far a score may exceed the reference maximum
 constexpr float kTreeTopLog2 = 7.f;       // e4m3 P: the reference maximum sits at 2^7 (e4m3 ends at 448) ...
+constexpr float kTreeValueMult = 0.5f;     // 2^7, times two_e4m3x4's 2^-8
 constexpr float kTreeRescale8Log2 = 1.f;  // ... and may be exceeded by a factor of two
 
 // A sequence's committed keys, its drafted tokens, the end of its keys and its tiles.
@@ -171,6 +176,26 @@ __device__ __forceinline__ void mma_ts_f8_elect(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  if (!DA_TMEM_OK(taddr, 4)) return;
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Waits for this thread's outstanding tcgen05.ld into 16 registers (tied in).
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
+               :
+               : "memory");
+}
+
+// 4-byte asynchronous copy to shared memory: `bytes` (4 or 0) of it from global, the rest zeros.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // Two floats as e4m3 codes (a in the low byte) and what the codes stand for.
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -179,8 +204,25 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
 
-template <int D, bool V2, int FMT>
-__global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+// Four non-negative floats, scaled to 2^-8 of what they stand for (at most
+// 448 2^-8), as two e4m3 terms each: hi truncates, hi + lo is within 2^-8 of
+// the value, or 2^-10 absolute, as a bf16 would be.  At that scale f16's
+// exponent field is e4m3's, so a code is bits 7-13 of the f16: pairs of f16
+// are shifted and masked as integers (the e4m3 conversion instructions take
+// about 16 issue cycles each, and bounded the kernel: 372 us against 247 us
+// at B8 H16 n32768 d64).  A NaN stays a NaN.
+__device__ __forceinline__ void two_e4m3x4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  uint32_t f0, f1, r0, r1;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f0) : "f"(b), "f"(a));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f1) : "f"(d), "f"(c));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(f0), "r"(f0 & 0x7f807f80u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(f1), "r"(f1 & 0x7f807f80u));
+  hi = __byte_perm(f0 << 1, f1 << 1, 0x7531);
+  lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531);
+}
+
+template <int D, bool V2, int FMT, bool WIDE>
+__global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
   grid_dep_launch_dependents();
@@ -199,7 +241,8 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
   uint64_t* s_full = sc_free + NS;   // [2] scores of the tile in buffer s
   uint64_t* p_ready = s_full + 2;    // [2] P of the tile written over them
   uint64_t* pv_done = p_ready + 2;   // [2] its P V completed
-  uint64_t* q_full = pv_done + 2;    // the segment's queries written
+  uint64_t* s_free = pv_done + 2;    // [2] (PSEP) its scores loaded
+  uint64_t* q_full = s_free + 2;    // the segment's queries written
   uint64_t* drained = q_full + 1;    // [2] every MMA of an MMA warp completed (abort)
   uint8_t* misc = smem + C::OFF_MISC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
@@ -208,9 +251,7 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
   unsigned long long* poison = reinterpret_cast<unsigned long long*>(misc + 32);  // [3] by segment
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_XM);
 
-  // Softmax warps with rows: quarter 0 (and 1) of map 1, quarter 2 (and 3) of map 2.
-  const bool wide = p.R > 32;
-  const int nact = wide ? 8 : 4;
+  constexpr int NACT = C::NACT;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NK; ++s) {
@@ -223,15 +264,16 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&sc_full[s], 32);
-      mbar_init(&sc_free[s], nact);
+      mbar_init(&sc_free[s], NACT);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_ready[s], nact);
+      mbar_init(&p_ready[s], NACT);
       mbar_init(&pv_done[s], 1);
+      mbar_init(&s_free[s], NACT);
       mbar_init(&drained[s], 1);
     }
-    mbar_init(q_full, nact);
+    mbar_init(q_full, NACT);
     *abort_flag = 0;
     poison[0] = poison[1] = poison[2] = 0;
     fence_mbar_init();
@@ -383,8 +425,9 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         ok = waitp(q_full, k & 1u);
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t s = g & 1u;
-          if (g >= 2 && !waitp(&pv_done[s], ((g - 2) >> 1) & 1u)) ok = false;
-#pragma unroll
+          // the buffer: its scores loaded, or (P in their place) their P V done
+          if (g >= 2 && !waitp(C::PSEP ? &s_free[s] : &pv_done[s], ((g - 2) >> 1) & 1u)) ok = false;
+#pragma unroll 1
           for (int m = 0; m < C::NMAP_K; ++m) {
             const int slot = fill % NK;
             if (ok && !waitp(&kfull[slot], static_cast<uint32_t>(fill / NK) & 1u)) ok = false;
@@ -393,7 +436,7 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
             const uint32_t qa = smem_u32(smem + C::OFF_Q) + m * 64 * C::KBOXB;  // rows 0-127 or 64-191
             const uint32_t ka = smem_u32(smem + C::OFF_K + slot * C::K_SLOT);
             const uint64_t dk = (C::KBOXB == 128) ? sdesc_sw128(ka, 16, 1024) : sdesc_sw64(ka, 16, 512);
-#pragma unroll
+#pragma unroll 1
             for (int term = 0; term < C::NTERM; ++term) {
               const uint32_t qt = qa + term * C::Q_TERM;
               const uint64_t dq = (C::KBOXB == 128) ? sdesc_sw128(qt, 16, 1024) : sdesc_sw64(qt, 16, 512);
@@ -416,7 +459,7 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t s = g & 1u;
           if (!waitp(&p_ready[s], (g >> 1) & 1u)) ok = false;
-#pragma unroll
+#pragma unroll 1
           for (int part = 0; part < 2; ++part) {
             const int slot = fill % NV;
             if (ok && !waitp(&vfull[slot], static_cast<uint32_t>(fill / NV) & 1u)) ok = false;
@@ -428,7 +471,7 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
 #pragma unroll
             for (int kk = 0; kk < C::VKEYS / KS; ++kk) {
               const uint64_t b = dv + static_cast<uint64_t>((kk * KS * 128) >> 4);
-              const uint32_t col = tmem + C::TM_S + s * BN + 8u * (part * (C::VKEYS / KS) + kk);
+              const uint32_t col = tmem + C::TM_P + s * C::P_STEP + 8u * (part * (C::VKEYS / KS) + kk);
               const uint32_t acc = (i > 0 || part > 0 || kk > 0) ? 1u : 0u;
               if constexpr (C::V8) {
                 mma_ts_f8_elect(tmem + C::TM_O, col, b, C::IDESC_PV, acc);
@@ -450,55 +493,95 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
   } else if (warp == 3) {
     // =============================================================== row scales (FP8)
     if constexpr (C::V8) {
-      uint32_t g = 0;
+      // Copies of kAhead tiles are in flight (a load a tile at a time would cost its whole latency a
+      // tile); a lane then turns the scales it copied into what the softmax reads.
+      constexpr int kAhead = 4;
+      static_assert(NS > kAhead, "scale ring");
+      Walk a = walk_begin(), w = a;
+      int ai = 0, wi = 0;  // tile of the segment: the next to copy, the next to finish
       bool ok = true;
-      Walk w = walk_begin();
-      for (uint32_t k = 0; ok && w.rem > 0; ++k) {
-        const int seg = walk_seg(w);
-        const size_t row = (static_cast<size_t>(w.b) * p.H + w.hm / p.mt) * p.n;
-        for (int i = 0; ok && i < seg; ++i, ++g) {
-          const uint32_t s = g % NS, use = g / NS;
-          float x[3][4];  // the loads do not wait for the buffer
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = (w.t + i) * BN + 32 * e + lane;
-            const bool in = j < w.len.end;
-            x[0][e] = in ? p.k1_scales[row + j] : 0.f;
-            x[1][e] = (!V2 && in) ? p.k2_scales[row + j] : 0.f;
-            x[2][e] = in ? p.v_scales[row + j] : 0.f;
-          }
-          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[s], (use - 1) & 1u, ab));
-          float* dst = reinterpret_cast<float*>(smem + C::OFF_SC) + s * 512;
+      float* const ring = reinterpret_cast<float*>(smem + C::OFF_SC);
+      auto copy_next = [&](int f) {
+        if (ok && f < count) {
+          const int s = f % NS, use = f / NS;
+          if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[s], static_cast<uint32_t>(use - 1) & 1u, ab));
+          const size_t row = (static_cast<size_t>(a.b) * p.H + a.hm / p.mt) * p.n;
+          const int key0 = (a.t + ai) * BN;
+          const uint32_t dst = smem_u32(ring + s * 512);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 32 * e + lane;
-            dst[j] = x[0][e];
-            dst[128 + j] = x[1][e];
-            // The scale, at the top of the range, and the log2 that the reference maximum goes
-            // by: at least 2^-100, so that the sum of weights stays far below fp32's end.
-            dst[256 + j] = x[2][e] * exp2f(kTreeTopLog2);
-            dst[384 + j] = fmaxf(log2f(x[2][e]), -100.f);
+            const int in = key0 + j < a.len.end ? 4 : 0;  // (rows past the end: zeros)
+            const size_t at = row + (in ? key0 + j : 0);
+            cp_async4(dst + 4 * j, p.k1_scales + at, in);
+            if (!V2) cp_async4(dst + 4 * (128 + j), p.k2_scales + at, in);
+            cp_async4(dst + 4 * (256 + j), p.v_scales + at, in);
           }
-          mbar_arrive(&sc_full[s]);
+          if (++ai == walk_seg(a)) {
+            walk_next(a, ai);
+            ai = 0;
+          }
         }
-        walk_next(w, seg);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int f = 0; f < kAhead; ++f) copy_next(f);
+      for (int g = 0; ok && g < count; ++g) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        float* dst = ring + (g % NS) * 512;
+        const int key0 = (w.t + wi) * BN;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 32 * e + lane;
+          const float x = dst[256 + j];
+          // A value scale that is not finite makes its row NaN: for everybody (P is NaN), or, for a
+          // drafted row, for the tokens that see it (marked by its log2, and weightless).
+          const bool bad = !(fabsf(x) < INFINITY);
+          const bool drafted = key0 + j >= w.len.L;
+          // The scale, at the top of the range (and at two_e4m3x4's 2^-8), and the log2 that the
+          // reference maximum goes by: at least 2^-100, so that the sum of weights stays far below
+          // fp32's end.
+          dst[256 + j] = bad ? (drafted ? 0.f : __uint_as_float(0x7fffffffu)) : x * kTreeValueMult;
+          dst[384 + j] = bad ? __uint_as_float(0x7fffffffu) : fmaxf(__log2f(x), -100.f);
+        }
+        mbar_arrive(&sc_full[g % NS]);
+        if (++wi == walk_seg(w)) {
+          walk_next(w, wi);
+          wi = 0;
+        }
+        copy_next(g + kAhead);
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else {
     // =============================================================== softmax
-    const int wq = warp & 3, half = (warp - 4) >> 2;
-    const int map = wq >> 1;
-    if ((wq & 1) == 0 || wide) {
-      const int r = (wq & 1) * 32 + lane;    // row of the map
+    const int wq = warp & 3, qd = (warp - 4) >> 2;  // lane quarter, which of its four warps
+    const int map = wq >> 1, sub = WIDE ? 0 : (wq & 1);
+    {
+      constexpr int NC = WIDE ? 32 : 16;                       // key columns of this warp,
+      const int col0 = WIDE ? 32 * qd : 64 * sub + 16 * qd;    // from this one
+      constexpr int OC = DV / 4;                               // output channels it rescales and writes
+      const int r = WIDE ? (wq & 1) * 32 + lane : lane;        // row of the map
       const bool valid = r < p.R;
-      const int row = wq * 32 + lane;        // MMA row
+      const int row = wq * 32 + lane;                          // MMA row
       const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
       const int pr = r / p.T, tok = r - pr * p.T;
-      // index among the threads of the softmax warps with rows
-      const int ti = (half * (wide ? 4 : 2) + (wide ? wq : (wq >> 1))) * 32 + lane;
-      const int nth = nact * 32;
+      const int ti = threadIdx.x - 128;                        // index among the softmax threads
+      constexpr int nth = NACT * 32;
+      if constexpr (C::PSEP && !WIDE) {  // the other half's keys: weights of zero, for good
+#pragma unroll
+        for (uint32_t s = 0; s < 2; ++s) {
+          const uint32_t tz = tl + C::TM_P + s * C::P_STEP;
+          if constexpr (C::V8) {
+            tmem_st4(tz + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
+            tmem_st4(tz + 32u + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
+          } else {
+            const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            tmem_st8(tz + 32u * (sub ^ 1) + 8u * qd, zero);
+          }
+        }
+        tmem_st_wait();
+      }
       float* xm = reinterpret_cast<float*>(smem + C::OFF_XM);
-      float* xl = reinterpret_cast<float*>(smem + C::OFF_XL);
       float* qi = reinterpret_cast<float*>(smem + C::OFF_QI);
       const float top = C::V8 ? kTreeRescale8Log2 : kTreeRescaleLog2;
       uint32_t g = 0;
@@ -529,8 +612,11 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
           const int qr = (V2 ? 64 : 128) * m + r2;  // row of the shared buffer
           uint8_t* q = smem + C::OFF_Q;
           if constexpr (!C::K8) {
-            if (in)
-              *reinterpret_cast<uint4*>(q + (ch >> 3) * (C::QROWS * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = x;
+            if (in) {
+              uint8_t* dst = q + (ch >> 3) * (C::QROWS * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4);
+              *reinterpret_cast<uint4*>(dst) = x;
+              if (!WIDE) *reinterpret_cast<uint4*>(dst + 32 * 128) = x;  // (the second copy of the rows)
+            }
           } else {
             // The row scaled by a power of two that puts its largest magnitude in [128, 256), in
             // two e4m3 terms: exact for every element down to 2^-10 of the largest.
@@ -567,6 +653,10 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
               uint8_t* dst = q + qr * C::KROW + (sw << 4) + 8 * (ch & 1);
               *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
               *reinterpret_cast<uint2*>(dst + C::Q_TERM) = make_uint2(lo8[0], lo8[1]);
+              if (!WIDE) {
+                *reinterpret_cast<uint2*>(dst + 32 * C::KROW) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(dst + 32 * C::KROW + C::Q_TERM) = make_uint2(lo8[0], lo8[1]);
+              }
               if (ch == 0) qi[64 * m + r2] = __int_as_float((127 - sh) << 23);
             }
           }
@@ -592,59 +682,72 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
           mbar_wait(&s_full[s], (g >> 1) & 1u, ab);
           __syncwarp();
           tc_fence_after();
-          uint32_t x[2][32];
-          tmem_ld32(tS + 64u * half, x[0]);
-          tmem_ld32(tS + 64u * half + 32u, x[1]);
-          const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + 64 * half;
+          uint32_t x[NC];
+          if constexpr (WIDE)
+            tmem_ld32(tS + col0, x);
+          else
+            tmem_ld16(tS + col0, x);
+          const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + col0;
           if constexpr (C::V8) {
             mbar_wait(&sc_full[g % NS], (g / NS) & 1u, ab);
             __syncwarp();
           }
-          tmem_ld_wait2(x[0], x[1]);
-          // ---- scores in the log2 domain
-          const bool special = key0 + BN > w.len.L;  // the tile reaches into the drafted keys or past them
-          unsigned long long vis = ~0ull;
-          if (special) {
-            const int rel = key0 + 64 * half - w.len.L;  // drafted token of the first column
-            vis = rel >= 64 ? 0ull : rel >= 0 ? see >> rel : rel <= -64 ? ~0ull : (see << -rel) | ((1ull << -rel) - 1ull);
+          if constexpr (WIDE)
+            tmem_ld_wait(x);
+          else
+            tmem_ld_wait16(x);
+          if constexpr (C::PSEP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[s]);
           }
+          // ---- scores
+          const bool special = key0 + BN > w.len.L;  // the tile reaches into the drafted keys or past them
+          const uint64_t rc2 = f2pack(rc, rc);
           float pm = -INFINITY;
           if constexpr (C::V8) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 ks = *reinterpret_cast<const float4*>(sc + 128 * ((map && !V2) ? 1 : 0) + 32 * q + c);
-                const float4 lv = *reinterpret_cast<const float4*>(sc + 384 + 32 * q + c);
-                const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, ll[4] = {lv.x, lv.y, lv.z, lv.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float v = __uint_as_float(x[q][c + e]) * rc * kk[e];
-                  if (special && !((vis >> (32 * q + c + e)) & 1ull)) v = -INFINITY;
-                  x[q][c + e] = __float_as_uint(v);
-                  pm = fmaxf(pm, v + ll[e]);
-                }
-              }
-          } else {
-            if (special) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (!((vis >> (32 * q + c)) & 1ull)) x[q][c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < NC; c += 4) {
+              const float4 ks = *reinterpret_cast<const float4*>(sc + 128 * ((map && !V2) ? 1 : 0) + c);
+              const float4 lv = *reinterpret_cast<const float4*>(sc + 384 + c);
+              float t0, t1, y0, y1;
+              const uint64_t ta = mul2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2pack(ks.x, ks.y));
+              const uint64_t tb = mul2(f2pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2pack(ks.z, ks.w));
+              f2unpack(fma2(ta, rc2, f2pack(lv.x, lv.y)), y0, y1);
+              pm = max3(pm, y0, y1);
+              f2unpack(fma2(tb, rc2, f2pack(lv.z, lv.w)), y0, y1);
+              pm = max3(pm, y0, y1);
+              f2unpack(ta, t0, t1);
+              x[c] = __float_as_uint(t0);
+              x[c + 1] = __float_as_uint(t1);
+              f2unpack(tb, t0, t1);
+              x[c + 2] = __float_as_uint(t0);
+              x[c + 3] = __float_as_uint(t1);
             }
+          } else if (!special) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int c = 0; c < 32; c += 2)
-                pm = max3(pm, __uint_as_float(x[q][c]), __uint_as_float(x[q][c + 1]));
-            pm *= rc;
+            for (int c = 0; c < NC; c += 2) pm = max3(pm, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
           }
-          // ---- the row's maximum over both halves of the tile
-          float* xg = xm + (g & 1u) * 256;
-          xg[half * 128 + row] = pm;
-          named_bar_sync(1 + wq, 64);
-          pm = fmaxf(pm, xg[(half ^ 1) * 128 + row]);
+          if (special) {  // hide what the row does not see
+            const int rel = key0 + col0 - w.len.L;  // drafted token of the first column
+            const uint32_t vis = static_cast<uint32_t>(
+                rel >= 64 ? 0ull : rel >= 0 ? see >> rel : rel <= -64 ? ~0ull : (see << -rel) | ((1ull << -rel) - 1ull));
+            pm = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              if (!((vis >> c) & 1u)) x[c] = __float_as_uint(-INFINITY);
+              if constexpr (C::V8)
+                pm = fmaxf(pm, fmaf(__uint_as_float(x[c]), rc, sc[384 + c]));
+              else
+                pm = fmaxf(pm, __uint_as_float(x[c]));
+            }
+          }
+          if (!C::V8) pm *= rc;  // (rc > 0)
+          // ---- the row's maximum over the quarter's four warps
+          float* xg = xm + (g & 1u) * 512;
+          xg[qd * 128 + row] = pm;
+          named_bar_sync(1 + wq, 128);
+          pm = fmaxf(max3(xg[row], xg[128 + row], xg[256 + row]), xg[384 + row]);
           const float m_new = fmaxf(m_used, pm);
           const bool rescale = __any_sync(0xffffffffu, m_new > m_used + top);
           if (rescale) {
@@ -655,70 +758,92 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
               mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
               __syncwarp();
               tc_fence_after();
-#pragma unroll
-              for (int q = 0; q < DV / 64; ++q) {
+#pragma unroll 1
+              for (int q = 0; q < OC / 32; ++q) {
                 uint32_t o[32];
-                tmem_ld32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+                tmem_ld32(tl + C::TM_O + OC * qd + 32u * q, o);
                 tmem_ld_wait(o);
 #pragma unroll
                 for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                tmem_st32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+                tmem_st32(tl + C::TM_O + OC * qd + 32u * q, o);
               }
             }
           }
           const float ref = (m_used == -INFINITY) ? 0.f : m_used;
-          // ---- weights, in place of the scores
+          // ---- weights
+          const uint32_t tP = tl + C::TM_P + s * C::P_STEP;
+          const uint64_t nb2 = f2pack(-ref, -ref);
+          uint64_t acc[2] = {0, 0};
           if constexpr (C::V8) {
-            float l0 = 0.f, l1 = 0.f;
-            uint32_t hi[16], lo8[16];
+            uint32_t hi[NC / 4], lo8[NC / 4];
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int c = 0; c < NC; c += 4) {
+              const float4 vs = *reinterpret_cast<const float4*>(sc + 256 + c);
+              float v[4];
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 vs4 = *reinterpret_cast<const float4*>(sc + 256 + 32 * q + c);
-                const float vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
-                float pw[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pw[e] = ex2(__uint_as_float(x[q][c + e]) - ref);
-                l0 += pw[0] + pw[1];
-                l1 += pw[2] + pw[3];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  pw[e] *= vs[e];
-                  // (a hidden row's scale may be anything)
-                  if (special && !((vis >> (32 * q + c + e)) & 1ull)) pw[e] = 0.f;
-                }
-                const uint32_t a = e4m3x2(pw[0], pw[1]), b = e4m3x2(pw[2], pw[3]);
-                const float2 fa = e4m3x2_value(a), fb = e4m3x2_value(b);
-                hi[(32 * q + c) >> 2] = a | (b << 16);
-                lo8[(32 * q + c) >> 2] = e4m3x2(pw[0] - fa.x, pw[1] - fa.y) | (e4m3x2(pw[2] - fb.x, pw[3] - fb.y) << 16);
-              }
-            l += l0 + l1;
-            tmem_st16(tS + 16u * half, hi);
-            tmem_st16(tS + 32u + 16u * half, lo8);
-          } else {
-            const uint64_t rc2 = f2pack(rc, rc), nb2 = f2pack(-ref, -ref);
-            uint64_t acc[2] = {0, 0};
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
+              for (int e = 0; e < 2; ++e) {
                 float a0, a1;
-                f2unpack(fma2(f2pack(__uint_as_float(x[q][c]), __uint_as_float(x[q][c + 1])), rc2, nb2), a0, a1);
-                const float p0 = ex2(a0), p1 = ex2(a1);
-                acc[q] = add2(acc[q], f2pack(p0, p1));
-                x[q][c >> 1] = pack_bf16x2(p0, p1);
+                f2unpack(fma2(f2pack(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), rc2, nb2), a0, a1);
+                const uint64_t pw = f2pack(ex2(a0), ex2(a1));
+                acc[e] = add2(acc[e], pw);
+                f2unpack(mul2(pw, e ? f2pack(vs.z, vs.w) : f2pack(vs.x, vs.y)), v[2 * e], v[2 * e + 1]);
               }
+              two_e4m3x4(v[0], v[1], v[2], v[3], hi[c >> 2], lo8[c >> 2]);
+            }
+            if (C::PSEP && g >= 2) {  // the P tile's last reader
+              mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
+              __syncwarp();
+              tc_fence_after();
+            }
+            if constexpr (WIDE) {
+              tmem_st8(tP + 8u * qd, hi);
+              tmem_st8(tP + 32u + 8u * qd, lo8);
+            } else {
+              tmem_st4(tP + 16u * sub + 4u * qd, hi[0], hi[1], hi[2], hi[3]);
+              tmem_st4(tP + 32u + 16u * sub + 4u * qd, lo8[0], lo8[1], lo8[2], lo8[3]);
+              if constexpr (!C::PSEP) {
+                tmem_st4(tP + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
+                tmem_st4(tP + 32u + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
+              }
+            }
+          } else {
+            uint32_t pk[NC / 2];
+#pragma unroll
+            for (int c = 0; c < NC; c += 2) {
+              float a0, a1;
+              f2unpack(fma2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rc2, nb2), a0, a1);
+              const float p0 = ex2(a0), p1 = ex2(a1);
+              acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], f2pack(p0, p1));
+              pk[c >> 1] = pack_bf16x2(p0, p1);
+            }
+            if (C::PSEP && g >= 2) {
+              mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
+              __syncwarp();
+              tc_fence_after();
+            }
+            if constexpr (WIDE) {
+              tmem_st16(tP + 16u * qd, pk);
+            } else {
+              tmem_st8(tP + 32u * sub + 8u * qd, pk);
+              if constexpr (!C::PSEP) {
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                tmem_st8(tP + 32u * (sub ^ 1) + 8u * qd, zero);
+              }
+            }
+          }
+          {
             float s0, s1;
             f2unpack(add2(acc[0], acc[1]), s0, s1);
             l += s0 + s1;
-            tmem_st16(tS + 32u * half, reinterpret_cast<const uint32_t(&)[16]>(x[0]));
-            tmem_st16(tS + 32u * half + 16u, reinterpret_cast<const uint32_t(&)[16]>(x[1]));
           }
           if (special) {
             // Value rows that some token must not see: rows past the drafted ones hold whatever the
             // cache held (zeroed here), and a drafted row with a NaN or an infinity is zeroed and
             // remembered, so that it reaches only the tokens that see it.
+            if (C::V8 && ti < BN && key0 + ti >= w.len.L && key0 + ti < w.len.end) {
+              const float lv = *(reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + 384 + ti);
+              if (lv != lv) atomicOr(&poison[k % 3], 1ull << (key0 + ti - w.len.L));
+            }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
               const uint32_t f = 2 * g + part;
@@ -770,28 +895,32 @@ __global__ void __launch_bounds__(384, 1) tree_kernel(const __grid_constant__ Tr
         mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
         __syncwarp();
         tc_fence_after();
-        if (half == 1) xl[(k & 1u) * 128 + row] = l;
-        named_bar_sync(1 + wq, 64);
+        float* xl = xm + (g & 1u) * 512;
+        xl[qd * 128 + row] = l;
+        named_bar_sync(1 + wq, 128);
+        if (qd == 0) l = (l + xl[128 + row]) + (xl[256 + row] + xl[384 + row]);
+        named_bar_sync(1 + wq, 128);  // (the next segment's maxima go there)
         if (ti == 0) poison[(k + 2) % 3] = 0;
         const size_t unit = static_cast<size_t>(w.b) * HM + w.hm;
+        const int rs = WIDE ? p.R : 2 * p.R, ri = sub * p.R + r;  // rows of a map in the state, this one
         float* piece = p.ws + (unit + blockIdx.x) * tree_state_floats(p.R, DV);
-        if (half == 0 && valid) {
-          l += xl[(k & 1u) * 128 + row];
+        if (qd == 0 && valid) {
           if (see & poison[k % 3]) l = __uint_as_float(0x7fffffffu);
-          if (DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM && r < kTreeRows, r))
-            reinterpret_cast<float2*>(piece)[map * p.R + r] = make_float2(m_used, l);
+          if (DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM && ri < kTreeRows, ri))
+            reinterpret_cast<float2*>(piece)[map * rs + ri] = make_float2(m_used, l);
         }
-        float4* o4 = reinterpret_cast<float4*>(piece + 4 * p.R) + (static_cast<size_t>(map) * (DV / 4) + (DV / 8) * half) * p.R;
-#pragma unroll
-        for (int q = 0; q < DV / 64; ++q) {
+        float4* o4 = reinterpret_cast<float4*>(piece + 4 * rs) +
+                     (static_cast<size_t>(map) * (DV / 4) + (OC / 4) * qd) * rs + ri;
+#pragma unroll 1
+        for (int q = 0; q < OC / 32; ++q) {
           uint32_t o[32];
-          tmem_ld32(tl + C::TM_O + (DV / 2) * half + 32u * q, o);
+          tmem_ld32(tl + C::TM_O + OC * qd + 32u * q, o);
           tmem_ld_wait(o);
-          if (valid && DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM, r)) {
+          if (valid && DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM, ri)) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              o4[(8 * q + c) * p.R + r] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                                      __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+            for (int c = 0; c < 8; ++c, o4 += rs)
+              *o4 = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]), __uint_as_float(o[4 * c + 2]),
+                                __uint_as_float(o[4 * c + 3]));
           }
         }
         tc_fence_before();
@@ -841,22 +970,26 @@ __global__ void __launch_bounds__(DV) tree_combine_kernel(const __grid_constant_
     const int c0 = static_cast<int>(((s + 1) * G - 1) / W), c1 = static_cast<int>(((e + 1) * G - 1) / W);
     const size_t pf = tree_state_floats(p.R, DV);
     const float* src = p.ws + (static_cast<size_t>(unit) + c0) * pf;
+    const int subs = p.R > 32 ? 1 : 2, rs = subs * p.R;
     float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, acc[2][4] = {};
     for (int c = c0; c <= c1; ++c, src += pf) {
+#pragma unroll 2
+      for (int sub = 0; sub < subs; ++sub)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float2 ml = reinterpret_cast<const float2*>(src)[m * p.R + r];
-        const float4 o = reinterpret_cast<const float4*>(src + 4 * p.R)[(static_cast<size_t>(m) * (DV / 4) + c4) * p.R + r];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen in this state
-        const float mn = fmaxf(M[m], ml.x);
-        const float fo = (M[m] == mn) ? 1.f : ex2(M[m] - mn), fn = (ml.x == mn) ? 1.f : ex2(ml.x - mn);
-        M[m] = mn;
-        L[m] = L[m] * fo + ml.y * fn;
-        acc[m][0] = acc[m][0] * fo + o.x * fn;
-        acc[m][1] = acc[m][1] * fo + o.y * fn;
-        acc[m][2] = acc[m][2] * fo + o.z * fn;
-        acc[m][3] = acc[m][3] * fo + o.w * fn;
-      }
+        for (int m = 0; m < 2; ++m) {
+          const int ri = sub * p.R + r;
+          const float2 ml = reinterpret_cast<const float2*>(src)[m * rs + ri];
+          const float4 o = reinterpret_cast<const float4*>(src + 4 * rs)[(static_cast<size_t>(m) * (DV / 4) + c4) * rs + ri];
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen in this state
+          const float mn = fmaxf(M[m], ml.x);
+          const float fo = (M[m] == mn) ? 1.f : ex2(M[m] - mn), fn = (ml.x == mn) ? 1.f : ex2(ml.x - mn);
+          M[m] = mn;
+          L[m] = L[m] * fo + ml.y * fn;
+          acc[m][0] = acc[m][0] * fo + o.x * fn;
+          acc[m][1] = acc[m][1] * fo + o.y * fn;
+          acc[m][2] = acc[m][2] * fo + o.z * fn;
+          acc[m][3] = acc[m][3] * fo + o.w * fn;
+        }
     }
     const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
     const float a1 = (L[0] == 0.f) ? 0.f : o_mult / L[0], a2 = (L[1] == 0.f) ? 0.f : -coef * o_mult / L[1];
@@ -895,7 +1028,7 @@ __global__ void __launch_bounds__(DV) tree_combine_kernel(const __grid_constant_
 template <int D, bool V2, int FMT>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   using C = TreeCfg<D, V2, FMT>;
-  auto kern = tree_kernel<D, V2, FMT>;
+  auto kern = p.R > 32 ? tree_kernel<D, V2, FMT, true> : tree_kernel<D, V2, FMT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];

@@ -211,8 +211,8 @@ def test_tree_refusals(L):
 
 
 def test_tree_workspace_sizes(L):
-    # one partial state of 2 R (dv + 2) floats a row tile and a CTA
-    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 2 * 5 * 130 * 4
+    # one partial state of 2 R (dv + 2) floats (R up to 32: twice) a row tile and a CTA
+    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 2 * 10 * 130 * 4
     assert da.v2_tree_decode_workspace_bytes(1, 20, 16, 2, 128) == (1 * 2 * 2 + 160) * 2 * 60 * 130 * 4
     assert da.v2_tree_decode_workspace_bytes(1, 64, 8, 1, 128) == (4 + 160) * 2 * 64 * 130 * 4
     assert da.tree_decode_workspace_bytes(1, 65, 1, 64) == 0
