@@ -44,11 +44,14 @@ int sms_or_default() {
 }
 
 // 4-D map over a contiguous [B, n, heads, W] tensor of bf16 or bytes: box =
-// `box_bytes` (64 or 128, the swizzle) of a row x 1 head x `rows` tokens.  L2 fetches 128 bytes at a
-// time: with 256 a 128-byte row (bf16 keys at d = 64) brings its neighbour head's along, which is gone
-// again before that head's CTA asks for it (B8 H16 n32768 d64: 393 us and 1.23x the bytes, against 323).
+// `box_bytes` (64 or 128, the swizzle) of a row x 1 head x `rows` tokens.
+// `side` heads are read side by side at about the same time: L2 fetches what
+// they ask for together (256 bytes at most).  Fetching more brings rows that
+// are gone again before their reader comes, fetching less leaves DRAM with
+// short bursts: e4m3 V1 d64 B8 H16 n32768, a 64-byte row a head, 8 side by
+// side: 223 us at 64 bytes, 199 us at 256; alone 240 us at 64, 338 us at 256.
 diffattn_status cache_map(CUtensorMap* m, const void* base, int B, int n, int heads, int W, int es, int box_bytes,
-                          int rows) {
+                          int rows, int side) {
   dh::EncodeTiled enc;
   diffattn_status s = dh::encoder(&enc);
   if (s != DIFFATTN_OK) return s;
@@ -62,7 +65,10 @@ diffattn_status cache_map(CUtensorMap* m, const void* base, int B, int n, int he
       enc(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base),
           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
           box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+          row * side >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+          : row * side >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                              : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DIFFATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
   return DIFFATTN_OK;
 }
@@ -231,6 +237,7 @@ diffattn_status keep(const char* fn, diffattn_cache_format fmt, int B, int A, in
 
 // CTAs the tree decode's key tiles are dealt to, at most (its workspace has a state for each).
 constexpr int kTreeMaxCtas = 160;
+constexpr int kTreeTeam = 8;  // CTAs of a team, at most
 
 struct TreeShape {
   int pairs, ppt, mt, R;
@@ -249,7 +256,7 @@ TreeShape tree_shape(int B, int T, int H, int pairs) {
 
 size_t tree_workspace(int B, int T, int H, int pairs, int dv) {
   const TreeShape s = tree_shape(B, T, H, pairs);
-  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, dv) * sizeof(float);
+  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, da::tree_subs(s.R), dv) * sizeof(float);
 }
 
 diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, int T, int H, int pairs, int n, int d,
@@ -281,12 +288,18 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   if (!aligned(workspace, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   int* status = nullptr;
   if ((st = dh::status_address(&status)) != DIFFATTN_OK) return st;
+  // Neighbouring heads side by side: their rows of a token are neighbours in memory.
+  p.team = 1;
+  while (p.team < kTreeTeam && H * sh.mt % (2 * p.team) == 0) p.team *= 2;
+  const int ctas = std::min(sms_or_default(), kTreeMaxCtas);
+  p.teams = static_cast<int>(std::max<long long>(1, std::min<long long>(tiles / p.team, ctas / p.team)));
   const bool k8 = fmt != DIFFATTN_CACHE_BF16, v8 = fmt == DIFFATTN_CACHE_FP8;
   const int nn = n > 0 ? n : 1;
+  const int side = std::max(1, p.team / sh.mt);  // heads
   const int kbox = (k8 && d == 64) ? 64 : 128;
-  if ((st = cache_map(&p.tm_k1, k1, B, nn, H, d, k8 ? 1 : 2, kbox, 128)) != DIFFATTN_OK) return st;
-  if (!v2 && (st = cache_map(&p.tm_k2, k2, B, nn, H, d, k8 ? 1 : 2, kbox, 128)) != DIFFATTN_OK) return st;
-  if ((st = cache_map(&p.tm_v, v, B, nn, H, dv, v8 ? 1 : 2, 128, 64)) != DIFFATTN_OK) return st;
+  if ((st = cache_map(&p.tm_k1, k1, B, nn, H, d, k8 ? 1 : 2, kbox, 128, side)) != DIFFATTN_OK) return st;
+  if (!v2 && (st = cache_map(&p.tm_k2, k2, B, nn, H, d, k8 ? 1 : 2, kbox, 128, side)) != DIFFATTN_OK) return st;
+  if ((st = cache_map(&p.tm_v, v, B, nn, H, dv, v8 ? 1 : 2, 128, da::tree_value_keys(dv, v8), side)) != DIFFATTN_OK) return st;
   p.q1 = static_cast<const __nv_bfloat16*>(q1);
   p.q2 = static_cast<const __nv_bfloat16*>(q2);
   p.k1_scales = kscales[0];
@@ -307,7 +320,7 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   p.ppt = sh.ppt;
   p.mt = sh.mt;
   p.R = sh.R;
-  p.grid = static_cast<int>(std::max<long long>(1, std::min<long long>({tiles, sms_or_default(), kTreeMaxCtas})));
+  p.subs = da::tree_subs(sh.R);
   p.ws = static_cast<float*>(workspace);
   p.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

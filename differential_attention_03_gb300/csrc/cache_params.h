@@ -66,7 +66,7 @@ struct KeepParams {
 struct TreeParams {
   CUtensorMap tm_k1;  // key caches: boxes of 128 keys x 128 bytes (e4m3 at d = 64: 64 bytes)
   CUtensorMap tm_k2;  // (V1 only)
-  CUtensorMap tm_v;   // value cache: boxes of 64 keys x 128 bytes
+  CUtensorMap tm_v;   // value cache: boxes of tree_value_keys keys x 128 bytes
   const __nv_bfloat16* q1;  // V1 [B, T, H, d]; V2 [B, T, Hq, d]
   const __nv_bfloat16* q2;  // V1 only
   const float* k1_scales;   // fp8: [B, H, n]
@@ -88,17 +88,24 @@ struct TreeParams {
   int ppt;            // pairs of one row tile
   int mt;             // row tiles of a key head
   int R;              // rows of one map in a row tile: ppt * T <= 64
-  int grid;           // CTAs the key tiles are dealt to
+  int team;           // CTAs that walk the same tiles of neighbouring units side by side (divides H mt)
+  int teams;          // teams the key tiles are dealt to
+  int subs;           // partial states of a CTA and unit
   float* ws;
   int* status;
 };
 
+// Keys of one value box of the tree decode.
+__host__ __device__ constexpr int tree_value_keys(int dv, bool v8) { return dv * (v8 ? 1 : 2) == 512 ? 32 : 64; }
+
 constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree decode
 
-// Floats of one partial state of the tree decode: (maximum, sum) and O of R rows of both maps, twice
-// (each half of the keys its own) where the rows leave room.
-__host__ __device__ __forceinline__ size_t tree_state_floats(int R, int dv) {
-  return 2 * static_cast<size_t>(R > kTreeRows / 2 ? R : 2 * R) * (dv + 2);
+// Subsets of a CTA's keys that keep their own partial state (the fewer rows, the more).
+__host__ __device__ constexpr int tree_subs(int R) { return R <= 8 ? 4 : R <= 32 ? 2 : 1; }
+
+// Floats of a partial state of the tree decode: (maximum, sum) and O of R rows of both maps, for each subset.
+__host__ __device__ __forceinline__ size_t tree_state_floats(int R, int subs, int dv) {
+  return 2 * static_cast<size_t>(subs) * R * (dv + 2);
 }
 
 cudaError_t launch_rope(const RopeParams& p, bool f32, bool vec, int grid_x, int grid_y, cudaStream_t s);

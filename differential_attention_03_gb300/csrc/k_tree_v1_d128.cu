@@ -1,5 +1,5 @@
 // Tree decode, V1 at d = 128, in the three cache formats.
-#include "tree.cuh"
+#include "tree_launch.cuh"
 
 namespace da {
 

@@ -46,20 +46,15 @@
 // replaces the scores.
 #pragma once
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "cache_params.h"
-#include "ptx.cuh"
+#include "tree_common.cuh"
 
 #undef DA_BOUNDS_FILE
-#define DA_BOUNDS_FILE 12
+#define DA_BOUNDS_FILE 13
 
 namespace da {
 
 template <int D, bool V2, int FMT>
-struct TreeCfg {
+struct TreeRowsCfg {
   static constexpr bool K8 = FMT != kCacheBf16, V8 = FMT == kCacheFp8;
   static constexpr int BN = 128;              // keys of a tile
   static constexpr int DV = V2 ? D : 2 * D;
@@ -71,6 +66,7 @@ struct TreeCfg {
   static constexpr int VROW = DV * (V8 ? 1 : 2);
   static constexpr int VBOX = VROW / 128;
   static constexpr int VKEYS = 64;  // keys of a value slot
+  static constexpr int VBOXK = tree_value_keys(DV, V8);  // keys of a value box
   static constexpr int K_SLOT = BN * KROW, V_SLOT = VKEYS * VROW;
   static constexpr int QROWS = V2 ? 128 : 192;          // Q_even | Q_odd, or Q_1 | zeros | Q_2
   static constexpr int Q_TERM = QROWS * KROW;
@@ -105,63 +101,9 @@ struct TreeCfg {
   static_assert(K_SLOT % 1024 == 0 && V_SLOT % 1024 == 0 && Q_TERM % 1024 == 0, "swizzled boxes start on 1 KB");
 };
 
-constexpr float kTreeRescaleLog2 = 8.f;   // bf16 P: how far a score may exceed the reference maximum
-constexpr float kTreeTopLog2 = 7.f;       // e4m3 P: the reference maximum sits at 2^7 (e4m3 ends at 448) ...
-constexpr float kTreeValueMult = 0.5f;     // 2^7, times two_e4m3x4's 2^-8
-constexpr float kTreeRescale8Log2 = 1.f;  // ... and may be exceeded by a factor of two
-
-// A sequence's committed keys, its drafted tokens, the end of its keys and its tiles.
-struct TreeLen {
-  int L, nt, end, tiles;
-};
-__device__ __forceinline__ TreeLen tree_len(const TreeParams& p, int b) {
-  TreeLen x;
-  x.L = max(0, min(p.lens ? p.lens[b] : p.n - p.T, p.n));
-  x.nt = max(0, min(p.ntok ? p.ntok[b] : p.T, p.T));
-  x.end = min(p.n, x.L + x.nt);
-  x.tiles = (x.end + 127) >> 7;
-  return x;
-}
-
-// Tiles of all sequences before `upto` and of all of them, per unit of a
-// sequence (each has the same units), by the whole CTA; scratch of 2 * 32 + 2
-// long longs.  Every thread returns with (before, total).
-__device__ __forceinline__ void tree_prefix(const TreeParams& p, int upto, long long* scratch, long long& before,
-                                            long long& total) {
-  long long a = 0, t = 0;
-  for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-    const int x = tree_len(p, b).tiles;
-    t += x;
-    if (b < upto) a += x;
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, x);
-    t += __shfl_xor_sync(0xffffffffu, t, x);
-  }
-  const int warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-    scratch[warp] = a;
-    scratch[32 + warp] = t;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < nw; ++w) {
-    before += scratch[w];
-    total += scratch[32 + w];
-  }
-  __syncthreads();
-}
-
-// Shared-memory matrix descriptor, 64-byte swizzle.
-__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(4) << 61;
-  return d;
+// 4-byte asynchronous copy to shared memory: `bytes` (4 or 0) of it from global, the rest zeros.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void mma_ts_f8_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -182,48 +124,9 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
                : "memory");
 }
 
-// Waits for this thread's outstanding tcgen05.ld into 16 registers (tied in).
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
-               :
-               : "memory");
-}
-
-// 4-byte asynchronous copy to shared memory: `bytes` (4 or 0) of it from global, the rest zeros.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-// Two floats as e4m3 codes (a in the low byte) and what the codes stand for.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
-}
-
-// Four non-negative floats, scaled to 2^-8 of what they stand for (at most
-// 448 2^-8), as two e4m3 terms each: hi truncates, hi + lo is within 2^-8 of
-// the value, or 2^-10 absolute, as a bf16 would be.  At that scale f16's
-// exponent field is e4m3's, so a code is bits 7-13 of the f16: pairs of f16
-// are shifted and masked as integers (the e4m3 conversion instructions take
-// about 16 issue cycles each, and bounded the kernel: 372 us against 247 us
-// at B8 H16 n32768 d64).  A NaN stays a NaN.
-__device__ __forceinline__ void two_e4m3x4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  uint32_t f0, f1, r0, r1;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f0) : "f"(b), "f"(a));
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f1) : "f"(d), "f"(c));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(f0), "r"(f0 & 0x7f807f80u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(f1), "r"(f1 & 0x7f807f80u));
-  hi = __byte_perm(f0 << 1, f1 << 1, 0x7531);
-  lo = __byte_perm(r0 * 2 + 0x00800080u, r1 * 2 + 0x00800080u, 0x7531);
-}
-
 template <int D, bool V2, int FMT, bool WIDE>
-__global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using C = TreeCfg<D, V2, FMT>;
+__global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
+  using C = TreeRowsCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
   grid_dep_launch_dependents();
   grid_dep_wait();
@@ -285,70 +188,14 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
   for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (rows without a query, and V1's zeros)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
 
-  // ---- this CTA's range of the line of tiles
-  const int HM = p.H * p.mt;
-  long long before, total;
-  tree_prefix(p, 0, scratch, before, total);
-  const long long W = total * HM;
-  const long long G = min(static_cast<long long>(p.grid), max(W, 1ll));  // no CTA between two with tiles is without
-  const long long lo = W * blockIdx.x / G, hi = W * (blockIdx.x + 1) / G;
-  const int count = blockIdx.x < G ? static_cast<int>(hi - lo) : 0;
-  if (warp == 0 && count > 0) {  // the sequence that tile `lo` falls in: 32 sequences a step
-    long long base = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const long long mine = (b0 + lane < p.B) ? static_cast<long long>(tree_len(p, b0 + lane).tiles) * HM : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-        if (lane >= x) incl += y;
-      }
-      const long long excl = base + incl - mine;
-      const bool here = lo >= excl && lo < excl + mine;
-      if (here) {
-        const int tiles = static_cast<int>(mine / HM);
-        start[0] = b0 + lane;
-        start[1] = static_cast<int>((lo - excl) / tiles);
-        start[2] = static_cast<int>((lo - excl) % tiles);
-      }
-      if (__any_sync(0xffffffffu, here)) break;
-      base += __shfl_sync(0xffffffffu, incl, 31);
-    }
-  }
+  const int groups = p.H * p.mt / p.team;  // of units of a sequence
+  const int count = tree_range(p, groups, scratch, start);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const AbortState ab{abort_flag, p.status};
-
-  // Every role walks the same segments: the CTA's tiles of one unit each.
-  struct Walk {
-    int b, hm, t, rem;
-    TreeLen len;
-  };
-  auto walk_begin = [&]() {
-    Walk w;
-    w.rem = count;
-    w.b = count > 0 ? start[0] : 0;
-    w.hm = count > 0 ? start[1] : 0;
-    w.t = count > 0 ? start[2] : 0;
-    if (count > 0) w.len = tree_len(p, w.b);
-    return w;
-  };
-  auto walk_seg = [&](const Walk& w) { return min(w.rem, w.len.tiles - w.t); };
-  auto walk_next = [&](Walk& w, int seg) {
-    w.rem -= seg;
-    w.t = 0;
-    if (w.rem <= 0) return;
-    if (++w.hm == HM) {
-      w.hm = 0;
-      do {
-        ++w.b;
-        w.len = tree_len(p, w.b);
-      } while (w.len.tiles == 0 && w.b + 1 < p.B);
-    }
-  };
 
   if (warp == 0) {
     // =============================================================== producer
@@ -379,16 +226,17 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
           uint8_t* dst = smem + C::OFF_V + s * C::V_SLOT;
           if (DA_BOUNDS_V(b < p.B && h < p.H, key0))  // (a box past n reads zeros)
             for (int bx = 0; bx < C::VBOX; ++bx)
-              tma_load_4d(dst + bx * C::VKEYS * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
-                          key0 + part * C::VKEYS, b);
+              for (int r = 0; r < C::VKEYS / C::VBOXK; ++r)
+                tma_load_4d(dst + bx * C::VKEYS * 128 + r * C::VBOXK * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
+                            key0 + part * C::VKEYS + r * C::VBOXK, b);
         }
         return true;
       };
       int pb = 0, ph = 0, pk = -1;  // the tile whose values come after the next tile's keys
-      Walk w = walk_begin();
+      TreeWalk w = walk_begin(p, count, start);
       while (ok && w.rem > 0) {
         const int seg = walk_seg(w);
-        const int h = w.hm / p.mt;
+        const int h = walk_unit(p, w) / p.mt;
         for (int i = 0; ok && i < seg; ++i) {
           const int key0 = (w.t + i) * BN;
           ok = load_k(&p.tm_k1, w.b, h, key0) && (V2 || load_k(&p.tm_k2, w.b, h, key0));
@@ -397,7 +245,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
           ph = h;
           pk = key0;
         }
-        walk_next(w, seg);
+        walk_next(p, groups, w, seg);
       }
       if (ok && pk >= 0) load_v(pb, ph, pk);
       if (*ab.flag) {  // aborted: let the copies already issued land before the CTA exits
@@ -416,76 +264,84 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
       return v;
     };
     bool ok = true;
+    // (descriptors and bounds broadcast and hoisted: see tree_cols.cuh)
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     uint32_t g = 0;  // tiles so far
-    int fill = 0;
-    Walk w = walk_begin();
-    for (uint32_t k = 0; ok && w.rem > 0; ++k) {
-      const int seg = walk_seg(w);
+    uint32_t slot = 0, phase = 0;
+    TreeWalk w = walk_begin(p, count, start);
+    for (uint32_t k = 0; ok && __shfl_sync(0xffffffffu, w.rem, 0) > 0; ++k) {
+      const int seg = __shfl_sync(0xffffffffu, walk_seg(w), 0);
       if (warp == 1) {
+        const uint64_t dk0 = sdesc_rows<C::KBOXB>(smem_u32(smem + C::OFF_K), 16);
+        const uint64_t dq0 = sdesc_rows<C::KBOXB>(smem_u32(smem + C::OFF_Q), 16);
         ok = waitp(q_full, k & 1u);
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t s = g & 1u;
           // the buffer: its scores loaded, or (P in their place) their P V done
           if (g >= 2 && !waitp(C::PSEP ? &s_free[s] : &pv_done[s], ((g - 2) >> 1) & 1u)) ok = false;
-#pragma unroll 1
+          const uint32_t d = tm + C::TM_S + s * BN;
+#pragma unroll
           for (int m = 0; m < C::NMAP_K; ++m) {
-            const int slot = fill % NK;
-            if (ok && !waitp(&kfull[slot], static_cast<uint32_t>(fill / NK) & 1u)) ok = false;
+            if (ok && !waitp(&kfull[slot], phase)) ok = false;
             if (!ok) break;
-            ++fill;
-            const uint32_t qa = smem_u32(smem + C::OFF_Q) + m * 64 * C::KBOXB;  // rows 0-127 or 64-191
-            const uint32_t ka = smem_u32(smem + C::OFF_K + slot * C::K_SLOT);
-            const uint64_t dk = (C::KBOXB == 128) ? sdesc_sw128(ka, 16, 1024) : sdesc_sw64(ka, 16, 512);
-#pragma unroll 1
+            const uint32_t koff = slot * (C::K_SLOT >> 4);
+#pragma unroll
             for (int term = 0; term < C::NTERM; ++term) {
-              const uint32_t qt = qa + term * C::Q_TERM;
-              const uint64_t dq = (C::KBOXB == 128) ? sdesc_sw128(qt, 16, 1024) : sdesc_sw64(qt, 16, 512);
 #pragma unroll
               for (int st = 0; st < C::QK_STEPS; ++st) {
-                const uint64_t a = dq + static_cast<uint64_t>((((st >> 2) * (C::QROWS * 128)) + (st & 3) * 32) >> 4);
-                const uint64_t bd = dk + static_cast<uint64_t>((((st >> 2) * (BN * 128)) + (st & 3) * 32) >> 4);
+                // rows 0-127 or 64-191 of the shared query buffer
+                const uint64_t a = desc_at(
+                    dq0, (term * C::Q_TERM + m * 64 * C::KBOXB + (st >> 2) * (C::QROWS * 128) + (st & 3) * 32) >> 4);
+                const uint64_t bd = desc_at(dk0, koff + (((st >> 2) * (BN * 128) + (st & 3) * 32) >> 4));
                 const uint32_t acc = (m > 0 || term > 0 || st > 0) ? 1u : 0u;
                 if constexpr (C::K8)
-                  mma_ss_f8_elect(tmem + C::TM_S + s * BN, a, bd, C::IDESC_QK, acc);
+                  mma_ss_f8_elect(d, a, bd, C::IDESC_QK, acc);
                 else
-                  mma_ss_elect(tmem + C::TM_S + s * BN, a, bd, C::IDESC_QK, acc);
+                  mma_ss_elect(d, a, bd, C::IDESC_QK, acc);
               }
             }
             tc_commit_elect(&kempty[slot]);
+            if (++slot == NK) {
+              slot = 0;
+              phase ^= 1u;
+            }
           }
           if (ok) tc_commit_elect(&s_full[s]);
         }
       } else {
+        const uint64_t dv0 = sdesc_rows<128>(smem_u32(smem + C::OFF_V), C::VKEYS * 128);
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t s = g & 1u;
           if (!waitp(&p_ready[s], (g >> 1) & 1u)) ok = false;
-#pragma unroll 1
+          const uint32_t again = i > 0 ? 1u : 0u;
+#pragma unroll
           for (int part = 0; part < 2; ++part) {
-            const int slot = fill % NV;
-            if (ok && !waitp(&vfull[slot], static_cast<uint32_t>(fill / NV) & 1u)) ok = false;
+            if (ok && !waitp(&vfull[slot], phase)) ok = false;
             if (!ok) break;
-            ++fill;
-            const uint64_t dv =
-                sdesc_sw128(smem_u32(smem + C::OFF_V + slot * C::V_SLOT), C::VKEYS * 128, 1024);
             constexpr int KS = C::V8 ? 32 : 16;  // keys of an MMA
+            const uint32_t voff = slot * (C::V_SLOT >> 4);
 #pragma unroll
             for (int kk = 0; kk < C::VKEYS / KS; ++kk) {
-              const uint64_t b = dv + static_cast<uint64_t>((kk * KS * 128) >> 4);
-              const uint32_t col = tmem + C::TM_P + s * C::P_STEP + 8u * (part * (C::VKEYS / KS) + kk);
-              const uint32_t acc = (i > 0 || part > 0 || kk > 0) ? 1u : 0u;
+              const uint64_t b = desc_at(dv0, voff + ((kk * KS * 128) >> 4));
+              const uint32_t col = tm + C::TM_P + s * C::P_STEP + 8u * (part * (C::VKEYS / KS) + kk);
+              const uint32_t acc = (part > 0 || kk > 0) ? 1u : again;
               if constexpr (C::V8) {
-                mma_ts_f8_elect(tmem + C::TM_O, col, b, C::IDESC_PV, acc);
-                mma_ts_f8_elect(tmem + C::TM_O, col + 32u, b, C::IDESC_PV, 1u);
+                mma_ts_f8_elect(tm + C::TM_O, col, b, C::IDESC_PV, acc);
+                mma_ts_f8_elect(tm + C::TM_O, col + 32u, b, C::IDESC_PV, 1u);
               } else {
-                mma_ts_elect(tmem + C::TM_O, col, b, C::IDESC_PV, acc);
+                mma_ts_elect(tm + C::TM_O, col, b, C::IDESC_PV, acc);
               }
             }
             tc_commit_elect(&vempty[slot]);
+            if (++slot == NV) {
+              slot = 0;
+              phase ^= 1u;
+            }
           }
           if (ok) tc_commit_elect(&pv_done[s]);
         }
       }
-      walk_next(w, seg);
+      walk_next(p, groups, w, seg);
     }
     tc_commit_elect(&drained[warp - 1]);
     if (*ab.flag) mbar_wait_drain(&drained[warp - 1], 0, kWaitBudgetCycles);
@@ -497,7 +353,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
       // tile); a lane then turns the scales it copied into what the softmax reads.
       constexpr int kAhead = 4;
       static_assert(NS > kAhead, "scale ring");
-      Walk a = walk_begin(), w = a;
+      TreeWalk a = walk_begin(p, count, start), w = a;
       int ai = 0, wi = 0;  // tile of the segment: the next to copy, the next to finish
       bool ok = true;
       float* const ring = reinterpret_cast<float*>(smem + C::OFF_SC);
@@ -505,7 +361,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
         if (ok && f < count) {
           const int s = f % NS, use = f / NS;
           if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[s], static_cast<uint32_t>(use - 1) & 1u, ab));
-          const size_t row = (static_cast<size_t>(a.b) * p.H + a.hm / p.mt) * p.n;
+          const size_t row = (static_cast<size_t>(a.b) * p.H + walk_unit(p, a) / p.mt) * p.n;
           const int key0 = (a.t + ai) * BN;
           const uint32_t dst = smem_u32(ring + s * 512);
 #pragma unroll
@@ -518,7 +374,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
             cp_async4(dst + 4 * (256 + j), p.v_scales + at, in);
           }
           if (++ai == walk_seg(a)) {
-            walk_next(a, ai);
+            walk_next(p, groups, a, ai);
             ai = 0;
           }
         }
@@ -538,14 +394,14 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
           const bool bad = !(fabsf(x) < INFINITY);
           const bool drafted = key0 + j >= w.len.L;
           // The scale, at the top of the range (and at two_e4m3x4's 2^-8), and the log2 that the
-          // reference maximum goes by: at least 2^-100, so that the sum of weights stays far below
+          // reference maximum goes by: at least -100, so that the sum of weights stays far below
           // fp32's end.
           dst[256 + j] = bad ? (drafted ? 0.f : __uint_as_float(0x7fffffffu)) : x * kTreeValueMult;
           dst[384 + j] = bad ? __uint_as_float(0x7fffffffu) : fmaxf(__log2f(x), -100.f);
         }
         mbar_arrive(&sc_full[g % NS]);
         if (++wi == walk_seg(w)) {
-          walk_next(w, wi);
+          walk_next(p, groups, w, wi);
           wi = 0;
         }
         copy_next(g + kAhead);
@@ -585,11 +441,11 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
       float* qi = reinterpret_cast<float*>(smem + C::OFF_QI);
       const float top = C::V8 ? kTreeRescale8Log2 : kTreeRescaleLog2;
       uint32_t g = 0;
-      Walk w = walk_begin();
+      TreeWalk w = walk_begin(p, count, start);
       // (an aborted CTA walks on: every wait then returns at once, and no warp misses a named barrier)
       for (uint32_t k = 0; w.rem > 0; ++k) {
         const int seg = walk_seg(w);
-        const int h = w.hm / p.mt, mtile = w.hm - h * p.mt;
+        const int hm = walk_unit(p, w), h = hm / p.mt, mtile = hm - h * p.mt;
         // ---- the segment's queries (the previous segment's score MMAs have completed: every warp
         // here has seen its last s_full)
         const int pair0 = mtile * p.ppt, npair = min(p.ppt, p.pairs - pair0);
@@ -600,7 +456,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
           const int m = rr >= p.R, r2 = rr - m * p.R;
           const int pj = r2 / p.T, tj = r2 - pj * p.T;
           const bool in = i < 2 * p.R * NCH;
-          const bool have = in && pj < npair;
+          const bool have = in && pj < npair && tj < w.len.nt;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (have) {
             const size_t at = static_cast<size_t>(w.b) * p.T + tj;
@@ -613,7 +469,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
           uint8_t* q = smem + C::OFF_Q;
           if constexpr (!C::K8) {
             if (in) {
-              uint8_t* dst = q + (ch >> 3) * (C::QROWS * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4);
+              uint8_t* dst = q + (ch >> 3) * (C::QROWS * 128) + swizzled<128>(qr, ch & 7);
               *reinterpret_cast<uint4*>(dst) = x;
               if (!WIDE) *reinterpret_cast<uint4*>(dst + 32 * 128) = x;  // (the second copy of the rows)
             }
@@ -621,41 +477,22 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
             // The row scaled by a power of two that puts its largest magnitude in [128, 256), in
             // two e4m3 terms: exact for every element down to 2^-10 of the largest.
             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-            float f[8], amax = 0.f;
+            float amax = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[2 * e] = __uint_as_float(u[e] << 16);
-              f[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-              amax = fmaxf(amax, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
-            }
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
 #pragma unroll
             for (int o = 1; o < NCH; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int bexp = (__float_as_int(amax) >> 23) & 0xff;
-            const int sh = (amax > 0.f) ? max(-100, min(100, 134 - bexp)) : 0;
-            const float mul = __int_as_float((127 + sh) << 23);
-            uint32_t hi[2], lo8[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t a[2], b[2];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const float v0 = f[4 * e + 2 * z] * mul, v1 = f[4 * e + 2 * z + 1] * mul;
-                a[z] = e4m3x2(v0, v1);
-                const float2 back = e4m3x2_value(a[z]);
-                b[z] = e4m3x2(v0 - back.x, v1 - back.y);
-              }
-              hi[e] = a[0] | (a[1] << 16);
-              lo8[e] = b[0] | (b[1] << 16);
-            }
+            const int sh = e4m3_shift(amax);
+            uint2 hi, lo8;
+            split_e4m3x8(x, sh, hi, lo8);
             if (in) {
-              const int c16 = ch >> 1;  // 16-byte chunk of the code row
-              const int sw = (C::KBOXB == 128) ? (c16 ^ (qr & 7)) : (c16 ^ ((qr >> 1) & 3));
-              uint8_t* dst = q + qr * C::KROW + (sw << 4) + 8 * (ch & 1);
-              *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(dst + C::Q_TERM) = make_uint2(lo8[0], lo8[1]);
+              uint8_t* dst = q + swizzled<C::KBOXB>(qr, ch >> 1) + 8 * (ch & 1);
+              *reinterpret_cast<uint2*>(dst) = hi;
+              *reinterpret_cast<uint2*>(dst + C::Q_TERM) = lo8;
               if (!WIDE) {
-                *reinterpret_cast<uint2*>(dst + 32 * C::KROW) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(dst + 32 * C::KROW + C::Q_TERM) = make_uint2(lo8[0], lo8[1]);
+                *reinterpret_cast<uint2*>(dst + 32 * C::KROW) = hi;
+                *reinterpret_cast<uint2*>(dst + 32 * C::KROW + C::Q_TERM) = lo8;
               }
               if (ch == 0) qi[64 * m + r2] = __int_as_float((127 - sh) << 23);
             }
@@ -669,10 +506,7 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
         if (C::K8) rc *= valid ? qi[64 * map + r] : 0.f;
         if (FMT == kCacheFp8k) rc *= (map && !V2) ? p.k2_scale : p.k1_scale;
         // ---- what the row sees of the drafted tokens
-        const int nt = w.len.end - w.len.L;
-        unsigned long long see = 0;
-        if (valid) see = p.mask ? p.mask[w.b * p.mask_sb + tok] : ((2ull << tok) - 1ull);
-        if (nt < 64) see &= (1ull << nt) - 1ull;
+        const unsigned long long see = valid ? tree_sees(p, w.b, tok, w.len) : 0ull;
 
         float m_used = -INFINITY, l = 0.f;
         for (int i = 0; i < seg; ++i, ++g) {
@@ -837,47 +671,21 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
             l += s0 + s1;
           }
           if (special) {
-            // Value rows that some token must not see: rows past the drafted ones hold whatever the
-            // cache held (zeroed here), and a drafted row with a NaN or an infinity is zeroed and
-            // remembered, so that it reaches only the tokens that see it.
             if (C::V8 && ti < BN && key0 + ti >= w.len.L && key0 + ti < w.len.end) {
               const float lv = *(reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + 384 + ti);
               if (lv != lv) atomicOr(&poison[k % 3], 1ull << (key0 + ti - w.len.L));
             }
-#pragma unroll
+            // (the previous tile's P V first: the slots' earlier fills are then all used, so that the
+            // parities below mean this tile's)
+            if (g > 0) mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
+#pragma unroll 1
             for (int part = 0; part < 2; ++part) {
               const uint32_t f = 2 * g + part;
               const int kp = key0 + part * C::VKEYS;
-              const int r0 = max(0, w.len.L - kp);  // first drafted row of the slot
-              if (r0 >= C::VKEYS) continue;
+              if (w.len.L - kp >= C::VKEYS) continue;
               mbar_wait(&vfull[f % NV], (f / NV) & 1u, ab);
               __syncwarp();
-              uint8_t* slot = smem + C::OFF_V + (f % NV) * C::V_SLOT;
-              constexpr int RCH = C::VROW / 16;  // 16-byte chunks of a value row
-              for (int i2 = ti; i2 < (C::VKEYS - r0) * RCH; i2 += nth) {
-                const int vr = r0 + i2 / RCH, vc = i2 % RCH;
-                uint4* at = reinterpret_cast<uint4*>(slot + (vc >> 3) * (C::VKEYS * 128) + vr * 128 + ((vc & 7) << 4));
-                bool zero = kp + vr >= w.len.end;
-                if (!zero) {
-                  const uint4 u = *at;
-                  const uint32_t v4[4] = {u.x, u.y, u.z, u.w};
-                  bool bad = false;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if constexpr (C::V8) {  // e4m3: 0x7f, 0xff
-                      const uint32_t t7 = (v4[e] & 0x7f7f7f7fu) + 0x01010101u;
-                      bad |= (t7 & 0x80808080u) != 0;
-                    } else {
-                      bad |= (v4[e] & 0x7f80u) == 0x7f80u || (v4[e] & 0x7f800000u) == 0x7f800000u;
-                    }
-                  }
-                  if (bad) {
-                    atomicOr(&poison[k % 3], 1ull << (kp + vr - w.len.L));
-                    zero = true;
-                  }
-                }
-                if (zero) *at = make_uint4(0, 0, 0, 0);
-              }
+              clean_values<C::VKEYS, C::VROW, C::V8>(smem + C::OFF_V + (f % NV) * C::V_SLOT, kp, w.len, &poison[k % 3], ti, nth);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -901,31 +709,30 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
         if (qd == 0) l = (l + xl[128 + row]) + (xl[256 + row] + xl[384 + row]);
         named_bar_sync(1 + wq, 128);  // (the next segment's maxima go there)
         if (ti == 0) poison[(k + 2) % 3] = 0;
-        const size_t unit = static_cast<size_t>(w.b) * HM + w.hm;
-        const int rs = WIDE ? p.R : 2 * p.R, ri = sub * p.R + r;  // rows of a map in the state, this one
-        float* piece = p.ws + (unit + blockIdx.x) * tree_state_floats(p.R, DV);
-        if (qd == 0 && valid) {
+        const long long group = static_cast<long long>(w.b) * groups + w.grp;
+        float* state = tree_state(p, group, static_cast<int>(blockIdx.x) / p.team, static_cast<int>(blockIdx.x) % p.team, DV);
+        const int sm = 2 * sub + map;
+        const bool here = valid && DA_BOUNDS_V(group < static_cast<long long>(p.B) * groups && r < kTreeRows, r);
+        if (qd == 0 && here) {
           if (see & poison[k % 3]) l = __uint_as_float(0x7fffffffu);
-          if (DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM && ri < kTreeRows, ri))
-            reinterpret_cast<float2*>(piece)[map * rs + ri] = make_float2(m_used, l);
+          reinterpret_cast<float2*>(state)[sm * p.R + r] = make_float2(m_used, l);
         }
-        float4* o4 = reinterpret_cast<float4*>(piece + 4 * rs) +
-                     (static_cast<size_t>(map) * (DV / 4) + (OC / 4) * qd) * rs + ri;
+        float4* o4 = reinterpret_cast<float4*>(state + 4 * p.subs * p.R + (static_cast<size_t>(sm) * p.R + r) * DV + OC * qd);
 #pragma unroll 1
         for (int q = 0; q < OC / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(tl + C::TM_O + OC * qd + 32u * q, o);
           tmem_ld_wait(o);
-          if (valid && DA_BOUNDS_V(unit < static_cast<size_t>(p.B) * HM, ri)) {
+          if (here) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c, o4 += rs)
+            for (int c = 0; c < 8; ++c, ++o4)
               *o4 = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]), __uint_as_float(o[4 * c + 2]),
                                 __uint_as_float(o[4 * c + 3]));
           }
         }
         tc_fence_before();
         __syncwarp();
-        walk_next(w, seg);
+        walk_next(p, groups, w, seg);
       }
     }
   }
@@ -940,117 +747,11 @@ __global__ void __launch_bounds__(640, 1) tree_kernel(const __grid_constant__ Tr
   }
 }
 
-// Merges the partial states of a unit and finishes four of its rows a CTA:
-// thread = (row of the four, 4 channels); DV threads.
-template <int DV, bool V2>
-__global__ void __launch_bounds__(DV) tree_combine_kernel(const __grid_constant__ TreeParams p, float o_mult) {
-  grid_dep_launch_dependents();
-  grid_dep_wait();
-  __shared__ long long scratch[64];
-  __shared__ float red[DV / 32][4];
-  const int HM = p.H * p.mt;
-  const int groups = (p.R + 3) >> 2;
-  const int unit = static_cast<int>(blockIdx.x / groups), rg = static_cast<int>(blockIdx.x % groups);
-  const int b = unit / HM, hm = unit - b * HM;
-  const int h = hm / p.mt, mtile = hm - h * p.mt;
-  long long before, total;
-  tree_prefix(p, b, scratch, before, total);
-  const TreeLen len = tree_len(p, b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = 4 * rg + (threadIdx.x & 3), c4 = threadIdx.x >> 2;
-  const int pj = r / p.T, t = r - pj * p.T;
-  const int pair = mtile * p.ppt + pj;
-  const bool have = r < p.R && pair < p.pairs;
-  float y[4] = {0.f, 0.f, 0.f, 0.f};
-  float ss = 0.f;
-  if (have && len.tiles > 0 && t < len.nt) {
-    const long long W = total * HM;
-    const long long s = before * HM + static_cast<long long>(hm) * len.tiles, e = s + len.tiles - 1;
-    const long long G = min(static_cast<long long>(p.grid), W);
-    const int c0 = static_cast<int>(((s + 1) * G - 1) / W), c1 = static_cast<int>(((e + 1) * G - 1) / W);
-    const size_t pf = tree_state_floats(p.R, DV);
-    const float* src = p.ws + (static_cast<size_t>(unit) + c0) * pf;
-    const int subs = p.R > 32 ? 1 : 2, rs = subs * p.R;
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, acc[2][4] = {};
-    for (int c = c0; c <= c1; ++c, src += pf) {
-#pragma unroll 2
-      for (int sub = 0; sub < subs; ++sub)
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int ri = sub * p.R + r;
-          const float2 ml = reinterpret_cast<const float2*>(src)[m * rs + ri];
-          const float4 o = reinterpret_cast<const float4*>(src + 4 * rs)[(static_cast<size_t>(m) * (DV / 4) + c4) * rs + ri];
-          if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen in this state
-          const float mn = fmaxf(M[m], ml.x);
-          const float fo = (M[m] == mn) ? 1.f : ex2(M[m] - mn), fn = (ml.x == mn) ? 1.f : ex2(ml.x - mn);
-          M[m] = mn;
-          L[m] = L[m] * fo + ml.y * fn;
-          acc[m][0] = acc[m][0] * fo + o.x * fn;
-          acc[m][1] = acc[m][1] * fo + o.y * fn;
-          acc[m][2] = acc[m][2] * fo + o.z * fn;
-          acc[m][3] = acc[m][3] * fo + o.w * fn;
-        }
-    }
-    const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
-    const float a1 = (L[0] == 0.f) ? 0.f : o_mult / L[0], a2 = (L[1] == 0.f) ? 0.f : -coef * o_mult / L[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = acc[0][i] * a1 + acc[1][i] * a2;
-      ss = fmaf(y[i], y[i], ss);
-    }
-  }
-  float rinv = 1.f;
-  if (!V2) {
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-    if (lane < 4) red[warp][lane] = ss;
-    __syncthreads();
-    float tot = 0.f;
-#pragma unroll
-    for (int w = 0; w < DV / 32; ++w) tot += red[w][threadIdx.x & 3];
-    rinv = p.norm_mult * rsqrtf(tot * (1.f / DV) + p.eps);
-  }
-  if (have) {
-    float g[4] = {1.f, 1.f, 1.f, 1.f};
-    if (!V2 && p.gamma) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) g[i] = p.gamma[4 * c4 + i];
-    }
-    const size_t orow = V2 ? (static_cast<size_t>(b) * p.T + t) * (p.H * p.pairs) + h * p.pairs + pair
-                           : (static_cast<size_t>(b) * p.T + t) * p.H + h;
-    if (DA_BOUNDS_V(b < p.B && t < p.T && h < p.H, t))
-      *reinterpret_cast<uint2*>(p.out + orow * DV + 4 * c4) =
-          make_uint2(pack_bf16x2(y[0] * rinv * g[0], y[1] * rinv * g[1]),
-                     pack_bf16x2(y[2] * rinv * g[2], y[3] * rinv * g[3]));
-  }
-}
-
 template <int D, bool V2, int FMT>
-cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
-  using C = TreeCfg<D, V2, FMT>;
-  auto kern = p.R > 32 ? tree_kernel<D, V2, FMT, true> : tree_kernel<D, V2, FMT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 1, 1);
-  cfg.blockDim = dim3(C::NTHREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM_BYTES;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cc = {};
-  const long long ctas = static_cast<long long>(p.B) * p.H * p.mt * ((p.R + 3) / 4);
-  cc.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-  cc.blockDim = dim3(C::DV, 1, 1);
-  cc.stream = s;
-  cc.attrs = attr;
-  cc.numAttrs = 1;
-  return cudaLaunchKernelEx(&cc, tree_combine_kernel<C::DV, V2>, p, C::V8 ? 1.f / 128.f : 1.f);
+cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t s) {
+  using C = TreeRowsCfg<D, V2, FMT>;
+  return launch_tree_pair<C::DV, V2>(p.R > 32 ? tree_rows_kernel<D, V2, FMT, true> : tree_rows_kernel<D, V2, FMT, false>,
+                                     C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / 128.f : 1.f, p, s);
 }
 
 }  // namespace da

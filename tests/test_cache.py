@@ -211,8 +211,9 @@ def test_tree_refusals(L):
 
 
 def test_tree_workspace_sizes(L):
-    # one partial state of 2 R (dv + 2) floats (R up to 32: twice) a row tile and a CTA
-    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 2 * 10 * 130 * 4
+    # a partial state of 2 R (dv + 2) floats a row tile and a CTA; four of them up to 8 rows, two up to 32
+    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 4 * 2 * 5 * 130 * 4
+    assert da.tree_decode_workspace_bytes(2, 9, 3, 128) == (6 + 160) * 2 * 2 * 9 * 258 * 4
     assert da.v2_tree_decode_workspace_bytes(1, 20, 16, 2, 128) == (1 * 2 * 2 + 160) * 2 * 60 * 130 * 4
     assert da.v2_tree_decode_workspace_bytes(1, 64, 8, 1, 128) == (4 + 160) * 2 * 64 * 130 * 4
     assert da.tree_decode_workspace_bytes(1, 65, 1, 64) == 0
