@@ -21,7 +21,7 @@
 // mask are its own registers.  (With tokens as rows, as in the forward, every
 // thread needs every key's scales: three broadcast shared-memory reads a
 // column, against which the MMAs' operands queued; e4m3 V1 d64 B8 H16 n32768,
-// one token: 312 us; this way %FP8D64% us.)
+// one token: 312 us; this way 188 us.)
 //
 // Softmax.  A column's reference maximum is shared memory's; scores come out
 // as score - reference in one FMA, and only when some score of the tile is

@@ -35,6 +35,12 @@ __device__ __forceinline__ TreeLen tree_len(const TreeParams& p, int b) {
   return x;
 }
 
+// a / b of non-negative numbers; 64-bit division only where it is needed.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 // Tiles of all sequences before `upto` and of all of them, per unit of a
 // sequence (each has the same units), by the whole CTA; scratch of 2 * 32 + 2
 // long longs.  Every thread returns with (before, total).
@@ -78,7 +84,7 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
 // the value, or 2^-10 absolute, as a bf16 would be.  At that scale f16's
 // exponent field is e4m3's, so a code is bits 7-13 of the f16: pairs of f16
 // are shifted and masked as integers (the e4m3 conversion instructions take
-// about 16 issue cycles each, and bounded the kernel: 372 us against 247 us
+// about 16 issue cycles each, and bounded the kernel: 372 us against 337 us
 // at B8 H16 n32768 d64).  A NaN stays a NaN.
 __device__ __forceinline__ void two_e4m3x4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
   uint32_t f0, f1, r0, r1;
@@ -154,7 +160,7 @@ __device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&r)[16]) 
 // `lane` of the team unit `lane` of each group.  Neighbouring units are
 // neighbouring heads, whose rows of a token lie side by side: read at about
 // the same time they make whole DRAM bursts of rows as short as 64 bytes
-// (e4m3 V1 d64 B8 H16 n32768: %TEAM1% us, each CTA for itself %TEAM0%).
+// (e4m3 V1 d64 B8 H16 n32768: 199 us, each CTA for itself 240).
 //
 // The CTA's range, by the whole CTA: its number of tiles; `scratch` 64 long longs, `start` three ints in shared memory.  The caller
 // synchronises the CTA before it reads `start`.
@@ -164,7 +170,7 @@ __device__ __forceinline__ int tree_range(const TreeParams& p, int groups, long 
   const long long W = total * groups;
   const long long G = min(static_cast<long long>(p.teams), max(W, 1ll));  // no team between two with tiles is without
   const int team = static_cast<int>(blockIdx.x) / p.team;
-  const long long lo = W * team / G, hi = W * (team + 1) / G;
+  const long long lo = quotient(W * team, G), hi = quotient(W * (team + 1), G);
   const int count = team < G ? static_cast<int>(hi - lo) : 0;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32 && count > 0) {  // the sequence that tile `lo` falls in: 32 sequences a step
@@ -182,8 +188,9 @@ __device__ __forceinline__ int tree_range(const TreeParams& p, int groups, long 
       if (here) {
         const int tiles = static_cast<int>(mine / groups);
         start[0] = b0 + lane;
-        start[1] = static_cast<int>((lo - excl) / tiles);
-        start[2] = static_cast<int>((lo - excl) % tiles);
+        const int grp = static_cast<int>(quotient(lo - excl, tiles));
+        start[1] = grp;
+        start[2] = static_cast<int>(lo - excl - static_cast<long long>(grp) * tiles);
       }
       if (__any_sync(0xffffffffu, here)) break;
       base += __shfl_sync(0xffffffffu, incl, 31);
@@ -301,77 +308,110 @@ __device__ __forceinline__ void split_e4m3x8(const uint4& x, int sh, uint2& hi, 
   lo = make_uint2(l[0], l[1]);
 }
 
-// Merges the partial states of a unit and finishes one row a CTA: two channels a thread.
+// Merges the partial states of a unit and finishes one row a CTA: two channels
+// a thread.  A handful of dependent loads is all that it does, so it is built
+// for latency: the states' maxima and sums by as many threads at once, then
+// their weights, then every state's O with nothing to wait for in between
+// (40 rows of 4 to 8 states: 14.4 us one state after the other, cold;
+// 11 us this way).
+constexpr int kTreeMaxStates = 160 * 4;  // of a unit: one a team and subset
+
 template <int DV, bool V2>
 __global__ void __launch_bounds__(DV / 2) tree_combine_kernel(const __grid_constant__ TreeParams p, float o_mult) {
   grid_dep_launch_dependents();
   grid_dep_wait();
+  constexpr int NT = DV / 2;
   __shared__ long long scratch[64];
-  __shared__ float red[DV / 64];
+  __shared__ float2 ml[2][kTreeMaxStates];  // maximum and sum, then weight and whether there is one
+  __shared__ float red[3 * NT / 32];
   const int HM = p.H * p.mt;
-  const int unit = static_cast<int>(blockIdx.x / p.R), r = static_cast<int>(blockIdx.x % p.R);
+  const int unit = static_cast<int>(blockIdx.x) / p.R, r = static_cast<int>(blockIdx.x) - unit * p.R;
   const int b = unit / HM, hm = unit - b * HM;
   const int h = hm / p.mt, mtile = hm - h * p.mt;
   const int pj = r / p.T, t = r - pj * p.T;
   const int pair = mtile * p.ppt + pj;
   if (pair >= p.pairs) return;
+  // what does not depend on the states, on its way
+  const size_t orow = V2 ? (static_cast<size_t>(b) * p.T + t) * (p.H * p.pairs) + h * p.pairs + pair
+                         : (static_cast<size_t>(b) * p.T + t) * p.H + h;
+  const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
+  float2 g = make_float2(1.f, 1.f);
+  if (!V2 && p.gamma) g = make_float2(p.gamma[2 * threadIdx.x], p.gamma[2 * threadIdx.x + 1]);
+  const TreeLen len = tree_len(p, b);
   long long before, total;
   tree_prefix(p, b, scratch, before, total);
-  const TreeLen len = tree_len(p, b);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float y0 = 0.f, y1 = 0.f;
-  if (len.tiles > 0 && t < len.nt) {
+  if (len.tiles > 0 && t < len.nt) {  // (the same for the whole CTA)
     const int groups = HM / p.team, grp = hm / p.team;
     const long long W = total * groups;
     const long long G = min(static_cast<long long>(p.teams), W);
     const long long s = before * groups + static_cast<long long>(grp) * len.tiles, e = s + len.tiles - 1;
-    const int c0 = static_cast<int>(((s + 1) * G - 1) / W), c1 = static_cast<int>(((e + 1) * G - 1) / W);
+    const int c0 = static_cast<int>(quotient((s + 1) * G - 1, W)), c1 = static_cast<int>(quotient((e + 1) * G - 1, W));
     const float* src = tree_state(p, static_cast<long long>(b) * groups + grp, c0, hm % p.team, DV);
     const size_t sf = p.team * tree_state_floats(p.R, p.subs, DV);
-    const int subs = p.subs;
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, a0[2] = {0.f, 0.f}, a1[2] = {0.f, 0.f};
-#pragma unroll 2
-    for (int c = 0; c < (c1 - c0 + 1) * subs; ++c) {
-      const float* st = src + (c / subs) * sf;
+    const int n = (c1 - c0 + 1) * p.subs;
+    float M[2] = {-INFINITY, -INFINITY};
+    for (int i = threadIdx.x; i < 2 * n; i += NT) {
+      const int m = i >= n, k = i - m * n, c = k / p.subs, sub = k - c * p.subs;
+      const float2 x = reinterpret_cast<const float2*>(src + c * sf)[(2 * sub + m) * p.R + r];
+      ml[m][k] = x;
+      M[m] = fmaxf(M[m], x.x);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) M[m] = fmaxf(M[m], __shfl_xor_sync(0xffffffffu, M[m], x));
+      if (lane == 0) red[m * (NT / 32) + warp] = M[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      M[m] = red[m * (NT / 32)];
+#pragma unroll
+      for (int i = 1; i < NT / 32; ++i) M[m] = fmaxf(M[m], red[m * (NT / 32) + i]);
+    }
+    for (int i = threadIdx.x; i < 2 * n; i += NT) {
+      const int m = i >= n, k = i - m * n;
+      const float2 x = ml[m][k];
+      const bool none = x.x == -INFINITY && x.y == 0.f;  // nothing seen in this state
+      const float w = none ? 0.f : (x.x == M[m]) ? 1.f : ex2(x.x - M[m]);
+      ml[m][k] = make_float2(none ? -1.f : w, none ? 0.f : x.y * w);  // (a weight of -1: O is not there)
+    }
+    __syncthreads();
+    float L[2] = {0.f, 0.f}, a0[2] = {0.f, 0.f}, a1[2] = {0.f, 0.f};
+    const float* o = src + p.subs * 4 * p.R + static_cast<size_t>(r) * DV;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const int c = k / p.subs, sub = k - c * p.subs;
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const int sm = (c % subs) * 2 + m;
-        const float2 ml = reinterpret_cast<const float2*>(st)[sm * p.R + r];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen in this state
-        const float2 o = reinterpret_cast<const float2*>(st + subs * 4 * p.R + (static_cast<size_t>(sm) * p.R + r) * DV)[threadIdx.x];
-        const float mn = fmaxf(M[m], ml.x);
-        const float fo = (M[m] == mn) ? 1.f : ex2(M[m] - mn), fn = (ml.x == mn) ? 1.f : ex2(ml.x - mn);
-        M[m] = mn;
-        L[m] = L[m] * fo + ml.y * fn;
-        a0[m] = a0[m] * fo + o.x * fn;
-        a1[m] = a1[m] * fo + o.y * fn;
+        const float2 w = ml[m][k];
+        float2 v = make_float2(0.f, 0.f);
+        if (w.x != -1.f) v = reinterpret_cast<const float2*>(o + c * sf + static_cast<size_t>(2 * sub + m) * p.R * DV)[threadIdx.x];
+        L[m] += w.y;
+        a0[m] = fmaf(v.x, w.x, a0[m]);
+        a1[m] = fmaf(v.y, w.x, a1[m]);
       }
     }
-    const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
     const float w1 = (L[0] == 0.f) ? 0.f : o_mult / L[0], w2 = (L[1] == 0.f) ? 0.f : -coef * o_mult / L[1];
     y0 = a0[0] * w1 + a0[1] * w2;
     y1 = a1[0] * w1 + a1[1] * w2;
   }
-  float rinv = 1.f, g0 = 1.f, g1 = 1.f;
+  float rinv = 1.f;
   if (!V2) {
     float ss = y0 * y0 + y1 * y1;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-    if (lane == 0) red[warp] = ss;
+    if (lane == 0) red[2 * (NT / 32) + warp] = ss;
     __syncthreads();
     float tot = 0.f;
 #pragma unroll
-    for (int i = 0; i < DV / 64; ++i) tot += red[i];
+    for (int i = 0; i < NT / 32; ++i) tot += red[2 * (NT / 32) + i];
     rinv = p.norm_mult * rsqrtf(tot * (1.f / DV) + p.eps);
-    if (p.gamma) {
-      g0 = p.gamma[2 * threadIdx.x];
-      g1 = p.gamma[2 * threadIdx.x + 1];
-    }
   }
-  const size_t orow = V2 ? (static_cast<size_t>(b) * p.T + t) * (p.H * p.pairs) + h * p.pairs + pair
-                         : (static_cast<size_t>(b) * p.T + t) * p.H + h;
   if (DA_BOUNDS_V(b < p.B && t < p.T && h < p.H, t))
-    reinterpret_cast<uint32_t*>(p.out + orow * DV)[threadIdx.x] = pack_bf16x2(y0 * rinv * g0, y1 * rinv * g1);
+    reinterpret_cast<uint32_t*>(p.out + orow * DV)[threadIdx.x] = pack_bf16x2(y0 * rinv * g.x, y1 * rinv * g.y);
 }
 
 // Launches a tree kernel and the merge, each a programmatic dependent of what precedes it.

@@ -39,9 +39,9 @@
 // rows.  So a ragged batch, one long sequence and many short ones all keep
 // every SM streaming.
 //
-// Roles (384 threads, one CTA per SM): warp 0 TMA producer; warp 1 score
-// MMAs; warp 2 P V MMAs; warp 3 value and key scales (FP8); warps 4-11
-// softmax, two warps per lane quarter, each half of a tile's key columns
+// Roles (640 threads, one CTA per SM): warp 0 TMA producer; warp 1 score
+// MMAs; warp 2 P V MMAs; warp 3 value and key scales (FP8); warps 4-19
+// softmax, four warps a lane quarter, each a quarter of a tile's key columns
 // (quarters without rows sleep).  TMEM: O, then two score tiles, in which P
 // replaces the scores.
 #pragma once
