@@ -43,6 +43,13 @@ int sms_or_default() {
   return s > 0 ? s : 148;
 }
 
+// 2^32 / n + 1, by whose high product fast_div divides numbers up to `most` by n exactly; 0 where it would not.
+unsigned division_magic(unsigned long long n, unsigned long long most) {
+  if (n < 2 || most >= (1ull << 32)) return 0;  // (n = 1: 2^32 + 1 does not fit)
+  const unsigned long long m = (1ull << 32) / n + 1;
+  return (m * n - (1ull << 32)) * most < (1ull << 32) ? static_cast<unsigned>(m) : 0;
+}
+
 // 4-D map over a contiguous [B, n, heads, W] tensor of bf16 or bytes: box =
 // `box_bytes` (64 or 128, the swizzle) of a row x 1 head x `rows` tokens.
 // `side` heads are read side by side at about the same time: L2 fetches what
@@ -177,6 +184,8 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
   // Several tokens a CTA once there are enough CTAs; with few tokens, several CTAs a token.
   const int sms = sms_or_default();
   p.tokens_per_cta = static_cast<int>(std::min<long long>(da::kAppendMaxTokens, std::max<long long>(1, tokens / (8 * sms))));
+  const long long of[3] = {static_cast<long long>(p.nq) * Hq, static_cast<long long>(nk) * H, H};
+  for (int k = 0; k < 3; ++k) p.magic[k] = division_magic(of[k], of[k] * p.tokens_per_cta);
   const int gx = static_cast<int>((tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
   const long long most = (lanes * p.tokens_per_cta + da::kAppendThreads - 1) / da::kAppendThreads;
   const int gy = static_cast<int>(std::max<long long>(1, std::min<long long>({most, 2ll * sms / gx, 65535ll})));
@@ -452,6 +461,12 @@ diffattn_status diffattn_rope(diffattn_dtype dt, int B, int n, int d, int count,
   p.tokens_per_cta = static_cast<int>(std::min<long long>(da::kRopeMaxTokens, std::max<long long>(1, tokens / (8 * sms))));
   const int gx = static_cast<int>((tokens + p.tokens_per_cta - 1) / p.tokens_per_cta);
   const long long per_head = vec ? d / N : d;
+  {
+    const int ri = vec ? (p.rope.inter ? p.rope.rot / N : p.rope.rot / 2 / N) : p.rope.rot / 2;
+    const long long ph = ri + (p.copy ? (d - p.rope.rot) / (vec ? N : 1) : 0);
+    p.magic_tok = division_magic(head_sum * ph, head_sum * ph * p.tokens_per_cta);
+    p.magic_head = division_magic(ph, head_sum * ph);
+  }
   const long long most = (head_sum * per_head * p.tokens_per_cta + da::kRopeThreads - 1) / da::kRopeThreads;
   const int gy = static_cast<int>(std::max<long long>(1, std::min<long long>({most, 2ll * sms / gx, 65535ll})));
   const cudaError_t e = da::launch_rope(p, f32, vec, gx, gy, static_cast<cudaStream_t>(stream));

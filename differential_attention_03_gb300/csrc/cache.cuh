@@ -76,6 +76,24 @@ struct RopeVec<true> {
   }
 };
 
+// Element c of a row, as a float and back.
+template <bool F32>
+__device__ __forceinline__ float rope_get(const uint8_t* row, int c) {
+  if constexpr (F32) return reinterpret_cast<const float*>(row)[c];
+  else return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[c]);
+}
+template <bool F32>
+__device__ __forceinline__ void rope_put(uint8_t* row, int c, float x) {
+  if constexpr (F32) reinterpret_cast<float*>(row)[c] = x;
+  else reinterpret_cast<__nv_bfloat16*>(row)[c] = __float2bfloat16_rn(x);
+}
+
+// a / n by the host's magic number 2^32 / n + 1 (0: plain division), exact while a times the
+// magic number's excess stays below 2^32 / n: the host sees to it.
+__device__ __forceinline__ unsigned fast_div(unsigned a, unsigned n, unsigned magic) {
+  return magic ? __umulhi(a, magic) : a / n;
+}
+
 // VEC: 16-byte accesses (rows and the rotated part whole vectors); else
 // element by element, for odd widths.  A work item is the two vectors (or
 // elements) of one rotation, or one vector (element) to copy.
@@ -85,7 +103,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   grid_dep_wait();
   using V = RopeVec<F32>;
   constexpr int N = V::N;
-  __shared__ float2 cs[kRopeMaxTokens * 64];
+  __shared__ __align__(16) float2 cs[kRopeMaxTokens * 64];
   const int half = p.rope.rot >> 1;
   const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens_per_cta;
   const long long tokens = static_cast<long long>(p.B) * p.n;
@@ -102,83 +120,99 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int step = VEC ? N : 1;
   const int ri = VEC ? (p.rope.inter ? p.rope.rot / N : half / N) : half;
   const int per_head = ri + (p.copy ? (p.d - p.rope.rot) / step : 0);
-  const int per_tok = p.head_sum * per_head;
-  const int total = nt * per_tok;
-  for (int i = blockIdx.y * kRopeThreads + threadIdx.x; i < total; i += gridDim.y * kRopeThreads) {
-    const int t = i / per_tok, j = i - t * per_tok;
-    int hh = j / per_head;
-    const int l = j - hh * per_head;
-    int ten = 0;
+  const unsigned per_tok = static_cast<unsigned>(p.head_sum * per_head);
+  const unsigned total = static_cast<unsigned>(nt) * per_tok;
+  // Two items a turn, their loads before either is worked on.
+  constexpr int U = 2;
+  const unsigned stride = gridDim.y * kRopeThreads;
+  for (unsigned i0 = blockIdx.y * kRopeThreads + threadIdx.x; i0 < total; i0 += U * stride) {
+    const uint8_t* src[U];
+    uint8_t* dst[U];
+    const float2* a[U];
+    int ca[U];
+    bool turn[U], go[U];
+    uint4 wa[U], wb[U];
+    float x0[U], x1[U];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (ten == k && k + 1 < p.count && hh >= p.heads[k]) {
-        hh -= p.heads[k];
-        ten = k + 1;
-      }
-    const size_t row = (static_cast<size_t>(tok0 + t) * p.heads[ten] + hh) * p.d;
-    const bool turn = l < ri;
-    const bool inplace = p.x[ten] == p.out[ten];
-    if (!turn && inplace) continue;
-    const float2* a = cs + t * half;
-    if (!DA_BOUNDS_V(tok0 + t < tokens && hh < p.heads[ten], tok0 + t)) continue;
-    if constexpr (VEC) {
-      const int ca = turn ? l * N : p.rope.rot + (l - ri) * N;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.x[ten]) + row * V::ES);
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out[ten]) + row * V::ES);
-      const uint4 wa = src[ca / N];
-      if (!turn) {
-        dst[ca / N] = wa;
-        continue;
-      }
-      float xa[N];
-      V::get(wa, xa);
-      if (p.rope.inter) {
-        float y[N];
+    for (int u = 0; u < U; ++u) {
+      const unsigned i = i0 + u * stride;
+      go[u] = i < total;
+      const unsigned ii = go[u] ? i : 0u;
+      const unsigned t = fast_div(ii, per_tok, p.magic_tok);
+      const unsigned j = ii - t * per_tok;
+      unsigned hh = fast_div(j, static_cast<unsigned>(per_head), p.magic_head);
+      const int l = static_cast<int>(j - hh * per_head);
+      int ten = 0;
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-          const float2 c = a[(ca + e) >> 1];
-          y[e] = xa[e] * c.x - xa[e + 1] * c.y;
-          y[e + 1] = xa[e + 1] * c.x + xa[e] * c.y;
+      for (int k = 0; k < 3; ++k)
+        if (ten == k && k + 1 < p.count && hh >= static_cast<unsigned>(p.heads[k])) {
+          hh -= p.heads[k];
+          ten = k + 1;
         }
-        dst[ca / N] = V::put(y);
+      const size_t row = (static_cast<size_t>(tok0 + t) * p.heads[ten] + hh) * p.d;
+      turn[u] = l < ri;
+      go[u] = go[u] && (turn[u] || p.x[ten] != p.out[ten]) &&
+              DA_BOUNDS_V(tok0 + t < tokens && hh < static_cast<unsigned>(p.heads[ten]), tok0 + t);
+      a[u] = cs + t * half;
+      src[u] = static_cast<const uint8_t*>(p.x[ten]) + row * V::ES;
+      dst[u] = static_cast<uint8_t*>(p.out[ten]) + row * V::ES;
+      if constexpr (VEC) {
+        ca[u] = turn[u] ? l * N : p.rope.rot + (l - ri) * N;
+        if (go[u]) {
+          wa[u] = reinterpret_cast<const uint4*>(src[u])[ca[u] / N];
+          if (turn[u] && !p.rope.inter) wb[u] = reinterpret_cast<const uint4*>(src[u])[(ca[u] + half) / N];
+        }
       } else {
-        float xb[N], ya[N], yb[N];
-        V::get(src[(ca + half) / N], xb);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float2 c = a[ca + e];
-          ya[e] = xa[e] * c.x - xb[e] * c.y;
-          yb[e] = xb[e] * c.x + xa[e] * c.y;
+        ca[u] = turn[u] ? (p.rope.inter ? 2 * l : l) : p.rope.rot + (l - ri);
+        a[u] += turn[u] ? l : 0;
+        if (go[u]) {
+          x0[u] = rope_get<F32>(src[u], ca[u]);
+          if (turn[u]) x1[u] = rope_get<F32>(src[u], ca[u] + (p.rope.inter ? 1 : half));
         }
-        dst[ca / N] = V::put(ya);
-        dst[(ca + half) / N] = V::put(yb);
       }
-    } else {
-      const int c0 = turn ? (p.rope.inter ? 2 * l : l) : p.rope.rot + (l - ri);
-      const int c1 = p.rope.inter ? c0 + 1 : c0 + half;
-      if constexpr (F32) {
-        const float* src = static_cast<const float*>(p.x[ten]) + row;
-        float* dst = static_cast<float*>(p.out[ten]) + row;
-        const float x0 = src[c0];
-        if (!turn) {
-          dst[c0] = x0;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!go[u]) continue;
+      if constexpr (VEC) {
+        uint4* out = reinterpret_cast<uint4*>(dst[u]);
+        if (!turn[u]) {
+          out[ca[u] / N] = wa[u];
           continue;
         }
-        const float x1 = src[c1];
-        const float2 c = a[l];
-        dst[c0] = x0 * c.x - x1 * c.y;
-        dst[c1] = x1 * c.x + x0 * c.y;
+        float xa[N];
+        V::get(wa[u], xa);
+        if (p.rope.inter) {
+          float y[N];
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            const float2 c = a[u][(ca[u] + e) >> 1];
+            y[e] = xa[e] * c.x - xa[e + 1] * c.y;
+            y[e + 1] = xa[e + 1] * c.x + xa[e] * c.y;
+          }
+          out[ca[u] / N] = V::put(y);
+        } else {
+          float xb[N], ya[N], yb[N];
+          V::get(wb[u], xb);
+#pragma unroll
+          for (int e = 0; e < N; e += 2) {
+            const float4 c = *reinterpret_cast<const float4*>(a[u] + ca[u] + e);
+            ya[e] = xa[e] * c.x - xb[e] * c.y;
+            yb[e] = xb[e] * c.x + xa[e] * c.y;
+            ya[e + 1] = xa[e + 1] * c.z - xb[e + 1] * c.w;
+            yb[e + 1] = xb[e + 1] * c.z + xa[e + 1] * c.w;
+          }
+          out[ca[u] / N] = V::put(ya);
+          out[(ca[u] + half) / N] = V::put(yb);
+        }
       } else {
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.x[ten]) + row;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out[ten]) + row;
-        if (!turn) {
-          dst[c0] = src[c0];
+        if (!turn[u]) {
+          rope_put<F32>(dst[u], ca[u], x0[u]);
           continue;
         }
-        const float x0 = __bfloat162float(src[c0]), x1 = __bfloat162float(src[c1]);
-        const float2 c = a[l];
-        dst[c0] = __float2bfloat16_rn(x0 * c.x - x1 * c.y);
-        dst[c1] = __float2bfloat16_rn(x1 * c.x + x0 * c.y);
+        const float2 c = *a[u];
+        rope_put<F32>(dst[u], ca[u], x0[u] * c.x - x1[u] * c.y);
+        rope_put<F32>(dst[u], ca[u] + (p.rope.inter ? 1 : half), x1[u] * c.x + x0[u] * c.y);
       }
     }
   }
@@ -198,174 +232,204 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8], float mul) {
   return make_uint2(w[0], w[1]);
 }
 
-// A row (token, tensor, head) is d / 16 (values: dv / 16) consecutive lanes of
-// 16 channels each.  Order of a token's rows: queries, keys, values; every
-// group starts at a multiple of its lanes (the host checks the widths).
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const __grid_constant__ AppendParams p) {
+// Largest magnitude of 8 numbers and m; a NaN stays one.
+__device__ __forceinline__ float amax8(float m, const float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(x[e])));
+  return m;
+}
+
+enum AppendKind { kAppendQuery, kAppendKey, kAppendValue };
+
+struct AppendShared {
+  float cos[kAppendMaxTokens * 64], sin[kAppendMaxTokens * 64];  // [token][frequency]
+  int at[kAppendMaxTokens];    // cache row of the token, -1: not written
+  int seq[kAppendMaxTokens];   // its sequence
+  int live[kAppendMaxTokens];  // whether the sequence has it
+};
+
+// The lane's channels of a rotated row in place: xa from channel ca, xb from cb.
+__device__ __forceinline__ void append_turn(const AppendParams& p, const AppendShared& sh, bool halves, int t, int l,
+                                            int ca, int cb, const __nv_bfloat16* src, float (&xa)[8], float (&xb)[8]) {
+  const int rot = p.rope.rot, half = rot >> 1;
+  const float *cs = sh.cos + t * half, *sn = sh.sin + t * half;
+  if (halves) {
+    if (16 * l >= rot) return;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const float4 c = *reinterpret_cast<const float4*>(cs + ca + e), s = *reinterpret_cast<const float4*>(sn + ca + e);
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {  // two pairs an instruction
+        const float c0 = k ? c.z : c.x, c1 = k ? c.w : c.y, s0 = k ? s.z : s.x, s1 = k ? s.w : s.y;
+        const uint64_t c2 = f2pack(c0, c1), s2 = f2pack(s0, s1), n2 = f2pack(-s0, -s1);
+        const uint64_t x = f2pack(xa[e + k], xa[e + k + 1]), z = f2pack(xb[e + k], xb[e + k + 1]);
+        f2unpack(fma2(z, n2, mul2(x, c2)), xa[e + k], xa[e + k + 1]);
+        f2unpack(fma2(x, s2, mul2(z, c2)), xb[e + k], xb[e + k + 1]);
+      }
+    }
+  } else if (p.rope.inter) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      const int ch = 16 * l + e;
+      if (ch >= rot) break;
+      const float c = cs[ch >> 1], s = sn[ch >> 1];
+      float &u = e < 8 ? xa[e & 7] : xb[e & 7], &w = e < 8 ? xa[(e + 1) & 7] : xb[(e + 1) & 7];
+      const float x0 = u, x1 = w;
+      u = x0 * c - x1 * s;
+      w = x1 * c + x0 * s;
+    }
+  } else {  // halves that do not end on 8 channels: the partner comes by its own load
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int ch = 16 * l + e;
+      if (ch >= rot) break;
+      const bool lo = ch < half;
+      const float c = cs[lo ? ch : ch - half], s = sn[lo ? ch : ch - half];
+      const float other = __bfloat162float(src[lo ? ch + half : ch - half]);
+      float& x = e < 8 ? xa[e & 7] : xb[e & 7];
+      x = lo ? x * c - other * s : x * c + other * s;
+    }
+  }
+}
+
+// 32 lanes' rows of one kind: W / 16 lanes a row, 16 channels a lane.
+template <int W, int KIND, int FMT>
+__device__ __forceinline__ void append_rows(const AppendParams& p, const AppendShared& sh, int tok0, int row0, int rows,
+                                            bool halves) {
+  constexpr int GL = W / 16;
+  constexpr bool kCodes = KIND != kAppendQuery && FMT != kCacheBf16 && !(KIND == kAppendValue && FMT == kCacheFp8k);
+  const int lane = threadIdx.x & 31, l = lane % GL;
+  const int i = min(row0 + lane / GL, rows - 1);
+  bool need = row0 + lane / GL < rows;
+  const int heads = KIND == kAppendQuery ? p.Hq : p.H;
+  const int per_tok = KIND == kAppendQuery ? p.nq * p.Hq : KIND == kAppendKey ? p.nk * p.H : p.H;
+  const int t = static_cast<int>(fast_div(i, per_tok, p.magic[KIND]));
+  const int j = i - t * per_tok;
+  const bool second = KIND != kAppendValue && j >= heads;
+  const int h = j - (second ? heads : 0);
+  const __nv_bfloat16* src = KIND == kAppendValue ? p.v
+                             : KIND == kAppendKey ? (second ? p.k[1] : p.k[0]) : (second ? p.q[1] : p.q[0]);
+  const size_t in_row = static_cast<size_t>(tok0 + t) * heads + h;
+  src += in_row * W;
+  const int at = sh.at[t], b = sh.seq[t];
+  const bool padding = KIND == kAppendQuery && !sh.live[t];
+  if (KIND != kAppendQuery) need = need && at >= 0;
+  // a lane of the rotated part holds both channels of its pairs
+  const bool split = KIND != kAppendValue && halves && 16 * l < p.rope.rot;
+  const int ca = split ? 8 * l : 16 * l, cb = split ? (p.rope.rot >> 1) + 8 * l : 16 * l + 8;
+  uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
+  if (need && !padding) {
+    wa = *reinterpret_cast<const uint4*>(src + ca);
+    wb = *reinterpret_cast<const uint4*>(src + cb);
+  }
+  if constexpr (KIND == kAppendQuery) {  // (padding tokens get zero queries)
+    need = need && DA_BOUNDS_V(tok0 + t < p.B * p.T && h < p.Hq, t);
+    if (p.rope.rot > 0 && !padding) {
+      float xa[8], xb[8];
+      unpack_bf16x8(wa, xa);
+      unpack_bf16x8(wb, xb);
+      append_turn(p, sh, halves, t, l, ca, cb, src, xa, xb);
+      wa = pack_bf16x8(xa);
+      wb = pack_bf16x8(xb);
+    }
+    if (need) {
+      __nv_bfloat16* dst = (second ? p.qo[1] : p.qo[0]) + in_row * W;
+      *reinterpret_cast<uint4*>(dst + ca) = wa;
+      *reinterpret_cast<uint4*>(dst + cb) = wb;
+    }
+  } else {
+    need = need && DA_BOUNDS_V(b < p.B && at < p.n && h < p.H, at);
+    const size_t out_row = (static_cast<size_t>(b) * p.n + (at < 0 ? 0 : at)) * p.H + h;
+    void* cache = KIND == kAppendValue ? p.vc : (second ? p.kc[1] : p.kc[0]);
+    float xa[8], xb[8];
+    const bool turned = KIND == kAppendKey && p.rope.rot > 0;
+    if (kCodes || turned) {
+      unpack_bf16x8(wa, xa);
+      unpack_bf16x8(wb, xb);
+      if (turned && need) append_turn(p, sh, halves, t, l, ca, cb, src, xa, xb);
+    }
+    if constexpr (kCodes) {
+      float mul = second ? p.kinv[1] : p.kinv[0], scale = 0.f;
+      if constexpr (FMT == kCacheFp8) {
+        float m = amax8(amax8(0.f, xa), xb);
+#pragma unroll
+        for (int x = 1; x < GL; x <<= 1) {
+          const float o = __shfl_xor_sync(0xffffffffu, m, x);
+          asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(o));
+        }
+        // A row below 448 * 2^-126 keeps the smallest normal scale.  448 / top as 1.75 / (top 2^-8),
+        // whose reciprocal neither over- nor underflows; one ulp off it at most.
+        const float top = m < 448.f * 0x1p-126f ? 448.f * 0x1p-126f : m;
+        scale = m == 0.f ? 0.f : top * (1.f / 448.f);
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(top * 0x1p-8f));
+        mul = 1.75f * r;
+      }
+      if (need) {
+        uint8_t* dst = static_cast<uint8_t*>(cache) + out_row * W;
+        const uint2 ea = pack_e4m3x8(xa, mul), eb = pack_e4m3x8(xb, mul);
+        if (!split) {
+          *reinterpret_cast<uint4*>(dst + ca) = make_uint4(ea.x, ea.y, eb.x, eb.y);
+        } else {
+          *reinterpret_cast<uint2*>(dst + ca) = ea;
+          *reinterpret_cast<uint2*>(dst + cb) = eb;
+        }
+        if (FMT == kCacheFp8 && l == 0) {
+          float* sc = KIND == kAppendValue ? p.vs : (second ? p.ks[1] : p.ks[0]);
+          sc[(static_cast<size_t>(b) * p.H + h) * p.n + at] = scale;
+        }
+      }
+    } else {
+      if (turned) {
+        wa = pack_bf16x8(xa);
+        wb = pack_bf16x8(xb);
+      }
+      if (need) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + out_row * W;
+        *reinterpret_cast<uint4*>(dst + ca) = wa;
+        *reinterpret_cast<uint4*>(dst + cb) = wb;
+      }
+    }
+  }
+}
+
+// A CTA's tokens' query, key and value rows, each kind in warps' loads of 32 / (W / 16) rows, so that a
+// warp runs one kind's code.
+template <int D, int DV, int FMT>
+__global__ void __launch_bounds__(kAppendThreads, 4) cache_append_kernel(const __grid_constant__ AppendParams p) {
   grid_dep_launch_dependents();
   grid_dep_wait();
-  __shared__ float2 cs[kAppendMaxTokens * 64];
-  __shared__ int at[kAppendMaxTokens];   // cache row of the token, -1: not written
-  __shared__ int live[kAppendMaxTokens];
+  __shared__ __align__(16) AppendShared sh;
   const int half = p.rope.rot >> 1;
-  const long long tok0 = static_cast<long long>(blockIdx.x) * p.tokens_per_cta;
-  const long long tokens = static_cast<long long>(p.B) * p.T;
-  const int nt = static_cast<int>(min(static_cast<long long>(p.tokens_per_cta), tokens - tok0));
+  const int tok0 = static_cast<int>(blockIdx.x) * p.tokens_per_cta;
+  const int nt = min(p.tokens_per_cta, p.B * p.T - tok0);
   for (int i = threadIdx.x; i < nt * max(half, 1); i += kAppendThreads) {
     const int t = half ? i / half : i, f = half ? i - t * half : 0;
-    const int b = static_cast<int>((tok0 + t) / p.T), tt = static_cast<int>((tok0 + t) % p.T);
+    const int b = (tok0 + t) / p.T, tt = tok0 + t - b * p.T;
     const long long row = static_cast<long long>(p.lens ? p.lens[b] : 0) + tt;
     if (f == 0) {
       const bool lv = tt < (p.ntok ? p.ntok[b] : p.T);
-      live[t] = lv;
-      at[t] = (lv && row >= 0 && row < p.n) ? static_cast<int>(row) : -1;
+      sh.live[t] = lv;
+      sh.seq[t] = b;
+      sh.at[t] = (lv && row >= 0 && row < p.n) ? static_cast<int>(row) : -1;
     }
-    if (half) cs[i] = rope_cos_sin(p.rope.turns[f], p.pos ? p.pos[tok0 + t] : static_cast<int>(row), p.rope.mult);
+    if (half) {
+      const float2 c = rope_cos_sin(p.rope.turns[f], p.pos ? p.pos[tok0 + t] : static_cast<int>(row), p.rope.mult);
+      sh.cos[i] = c.x;
+      sh.sin[i] = c.y;
+    }
   }
   __syncthreads();
-  const int gl = p.d >> 4, gv = p.dv >> 4;  // lanes of a query / key row, of a value row
-  const int nrow = p.nq * p.Hq + p.nk * p.H;
-  const int per_tok = nrow * gl + p.H * gv;
-  const int total = nt * per_tok;
-  // (whole warps iterate together: the row maxima are shuffles)
-  for (int base = (blockIdx.y * kAppendThreads + (threadIdx.x & ~31)); base < total;
-       base += gridDim.y * kAppendThreads) {
-    const int i = min(base + static_cast<int>(threadIdx.x & 31), total - 1);
-    const bool mine = base + static_cast<int>(threadIdx.x & 31) < total;
-    const int t = i / per_tok;
-    int j = i - t * per_tok;
-    const long long tok = tok0 + t;
-    const bool isv = j >= nrow * gl;
-    int which = 0, h, l;
-    bool isq = false;
-    if (isv) {
-      j -= nrow * gl;
-      h = j / gv;
-      l = j - h * gv;
-    } else {
-      h = j / gl;
-      l = j - h * gl;
-      isq = h < p.nq * p.Hq;
-      if (isq) {
-        which = h >= p.Hq;
-        h -= which * p.Hq;
-      } else {
-        h -= p.nq * p.Hq;
-        which = h >= p.H;
-        h -= which * p.H;
-      }
-    }
-    const int heads = isq ? p.Hq : p.H, width = isv ? p.dv : p.d;
-    const __nv_bfloat16* src = isv ? p.v : isq ? (which ? p.q[1] : p.q[0]) : (which ? p.k[1] : p.k[0]);
-    src += (static_cast<size_t>(tok) * heads + h) * width;
-    const int row = at[t];
-    const bool lv = live[t];
-    const bool need = mine && (isq ? lv : row >= 0);
-    // this lane's channels: 8 from ca, 8 from cb
-    const bool split = !isv && !p.rope.inter && half > 0 && (p.rope.rot & 15) == 0;
-    int ca = 16 * l, cb = 16 * l + 8;
-    if (split) {
-      const bool turn = 16 * l < p.rope.rot;
-      ca = turn ? 8 * l : ca;
-      cb = turn ? half + 8 * l : cb;
-    }
-    float xa[8], xb[8];
-    if (need) {
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(src + ca), xa);
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(src + cb), xb);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xa[e] = xb[e] = 0.f;
-    }
-    if (!isv && half > 0 && need) {
-      const float2* a = cs + t * half;
-      if (p.rope.inter) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          if (ca + e < p.rope.rot) {
-            const float2 c = a[(ca + e) >> 1];
-            const float x0 = xa[e], x1 = xa[e + 1];
-            xa[e] = x0 * c.x - x1 * c.y;
-            xa[e + 1] = x1 * c.x + x0 * c.y;
-          }
-          if (cb + e < p.rope.rot) {
-            const float2 c = a[(cb + e) >> 1];
-            const float x0 = xb[e], x1 = xb[e + 1];
-            xb[e] = x0 * c.x - x1 * c.y;
-            xb[e + 1] = x1 * c.x + x0 * c.y;
-          }
-        }
-      } else if (split) {
-        if (16 * l < p.rope.rot) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 c = a[ca + e];
-            const float x0 = xa[e], x1 = xb[e];
-            xa[e] = x0 * c.x - x1 * c.y;
-            xb[e] = x1 * c.x + x0 * c.y;
-          }
-        }
-      } else {  // halves that do not end on 8 channels: the partner comes by its own load
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int ch = 16 * l + e;
-          if (ch >= p.rope.rot) continue;
-          const bool lo = ch < half;
-          const float2 c = a[lo ? ch : ch - half];
-          const float other = __bfloat162float(src[lo ? ch + half : ch - half]);
-          float& x = e < 8 ? xa[e & 7] : xb[e & 7];
-          x = lo ? x * c.x - other * c.y : x * c.x + other * c.y;
-        }
-      }
-    }
-    if (isq) {  // (padding tokens get zero queries)
-      if (mine && DA_BOUNDS_V(tok < tokens && h < p.Hq, tok)) {
-        __nv_bfloat16* dst = (which ? p.qo[1] : p.qo[0]) + (static_cast<size_t>(tok) * p.Hq + h) * p.d;
-        *reinterpret_cast<uint4*>(dst + ca) = pack_bf16x8(xa);
-        *reinterpret_cast<uint4*>(dst + cb) = pack_bf16x8(xb);
-      }
-    }
-    const int b = static_cast<int>(tok / p.T);
-    const size_t crow = (static_cast<size_t>(b) * p.n + (row < 0 ? 0 : row)) * p.H + h;
-    void* cache = isv ? p.vc : (which ? p.kc[1] : p.kc[0]);
-    const bool write = need && !isq && DA_BOUNDS_V(b < p.B && row < p.n && h < p.H, row);
-    if (p.fmt == kCacheBf16 || (isv && p.fmt == kCacheFp8k)) {
-      if (write) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(cache) + crow * width;
-        *reinterpret_cast<uint4*>(dst + ca) = pack_bf16x8(xa);
-        *reinterpret_cast<uint4*>(dst + cb) = pack_bf16x8(xb);
-      }
-    } else {
-      float mul = which ? p.kinv[1] : p.kinv[0];
-      float scale = 0.f;
-      if (p.fmt == kCacheFp8) {  // (uniform: every lane of the warp takes part)
-        // largest magnitude as bits: a NaN or an infinity stays the largest
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          m = max(m, max(__float_as_uint(xa[e]) & 0x7fffffffu, __float_as_uint(xb[e]) & 0x7fffffffu));
-        const int lanes = isv ? gv : gl;
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) {
-          const uint32_t o = __shfl_xor_sync(0xffffffffu, m, x);
-          if (x < lanes) m = max(m, o);
-        }
-        const float amax = __uint_as_float(m);
-        // a row below 448 * 2^-126 keeps the smallest normal scale (its inverse stays finite)
-        const float top = (amax < 448.f * 0x1p-126f) ? 448.f * 0x1p-126f : amax;
-        scale = (m == 0) ? 0.f : top / 448.f;
-        mul = 448.f / top;
-      }
-      if (write) {
-        uint8_t* dst = static_cast<uint8_t*>(cache) + crow * width;
-        *reinterpret_cast<uint2*>(dst + ca) = pack_e4m3x8(xa, mul);
-        *reinterpret_cast<uint2*>(dst + cb) = pack_e4m3x8(xb, mul);
-        if (p.fmt == kCacheFp8 && l == 0) {
-          float* sc = isv ? p.vs : (which ? p.ks[1] : p.ks[0]);
-          sc[(static_cast<size_t>(b) * p.H + h) * p.n + row] = scale;
-        }
-      }
-    }
+  const bool halves = !p.rope.inter && half > 0 && (p.rope.rot & 15) == 0;
+  constexpr int RK = 32 / (D / 16), RV = 32 / (DV / 16);  // rows a warp
+  const int rq = nt * p.nq * p.Hq, rk = nt * p.nk * p.H, rv = nt * p.H;
+  const int cq = (rq + RK - 1) / RK, ck = cq + (rk + RK - 1) / RK, cv = ck + (rv + RV - 1) / RV;
+  constexpr int NW = kAppendThreads / 32;
+  for (int c = blockIdx.y * NW + (threadIdx.x >> 5); c < cv; c += gridDim.y * NW) {
+    if (c < cq) append_rows<D, kAppendQuery, FMT>(p, sh, tok0, c * RK, rq, halves);
+    else if (c < ck) append_rows<D, kAppendKey, FMT>(p, sh, tok0, (c - cq) * RK, rk, halves);
+    else append_rows<DV, kAppendValue, FMT>(p, sh, tok0, (c - ck) * RV, rv, halves);
   }
 }
 

@@ -28,6 +28,7 @@ struct RopeParams {
   int copy;        // some tensor is not rotated in place: its other channels are copied
   int inverse;
   int tokens_per_cta;
+  unsigned magic_tok, magic_head;  // for the divisions by a token's and a head's work items (fast_div)
   const int* pos;  // [B, n], or nullptr: token t at position t
   RopeTurns rope;
 };
@@ -49,6 +50,7 @@ struct AppendParams {
   const int* ntok;            // [B], or nullptr: T
   int B, T, Hq, H, n, d, dv, nq, nk, fmt;
   int tokens_per_cta;
+  unsigned magic[3];  // for the divisions by a token's query, key and value rows (fast_div)
   RopeTurns rope;
 };
 

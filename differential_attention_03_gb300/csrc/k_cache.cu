@@ -30,9 +30,17 @@ cudaError_t launch_rope(const RopeParams& p, bool f32, bool vec, int gx, int gy,
              : launch_pdl(rope_kernel<false, false>, p, grid, kRopeThreads, s);
 }
 
+template <int FMT>
+static cudaError_t launch_append(const AppendParams& p, dim3 grid, cudaStream_t s) {
+  if (p.d == 64) return launch_pdl(cache_append_kernel<64, 128, FMT>, p, grid, kAppendThreads, s);
+  return p.dv == 256 ? launch_pdl(cache_append_kernel<128, 256, FMT>, p, grid, kAppendThreads, s)
+                     : launch_pdl(cache_append_kernel<128, 128, FMT>, p, grid, kAppendThreads, s);
+}
+
 cudaError_t launch_cache_append(const AppendParams& p, int gx, int gy, cudaStream_t s) {
-  return launch_pdl(cache_append_kernel, p, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1),
-                    kAppendThreads, s);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), 1);
+  if (p.fmt == kCacheBf16) return launch_append<kCacheBf16>(p, grid, s);
+  return p.fmt == kCacheFp8k ? launch_append<kCacheFp8k>(p, grid, s) : launch_append<kCacheFp8>(p, grid, s);
 }
 
 cudaError_t launch_cache_keep(const KeepParams& p, int gy, cudaStream_t s) {
