@@ -173,8 +173,9 @@ def _check(status: int):
 
 
 def _stream(stream=None) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:  # (without the Stream object that torch.cuda.current_stream() makes: 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t):
@@ -1119,11 +1120,13 @@ def cache_keep(cache: KVCache, lens, path, nkeep, new_lens=None, stream=None) ->
     return new_lens
 
 
+@functools.lru_cache(maxsize=256)
 def tree_decode_workspace_bytes(B: int, T: int, H: int, d: int) -> int:
     """Device workspace of tree_decode (partial softmax states)."""
     return int(lib().diffattn_tree_decode_workspace(B, T, H, d))
 
 
+@functools.lru_cache(maxsize=256)
 def v2_tree_decode_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d: int) -> int:
     return int(lib().diffattn_v2_tree_decode_workspace(B, T, Hq, Hkv, d))
 
