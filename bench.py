@@ -61,10 +61,10 @@ KERNEL_FILES = {
     "v2-bf16-B8Hq32Hkv16-n8192-d128": ['onepass.cuh', 'onepass_inst.cuh', 'k_onepass_v2_d128.cu', 'params.h', 'ptx.cuh', 'status.cuh', 'bounds.cuh', 'api.cu'],
 }
 NCU_TRAFFIC = {  # workload: (source hash of its kernel, bytes per launch: dram__bytes_read.sum + dram__bytes_write.sum)
-    "v1-bf16-B4H16-n2048-d64": ("eda8ec60b9e91f7f", 139291648 + 12816640),
-    "v1-bf16-B2H12-n4096-d128": ("a645e087502723ac", 152373248 + 30054400),
-    "v1-bf16-B1H12-n65536-d128": ("a645e087502723ac", 1761939968 + 405562368),
-    "v2-bf16-B8Hq32Hkv16-n8192-d128": ("ae8a8492959243df", 1073912832 + 254664704),
+    "v1-bf16-B4H16-n2048-d64": ("5ebd0a3c6088e689", 136942336 + 12756992),
+    "v1-bf16-B2H12-n4096-d128": ("e59a6ee7c1d4d565", 152433664 + 30097152),
+    "v1-bf16-B1H12-n65536-d128": ("e59a6ee7c1d4d565", 1757461760 + 404835072),
+    "v2-bf16-B8Hq32Hkv16-n8192-d128": ("b40ac21271493fc3", 1074439680 + 254756096),
 }
 
 
