@@ -265,7 +265,8 @@ TreeShape tree_shape(int B, int T, int H, int pairs) {
 
 size_t tree_workspace(int B, int T, int H, int pairs, int dv) {
   const TreeShape s = tree_shape(B, T, H, pairs);
-  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, da::tree_subs(s.R), dv) * sizeof(float);
+  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, da::tree_subs(s.R), dv) * sizeof(float) +
+         16;  // (states start on 32 bytes)
 }
 
 diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, int T, int H, int pairs, int n, int d,
@@ -330,7 +331,7 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   p.mt = sh.mt;
   p.R = sh.R;
   p.subs = da::tree_subs(sh.R);
-  p.ws = static_cast<float*>(workspace);
+  p.ws = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
   p.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = v2 ? da::launch_tree_v2_d128(p, fmt, s)

@@ -105,9 +105,13 @@ constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree deco
 // Subsets of a CTA's keys that keep their own partial state (the fewer rows, the more).
 __host__ __device__ constexpr int tree_subs(int R) { return R <= 8 ? 4 : R <= 32 ? 2 : 1; }
 
-// Floats of a partial state of the tree decode: (maximum, sum) and O of R rows of both maps, for each subset.
+// A partial state of the tree decode: (maximum, sum) of R rows of both maps, for each subset, then their
+// O from this float on (32-byte sectors), and its floats in all.
+__host__ __device__ __forceinline__ size_t tree_state_o(int R, int subs) {
+  return (4 * static_cast<size_t>(subs) * R + 7) & ~static_cast<size_t>(7);
+}
 __host__ __device__ __forceinline__ size_t tree_state_floats(int R, int subs, int dv) {
-  return 2 * static_cast<size_t>(subs) * R * (dv + 2);
+  return tree_state_o(R, subs) + 2 * static_cast<size_t>(subs) * R * dv;
 }
 
 cudaError_t launch_rope(const RopeParams& p, bool f32, bool vec, int grid_x, int grid_y, cudaStream_t s);

@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
   using C = TreeColsCfg<D, V2, FMT, TP>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NC = C::NC, COLS = C::COLS;
   grid_dep_launch_dependents();
-  grid_dep_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
   uint8_t* misc = smem + C::OFF_MISC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  int* start = reinterpret_cast<int*>(misc + 8);  // sequence, its unit, tile
+  int* start = reinterpret_cast<int*>(misc + 8);  // sequence, group of its units, tile; tiles in all
   unsigned long long* poison = reinterpret_cast<unsigned long long*>(misc + 24);  // [3] by segment
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_XM);
 
@@ -202,20 +201,22 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
     poison[0] = poison[1] = poison[2] = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (columns without a token)
+    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  grid_dep_wait();  // (what came before it touches no global memory)
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (columns without a token)
-    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
 
   const int groups = p.H * p.mt / p.team;  // of units of a sequence
-  const int count = tree_range(p, groups, scratch, start);
+  tree_range(p, groups, scratch, start);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int count = start[3];
   const AbortState ab{abort_flag, p.status};
 
   // Stream of the CTA's tile g, and its number in the stream.
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         reinterpret_cast<float2*>(state)[sm * p.R + row_of(own)] = make_float2((def && live) ? ref : -INFINITY, ls);
       }
       if (any) {
-        float* o = state + 4 * p.subs * p.R + 32 * wq + lane;
+        float* o = state + tree_state_o(p.R, p.subs) + 32 * wq + lane;
 #pragma unroll 1
         for (int mt = 0; mt < C::NMT; ++mt) {
           const uint32_t to = tl + C::TM_O + (stream * C::NMT + mt) * C::PCOLS + map * TP + c0;

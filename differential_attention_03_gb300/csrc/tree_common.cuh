@@ -3,7 +3,8 @@
 //
 // A partial state holds, for each of `subs` subsets of a CTA's keys of a unit
 // and each map: (reference maximum, sum of weights) of the R rows, then O of
-// the rows, unnormalised: float2 [subs][2][R], float [subs][2][R][DV].
+// the rows, unnormalised: float2 [subs][2][R], then, from a 32-byte boundary,
+// float [subs][2][R][DV].
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,6 +47,12 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // long longs.  Every thread returns with (before, total).
 __device__ __forceinline__ void tree_prefix(const TreeParams& p, int upto, long long* scratch, long long& before,
                                             long long& total) {
+  if (p.B <= 32) {  // (every warp for itself, without a barrier)
+    const int lane = threadIdx.x & 31, x = lane < p.B ? tree_len(p, lane).tiles : 0;
+    before = __reduce_add_sync(0xffffffffu, lane < upto ? x : 0);
+    total = __reduce_add_sync(0xffffffffu, x);
+    return;
+  }
   long long a = 0, t = 0;
   for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
     const int x = tree_len(p, b).tiles;
@@ -162,41 +169,61 @@ __device__ __forceinline__ void tmem_store(uint32_t t, const uint32_t (&r)[16]) 
 // the same time they make whole DRAM bursts of rows as short as 64 bytes
 // (e4m3 V1 d64 B8 H16 n32768: 199 us, each CTA for itself 240).
 //
-// The CTA's range, by the whole CTA: its number of tiles; `scratch` 64 long longs, `start` three ints in shared memory.  The caller
-// synchronises the CTA before it reads `start`.
-__device__ __forceinline__ int tree_range(const TreeParams& p, int groups, long long* scratch, int* start) {
-  long long before, total;
-  tree_prefix(p, 0, scratch, before, total);
-  const long long W = total * groups;
+// The range of the CTA's team, from its place among the teams and the line's length W: the first tile and how many.
+__device__ __forceinline__ int team_range(const TreeParams& p, long long W, long long& lo) {
   const long long G = min(static_cast<long long>(p.teams), max(W, 1ll));  // no team between two with tiles is without
   const int team = static_cast<int>(blockIdx.x) / p.team;
-  const long long lo = quotient(W * team, G), hi = quotient(W * (team + 1), G);
-  const int count = team < G ? static_cast<int>(hi - lo) : 0;
+  lo = quotient(W * team, G);
+  return team < G ? static_cast<int>(quotient(W * (team + 1), G) - lo) : 0;
+}
+
+// The sequence among 32 (this lane's has `mine` tiles of all groups) that tile `lo` falls in, whose place
+// is written by its lane: sequence, group, tile.  `base`: tiles before the 32; returns with those after.
+__device__ __forceinline__ bool find_start(int b, long long mine, int groups, long long lo, long long& base, int* start) {
+  long long incl = mine;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, x);
+    if ((threadIdx.x & 31) >= x) incl += y;
+  }
+  const long long excl = base + incl - mine;
+  const bool here = lo >= excl && lo < excl + mine;
+  if (here) {
+    const int tiles = static_cast<int>(quotient(mine, groups));
+    const int grp = static_cast<int>(quotient(lo - excl, tiles));
+    start[0] = b;
+    start[1] = grp;
+    start[2] = static_cast<int>(lo - excl - static_cast<long long>(grp) * tiles);
+  }
+  base += __shfl_sync(0xffffffffu, incl, 31);
+  return __any_sync(0xffffffffu, here);
+}
+
+// The CTA's range, by the whole CTA: start[0..2] are the sequence, its group and tile, start[3] the number
+// of tiles; `scratch` 64 long longs, `start` four ints in shared memory.  The caller synchronises the CTA
+// before it reads them.  Up to 32 sequences are warp 2's alone (one load a lane, no barrier: every CTA
+// begins with this).
+__device__ __forceinline__ void tree_range(const TreeParams& p, int groups, long long* scratch, int* start) {
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32 && count > 0) {  // the sequence that tile `lo` falls in: 32 sequences a step
-    long long base = 0;
+  if (p.B <= 32) {
+    if (threadIdx.x >> 5 != 2) return;
+    const int tiles = lane < p.B ? tree_len(p, lane).tiles : 0;
+    const int total = __reduce_add_sync(0xffffffffu, tiles);
+    long long lo, base = 0;
+    const int count = team_range(p, static_cast<long long>(total) * groups, lo);
+    if (lane == 0) start[3] = count;
+    if (count > 0) find_start(lane, static_cast<long long>(tiles) * groups, groups, lo, base, start);
+    return;
+  }
+  long long before, total, lo, base = 0;
+  tree_prefix(p, 0, scratch, before, total);
+  const int count = team_range(p, total * groups, lo);
+  if (threadIdx.x == 0) start[3] = count;
+  if (threadIdx.x < 32 && count > 0)
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const long long mine = (b0 + lane < p.B) ? static_cast<long long>(tree_len(p, b0 + lane).tiles) * groups : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, x);
-        if (lane >= x) incl += y;
-      }
-      const long long excl = base + incl - mine;
-      const bool here = lo >= excl && lo < excl + mine;
-      if (here) {
-        const int tiles = static_cast<int>(mine / groups);
-        start[0] = b0 + lane;
-        const int grp = static_cast<int>(quotient(lo - excl, tiles));
-        start[1] = grp;
-        start[2] = static_cast<int>(lo - excl - static_cast<long long>(grp) * tiles);
-      }
-      if (__any_sync(0xffffffffu, here)) break;
-      base += __shfl_sync(0xffffffffu, incl, 31);
+      if (find_start(b0 + lane, mine, groups, lo, base, start)) break;
     }
-  }
-  return count;
 }
 
 // Every role walks the same segments: the CTA's tiles of one unit each.
@@ -233,6 +260,13 @@ __device__ __forceinline__ int walk_unit(const TreeParams& p, const TreeWalk& w)
 }
 __device__ __forceinline__ float* tree_state(const TreeParams& p, long long group, int team, int lane, int dv) {
   return p.ws + (static_cast<size_t>(group + team) * p.team + lane) * tree_state_floats(p.R, p.subs, dv);
+}
+
+// Eight floats to a 32-byte boundary: a whole sector, where a lane has a row of its own.
+__device__ __forceinline__ void store8(float* at, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 // What token `tok` of sequence b sees of the drafts in the cache.
@@ -308,22 +342,28 @@ __device__ __forceinline__ void split_e4m3x8(const uint4& x, int sh, uint2& hi, 
   lo = make_uint2(l[0], l[1]);
 }
 
-// Merges the partial states of a unit and finishes one row a CTA: two channels
-// a thread.  A handful of dependent loads is all that it does, so it is built
-// for latency: the states' maxima and sums by as many threads at once, then
-// their weights, then every state's O with nothing to wait for in between
-// (40 rows of 4 to 8 states: 14.4 us one state after the other, cold;
-// 11 us this way).
+// Merges the partial states of a unit and finishes one row a CTA.  A handful
+// of dependent loads is all that it does, so it is built for latency: the
+// states' maxima and sums by as many threads at once, and every state's O with
+// nothing to wait for, the first ones beside the maxima.  The threads are
+// kTreeMergers groups, each of which takes every kTreeMergers-th state, two
+// channels a thread.  (Both kernels of a call of 5 tokens over 512 keys of 8
+// V1 heads, d64, replayed from a graph: 14.3 us with one state after the other
+// and the CTA's range found by all its warps, 9.7 us this way; one head's 512
+// tiles on every SM: 140 and 30 us.  Four groups take 22 us there, but 85
+// instead of 77 where 768 rows want to be on the SMs at once.)
 constexpr int kTreeMaxStates = 160 * 4;  // of a unit: one a team and subset
+constexpr int kTreeMergers = 2;
 
 template <int DV, bool V2>
-__global__ void __launch_bounds__(DV / 2) tree_combine_kernel(const __grid_constant__ TreeParams p, float o_mult) {
+__global__ void __launch_bounds__(kTreeMergers * DV / 2) tree_combine_kernel(const __grid_constant__ TreeParams p, float o_mult) {
   grid_dep_launch_dependents();
   grid_dep_wait();
-  constexpr int NT = DV / 2;
+  constexpr int NG = DV / 2, NT = kTreeMergers * NG, NW = NT / 32;
   __shared__ long long scratch[64];
   __shared__ float2 ml[2][kTreeMaxStates];  // maximum and sum, then weight and whether there is one
-  __shared__ float red[3 * NT / 32];
+  __shared__ float red[4 * NW + NG / 32];
+  __shared__ float2 part[kTreeMergers][NG];
   const int HM = p.H * p.mt;
   const int unit = static_cast<int>(blockIdx.x) / p.R, r = static_cast<int>(blockIdx.x) - unit * p.R;
   const int b = unit / HM, hm = unit - b * HM;
@@ -331,18 +371,20 @@ __global__ void __launch_bounds__(DV / 2) tree_combine_kernel(const __grid_const
   const int pj = r / p.T, t = r - pj * p.T;
   const int pair = mtile * p.ppt + pj;
   if (pair >= p.pairs) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / NG, i2 = threadIdx.x % NG;  // this thread's states and channels
   // what does not depend on the states, on its way
   const size_t orow = V2 ? (static_cast<size_t>(b) * p.T + t) * (p.H * p.pairs) + h * p.pairs + pair
                          : (static_cast<size_t>(b) * p.T + t) * p.H + h;
   const float coef = V2 ? 1.f / (1.f + expf(-p.lam_logits[b * p.sb + t * p.st + h * p.pairs + pair])) : *p.lambda;
   float2 g = make_float2(1.f, 1.f);
-  if (!V2 && p.gamma) g = make_float2(p.gamma[2 * threadIdx.x], p.gamma[2 * threadIdx.x + 1]);
+  if (!V2 && p.gamma) g = make_float2(p.gamma[2 * i2], p.gamma[2 * i2 + 1]);
   const TreeLen len = tree_len(p, b);
   long long before, total;
   tree_prefix(p, b, scratch, before, total);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float y0 = 0.f, y1 = 0.f;
-  if (len.tiles > 0 && t < len.nt) {  // (the same for the whole CTA)
+  const bool any = len.tiles > 0 && t < len.nt;  // (the same for the whole CTA)
+  float2 y = make_float2(0.f, 0.f);
+  if (any) {
     const int groups = HM / p.team, grp = hm / p.team;
     const long long W = total * groups;
     const long long G = min(static_cast<long long>(p.teams), W);
@@ -350,68 +392,110 @@ __global__ void __launch_bounds__(DV / 2) tree_combine_kernel(const __grid_const
     const int c0 = static_cast<int>(quotient((s + 1) * G - 1, W)), c1 = static_cast<int>(quotient((e + 1) * G - 1, W));
     const float* src = tree_state(p, static_cast<long long>(b) * groups + grp, c0, hm % p.team, DV);
     const size_t sf = p.team * tree_state_floats(p.R, p.subs, DV);
-    const int n = (c1 - c0 + 1) * p.subs;
-    float M[2] = {-INFINITY, -INFINITY};
+    const int n = (c1 - c0 + 1) * p.subs, shift = p.subs >> 1;  // (subs: 1, 2 or 4)
+    const float* o = src + tree_state_o(p.R, p.subs) + static_cast<size_t>(r) * DV + 2 * i2;
+    constexpr int U = 4;
+    float2 v[U][2];
+    auto load = [&](int k0) {  // O of states k0, k0 + kTreeMergers, ... (what is not there is not used)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kTreeMergers;
+        if (k >= n) continue;
+        const float* at = o + (k >> shift) * sf + static_cast<size_t>(2 * (k & (p.subs - 1))) * p.R * DV;
+        v[u][0] = *reinterpret_cast<const float2*>(at);
+        v[u][1] = *reinterpret_cast<const float2*>(at + static_cast<size_t>(p.R) * DV);
+      }
+    };
+    load(group);
+    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
     for (int i = threadIdx.x; i < 2 * n; i += NT) {
-      const int m = i >= n, k = i - m * n, c = k / p.subs, sub = k - c * p.subs;
-      const float2 x = reinterpret_cast<const float2*>(src + c * sf)[(2 * sub + m) * p.R + r];
+      const int m = i >= n, k = i - m * n;
+      const float2 x = reinterpret_cast<const float2*>(src + (k >> shift) * sf)[(2 * (k & (p.subs - 1)) + m) * p.R + r];
       ml[m][k] = x;
-      M[m] = fmaxf(M[m], x.x);
+      M[0] = m ? M[0] : fmaxf(M[0], x.x);
+      M[1] = m ? fmaxf(M[1], x.x) : M[1];
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) M[m] = fmaxf(M[m], __shfl_xor_sync(0xffffffffu, M[m], x));
-      if (lane == 0) red[m * (NT / 32) + warp] = M[m];
+      if (lane == 0) red[m * NW + warp] = M[m];
     }
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      M[m] = red[m * (NT / 32)];
+      M[m] = red[m * NW];
 #pragma unroll
-      for (int i = 1; i < NT / 32; ++i) M[m] = fmaxf(M[m], red[m * (NT / 32) + i]);
+      for (int i = 1; i < NW; ++i) M[m] = fmaxf(M[m], red[m * NW + i]);
     }
     for (int i = threadIdx.x; i < 2 * n; i += NT) {
       const int m = i >= n, k = i - m * n;
       const float2 x = ml[m][k];
       const bool none = x.x == -INFINITY && x.y == 0.f;  // nothing seen in this state
-      const float w = none ? 0.f : (x.x == M[m]) ? 1.f : ex2(x.x - M[m]);
-      ml[m][k] = make_float2(none ? -1.f : w, none ? 0.f : x.y * w);  // (a weight of -1: O is not there)
+      const float top = m ? M[1] : M[0];
+      const float w = none ? 0.f : (x.x == top) ? 1.f : ex2(x.x - top);
+      ml[m][k].x = none ? -1.f : w;  // (a weight of -1: O is not there)
+      const float lw = none ? 0.f : x.y * w;
+      L[0] += m ? 0.f : lw;
+      L[1] += m ? lw : 0.f;
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) L[m] += __shfl_xor_sync(0xffffffffu, L[m], x);
+      if (lane == 0) red[(2 + m) * NW + warp] = L[m];
     }
     __syncthreads();
-    float L[2] = {0.f, 0.f}, a0[2] = {0.f, 0.f}, a1[2] = {0.f, 0.f};
-    const float* o = src + p.subs * 4 * p.R + static_cast<size_t>(r) * DV;
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const int c = k / p.subs, sub = k - c * p.subs;
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    for (int k0 = group; k0 < n; k0 += U * kTreeMergers) {
+      if (k0 != group) load(k0);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float2 w = ml[m][k];
-        float2 v = make_float2(0.f, 0.f);
-        if (w.x != -1.f) v = reinterpret_cast<const float2*>(o + c * sf + static_cast<size_t>(2 * sub + m) * p.R * DV)[threadIdx.x];
-        L[m] += w.y;
-        a0[m] = fmaf(v.x, w.x, a0[m]);
-        a1[m] = fmaf(v.y, w.x, a1[m]);
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kTreeMergers;
+        if (k >= n) continue;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float w = ml[m][k].x;
+          if (w == -1.f) continue;
+          acc[m].x = fmaf(v[u][m].x, w, acc[m].x);
+          acc[m].y = fmaf(v[u][m].y, w, acc[m].y);
+        }
       }
     }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      L[m] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) L[m] += red[(2 + m) * NW + i];
+    }
     const float w1 = (L[0] == 0.f) ? 0.f : o_mult / L[0], w2 = (L[1] == 0.f) ? 0.f : -coef * o_mult / L[1];
-    y0 = a0[0] * w1 + a0[1] * w2;
-    y1 = a1[0] * w1 + a1[1] * w2;
+    y = make_float2(acc[0].x * w1 + acc[1].x * w2, acc[0].y * w1 + acc[1].y * w2);
+    part[group][i2] = y;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int i = 1; i < kTreeMergers; ++i) {
+        y.x += part[i][i2].x;
+        y.y += part[i][i2].y;
+      }
+    }
   }
   float rinv = 1.f;
   if (!V2) {
-    float ss = y0 * y0 + y1 * y1;
+    if (group == 0) {
+      float ss = y.x * y.x + y.y * y.y;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-    if (lane == 0) red[2 * (NT / 32) + warp] = ss;
+      for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
+      if (lane == 0) red[4 * NW + warp] = ss;
+    }
     __syncthreads();
     float tot = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) tot += red[2 * (NT / 32) + i];
+    for (int i = 0; i < NG / 32; ++i) tot += red[4 * NW + i];
     rinv = p.norm_mult * rsqrtf(tot * (1.f / DV) + p.eps);
   }
-  if (DA_BOUNDS_V(b < p.B && t < p.T && h < p.H, t))
-    reinterpret_cast<uint32_t*>(p.out + orow * DV)[threadIdx.x] = pack_bf16x2(y0 * rinv * g.x, y1 * rinv * g.y);
+  if (group == 0 && DA_BOUNDS_V(b < p.B && t < p.T && h < p.H, t))
+    reinterpret_cast<uint32_t*>(p.out + orow * DV)[i2] = pack_bf16x2(y.x * rinv * g.x, y.y * rinv * g.y);
 }
 
 // Launches a tree kernel and the merge, each a programmatic dependent of what precedes it.
@@ -434,7 +518,7 @@ cudaError_t launch_tree_pair(void (*kern)(TreeParams), int threads, int smem_byt
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cc = {};
   cc.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(p.B) * p.H * p.mt * p.R), 1, 1);
-  cc.blockDim = dim3(DV / 2, 1, 1);
+  cc.blockDim = dim3(kTreeMergers * DV / 2, 1, 1);
   cc.stream = s;
   cc.attrs = attr;
   cc.numAttrs = 1;

@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   using C = TreeRowsCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
   grid_dep_launch_dependents();
-  grid_dep_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -150,7 +149,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   uint8_t* misc = smem + C::OFF_MISC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
-  int* start = reinterpret_cast<int*>(misc + 16);  // b, unit of the sequence, tile
+  int* start = reinterpret_cast<int*>(misc + 16);  // sequence, group of its units, tile; tiles in all
   unsigned long long* poison = reinterpret_cast<unsigned long long*>(misc + 32);  // [3] by segment
   long long* scratch = reinterpret_cast<long long*>(smem + C::OFF_XM);
 
@@ -181,20 +180,22 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
     poison[0] = poison[1] = poison[2] = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (rows without a query, and V1's zeros)
+    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+  grid_dep_wait();  // (what came before it touches no global memory)
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < C::Q_BYTES / 16; i += C::NTHREADS)  // (rows without a query, and V1's zeros)
-    reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
 
   const int groups = p.H * p.mt / p.team;  // of units of a sequence
-  const int count = tree_range(p, groups, scratch, start);
+  tree_range(p, groups, scratch, start);
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int count = start[3];
   const AbortState ab{abort_flag, p.status};
 
   if (warp == 0) {
@@ -717,7 +718,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
           if (see & poison[k % 3]) l = __uint_as_float(0x7fffffffu);
           reinterpret_cast<float2*>(state)[sm * p.R + r] = make_float2(m_used, l);
         }
-        float4* o4 = reinterpret_cast<float4*>(state + 4 * p.subs * p.R + (static_cast<size_t>(sm) * p.R + r) * DV + OC * qd);
+        float* o8 = state + tree_state_o(p.R, p.subs) + (static_cast<size_t>(sm) * p.R + r) * DV + OC * qd;
 #pragma unroll 1
         for (int q = 0; q < OC / 32; ++q) {
           uint32_t o[32];
@@ -725,9 +726,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
           tmem_ld_wait(o);
           if (here) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c, ++o4)
-              *o4 = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]), __uint_as_float(o[4 * c + 2]),
-                                __uint_as_float(o[4 * c + 3]));
+            for (int c = 0; c < 4; ++c, o8 += 8) store8(o8, o + 8 * c);
           }
         }
         tc_fence_before();

@@ -212,10 +212,11 @@ def test_tree_refusals(L):
 
 def test_tree_workspace_sizes(L):
     # a partial state of 2 R (dv + 2) floats a row tile and a CTA; four of them up to 8 rows, two up to 32
-    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 4 * 2 * 5 * 130 * 4
-    assert da.tree_decode_workspace_bytes(2, 9, 3, 128) == (6 + 160) * 2 * 2 * 9 * 258 * 4
-    assert da.v2_tree_decode_workspace_bytes(1, 20, 16, 2, 128) == (1 * 2 * 2 + 160) * 2 * 60 * 130 * 4
-    assert da.v2_tree_decode_workspace_bytes(1, 64, 8, 1, 128) == (4 + 160) * 2 * 64 * 130 * 4
+    # (O from a multiple of 8 floats on; 16 bytes to reach a 32-byte boundary)
+    assert da.tree_decode_workspace_bytes(2, 5, 3, 64) == (6 + 160) * 4 * 2 * 5 * 130 * 4 + 16
+    assert da.tree_decode_workspace_bytes(2, 9, 3, 128) == (6 + 160) * 2 * 2 * 9 * 258 * 4 + 16
+    assert da.v2_tree_decode_workspace_bytes(1, 20, 16, 2, 128) == (1 * 2 * 2 + 160) * 2 * 60 * 130 * 4 + 16
+    assert da.v2_tree_decode_workspace_bytes(1, 64, 8, 1, 128) == (4 + 160) * 2 * 64 * 130 * 4 + 16
     assert da.tree_decode_workspace_bytes(1, 65, 1, 64) == 0
     assert da.v2_tree_decode_workspace_bytes(1, 4, 6, 2, 128) == 0
 
