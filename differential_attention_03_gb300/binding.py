@@ -912,6 +912,10 @@ def _current(t, name) -> int:
     return dev
 
 
+_PTRS = [ctypes.c_void_p * k for k in range(5)]
+_INTS = [ctypes.c_int * k for k in range(5)]
+
+
 def rope(tensors, spec: RopeSpec, positions=None, inverse: bool = False, out=None, stream=None) -> list:
     """Rotary positions on up to four tensors [B, n, heads, d] (bf16 or fp32, d <= 128) in one kernel.
 
@@ -941,10 +945,9 @@ def rope(tensors, spec: RopeSpec, positions=None, inverse: bool = False, out=Non
         for k, (x, o) in enumerate(zip(xs, out)):
             _on(o, f"out[{k}]", dt, x.shape, dev)
     m = len(xs)
-    _check(lib().diffattn_rope(_dt(xs[0]), B, n, d, m, (ctypes.c_void_p * m)(*[x.data_ptr() for x in xs]),
-                               (ctypes.c_int * m)(*[x.shape[2] for x in xs]), ctypes.byref(spec), _ptr(positions),
-                               1 if inverse else 0, (ctypes.c_void_p * m)(*[o.data_ptr() for o in out]),
-                               _stream(stream)))
+    _check(lib().diffattn_rope(_dt(xs[0]), B, n, d, m, _PTRS[m](*[x.data_ptr() for x in xs]),
+                               _INTS[m](*[x.shape[2] for x in xs]), ctypes.byref(spec), _addr(positions),
+                               1 if inverse else 0, _PTRS[m](*[o.data_ptr() for o in out]), _stream(stream)))
     return out
 
 

@@ -44,6 +44,22 @@
 // softmax, four warps a lane quarter, each a quarter of a tile's key columns
 // (quarters without rows sleep).  TMEM: O, then two score tiles, in which P
 // replaces the scores.
+//
+// Rounding.  Weights are rounded to bf16 (FP8: two e4m3 terms, about as near)
+// before they meet the values, as in the forward and the one-token decode: half
+// a step of 2^-8 each, at random, which is 1.8e-3 of an output over 8192 random
+// keys beside the 1.7e-3 of rounding the output itself.  Scores, maxima, sums
+// and O stay fp32.
+//
+// Measured (this kernel alone): bf16 V1 d128 B4 H12 T16 n8192 71 us (403 MB, 5.7
+// TB/s; about 10 us of it are the way in and the last states' stores), V2 d128
+// B4 H16 T8 47 us (269 MB); over 32768 keys HBM's rate (bf16 V1 d128 B8 H8 312
+// us, 6.9 TB/s).  e4m3 with 64 tokens, V1 d128 H12 n65536: 118 us (415 MB, 3.5
+// TB/s), bound by the softmax warps: 128 x 128 weights a tile are scaled,
+// exponentiated and split for the 64 KB that the tile reads.  (Tried there: keys
+// as the MMAs' rows with 64 columns, whose 32 columns a thread do not fit the
+// registers, 216 us against 138; maxima exchanged only when one moves, and early
+// looks at the barriers: no gain.)
 #pragma once
 
 #include "tree_common.cuh"
