@@ -310,7 +310,7 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   const int kbox = (k8 && d == 64) ? 64 : 128;
   if ((st = cache_map(&p.tm_k1, k1, B, nn, H, d, k8 ? 1 : 2, kbox, 128, side)) != DIFFATTN_OK) return st;
   if (!v2 && (st = cache_map(&p.tm_k2, k2, B, nn, H, d, k8 ? 1 : 2, kbox, 128, side)) != DIFFATTN_OK) return st;
-  if ((st = cache_map(&p.tm_v, v, B, nn, H, dv, v8 ? 1 : 2, 128, da::tree_value_keys(dv, v8), side)) != DIFFATTN_OK) return st;
+  if ((st = cache_map(&p.tm_v, v, B, nn, H, dv, v8 ? 1 : 2, 128, da::kTreeValueKeys, side)) != DIFFATTN_OK) return st;
   p.q1 = static_cast<const __nv_bfloat16*>(q1);
   p.q2 = static_cast<const __nv_bfloat16*>(q2);
   p.k1_scales = kscales[0];

@@ -68,7 +68,7 @@ struct KeepParams {
 struct TreeParams {
   CUtensorMap tm_k1;  // key caches: boxes of 128 keys x 128 bytes (e4m3 at d = 64: 64 bytes)
   CUtensorMap tm_k2;  // (V1 only)
-  CUtensorMap tm_v;   // value cache: boxes of tree_value_keys keys x 128 bytes
+  CUtensorMap tm_v;   // value cache: boxes of kTreeValueKeys keys x 128 bytes
   const __nv_bfloat16* q1;  // V1 [B, T, H, d]; V2 [B, T, Hq, d]
   const __nv_bfloat16* q2;  // V1 only
   const float* k1_scales;   // fp8: [B, H, n]
@@ -97,8 +97,7 @@ struct TreeParams {
   int* status;
 };
 
-// Keys of one value box of the tree decode.
-__host__ __device__ constexpr int tree_value_keys(int dv, bool v8) { return dv * (v8 ? 1 : 2) == 512 ? 32 : 64; }
+constexpr int kTreeValueKeys = 64;  // keys of a value box of the tree decode, and of a value slot of its rings
 
 constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree decode
 

@@ -29,9 +29,8 @@
 // reduce the column maxima, and rescale the sums and O^T.  Sums of weights
 // stay in the threads' registers until the unit ends.
 //
-// Formats.  bf16; FP8K: e4m3 keys with one scale a tensor, bf16 values; FP8:
-// e4m3 keys and values with an fp32 scale a row.  8-bit operands are not
-// converted: a query row is scaled by a power of two and split into two e4m3
+// Operands.  e4m3 keys and values with an fp32 scale a row, as the cache holds
+// them: a query row is scaled by a power of two and split into two e4m3
 // terms (hi + lo holds a bf16 value's eight bits), and so is P, at twice the
 // MMA rate.  A key's scale multiplies its scores; a value row's scale is
 // folded into P before the split, and the reference is the maximum of score +
@@ -48,9 +47,15 @@
 //
 // Roles (640 threads, one CTA per SM): warp 0 TMA producer; warp 1 score
 // MMAs; warp 2 P V MMAs; warps 4-19 softmax, four warpgroups (one key a
-// thread).  Up to 32 columns a map: (stream, map), where even and odd tiles
-// are two streams with references, O^T and partial states of their own, so
-// that neither waits for the other; 64 columns: (map, half of the columns).
+// thread).  With 8 columns a map each is a stream (every fourth tile, with
+// references, O^T and a partial state of its own, so that none waits for
+// another) of both maps; with 16, a map of one of two streams; with 32, half
+// the columns of a map.
+//
+// Measured (this kernel alone, one token): V1 d64 B8 H16 n32768 176 us (1.12
+// GB with the scales, 6.4 TB/s); 32 tokens V1 d128 B8 H8 n32768 203 us with
+// the merge (5.4 TB/s), V1 d64 B8 H16 284 us (3.9 TB/s), where the softmax
+// warps bound it.
 #pragma once
 
 #include "tree_common.cuh"
@@ -60,42 +65,35 @@
 
 namespace da {
 
-template <int D, bool V2, int FMT, int TP>
+template <int D, bool V2, int TP>
 struct TreeColsCfg {
-  static constexpr bool K8 = FMT != kCacheBf16, V8 = FMT == kCacheFp8;
   static constexpr int BN = 128;              // keys of a tile
   static constexpr int DV = V2 ? D : 2 * D;
   static constexpr int NMT = DV / 128;        // 128-channel MMAs of V^T
   static constexpr int NMAP_K = V2 ? 1 : 2;   // key tensors
-  static constexpr int NTERM = K8 ? 2 : 1;    // terms of a query row
   // Streams: tile g belongs to stream g % NSTREAM, which has its own references, O^T and P.  With 8
   // columns a map a warpgroup takes a stream's both maps, with 16 one map, with 32 half a map.
   static constexpr int NSTREAM = 32 / TP;
   static constexpr int NBUF = NSTREAM > 2 ? NSTREAM : 2;  // score tiles
   static constexpr int NC = 16;                 // columns of a softmax thread
   static constexpr int COLS = 2 * TP;           // columns of both maps
-  // The terms of an 8-bit operand stand side by side as columns, so that one MMA takes both.
-  static constexpr int SCOLS = COLS * NTERM;            // of a score tile: [map][term][TP]
-  static constexpr int PCOLS = COLS * (V8 ? 2 : 1);     // of P and O^T: [term][map][TP]
-  static constexpr int KROW = D * (K8 ? 1 : 2);          // bytes of a key row
-  static constexpr int KBOXB = KROW < 128 ? KROW : 128;  // bytes of a key box row (its swizzle width)
-  static constexpr int KBOX = KROW / KBOXB;
-  static constexpr int VROW = DV * (V8 ? 1 : 2);
+  // The terms of an operand stand side by side as columns, so that one MMA takes both.
+  static constexpr int SCOLS = 2 * COLS;  // of a score tile: [map][term][TP]
+  static constexpr int PCOLS = 2 * COLS;  // of P and O^T: [term][map][TP]
+  static constexpr int KROW = D;          // bytes of a key row (and its swizzle width)
+  static constexpr int VROW = DV;
   static constexpr int VBOX = VROW / 128;
-  static constexpr int VKEYS = tree_value_keys(DV, V8);  // keys of a value slot
+  static constexpr int VKEYS = kTreeValueKeys;  // of a value slot
   static constexpr int VF = BN / VKEYS;
   static constexpr int K_SLOT = BN * KROW, V_SLOT = VKEYS * VROW;
-  // Query rows in shared memory, as the score MMAs' B operands.  A V1 map's operand is its own rows;
-  // an MMA wants 16 columns at least, so 8 bf16 rows a map share 16 columns: map 1's operand is
-  // [Q_1; 0], map 2's [0; Q_2], windows of Q_1 | zeros | Q_2, and their MMAs add up.
-  static constexpr bool SHARED = !V2 && TP * NTERM < 16;
-  static constexpr int QROWS = SHARED ? 3 * TP : SCOLS;
-  static constexpr int QK_N = (V2 || SHARED) ? SCOLS : TP * NTERM;
+  // Query rows in shared memory, as the score MMAs' B operands: a V1 map's are its own rows.
+  static constexpr int QROWS = SCOLS;
+  static constexpr int QK_N = V2 ? SCOLS : 2 * TP;
   static constexpr int Q_BYTES = (QROWS * KROW + 1023) / 1024 * 1024;
-  static constexpr int PROW = PCOLS * (V8 ? 1 : 2);  // bytes of a key's row of P^T (its swizzle width)
+  static constexpr int PROW = PCOLS;         // bytes of a key's row of P^T (its swizzle width)
   static constexpr int P_BYTES = BN * PROW;          // of a stream
   // Rings: about 160 KB in flight.
-  static constexpr int NK = D == 64 ? (V8 ? 10 : K8 ? 8 : 6) : (K8 ? 5 : 2);
+  static constexpr int NK = D == 64 ? 10 : 5;
   static constexpr int NV = V_SLOT == 8192 ? (D == 64 ? 11 : 10) : 6;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = Q_BYTES;
@@ -113,9 +111,8 @@ struct TreeColsCfg {
   static constexpr uint32_t TM_O = 0, TM_S = NSTREAM * NMT * PCOLS;  // O^T [stream][128 channels], the score tiles
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int QK_STEPS = KROW / 32;
-  static constexpr uint32_t IDESC_QK = K8 ? idesc_e4m3(128, QK_N) : idesc_bf16(128, QK_N, false, false);
-  static constexpr uint32_t IDESC_PV =
-      V8 ? (idesc_e4m3(128, PCOLS) | (3u << 15)) : idesc_bf16(128, PCOLS, true, true);
+  static constexpr uint32_t IDESC_QK = idesc_e4m3(128, QK_N);
+  static constexpr uint32_t IDESC_PV = idesc_e4m3(128, PCOLS) | (3u << 15);  // (V^T and P^T: both transposed)
   static constexpr int NSOFT = 16;              // softmax warps
   static constexpr int NARR = NSOFT / NSTREAM;  // of a stream
   static constexpr int NTHREADS = (4 + NSOFT) * 32;
@@ -152,9 +149,9 @@ __device__ __forceinline__ float lanes_reduce(const float (&v)[NC], int lane, Op
   return t[0];
 }
 
-template <int D, bool V2, int FMT, int TP>
+template <int D, bool V2, int TP>
 __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant__ TreeParams p) {
-  using C = TreeColsCfg<D, V2, FMT, TP>;
+  using C = TreeColsCfg<D, V2, TP>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NC = C::NC, COLS = C::COLS;
   grid_dep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
@@ -239,7 +236,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         mbar_arrive_expect_tx(&kfull[s], C::K_SLOT);
         uint8_t* dst = smem + C::OFF_K + s * C::K_SLOT;
         if (DA_BOUNDS_V(key0 < p.n && b < p.B && h < p.H, key0))
-          for (int bx = 0; bx < C::KBOX; ++bx) tma_load_4d(dst + bx * BN * C::KBOXB, map, &kfull[s], bx * 64, h, key0, b);
+          tma_load_4d(dst, map, &kfull[s], 0, h, key0, b);
         return true;
       };
       auto load_v = [&](int b, int h, int key0) {
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           uint8_t* dst = smem + C::OFF_V + s * C::V_SLOT;
           if (DA_BOUNDS_V(b < p.B && h < p.H, key0))  // (a box past n reads zeros)
             for (int bx = 0; bx < C::VBOX; ++bx)
-              tma_load_4d(dst + bx * C::VKEYS * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
+              tma_load_4d(dst + bx * C::VKEYS * 128, &p.tm_v, &vfull[s], bx * 128, h,
                           key0 + part * C::VKEYS, b);
         }
         return true;
@@ -300,8 +297,8 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
     for (uint32_t k = 0; ok && __shfl_sync(0xffffffffu, w.rem, 0) > 0; ++k) {
       const int seg = __shfl_sync(0xffffffffu, walk_seg(w), 0);
       if (warp == 1) {
-        const uint64_t dk0 = sdesc_rows<C::KBOXB>(smem_u32(smem + C::OFF_K), 16);
-        const uint64_t dq0 = sdesc_rows<C::KBOXB>(smem_u32(smem + C::OFF_Q), 16);
+        const uint64_t dk0 = sdesc_rows<C::KROW>(smem_u32(smem + C::OFF_K), 16);
+        const uint64_t dq0 = sdesc_rows<C::KROW>(smem_u32(smem + C::OFF_Q), 16);
         ok = waitp(q_full, k & 1u);
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t s = g % C::NBUF;
@@ -310,18 +307,13 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           for (int m = 0; m < C::NMAP_K; ++m) {
             if (ok && !waitp(&kfull[slot], phase)) ok = false;
             if (!ok) break;
-            const uint32_t d = tm + C::TM_S + s * C::SCOLS + (C::SHARED ? 0 : m * TP * C::NTERM);
+            const uint32_t d = tm + C::TM_S + s * C::SCOLS + m * 2 * TP;
             const uint32_t koff = slot * (C::K_SLOT >> 4);
 #pragma unroll
             for (int st = 0; st < C::QK_STEPS; ++st) {
-              const uint64_t a = desc_at(dk0, koff + (((st >> 2) * (BN * 128) + (st & 3) * 32) >> 4));
-              const uint64_t bd = desc_at(
-                  dq0, (m * TP * C::NTERM * C::KBOXB + (st >> 2) * (C::QROWS * 128) + (st & 3) * 32) >> 4);
-              const uint32_t acc = (st > 0 || (C::SHARED && m > 0)) ? 1u : 0u;
-              if constexpr (C::K8)
-                mma_ss_f8_elect(d, a, bd, C::IDESC_QK, acc);
-              else
-                mma_ss_elect(d, a, bd, C::IDESC_QK, acc);
+              const uint64_t a = desc_at(dk0, koff + ((st * 32) >> 4));
+              const uint64_t bd = desc_at(dq0, (m * 2 * TP * C::KROW + st * 32) >> 4);
+              mma_ss_f8_elect(d, a, bd, C::IDESC_QK, st > 0 ? 1u : 0u);
             }
             tc_commit_elect(&kempty[slot]);
             if (++slot == NK) {
@@ -344,20 +336,16 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
             if (ok && !waitp(&vfull[slot], phase)) ok = false;
             if (!ok) break;
             const uint32_t voff = slot * (C::V_SLOT >> 4);
-            constexpr int KS = C::V8 ? 32 : 16;  // keys of an MMA
+            constexpr int KS = 32;  // keys of an MMA
 #pragma unroll
             for (int mt = 0; mt < C::NMT; ++mt) {
               const uint32_t d = tm + C::TM_O + (st * C::NMT + mt) * C::PCOLS;
 #pragma unroll
               for (int kk = 0; kk < C::VKEYS / KS; ++kk) {
-                // V^T: 128 channels are one box of e4m3, two boxes of bf16
-                const uint64_t a = desc_at(dv0, voff + ((mt * (C::V8 ? 1 : 2) * C::VKEYS * 128 + kk * KS * 128) >> 4));
+                // V^T: 128 channels are one box
+                const uint64_t a = desc_at(dv0, voff + ((mt * C::VKEYS * 128 + kk * KS * 128) >> 4));
                 const uint64_t bd = desc_at(dp0, poff + (((part * C::VKEYS + kk * KS) * C::PROW) >> 4));
-                const uint32_t acc = (part > 0 || kk > 0) ? 1u : again;
-                if constexpr (C::V8)
-                  mma_ss_f8_elect(d, a, bd, C::IDESC_PV, acc);
-                else
-                  mma_ss_elect(d, a, bd, C::IDESC_PV, acc);
+                mma_ss_f8_elect(d, a, bd, C::IDESC_PV, (part > 0 || kk > 0) ? 1u : again);
               }
             }
             tc_commit_elect(&vempty[slot]);
@@ -390,7 +378,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
     const int own = lane % NC;                           // the column this lane reduces
     float* xm = reinterpret_cast<float*>(smem + C::OFF_XM) + wg * 64;
     float* ac = reinterpret_cast<float*>(smem + C::OFF_AC) + wg * 16;
-    const float top = C::V8 ? kTreeRescale8Log2 : kTreeRescaleLog2;
+    const float top = kTreeRescale8Log2;
     uint32_t g0 = 0;  // the segment's first tile
     TreeWalk w = walk_begin(p, count, start);
     // (an aborted CTA walks on: every wait then returns at once, and no warp misses a named barrier)
@@ -399,24 +387,17 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
       const int hm = walk_unit(p, w), h = hm / p.mt, mtile = hm - h * p.mt;
       const int first = static_cast<int>((stream - g0) % C::NSTREAM);  // this stream's first tile of the segment
       // this thread's key and value scales of tile i of the segment
-      const float* krow = nullptr;
-      const float* krow2 = nullptr;
-      const float* vrow = nullptr;
-      if constexpr (C::V8) {
-        const size_t row = (static_cast<size_t>(w.b) * p.H + h) * p.n;
-        krow = ((map && !V2) ? p.k2_scales : p.k1_scales) + row;
-        if (BOTH && !V2) krow2 = p.k2_scales + row;
-        vrow = p.v_scales + row;
-      }
+      const size_t srow = (static_cast<size_t>(w.b) * p.H + h) * p.n;
+      const float* krow = ((map && !V2) ? p.k2_scales : p.k1_scales) + srow;
+      const float* krow2 = (BOTH && !V2) ? p.k2_scales + srow : nullptr;
+      const float* vrow = p.v_scales + srow;
       float ks_next = 0.f, ks2_next = 0.f, vs_next = 0.f;
       auto fetch_scales = [&](int i) {
-        if constexpr (C::V8) {
-          const int j = (w.t + i) * BN + key;
-          const bool in = i < seg && j < w.len.end;
-          ks_next = in ? krow[j] : 0.f;
-          if (BOTH && !V2) ks2_next = in ? krow2[j] : 0.f;
-          vs_next = in ? vrow[j] : 0.f;
-        }
+        const int j = (w.t + i) * BN + key;
+        const bool in = i < seg && j < w.len.end;
+        ks_next = in ? krow[j] : 0.f;
+        if (BOTH && !V2) ks2_next = in ? krow2[j] : 0.f;
+        vs_next = in ? vrow[j] : 0.f;
       };
       fetch_scales(first);
       // ---- the segment's queries, once the previous segment's last score MMAs are done with theirs
@@ -445,26 +426,17 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         return x;
       };
       const int nchunk = 2 * p.R * NCH;
-      if constexpr (!C::K8) {
-        for (int i = ti; i < nchunk; i += nth) {
-          int m, r, ch;
-          const uint4 x = query_chunk(i, m, r, ch);
-          const int row = (C::SHARED ? 2 : 1) * m * TP + r;
-          *reinterpret_cast<uint4*>(smem + C::OFF_Q + (ch >> 3) * (C::QROWS * 128) + swizzled<128>(row, ch & 7)) = x;
-        }
-      } else {
-        for (int i0 = 0; i0 < nchunk; i0 += nth) {  // the rows' largest magnitudes (NCH lanes a row)
-          int m, r, ch;
-          const uint4 x = query_chunk(i0 + ti, m, r, ch);
-          const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-          float amax = 0.f;
+      for (int i0 = 0; i0 < nchunk; i0 += nth) {  // the rows' largest magnitudes (NCH lanes a row)
+        int m, r, ch;
+        const uint4 x = query_chunk(i0 + ti, m, r, ch);
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
+        for (int e = 0; e < 4; ++e)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)), fabsf(__uint_as_float(u[e] & 0xffff0000u))));
 #pragma unroll
-          for (int o = 1; o < NCH; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          if (ch == 0 && i0 + ti < nchunk) qm[32 * m + r] = amax;
-        }
+        for (int o = 1; o < NCH; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (ch == 0 && i0 + ti < nchunk) qm[32 * m + r] = amax;
       }
       if (ti < 32) see[ti] = ti < p.R ? tree_sees(p, w.b, ti % p.T, w.len) : 0ull;
       // columns with a token, and their references
@@ -479,40 +451,38 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
       named_bar_sync(5, nth);
       float rc = p.scale_log2;
       bool alike = true;  // the query rows share one power of two
-      if constexpr (C::K8) {
-        // Every row has its largest magnitude scaled into [128, 256); its two e4m3 terms are then exact
-        // for elements down to 2^-10 of it.  Rows within a factor of eight of the largest take the
-        // largest one's scale (exact down to 2^-7 of their own), which then is a constant of the tile.
-        float big = 0.f, small = INFINITY;
-        if (lane < p.R) {
-          const float x0 = qm[lane], x1 = qm[32 + lane];
-          big = fmaxf(x0, x1);
-          small = fminf(x0 > 0.f ? x0 : INFINITY, x1 > 0.f ? x1 : INFINITY);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-          small = fminf(small, __shfl_xor_sync(0xffffffffu, small, o));
-        }
-        alike = small * 8.f >= big;
-        const int all = e4m3_shift(big);
-        for (int i = ti; i < nchunk; i += nth) {
-          int m, r, ch;
-          const uint4 x = query_chunk(i, m, r, ch);
-          const int sh = alike ? all : e4m3_shift(qm[32 * m + r]);
-          uint2 hi, lo;
-          split_e4m3x8(x, sh, hi, lo);
-          uint8_t* q = smem + C::OFF_Q + 8 * (ch & 1);
-          *reinterpret_cast<uint2*>(q + swizzled<C::KBOXB>((2 * m) * TP + r, ch >> 1)) = hi;
-          *reinterpret_cast<uint2*>(q + swizzled<C::KBOXB>((2 * m + 1) * TP + r, ch >> 1)) = lo;
-          if (ch == 0) qs[32 * m + r] = __int_as_float((127 - sh) << 23);
-        }
-        if (alike) rc *= __int_as_float((127 - all) << 23);
+      // Every row has its largest magnitude scaled into [128, 256); its two e4m3 terms are then exact
+      // for elements down to 2^-10 of it.  Rows within a factor of eight of the largest take the
+      // largest one's scale (exact down to 2^-7 of their own), which then is a constant of the tile.
+      float big = 0.f, small = INFINITY;
+      if (lane < p.R) {
+        const float x0 = qm[lane], x1 = qm[32 + lane];
+        big = fmaxf(x0, x1);
+        small = fminf(x0 > 0.f ? x0 : INFINITY, x1 > 0.f ? x1 : INFINITY);
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        small = fminf(small, __shfl_xor_sync(0xffffffffu, small, o));
+      }
+      alike = small * 8.f >= big;
+      const int all = e4m3_shift(big);
+      for (int i = ti; i < nchunk; i += nth) {
+        int m, r, ch;
+        const uint4 x = query_chunk(i, m, r, ch);
+        const int sh = alike ? all : e4m3_shift(qm[32 * m + r]);
+        uint2 hi, lo;
+        split_e4m3x8(x, sh, hi, lo);
+        uint8_t* q = smem + C::OFF_Q + 8 * (ch & 1);
+        *reinterpret_cast<uint2*>(q + swizzled<C::KROW>((2 * m) * TP + r, ch >> 1)) = hi;
+        *reinterpret_cast<uint2*>(q + swizzled<C::KROW>((2 * m + 1) * TP + r, ch >> 1)) = lo;
+        if (ch == 0) qs[32 * m + r] = __int_as_float((127 - sh) << 23);
+      }
+      if (alike) rc *= __int_as_float((127 - all) << 23);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      if (C::K8) named_bar_sync(5, nth);  // (qs)
+      named_bar_sync(5, nth);  // (qs)
       bool open = named_bar_any(1 + wg, !def);
 
       uint64_t l2[NC / 2];
@@ -525,29 +495,23 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         const int key0 = (w.t + i) * BN, j = key0 + key;
         const bool special = key0 + BN > w.len.L;  // the tile reaches into the drafted keys or past them
         float rk = rc, rk_b = rc, vs = 1.f, lv = 0.f;
-        if constexpr (FMT == kCacheFp8k) {
-          rk *= (map && !V2) ? p.k2_scale : p.k1_scale;
-          rk_b *= V2 ? p.k1_scale : p.k2_scale;
-        }
-        if constexpr (C::V8) {
-          // A value scale that is not finite makes its row NaN: for everybody, or, for a drafted row,
-          // for the tokens that see it (poison, and weightless).  The log2 the reference goes by is at
-          // least 2^-100, so that the sum of weights stays far below fp32's end.
-          rk *= ks_next;
-          rk_b *= V2 ? ks_next : ks2_next;
-          vs = vs_next;
-          lv = fmaxf(__log2f(vs), -100.f);
-          if (!(fabsf(vs) < INFINITY)) {
-            vs = __uint_as_float(0x7fffffffu);
-            lv = -100.f;
-            if (j >= w.len.L) {
-              atomicOr(&poison[k % 3], 1ull << (j - w.len.L));
-              vs = 0.f;
-            }
+        // A value scale that is not finite makes its row NaN: for everybody, or, for a drafted row,
+        // for the tokens that see it (poison, and weightless).  The log2 the reference goes by is at
+        // least 2^-100, so that the sum of weights stays far below fp32's end.
+        rk *= ks_next;
+        rk_b *= V2 ? ks_next : ks2_next;
+        vs = vs_next;
+        lv = fmaxf(__log2f(vs), -100.f);
+        if (!(fabsf(vs) < INFINITY)) {
+          vs = __uint_as_float(0x7fffffffu);
+          lv = -100.f;
+          if (j >= w.len.L) {
+            atomicOr(&poison[k % 3], 1ull << (j - w.len.L));
+            vs = 0.f;
           }
-          vs *= kTreeValueMult;
-          fetch_scales(i + C::NSTREAM);
         }
+        vs *= kTreeValueMult;
+        fetch_scales(i + C::NSTREAM);
         if (!ready) mbar_wait(&s_full[s], (g / C::NBUF) & 1u, ab);
         __syncwarp();
         tc_fence_after();
@@ -556,12 +520,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         float x[NC];
         {
           const uint32_t ts = tl + C::TM_S + s * C::SCOLS;
-          if constexpr (!C::K8) {
-            uint32_t raw[16];
-            tmem_load(ts + map * TP + c0, raw);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) x[c] = __uint_as_float(raw[c]);
-          } else if constexpr (TP == 32) {
+          if constexpr (TP == 32) {
             uint32_t hi[16], lo[16];
             tmem_ld16(ts + map * 2 * TP + c0, hi);
             tmem_ld16(ts + map * 2 * TP + TP + c0, lo);
@@ -581,7 +540,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[s]);
-        if (C::K8 && !alike) {
+        if (!alike) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) x[c] *= qs[32 * map_of(c) + row_of(c)];
         }
@@ -632,7 +591,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < C::NMT * (C::V8 ? 2 : 1); ++q) {  // [128 channels][term]
+            for (int q = 0; q < 2 * C::NMT; ++q) {  // [128 channels][term]
               const uint32_t to = tl + C::TM_O + (stream * C::NMT * C::PCOLS + q * COLS) + map * TP + c0;
               uint32_t o[NC];
               tmem_load(to, o);
@@ -653,28 +612,20 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           l2[c >> 1] = add2(l2[c >> 1], ea);
           l2[(c >> 1) + 1] = add2(l2[(c >> 1) + 1], eb);
           float v0, v1, v2, v3;
-          if constexpr (C::V8) {
-            const uint64_t vs2 = f2pack(vs, vs);
-            f2unpack(mul2(ea, vs2), v0, v1);
-            f2unpack(mul2(eb, vs2), v2, v3);
-            two_e4m3x4(v0, v1, v2, v3, pk[c >> 2], pk[NC / 4 + (c >> 2)]);
-          } else {
-            f2unpack(ea, v0, v1);
-            f2unpack(eb, v2, v3);
-            pk[c >> 1] = pack_bf16x2(v0, v1);
-            pk[(c >> 1) + 1] = pack_bf16x2(v2, v3);
-          }
+          const uint64_t vs2 = f2pack(vs, vs);
+          f2unpack(mul2(ea, vs2), v0, v1);
+          f2unpack(mul2(eb, vs2), v2, v3);
+          two_e4m3x4(v0, v1, v2, v3, pk[c >> 2], pk[NC / 4 + (c >> 2)]);
         }
         if (!pv_over) mbar_wait(&pv_done[stream], (nb - 1) & 1u, ab);  // the P tile's last reader
         __syncwarp();
         any = true;
         {
-          // chunks of 16 bytes of the key's row: e4m3 the columns' hi terms, then all columns' lo terms;
-          // bf16 eight columns each
+          // chunks of 16 bytes of the key's row: the columns' hi terms, then all columns' lo terms
           uint8_t* pt = smem + C::OFF_P + stream * C::P_BYTES;
-          const int ch = (map * TP + c0) * (C::V8 ? 1 : 2) / 16;
+          const int ch = (map * TP + c0) / 16;
           *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch + (C::V8 ? COLS / 16 : 1))) =
+          *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch + COLS / 16)) =
               make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
         if (special) {
@@ -688,7 +639,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
             if (w.len.L - kp >= C::VKEYS) continue;
             mbar_wait(&vfull[fl % NV], (fl / NV) & 1u, ab);
             __syncwarp();
-            clean_values<C::VKEYS, C::VROW, C::V8>(smem + C::OFF_V + (fl % NV) * C::V_SLOT, kp, w.len, &poison[k % 3], si, nst);
+            clean_values<C::VKEYS, C::VROW, true>(smem + C::OFF_V + (fl % NV) * C::V_SLOT, kp, w.len, &poison[k % 3], si, nst);
           }
         }
         fence_proxy_async_smem();
@@ -728,11 +679,9 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           const uint32_t to = tl + C::TM_O + (stream * C::NMT + mt) * C::PCOLS + map * TP + c0;
           uint32_t a[NC], b[NC];
           tmem_load(to, a);
-          if constexpr (C::V8) {
-            tmem_load(to + COLS, b);
+          tmem_load(to + COLS, b);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) a[c] = __float_as_uint(__uint_as_float(a[c]) + __uint_as_float(b[c]));
-          }
+          for (int c = 0; c < NC; ++c) a[c] = __float_as_uint(__uint_as_float(a[c]) + __uint_as_float(b[c]));
 #pragma unroll
           for (int c = 0; c < NC; ++c)
             if (row_of(c) < p.R && here)
@@ -757,11 +706,10 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
   }
 }
 
-template <int D, bool V2, int FMT, int TP>
+template <int D, bool V2, int TP>
 cudaError_t launch_tree_cols(const TreeParams& p, cudaStream_t s) {
-  using C = TreeColsCfg<D, V2, FMT, TP>;
-  return launch_tree_pair<C::DV, V2>(tree_cols_kernel<D, V2, FMT, TP>, C::NTHREADS, C::SMEM_BYTES,
-                                     C::V8 ? 1.f / 128.f : 1.f, p, s);
+  using C = TreeColsCfg<D, V2, TP>;
+  return launch_tree_pair<C::DV, V2>(tree_cols_kernel<D, V2, TP>, C::NTHREADS, C::SMEM_BYTES, 1.f / 128.f, p, s);
 }
 
 }  // namespace da

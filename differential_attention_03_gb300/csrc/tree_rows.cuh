@@ -19,7 +19,7 @@
 // each key and value byte is read once.  The half of the score MMAs that
 // multiplies zeros is free, as HBM bounds the kernel: 128 keys of bf16 V1 at
 // d = 128 are 128 KB, 5600 cycles of this SM's share of HBM, against 3072
-// cycles of MMA.
+// cycles of MMA (1024 of scores, 2048 of both terms of P).
 //
 // Formats.  bf16; FP8K: e4m3 keys with one scale a tensor, bf16 values; FP8:
 // e4m3 keys and values with an fp32 scale a row.  8-bit operands are not
@@ -45,11 +45,12 @@
 // (quarters without rows sleep).  TMEM: O, then two score tiles, in which P
 // replaces the scores.
 //
-// Rounding.  Weights are rounded to bf16 (FP8: two e4m3 terms, about as near)
-// before they meet the values, as in the forward and the one-token decode: half
-// a step of 2^-8 each, at random, which is 1.8e-3 of an output over 8192 random
-// keys beside the 1.7e-3 of rounding the output itself.  Scores, maxima, sums
-// and O stay fp32.
+// Rounding.  Weights meet the values as two terms, bf16 or e4m3 as the values
+// are: hi + lo holds 16 bits of a weight with bf16 values, 8 with e4m3 ones
+// (whose own rounding is far coarser).  With hi alone, bf16 outputs over 8192
+// random keys were 2.5e-3 off the formula instead of 1.7e-3, which rounding the
+// output itself is; the second term costs 0 to 5 % of a bf16 call's time.
+// Scores, maxima, sums and O stay fp32.
 //
 // Measured (this kernel alone): bf16 V1 d128 B4 H12 T16 n8192 71 us (403 MB, 5.7
 // TB/s; about 10 us of it are the way in and the last states' stores), V2 d128
@@ -81,8 +82,7 @@ struct TreeRowsCfg {
   static constexpr int KBOX = KROW / KBOXB;
   static constexpr int VROW = DV * (V8 ? 1 : 2);
   static constexpr int VBOX = VROW / 128;
-  static constexpr int VKEYS = 64;  // keys of a value slot
-  static constexpr int VBOXK = tree_value_keys(DV, V8);  // keys of a value box
+  static constexpr int VKEYS = kTreeValueKeys;  // of a value slot
   static constexpr int K_SLOT = BN * KROW, V_SLOT = VKEYS * VROW;
   static constexpr int QROWS = V2 ? 128 : 192;          // Q_even | Q_odd, or Q_1 | zeros | Q_2
   static constexpr int Q_TERM = QROWS * KROW;
@@ -101,9 +101,9 @@ struct TreeRowsCfg {
   static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NS + 2 + 2 + 2 + 2 + 1 + 2;
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 256 + 1024;
-  // Tensor memory: O, two score tiles, and, where O leaves the room (DV = 128), two P tiles of 64
-  // columns; else P takes the place of its scores.
-  static constexpr bool PSEP = DV == 128;
+  // Tensor memory: O, two score tiles, and, where O leaves the room and P is e4m3 (DV = 128), two P
+  // tiles of 64 columns; else P takes the place of its scores.  P: hi terms, then lo terms.
+  static constexpr bool PSEP = DV == 128 && V8;
   static constexpr uint32_t TM_O = 0, TM_S = DV;
   static constexpr uint32_t TM_P = PSEP ? TM_S + 2 * BN : TM_S, P_STEP = PSEP ? 64 : BN;
   static constexpr uint32_t TMEM_COLS = 512;
@@ -134,12 +134,8 @@ __device__ __forceinline__ void mma_ts_f8_elect(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  if (!DA_TMEM_OK(taddr, 4)) return;
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
-
+// WIDE: more than 32 rows a map.  Else each row stands twice, once for either half of a tile's keys, and
+// the two are partial states of their own: half the keys a softmax thread, and no row idles.
 template <int D, bool V2, int FMT, bool WIDE>
 __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeRowsCfg<D, V2, FMT>;
@@ -243,9 +239,8 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
           uint8_t* dst = smem + C::OFF_V + s * C::V_SLOT;
           if (DA_BOUNDS_V(b < p.B && h < p.H, key0))  // (a box past n reads zeros)
             for (int bx = 0; bx < C::VBOX; ++bx)
-              for (int r = 0; r < C::VKEYS / C::VBOXK; ++r)
-                tma_load_4d(dst + bx * C::VKEYS * 128 + r * C::VBOXK * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
-                            key0 + part * C::VKEYS + r * C::VBOXK, b);
+              tma_load_4d(dst + bx * C::VKEYS * 128, &p.tm_v, &vfull[s], bx * (C::V8 ? 128 : 64), h,
+                          key0 + part * C::VKEYS, b);
         }
         return true;
       };
@@ -347,6 +342,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
                 mma_ts_f8_elect(tm + C::TM_O, col + 32u, b, C::IDESC_PV, 1u);
               } else {
                 mma_ts_elect(tm + C::TM_O, col, b, C::IDESC_PV, acc);
+                mma_ts_elect(tm + C::TM_O, col + 64u, b, C::IDESC_PV, 1u);
               }
             }
             tc_commit_elect(&vempty[slot]);
@@ -440,20 +436,6 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
       const int pr = r / p.T, tok = r - pr * p.T;
       const int ti = threadIdx.x - 128;                        // index among the softmax threads
       constexpr int nth = NACT * 32;
-      if constexpr (C::PSEP && !WIDE) {  // the other half's keys: weights of zero, for good
-#pragma unroll
-        for (uint32_t s = 0; s < 2; ++s) {
-          const uint32_t tz = tl + C::TM_P + s * C::P_STEP;
-          if constexpr (C::V8) {
-            tmem_st4(tz + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
-            tmem_st4(tz + 32u + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
-          } else {
-            const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            tmem_st8(tz + 32u * (sub ^ 1) + 8u * qd, zero);
-          }
-        }
-        tmem_st_wait();
-      }
       float* xm = reinterpret_cast<float*>(smem + C::OFF_XM);
       float* qi = reinterpret_cast<float*>(smem + C::OFF_QI);
       const float top = C::V8 ? kTreeRescale8Log2 : kTreeRescaleLog2;
@@ -646,40 +628,28 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
               __syncwarp();
               tc_fence_after();
             }
-            if constexpr (WIDE) {
-              tmem_st8(tP + 8u * qd, hi);
-              tmem_st8(tP + 32u + 8u * qd, lo8);
-            } else {
-              tmem_st4(tP + 16u * sub + 4u * qd, hi[0], hi[1], hi[2], hi[3]);
-              tmem_st4(tP + 32u + 16u * sub + 4u * qd, lo8[0], lo8[1], lo8[2], lo8[3]);
-              if constexpr (!C::PSEP) {
-                tmem_st4(tP + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
-                tmem_st4(tP + 32u + 16u * (sub ^ 1) + 4u * qd, 0, 0, 0, 0);
-              }
-            }
+            tmem_st8(tP + 8u * qd, hi);
+            tmem_st8(tP + 32u + 8u * qd, lo8);
           } else {
-            uint32_t pk[NC / 2];
+            uint32_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
             for (int c = 0; c < NC; c += 2) {
               float a0, a1;
               f2unpack(fma2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rc2, nb2), a0, a1);
               const float p0 = ex2(a0), p1 = ex2(a1);
               acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], f2pack(p0, p1));
-              pk[c >> 1] = pack_bf16x2(p0, p1);
-            }
-            if (C::PSEP && g >= 2) {
-              mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
-              __syncwarp();
-              tc_fence_after();
+              hi[c >> 1] = pack_bf16x2(p0, p1);
+              lo[c >> 1] = pack_bf16x2(p0 - __uint_as_float(hi[c >> 1] << 16), p1 - __uint_as_float(hi[c >> 1] & 0xffff0000u));
             }
             if constexpr (WIDE) {
-              tmem_st16(tP + 16u * qd, pk);
+              tmem_st16(tP + 16u * qd, hi);
+              tmem_st16(tP + 64u + 16u * qd, lo);
             } else {
-              tmem_st8(tP + 32u * sub + 8u * qd, pk);
-              if constexpr (!C::PSEP) {
-                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                tmem_st8(tP + 32u * (sub ^ 1) + 8u * qd, zero);
-              }
+              const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+              tmem_st8(tP + 32u * sub + 8u * qd, hi);
+              tmem_st8(tP + 64u + 32u * sub + 8u * qd, lo);
+              tmem_st8(tP + 32u * (sub ^ 1) + 8u * qd, zero);
+              tmem_st8(tP + 64u + 32u * (sub ^ 1) + 8u * qd, zero);
             }
           }
           {
@@ -765,8 +735,11 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
 template <int D, bool V2, int FMT>
 cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t s) {
   using C = TreeRowsCfg<D, V2, FMT>;
-  return launch_tree_pair<C::DV, V2>(p.R > 32 ? tree_rows_kernel<D, V2, FMT, true> : tree_rows_kernel<D, V2, FMT, false>,
-                                     C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / 128.f : 1.f, p, s);
+  void (*kern)(TreeParams) = tree_rows_kernel<D, V2, FMT, true>;
+  if constexpr (!C::V8) {  // (e4m3 values: more than 32 rows only, see launch_tree)
+    if (p.R <= 32) kern = tree_rows_kernel<D, V2, FMT, false>;
+  }
+  return launch_tree_pair<C::DV, V2>(kern, C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / 128.f : 1.f, p, s);
 }
 
 }  // namespace da
