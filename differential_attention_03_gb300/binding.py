@@ -1145,6 +1145,14 @@ def _tree_args(lens, ntok, mask, B, T, dev):
     return _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(mask), sb
 
 
+def _tree_workspace(workspace, need, dev, like):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError(f"workspace must be contiguous and on device {dev}")
+    return workspace
+
+
 def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=None, eps: float = 1e-5, lens=None,
                 ntok=None, mask=None, out=None, workspace=None, stream=None) -> torch.Tensor:
     """DIFF V1 attention of T <= 64 drafted tokens a sequence over a cache that already holds their keys and values.
@@ -1171,9 +1179,7 @@ def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=Non
         out = torch.empty((B, T, H, 2 * d), device=q1.device, dtype=bf)
     _on(out, "out", bf, (B, T, H, 2 * d), dev)
     need = tree_decode_workspace_bytes(B, T, H, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q1.device)
-    wp, wn = _ws_args(workspace, need)
+    wp, wn = _ws_args(_tree_workspace(workspace, need, dev, q1), need)
     _check(lib().diffattn_tree_decode(
         cache.code, B, T, H, cache.n, d, q1.data_ptr(), q2.data_ptr(), cache.k1.data_ptr(), cache.k2.data_ptr(),
         cache.k1_scale, cache.k2_scale, _addr(cache.k1_scales), _addr(cache.k2_scales), cache.v.data_ptr(),
@@ -1202,9 +1208,7 @@ def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=Non
         out = torch.empty((B, T, G, d), device=q.device, dtype=bf)
     _on(out, "out", bf, (B, T, G, d), dev)
     need = v2_tree_decode_workspace_bytes(B, T, Hq, cache.H, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    wp, wn = _ws_args(workspace, need)
+    wp, wn = _ws_args(_tree_workspace(workspace, need, dev, q), need)
     _check(lib().diffattn_v2_tree_decode(
         cache.code, B, T, Hq, cache.H, cache.n, d, q.data_ptr(), cache.k1.data_ptr(), cache.k1_scale,
         _addr(cache.k1_scales), cache.v.data_ptr(), _addr(cache.v_scales), *a, lam_logits.data_ptr(), sb, st,

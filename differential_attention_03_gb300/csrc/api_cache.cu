@@ -137,16 +137,41 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
   const float* ksc[2] = {kscales[0], kscales[1]};
   diffattn_status st = check_scales(fn, fmt, nk, n, ks, ksc, vscales);
   if (st != DIFFATTN_OK) return st;
-  const size_t qbytes = static_cast<size_t>(B) * T * Hq * d * 2;
-  for (int i = 0; i < nk; ++i) {
+  for (int i = 0; i < nk; ++i)
     if (!aligned(k[i], 16) || !aligned(kc[i], 16) || (hasq && (!aligned(q[i], 16) || !aligned(qo[i], 16))))
       return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
-    if (hasq)
-      for (int j = 0; j < nk; ++j)
-        if (overlap(q[i], qbytes, qo[j], qbytes))
-          return fail(DIFFATTN_ERR_SHAPE, "%s: the rotated queries may not overlap the queries", fn);
-  }
   if (!aligned(v, 16) || !aligned(vc, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  {
+    // what is written may not overlap anything else of the call: every row is read and written by its own threads
+    struct Span {
+      const void* at;
+      size_t bytes;
+    } w[8], r[5];
+    int nw = 0, nr = 0;
+    const size_t tok = static_cast<size_t>(B) * T, rows = static_cast<size_t>(B) * n * H;
+    const size_t kes = fmt == DIFFATTN_CACHE_BF16 ? 2 : 1, ves = fmt == DIFFATTN_CACHE_FP8 ? 1 : 2;
+    for (int i = 0; i < nk; ++i) {
+      r[nr++] = {k[i], tok * H * d * 2};
+      w[nw++] = {kc[i], rows * d * kes};
+      if (fmt == DIFFATTN_CACHE_FP8) w[nw++] = {kscales[i], rows * 4};
+      if (hasq) {
+        r[nr++] = {q[i], tok * Hq * d * 2};
+        w[nw++] = {qo[i], tok * Hq * d * 2};
+      }
+    }
+    r[nr++] = {v, tok * H * dv * 2};
+    w[nw++] = {vc, rows * dv * ves};
+    if (fmt == DIFFATTN_CACHE_FP8) w[nw++] = {vscales, rows * 4};
+    for (int i = 0; i < nw; ++i) {
+      if (w[i].bytes == 0) continue;
+      for (int j = 0; j < nr; ++j)
+        if (r[j].bytes && overlap(w[i].at, w[i].bytes, r[j].at, r[j].bytes))
+          return fail(DIFFATTN_ERR_SHAPE, "%s: an output or the cache overlaps an input", fn);
+      for (int j = 0; j < i; ++j)
+        if (w[j].bytes && overlap(w[i].at, w[i].bytes, w[j].at, w[j].bytes))
+          return fail(DIFFATTN_ERR_SHAPE, "%s: outputs or cache tensors overlap", fn);
+    }
+  }
   da::AppendParams p;
   memset(&p, 0, sizeof(p));
   if ((st = rope_turns(fn, rope, d, &p.rope)) != DIFFATTN_OK) return st;
@@ -227,6 +252,9 @@ diffattn_status keep(const char* fn, diffattn_cache_format fmt, int B, int A, in
     if (rb > 0x3fffffffll) return fail(DIFFATTN_ERR_SHAPE, "%s: too many heads", fn);
     p.row_bytes[i] = static_cast<int>(rb);
     if (!aligned(p.base[i], 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+    for (int j = 0; n > 0 && j < i; ++j)  // (each moves by itself)
+      if (overlap(p.base[i], static_cast<size_t>(B) * n * p.row_bytes[i], p.base[j], static_cast<size_t>(B) * n * p.row_bytes[j]))
+        return fail(DIFFATTN_ERR_SHAPE, "%s: cache tensors overlap", fn);
   }
   p.B = B;
   p.A = A;
@@ -290,7 +318,7 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   if (!aligned(mask, 8)) return fail(DIFFATTN_ERR_ALIGN, "%s: mask words must be 8-byte aligned", fn);
   const TreeShape sh = tree_shape(B, T, H, pairs);
   const long long tiles = sh.units * ((static_cast<long long>(n) + 127) / 128);
-  if (sh.units * 16 > 0x7fffffffll || tiles > 0x7fffffffll)
+  if (sh.units * sh.R > 0x7fffffffll || tiles > 0x7fffffffll)
     return fail(DIFFATTN_ERR_SHAPE, "%s: too many (sequence, head) pairs or keys", fn);
   if (!workspace) return fail(DIFFATTN_ERR_NULL, "%s: NULL workspace", fn);
   const size_t need = tree_workspace(B, T, H, pairs, dv);

@@ -664,7 +664,8 @@ typedef enum {
  * into q1_out, q2_out: a decode step's or a prefill's work between the
  * projections and the attention, in one kernel.
  *   q1, q2    : bf16 [B, T, H, d], or both NULL (no queries); q1_out, q2_out
- *               the same shape, not overlapping q1 or q2 (ERR_SHAPE).
+ *               the same shape.  Nothing written (queries, cache, row scales)
+ *               may overlap anything else of the call (ERR_SHAPE).
  *   k1, k2, v : bf16 [B, T, H, d], [B, T, H, 2d]; d in {64, 128}.
  *   positions : device int32 [B, T] (e.g. the depths in a draft tree), or
  *               NULL: the cache row.
@@ -751,7 +752,8 @@ diffattn_status diffattn_v2_tree_decode(diffattn_cache_format fmt, int B, int T,
  *   lens     : device int32 [B], required.
  *   new_lens : device int32 [B] or NULL, receives lens[b] plus the nodes kept;
  *              may not overlap lens (ERR_SHAPE).
- * Other rows are left as they are.  Asynchronous on `stream`.
+ * Other rows are left as they are; cache tensors that overlap -> ERR_SHAPE.
+ * Asynchronous on `stream`.
  */
 diffattn_status diffattn_cache_keep(diffattn_cache_format fmt, int B, int A, int H, int n, int d, void* k1_cache,
                                     void* k2_cache, void* v_cache, float* k1_scales, float* k2_scales,

@@ -172,6 +172,30 @@ def test_append_refusals(L):
     assert v2(q=A2) == da.ERR_SHAPE
 
 
+def test_append_refuses_overlaps(L):
+    # distinct tensors of 64 KB each but for one: what is written meets an input, or another output
+    at = [P(0x100000 * (i + 1)) for i in range(13)]
+    full = dict(fmt=2, q=(at[0], at[1]), k=(at[2], at[3]), v=at[4], qo=(at[5], at[6]), kc=(at[7], at[8]), vc=at[9],
+                sc=(at[10], at[11], at[12]))
+
+    def with_(**kw):
+        status = _append(L, **{**full, **kw})
+        return status, L.diffattn_last_error()
+    for kw in (dict(qo=(at[0], at[6])), dict(qo=(at[5], at[0])), dict(qo=(at[2], at[6])), dict(qo=(at[5], at[5])),
+               dict(qo=(at[7], at[6])), dict(kc=(at[2], at[8])), dict(kc=(at[7], at[7])), dict(kc=(at[7], at[4])),
+               dict(vc=at[4]), dict(vc=at[8]), dict(sc=(at[10], at[10], at[12])), dict(sc=(at[10], at[11], at[9])),
+               dict(vc=P(at[4].value + 16)), dict(sc=(at[3], at[11], at[12]))):
+        status, why = with_(**kw)
+        assert status == da.ERR_SHAPE and b"overlap" in why, kw
+
+
+def test_keep_refuses_overlaps(L):
+    a, b = P(0x100000), P(0x200000)
+    for tensors in ((a, a, b), (a, b, a), (a, b, P(0x200000 + 512))):
+        assert L.diffattn_cache_keep(0, 1, 2, 1, 8, 64, *tensors, None, None, None, A, A2, A3, None, None) == da.ERR_SHAPE
+        assert b"overlap" in L.diffattn_last_error()
+
+
 def _tree(L, fmt=0, B=1, T=2, H=1, n=8, d=64, q=(A, A), k=(A, A), v=A, ks=(1.0, 1.0), sc=(A, A, A), mask=None, sb=0,
           lam=A, lin=0.2, out=A, ws=A, wn=1 << 30):
     f = ctypes.c_float

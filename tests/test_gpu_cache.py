@@ -6,8 +6,8 @@ Bars (derived from the formats; a rounding is off by at most finfo(t).eps / 2 re
     and the output's own rounding;
   * 8-bit rows: half an e4m3 step of the scaled value (2^-4 relative, 2^-10 absolute), plus the
     rotary error before it; scales 2^-22 relative on top of the rotary error;
-  * attention: the weights are rounded to bf16 (2^-8 relative; two e4m3 terms: 2^-4 2^-4 = 2^-8, and
-    2^-10 absolute where the largest contribution is at least 2^7, 2^-17 of it a key), and 2^-10 more for
+  * attention: the weights stand in two terms (e4m3: 2^-4 2^-4 = 2^-8 relative, and 2^-10 absolute where
+    the largest contribution is at least 2^7, 2^-17 of it a key; bf16: 2^-16, under the same bar), and 2^-10 more for
     the two-term query, exp2 and the fp32 sums: E = (2^-8 + 2^-10) sum_j p_j |v_j| (+ 2^-17 n max_j
     p_j |v_j|) on a map's output; the norm multiplies it by its gain and adds the change of the row's
     rms; the output rounds to bf16.
@@ -673,6 +673,64 @@ def test_chain_of_drafts_equals_the_causal_forward():
     assert torch.equal(qa, cut(q1, 60, n)) and torch.equal(qb, cut(q2, 60, n))
     a, b = _np(out), _np(ref)[:, 60:]
     assert np.abs(a - b).max() <= 2e-2 * max(1.0, np.abs(b).max())
+
+
+def test_bf16_weights_lose_nothing():
+    # 8000 alike keys: the output is off by its own rounding (uniform, at most 2^-8 of the value's power of
+    # two: 2^-8 / sqrt 3, over 1.44 rms: 1.6e-3 of the norm); weights in one bf16 term alone would make it 2.4e-3.
+    B, T, H, d, n = 1, 4, 2, 64, 8000
+    g = _gen(5)
+    c, keys, val = _random_cache(g, B, n, H, d, True, "bf16")
+    q1, q2 = _bf(g, B, T, H, d), _bf(g, B, T, H, d)
+    out = da.tree_decode(q1, q2, c, torch.tensor([0.4], device="cuda"), 0.3)
+    da.device_status()
+    ref = oracle.tree_v1(q1.cpu(), q2.cpu(), *keys, val, [n - T], [T], None, float(np.float32(0.4)), 0.3, np.ones(2 * d),
+                         1e-5)[0]
+    assert np.linalg.norm(_np(out) - ref) <= 2.0e-3 * np.linalg.norm(ref)
+
+
+def test_offsets_past_32_bits():
+    # Caches of 2^32 and more values, e4m3: rows near their end are written, found, and moved.
+    n, H, d, T = 2 ** 21 + 5000, 16, 128, 4
+    g = _gen(21)
+    c = da.cache_v2(1, n, H, d, "fp8")
+    L = n - 40
+    k, v = _bf(g, 1, T, H, d), _bf(g, 1, T, H, d)
+    da.v2_cache_append(c, k, v, lens=_i32([L - T]))          # committed rows, far in
+    da.v2_cache_append(c, _bf(g, 1, 8, H, d), v.repeat(1, 2, 1, 1), lens=_i32([L]))
+    da.device_status()
+    for t, s, x in ((c.k1, c.k1_scales, k), (c.v, c.v_scales, v)):
+        codes, scale = oracle.quantise_rows(x.cpu())
+        back = _np(t[:, L - T:L]) * _np(s[:, :, L - T:L]).transpose(0, 2, 1)[..., None]
+        assert np.abs(back - _np(x)).max() <= (2.0 ** -4 + 2.0 ** -10) * np.abs(_np(x)).max()
+    assert not c.k1[0, :L - T].view(torch.uint8).any() and not c.v[0, L + 8:].view(torch.uint8).any()
+    # a query along one far key (every other key but the drafts' is zero): its value is the output
+    q = (4 * k[:, 1:2].float().repeat_interleave(2, 2)).to(torch.bfloat16)
+    logits = torch.zeros(H, device="cuda")
+    out = da.v2_tree_decode(q, c, logits, lens=_i32([L]), ntok=_i32([1]), mask=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    da.device_status()
+    ref = 0.5 * _np(c.v[:, L - T + 1:L - T + 2]) * _np(c.v_scales[:, :, L - T + 1:L - T + 2]).transpose(0, 2, 1)[..., None]
+    # (q.k / sqrt d is 4 |k|^2 / 11.3, some 45 of e: what 2^21 zero keys and three others weigh is below 2^-30)
+    assert np.abs(_np(out) - ref).max() <= 2.0 ** -6 * np.abs(ref).max()
+    rows = c.k1[0, [L + 1, L + 3, L + 7]].view(torch.uint8).clone(), c.v_scales[0, :, [L + 1, L + 3, L + 7]].clone()
+    new = da.cache_keep(c, _i32([L]), _i32([[1, 3, 7]]), _i32([3]))
+    da.device_status()
+    assert new.tolist() == [L + 3]
+    assert torch.equal(c.k1[0, L:L + 3].view(torch.uint8), rows[0]) and torch.equal(c.v_scales[0, :, L:L + 3], rows[1])
+
+
+def test_rope_past_32_bits():
+    n, H, d = 2 ** 21 + 777, 16, 128
+    x = torch.zeros((1, n, H, d), device="cuda", dtype=torch.bfloat16)
+    x[:, -3:] = _bf(_gen(4), 1, 3, H, d)
+    last = x[:, -3:].clone()
+    th, m = oracle.rope_frequencies(d)
+    da.rope([x], da.rope_spec(d), out=[x])
+    da.device_status()
+    ref = oracle.rope(last.cpu(), np.arange(n - 3, n)[None], th, m)
+    bound = 8 * 2.0 ** -24 * _pair_sum(_np(last), d, False) + 2.0 ** -20 * _pair_sum(_np(last), d, False)
+    _close(x[:, -3:], ref, bound + 2.0 ** -8 * (np.abs(ref) + bound), "rope")
+    assert not x[:, :-3].any()
 
 
 def test_step_replays_in_a_graph_and_on_two_streams():
