@@ -53,8 +53,8 @@
 // the columns of a map.
 //
 // Measured (this kernel alone, one token): V1 d64 B8 H16 n32768 176 us (1.12
-// GB with the scales, 6.4 TB/s); 32 tokens V1 d128 B8 H8 n32768 203 us with
-// the merge (5.4 TB/s), V1 d64 B8 H16 284 us (3.9 TB/s), where the softmax
+// GB with the scales, 6.4 TB/s); 32 tokens V1 d128 B8 H8 n32768 193 us with
+// the merge (5.6 TB/s), V1 d64 B8 H16 256 us (4.2 TB/s), where the softmax
 // warps bound it.
 #pragma once
 
@@ -565,6 +565,8 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
             pm = fmaxf(pm, x[c]);
           }
         }
+        float f = 1.f;     // what the reference of this lane's column rises by, as a factor on its O^T,
+        bool fix = false;  // if there is some
         if (named_bar_any(1 + wg, open || pm + lv > top)) {
           // ---- new references: column maxima over the tile's keys
           float y[NC];
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           const float cm = fmaxf(fmaxf(xm[own], xm[16 + own]), fmaxf(xm[32 + own], xm[48 + own]));
           float up = 0.f;  // how much the reference rises
           if (live && cm > -INFINITY && (!def || cm > 0.f)) up = cm;
-          const float f = def ? ex2(-up) : 1.f;  // (before the first reference there is nothing to scale)
+          f = def ? ex2(-up) : 1.f;  // (before the first reference there is nothing to scale)
           ref += up;
           def = def || cm > -INFINITY;
           if (wq == 0 && lane < NC && live) ac[own] = -ref;
@@ -586,22 +588,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
             x[c + 1] -= __shfl_sync(0xffffffffu, up, c + 1);
             l2[c >> 1] = mul2(l2[c >> 1], f2pack(__shfl_sync(0xffffffffu, f, c), __shfl_sync(0xffffffffu, f, c + 1)));
           }
-          if (any) {
-            mbar_wait(&pv_done[stream], (nb - 1) & 1u, ab);
-            __syncwarp();
-            tc_fence_after();
-#pragma unroll 1
-            for (int q = 0; q < 2 * C::NMT; ++q) {  // [128 channels][term]
-              const uint32_t to = tl + C::TM_O + (stream * C::NMT * C::PCOLS + q * COLS) + map * TP + c0;
-              uint32_t o[NC];
-              tmem_load(to, o);
-#pragma unroll
-              for (int c = 0; c < NC; ++c)
-                o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, f, c));
-              tmem_st16(to, o);
-            }
-            tmem_st_wait();
-          }
+          fix = any;
           open = named_bar_any(1 + wg, !def);  // (and the references are in place)
         }
         // ---- weights
@@ -627,6 +614,19 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch + COLS / 16)) =
               make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        }
+        if (fix) {  // (last of all, when the previous P V is over: V1 d64 B8 H16, 32 tokens, 286 us and 267 this way)
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 2 * C::NMT; ++q) {  // [128 channels][term]
+            const uint32_t to = tl + C::TM_O + (stream * C::NMT * C::PCOLS + q * COLS) + map * TP + c0;
+            uint32_t o[NC];
+            tmem_load(to, o);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * __shfl_sync(0xffffffffu, f, c));
+            tmem_st16(to, o);
+          }
+          tmem_st_wait();
         }
         if (special) {
           // (the previous tile's P V first: the slots' earlier fills are then all used, so that the

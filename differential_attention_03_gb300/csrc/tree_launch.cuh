@@ -7,11 +7,11 @@
 namespace da {
 
 // Row scales make keys as rows the faster one for as many rows (tokens times
-// pairs) of a map as it takes: fp8, n32768, one token: V1 d64 B8 H16 188 us
-// against 286, V1 d128 B8 H8 192 against 222; 32 tokens: 284 against 325, 203
-// against 244.  Without them HBM bounds both, and tokens as rows, with deeper
-// rings, comes nearer to it (bf16, one token: V1 d64 323 against 336, V1 d128
-// 312 against 320).
+// pairs) of a map as it takes: fp8, n32768, when both took them, one token: V1
+// d64 B8 H16 188 us against 286, V1 d128 B8 H8 192 against 222; 32 tokens: 284
+// against 325, 203 against 244 (256 and 193 by now).  Without them HBM bounds
+// both, and tokens as rows, with deeper rings, comes nearer to it (bf16, one
+// token: V1 d64 323 against 336, V1 d128 312 against 320).
 template <int D, bool V2, int FMT>
 cudaError_t launch_tree(TreeParams p, cudaStream_t s) {
   if constexpr (FMT == kCacheFp8) {
