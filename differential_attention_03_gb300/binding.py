@@ -916,6 +916,18 @@ _PTRS = [ctypes.c_void_p * k for k in range(5)]
 _INTS = [ctypes.c_int * k for k in range(5)]
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a kernel on `stream`: memory of that stream's own, as under torch.cuda.stream(stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(x, stream):
+    return torch.empty_like(x) if stream is None else _empty(x.shape, x.dtype, x.device, stream)
+
+
 def rope(tensors, spec: RopeSpec, positions=None, inverse: bool = False, out=None, stream=None) -> list:
     """Rotary positions on up to four tensors [B, n, heads, d] (bf16 or fp32, d <= 128) in one kernel.
 
@@ -937,7 +949,7 @@ def rope(tensors, spec: RopeSpec, positions=None, inverse: bool = False, out=Non
     if positions is not None:
         _on(positions, "positions", torch.int32, (B, n), dev)
     if out is None:
-        out = [torch.empty_like(x) for x in xs]
+        out = [_like(x, stream) for x in xs]
     else:
         out = list(out)
         if len(out) != len(xs):
@@ -1059,8 +1071,8 @@ def cache_append(cache: KVCache, k1, k2, v, q1=None, q2=None, rope=None, positio
     if q1 is not None:
         _on(q1, "q1", bf, shp, dev)
         _on(q2, "q2", bf, shp, dev)
-        q1_out = torch.empty_like(q1) if q1_out is None else q1_out
-        q2_out = torch.empty_like(q2) if q2_out is None else q2_out
+        q1_out = _like(q1, stream) if q1_out is None else q1_out
+        q2_out = _like(q2, stream) if q2_out is None else q2_out
         _on(q1_out, "q1_out", bf, shp, dev)
         _on(q2_out, "q2_out", bf, shp, dev)
     _check(lib().diffattn_cache_append(
@@ -1086,7 +1098,7 @@ def v2_cache_append(cache: KVCache, k, v, q=None, rope=None, positions=None, len
     if q is not None:
         Hq = q.shape[2]
         _on(q, "q", bf, (B, T, Hq, d), dev)
-        q_out = torch.empty_like(q) if q_out is None else q_out
+        q_out = _like(q, stream) if q_out is None else q_out
         _on(q_out, "q_out", bf, (B, T, Hq, d), dev)
     _check(lib().diffattn_v2_cache_append(
         cache.code, B, T, Hq, H, cache.n, d, _addr(q), k.data_ptr(), v.data_ptr(),
@@ -1109,7 +1121,7 @@ def cache_keep(cache: KVCache, lens, path, nkeep, new_lens=None, stream=None) ->
         raise ValueError(f"path must be [B, A], got {tuple(path.shape)}")
     A = path.shape[1]
     if new_lens is None:
-        new_lens = torch.empty_like(lens)
+        new_lens = _like(lens, stream)
     a = (_int32(lens, "lens", (B,), dev), _int32(path, "path", (B, A), dev), _int32(nkeep, "nkeep", (B,), dev),
          _int32(new_lens, "new_lens", (B,), dev), _stream(stream))
     if cache.k2 is not None:
@@ -1145,9 +1157,9 @@ def _tree_args(lens, ntok, mask, B, T, dev):
     return _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(mask), sb
 
 
-def _tree_workspace(workspace, need, dev, like):
+def _tree_workspace(workspace, need, dev, like, stream):
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+        return _empty((max(need, 16),), torch.uint8, like.device, stream)
     if not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError(f"workspace must be contiguous and on device {dev}")
     return workspace
@@ -1176,10 +1188,11 @@ def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=Non
         _on(gamma, "gamma", torch.float32, (2 * d,), dev)
     a = _tree_args(lens, ntok, mask, B, T, dev)
     if out is None:
-        out = torch.empty((B, T, H, 2 * d), device=q1.device, dtype=bf)
+        out = _empty((B, T, H, 2 * d), bf, q1.device, stream)
     _on(out, "out", bf, (B, T, H, 2 * d), dev)
     need = tree_decode_workspace_bytes(B, T, H, d)
-    wp, wn = _ws_args(_tree_workspace(workspace, need, dev, q1), need)
+    workspace = _tree_workspace(workspace, need, dev, q1, stream)  # (alive until the kernels are in their stream)
+    wp, wn = _ws_args(workspace, need)
     _check(lib().diffattn_tree_decode(
         cache.code, B, T, H, cache.n, d, q1.data_ptr(), q2.data_ptr(), cache.k1.data_ptr(), cache.k2.data_ptr(),
         cache.k1_scale, cache.k2_scale, _addr(cache.k1_scales), _addr(cache.k2_scales), cache.v.data_ptr(),
@@ -1205,10 +1218,11 @@ def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=Non
         if 1 <= lam_logits.dim() <= 3 else (B, T, G), dev)
     a = _tree_args(lens, ntok, mask, B, T, dev)
     if out is None:
-        out = torch.empty((B, T, G, d), device=q.device, dtype=bf)
+        out = _empty((B, T, G, d), bf, q.device, stream)
     _on(out, "out", bf, (B, T, G, d), dev)
     need = v2_tree_decode_workspace_bytes(B, T, Hq, cache.H, d)
-    wp, wn = _ws_args(_tree_workspace(workspace, need, dev, q), need)
+    workspace = _tree_workspace(workspace, need, dev, q, stream)
+    wp, wn = _ws_args(workspace, need)
     _check(lib().diffattn_v2_tree_decode(
         cache.code, B, T, Hq, cache.H, cache.n, d, q.data_ptr(), cache.k1.data_ptr(), cache.k1_scale,
         _addr(cache.k1_scales), cache.v.data_ptr(), _addr(cache.v_scales), *a, lam_logits.data_ptr(), sb, st,

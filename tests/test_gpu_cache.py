@@ -733,6 +733,32 @@ def test_rope_past_32_bits():
     assert not x[:, :-3].any()
 
 
+def test_tree_on_a_stream_of_its_own_keeps_its_memory():
+    # What the call allocates for another stream is that stream's: neither a block that the current stream
+    # still writes, nor, freed on return, one that it may write next while the other still computes.
+    B, T, H, d, n = 1, 8, 8, 64, 200000
+    g = _gen(8)
+    c = da.cache_v1(B, n, H, d)
+    for t in (c.k1, c.k2, c.v):
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+    q1, q2, lam = _bf(g, B, T, H, d), _bf(g, B, T, H, d), torch.tensor([0.4], device="cuda")
+    ref = da.tree_decode(q1, q2, c, lam, 0.3)
+    need = da.tree_decode_workspace_bytes(B, T, H, d)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a, b = torch.empty_like(ref), torch.empty(need, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(2000000)
+        a.fill_(float("nan"))
+        b.fill_(255)
+        del a, b
+        out = da.tree_decode(q1, q2, c, lam, 0.3, stream=s)
+        torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    da.device_status()
+
+
 def test_step_replays_in_a_graph_and_on_two_streams():
     # One speculative step captured and replayed on new inputs: the eager call's bits; and two such
     # steps at once on two streams, with caches of their own.
