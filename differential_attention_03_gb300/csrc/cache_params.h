@@ -101,7 +101,7 @@ constexpr int kTreeValueKeys = 64;  // keys of a value box of the tree decode, a
 
 constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree decode
 
-// Subsets of a CTA's keys that keep their own partial state (the fewer rows, the more).
+// Subsets of a CTA's keys that keep their own partial state, at most (the fewer rows, the more).
 __host__ __device__ constexpr int tree_subs(int R) { return R <= 8 ? 4 : R <= 32 ? 2 : 1; }
 
 // A partial state of the tree decode: (maximum, sum) of R rows of both maps, for each subset, then their

@@ -22,7 +22,6 @@ cudaError_t launch_tree(TreeParams p, cudaStream_t s) {
       return launch_tree_cols<D, V2, 32>(p, s);
     }
   }
-  p.subs = p.R <= 32 ? 2 : 1;
   return launch_tree_rows<D, V2, FMT>(p, s);
 }
 

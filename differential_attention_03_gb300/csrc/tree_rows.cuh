@@ -134,9 +134,9 @@ __device__ __forceinline__ void mma_ts_f8_elect(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
-// WIDE: more than 32 rows a map.  Else each row stands twice, once for either half of a tile's keys, and
-// the two are partial states of their own: half the keys a softmax thread, and no row idles.
-template <int D, bool V2, int FMT, bool WIDE>
+// SPLIT: up to 32 rows a map stand twice, once for either half of a tile's keys, and the two are partial
+// states of their own: half the keys a softmax thread.
+template <int D, bool V2, int FMT, bool SPLIT>
 __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeRowsCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
@@ -424,12 +424,13 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   } else {
     // =============================================================== softmax
     const int wq = warp & 3, qd = (warp - 4) >> 2;  // lane quarter, which of its four warps
-    const int map = wq >> 1, sub = WIDE ? 0 : (wq & 1);
+    const int map = wq >> 1, sub = SPLIT ? (wq & 1) : 0;
+    const bool act = C::V8 || SPLIT || 32 * (wq & 1) < p.R;  // the quarter has rows (e4m3 values: more than 32)
     {
-      constexpr int NC = WIDE ? 32 : 16;                       // key columns of this warp,
-      const int col0 = WIDE ? 32 * qd : 64 * sub + 16 * qd;    // from this one
+      constexpr int NC = SPLIT ? 16 : 32;                      // key columns of this warp,
+      const int col0 = SPLIT ? 64 * sub + 16 * qd : 32 * qd;   // from this one
       constexpr int OC = DV / 4;                               // output channels it rescales and writes
-      const int r = WIDE ? (wq & 1) * 32 + lane : lane;        // row of the map
+      const int r = SPLIT ? lane : (wq & 1) * 32 + lane;       // row of the map
       const bool valid = r < p.R;
       const int row = wq * 32 + lane;                          // MMA row
       const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
             if (in) {
               uint8_t* dst = q + (ch >> 3) * (C::QROWS * 128) + swizzled<128>(qr, ch & 7);
               *reinterpret_cast<uint4*>(dst) = x;
-              if (!WIDE) *reinterpret_cast<uint4*>(dst + 32 * 128) = x;  // (the second copy of the rows)
+              if (SPLIT) *reinterpret_cast<uint4*>(dst + 32 * 128) = x;  // (the second copy of the rows)
             }
           } else {
             // The row scaled by a power of two that puts its largest magnitude in [128, 256), in
@@ -489,7 +490,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
               uint8_t* dst = q + swizzled<C::KBOXB>(qr, ch >> 1) + 8 * (ch & 1);
               *reinterpret_cast<uint2*>(dst) = hi;
               *reinterpret_cast<uint2*>(dst + C::Q_TERM) = lo8;
-              if (!WIDE) {
+              if (SPLIT) {
                 *reinterpret_cast<uint2*>(dst + 32 * C::KROW) = hi;
                 *reinterpret_cast<uint2*>(dst + 32 * C::KROW + C::Q_TERM) = lo8;
               }
@@ -533,134 +534,136 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
           mbar_wait(&s_full[s], (g >> 1) & 1u, ab);
           __syncwarp();
           tc_fence_after();
-          uint32_t x[NC];
-          if constexpr (WIDE)
-            tmem_ld32(tS + col0, x);
-          else
-            tmem_ld16(tS + col0, x);
-          const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + col0;
-          if constexpr (C::V8) {
-            mbar_wait(&sc_full[g % NS], (g / NS) & 1u, ab);
-            __syncwarp();
-          }
-          if constexpr (WIDE)
-            tmem_ld_wait(x);
-          else
-            tmem_ld_wait16(x);
-          if constexpr (C::PSEP) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[s]);
-          }
-          // ---- scores
           const bool special = key0 + BN > w.len.L;  // the tile reaches into the drafted keys or past them
-          const uint64_t rc2 = f2pack(rc, rc);
-          float pm = -INFINITY;
-          if constexpr (C::V8) {
-#pragma unroll
-            for (int c = 0; c < NC; c += 4) {
-              const float4 ks = *reinterpret_cast<const float4*>(sc + 128 * ((map && !V2) ? 1 : 0) + c);
-              const float4 lv = *reinterpret_cast<const float4*>(sc + 384 + c);
-              float t0, t1, y0, y1;
-              const uint64_t ta = mul2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2pack(ks.x, ks.y));
-              const uint64_t tb = mul2(f2pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2pack(ks.z, ks.w));
-              f2unpack(fma2(ta, rc2, f2pack(lv.x, lv.y)), y0, y1);
-              pm = max3(pm, y0, y1);
-              f2unpack(fma2(tb, rc2, f2pack(lv.z, lv.w)), y0, y1);
-              pm = max3(pm, y0, y1);
-              f2unpack(ta, t0, t1);
-              x[c] = __float_as_uint(t0);
-              x[c + 1] = __float_as_uint(t1);
-              f2unpack(tb, t0, t1);
-              x[c + 2] = __float_as_uint(t0);
-              x[c + 3] = __float_as_uint(t1);
-            }
-          } else if (!special) {
-#pragma unroll
-            for (int c = 0; c < NC; c += 2) pm = max3(pm, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-          }
-          if (special) {  // hide what the row does not see
-            const int rel = key0 + col0 - w.len.L;  // drafted token of the first column
-            const uint32_t vis = static_cast<uint32_t>(
-                rel >= 64 ? 0ull : rel >= 0 ? see >> rel : rel <= -64 ? ~0ull : (see << -rel) | ((1ull << -rel) - 1ull));
-            pm = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              if (!((vis >> c) & 1u)) x[c] = __float_as_uint(-INFINITY);
-              if constexpr (C::V8)
-                pm = fmaxf(pm, fmaf(__uint_as_float(x[c]), rc, sc[384 + c]));
-              else
-                pm = fmaxf(pm, __uint_as_float(x[c]));
-            }
-          }
-          if (!C::V8) pm *= rc;  // (rc > 0)
-          // ---- the row's maximum over the quarter's four warps
-          float* xg = xm + (g & 1u) * 512;
-          xg[qd * 128 + row] = pm;
-          named_bar_sync(1 + wq, 128);
-          pm = fmaxf(max3(xg[row], xg[128 + row], xg[256 + row]), xg[384 + row]);
-          const float m_new = fmaxf(m_used, pm);
-          float f = 1.f;  // what O and the sum go by under the new reference
-          if (__any_sync(0xffffffffu, m_new > m_used + top)) {
-            f = (m_used == m_new) ? 1.f : ex2(m_used - m_new);
-            l *= f;
-            m_used = m_new;
-            if (!C::PSEP && i > 0) scale_o(f);
-          }
-          const float ref = (m_used == -INFINITY) ? 0.f : m_used;
-          // ---- weights
-          const uint32_t tP = tl + C::TM_P + s * C::P_STEP;
-          const uint64_t nb2 = f2pack(-ref, -ref);
-          uint64_t acc[2] = {0, 0};
-          if constexpr (C::V8) {
-            uint32_t hi[NC / 4], lo8[NC / 4];
-#pragma unroll
-            for (int c = 0; c < NC; c += 4) {
-              const float4 vs = *reinterpret_cast<const float4*>(sc + 256 + c);
-              float v[4];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float a0, a1;
-                f2unpack(fma2(f2pack(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), rc2, nb2), a0, a1);
-                const uint64_t pw = f2pack(ex2(a0), ex2(a1));
-                acc[e] = add2(acc[e], pw);
-                f2unpack(mul2(pw, e ? f2pack(vs.z, vs.w) : f2pack(vs.x, vs.y)), v[2 * e], v[2 * e + 1]);
-              }
-              two_e4m3x4(v[0], v[1], v[2], v[3], hi[c >> 2], lo8[c >> 2]);
-            }
-            if (C::PSEP && g >= 2) {  // the P tile's last reader
-              mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
+          float f = 1.f;                             // what O and the sum go by under a new reference
+          if (act) {
+            uint32_t x[NC];
+            if constexpr (SPLIT)
+              tmem_ld16(tS + col0, x);
+            else
+              tmem_ld32(tS + col0, x);
+            const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (g % NS) * 512 + col0;
+            if constexpr (C::V8) {
+              mbar_wait(&sc_full[g % NS], (g / NS) & 1u, ab);
               __syncwarp();
-              tc_fence_after();
             }
-            tmem_st8(tP + 8u * qd, hi);
-            tmem_st8(tP + 32u + 8u * qd, lo8);
-          } else {
-            uint32_t hi[NC / 2], lo[NC / 2];
+            if constexpr (SPLIT)
+              tmem_ld_wait16(x);
+            else
+              tmem_ld_wait(x);
+            if constexpr (C::PSEP) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&s_free[s]);
+            }
+            // ---- scores
+            const uint64_t rc2 = f2pack(rc, rc);
+            float pm = -INFINITY;
+            if constexpr (C::V8) {
 #pragma unroll
-            for (int c = 0; c < NC; c += 2) {
-              float a0, a1;
-              f2unpack(fma2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rc2, nb2), a0, a1);
-              const float p0 = ex2(a0), p1 = ex2(a1);
-              acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], f2pack(p0, p1));
-              hi[c >> 1] = pack_bf16x2(p0, p1);
-              lo[c >> 1] = pack_bf16x2(p0 - __uint_as_float(hi[c >> 1] << 16), p1 - __uint_as_float(hi[c >> 1] & 0xffff0000u));
+              for (int c = 0; c < NC; c += 4) {
+                const float4 ks = *reinterpret_cast<const float4*>(sc + 128 * ((map && !V2) ? 1 : 0) + c);
+                const float4 lv = *reinterpret_cast<const float4*>(sc + 384 + c);
+                float t0, t1, y0, y1;
+                const uint64_t ta = mul2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2pack(ks.x, ks.y));
+                const uint64_t tb = mul2(f2pack(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])), f2pack(ks.z, ks.w));
+                f2unpack(fma2(ta, rc2, f2pack(lv.x, lv.y)), y0, y1);
+                pm = max3(pm, y0, y1);
+                f2unpack(fma2(tb, rc2, f2pack(lv.z, lv.w)), y0, y1);
+                pm = max3(pm, y0, y1);
+                f2unpack(ta, t0, t1);
+                x[c] = __float_as_uint(t0);
+                x[c + 1] = __float_as_uint(t1);
+                f2unpack(tb, t0, t1);
+                x[c + 2] = __float_as_uint(t0);
+                x[c + 3] = __float_as_uint(t1);
+              }
+            } else if (!special) {
+#pragma unroll
+              for (int c = 0; c < NC; c += 2) pm = max3(pm, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
             }
-            if constexpr (WIDE) {
-              tmem_st16(tP + 16u * qd, hi);
-              tmem_st16(tP + 64u + 16u * qd, lo);
+            if (special) {  // hide what the row does not see
+              const int rel = key0 + col0 - w.len.L;  // drafted token of the first column
+              const uint32_t vis = static_cast<uint32_t>(
+                  rel >= 64 ? 0ull : rel >= 0 ? see >> rel : rel <= -64 ? ~0ull : (see << -rel) | ((1ull << -rel) - 1ull));
+              pm = -INFINITY;
+#pragma unroll
+              for (int c = 0; c < NC; ++c) {
+                if (!((vis >> c) & 1u)) x[c] = __float_as_uint(-INFINITY);
+                if constexpr (C::V8)
+                  pm = fmaxf(pm, fmaf(__uint_as_float(x[c]), rc, sc[384 + c]));
+                else
+                  pm = fmaxf(pm, __uint_as_float(x[c]));
+              }
+            }
+            if (!C::V8) pm *= rc;  // (rc > 0)
+            // ---- the row's maximum over the quarter's four warps
+            float* xg = xm + (g & 1u) * 512;
+            xg[qd * 128 + row] = pm;
+            named_bar_sync(1 + wq, 128);
+            pm = fmaxf(max3(xg[row], xg[128 + row], xg[256 + row]), xg[384 + row]);
+            const float m_new = fmaxf(m_used, pm);
+            if (__any_sync(0xffffffffu, m_new > m_used + top)) {
+              f = (m_used == m_new) ? 1.f : ex2(m_used - m_new);
+              l *= f;
+              m_used = m_new;
+              if (!C::PSEP && i > 0) scale_o(f);
+            }
+            const float ref = (m_used == -INFINITY) ? 0.f : m_used;
+            // ---- weights
+            const uint32_t tP = tl + C::TM_P + s * C::P_STEP;
+            const uint64_t nb2 = f2pack(-ref, -ref);
+            uint64_t acc[2] = {0, 0};
+            if constexpr (C::V8) {
+              uint32_t hi[NC / 4], lo8[NC / 4];
+#pragma unroll
+              for (int c = 0; c < NC; c += 4) {
+                const float4 vs = *reinterpret_cast<const float4*>(sc + 256 + c);
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float a0, a1;
+                  f2unpack(fma2(f2pack(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), rc2, nb2), a0, a1);
+                  const uint64_t pw = f2pack(ex2(a0), ex2(a1));
+                  acc[e] = add2(acc[e], pw);
+                  f2unpack(mul2(pw, e ? f2pack(vs.z, vs.w) : f2pack(vs.x, vs.y)), v[2 * e], v[2 * e + 1]);
+                }
+                two_e4m3x4(v[0], v[1], v[2], v[3], hi[c >> 2], lo8[c >> 2]);
+              }
+              if (C::PSEP && g >= 2) {  // the P tile's last reader
+                mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
+                __syncwarp();
+                tc_fence_after();
+              }
+              tmem_st8(tP + 8u * qd, hi);
+              tmem_st8(tP + 32u + 8u * qd, lo8);
             } else {
-              const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-              tmem_st8(tP + 32u * sub + 8u * qd, hi);
-              tmem_st8(tP + 64u + 32u * sub + 8u * qd, lo);
-              tmem_st8(tP + 32u * (sub ^ 1) + 8u * qd, zero);
-              tmem_st8(tP + 64u + 32u * (sub ^ 1) + 8u * qd, zero);
+              uint32_t hi[NC / 2], lo[NC / 2];
+#pragma unroll
+              for (int c = 0; c < NC; c += 2) {
+                float a0, a1;
+                f2unpack(fma2(f2pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rc2, nb2), a0, a1);
+                const float p0 = ex2(a0), p1 = ex2(a1);
+                acc[(c >> 1) & 1] = add2(acc[(c >> 1) & 1], f2pack(p0, p1));
+                hi[c >> 1] = pack_bf16x2(p0, p1);
+                lo[c >> 1] = pack_bf16x2(p0 - __uint_as_float(hi[c >> 1] << 16), p1 - __uint_as_float(hi[c >> 1] & 0xffff0000u));
+              }
+              if constexpr (!SPLIT) {
+                tmem_st16(tP + 16u * qd, hi);
+                tmem_st16(tP + 64u + 16u * qd, lo);
+              } else {
+                const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                tmem_st8(tP + 32u * sub + 8u * qd, hi);
+                tmem_st8(tP + 64u + 32u * sub + 8u * qd, lo);
+                tmem_st8(tP + 32u * (sub ^ 1) + 8u * qd, zero);
+                tmem_st8(tP + 64u + 32u * (sub ^ 1) + 8u * qd, zero);
+              }
             }
-          }
-          {
-            float s0, s1;
-            f2unpack(add2(acc[0], acc[1]), s0, s1);
-            l += s0 + s1;
+            {
+              float s0, s1;
+              f2unpack(add2(acc[0], acc[1]), s0, s1);
+              l += s0 + s1;
+            }
           }
           if (special) {
             if (C::V8 && ti < BN && key0 + ti >= w.len.L && key0 + ti < w.len.end) {
@@ -712,7 +715,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
         }
         float* o8 = state + tree_state_o(p.R, p.subs) + (static_cast<size_t>(sm) * p.R + r) * DV + OC * qd;
 #pragma unroll 1
-        for (int q = 0; q < OC / 32; ++q) {
+        for (int q = 0; act && q < OC / 32; ++q) {
           uint32_t o[32];
           tmem_ld32(tl + C::TM_O + OC * qd + 32u * q, o);
           tmem_ld_wait(o);
@@ -738,12 +741,25 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   }
 }
 
+// Small tiles want SPLIT: 128 keys of e4m3 keys and bf16 values at DV = 128 are 48 KB, 2100 cycles of HBM, and
+// the softmax's way through a tile is too long for that with 32 keys a thread (fp8k V1 d64 B8 H16 n32768, one
+// token, 253 us split, 289 not).  Larger ones don't, as the second state of every row is written and merged
+// (bf16 V1 d128 B4 H12 T16 n8192 79.0 us split, 76.9 not; T32 90.3 and 85.4; d64 B8 H16 T1 n32768 311 and 307).
 template <int D, bool V2, int FMT>
-cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t s) {
+constexpr bool tree_splits(int R) {
+  return FMT == kCacheFp8k && (V2 ? D : 2 * D) == 128 && R <= 32;
+}
+
+template <int D, bool V2, int FMT>
+cudaError_t launch_tree_rows(TreeParams p, cudaStream_t s) {
   using C = TreeRowsCfg<D, V2, FMT>;
-  void (*kern)(TreeParams) = tree_rows_kernel<D, V2, FMT, true>;
-  if constexpr (!C::V8) {  // (e4m3 values: more than 32 rows only, see launch_tree)
-    if (p.R <= 32) kern = tree_rows_kernel<D, V2, FMT, false>;
+  void (*kern)(TreeParams) = tree_rows_kernel<D, V2, FMT, false>;
+  p.subs = 1;
+  if constexpr (tree_splits<D, V2, FMT>(1)) {
+    if (tree_splits<D, V2, FMT>(p.R)) {
+      kern = tree_rows_kernel<D, V2, FMT, true>;
+      p.subs = 2;
+    }
   }
   return launch_tree_pair<C::DV, V2>(kern, C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / 128.f : 1.f, p, s);
 }
