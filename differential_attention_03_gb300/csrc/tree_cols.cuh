@@ -1,6 +1,7 @@
 // Attention of drafted tokens over a key/value cache (tcgen05 tensor cores,
-// TMA, mbarriers; sm_103a): up to 64 new tokens of a sequence, the nodes of a
-// draft tree, against its cached keys.
+// TMA, mbarriers; sm_103a): new tokens of a sequence, the nodes of a draft
+// tree, against its cached keys, up to 32 rows (tokens times pairs) of a map
+// over an fp8 cache (more, and the other formats: tree_rows.cuh).
 //
 // What it computes, for sequence b with L = lens[b] committed keys and the
 // keys of its nt drafted tokens in cache rows L .. L + nt - 1:

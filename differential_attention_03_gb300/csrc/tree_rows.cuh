@@ -42,8 +42,8 @@
 // Roles (640 threads, one CTA per SM): warp 0 TMA producer; warp 1 score
 // MMAs; warp 2 P V MMAs; warp 3 value and key scales (FP8); warps 4-19
 // softmax, four warps a lane quarter, each a quarter of a tile's key columns
-// (quarters without rows sleep).  TMEM: O, then two score tiles, in which P
-// replaces the scores.
+// (quarters without rows only pass the barriers).  TMEM: O, then two score
+// tiles, in which P replaces the scores where it has no tiles of its own.
 //
 // Rounding.  Weights meet the values as two terms, bf16 or e4m3 as the values
 // are: hi + lo holds 16 bits of a weight with bf16 values, 8 with e4m3 ones
