@@ -20,10 +20,8 @@
 // bf16 V1 d64, 8192 tokens of 64 heads (134 MB) 25 us, 5.4 TB/s; append V2 d128
 // fp8, 8002 tokens of 32 + 16 + 16 heads (173 MB) 37 us, 4.6 TB/s with the
 // issue slots 53 % busy (unpacking, rotating, finding the maximum and
-// converting are some 200 instructions per 32 x 16 values; staging a CTA's rows
-// in shared memory by asynchronous copies took 10 % off 30000 unpadded tokens,
-// but put 10 % on these, whose copies wait for ntok, and on a few hundred); a
-// few tokens 2.5 us after one another, the launch and two dependent loads.
+// converting are some 200 instructions per 32 x 16 values); a few tokens 5 us
+// on the GPU, the launch and two dependent loads.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -230,15 +228,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 // ----------------------------------------------------------------- append
 __device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8], float mul) {
-  const uint64_t m2 = f2pack(mul, mul);
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float a, b, c, d;
-    f2unpack(mul2(f2pack(f[4 * h], f[4 * h + 1]), m2), a, b);
-    f2unpack(mul2(f2pack(f[4 * h + 2], f[4 * h + 3]), m2), c, d);
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lo =
+        __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h] * mul, f[4 * h + 1] * mul), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi =
+        __nv_cvt_float2_to_fp8x2(make_float2(f[4 * h + 2] * mul, f[4 * h + 3] * mul), __NV_SATFINITE, __NV_E4M3);
     w[h] = lo | (hi << 16);
   }
   return make_uint2(w[0], w[1]);
@@ -247,8 +243,8 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8], float mul) {
 // Largest magnitude of 8 numbers and m; a NaN stays one.
 __device__ __forceinline__ float amax8(float m, const float (&x)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 2)
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(fabsf(x[e])), "f"(fabsf(x[e + 1])));
+  for (int e = 0; e < 8; ++e)
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(x[e])));
   return m;
 }
 
