@@ -20,8 +20,11 @@
 // bf16 V1 d64, 8192 tokens of 64 heads (134 MB) 25 us, 5.4 TB/s; append V2 d128
 // fp8, 8002 tokens of 32 + 16 + 16 heads (173 MB) 37 us, 4.6 TB/s with the
 // issue slots 53 % busy (unpacking, rotating, finding the maximum and
-// converting are some 200 instructions per 32 x 16 values); a few tokens 5 us
-// on the GPU, the launch and two dependent loads.
+// converting are some 200 instructions per 32 x 16 values; staging a CTA's rows
+// in shared memory by asynchronous copies took 10 % off 30000 unpadded tokens,
+// but put 10 % on these, whose copies wait for ntok, and on a few hundred; two
+// values an instruction in the maximum and the scaling changed nothing); a few
+// tokens 2.3 us one call after the other, the launch and two dependent loads.
 #pragma once
 
 #include <cuda_bf16.h>
