@@ -32,12 +32,14 @@
 //
 // Operands.  e4m3 keys and values with an fp32 scale a row, as the cache holds
 // them: a query row is scaled by a power of two and split into two e4m3
-// terms (hi + lo holds a bf16 value's eight bits), and so is P, at twice the
-// MMA rate.  A key's scale multiplies its scores; a value row's scale is
+// terms (hi + lo holds a bf16 value's eight bits; rows within a factor of
+// eight of the largest share its power of two, and hold them down to 2^-7 of
+// their own largest element instead of 2^-10), P into three e5m2 terms
+// (three_e5m2x4).  A key's scale multiplies its scores; a value row's scale is
 // folded into P before the split, and the reference is the maximum of score +
 // log2(value scale), so that the largest contribution, not the largest weight,
-// sits at the top of e4m3's range (a key with a large weight and a small value
-// row would otherwise push every other weight to e4m3's absolute floor).
+// sits at the top of e5m2's range (a key with a large weight and a small value
+// row would otherwise push every other weight towards its floor).
 //
 // Split.  The key tiles (128 keys) of all units form one line that is dealt
 // out evenly, a contiguous range to each CTA, from the lengths on the device;
@@ -80,7 +82,11 @@ struct TreeColsCfg {
   static constexpr int COLS = 2 * TP;           // columns of both maps
   // The terms of an operand stand side by side as columns, so that one MMA takes both.
   static constexpr int SCOLS = 2 * COLS;  // of a score tile: [map][term][TP]
-  static constexpr int PCOLS = 2 * COLS;  // of P and O^T: [term][map][TP]
+  // P and O^T: [term][map][TP] with the three terms side by side, or, where tensor memory has no room for
+  // them, two, and the third added to the first's O^T by MMAs of its own.
+  static constexpr bool P3APART = TP == 32;
+  static constexpr int PTERMS = P3APART ? 2 : 3;
+  static constexpr int PCOLS = PTERMS * COLS;
   static constexpr int KROW = D;          // bytes of a key row (and its swizzle width)
   static constexpr int VROW = DV;
   static constexpr int VBOX = VROW / 128;
@@ -91,11 +97,12 @@ struct TreeColsCfg {
   static constexpr int QROWS = SCOLS;
   static constexpr int QK_N = V2 ? SCOLS : 2 * TP;
   static constexpr int Q_BYTES = (QROWS * KROW + 1023) / 1024 * 1024;
-  static constexpr int PROW = PCOLS;         // bytes of a key's row of P^T (its swizzle width)
-  static constexpr int P_BYTES = BN * PROW;          // of a stream
-  // Rings: about 160 KB in flight.
+  static constexpr int PROW = TP == 8 ? 64 : 128;      // bytes of a key's row of P^T (its swizzle width)
+  static constexpr int P3ROW = P3APART ? COLS : 0;     // and of the third terms' own
+  static constexpr int P_BYTES = BN * (PROW + P3ROW);  // of a stream
+  // Rings: 160-168 KB in flight; some 14 KB stay free for a CTA of the merge, which is launched meanwhile.
   static constexpr int NK = D == 64 ? 10 : 5;
-  static constexpr int NV = V_SLOT == 8192 ? (D == 64 ? 11 : 10) : 6;
+  static constexpr int NV = V_SLOT == 8192 ? (D == 64 ? 11 : 10) : 5;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = Q_BYTES;
   static constexpr int OFF_K = OFF_P + NSTREAM * P_BYTES;
@@ -113,7 +120,8 @@ struct TreeColsCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int QK_STEPS = KROW / 32;
   static constexpr uint32_t IDESC_QK = idesc_e4m3(128, QK_N);
-  static constexpr uint32_t IDESC_PV = idesc_e4m3(128, PCOLS) | (3u << 15);  // (V^T and P^T: both transposed)
+  static constexpr uint32_t IDESC_PV = idesc_e4m3(128, PCOLS) | kIdescB5 | (3u << 15);  // (V^T and P^T: both transposed)
+  static constexpr uint32_t IDESC_P3 = idesc_e4m3(128, COLS) | kIdescB5 | (3u << 15);
   static constexpr int NSOFT = 16;              // softmax warps
   static constexpr int NARR = NSOFT / NSTREAM;  // of a stream
   static constexpr int NTHREADS = (4 + NSOFT) * 32;
@@ -122,7 +130,7 @@ struct TreeColsCfg {
   static_assert(TM_S + NBUF * SCOLS <= 512, "tensor memory");
   static_assert(K_SLOT % 1024 == 0 && V_SLOT % 1024 == 0 && P_BYTES % 1024 == 0, "swizzled operands start on 1 KB");
   static_assert(QK_N % 16 == 0 && PCOLS % 16 == 0, "MMA columns");
-  static_assert(PROW == 32 || PROW == 64 || PROW == 128, "P rows are one swizzle width");
+  static_assert(PCOLS <= PROW && (P3ROW == 0 || P3ROW == 64), "P rows are one swizzle width");
 };
 
 constexpr float kTreeDead = -16384.f;  // minus the reference of a column without a token: weights of zero
@@ -327,6 +335,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
       } else {
         const uint64_t dv0 = sdesc_rows<128>(smem_u32(smem + C::OFF_V), C::VKEYS * 128);
         const uint64_t dp0 = sdesc_rows<C::PROW>(smem_u32(smem + C::OFF_P), 16);
+        const uint64_t dt0 = sdesc_rows<64>(smem_u32(smem + C::OFF_P + BN * C::PROW), 16);  // (P3APART: one stream)
         for (int i = 0; ok && i < seg; ++i, ++g) {
           const uint32_t st = stream_of(g);
           if (!waitp(&p_ready[st], number_of(g) & 1u)) ok = false;
@@ -347,6 +356,8 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
                 const uint64_t a = desc_at(dv0, voff + ((mt * C::VKEYS * 128 + kk * KS * 128) >> 4));
                 const uint64_t bd = desc_at(dp0, poff + (((part * C::VKEYS + kk * KS) * C::PROW) >> 4));
                 mma_ss_f8_elect(d, a, bd, C::IDESC_PV, (part > 0 || kk > 0) ? 1u : again);
+                if constexpr (C::P3APART)
+                  mma_ss_f8_elect(d, a, desc_at(dt0, ((part * C::VKEYS + kk * KS) * C::P3ROW) >> 4), C::IDESC_P3, 1u);
               }
             }
             tc_commit_elect(&vempty[slot]);
@@ -379,7 +390,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
     const int own = lane % NC;                           // the column this lane reduces
     float* xm = reinterpret_cast<float*>(smem + C::OFF_XM) + wg * 64;
     float* ac = reinterpret_cast<float*>(smem + C::OFF_AC) + wg * 16;
-    const float top = kTreeRescale8Log2;
+    const float top = kTreeRoom8Log2 + kTreeRescale8Log2;
     uint32_t g0 = 0;  // the segment's first tile
     TreeWalk w = walk_begin(p, count, start);
     // (an aborted CTA walks on: every wait then returns at once, and no warp misses a named barrier)
@@ -498,14 +509,14 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
         float rk = rc, rk_b = rc, vs = 1.f, lv = 0.f;
         // A value scale that is not finite makes its row NaN: for everybody, or, for a drafted row,
         // for the tokens that see it (poison, and weightless).  The log2 the reference goes by is at
-        // least 2^-100, so that the sum of weights stays far below fp32's end.
+        // least kTreeLeastValueLog2, so that the sum of weights stays below fp32's end.
         rk *= ks_next;
         rk_b *= V2 ? ks_next : ks2_next;
         vs = vs_next;
-        lv = fmaxf(__log2f(vs), -100.f);
+        lv = fmaxf(__log2f(vs), kTreeLeastValueLog2);
         if (!(fabsf(vs) < INFINITY)) {
           vs = __uint_as_float(0x7fffffffu);
-          lv = -100.f;
+          lv = kTreeLeastValueLog2;
           if (j >= w.len.L) {
             atomicOr(&poison[k % 3], 1ull << (j - w.len.L));
             vs = 0.f;
@@ -576,7 +587,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           const float mine = lanes_reduce<NC>(y, lane, [](float a, float b) { return fmaxf(a, b); });
           if (lane < NC) xm[wq * 16 + lane] = mine;
           named_bar_sync(1 + wg, 128);
-          const float cm = fmaxf(fmaxf(xm[own], xm[16 + own]), fmaxf(xm[32 + own], xm[48 + own]));
+          const float cm = fmaxf(fmaxf(xm[own], xm[16 + own]), fmaxf(xm[32 + own], xm[48 + own])) - kTreeRoom8Log2;
           float up = 0.f;  // how much the reference rises
           if (live && cm > -INFINITY && (!def || cm > 0.f)) up = cm;
           f = def ? ex2(-up) : 1.f;  // (before the first reference there is nothing to scale)
@@ -593,7 +604,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           open = named_bar_any(1 + wg, !def);  // (and the references are in place)
         }
         // ---- weights
-        uint32_t pk[NC / 2];
+        uint32_t pk[3][NC / 4];
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
           const uint64_t ea = f2pack(ex2(x[c]), ex2(x[c + 1])), eb = f2pack(ex2(x[c + 2]), ex2(x[c + 3]));
@@ -603,23 +614,26 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           const uint64_t vs2 = f2pack(vs, vs);
           f2unpack(mul2(ea, vs2), v0, v1);
           f2unpack(mul2(eb, vs2), v2, v3);
-          two_e4m3x4(v0, v1, v2, v3, pk[c >> 2], pk[NC / 4 + (c >> 2)]);
+          three_e5m2x4(v0, v1, v2, v3, pk[0][c >> 2], pk[1][c >> 2], pk[2][c >> 2]);
         }
         if (!pv_over) mbar_wait(&pv_done[stream], (nb - 1) & 1u, ab);  // the P tile's last reader
         __syncwarp();
         any = true;
         {
-          // chunks of 16 bytes of the key's row: the columns' hi terms, then all columns' lo terms
+          // chunks of 16 bytes of the key's row: the columns' first terms, then all columns' second and third
           uint8_t* pt = smem + C::OFF_P + stream * C::P_BYTES;
           const int ch = (map * TP + c0) / 16;
-          *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(pt + swizzled<C::PROW>(key, ch + COLS / 16)) =
-              make_uint4(pk[4], pk[5], pk[6], pk[7]);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            const uint32_t at = (C::P3APART && e == 2) ? BN * C::PROW + swizzled<64>(key, ch)
+                                                       : swizzled<C::PROW>(key, ch + e * (COLS / 16));
+            *reinterpret_cast<uint4*>(pt + at) = make_uint4(pk[e][0], pk[e][1], pk[e][2], pk[e][3]);
+          }
         }
         if (fix) {  // (last of all, when the previous P V is over: V1 d64 B8 H16, 32 tokens, 286 us and 267 this way)
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < 2 * C::NMT; ++q) {  // [128 channels][term]
+          for (int q = 0; q < C::PTERMS * C::NMT; ++q) {  // [128 channels][term]
             const uint32_t to = tl + C::TM_O + (stream * C::NMT * C::PCOLS + q * COLS) + map * TP + c0;
             uint32_t o[NC];
             tmem_load(to, o);
@@ -680,9 +694,12 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
           const uint32_t to = tl + C::TM_O + (stream * C::NMT + mt) * C::PCOLS + map * TP + c0;
           uint32_t a[NC], b[NC];
           tmem_load(to, a);
-          tmem_load(to + COLS, b);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) a[c] = __float_as_uint(__uint_as_float(a[c]) + __uint_as_float(b[c]));
+          for (int e = 1; e < C::PTERMS; ++e) {
+            tmem_load(to + e * COLS, b);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) a[c] = __float_as_uint(__uint_as_float(a[c]) + __uint_as_float(b[c]));
+          }
 #pragma unroll
           for (int c = 0; c < NC; ++c)
             if (row_of(c) < p.R && here)
@@ -710,7 +727,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
 template <int D, bool V2, int TP>
 cudaError_t launch_tree_cols(const TreeParams& p, cudaStream_t s) {
   using C = TreeColsCfg<D, V2, TP>;
-  return launch_tree_pair<C::DV, V2>(tree_cols_kernel<D, V2, TP>, C::NTHREADS, C::SMEM_BYTES, 1.f / 128.f, p, s);
+  return launch_tree_pair<C::DV, V2>(tree_cols_kernel<D, V2, TP>, C::NTHREADS, C::SMEM_BYTES, 1.f / kTreeValueMult, p, s);
 }
 
 }  // namespace da

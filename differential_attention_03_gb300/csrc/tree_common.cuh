@@ -1,5 +1,5 @@
 // What the two tree-decode kernels share: the line of key tiles, descriptors,
-// two-term e4m3 weights, and the kernel that merges their partial states.
+// e5m2 weights in three terms, and the kernel that merges their partial states.
 //
 // A partial state holds, for each of `subs` subsets of a CTA's keys of a unit
 // and each map: (reference maximum, sum of weights) of the R rows, then O of
@@ -20,10 +20,11 @@
 namespace da {
 
 constexpr float kTreeRescaleLog2 = 8.f;    // bf16 P: how far a score may exceed the reference maximum
-// e4m3 P: the reference sits at 2^7 and e4m3 ends at 448 = 2^8.8; the more room, the fewer new references
-// (V1 d64 B8 H16, 32 tokens, n32768: 267 us with 1, 256 with 1.75; a bit less of depth would give 248).
-constexpr float kTreeRescale8Log2 = 1.75f;
-constexpr float kTreeValueMult = 0.5f;     // 2^7, times two_e4m3x4's 2^-8
+// e4m3 values: the reference sits at 2^8 on the scale that P is split at, 2^3 below the largest contribution
+// when it is set, and moves once one is 2^4 above that: 2^15 at most (e5m2 ends at 57344 = 2^15.8).
+constexpr float kTreeRoom8Log2 = 3.f, kTreeRescale8Log2 = 4.f;
+constexpr float kTreeValueMult = 256.f;    // (a scale is at most 2^128 / 448: no overflow)
+constexpr float kTreeLeastValueLog2 = -96.f;  // what a value row counts at least for the reference (sums stay below 2^128)
 
 // A sequence's committed keys, its drafted tokens, the end of its keys and its tiles.
 struct TreeLen {
@@ -88,22 +89,37 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t c) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3)));
 }
 
-// Four non-negative floats, scaled to 2^-8 of what they stand for (at most
-// 448 2^-8), as two e4m3 terms each: hi truncates, hi + lo is within 2^-8 of
-// the value, or 2^-10 absolute, as a bf16 would be.  At that scale f16's
-// exponent field is e4m3's, so a code is bits 7-13 of the f16: pairs of f16
-// are shifted and masked as integers (the e4m3 conversion instructions take
-// about 16 issue cycles each, and bounded the kernel: 372 us against 337 us
-// at B8 H16 n32768 d64).  A NaN stays a NaN.
-__device__ __forceinline__ void two_e4m3x4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  uint32_t f0, f1, r0, r1;
+// Four non-negative floats of at most 2^15.8 as three e5m2 terms each.  An
+// e5m2 code is the upper byte of an f16, so a term is that byte, and what is
+// left an exact f16 subtraction; the last term rounds.  The three are within
+// 2^-8.8 of the value, or 2^-16.8 absolute: 2^-28 of the largest contribution,
+// so that weights too small to be told from zero do not add up to anything
+// over any cache that fits the GPU.  (Two e4m3 terms hold the same bits, but
+// end at 2^-17 of the largest: of 27000 keys 12 powers of e below one, 15 % of
+// the sum was lost.)  Integer and f16 work, as the 8-bit conversion instructions
+// take about 16 issue cycles each.  A NaN stays a NaN.
+__device__ __forceinline__ void three_e5m2x4(float a, float b, float c, float d, uint32_t& t1, uint32_t& t2, uint32_t& t3) {
+  uint32_t f0, f1;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f0) : "f"(b), "f"(a));
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(f1) : "f"(d), "f"(c));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(f0), "r"(f0 & 0x7f807f80u));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(f1), "r"(f1 & 0x7f807f80u));
-  hi = __byte_perm(f0 << 1, f1 << 1, 0x7531);
-  // (a NaN in one column must not carry into the next: its hi code says it already)
-  lo = __byte_perm((r0 & 0x3fff3fffu) * 2 + 0x00800080u, (r1 & 0x3fff3fffu) * 2 + 0x00800080u, 0x7531);
+  t1 = __byte_perm(f0, f1, 0x7531);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(f0) : "r"(f0 & 0xff00ff00u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(f1) : "r"(f1 & 0xff00ff00u));
+  t2 = __byte_perm(f0, f1, 0x7531);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(f0) : "r"(f0 & 0xff00ff00u));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(f1) : "r"(f1 & 0xff00ff00u));
+  t3 = __byte_perm(f0 + 0x00800080u, f1 + 0x00800080u, 0x7531);  // (a NaN, 0x7fff, does not carry into its neighbour)
+}
+
+// Instruction descriptor bits of kind::f8f6f4: A, or B, is e5m2 instead of e4m3.
+constexpr uint32_t kIdescA5 = 1u << 7, kIdescB5 = 1u << 10;
+
+// 32 lanes x 4 columns store.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&v)[4]) {
+  if (!DA_TMEM_OK(taddr, 4)) return;
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
 }
 
 // Matrix descriptor over rows of `width` bytes (128, 64 or 32: the swizzle).

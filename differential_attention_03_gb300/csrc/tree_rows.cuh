@@ -24,13 +24,13 @@
 // Formats.  bf16; FP8K: e4m3 keys with one scale a tensor, bf16 values; FP8:
 // e4m3 keys and values with an fp32 scale a row.  8-bit operands are not
 // converted: the query row is scaled by a power of two and split into two e4m3
-// terms (hi + lo holds a bf16 value's eight bits), and so is P, at twice the
-// MMA rate.  A key's scale multiplies its scores; a value row's scale is
-// folded into P before the split, and the reference maximum is that of score
-// + log2(value scale), so that the largest contribution, not the largest
-// weight, sits at the top of e4m3's range (a key with a large weight and a
-// small value row would otherwise push every other weight towards e4m3's
-// absolute floor).
+// terms (hi + lo holds a bf16 value's eight bits), P into three e5m2 terms
+// (three_e5m2x4), at twice the MMA rate.  A key's scale multiplies its scores; a
+// value row's scale is folded into P before the split, and the reference
+// maximum is that of score + log2(value scale), so that the largest
+// contribution, not the largest weight, sits at the top of e5m2's range (a key
+// with a large weight and a small value row would otherwise push every other
+// weight towards its floor).
 //
 // Split.  The key tiles (128 keys) of all units form one line that is dealt
 // out evenly, a contiguous range to each CTA, from the lengths on the device;
@@ -45,11 +45,11 @@
 // (quarters without rows only pass the barriers).  TMEM: O, then two score
 // tiles, in which P replaces the scores where it has no tiles of its own.
 //
-// Rounding.  Weights meet the values as two terms, bf16 or e4m3 as the values
-// are: hi + lo holds 16 bits of a weight with bf16 values, 8 with e4m3 ones
-// (whose own rounding is far coarser).  With hi alone, bf16 outputs over 8192
-// random keys were 2.5e-3 off the formula instead of 1.7e-3, which rounding the
-// output itself is; the second term costs 0 to 5 % of a bf16 call's time.
+// Rounding.  Weights meet bf16 values as two bf16 terms, 16 bits, and e4m3
+// ones (whose own rounding is far coarser) as three e5m2 terms, 9 bits.  With
+// one bf16 term, outputs over 8192 random keys were 2.5e-3 off the formula
+// instead of 1.7e-3, which rounding the output itself is; the second term costs
+// 0 to 5 % of a bf16 call's time.
 // Scores, maxima, sums and O stay fp32.
 //
 // Measured (this kernel alone): bf16 V1 d128 B4 H12 T16 n8192 71 us (403 MB, 5.7
@@ -101,19 +101,19 @@ struct TreeRowsCfg {
   static constexpr int NBARS = 2 * NK + 2 * NV + 2 * NS + 2 + 2 + 2 + 2 + 1 + 2;
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 256 + 1024;
-  // Tensor memory: O, two score tiles, and, where O leaves the room and P is e4m3 (DV = 128), two P
-  // tiles of 64 columns; else P takes the place of its scores.  P: hi terms, then lo terms.
+  // Tensor memory: O, two score tiles, and, where O leaves the room and P is e5m2 (DV = 128), a P tile of
+  // 96 columns; else P takes the place of its scores.  P: first terms, then second, then third.
   static constexpr bool PSEP = DV == 128 && V8;
   static constexpr uint32_t TM_O = 0, TM_S = DV;
-  static constexpr uint32_t TM_P = PSEP ? TM_S + 2 * BN : TM_S, P_STEP = PSEP ? 64 : BN;
+  static constexpr uint32_t TM_P = PSEP ? TM_S + 2 * BN : TM_S, P_STEP = PSEP ? 0 : BN;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int QK_STEPS = KROW / 32;
   static constexpr uint32_t IDESC_QK = K8 ? idesc_e4m3(128, BN) : idesc_bf16(128, BN, false, false);
-  static constexpr uint32_t IDESC_PV = V8 ? (idesc_e4m3(128, DV) | (1u << 16)) : idesc_bf16(128, DV, false, true);
+  static constexpr uint32_t IDESC_PV = V8 ? (idesc_e4m3(128, DV) | kIdescA5 | (1u << 16)) : idesc_bf16(128, DV, false, true);
   static constexpr int NACT = 16;  // softmax warps: four a lane quarter
   static constexpr int NTHREADS = (4 + NACT) * 32;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
-  static_assert(DV + 2 * BN + (PSEP ? 128 : 0) <= 512, "tensor memory");
+  static_assert(DV + 2 * BN + (PSEP ? 96 : 0) <= 512, "tensor memory");
   static_assert(K_SLOT % 1024 == 0 && V_SLOT % 1024 == 0 && Q_TERM % 1024 == 0, "swizzled boxes start on 1 KB");
 };
 
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
               if constexpr (C::V8) {
                 mma_ts_f8_elect(tm + C::TM_O, col, b, C::IDESC_PV, acc);
                 mma_ts_f8_elect(tm + C::TM_O, col + 32u, b, C::IDESC_PV, 1u);
+                mma_ts_f8_elect(tm + C::TM_O, col + 64u, b, C::IDESC_PV, 1u);
               } else {
                 mma_ts_elect(tm + C::TM_O, col, b, C::IDESC_PV, acc);
                 mma_ts_elect(tm + C::TM_O, col + 64u, b, C::IDESC_PV, 1u);
@@ -406,11 +407,10 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
           // drafted row, for the tokens that see it (marked by its log2, and weightless).
           const bool bad = !(fabsf(x) < INFINITY);
           const bool drafted = key0 + j >= w.len.L;
-          // The scale, at the top of the range (and at two_e4m3x4's 2^-8), and the log2 that the
-          // reference maximum goes by: at least -100, so that the sum of weights stays far below
-          // fp32's end.
+          // The scale, where P is split at, and the log2 that the reference maximum goes by: at
+          // least kTreeLeastValueLog2, so that the sum of weights stays below fp32's end.
           dst[256 + j] = bad ? (drafted ? 0.f : __uint_as_float(0x7fffffffu)) : x * kTreeValueMult;
-          dst[384 + j] = bad ? __uint_as_float(0x7fffffffu) : fmaxf(__log2f(x), -100.f);
+          dst[384 + j] = bad ? __uint_as_float(0x7fffffffu) : fmaxf(__log2f(x), kTreeLeastValueLog2);
         }
         mbar_arrive(&sc_full[g % NS]);
         if (++wi == walk_seg(w)) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
             float* xg = xm + (g & 1u) * 512;
             xg[qd * 128 + row] = pm;
             named_bar_sync(1 + wq, 128);
-            pm = fmaxf(max3(xg[row], xg[128 + row], xg[256 + row]), xg[384 + row]);
+            pm = fmaxf(max3(xg[row], xg[128 + row], xg[256 + row]), xg[384 + row]) - (C::V8 ? kTreeRoom8Log2 : 0.f);
             const float m_new = fmaxf(m_used, pm);
             if (__any_sync(0xffffffffu, m_new > m_used + top)) {
               f = (m_used == m_new) ? 1.f : ex2(m_used - m_new);
@@ -615,28 +615,33 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
             const uint64_t nb2 = f2pack(-ref, -ref);
             uint64_t acc[2] = {0, 0};
             if constexpr (C::V8) {
-              uint32_t hi[NC / 4], lo8[NC / 4];
 #pragma unroll
-              for (int c = 0; c < NC; c += 4) {
-                const float4 vs = *reinterpret_cast<const float4*>(sc + 256 + c);
-                float v[4];
+              for (int c0 = 0; c0 < NC; c0 += 16) {  // (16 columns' terms at a time, for the registers' sake)
+                uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float a0, a1;
-                  f2unpack(fma2(f2pack(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), rc2, nb2), a0, a1);
-                  const uint64_t pw = f2pack(ex2(a0), ex2(a1));
-                  acc[e] = add2(acc[e], pw);
-                  f2unpack(mul2(pw, e ? f2pack(vs.z, vs.w) : f2pack(vs.x, vs.y)), v[2 * e], v[2 * e + 1]);
+                for (int c = c0; c < c0 + 16; c += 4) {
+                  const float4 vs = *reinterpret_cast<const float4*>(sc + 256 + c);
+                  float v[4];
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    float a0, a1;
+                    f2unpack(fma2(f2pack(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])), rc2, nb2), a0, a1);
+                    const uint64_t pw = f2pack(ex2(a0), ex2(a1));
+                    acc[e] = add2(acc[e], pw);
+                    f2unpack(mul2(pw, e ? f2pack(vs.z, vs.w) : f2pack(vs.x, vs.y)), v[2 * e], v[2 * e + 1]);
+                  }
+                  const int z = (c - c0) >> 2;
+                  three_e5m2x4(v[0], v[1], v[2], v[3], t1[z], t2[z], t3[z]);
                 }
-                two_e4m3x4(v[0], v[1], v[2], v[3], hi[c >> 2], lo8[c >> 2]);
+                if (C::PSEP && c0 == 0 && g >= 1) {  // the P tile's last reader
+                  mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
+                  __syncwarp();
+                  tc_fence_after();
+                }
+                tmem_st4(tP + 8u * qd + (c0 >> 2), t1);
+                tmem_st4(tP + 32u + 8u * qd + (c0 >> 2), t2);
+                tmem_st4(tP + 64u + 8u * qd + (c0 >> 2), t3);
               }
-              if (C::PSEP && g >= 2) {  // the P tile's last reader
-                mbar_wait(&pv_done[s], ((g - 2) >> 1) & 1u, ab);
-                __syncwarp();
-                tc_fence_after();
-              }
-              tmem_st8(tP + 8u * qd, hi);
-              tmem_st8(tP + 32u + 8u * qd, lo8);
             } else {
               uint32_t hi[NC / 2], lo[NC / 2];
 #pragma unroll
@@ -761,7 +766,7 @@ cudaError_t launch_tree_rows(TreeParams p, cudaStream_t s) {
       p.subs = 2;
     }
   }
-  return launch_tree_pair<C::DV, V2>(kern, C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / 128.f : 1.f, p, s);
+  return launch_tree_pair<C::DV, V2>(kern, C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / kTreeValueMult : 1.f, p, s);
 }
 
 }  // namespace da

@@ -716,6 +716,11 @@ diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T
  *   workspace : required, at least the workspace call's bytes, 16-byte
  *               aligned; partial states, nothing kept between calls.  Calls
  *               that can overlap need their own.
+ * Rounding: scores, sums and accumulators are fp32.  A softmax weight meets
+ * bf16 values as two bf16 terms (2^-16 of it) and e4m3 values as three e5m2
+ * terms (2^-8.8 of it, or 2^-28 of the row's largest contribution).  Over e4m3
+ * keys a query row stands as two e4m3 terms, exact for elements down to 2^-7
+ * of the row's largest.
  * A drafted key or value row with a NaN or an infinity makes the tokens that
  * see it NaN, and no others.  Two kernels; results do not depend on the
  * order in which they run (the same inputs give the same bits on the same
