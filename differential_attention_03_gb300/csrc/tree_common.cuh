@@ -337,7 +337,8 @@ __device__ __forceinline__ int e4m3_shift(float amax) {
   return (amax > 0.f) ? max(-100, min(100, 134 - bexp)) : 0;
 }
 
-// Eight bf16 values times 2^sh as two e4m3 terms each.
+// Eight bf16 values times 2^sh as two e4m3 terms each.  An infinity becomes a NaN (the conversion would
+// make it 448): its row's scores are infinite or NaN in the formula, so its softmax is NaN.
 __device__ __forceinline__ void split_e4m3x8(const uint4& x, int sh, uint2& hi, uint2& lo) {
   const float mul = __int_as_float((127 + sh) << 23);
   const uint32_t u[4] = {x.x, x.y, x.z, x.w};
@@ -347,8 +348,8 @@ __device__ __forceinline__ void split_e4m3x8(const uint4& x, int sh, uint2& hi, 
     uint32_t a[2], b[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
-      const float v0 = __uint_as_float(u[2 * e + z] << 16) * mul;
-      const float v1 = __uint_as_float(u[2 * e + z] & 0xffff0000u) * mul;
+      const float x0 = __uint_as_float(u[2 * e + z] << 16), x1 = __uint_as_float(u[2 * e + z] & 0xffff0000u);
+      const float v0 = fmaf(x0, mul, x0 * 0.f), v1 = fmaf(x1, mul, x1 * 0.f);  // (infinity times 0)
       a[z] = e4m3x2(v0, v1);
       const float2 back = e4m3x2_value(a[z]);
       b[z] = e4m3x2(v0 - back.x, v1 - back.y);

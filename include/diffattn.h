@@ -721,6 +721,7 @@ diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T
  * terms (2^-8.8 of it, or 2^-28 of the row's largest contribution).  Over e4m3
  * keys a query row stands as two e4m3 terms, exact for elements down to 2^-7
  * of the row's largest.
+ * A query with a NaN or an infinity gives NaN for its token and head.
  * A drafted key or value row with a NaN or an infinity makes the tokens that
  * see it NaN, and no others.  Two kernels; results do not depend on the
  * order in which they run (the same inputs give the same bits on the same

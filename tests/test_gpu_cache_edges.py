@@ -154,3 +154,41 @@ def test_references_move_and_values_differ_in_size(T):
     bound = gain * (e + np.abs(pre) * de / np.maximum(rms - de, 1e-9))
     over = np.abs(_np(out) - ref) - (bound + 2.0 ** -8 * (np.abs(ref) + bound))
     assert over.max() <= 0, over.max()
+
+
+def _random(g, B, n, H, d, v1, fmt, k_mult=1.0):
+    """A cache of random rows and the values they stand for: (cache, keys, values)."""
+    dv, ks = (2 * d, (0.013 * k_mult, 0.021 * k_mult)) if v1 else (d, (0.013 * k_mult,))
+    c = (da.cache_v1(B, n, H, d, fmt, k1_scale=ks[0], k2_scale=ks[1]) if v1 else
+         da.cache_v2(B, n, H, d, fmt, k_scale=ks[0]))
+    keys = [_fill(t, s, f, torch.randn((B, n, H, d), generator=g, device="cuda") * k_mult, fmt)
+            for t, s, f in ((c.k1, c.k1_scales, c.k1_scale), (c.k2, c.k2_scales, c.k2_scale)) if t is not None]
+    val = _fill(c.v, c.v_scales, None, torch.randn((B, n, H, dv), generator=g, device="cuda"), fmt)
+    return c, keys, val
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8k", "fp8"])
+@pytest.mark.parametrize("v1,T,d", [(True, 1, 64), (True, 5, 64), (True, 14, 128), (True, 20, 64), (True, 40, 128),
+                                    (False, 3, 128), (False, 30, 128)])
+def test_non_finite_queries_give_nan(v1, T, d, fmt):
+    B, H, n = 2, 2, 300
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    c, _, _ = _random(g, B, n, H, d, v1, fmt)
+    q = [_bf(g, B, T, H if v1 else 4 * H, d) for _ in range(2)]
+    lam, logits = torch.tensor([0.4], device="cuda"), torch.randn(2 * H, generator=g, device="cuda")
+    lens = torch.tensor([n - T, 17], dtype=torch.int32, device="cuda")
+
+    def call():
+        out = da.tree_decode(*q, c, lam, 0.2, lens=lens) if v1 else da.v2_tree_decode(q[0], c, logits, lens=lens)
+        da.device_status()
+        return out
+    clean = call()
+    assert torch.isfinite(clean).all()
+    want = torch.zeros(clean.shape[:3], dtype=torch.bool, device="cuda")
+    for b, t, h, x in ((0, 0, 1, float("inf")), (1, T - 1, 0, float("-inf")), (1, T // 2, 1, float("nan"))):
+        q[0][b, t, h, 3] = x
+        want[b, t, h if v1 else h // 2] = True
+    out = call()
+    assert torch.equal(out.isnan().all(-1), want) and torch.equal(out.isnan().any(-1), want)
+    # (the others' query rows may be scaled by another power of two: a rounding of the output apart)
+    assert ((out - clean).abs() <= 2.0 ** -7 * clean.abs() + 2.0 ** -10)[~want].all()
