@@ -334,7 +334,7 @@ __device__ __forceinline__ void clean_values(uint8_t* slot, int kp, const TreeLe
 // The power of two (as its exponent) that puts a row's largest magnitude in [128, 256).
 __device__ __forceinline__ int e4m3_shift(float amax) {
   const int bexp = (__float_as_int(amax) >> 23) & 0xff;
-  return (amax > 0.f) ? max(-100, min(100, 134 - bexp)) : 0;
+  return (amax > 0.f) ? max(-120, min(100, 134 - bexp)) : 0;  // (-120: the largest finite rows)
 }
 
 // Eight bf16 values times 2^sh as two e4m3 terms each.  An infinity becomes a NaN (the conversion would

@@ -192,3 +192,22 @@ def test_non_finite_queries_give_nan(v1, T, d, fmt):
     assert torch.equal(out.isnan().all(-1), want) and torch.equal(out.isnan().any(-1), want)
     # (the others' query rows may be scaled by another power of two: a rounding of the output apart)
     assert ((out - clean).abs() <= 2.0 ** -7 * clean.abs() + 2.0 ** -10)[~want].all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8k", "fp8"])
+@pytest.mark.parametrize("T,d", [(2, 64), (20, 64), (40, 128)])
+def test_large_queries_meet_small_keys(T, d, fmt):
+    B, H, n, big = 1, 2, 200, 2.0 ** 115
+    g = torch.Generator(device="cuda").manual_seed(T)
+    c, keys, val = _random(g, B, n, H, d, True, fmt, 1 / big)
+    q1, q2 = ((_bf(g, B, T, H, d).float() * big).to(torch.bfloat16) for _ in range(2))
+    out = da.tree_decode(q1, q2, c, torch.tensor([0.37], device="cuda"), 0.3)
+    da.device_status()
+    ref, pre, spread, _, gain = oracle.tree_v1(q1.cpu(), q2.cpu(), *keys, val, [n - T], [T], None, float(np.float32(0.37)),
+                                               0.3, np.ones(2 * d), 1e-5)
+    e = E_MAP * spread
+    rms = np.sqrt((pre ** 2).mean(-1, keepdims=True) + 1e-5)
+    de = np.sqrt((e ** 2).mean(-1, keepdims=True))
+    bound = gain * (e + np.abs(pre) * de / np.maximum(rms - de, 1e-9))
+    over = np.abs(_np(out) - ref) - (bound + 2.0 ** -8 * (np.abs(ref) + bound))
+    assert over.max() <= 0, over.max()
