@@ -38,6 +38,27 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
+// A tensor of a call.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+// What a call writes may overlap nothing else of the call: rows are read and written by threads of their own.
+diffattn_status disjoint(const char* fn, const Span* written, int nw, const Span* read, int nr) {
+  for (int i = 0; i < nw; ++i) {
+    const Span& w = written[i];
+    if (!w.at || w.bytes == 0) continue;
+    for (int j = 0; j < nr; ++j)
+      if (read[j].at && read[j].bytes && overlap(w.at, w.bytes, read[j].at, read[j].bytes))
+        return fail(DIFFATTN_ERR_SHAPE, "%s: an output or the cache overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (written[j].at && written[j].bytes && overlap(w.at, w.bytes, written[j].at, written[j].bytes))
+        return fail(DIFFATTN_ERR_SHAPE, "%s: outputs or cache tensors overlap", fn);
+  }
+  return DIFFATTN_OK;
+}
+
 int sms_or_default() {
   const int s = dh::sms();
   return s > 0 ? s : 148;
@@ -142,11 +163,7 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
       return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
   if (!aligned(v, 16) || !aligned(vc, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
   {
-    // what is written may not overlap anything else of the call: every row is read and written by its own threads
-    struct Span {
-      const void* at;
-      size_t bytes;
-    } w[8], r[5];
+    Span w[8], r[5];
     int nw = 0, nr = 0;
     const size_t tok = static_cast<size_t>(B) * T, rows = static_cast<size_t>(B) * n * H;
     const size_t kes = fmt == DIFFATTN_CACHE_BF16 ? 2 : 1, ves = fmt == DIFFATTN_CACHE_FP8 ? 1 : 2;
@@ -162,15 +179,7 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
     r[nr++] = {v, tok * H * dv * 2};
     w[nw++] = {vc, rows * dv * ves};
     if (fmt == DIFFATTN_CACHE_FP8) w[nw++] = {vscales, rows * 4};
-    for (int i = 0; i < nw; ++i) {
-      if (w[i].bytes == 0) continue;
-      for (int j = 0; j < nr; ++j)
-        if (r[j].bytes && overlap(w[i].at, w[i].bytes, r[j].at, r[j].bytes))
-          return fail(DIFFATTN_ERR_SHAPE, "%s: an output or the cache overlaps an input", fn);
-      for (int j = 0; j < i; ++j)
-        if (w[j].bytes && overlap(w[i].at, w[i].bytes, w[j].at, w[j].bytes))
-          return fail(DIFFATTN_ERR_SHAPE, "%s: outputs or cache tensors overlap", fn);
-    }
+    if ((st = disjoint(fn, w, nw, r, nr)) != DIFFATTN_OK) return st;
   }
   da::AppendParams p;
   memset(&p, 0, sizeof(p));
@@ -239,8 +248,6 @@ diffattn_status keep(const char* fn, diffattn_cache_format fmt, int B, int A, in
   const float* ksc[2] = {kscales[0], kscales[1]};
   diffattn_status st = check_scales(fn, fmt, nk, n, one, ksc, vscales);
   if (st != DIFFATTN_OK) return st;
-  if (new_lens && overlap(new_lens, sizeof(int) * B, lens, sizeof(int) * B))
-    return fail(DIFFATTN_ERR_SHAPE, "%s: new_lens may not overlap lens", fn);
   da::KeepParams p;
   memset(&p, 0, sizeof(p));
   p.count = nk + 1;
@@ -252,9 +259,20 @@ diffattn_status keep(const char* fn, diffattn_cache_format fmt, int B, int A, in
     if (rb > 0x3fffffffll) return fail(DIFFATTN_ERR_SHAPE, "%s: too many heads", fn);
     p.row_bytes[i] = static_cast<int>(rb);
     if (!aligned(p.base[i], 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
-    for (int j = 0; n > 0 && j < i; ++j)  // (each moves by itself)
-      if (overlap(p.base[i], static_cast<size_t>(B) * n * p.row_bytes[i], p.base[j], static_cast<size_t>(B) * n * p.row_bytes[j]))
-        return fail(DIFFATTN_ERR_SHAPE, "%s: cache tensors overlap", fn);
+  }
+  {
+    // (every CTA of a sequence reads lens, path and nkeep for itself, one of them writes new_lens)
+    Span w[7];
+    int nw = 0;
+    const size_t rows = static_cast<size_t>(B) * n;
+    for (int i = 0; i <= nk; ++i) {
+      w[nw++] = {p.base[i], rows * p.row_bytes[i]};
+      if (fmt == DIFFATTN_CACHE_FP8) w[nw++] = {p.scales[i], rows * H * 4};
+    }
+    const size_t ints = sizeof(int) * static_cast<size_t>(B);
+    w[nw++] = {new_lens, ints};
+    const Span r[3] = {{lens, ints}, {path, ints * A}, {nkeep, ints}};
+    if ((st = disjoint(fn, w, nw, r, 3)) != DIFFATTN_OK) return st;
   }
   p.B = B;
   p.A = A;

@@ -756,9 +756,9 @@ diffattn_status diffattn_v2_tree_decode(diffattn_cache_format fmt, int B, int T,
  *              not in the cache ends the sequence's path there.
  *   nkeep    : device int32 [B], clamped to [0, A].
  *   lens     : device int32 [B], required.
- *   new_lens : device int32 [B] or NULL, receives lens[b] plus the nodes kept;
- *              may not overlap lens (ERR_SHAPE).
- * Other rows are left as they are; cache tensors that overlap -> ERR_SHAPE.
+ *   new_lens : device int32 [B] or NULL, receives lens[b] plus the nodes kept.
+ * Other rows are left as they are.  What is written (cache, row scales,
+ * new_lens) may not overlap anything else of the call (ERR_SHAPE).
  * Asynchronous on `stream`.
  */
 diffattn_status diffattn_cache_keep(diffattn_cache_format fmt, int B, int A, int H, int n, int d, void* k1_cache,

@@ -1,0 +1,40 @@
+"""Calls of the cache operators that are refused on the host (fake addresses: nothing is launched)."""
+
+import ctypes
+
+import pytest
+
+from differential_attention_03_gb300 import binding as da
+from differential_attention_03_gb300 import build
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return da.lib()
+
+
+P = ctypes.c_void_p
+AT = [P(0x100000 * (i + 1)) for i in range(24)]  # 1 MB apart; the tensors here are smaller
+
+
+def _overlap(L, status):
+    return status == da.ERR_SHAPE and b"overlap" in L.diffattn_last_error()
+
+
+def _keep(L, fmt=2, k=(AT[0], AT[1]), v=AT[2], sc=(AT[3], AT[4], AT[5]), lens=AT[6], path=AT[7], nkeep=AT[8],
+          new=AT[9]):
+    return L.diffattn_cache_keep(fmt, 4, 8, 2, 64, 64, *k, v, *sc, lens, path, nkeep, new, None)
+
+
+def test_keep_refuses_what_it_writes_over_what_it_reads(L):
+    # new_lens is written by one CTA of a sequence while others still read nkeep and path
+    for kw in (dict(new=AT[8]), dict(new=P(AT[8].value + 12)), dict(new=AT[7]), dict(new=P(AT[7].value + 4 * 31)),
+               dict(new=AT[6]), dict(new=AT[1]), dict(new=P(AT[2].value + 128)), dict(new=AT[5]),
+               dict(sc=(AT[3], AT[3], AT[5])), dict(sc=(AT[3], AT[4], AT[4])), dict(sc=(AT[0], AT[4], AT[5])),
+               dict(sc=(AT[3], AT[4], P(AT[2].value + 64))), dict(path=AT[0]), dict(lens=AT[4]), dict(nkeep=AT[2])):
+        assert _overlap(L, _keep(L, **kw)), kw
+    for kw in (dict(new=AT[8]), dict(k=(AT[0], AT[0]))):
+        assert _overlap(L, _keep(L, fmt=0, sc=(None, None, None), **kw)), kw
+    assert _overlap(L, L.diffattn_v2_cache_keep(2, 4, 8, 2, 64, 128, AT[0], AT[1], AT[2], AT[2], AT[6], AT[7], AT[8],
+                                                AT[9], None))
