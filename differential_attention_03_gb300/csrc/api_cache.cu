@@ -163,7 +163,7 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
       return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
   if (!aligned(v, 16) || !aligned(vc, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
   {
-    Span w[8], r[5];
+    Span w[8], r[8];
     int nw = 0, nr = 0;
     const size_t tok = static_cast<size_t>(B) * T, rows = static_cast<size_t>(B) * n * H;
     const size_t kes = fmt == DIFFATTN_CACHE_BF16 ? 2 : 1, ves = fmt == DIFFATTN_CACHE_FP8 ? 1 : 2;
@@ -177,6 +177,9 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
       }
     }
     r[nr++] = {v, tok * H * dv * 2};
+    r[nr++] = {positions, tok * 4};
+    r[nr++] = {lens, static_cast<size_t>(B) * 4};
+    r[nr++] = {ntok, static_cast<size_t>(B) * 4};
     w[nw++] = {vc, rows * dv * ves};
     if (fmt == DIFFATTN_CACHE_FP8) w[nw++] = {vscales, rows * 4};
     if ((st = disjoint(fn, w, nw, r, nr)) != DIFFATTN_OK) return st;

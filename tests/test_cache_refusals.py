@@ -38,3 +38,16 @@ def test_keep_refuses_what_it_writes_over_what_it_reads(L):
         assert _overlap(L, _keep(L, fmt=0, sc=(None, None, None), **kw)), kw
     assert _overlap(L, L.diffattn_v2_cache_keep(2, 4, 8, 2, 64, 128, AT[0], AT[1], AT[2], AT[2], AT[6], AT[7], AT[8],
                                                 AT[9], None))
+
+
+def _append(L, fmt=2, q=(AT[0], AT[1]), k=(AT[2], AT[3]), v=AT[4], pos=AT[5], lens=AT[6], ntok=AT[7], qo=(AT[8], AT[9]),
+            kc=(AT[10], AT[11]), vc=AT[12], sc=(AT[13], AT[14], AT[15]), scale=1.0):
+    f = ctypes.c_float
+    return L.diffattn_cache_append(fmt, 4, 8, 2, 64, 64, *q, *k, v, None, pos, lens, ntok, *qo, *kc, vc, f(scale),
+                                   f(scale), *sc, None)
+
+
+def test_append_refuses_outputs_over_its_index_tensors(L):
+    for name in ("pos", "lens", "ntok"):
+        for at in (AT[8], AT[9], AT[10], AT[11], AT[12], AT[13], AT[15], P(AT[8].value + 64)):
+            assert _overlap(L, _append(L, **{name: at})), (name, at)
