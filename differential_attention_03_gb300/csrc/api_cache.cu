@@ -495,6 +495,8 @@ diffattn_status diffattn_rope(diffattn_dtype dt, int B, int n, int d, int count,
         return fail(DIFFATTN_ERR_SHAPE, "%s: an output overlaps an input other than its own", fn);
       if (i < j && overlap(out[i], ni, out[j], nj) && ni && nj)
         return fail(DIFFATTN_ERR_SHAPE, "%s: outputs overlap", fn);
+      if (i == j && positions && ni && overlap(out[i], ni, positions, sizeof(int) * static_cast<size_t>(B) * n))
+        return fail(DIFFATTN_ERR_SHAPE, "%s: an output overlaps the positions", fn);
     }
   if (head_sum == 0) return dh::success();
   const long long tokens = static_cast<long long>(B) * n;

@@ -51,3 +51,11 @@ def test_append_refuses_outputs_over_its_index_tensors(L):
     for name in ("pos", "lens", "ntok"):
         for at in (AT[8], AT[9], AT[10], AT[11], AT[12], AT[13], AT[15], P(AT[8].value + 64)):
             assert _overlap(L, _append(L, **{name: at})), (name, at)
+
+
+def test_rope_refuses_an_output_over_the_positions(L):
+    spec = da.rope_spec(64)
+    for pos in (AT[1], P(AT[1].value + 256), AT[0]):
+        xs, outs = (P * 2)(AT[0].value, AT[3].value), (P * 2)(AT[0].value, AT[1].value)
+        assert _overlap(L, L.diffattn_rope(1, 2, 8, 64, 2, xs, (ctypes.c_int * 2)(2, 2), ctypes.byref(spec), pos, 0, outs,
+                                           None)), pos
