@@ -346,6 +346,20 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   if (workspace_bytes < need)
     return fail(DIFFATTN_ERR_SHAPE, "%s: workspace of %zu bytes, %zu needed", fn, workspace_bytes, need);
   if (!aligned(workspace, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  {
+    // (out is written when the queries and the cache have been read, beside what the second kernel reads)
+    const size_t rows = static_cast<size_t>(B) * n * H, tok = static_cast<size_t>(B) * T, ints = sizeof(int) * static_cast<size_t>(B);
+    const size_t kes = fmt == DIFFATTN_CACHE_BF16 ? 2 : 1, ves = fmt == DIFFATTN_CACHE_FP8 ? 1 : 2;
+    const size_t rowscales = fmt == DIFFATTN_CACHE_FP8 ? rows * 4 : 0;
+    const Span w[2] = {{out, tok * H * pairs * dv * 2}, {workspace, need}};
+    const Span r[12] = {{k1, rows * d * kes}, {k2, v2 ? 0 : rows * d * kes}, {v, rows * dv * ves},
+                        {kscales[0], rowscales}, {kscales[1], v2 ? 0 : rowscales}, {vscales, rowscales},
+                        {lens, ints}, {ntok, ints}, {mask, 8 * (static_cast<size_t>(mask_sb) * (B - 1) + T)},
+                        {p.lambda, 4}, {p.gamma, 4 * static_cast<size_t>(dv)},
+                        {p.lam_logits, p.sb < 0 || p.st < 0 ? 0 : 4 * static_cast<size_t>(p.sb * (B - 1) + p.st * (T - 1) + static_cast<long long>(H) * pairs)}};
+    const Span q[2] = {{q1, tok * H * pairs * (v2 ? 2 : 1) * d * 2}, {q2, tok * H * d * 2}};
+    if ((st = disjoint(fn, w, 2, r, 12)) != DIFFATTN_OK || (st = disjoint(fn, w + 1, 1, q, 2)) != DIFFATTN_OK) return st;
+  }
   int* status = nullptr;
   if ((st = dh::status_address(&status)) != DIFFATTN_OK) return st;
   // Neighbouring heads side by side: their rows of a token are neighbours in memory.

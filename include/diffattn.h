@@ -715,7 +715,9 @@ diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T
  *               softmax_scale <= 0 selects 1/sqrt(d), out [B, T, Hq/2, d].
  *   workspace : required, at least the workspace call's bytes, 16-byte
  *               aligned; partial states, nothing kept between calls.  Calls
- *               that can overlap need their own.
+ *               that can overlap need their own.  Neither it nor out may
+ *               overlap anything that the call reads, or one another
+ *               (ERR_SHAPE); out may reuse the queries' memory.
  * Rounding: scores, sums and accumulators are fp32.  A softmax weight meets
  * bf16 values as two bf16 terms (2^-16 of it) and e4m3 values as three e5m2
  * terms (2^-8.8 of it, or 2^-28 of the row's largest contribution).  Over e4m3

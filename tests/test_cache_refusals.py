@@ -59,3 +59,27 @@ def test_rope_refuses_an_output_over_the_positions(L):
         xs, outs = (P * 2)(AT[0].value, AT[3].value), (P * 2)(AT[0].value, AT[1].value)
         assert _overlap(L, L.diffattn_rope(1, 2, 8, 64, 2, xs, (ctypes.c_int * 2)(2, 2), ctypes.byref(spec), pos, 0, outs,
                                            None)), pos
+
+
+def _tree(L, fmt=2, q=(AT[0], AT[1]), k=(AT[2], AT[3]), v=AT[4], sc=(AT[5], AT[6], AT[7]), lens=AT[8], ntok=AT[9],
+          mask=AT[10], sb=4, lam=AT[11], gamma=AT[12], out=AT[13], ws=P(0x10000000)):
+    f = ctypes.c_float
+    return L.diffattn_tree_decode(fmt, 4, 4, 2, 64, 64, *q, *k, f(1), f(1), sc[0], sc[1], v, sc[2], lens, ntok, mask, sb,
+                                  lam, f(0.2), gamma, f(1e-5), out, ws, 1 << 30, None)
+
+
+def test_tree_refuses_outputs_over_what_it_reads(L):
+    for at in AT[2:13]:
+        assert _overlap(L, _tree(L, out=at)), at
+    for at in AT[:14]:
+        assert _overlap(L, _tree(L, ws=at)), at
+    assert _overlap(L, _tree(L, out=P(0x10000000 + 4096)))
+    assert _overlap(L, _tree(L, out=P(AT[10].value + 96)))  # (the last sequence's mask words)
+    f = ctypes.c_float
+
+    def v2(out=AT[5], ws=P(0x10000000), logits=AT[4]):
+        return L.diffattn_v2_tree_decode(0, 2, 4, 8, 2, 64, 128, AT[0], AT[1], f(1), None, AT[2], None, None, None, None, 0,
+                                         logits, 16, 4, f(0), out, ws, 1 << 30, None)
+    for kw in (dict(out=AT[1]), dict(out=AT[2]), dict(out=AT[4]), dict(out=P(AT[4].value + 112)), dict(ws=AT[0]),
+               dict(ws=AT[4]), dict(ws=AT[2])):
+        assert _overlap(L, v2(**kw)), kw
