@@ -124,8 +124,8 @@ diffattn_status check_scales(const char* fn, int fmt, int nk, int n, const float
                              const float* vscales) {
   if (fmt == DIFFATTN_CACHE_FP8K)
     for (int i = 0; i < nk; ++i)
-      if (!(std::isfinite(ks[i]) && ks[i] > 0.f))
-        return fail(DIFFATTN_ERR_SHAPE, "%s: key scales must be finite and positive", fn);
+      if (!(std::isfinite(ks[i]) && ks[i] > 0.f && std::isfinite(1.f / ks[i])))
+        return fail(DIFFATTN_ERR_SHAPE, "%s: key scales must be finite and positive, as must their reciprocals", fn);
   if (fmt == DIFFATTN_CACHE_FP8 && n > 0) {  // (an empty cache has no rows to point to)
     for (int i = 0; i < nk; ++i) {
       if (!kscales[i]) return fail(DIFFATTN_ERR_NULL, "%s: NULL key row scales", fn);

@@ -673,7 +673,8 @@ typedef enum {
  *   ntok      : device int32 [B], tokens of each sequence; NULL: T.  A token
  *               t >= ntok[b] leaves the cache as it is and gives zero queries;
  *               rows outside [0, n) are not written.
- *   k1_scale, k2_scale : FP8K only, finite and positive (else ERR_SHAPE).
+ *   k1_scale, k2_scale : FP8K only, finite and positive, and so that 1 / scale
+ *               is finite, as for the tree decode (else ERR_SHAPE).
  *   k1_scales, k2_scales, v_scales : FP8 only, device fp32 [B, H, n].
  * An unknown format -> ERR_DTYPE.  Tensors 16-byte aligned.  Asynchronous on
  * `stream`.  The V2 form has one key tensor and Hq query heads (d = 128).

@@ -83,3 +83,10 @@ def test_tree_refuses_outputs_over_what_it_reads(L):
     for kw in (dict(out=AT[1]), dict(out=AT[2]), dict(out=AT[4]), dict(out=P(AT[4].value + 112)), dict(ws=AT[0]),
                dict(ws=AT[4]), dict(ws=AT[2])):
         assert _overlap(L, v2(**kw)), kw
+
+
+def test_a_key_scale_without_a_reciprocal_is_refused(L):
+    # keys are multiplied by 1 / scale: an infinity would make a zero key NaN
+    for scale in (2.0 ** -129, 1e-45):
+        assert _append(L, fmt=1, scale=scale) == da.ERR_SHAPE, scale
+        assert b"reciprocal" in L.diffattn_last_error()
