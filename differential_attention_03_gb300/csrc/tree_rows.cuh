@@ -505,6 +505,8 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
         float rc = p.scale_log2;
         if (C::K8) rc *= valid ? qi[64 * map + r] : 0.f;
         if (FMT == kCacheFp8k) rc *= (map && !V2) ? p.k2_scale : p.k1_scale;
+        // (a finite number above zero, as hidden scores are minus infinity: below 2^-126 every score is as good as zero)
+        if (C::K8) rc = fminf(fmaxf(rc, 0x1p-126f), 0x1.fffffep127f);
         // ---- what the row sees of the drafted tokens
         const unsigned long long see = valid ? tree_sees(p, w.b, tok, w.len) : 0ull;
 
@@ -596,7 +598,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
                   pm = fmaxf(pm, __uint_as_float(x[c]));
               }
             }
-            if (!C::V8) pm *= rc;  // (rc > 0)
+            if (!C::V8) pm *= rc;  // (0 < rc < infinity)
             // ---- the row's maximum over the quarter's four warps
             float* xg = xm + (g & 1u) * 512;
             xg[qd * 128 + row] = pm;

@@ -211,3 +211,23 @@ def test_large_queries_meet_small_keys(T, d, fmt):
     bound = gain * (e + np.abs(pre) * de / np.maximum(rms - de, 1e-9))
     over = np.abs(_np(out) - ref) - (bound + 2.0 ** -8 * (np.abs(ref) + bound))
     assert over.max() <= 0, over.max()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8k", "fp8"])
+@pytest.mark.parametrize("T,d", [(3, 64), (20, 128), (40, 64)])
+def test_scores_that_underflow_weigh_alike(T, d, fmt):
+    # queries and keys of some 2^-100: every seen key weighs the same, a hidden one nothing
+    B, H, n, tiny = 1, 2, 200, 2.0 ** -100
+    g = torch.Generator(device="cuda").manual_seed(T)
+    c, _, val = _random(g, B, n, H, d, True, fmt, tiny)
+    q1, q2 = ((_bf(g, B, T, H, d).float() * tiny).to(torch.bfloat16) for _ in range(2))
+    out = da.tree_decode(q1, q2, c, torch.tensor([0.25], device="cuda"), 0.0)
+    da.device_status()
+    for t in range(T):
+        mean, size = val[0, :n - T + t + 1].mean(0), np.abs(val[0, :n - T + t + 1]).mean(0)  # [H, 2 d]
+        pre, e = 0.75 * mean, 1.25 * E_MAP * size
+        rms = np.sqrt((pre ** 2).mean(-1, keepdims=True) + 1e-5)
+        de = np.sqrt((e ** 2).mean(-1, keepdims=True))
+        bound = (e + np.abs(pre) * de / np.maximum(rms - de, 1e-9)) / rms
+        over = np.abs(_np(out)[0, t] - pre / rms) - (bound + 2.0 ** -8 * (np.abs(pre / rms) + bound))
+        assert over.max() <= 0, (t, over.max())
