@@ -241,15 +241,16 @@ diffattn_status keep(const char* fn, diffattn_cache_format fmt, int B, int A, in
     return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes B=%d A=%d H=%d n=%d d=%d", fn, B, A, H, n, d);
   if (A > da::kKeepMaxPath)
     return fail(DIFFATTN_ERR_UNSUPPORTED, "%s: paths of at most %d nodes (got %d)", fn, da::kKeepMaxPath, A);
-  if (B == 0 || H == 0) return dh::success();
+  if (B == 0) return dh::success();
   if (nk == 2 ? (d != 64 && d != 128) : d != 128)
     return fail(DIFFATTN_ERR_UNSUPPORTED, "%s: d = %d", fn, d);
-  if ((n > 0 && !vc) || !lens || !nkeep || (A > 0 && !path)) return fail(DIFFATTN_ERR_NULL, "%s: NULL pointer", fn);
+  const bool empty = n == 0 || H == 0;  // (no rows to point to; new_lens is written all the same)
+  if ((!empty && !vc) || !lens || !nkeep || (A > 0 && !path)) return fail(DIFFATTN_ERR_NULL, "%s: NULL pointer", fn);
   for (int i = 0; i < nk; ++i)
-    if (n > 0 && !kc[i]) return fail(DIFFATTN_ERR_NULL, "%s: NULL pointer", fn);
+    if (!empty && !kc[i]) return fail(DIFFATTN_ERR_NULL, "%s: NULL pointer", fn);
   const float one[2] = {1.f, 1.f};
   const float* ksc[2] = {kscales[0], kscales[1]};
-  diffattn_status st = check_scales(fn, fmt, nk, n, one, ksc, vscales);
+  diffattn_status st = check_scales(fn, fmt, nk, empty ? 0 : n, one, ksc, vscales);
   if (st != DIFFATTN_OK) return st;
   da::KeepParams p;
   memset(&p, 0, sizeof(p));

@@ -231,3 +231,13 @@ def test_scores_that_underflow_weigh_alike(T, d, fmt):
         bound = (e + np.abs(pre) * de / np.maximum(rms - de, 1e-9)) / rms
         over = np.abs(_np(out)[0, t] - pre / rms) - (bound + 2.0 ** -8 * (np.abs(pre / rms) + bound))
         assert over.max() <= 0, (t, over.max())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_keep_of_a_cache_without_heads_counts(fmt):
+    c = da.cache_v1(2, 20, 0, 64, fmt)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    new = i32([-7, -7])
+    assert da.cache_keep(c, i32([5, 19]), i32([[0, 2], [0, 1]]), i32([2, 2]), new_lens=new) is new
+    da.device_status()
+    assert new.tolist() == [7, 20]
