@@ -146,10 +146,12 @@ diffattn_status append(const char* fn, diffattn_cache_format fmt, int B, int T, 
   if (bad_format(fmt)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown cache format %d", fn, (int)fmt);
   if (B < 0 || T < 0 || Hq < 0 || H < 0 || n < 0 || d < 1)
     return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes B=%d T=%d Hq=%d H=%d n=%d d=%d", fn, B, T, Hq, H, n, d);
-  if (B == 0 || T == 0 || H == 0) return dh::success();
+  if (B == 0 || T == 0) return dh::success();
+  const bool hasq = q[0] != nullptr || (nk == 2 && q[1] != nullptr);
+  if (H == 0 && Hq > 0 && hasq) return fail(DIFFATTN_ERR_SHAPE, "%s: Hq = %d queries without a key head", fn, Hq);
+  if (H == 0) return dh::success();
   if (nk == 2 ? (d != 64 && d != 128) : d != 128)
     return fail(DIFFATTN_ERR_UNSUPPORTED, "%s: d = %d", fn, d);
-  const bool hasq = q[0] != nullptr || (nk == 2 && q[1] != nullptr);
   for (int i = 0; i < nk; ++i) {
     if (!k[i] || (n > 0 && !kc[i])) return fail(DIFFATTN_ERR_NULL, "%s: NULL key pointer", fn);
     if (hasq && (!q[i] || !qo[i])) return fail(DIFFATTN_ERR_NULL, "%s: NULL query pointer", fn);

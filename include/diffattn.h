@@ -677,7 +677,8 @@ typedef enum {
  *               is finite, as for the tree decode (else ERR_SHAPE).
  *   k1_scales, k2_scales, v_scales : FP8 only, device fp32 [B, H, n].
  * An unknown format -> ERR_DTYPE.  Tensors 16-byte aligned.  Asynchronous on
- * `stream`.  The V2 form has one key tensor and Hq query heads (d = 128).
+ * `stream`.  The V2 form has one key tensor and Hq query heads (d = 128); queries
+ * for a cache without key heads -> ERR_SHAPE.
  */
 diffattn_status diffattn_cache_append(diffattn_cache_format fmt, int B, int T, int H, int n, int d, const void* q1,
                                       const void* q2, const void* k1, const void* k2, const void* v,

@@ -90,3 +90,13 @@ def test_a_key_scale_without_a_reciprocal_is_refused(L):
     for scale in (2.0 ** -129, 1e-45):
         assert _append(L, fmt=1, scale=scale) == da.ERR_SHAPE, scale
         assert b"reciprocal" in L.diffattn_last_error()
+
+
+def test_append_refuses_queries_without_a_key_head(L):
+    f = ctypes.c_float
+
+    def v2(Hq, q):
+        return L.diffattn_v2_cache_append(0, 1, 2, Hq, 0, 8, 128, q, None, None, None, None, None, None, AT[1], None, None,
+                                          f(1), None, None, None)
+    assert v2(4, AT[0]) == da.ERR_SHAPE and b"key head" in L.diffattn_last_error()
+    assert v2(4, None) == da.OK and v2(0, AT[0]) == da.OK
