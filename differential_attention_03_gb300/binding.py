@@ -858,9 +858,20 @@ def v2_layer_forward(x, w_qkvl, w_o, Hq: int, Hkv: int, causal: bool = True, out
 
 # ----------------------------------------------------------------------------- positions and caches
 class RopeSpec(ctypes.Structure):
-    """A rotation, as rope_spec or rope_from_frequencies makes it (immutable: they are shared)."""
+    """A rotation, as rope_spec or rope_from_frequencies makes it."""
     _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("mult", ctypes.c_float),
                 ("turns", ctypes.c_ulonglong * 64)]
+
+
+class _SharedRopeSpec(RopeSpec):
+    """What rope_spec hands to every caller of the same arguments: its fields cannot be set."""
+
+    def __setattr__(self, name, value):
+        raise AttributeError("rope_spec's rotations are shared; RopeSpec.from_buffer_copy(spec) is one to change")
+
+    @property
+    def turns(self):
+        return RopeSpec.turns.__get__(self)[:]
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -875,14 +886,14 @@ def rope_spec(rot_dim: int, base: float = 10000.0, interleaved: bool = False, sc
     interleaved: pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2).  scaling: "none", "linear"
     (theta / factor), "ntk" (base factor^(rot_dim / (rot_dim - 2))) or "yarn" (between the two, by the
     turns a pair makes over original_context positions; the rotated values times 0.1 ln(factor) + 1).
-    Host only.
+    Host only.  The same arguments give the same object, which cannot be changed.
     """
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     spec = RopeSpec()
     _check(lib().diffattn_rope_init(ctypes.byref(spec), rot_dim, 1 if interleaved else 0, base, ROPE_SCALINGS[scaling],
                                     factor, original_context, beta_fast, beta_slow))
-    return spec
+    return _SharedRopeSpec.from_buffer_copy(spec)
 
 
 def rope_from_frequencies(frequencies, interleaved: bool = False, mult: float = 1.0) -> RopeSpec:

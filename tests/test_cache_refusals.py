@@ -100,3 +100,16 @@ def test_append_refuses_queries_without_a_key_head(L):
                                           f(1), None, None, None)
     assert v2(4, AT[0]) == da.ERR_SHAPE and b"key head" in L.diffattn_last_error()
     assert v2(4, None) == da.OK and v2(0, AT[0]) == da.OK
+
+
+def test_a_shared_rotation_cannot_be_changed(L):
+    spec = da.rope_spec(64, base=777.0)
+    before = bytes(spec)
+    for name, x in (("mult", 2.0), ("rot_dim", 2), ("interleaved", 1), ("turns", (ctypes.c_ulonglong * 64)())):
+        with pytest.raises(AttributeError):
+            setattr(spec, name, x)
+    spec.turns[1] = 5  # (a copy's)
+    assert da.rope_spec(64, base=777.0) is spec and bytes(spec) == before
+    own = da.RopeSpec.from_buffer_copy(spec)
+    own.mult, own.turns[1] = 2.0, 5
+    assert (own.mult, own.turns[1]) == (2.0, 5) and bytes(spec) == before
