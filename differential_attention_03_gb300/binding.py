@@ -983,7 +983,8 @@ class KVCache:
 
     fmt: "bf16"; "fp8k" (e4m3 keys, one scale a tensor: k1_scale, k2_scale; bf16 values); "fp8" (e4m3
     keys and values, fp32 scales a row: k1_scales, k2_scales, v_scales [B, H, n]).  e4m3 tensors are
-    torch.float8_e4m3fn or their bytes as torch.uint8.  cache_v1 and cache_v2 allocate one.
+    torch.float8_e4m3fn or their bytes as torch.uint8.  cache_v1 and cache_v2 allocate one.  A tensor may
+    be replaced by one of the same type, shape and device, a key scale by another number; the rest is fixed.
     """
 
     __slots__ = ("fmt", "code", "k1", "k2", "v", "k1_scale", "k2_scale", "k1_scales", "k2_scales", "v_scales", "B", "n",
@@ -995,9 +996,8 @@ class KVCache:
             raise ValueError(f"the cache format must be one of {sorted(CACHE_FORMATS)}, got {fmt!r}")
         if not k1.is_cuda:
             raise ValueError("k1 must be a CUDA tensor")
-        self.fmt, self.code = fmt, CACHE_FORMATS[fmt]
-        self.B, self.n, self.H, self.d = B, n, H, d = k1.shape
-        self.dev = dev = k1.get_device()
+        B, n, H, d = k1.shape
+        dev = k1.get_device()
         kt, vt = (torch.bfloat16 if fmt == "bf16" else k1.dtype), (v.dtype if fmt == "fp8" else torch.bfloat16)
         if (fmt != "bf16" and kt not in _CODES) or (fmt == "fp8" and vt not in _CODES):
             raise ValueError("e4m3 tensors must be torch.float8_e4m3fn or torch.uint8")
@@ -1012,9 +1012,21 @@ class KVCache:
                     if x is None:
                         raise ValueError(f"an fp8 cache needs {name}")
                     _on(x, name, torch.float32, (B, H, n), dev)
-        self.k1, self.k2, self.v = k1, k2, v
-        self.k1_scale, self.k2_scale = float(k1_scale), float(k2_scale)
-        self.k1_scales, self.k2_scales, self.v_scales = k1_scales, k2_scales, v_scales
+        for name, x in zip(KVCache.__slots__, (fmt, CACHE_FORMATS[fmt], k1, k2, v, float(k1_scale), float(k2_scale),
+                                               k1_scales, k2_scales, v_scales, B, n, H, d, dev)):
+            object.__setattr__(self, name, x)
+
+    def __setattr__(self, name, value):
+        # (the calls take the shapes for checked, so that a tensor of another would be read past its end)
+        if hasattr(self, name):  # (else a copy is being made)
+            old = getattr(self, name)
+            if name in ("k1_scale", "k2_scale"):
+                value = float(value)
+            elif isinstance(old, torch.Tensor):
+                _on(value, name, old.dtype, old.shape, self.dev)
+            else:
+                raise AttributeError(f"{name} of a cache cannot be set")
+        object.__setattr__(self, name, value)
 
 
 def _new_cache(B, n, H, d, dv, two, fmt, device, scales):

@@ -8,6 +8,7 @@ contribution is below 2^-11 of the sum for n up to 2^17).  The norm multiplies E
 the change of the row's rms; the output rounds to bf16.
 """
 
+import copy
 import math
 
 import numpy as np
@@ -241,3 +242,21 @@ def test_keep_of_a_cache_without_heads_counts(fmt):
     assert da.cache_keep(c, i32([5, 19]), i32([[0, 2], [0, 1]]), i32([2, 2]), new_lens=new) is new
     da.device_status()
     assert new.tolist() == [7, 20]
+
+
+def test_a_cache_keeps_its_shapes():
+    c = da.cache_v1(1, 8, 2, 64, "fp8")
+    other = torch.ones((1, 8, 2), device="cuda").transpose(1, 2).contiguous()
+    c.k1_scales, c.k1_scale = other, 2
+    assert c.k1_scales is other and c.k1_scale == 2.0
+    for name, x in (("k1", c.k1[:, :4].contiguous()), ("v", c.k1), ("k2", c.k2.cpu()), ("v_scales", other.double()),
+                    ("k2", c.k2.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            setattr(c, name, x)
+    for name, x in (("n", 9), ("H", 4), ("fmt", "bf16"), ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(c, name, x)
+    again = copy.copy(c)
+    assert again.k1 is c.k1 and again.n == 8 and copy.deepcopy(c).v.shape == c.v.shape
+    with pytest.raises(AttributeError):
+        da.cache_v2(1, 8, 2, 128).k2 = torch.zeros((1, 8, 2, 128), device="cuda", dtype=torch.bfloat16)
