@@ -318,7 +318,7 @@ TreeShape tree_shape(int B, int T, int H, int pairs) {
 
 size_t tree_workspace(int B, int T, int H, int pairs, int dv) {
   const TreeShape s = tree_shape(B, T, H, pairs);
-  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, da::tree_subs(s.R), dv) * sizeof(float) +
+  return (static_cast<size_t>(s.units) + kTreeMaxCtas) * da::tree_state_floats(s.R, da::tree_subs_most(s.R), dv) * sizeof(float) +
          16;  // (states start on 32 bytes)
 }
 
@@ -397,7 +397,7 @@ diffattn_status tree(const char* fn, bool v2, diffattn_cache_format fmt, int B, 
   p.ppt = sh.ppt;
   p.mt = sh.mt;
   p.R = sh.R;
-  p.subs = da::tree_subs(sh.R);
+  p.subs = da::tree_subs(fmt, dv, sh.R);
   p.ws = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 31) & ~uintptr_t(31));
   p.status = status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

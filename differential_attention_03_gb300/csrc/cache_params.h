@@ -101,8 +101,14 @@ constexpr int kTreeValueKeys = 64;  // keys of a value box of the tree decode, a
 
 constexpr int kTreeRows = 64;  // rows of one map in a row tile of the tree decode
 
-// Subsets of a CTA's keys that keep their own partial state, at most (the fewer rows, the more).
-__host__ __device__ constexpr int tree_subs(int R) { return R <= 8 ? 4 : R <= 32 ? 2 : 1; }
+// Subsets of a CTA's keys that keep their own partial state: over fp8 caches tree_cols_kernel's streams, over
+// fp8k ones both halves of a tile where tree_rows_kernel splits it.
+__host__ __device__ constexpr int tree_subs(int fmt, int dv, int R) {
+  if (fmt == kCacheFp8) return R <= 8 ? 4 : R <= 16 ? 2 : 1;
+  return fmt == kCacheFp8k && dv == 128 && R <= 32 ? 2 : 1;
+}
+// The most of any format: what the workspace has room for.
+__host__ __device__ constexpr int tree_subs_most(int R) { return R <= 8 ? 4 : R <= 32 ? 2 : 1; }
 
 // A partial state of the tree decode: (maximum, sum) of R rows of both maps, for each subset, then their
 // O from this float on (32-byte sectors), and its floats in all.

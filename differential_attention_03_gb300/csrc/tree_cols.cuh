@@ -124,6 +124,7 @@ struct TreeColsCfg {
   static constexpr uint32_t IDESC_P3 = idesc_e4m3(128, COLS) | kIdescB5 | (3u << 15);
   static constexpr int NSOFT = 16;              // softmax warps
   static constexpr int NARR = NSOFT / NSTREAM;  // of a stream
+  static_assert(NSTREAM == tree_subs(kCacheFp8, DV, TP), "a partial state a stream");
   static constexpr int NTHREADS = (4 + NSOFT) * 32;
   static_assert(TP == 8 || TP == 16 || TP == 32, "columns of a map");
   static_assert(SMEM_BYTES <= 232448, "shared memory");

@@ -13,10 +13,9 @@ namespace da {
 // both, and tokens as rows, with deeper rings, comes nearer to it (bf16, one
 // token: V1 d64 323 against 336, V1 d128 312 against 320).
 template <int D, bool V2, int FMT>
-cudaError_t launch_tree(TreeParams p, cudaStream_t s) {
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
   if constexpr (FMT == kCacheFp8) {
     if (p.R <= 32) {
-      p.subs = p.R <= 8 ? 4 : p.R <= 16 ? 2 : 1;
       if (p.R <= 8) return launch_tree_cols<D, V2, 8>(p, s);
       if (p.R <= 16) return launch_tree_cols<D, V2, 16>(p, s);
       return launch_tree_cols<D, V2, 32>(p, s);

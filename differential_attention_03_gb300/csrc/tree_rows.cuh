@@ -140,6 +140,7 @@ template <int D, bool V2, int FMT, bool SPLIT>
 __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeRowsCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
+  static_assert(!SPLIT || FMT == kCacheFp8k, "only 8-bit keys with bf16 values stand twice");
   grid_dep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -471,7 +472,6 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
             if (in) {
               uint8_t* dst = q + (ch >> 3) * (C::QROWS * 128) + swizzled<128>(qr, ch & 7);
               *reinterpret_cast<uint4*>(dst) = x;
-              if (SPLIT) *reinterpret_cast<uint4*>(dst + 32 * 128) = x;  // (the second copy of the rows)
             }
           } else {
             // The row scaled by a power of two that puts its largest magnitude in [128, 256), in
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
               uint8_t* dst = q + swizzled<C::KBOXB>(qr, ch >> 1) + 8 * (ch & 1);
               *reinterpret_cast<uint2*>(dst) = hi;
               *reinterpret_cast<uint2*>(dst + C::Q_TERM) = lo8;
-              if (SPLIT) {
+              if (SPLIT) {  // (the second copy of the rows)
                 *reinterpret_cast<uint2*>(dst + 32 * C::KROW) = hi;
                 *reinterpret_cast<uint2*>(dst + 32 * C::KROW + C::Q_TERM) = lo8;
               }
@@ -753,20 +753,11 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
 // token, 253 us split, 289 not).  Larger ones don't, as the second state of every row is written and merged
 // (bf16 V1 d128 B4 H12 T16 n8192 79.0 us split, 76.9 not; T32 90.3 and 85.4; d64 B8 H16 T1 n32768 311 and 307).
 template <int D, bool V2, int FMT>
-constexpr bool tree_splits(int R) {
-  return FMT == kCacheFp8k && (V2 ? D : 2 * D) == 128 && R <= 32;
-}
-
-template <int D, bool V2, int FMT>
-cudaError_t launch_tree_rows(TreeParams p, cudaStream_t s) {
+cudaError_t launch_tree_rows(const TreeParams& p, cudaStream_t s) {
   using C = TreeRowsCfg<D, V2, FMT>;
   void (*kern)(TreeParams) = tree_rows_kernel<D, V2, FMT, false>;
-  p.subs = 1;
-  if constexpr (tree_splits<D, V2, FMT>(1)) {
-    if (tree_splits<D, V2, FMT>(p.R)) {
-      kern = tree_rows_kernel<D, V2, FMT, true>;
-      p.subs = 2;
-    }
+  if constexpr (FMT == kCacheFp8k && C::DV == 128) {
+    if (p.subs == 2) kern = tree_rows_kernel<D, V2, FMT, true>;
   }
   return launch_tree_pair<C::DV, V2>(kern, C::NTHREADS, C::SMEM_BYTES, C::V8 ? 1.f / kTreeValueMult : 1.f, p, s);
 }

@@ -715,7 +715,8 @@ diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T
  *   lambda, lambda_init, gamma, eps, out [B, T, H, 2d] : as for
  *               diffattn_decode.  V2: lam_logits at b * sb + t * st + pair,
  *               softmax_scale <= 0 selects 1/sqrt(d), out [B, T, Hq/2, d].
- *   workspace : required, at least the workspace call's bytes, 16-byte
+ *   workspace : required, at least the workspace call's bytes (room for any
+ *               format; each keeps one to four partial states a row), 16-byte
  *               aligned; partial states, nothing kept between calls.  Calls
  *               that can overlap need their own.  Neither it nor out may
  *               overlap anything that the call reads, or one another
