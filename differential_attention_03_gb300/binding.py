@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -987,8 +988,8 @@ class KVCache:
     be replaced by one of the same type, shape and device, a key scale by another number; the rest is fixed.
     """
 
-    __slots__ = ("fmt", "code", "k1", "k2", "v", "k1_scale", "k2_scale", "k1_scales", "k2_scales", "v_scales", "B", "n",
-                 "H", "d", "dev")
+    __slots__ = ("_fmt", "_code", "_k1", "_k2", "_v", "k1_scale", "k2_scale", "_k1_scales", "_k2_scales", "_v_scales",
+                 "_B", "_n", "_H", "_d", "_dev")
 
     def __init__(self, fmt, k1, k2, v, k1_scale: float = 1.0, k2_scale: float = 1.0, k1_scales=None, k2_scales=None,
                  v_scales=None):
@@ -1012,21 +1013,29 @@ class KVCache:
                     if x is None:
                         raise ValueError(f"an fp8 cache needs {name}")
                     _on(x, name, torch.float32, (B, H, n), dev)
-        for name, x in zip(KVCache.__slots__, (fmt, CACHE_FORMATS[fmt], k1, k2, v, float(k1_scale), float(k2_scale),
-                                               k1_scales, k2_scales, v_scales, B, n, H, d, dev)):
-            object.__setattr__(self, name, x)
+        self._fmt, self._code = fmt, CACHE_FORMATS[fmt]
+        self._B, self._n, self._H, self._d, self._dev = B, n, H, d, dev
+        self._k1, self._k2, self._v = k1, k2, v
+        self.k1_scale, self.k2_scale = float(k1_scale), float(k2_scale)
+        self._k1_scales, self._k2_scales, self._v_scales = k1_scales, k2_scales, v_scales
 
-    def __setattr__(self, name, value):
-        # (the calls take the shapes for checked, so that a tensor of another would be read past its end)
-        if hasattr(self, name):  # (else a copy is being made)
-            old = getattr(self, name)
-            if name in ("k1_scale", "k2_scale"):
-                value = float(value)
-            elif isinstance(old, torch.Tensor):
-                _on(value, name, old.dtype, old.shape, self.dev)
-            else:
-                raise AttributeError(f"{name} of a cache cannot be set")
-        object.__setattr__(self, name, value)
+
+def _replaceable(name):
+    """A cache's tensor, to be replaced by its like alone: the calls take the shapes for checked."""
+    def put(self, x):
+        old = getattr(self, "_" + name)
+        if old is None:
+            raise AttributeError(f"this cache has no {name}")
+        _on(x, name, old.dtype, old.shape, self._dev)
+        setattr(self, "_" + name, x)
+    return property(operator.attrgetter("_" + name), put)
+
+
+for _name in ("k1", "k2", "v", "k1_scales", "k2_scales", "v_scales"):
+    setattr(KVCache, _name, _replaceable(_name))
+for _name in ("fmt", "code", "B", "n", "H", "d", "dev"):
+    setattr(KVCache, _name, property(operator.attrgetter("_" + _name)))
+del _name
 
 
 def _new_cache(B, n, H, d, dv, two, fmt, device, scales):
@@ -1054,10 +1063,10 @@ def cache_v2(B: int, n: int, Hkv: int, d: int, fmt: str = "bf16", device="cuda",
 
 
 def _need_kind(cache, two):
-    if (cache.k2 is not None) != two:
+    if (cache._k2 is not None) != two:
         raise ValueError("a V1 cache (k1 and k2) is needed" if two else "a V2 cache (one key tensor) is needed")
-    if cache.dev != torch.cuda.current_device():
-        raise ValueError(f"the cache is on device {cache.dev}, the current device is {torch.cuda.current_device()}")
+    if cache._dev != torch.cuda.current_device():
+        raise ValueError(f"the cache is on device {cache._dev}, the current device is {torch.cuda.current_device()}")
 
 
 def _int32(t, name, shape, dev):
@@ -1082,9 +1091,9 @@ def cache_append(cache: KVCache, k1, k2, v, q1=None, q2=None, rope=None, positio
     """
     _need_kind(cache, True)
     B, T, H, d = k1.shape
-    dev, bf = cache.dev, torch.bfloat16
-    if (B, H, d) != (cache.B, cache.H, cache.d):
-        raise ValueError(f"keys {tuple(k1.shape)} do not fit a cache of B={cache.B}, H={cache.H}, d={cache.d}")
+    dev, bf = cache._dev, torch.bfloat16
+    if (B, H, d) != (cache._B, cache._H, cache._d):
+        raise ValueError(f"keys {tuple(k1.shape)} do not fit a cache of B={cache._B}, H={cache._H}, d={cache._d}")
     shp = (B, T, H, d)
     _on(k1, "k1", bf, shp, dev)
     _on(k2, "k2", bf, shp, dev)
@@ -1099,11 +1108,11 @@ def cache_append(cache: KVCache, k1, k2, v, q1=None, q2=None, rope=None, positio
         _on(q1_out, "q1_out", bf, shp, dev)
         _on(q2_out, "q2_out", bf, shp, dev)
     _check(lib().diffattn_cache_append(
-        cache.code, B, T, H, cache.n, d, _addr(q1), _addr(q2), k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
+        cache._code, B, T, H, cache._n, d, _addr(q1), _addr(q2), k1.data_ptr(), k2.data_ptr(), v.data_ptr(),
         None if rope is None else ctypes.byref(rope), _int32(positions, "positions", (B, T), dev),
         _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(q1_out), _addr(q2_out),
-        cache.k1.data_ptr(), cache.k2.data_ptr(), cache.v.data_ptr(), cache.k1_scale, cache.k2_scale,
-        _addr(cache.k1_scales), _addr(cache.k2_scales), _addr(cache.v_scales), _stream(stream)))
+        cache._k1.data_ptr(), cache._k2.data_ptr(), cache._v.data_ptr(), cache.k1_scale, cache.k2_scale,
+        _addr(cache._k1_scales), _addr(cache._k2_scales), _addr(cache._v_scales), _stream(stream)))
     return None if q1 is None else (q1_out, q2_out)
 
 
@@ -1112,9 +1121,9 @@ def v2_cache_append(cache: KVCache, k, v, q=None, rope=None, positions=None, len
     """cache_append for a V2 cache: k, v bf16 [B, T, Hkv, d]; q [B, T, Hq, d] or None.  Returns q_out."""
     _need_kind(cache, False)
     B, T, H, d = k.shape
-    dev, bf = cache.dev, torch.bfloat16
-    if (B, H, d) != (cache.B, cache.H, cache.d):
-        raise ValueError(f"keys {tuple(k.shape)} do not fit a cache of B={cache.B}, Hkv={cache.H}, d={cache.d}")
+    dev, bf = cache._dev, torch.bfloat16
+    if (B, H, d) != (cache._B, cache._H, cache._d):
+        raise ValueError(f"keys {tuple(k.shape)} do not fit a cache of B={cache._B}, Hkv={cache._H}, d={cache._d}")
     _on(k, "k", bf, (B, T, H, d), dev)
     _on(v, "v", bf, (B, T, H, d), dev)
     Hq = 0
@@ -1124,10 +1133,10 @@ def v2_cache_append(cache: KVCache, k, v, q=None, rope=None, positions=None, len
         q_out = _like(q, stream) if q_out is None else q_out
         _on(q_out, "q_out", bf, (B, T, Hq, d), dev)
     _check(lib().diffattn_v2_cache_append(
-        cache.code, B, T, Hq, H, cache.n, d, _addr(q), k.data_ptr(), v.data_ptr(),
+        cache._code, B, T, Hq, H, cache._n, d, _addr(q), k.data_ptr(), v.data_ptr(),
         None if rope is None else ctypes.byref(rope), _int32(positions, "positions", (B, T), dev),
-        _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(q_out), cache.k1.data_ptr(),
-        cache.v.data_ptr(), cache.k1_scale, _addr(cache.k1_scales), _addr(cache.v_scales), _stream(stream)))
+        _int32(lens, "lens", (B,), dev), _int32(ntok, "ntok", (B,), dev), _addr(q_out), cache._k1.data_ptr(),
+        cache._v.data_ptr(), cache.k1_scale, _addr(cache._k1_scales), _addr(cache._v_scales), _stream(stream)))
     return None if q is None else q_out
 
 
@@ -1138,8 +1147,8 @@ def cache_keep(cache: KVCache, lens, path, nkeep, new_lens=None, stream=None) ->
     node numbers, A <= 64; lens, nkeep: int32 [B].  Works on V1 and V2 caches.  Returns new_lens,
     int32 [B]: lens plus the nodes kept.
     """
-    _need_kind(cache, cache.k2 is not None)
-    B, dev = cache.B, cache.dev
+    _need_kind(cache, cache._k2 is not None)
+    B, dev = cache._B, cache._dev
     if path.dim() != 2:
         raise ValueError(f"path must be [B, A], got {tuple(path.shape)}")
     A = path.shape[1]
@@ -1147,14 +1156,14 @@ def cache_keep(cache: KVCache, lens, path, nkeep, new_lens=None, stream=None) ->
         new_lens = _like(lens, stream)
     a = (_int32(lens, "lens", (B,), dev), _int32(path, "path", (B, A), dev), _int32(nkeep, "nkeep", (B,), dev),
          _int32(new_lens, "new_lens", (B,), dev), _stream(stream))
-    if cache.k2 is not None:
+    if cache._k2 is not None:
         _check(lib().diffattn_cache_keep(
-            cache.code, B, A, cache.H, cache.n, cache.d, cache.k1.data_ptr(), cache.k2.data_ptr(), cache.v.data_ptr(),
-            _addr(cache.k1_scales), _addr(cache.k2_scales), _addr(cache.v_scales), *a))
+            cache._code, B, A, cache._H, cache._n, cache._d, cache._k1.data_ptr(), cache._k2.data_ptr(), cache._v.data_ptr(),
+            _addr(cache._k1_scales), _addr(cache._k2_scales), _addr(cache._v_scales), *a))
     else:
         _check(lib().diffattn_v2_cache_keep(
-            cache.code, B, A, cache.H, cache.n, cache.d, cache.k1.data_ptr(), cache.v.data_ptr(),
-            _addr(cache.k1_scales), _addr(cache.v_scales), *a))
+            cache._code, B, A, cache._H, cache._n, cache._d, cache._k1.data_ptr(), cache._v.data_ptr(),
+            _addr(cache._k1_scales), _addr(cache._v_scales), *a))
     return new_lens
 
 
@@ -1201,9 +1210,9 @@ def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=Non
     """
     _need_kind(cache, True)
     B, T, H, d = q1.shape
-    dev, bf = cache.dev, torch.bfloat16
-    if (B, H, d) != (cache.B, cache.H, cache.d):
-        raise ValueError(f"queries {tuple(q1.shape)} do not fit a cache of B={cache.B}, H={cache.H}, d={cache.d}")
+    dev, bf = cache._dev, torch.bfloat16
+    if (B, H, d) != (cache._B, cache._H, cache._d):
+        raise ValueError(f"queries {tuple(q1.shape)} do not fit a cache of B={cache._B}, H={cache._H}, d={cache._d}")
     _on(q1, "q1", bf, (B, T, H, d), dev)
     _on(q2, "q2", bf, (B, T, H, d), dev)
     _on(lam, "lambda", torch.float32, (1,), dev)
@@ -1217,9 +1226,9 @@ def tree_decode(q1, q2, cache: KVCache, lam, lambda_init_value: float, gamma=Non
     workspace = _tree_workspace(workspace, need, dev, q1, stream)  # (alive until the kernels are in their stream)
     wp, wn = _ws_args(workspace, need)
     _check(lib().diffattn_tree_decode(
-        cache.code, B, T, H, cache.n, d, q1.data_ptr(), q2.data_ptr(), cache.k1.data_ptr(), cache.k2.data_ptr(),
-        cache.k1_scale, cache.k2_scale, _addr(cache.k1_scales), _addr(cache.k2_scales), cache.v.data_ptr(),
-        _addr(cache.v_scales), *a, lam.data_ptr(), lambda_init_value, _addr(gamma), eps, out.data_ptr(), wp, wn,
+        cache._code, B, T, H, cache._n, d, q1.data_ptr(), q2.data_ptr(), cache._k1.data_ptr(), cache._k2.data_ptr(),
+        cache.k1_scale, cache.k2_scale, _addr(cache._k1_scales), _addr(cache._k2_scales), cache._v.data_ptr(),
+        _addr(cache._v_scales), *a, lam.data_ptr(), lambda_init_value, _addr(gamma), eps, out.data_ptr(), wp, wn,
         _stream(stream)))
     return out
 
@@ -1232,9 +1241,9 @@ def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=Non
     """
     _need_kind(cache, False)
     B, T, Hq, d = q.shape
-    dev, bf, G = cache.dev, torch.bfloat16, Hq // 2
-    if (B, d) != (cache.B, cache.d):
-        raise ValueError(f"queries {tuple(q.shape)} do not fit a cache of B={cache.B}, d={cache.d}")
+    dev, bf, G = cache._dev, torch.bfloat16, Hq // 2
+    if (B, d) != (cache._B, cache._d):
+        raise ValueError(f"queries {tuple(q.shape)} do not fit a cache of B={cache._B}, d={cache._d}")
     _on(q, "q", bf, (B, T, Hq, d), dev)
     sb, st = (T * G, G) if lam_logits.dim() == 3 else (G, 0) if lam_logits.dim() == 2 else (0, 0)
     _on(lam_logits, "lam_logits", torch.float32, ((B, T, G), (B, G), (G,))[3 - lam_logits.dim()]
@@ -1243,12 +1252,12 @@ def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=Non
     if out is None:
         out = _empty((B, T, G, d), bf, q.device, stream)
     _on(out, "out", bf, (B, T, G, d), dev)
-    need = v2_tree_decode_workspace_bytes(B, T, Hq, cache.H, d)
+    need = v2_tree_decode_workspace_bytes(B, T, Hq, cache._H, d)
     workspace = _tree_workspace(workspace, need, dev, q, stream)
     wp, wn = _ws_args(workspace, need)
     _check(lib().diffattn_v2_tree_decode(
-        cache.code, B, T, Hq, cache.H, cache.n, d, q.data_ptr(), cache.k1.data_ptr(), cache.k1_scale,
-        _addr(cache.k1_scales), cache.v.data_ptr(), _addr(cache.v_scales), *a, lam_logits.data_ptr(), sb, st,
+        cache._code, B, T, Hq, cache._H, cache._n, d, q.data_ptr(), cache._k1.data_ptr(), cache.k1_scale,
+        _addr(cache._k1_scales), cache._v.data_ptr(), _addr(cache._v_scales), *a, lam_logits.data_ptr(), sb, st,
         float(softmax_scale), out.data_ptr(), wp, wn, _stream(stream)))
     return out
 
