@@ -260,3 +260,31 @@ def test_a_cache_keeps_its_shapes():
     assert again.k1 is c.k1 and again.n == 8 and copy.deepcopy(c).v.shape == c.v.shape
     with pytest.raises(AttributeError):
         da.cache_v2(1, 8, 2, 128).k2 = torch.zeros((1, 8, 2, 128), device="cuda", dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8k", "fp8"])
+@pytest.mark.parametrize("v1,d,H", [(True, 64, 3), (False, 128, 16)])
+def test_keep_moves_long_paths(v1, d, H, fmt):
+    B, n, A = 4, 100, 64
+    g = torch.Generator(device="cuda").manual_seed(H)
+    c, _, _ = _random(g, B, n, H, d, v1, fmt)
+    tensors = [t for t in (c.k1, c.k2, c.v, c.k1_scales, c.k2_scales, c.v_scales) if t is not None]
+    before = [t.clone() for t in tensors]
+    rs = np.random.RandomState(H)
+    lens, kept = [0, 36, 20, 5], [33, 64, 50, 63]
+    path = np.zeros((B, A), np.int32)
+    for b in range(B):
+        path[b, :kept[b]] = np.sort(rs.permutation(64)[:kept[b]])
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    new = da.cache_keep(c, i32(lens), i32(path), i32(kept))
+    da.device_status()
+    assert new.tolist() == [x + k for x, k in zip(lens, kept)]
+    for old, now in zip(before, tensors):
+        want = old.clone()
+        for b in range(B):
+            src, dst = [lens[b] + int(x) for x in path[b, :kept[b]]], slice(lens[b], lens[b] + kept[b])
+            if old.dim() == 4:
+                want[b, dst] = old[b, src]
+            else:
+                want[b, :, dst] = old[b][:, src]
+        assert torch.equal(now.view(torch.uint8), want.view(torch.uint8))
