@@ -18,13 +18,15 @@
 // All three kernels read and write each value once.  Measured: rotary fp32 V1
 // d128, 8192 tokens of 48 heads (403 MB) 61 us, 6.55 TB/s, which is HBM's rate;
 // bf16 V1 d64, 8192 tokens of 64 heads (134 MB) 25 us, 5.4 TB/s; append V2 d128
-// fp8, 8002 tokens of 32 + 16 + 16 heads (173 MB) 37 us, 4.6 TB/s with the
-// issue slots 53 % busy (unpacking, rotating, finding the maximum and
-// converting are some 200 instructions per 32 x 16 values; staging a CTA's rows
-// in shared memory by asynchronous copies took 10 % off 30000 unpadded tokens,
-// but put 10 % on these, whose copies wait for ntok, and on a few hundred; two
-// values an instruction in the maximum and the scaling changed nothing); a few
-// tokens 2.3 us one call after the other, the launch and two dependent loads.
+// fp8, 8002 padded tokens of 32 + 16 + 16 heads (173 MB) 37 us, 4.6 TB/s: a warp
+// holds 32 bytes a lane in flight and nothing of its next rows while it rotates,
+// finds the maximum and converts (some 200 instructions per 32 x 16 values, 57 %
+// of the issue slots; staging a CTA's rows in shared memory by asynchronous
+// copies took 10 % off 30000 unpadded tokens, but put 10 % on these, whose copies
+// wait for ntok, and on a few hundred; two values an instruction in the maximum
+// and the scaling changed nothing).  8000 unpadded tokens: V2 d128 bf16 45 us
+// (262 MB), fp8k 44, fp8 46 (230 MB); V1 d64 H16 35, 34, 35.  A token 2.1 us one
+// call after the other, the launch and two dependent loads; 300 tokens 3 to 4.
 #pragma once
 
 #include <cuda_bf16.h>

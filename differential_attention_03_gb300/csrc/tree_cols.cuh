@@ -55,10 +55,10 @@
 // another) of both maps; with 16, a map of one of two streams; with 32, half
 // the columns of a map.
 //
-// Measured (this kernel alone, one token): V1 d64 B8 H16 n32768 176 us (1.12
-// GB with the scales, 6.4 TB/s); 32 tokens V1 d128 B8 H8 n32768 193 us with
-// the merge (5.6 TB/s), V1 d64 B8 H16 256 us (4.2 TB/s), where the softmax
-// warps bound it.
+// Measured (with the merge, replayed from a graph): one token V1 d64 B8 H16
+// n32768 187 us (1.12 GB with the scales, 6.0 TB/s), V1 d128 B8 H8 172 us; 16
+// tokens 180 us each; 32 tokens V1 d128 B8 H8 190 us (5.7 TB/s), V1 d64 B8 H16
+// 261 us (4.3 TB/s), where the softmax warps bound it.
 #pragma once
 
 #include "tree_common.cuh"

@@ -55,7 +55,7 @@
 // Measured (this kernel alone): bf16 V1 d128 B4 H12 T16 n8192 71 us (403 MB, 5.7
 // TB/s; about 10 us of it are the way in and the last states' stores), V2 d128
 // B4 H16 T8 47 us (269 MB); over 32768 keys HBM's rate (bf16 V1 d128 B8 H8 312
-// us, 6.9 TB/s).  e4m3 with 64 tokens, V1 d128 H12 n65536: 118 us (415 MB, 3.5
+// us, 6.9 TB/s).  e4m3 with 64 tokens, V1 d128 H12 n65536: 124 us (415 MB, 3.3
 // TB/s), bound by the softmax warps: 128 x 128 weights a tile are scaled,
 // exponentiated and split for the 64 KB that the tile reads.  (Tried there: keys
 // as the MMAs' rows with 64 columns, whose 32 columns a thread do not fit the
@@ -514,7 +514,8 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
         // O times f (the first P V of a segment overwrites O).  It has to wait for the previous tile's P V,
         // still busy when the maxima are known: where P has tiles of its own, it comes last, behind the
         // weights (e4m3 V1 d64 B8 H16 T64 n32768: 464 us, 422 last); where P's place is the scores' it comes
-        // first, so that their next MMAs are not held up (d128 B8 H8: 285 us, 296 last).
+        // first, so that their next MMAs are not held up (d128 B8 H8: 285 us, 296 last; all four with P in two
+        // terms, now 431 and 297).
         auto scale_o = [&](float f) {
           mbar_wait(&pv_done[(g - 1) & 1u], ((g - 1) >> 1) & 1u, ab);
           __syncwarp();

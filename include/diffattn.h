@@ -728,7 +728,9 @@ diffattn_status diffattn_v2_cache_append(diffattn_cache_format fmt, int B, int T
  * of the row's largest.
  * A query with a NaN or an infinity gives NaN for its token and head.
  * A drafted key or value row with a NaN or an infinity makes the tokens that
- * see it NaN, and no others.  Two kernels; results do not depend on the
+ * see it NaN, and no others.  (Only a V2 key, or an infinite key scale, whose
+ * score is minus infinity weighs nothing; a token all of whose scores are that
+ * gives zeros.)  Two kernels; results do not depend on the
  * order in which they run (the same inputs give the same bits on the same
  * GPU).  Errors as for diffattn_decode; an unknown format -> ERR_DTYPE.
  */

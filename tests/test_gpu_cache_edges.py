@@ -288,3 +288,33 @@ def test_keep_moves_long_paths(v1, d, H, fmt):
             else:
                 want[b, :, dst] = old[b][:, src]
         assert torch.equal(now.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_an_infinite_key_weighs_by_its_scores(T):
+    # V1: NaN for who sees it (a map's rows meet both maps' keys); V2: nothing where its score is minus infinity
+    B, H, n = 1, 2, 150
+    g = torch.Generator(device="cuda").manual_seed(T)
+    L, see, but = n - T, [7] * T, [5] * T
+    for v1, d in ((True, 64), (False, 128)):
+        c, _, _ = _random(g, B, n, H, d, v1, "bf16")
+        q = [_bf(g, B, T, H if v1 else 2 * H, d) for _ in range(2)]
+        for x in q:
+            x[..., 0] = 1.0
+        lam, logits = torch.tensor([0.25], device="cuda"), torch.randn(H, generator=g, device="cuda")
+
+        def call(length, words):
+            a = dict(lens=torch.tensor([length], dtype=torch.int32, device="cuda"),
+                     mask=torch.tensor(words, dtype=torch.int64, device="cuda"))
+            out = da.tree_decode(*q, c, lam, 0.2, **a) if v1 else da.v2_tree_decode(q[0], c, logits, **a)
+            da.device_status()
+            return out
+        hidden = call(L, but)
+        for x in (float("-inf"), float("inf")):
+            c.k1[:, L + 1, :, 0] = x
+            assert torch.equal(call(L, but), hidden)
+            out = call(L, see)
+            assert torch.equal(out, hidden) if x < 0 and not v1 else out.isnan().all()
+        if not v1:
+            c.k1[:, 1, :, 0] = float("-inf")
+            assert not call(0, [2] * T).any()  # (nothing but that key)
