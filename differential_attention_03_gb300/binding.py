@@ -150,6 +150,24 @@ def lib() -> ctypes.CDLL:
             L.diffattn_v2_tree_decode.argtypes = [i, i, i, i, i, i, i, vp, vp, f, vp, vp, vp, vp, vp, vp, ll, vp, ll,
                                                   ll, f, vp, vp, sz, vp]
             L.diffattn_v2_tree_decode.restype = i
+            L.diffattn_linear.argtypes = [i, i, i, vp, ll, vp, vp, i, vp, ll, i, vp, ll, vp, vp]
+            L.diffattn_linear.restype = i
+            L.diffattn_linear_backward_workspace.argtypes = [i, i, i]
+            L.diffattn_linear_backward_workspace.restype = sz
+            L.diffattn_linear_backward.argtypes = [i, i, i, vp, ll, vp, vp, ll, vp, i, vp, vp, i, vp, vp, sz, vp]
+            L.diffattn_linear_backward.restype = i
+            L.diffattn_gated_linear.argtypes = [i, i, i, vp, ll, vp, i, vp, ll, vp, vp]
+            L.diffattn_gated_linear.restype = i
+            L.diffattn_gated_linear_backward_workspace.argtypes = [i, i, i]
+            L.diffattn_gated_linear_backward_workspace.restype = sz
+            L.diffattn_gated_linear_backward.argtypes = [i, i, i, vp, ll, vp, vp, vp, ll, i, vp, vp, i, vp, sz, vp]
+            L.diffattn_gated_linear_backward.restype = i
+            L.diffattn_residual_norm.argtypes = [i, i, i, i, vp, vp, vp, i, f, i, vp, vp, f, vp, vp, vp]
+            L.diffattn_residual_norm.restype = i
+            L.diffattn_residual_norm_backward_workspace.argtypes = [i, i, i]
+            L.diffattn_residual_norm_backward_workspace.restype = sz
+            L.diffattn_residual_norm_backward.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, i, f, i, vp, vp, f] + [vp] * 6 + [sz, vp]
+            L.diffattn_residual_norm_backward.restype = i
             L.diffattn_device_status.argtypes = [vp]
             L.diffattn_device_status.restype = i
             L.diffattn_bounds_checked.argtypes = []
@@ -1260,6 +1278,325 @@ def v2_tree_decode(q, cache: KVCache, lam_logits, lens=None, ntok=None, mask=Non
         _addr(cache._k1_scales), cache._v.data_ptr(), _addr(cache._v_scales), *a, lam_logits.data_ptr(), sb, st,
         float(softmax_scale), out.data_ptr(), wp, wn, _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------------------- the block around the layer
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _act_code(act: str) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"the activation must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def _rows(t, name, dtype, shape, dev):
+    """The row stride (elements) of a tensor [..., width]: contiguous, or 2-D with contiguous rows."""
+    if t.dtype == dtype and t.shape == shape and t.is_cuda and t.get_device() == dev:
+        if t.is_contiguous():
+            return shape[-1]
+        if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= shape[1]:
+            return t.stride(0)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
+
+
+def _count(shape) -> int:
+    n = 1
+    for k in shape:
+        n *= k
+    return n
+
+
+def _linear(a, w, bias, act, residual, dtype, out, pre, stream):
+    dev = _current(a, "a")
+    if w.dim() != 2 or a.dim() < 1:
+        raise ValueError("a must be [..., K] and w [N, K]")
+    N, K = w.shape
+    lead = a.shape[:-1]
+    shape = lead + (N,)
+    M = _count(lead)
+    lda = _rows(a, "a", torch.bfloat16, lead + (K,), dev)
+    _on(w, "w", torch.bfloat16, w.shape, dev)
+    if out is None:
+        out = _empty(shape, dtype or torch.bfloat16, a.device, stream)
+    elif dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    dt = _dt(out)
+    ldo = _rows(out, "out", out.dtype, shape, dev)
+    ldr = 0
+    if bias is not None:
+        _on(bias, "bias", torch.float32, (N,), dev)
+    if residual is not None:
+        ldr = _rows(residual, "residual", out.dtype, shape, dev)
+    if pre is not None:
+        _on(pre, "pre", torch.bfloat16, shape, dev)
+    _check(lib().diffattn_linear(M, N, K, a.data_ptr(), lda, w.data_ptr(), _addr(bias), _act_code(act), _addr(residual),
+                                 ldr, dt, out.data_ptr(), ldo, _addr(pre), _stream(stream)))
+    return out
+
+
+def linear(a, w, bias=None, act: str = "none", residual=None, dtype=None, out=None, stream=None) -> torch.Tensor:
+    """out = residual + act(a w^T + bias) in one kernel: a [..., K], w [N, K] (bf16; N, K multiples of 8).
+
+    bias: fp32 [N]; act: "none", "relu", "gelu", "gelu_tanh" or "silu"; residual: [..., N] of the output's
+    type, and may be out itself; dtype: bf16 (default) or fp32.  a, residual and out may be 2-D with rows
+    further apart (multiples of 8 elements; fp32: of 4), e.g. columns of a wider tensor.
+    """
+    return _linear(a, w, bias, act, residual, dtype, out, None, stream)
+
+
+def linear_train(a, w, bias=None, act: str = "none", residual=None, dtype=None, out=None, pre=None, stream=None):
+    """linear that also keeps a w^T + bias (bf16) for linear_backward: returns (out, pre)."""
+    if pre is None:
+        pre = _empty(a.shape[:-1] + w.shape[:1], torch.bfloat16, a.device, stream)
+    return _linear(a, w, bias, act, residual, dtype, out, pre, stream), pre
+
+
+def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().diffattn_linear_backward_workspace(M, N, K))
+
+
+def _workspace(workspace, need, dev, like, stream):
+    if workspace is None:
+        return _empty((need,), torch.uint8, like.device, stream) if need else None
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous() or workspace.nbytes < need:
+        raise ValueError(f"workspace must be a contiguous CUDA tensor of at least {need} bytes on device {dev}")
+    return workspace
+
+
+def _grad(out, name, shape, dtype, dev, like, stream):
+    """A gradient's tensor: the caller's, or a new one."""
+    t = (out or {}).get(name)
+    if t is None:
+        return _empty(shape, dtype, like.device, stream)
+    _on(t, name, dtype, shape, dev)
+    return t
+
+
+def _known(out, names):
+    for k in out or ():
+        if k not in names:
+            raise ValueError(f"out may hold {names}, got {k!r}")
+
+
+def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, da: bool = True, dw: bool = True,
+                    dw_dtype=torch.float32, out=None, workspace=None, stream=None) -> dict:
+    """Gradients of linear, given dy [..., N] (bf16), the gradient of its output (and so of the residual).
+
+    pre: what linear_train kept (not needed without an activation).  Returns a dict of da (bf16, like a), dw
+    [N, K] (dw_dtype: fp32 or bf16) and, with bias, dbias (fp32 [N]); da=False / dw=False leave one out.
+    Behind an activation the products take dy act'(pre) rounded to bf16.  out: None or a dict of tensors to
+    write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K) bytes.
+    """
+    dev = _current(a, "a")
+    if w.dim() != 2 or a.dim() < 1:
+        raise ValueError("a must be [..., K] and w [N, K]")
+    N, K = w.shape
+    lead = a.shape[:-1]
+    shape = lead + (N,)
+    M = _count(lead)
+    lda = _rows(a, "a", torch.bfloat16, lead + (K,), dev)
+    _on(w, "w", torch.bfloat16, w.shape, dev)
+    ldy = _rows(dy, "dy", torch.bfloat16, shape, dev)
+    code = _act_code(act)
+    if code:
+        if pre is None:
+            raise ValueError("pre is needed behind an activation")
+        _on(pre, "pre", torch.bfloat16, shape, dev)
+    _known(out, ("da", "dw", "dbias"))
+    r = {}
+    if da:
+        r["da"] = _grad(out, "da", a.shape, torch.bfloat16, dev, a, stream)
+    if dw:
+        r["dw"] = _grad(out, "dw", w.shape, dw_dtype, dev, a, stream)
+    if bias:
+        r["dbias"] = _grad(out, "dbias", (N,), torch.float32, dev, a, stream)
+    ws = _workspace(workspace, linear_backward_workspace_bytes(M, N, K), dev, a, stream)
+    _check(lib().diffattn_linear_backward(M, N, K, a.data_ptr(), lda, w.data_ptr(), dy.data_ptr(), ldy,
+                                          _addr(pre) if code else None, code, _addr(r.get("da")), _addr(r.get("dw")),
+                                          _dt(r["dw"]) if dw else F32, _addr(r.get("dbias")), _addr(ws),
+                                          0 if ws is None else ws.nbytes, _stream(stream)))
+    return r
+
+
+def _gated(x, w_gu, act, out, gu, stream):
+    dev = _current(x, "x")
+    if w_gu.dim() != 2 or w_gu.shape[0] % 2 or x.dim() < 1:
+        raise ValueError("x must be [..., D] and w_gu [2 F, D]")
+    F, D = w_gu.shape[0] // 2, w_gu.shape[1]
+    lead = x.shape[:-1]
+    ldx = _rows(x, "x", torch.bfloat16, lead + (D,), dev)
+    _on(w_gu, "w_gu", torch.bfloat16, w_gu.shape, dev)
+    if out is None:
+        out = _empty(lead + (F,), torch.bfloat16, x.device, stream)
+    ldh = _rows(out, "out", torch.bfloat16, lead + (F,), dev)
+    if gu is not None:
+        _on(gu, "gu", torch.bfloat16, lead + (2 * F,), dev)
+    _check(lib().diffattn_gated_linear(_count(lead), D, F, x.data_ptr(), ldx, w_gu.data_ptr(), _act_code(act),
+                                       out.data_ptr(), ldh, _addr(gu), _stream(stream)))
+    return out
+
+
+def gated_linear(x, w_gu, act: str = "silu", out=None, stream=None) -> torch.Tensor:
+    """h = act(x Wg^T) * (x Wu^T) in one kernel: x [..., D], w_gu = [Wg; Wu] [2 F, D] (bf16) -> [..., F] bf16.
+
+    linear(h, w_down, residual=...) is the rest of a feed-forward block.  x and out may be 2-D with rows
+    further apart (multiples of 8 elements).
+    """
+    return _gated(x, w_gu, act, out, None, stream)
+
+
+def gated_linear_train(x, w_gu, act: str = "silu", out=None, gu=None, stream=None):
+    """gated_linear that also keeps [x Wg^T | x Wu^T] (bf16 [..., 2 F]) for its backward: returns (h, gu)."""
+    if gu is None:
+        gu = _empty(x.shape[:-1] + w_gu.shape[:1], torch.bfloat16, x.device, stream)
+    return _gated(x, w_gu, act, out, gu, stream), gu
+
+
+def gated_linear_backward_workspace_bytes(M: int, D: int, F: int) -> int:
+    return int(lib().diffattn_gated_linear_backward_workspace(M, D, F))
+
+
+def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, dw: bool = True, dw_dtype=torch.float32,
+                          out=None, workspace=None, stream=None) -> dict:
+    """Gradients of gated_linear, given dh [..., F] (bf16) and gu as gated_linear_train kept it.
+
+    Returns a dict of dx (bf16, like x) and dw (like w_gu, of dw_dtype: fp32 or bf16).  The products take
+    the gradients of gu rounded to bf16.  out: None or a dict of tensors to write to; workspace: None or a
+    tensor of gated_linear_backward_workspace_bytes(M, D, F) bytes.
+    """
+    dev = _current(x, "x")
+    if w_gu.dim() != 2 or w_gu.shape[0] % 2 or x.dim() < 1:
+        raise ValueError("x must be [..., D] and w_gu [2 F, D]")
+    F, D = w_gu.shape[0] // 2, w_gu.shape[1]
+    lead = x.shape[:-1]
+    M = _count(lead)
+    ldx = _rows(x, "x", torch.bfloat16, lead + (D,), dev)
+    _on(w_gu, "w_gu", torch.bfloat16, w_gu.shape, dev)
+    _on(gu, "gu", torch.bfloat16, lead + (2 * F,), dev)
+    ldh = _rows(dh, "dh", torch.bfloat16, lead + (F,), dev)
+    _known(out, ("dx", "dw"))
+    r = {}
+    if dx:
+        r["dx"] = _grad(out, "dx", x.shape, torch.bfloat16, dev, x, stream)
+    if dw:
+        r["dw"] = _grad(out, "dw", w_gu.shape, dw_dtype, dev, x, stream)
+    ws = _workspace(workspace, gated_linear_backward_workspace_bytes(M, D, F), dev, x, stream)
+    _check(lib().diffattn_gated_linear_backward(M, D, F, x.data_ptr(), ldx, w_gu.data_ptr(), gu.data_ptr(),
+                                                dh.data_ptr(), ldh, _act_code(act), _addr(r.get("dx")), _addr(r.get("dw")),
+                                                _dt(r["dw"]) if dw else F32, _addr(ws), 0 if ws is None else ws.nbytes,
+                                                _stream(stream)))
+    return r
+
+
+def _gate_rows(gate, x, dev) -> int:
+    """The rows of a gate: [D], [G, D] with G dividing the rows of x, or like x."""
+    if gate is None:
+        return 0
+    D = x.shape[-1]
+    if gate.dim() == 1:
+        n = 1
+    elif gate.shape == x.shape:
+        n = _count(x.shape[:-1])
+    elif gate.dim() == 2:
+        n = gate.shape[0]
+    else:
+        raise ValueError(f"gate must be [D], [G, D] or like x {tuple(x.shape)}, got {tuple(gate.shape)}")
+    _on(gate, "gate", torch.float32, gate.shape[:-1] + (D,), dev)
+    return n
+
+
+def _norm_args(x, stream_dtype, gate, gamma_post, post, gamma):
+    dev = _current(x, "x")
+    D = x.shape[-1]
+    _on(x, "x", x.dtype, x.shape, dev)
+    for name, g in (("gamma_post", gamma_post), ("gamma", gamma)):
+        if g is not None:
+            _on(g, name, torch.float32, (D,), dev)
+    dt = _dt(x)
+    return dev, D, _count(x.shape[:-1]), dt, BF16 if stream_dtype == torch.bfloat16 else F32, _gate_rows(gate, x, dev), (
+        gamma_post is not None if post is None else bool(post))
+
+
+def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=None, post=None, gamma=None,
+                  norm: bool = True, eps: float = 1e-5, stream_dtype=None, out=None, y=None, stream=None):
+    """The norms after and before a block with its gate and residual scale, in one pass.
+
+    p = x / rms(x) * gamma_post (post, the default where gamma_post is given; else p = x),
+    s = residual + scale * gate * p, y = s / rms(s) * gamma, over the last dimension (1 to 8192).
+    x: [..., D] bf16 or fp32; residual: like x, or fp32 beside a bf16 x; gate: fp32 [D], like x, or
+    [G, D] where G divides x's rows (G sequences: each its own row); gammas: fp32 [D] or None (ones).  norm=False: without the second norm.
+    stream_dtype: the type of s where there is no residual (default x's).  out: s, which may be residual
+    itself.  Returns (y, s); y is None without the second norm.
+    """
+    sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or x.dtype)
+    dev, D, rows, dt, sd, gate_rows, post = _norm_args(x, sdt, gate, gamma_post, post, gamma)
+    if sdt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {sdt} (bf16 or fp32)")
+    if residual is not None:
+        _on(residual, "residual", sdt, x.shape, dev)
+    if out is None:
+        out = _empty(x.shape, sdt, x.device, stream)
+    else:
+        _on(out, "out", sdt, x.shape, dev)
+    if not norm:
+        if y is not None or gamma is not None:
+            raise ValueError("y and gamma belong to the second norm")
+    elif y is None:
+        y = _like(x, stream)
+    else:
+        _on(y, "y", x.dtype, x.shape, dev)
+    _check(lib().diffattn_residual_norm(dt, sd, rows, D, x.data_ptr(), _addr(residual), _addr(gate), gate_rows, scale,
+                                        1 if post else 0, _addr(gamma_post), _addr(gamma), eps, out.data_ptr(), _addr(y),
+                                        _stream(stream)))
+    return y, out
+
+
+def residual_norm_backward_workspace_bytes(rows: int, D: int, gate_rows: int = 0) -> int:
+    return int(lib().diffattn_residual_norm_backward_workspace(rows, D, gate_rows))
+
+
+def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0, gamma_post=None, post=None, gamma=None,
+                           eps: float = 1e-5, out=None, workspace=None, stream=None) -> dict:
+    """Gradients of residual_norm from x, the s it returned, dy (like y) and ds (like s; either may be None).
+
+    Returns a dict of dx, dresidual (like s), and of those that apply: dgate (like gate), dgamma_post (post),
+    dgamma (with dy), fp32.  out: None or a dict of tensors to write to (dresidual may be ds); workspace:
+    None or a tensor of residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
+    """
+    dev, D, rows, dt, sd, gate_rows, post = _norm_args(x, s.dtype, gate, gamma_post, post, gamma)
+    if s.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {s.dtype} (bf16 or fp32)")
+    _on(s, "s", s.dtype, x.shape, dev)
+    if dy is not None:
+        _on(dy, "dy", x.dtype, x.shape, dev)
+    if ds is not None:
+        _on(ds, "ds", s.dtype, x.shape, dev)
+    _known(out, ("dx", "dresidual", "dgate", "dgamma_post", "dgamma"))
+    r = {"dx": _grad(out, "dx", x.shape, x.dtype, dev, x, stream),
+         "dresidual": _grad(out, "dresidual", x.shape, s.dtype, dev, x, stream)}
+    if gate is not None:
+        r["dgate"] = _grad(out, "dgate", gate.shape, torch.float32, dev, x, stream)
+    if post:
+        r["dgamma_post"] = _grad(out, "dgamma_post", (D,), torch.float32, dev, x, stream)
+    if dy is not None:
+        r["dgamma"] = _grad(out, "dgamma", (D,), torch.float32, dev, x, stream)
+    ws = _workspace(workspace, residual_norm_backward_workspace_bytes(rows, D, gate_rows), dev, x, stream)
+    _check(lib().diffattn_residual_norm_backward(dt, sd, rows, D, x.data_ptr(), s.data_ptr(), _addr(dy), _addr(ds),
+                                                 _addr(gate), gate_rows, scale, 1 if post else 0, _addr(gamma_post),
+                                                 _addr(gamma), eps, r["dx"].data_ptr(), r["dresidual"].data_ptr(),
+                                                 _addr(r.get("dgate")), _addr(r.get("dgamma_post")), _addr(r.get("dgamma")),
+                                                 _addr(ws), 0 if ws is None else ws.nbytes, _stream(stream)))
+    return r
 
 
 def bounds_checked() -> bool:

@@ -1,0 +1,584 @@
+// C entry points of what stands around the attention layer in a block: the
+// products with their epilogue, the gated feed-forward product, the norms with
+// gate and residual, and their backward passes: argument validation, TMA
+// descriptors, launch shapes.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+
+#include "block_params.h"
+#include "diffattn.h"
+#include "host.h"
+#include "launch.h"
+#include "linear_params.h"
+
+namespace {
+
+namespace dh = da::host;
+
+diffattn_status fail(diffattn_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return dh::error(s, buf);
+}
+
+diffattn_status cuda_fail(cudaError_t e, const char* fn) {
+  return fail(DIFFATTN_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+int sms_or_default() {
+  const int s = dh::sms();
+  return s > 0 ? s : 152;
+}
+
+// ---- overlap
+// A tensor of a call: `rows` rows of `width` bytes, `ld` bytes apart.
+struct Span {
+  const void* at;
+  long long rows, width, ld;
+};
+
+Span flat(const void* at, long long bytes) { return Span{at, 1, bytes, bytes}; }
+
+bool overlap(const Span& a, const Span& b) {
+  if (!a.at || !b.at || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  const uintptr_t xn = x + static_cast<uintptr_t>((a.rows - 1) * a.ld + a.width);
+  const uintptr_t yn = y + static_cast<uintptr_t>((b.rows - 1) * b.ld + b.width);
+  if (x >= yn || y >= xn) return false;
+  // Rows of the same stride that lie side by side: b's columns behind a's, and the next row of a behind b's.
+  const long long ld = a.rows > 1 ? a.ld : b.ld;
+  if ((a.rows == 1 || a.ld == ld) && (b.rows == 1 || b.ld == ld) && a.width <= ld && b.width <= ld) {
+    const long long off = static_cast<long long>((y >= x ? (y - x) % static_cast<uintptr_t>(ld)
+                                                         : (static_cast<uintptr_t>(ld) - (x - y) % static_cast<uintptr_t>(ld)) %
+                                                               static_cast<uintptr_t>(ld)));
+    if (off >= a.width && off + b.width <= ld) return false;
+  }
+  return true;
+}
+
+// What a call writes overlaps nothing else of it.
+diffattn_status disjoint(const char* fn, const Span* written, int nw, const Span* read, int nr) {
+  for (int i = 0; i < nw; ++i) {
+    for (int j = 0; j < nr; ++j)
+      if (overlap(written[i], read[j])) return fail(DIFFATTN_ERR_SHAPE, "%s: an output overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j])) return fail(DIFFATTN_ERR_SHAPE, "%s: outputs overlap", fn);
+  }
+  return DIFFATTN_OK;
+}
+
+// ---- arguments of the products
+bool bad_act(int act) { return act < DIFFATTN_ACT_NONE || act > DIFFATTN_ACT_SILU; }
+bool bad_dtype(int dt) { return dt != DIFFATTN_BF16 && dt != DIFFATTN_F32; }
+
+// A matrix of rows `width` wide, `ld` apart, elements of `es` bytes: aligned for 16-byte accesses.
+diffattn_status check_rows(const char* fn, const char* name, const void* at, long long width, long long ld, int es) {
+  if (!at) return fail(DIFFATTN_ERR_NULL, "%s: %s is NULL", fn, name);
+  if (!aligned(at, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: %s must be 16-byte aligned", fn, name);
+  if (ld < width || ld % (16 / es) != 0 || ld > (1ll << 36))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: row stride %lld of %s: at least %lld, a multiple of %d", fn, ld, name, width, 16 / es);
+  return DIFFATTN_OK;
+}
+
+diffattn_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return DIFFATTN_OK;
+  if (!ws) return fail(DIFFATTN_ERR_NULL, "%s: NULL workspace", fn);
+  if (bytes < need) return fail(DIFFATTN_ERR_SHAPE, "%s: workspace of %zu bytes, %zu needed", fn, bytes, need);
+  if (!aligned(ws, 256)) return fail(DIFFATTN_ERR_ALIGN, "%s: workspace not 256-byte aligned", fn);
+  return DIFFATTN_OK;
+}
+
+// 2-D map over bf16 rows: box = 64 columns (128 bytes, swizzled) x box_rows rows; zeros past the edges.
+diffattn_status map_rows(CUtensorMap* m, const void* base, long long rows, long long cols, long long ld, int box_rows) {
+  dh::EncodeTiled enc;
+  diffattn_status s = dh::encoder(&enc);
+  if (s != DIFFATTN_OK) return s;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DIFFATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return DIFFATTN_OK;
+}
+
+enum class Kind { kForward, kGated, kDgrad, kWgrad };
+
+constexpr int kGroupRows = 2048;  // rows of a group of the tile walk
+
+// Tiles, status word and launch of a product whose operands and epilogue are in p.
+diffattn_status launch_product(const char* fn, Kind kind, da::LinearParams& p, int epi, cudaStream_t s) {
+  diffattn_status st = dh::status_address(&p.status);
+  if (st != DIFFATTN_OK) return st;
+  const int sms = sms_or_default();
+  const int cg = 1;
+  const int bm = da::kLinBM * cg, bn = kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
+  p.tiles_m = (p.M + bm - 1) / bm;
+  p.tiles_n = (p.N + bn - 1) / bn;
+  p.group_m = kGroupRows / bm;
+  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+  if (tiles > 0x7fffffffll - sms || static_cast<long long>(p.M) + 2 * da::kLinBM > 0x7fffffffll ||
+      2ll * p.N + 2 * da::kLinBN > 0x7fffffffll || static_cast<long long>(p.K) + da::kLinBK > 0x7fffffffll)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+  const int grid = static_cast<int>(std::min<long long>(tiles, sms / cg)) * cg;
+  const cudaError_t e = kind == Kind::kDgrad   ? da::launch_linear_dgrad(p, cg, grid, s)
+                        : kind == Kind::kWgrad ? da::launch_linear_wgrad(p, epi, cg, grid, s)
+                                               : da::launch_linear_fwd(p, epi, cg, grid, s);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  dh::count_launches(1);
+  return DIFFATTN_OK;
+}
+
+// out [M, N] = dz [M, C] w [C, N], bf16.
+diffattn_status dgrad(const char* fn, int M, int N, int C, const void* dz, long long ldz, const void* w, void* out,
+                      cudaStream_t s) {
+  da::LinearParams p;
+  memset(&p, 0, sizeof(p));
+  diffattn_status st;
+  if ((st = map_rows(&p.tm_a, dz, M, C, ldz, 128)) != DIFFATTN_OK) return st;
+  if ((st = map_rows(&p.tm_b, w, C, N, N, 64)) != DIFFATTN_OK) return st;
+  p.M = M, p.N = N, p.K = C;
+  p.out = out, p.ldo = N;
+  return launch_product(fn, Kind::kDgrad, p, da::kEpiBf16, s);
+}
+
+// out [M, N] = dz^T a with dz [C, M] and a [C, N].
+diffattn_status wgrad(const char* fn, int M, int N, int C, const void* dz, long long ldz, const void* a, long long lda,
+                      void* out, diffattn_dtype dt, cudaStream_t s) {
+  da::LinearParams p;
+  memset(&p, 0, sizeof(p));
+  diffattn_status st;
+  if ((st = map_rows(&p.tm_a, dz, C, M, ldz, 64)) != DIFFATTN_OK) return st;
+  if ((st = map_rows(&p.tm_b, a, C, N, lda, 64)) != DIFFATTN_OK) return st;
+  p.M = M, p.N = N, p.K = C;
+  p.out = out, p.ldo = N;
+  return launch_product(fn, Kind::kWgrad, p, dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16, s);
+}
+
+// Row chunks of the element-wise kernels: some eight CTAs an SM, at least 32 rows each.
+int act_grad_chunks(int M, int N) {
+  const long long across = (N + 255) / 256;
+  const long long want = (152 * 8 + across - 1) / across, most = (M + 31) / 32;
+  return static_cast<int>(std::max(1ll, std::min({want, most, 65535ll})));
+}
+
+diffattn_status act_grad(const char* fn, const da::ActGradParams& p, bool gated, cudaStream_t s) {
+  const cudaError_t e = da::launch_act_grad(p, gated, s);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  dh::count_launches(1);
+  return DIFFATTN_OK;
+}
+
+diffattn_status sum_parts(const char* fn, const da::SumParts& p, cudaStream_t s) {
+  const cudaError_t e = da::launch_sum_parts(p, s);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  dh::count_launches(1);
+  return DIFFATTN_OK;
+}
+
+diffattn_status zero(const char* fn, void* at, size_t bytes, cudaStream_t s) {
+  if (!at || !bytes) return DIFFATTN_OK;
+  const cudaError_t e = cudaMemsetAsync(at, 0, bytes, s);
+  return e == cudaSuccess ? DIFFATTN_OK : cuda_fail(e, fn);
+}
+
+size_t dtype_bytes(int dt) { return dt == DIFFATTN_F32 ? 4 : 2; }
+
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long lda, const void* w, const float* bias,
+                                diffattn_activation act, const void* residual, long long ldr, diffattn_dtype out_dt,
+                                void* out, long long ldo, void* pre, void* stream) {
+  const char* fn = "diffattn_linear";
+  if (M < 0 || N < 0 || K < 1) return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes M=%d N=%d K=%d", fn, M, N, K);
+  if (N % 8 != 0 || K % 8 != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: N and K must be multiples of 8 (16-byte rows; got N=%d K=%d)", fn, N, K);
+  if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
+  if (bad_dtype(out_dt)) return fail(DIFFATTN_ERR_DTYPE, "%s: the output must be bf16 or fp32", fn);
+  if (M == 0 || N == 0) return dh::success();
+  const int es = static_cast<int>(dtype_bytes(out_dt));
+  diffattn_status st;
+  if ((st = check_rows(fn, "a", a, K, lda, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "w", w, K, K, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "out", out, N, ldo, es)) != DIFFATTN_OK) return st;
+  if (residual && (st = check_rows(fn, "residual", residual, N, ldr, es)) != DIFFATTN_OK) return st;
+  if (pre && (st = check_rows(fn, "pre", pre, N, N, 2)) != DIFFATTN_OK) return st;
+  if (!aligned(bias, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: bias must be 16-byte aligned", fn);
+  {
+    const long long n = N, k = K;
+    const bool in_place = residual == out && ldr == ldo;
+    const Span wr[2] = {{out, M, n * es, ldo * es}, {pre, M, n * 2, n * 2}};
+    const Span rd[4] = {{a, M, k * 2, lda * 2}, {w, N, k * 2, k * 2}, flat(bias, n * 4),
+                        {in_place ? nullptr : residual, M, n * es, ldr * es}};
+    if ((st = disjoint(fn, wr, 2, rd, 4)) != DIFFATTN_OK) return st;
+    if (in_place && overlap(wr[1], wr[0])) return fail(DIFFATTN_ERR_SHAPE, "%s: an output overlaps an input", fn);
+  }
+  da::LinearParams p;
+  memset(&p, 0, sizeof(p));
+  if ((st = map_rows(&p.tm_a, a, M, K, lda, 128)) != DIFFATTN_OK) return st;
+  if ((st = map_rows(&p.tm_b, w, N, K, K, 128)) != DIFFATTN_OK) return st;
+  p.bias = bias;
+  p.residual = residual;
+  p.out = out;
+  p.pre = static_cast<__nv_bfloat16*>(pre);
+  p.ldr = ldr, p.ldo = ldo, p.ldp = N;
+  p.M = M, p.N = N, p.K = K, p.act = act;
+  if ((st = launch_product(fn, Kind::kForward, p, out_dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16,
+                           static_cast<cudaStream_t>(stream))) != DIFFATTN_OK)
+    return st;
+  return dh::success();
+}
+
+size_t diffattn_linear_backward_workspace(int M, int N, int K) {
+  if (M < 1 || N < 1 || K < 1) return 0;
+  return round256(static_cast<size_t>(M) * N * 2) + round256(static_cast<size_t>(act_grad_chunks(M, N)) * N * 4);
+}
+
+diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, long long lda, const void* w, const void* dy,
+                                         long long ldy, const void* pre, diffattn_activation act, void* da_, void* dw,
+                                         diffattn_dtype dw_dt, float* dbias, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  const char* fn = "diffattn_linear_backward";
+  if (M < 0 || N < 0 || K < 1) return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes M=%d N=%d K=%d", fn, M, N, K);
+  if (N % 8 != 0 || K % 8 != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: N and K must be multiples of 8 (16-byte rows; got N=%d K=%d)", fn, N, K);
+  if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
+  if (bad_dtype(dw_dt)) return fail(DIFFATTN_ERR_DTYPE, "%s: dw must be bf16 or fp32", fn);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t wes = dtype_bytes(dw_dt);
+  diffattn_status st;
+  if (N > 0 && dw && (st = check_rows(fn, "dw", dw, K, K, static_cast<int>(wes))) != DIFFATTN_OK) return st;
+  if (!aligned(dbias, 4)) return fail(DIFFATTN_ERR_ALIGN, "%s: dbias must be 4-byte aligned", fn);
+  if (M > 0 && da_ && (st = check_rows(fn, "da", da_, K, K, 2)) != DIFFATTN_OK) return st;
+  if (M == 0 || N == 0) {  // sums over nothing
+    if (N > 0 && (st = zero(fn, dw, static_cast<size_t>(N) * K * wes, s)) != DIFFATTN_OK) return st;
+    if (N > 0 && (st = zero(fn, dbias, static_cast<size_t>(N) * 4, s)) != DIFFATTN_OK) return st;
+    if (M > 0 && (st = zero(fn, da_, static_cast<size_t>(M) * K * 2, s)) != DIFFATTN_OK) return st;
+    return dh::success();
+  }
+  if (!da_ && !dw && !dbias) return dh::success();
+  const bool bent = act != DIFFATTN_ACT_NONE;
+  if (dw && (st = check_rows(fn, "a", a, K, lda, 2)) != DIFFATTN_OK) return st;
+  if (da_ && (st = check_rows(fn, "w", w, K, K, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "dy", dy, N, ldy, 2)) != DIFFATTN_OK) return st;
+  if (bent && (st = check_rows(fn, "pre", pre, N, N, 2)) != DIFFATTN_OK) return st;
+  const size_t need = (bent || dbias) ? diffattn_linear_backward_workspace(M, N, K) : 0;
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != DIFFATTN_OK) return st;
+  {
+    const long long n = N, k = K;
+    const Span wr[4] = {{da_, M, k * 2, k * 2}, flat(dw, n * k * static_cast<long long>(wes)), flat(dbias, n * 4),
+                        flat(workspace, static_cast<long long>(need))};
+    const Span rd[4] = {{dw ? a : nullptr, M, k * 2, lda * 2}, {da_ ? w : nullptr, N, k * 2, k * 2}, {dy, M, n * 2, ldy * 2},
+                        {bent ? pre : nullptr, M, n * 2, n * 2}};
+    if ((st = disjoint(fn, wr, 4, rd, 4)) != DIFFATTN_OK) return st;
+  }
+  const void* dz = dy;
+  long long ldz = ldy;
+  if (bent || dbias) {
+    da::ActGradParams p;
+    memset(&p, 0, sizeof(p));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.dy = static_cast<const __nv_bfloat16*>(dy);
+    p.pre = static_cast<const __nv_bfloat16*>(pre);
+    p.dz = reinterpret_cast<__nv_bfloat16*>(ws);
+    p.part = dbias ? reinterpret_cast<float*>(ws + round256(static_cast<size_t>(M) * N * 2)) : nullptr;
+    p.ldy = ldy, p.ldp = N, p.ldz = N;
+    p.M = M, p.N = N, p.act = act, p.chunks = act_grad_chunks(M, N);
+    if ((st = act_grad(fn, p, false, s)) != DIFFATTN_OK) return st;
+    if (dbias) {
+      da::SumParts q;
+      memset(&q, 0, sizeof(q));
+      q.part[0] = p.part, q.dst[0] = dbias, q.width[0] = N, q.count[0] = p.chunks;
+      if ((st = sum_parts(fn, q, s)) != DIFFATTN_OK) return st;
+    }
+    if (bent) dz = ws, ldz = N;
+  }
+  if (da_ && (st = dgrad(fn, M, K, N, dz, ldz, w, da_, s)) != DIFFATTN_OK) return st;
+  if (dw && (st = wgrad(fn, N, K, M, dz, ldz, a, lda, dw, dw_dt, s)) != DIFFATTN_OK) return st;
+  return dh::success();
+}
+
+diffattn_status diffattn_gated_linear(int M, int D, int F, const void* x, long long ldx, const void* w_gu,
+                                      diffattn_activation act, void* h, long long ldh, void* gu, void* stream) {
+  const char* fn = "diffattn_gated_linear";
+  if (M < 0 || F < 0 || D < 1) return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes M=%d D=%d F=%d", fn, M, D, F);
+  if (D % 8 != 0 || F % 8 != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: D and F must be multiples of 8 (16-byte rows; got D=%d F=%d)", fn, D, F);
+  if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
+  if (M == 0 || F == 0) return dh::success();
+  if (F > 0x3fffffff) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+  diffattn_status st;
+  if ((st = check_rows(fn, "x", x, D, ldx, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "w_gu", w_gu, D, D, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "h", h, F, ldh, 2)) != DIFFATTN_OK) return st;
+  if (gu && (st = check_rows(fn, "gu", gu, 2ll * F, 2ll * F, 2)) != DIFFATTN_OK) return st;
+  {
+    const long long d = D, f = F;
+    const Span wr[2] = {{h, M, f * 2, ldh * 2}, {gu, M, f * 4, f * 4}};
+    const Span rd[2] = {{x, M, d * 2, ldx * 2}, {w_gu, 2 * f, d * 2, d * 2}};
+    if ((st = disjoint(fn, wr, 2, rd, 2)) != DIFFATTN_OK) return st;
+  }
+  da::LinearParams p;
+  memset(&p, 0, sizeof(p));
+  if ((st = map_rows(&p.tm_a, x, M, D, ldx, 128)) != DIFFATTN_OK) return st;
+  if ((st = map_rows(&p.tm_b, w_gu, 2ll * F, D, D, 128)) != DIFFATTN_OK) return st;
+  p.out = h;
+  p.pre = static_cast<__nv_bfloat16*>(gu);
+  p.ldo = ldh, p.ldp = 2ll * F;
+  p.M = M, p.N = F, p.K = D, p.act = act;
+  if ((st = launch_product(fn, Kind::kGated, p, da::kEpiGated, static_cast<cudaStream_t>(stream))) != DIFFATTN_OK) return st;
+  return dh::success();
+}
+
+size_t diffattn_gated_linear_backward_workspace(int M, int D, int F) {
+  if (M < 1 || D < 1 || F < 1) return 0;
+  return round256(static_cast<size_t>(M) * F * 4);
+}
+
+diffattn_status diffattn_gated_linear_backward(int M, int D, int F, const void* x, long long ldx, const void* w_gu,
+                                               const void* gu, const void* dh_, long long ldh, diffattn_activation act,
+                                               void* dx, void* dw, diffattn_dtype dw_dt, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  const char* fn = "diffattn_gated_linear_backward";
+  if (M < 0 || F < 0 || D < 1) return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes M=%d D=%d F=%d", fn, M, D, F);
+  if (D % 8 != 0 || F % 8 != 0)
+    return fail(DIFFATTN_ERR_SHAPE, "%s: D and F must be multiples of 8 (16-byte rows; got D=%d F=%d)", fn, D, F);
+  if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
+  if (bad_dtype(dw_dt)) return fail(DIFFATTN_ERR_DTYPE, "%s: dw must be bf16 or fp32", fn);
+  if (F > 0x3fffffff) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t wes = dtype_bytes(dw_dt);
+  diffattn_status st;
+  if (F > 0 && dw && (st = check_rows(fn, "dw", dw, D, D, static_cast<int>(wes))) != DIFFATTN_OK) return st;
+  if (M > 0 && dx && (st = check_rows(fn, "dx", dx, D, D, 2)) != DIFFATTN_OK) return st;
+  if (M == 0 || F == 0) {
+    if (F > 0 && (st = zero(fn, dw, static_cast<size_t>(2) * F * D * wes, s)) != DIFFATTN_OK) return st;
+    if (M > 0 && (st = zero(fn, dx, static_cast<size_t>(M) * D * 2, s)) != DIFFATTN_OK) return st;
+    return dh::success();
+  }
+  if (!dx && !dw) return dh::success();
+  if (dw && (st = check_rows(fn, "x", x, D, ldx, 2)) != DIFFATTN_OK) return st;
+  if (dx && (st = check_rows(fn, "w_gu", w_gu, D, D, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "gu", gu, 2ll * F, 2ll * F, 2)) != DIFFATTN_OK) return st;
+  if ((st = check_rows(fn, "dh", dh_, F, ldh, 2)) != DIFFATTN_OK) return st;
+  const size_t need = diffattn_gated_linear_backward_workspace(M, D, F);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != DIFFATTN_OK) return st;
+  {
+    const long long d = D, f = F;
+    const Span wr[3] = {{dx, M, d * 2, d * 2}, flat(dw, 2 * f * d * static_cast<long long>(wes)),
+                        flat(workspace, static_cast<long long>(need))};
+    const Span rd[4] = {{dw ? x : nullptr, M, d * 2, ldx * 2}, flat(dx ? w_gu : nullptr, 4 * f * d),
+                        flat(gu, 4ll * M * f), {dh_, M, f * 2, ldh * 2}};
+    if ((st = disjoint(fn, wr, 3, rd, 4)) != DIFFATTN_OK) return st;
+  }
+  da::ActGradParams p;
+  memset(&p, 0, sizeof(p));
+  p.dy = static_cast<const __nv_bfloat16*>(dh_);
+  p.pre = static_cast<const __nv_bfloat16*>(gu);
+  p.dz = static_cast<__nv_bfloat16*>(workspace);
+  p.ldy = ldh, p.ldp = 2ll * F, p.ldz = 2ll * F;
+  p.M = M, p.N = F, p.act = act, p.chunks = act_grad_chunks(M, F);
+  if ((st = act_grad(fn, p, true, s)) != DIFFATTN_OK) return st;
+  if (dx && (st = dgrad(fn, M, D, 2 * F, workspace, 2ll * F, w_gu, dx, s)) != DIFFATTN_OK) return st;
+  if (dw && (st = wgrad(fn, 2 * F, D, M, workspace, 2ll * F, x, ldx, dw, dw_dt, s)) != DIFFATTN_OK) return st;
+  return dh::success();
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- norms
+namespace {
+
+// How a row of D elements is laid over threads: 16-byte vectors (8 elements) where rows allow it.  A warp a row up
+// to 256 elements; above, a CTA a row, a vector a thread up to 4096 elements and two above.
+da::NormShape norm_shape(int D, bool vec) {
+  da::NormShape h;
+  h.vec = vec ? 8 : 1;
+  const int per = vec ? (D > 4096 ? 16 : 8) : (D > 4096 ? 16 : 8);  // elements a thread
+  h.warp = D <= 256;
+  h.nv = per / h.vec;
+  h.threads = h.warp ? 256 : std::max(64, (((D + per - 1) / per) + 31) / 32 * 32);
+  return h;
+}
+
+diffattn_status norm_common(const char* fn, int dt, int sdt, int rows, int D, const float* gate, int gate_rows) {
+  if (bad_dtype(dt) || bad_dtype(sdt) || (dt == DIFFATTN_F32 && sdt != DIFFATTN_F32))
+    return fail(DIFFATTN_ERR_DTYPE, "%s: types: both bf16, both fp32, or bf16 on an fp32 stream", fn);
+  if (rows < 0 || D < 1) return fail(DIFFATTN_ERR_SHAPE, "%s: bad sizes rows=%d D=%d", fn, rows, D);
+  if (D > da::kNormMaxD) return fail(DIFFATTN_ERR_UNSUPPORTED, "%s: D at most %d (got %d)", fn, da::kNormMaxD, D);
+  if (gate && (gate_rows < 1 || rows % gate_rows != 0))
+    return fail(DIFFATTN_ERR_SHAPE, "%s: rows (%d) must be a multiple of gate_rows (%d)", fn, rows, gate_rows);
+  return DIFFATTN_OK;
+}
+
+// Workers and pieces of the backward pass.  A piece is a run of rows that share a gate row; a worker takes a
+// contiguous range of pieces and keeps its sums over them.
+struct NormPlan {
+  long long groups, group_rows, chunk_rows, pieces;
+  int chunks;
+  int grid;
+  long long workers;
+};
+
+constexpr int kNormCtas = 152 * 2;  // backward: about two CTAs an SM (eight workers each where a warp takes a row)
+
+NormPlan norm_plan(int rows, int D, int gate_rows) {
+  NormPlan n;
+  const long long per_cta = D <= 256 ? 8 : 1;
+  n.groups = gate_rows > 0 ? gate_rows : 1;
+  n.group_rows = std::max<long long>(1, rows / n.groups);
+  const long long want = std::max<long long>(1, std::min<long long>(rows, kNormCtas * per_cta));
+  const long long chunks = n.groups >= want ? 1 : std::min(n.group_rows, (want + n.groups - 1) / n.groups);
+  n.chunk_rows = (n.group_rows + chunks - 1) / chunks;
+  n.chunks = static_cast<int>((n.group_rows + n.chunk_rows - 1) / n.chunk_rows);
+  n.pieces = n.groups * n.chunks;
+  n.grid = static_cast<int>((std::min(n.pieces, want) + per_cta - 1) / per_cta);
+  n.workers = n.grid * per_cta;
+  return n;
+}
+
+}  // namespace
+
+extern "C" {
+
+diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_dt, int rows, int D, const void* x,
+                                       const void* residual, const float* gate, int gate_rows, float scale, int post,
+                                       const float* gamma_post, const float* gamma, float eps, void* s_out, void* y,
+                                       void* stream) {
+  const char* fn = "diffattn_residual_norm";
+  diffattn_status st = norm_common(fn, dt, stream_dt, rows, D, gate, gate_rows);
+  if (st != DIFFATTN_OK) return st;
+  if (!std::isfinite(scale)) return fail(DIFFATTN_ERR_SHAPE, "%s: scale not finite", fn);
+  if (gamma_post && !post) return fail(DIFFATTN_ERR_SHAPE, "%s: gamma_post without post", fn);
+  if (rows == 0) return dh::success();
+  if (!s_out && !y) return fail(DIFFATTN_ERR_SHAPE, "%s: neither s nor y wanted", fn);
+  if (gamma && !y) return fail(DIFFATTN_ERR_SHAPE, "%s: gamma without y", fn);
+  if (!x) return fail(DIFFATTN_ERR_NULL, "%s: x is NULL", fn);
+  for (const void* q : {x, residual, static_cast<const void*>(s_out), static_cast<const void*>(y),
+                        static_cast<const void*>(gate), static_cast<const void*>(gamma_post), static_cast<const void*>(gamma)})
+    if (!aligned(q, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  const long long v = static_cast<long long>(rows) * D, xe = dtype_bytes(dt), se = dtype_bytes(stream_dt);
+  {
+    const Span wr[2] = {flat(s_out, v * se), flat(y, v * xe)};
+    const Span rd[5] = {flat(x, v * xe), flat(residual == s_out ? nullptr : residual, v * se),
+                        flat(gate, gate ? 4ll * gate_rows * D : 0), flat(gamma_post, 4ll * D), flat(gamma, 4ll * D)};
+    if ((st = disjoint(fn, wr, 2, rd, 5)) != DIFFATTN_OK) return st;
+  }
+  da::NormParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = x, p.residual = residual, p.gate = gate, p.gamma_post = gamma_post, p.gamma = gamma;
+  p.s_out = s_out, p.y_out = y;
+  p.rows = rows, p.D = D;
+  p.groups = gate ? gate_rows : 1;
+  p.group_rows = rows / p.groups;
+  p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
+  p.post = post ? 1 : 0, p.norm = y ? 1 : 0;
+  const da::NormShape h = norm_shape(D, D % 8 == 0);
+  const long long ctas = h.warp ? (rows + 7ll) / 8 : rows;
+  // As many CTAs as an SM holds at once (2048 threads, 16 of the narrow ones); each walks its rows.
+  const int per_sm = std::max(1, std::min(16, 2048 / h.threads));
+  const int grid = static_cast<int>(std::min<long long>(ctas, static_cast<long long>(sms_or_default()) * per_sm));
+  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, false, grid,
+                                                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  dh::count_launches(1);
+  return dh::success();
+}
+
+size_t diffattn_residual_norm_backward_workspace(int rows, int D, int gate_rows) {
+  if (rows < 1 || D < 1 || gate_rows < 0) return 0;
+  const NormPlan n = norm_plan(rows, D, gate_rows);
+  return 2 * round256(static_cast<size_t>(n.workers) * D * 4) +
+         (gate_rows > 0 && n.chunks > 1 ? round256(static_cast<size_t>(n.pieces) * D * 4) : 0);
+}
+
+diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtype stream_dt, int rows, int D,
+                                                const void* x, const void* s_in, const void* dy, const void* ds,
+                                                const float* gate, int gate_rows, float scale, int post,
+                                                const float* gamma_post, const float* gamma, float eps, void* dx,
+                                                void* dresidual, float* dgate, float* dgamma_post, float* dgamma,
+                                                void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "diffattn_residual_norm_backward";
+  diffattn_status st = norm_common(fn, dt, stream_dt, rows, D, gate, gate_rows);
+  if (st != DIFFATTN_OK) return st;
+  if (!std::isfinite(scale)) return fail(DIFFATTN_ERR_SHAPE, "%s: scale not finite", fn);
+  if (dgate && !gate) return fail(DIFFATTN_ERR_SHAPE, "%s: dgate without gate", fn);
+  if ((dgamma_post || gamma_post) && !post) return fail(DIFFATTN_ERR_SHAPE, "%s: dgamma_post or gamma_post without post", fn);
+  for (const void* q : {x, s_in, dy, ds, static_cast<const void*>(gate), static_cast<const void*>(gamma_post),
+                        static_cast<const void*>(gamma), static_cast<const void*>(dx), static_cast<const void*>(dresidual),
+                        static_cast<const void*>(dgate), static_cast<const void*>(dgamma_post), static_cast<const void*>(dgamma)})
+    if (!aligned(q, 16)) return fail(DIFFATTN_ERR_ALIGN, "%s: tensors must be 16-byte aligned", fn);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if ((st = zero(fn, dgamma, 4ull * D, s)) != DIFFATTN_OK) return st;
+    if ((st = zero(fn, dgamma_post, 4ull * D, s)) != DIFFATTN_OK) return st;
+    if (gate && (st = zero(fn, dgate, 4ull * D * gate_rows, s)) != DIFFATTN_OK) return st;
+    return dh::success();
+  }
+  if (!dy && !ds) return fail(DIFFATTN_ERR_NULL, "%s: neither dy nor ds", fn);
+  if ((dgamma || gamma) && !dy) return fail(DIFFATTN_ERR_SHAPE, "%s: dgamma or gamma without dy", fn);
+  if (dy && !s_in) return fail(DIFFATTN_ERR_NULL, "%s: s is NULL", fn);
+  if (!x && (post || dgate)) return fail(DIFFATTN_ERR_NULL, "%s: x is NULL", fn);
+  if (!dx && !dresidual && !dgate && !dgamma_post && !dgamma) return dh::success();
+  const NormPlan n = norm_plan(rows, D, gate ? gate_rows : 0);
+  const size_t need = diffattn_residual_norm_backward_workspace(rows, D, gate ? gate_rows : 0);
+  if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != DIFFATTN_OK) return st;
+  const long long v = static_cast<long long>(rows) * D, xe = dtype_bytes(dt), se = dtype_bytes(stream_dt);
+  const long long gb = gate ? 4ll * gate_rows * D : 0;
+  {
+    const Span wr[6] = {flat(dx, v * xe), flat(dresidual, v * se), flat(dgate, gb), flat(dgamma_post, 4ll * D),
+                        flat(dgamma, 4ll * D), flat(workspace, static_cast<long long>(need))};
+    const Span rd[7] = {flat(x, v * xe), flat(s_in, v * se), flat(dy, v * xe), flat(ds == dresidual ? nullptr : ds, v * se),
+                        flat(gate, gb), flat(gamma_post, 4ll * D), flat(gamma, 4ll * D)};
+    if ((st = disjoint(fn, wr, 6, rd, 7)) != DIFFATTN_OK) return st;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t part = round256(static_cast<size_t>(n.workers) * D * 4);
+  da::NormParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = x, p.s = s_in, p.dy = dy, p.ds = ds, p.gate = gate, p.gamma_post = gamma_post, p.gamma = gamma;
+  p.dx = dx, p.dresidual = dresidual;
+  p.part_gamma = dgamma ? reinterpret_cast<float*>(ws) : nullptr;
+  p.part_post = dgamma_post ? reinterpret_cast<float*>(ws + part) : nullptr;
+  p.part_gate = !dgate ? nullptr : n.chunks > 1 ? reinterpret_cast<float*>(ws + 2 * part) : dgate;
+  p.rows = rows, p.group_rows = n.group_rows, p.groups = n.groups, p.chunk_rows = n.chunk_rows, p.pieces = n.pieces;
+  p.chunks = n.chunks, p.D = D;
+  p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
+  p.post = post ? 1 : 0, p.norm = dy ? 1 : 0;
+  cudaError_t e = da::launch_residual_norm(p, norm_shape(D, D % 8 == 0), dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, true,
+                                           n.grid, s);
+  if (e != cudaSuccess) return cuda_fail(e, fn);
+  dh::count_launches(1);
+  da::SumParts q;
+  memset(&q, 0, sizeof(q));
+  int k = 0;
+  auto add = [&](const float* from, float* to, long long width, long long count) {
+    q.part[k] = from, q.dst[k] = to, q.width[k] = width, q.count[k] = static_cast<int>(count);
+    ++k;
+  };
+  if (dgamma) add(p.part_gamma, dgamma, D, n.workers);
+  if (dgamma_post) add(p.part_post, dgamma_post, D, n.workers);
+  if (dgate && n.chunks > 1) add(p.part_gate, dgate, static_cast<long long>(n.groups) * D, n.chunks);
+  if (k > 0 && (st = sum_parts(fn, q, s)) != DIFFATTN_OK) return st;
+  return dh::success();
+}
+
+}  // extern "C"

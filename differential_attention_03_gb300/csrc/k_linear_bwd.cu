@@ -1,0 +1,51 @@
+// Launchers of the backward products (one or both operands MN-major) and of
+// the element-wise kernels of the backward pass.
+#include "act_grad.cuh"
+#include "launch.h"
+#include "linear_launch.cuh"
+
+namespace da {
+
+cudaError_t launch_linear_dgrad(const LinearParams& p, int cg, int grid, cudaStream_t s) {
+  return launch_linear_as<false, true, kEpiBf16>(p, cg, grid, s);
+}
+
+cudaError_t launch_linear_wgrad(const LinearParams& p, int epi, int cg, int grid, cudaStream_t s) {
+  return epi == kEpiF32 ? launch_linear_as<true, true, kEpiF32>(p, cg, grid, s)
+                        : launch_linear_as<true, true, kEpiBf16>(p, cg, grid, s);
+}
+
+namespace {
+template <bool kGated, int ACT>
+void launch_act_grad_as(const ActGradParams& p, cudaStream_t s) {
+  const dim3 grid((p.N + 255) / 256, p.chunks);
+  act_grad_kernel<kGated, ACT><<<grid, kActGradThreads, 0, s>>>(p);
+}
+template <bool kGated>
+cudaError_t launch_act_grad_of(const ActGradParams& p, cudaStream_t s) {
+  switch (p.act) {
+    case DIFFATTN_ACT_RELU: launch_act_grad_as<kGated, DIFFATTN_ACT_RELU>(p, s); break;
+    case DIFFATTN_ACT_GELU: launch_act_grad_as<kGated, DIFFATTN_ACT_GELU>(p, s); break;
+    case DIFFATTN_ACT_GELU_TANH: launch_act_grad_as<kGated, DIFFATTN_ACT_GELU_TANH>(p, s); break;
+    case DIFFATTN_ACT_SILU: launch_act_grad_as<kGated, DIFFATTN_ACT_SILU>(p, s); break;
+    default: launch_act_grad_as<kGated, DIFFATTN_ACT_NONE>(p, s); break;
+  }
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s) {
+  return gated ? launch_act_grad_of<true>(p, s) : launch_act_grad_of<false>(p, s);
+}
+
+cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s) {
+  long long widest = 0;
+  int n = 0;
+  for (; n < 3 && p.count[n] > 0; ++n)
+    if (p.width[n] > widest) widest = p.width[n];
+  if (n == 0) return cudaSuccess;
+  sum_parts_kernel<<<dim3(static_cast<unsigned>((widest + 31) / 32), n), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace da

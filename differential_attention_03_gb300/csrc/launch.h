@@ -13,6 +13,11 @@ struct SimtBwdExtra;
 struct GemmParams;
 struct BwdTcParams;
 struct BwdPrepParams;
+struct LinearParams;
+struct ActGradParams;
+struct SumParts;
+struct NormParams;
+struct NormShape;
 }
 
 namespace da {
@@ -63,6 +68,17 @@ cudaError_t launch_bwd_tc(const BwdTcParams& p, bool v2, int grid, cudaStream_t 
 cudaError_t launch_bwd_reduce(const BwdParams& p, cudaStream_t s);
 // Projection GEMM C = A B^T (bf16, fp32 accumulation), `grid` persistent CTAs.
 cudaError_t launch_gemm_bf16(const GemmParams& p, int grid, cudaStream_t s);
+// Products with their epilogue (epi: kEpiBf16, kEpiF32, kEpiGated), clusters of `cg` CTAs (1 or 2), `grid` CTAs.
+cudaError_t launch_linear_fwd(const LinearParams& p, int epi, int cg, int grid, cudaStream_t s);
+// da = dz w (the weights MN-major) and dw = dz^T a (both operands MN-major).
+cudaError_t launch_linear_dgrad(const LinearParams& p, int cg, int grid, cudaStream_t s);
+cudaError_t launch_linear_wgrad(const LinearParams& p, int epi, int cg, int grid, cudaStream_t s);
+// The element-wise part of their backward pass, and the sums over partial rows.
+cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s);
+cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s);
+// The norms around a block, forward or backward.
+cudaError_t launch_residual_norm(const NormParams& p, const NormShape& h, bool x_f32, bool s_f32, bool grad, int grid,
+                                 cudaStream_t s);
 cudaError_t launch_wait_selftest(unsigned long long budget_cycles, int* status, cudaStream_t s);
 
 }  // namespace da

@@ -1,0 +1,578 @@
+// Products with their epilogue on tcgen05 tensor cores (sm_103a):
+//
+//   z = A B^T (+ bias);  out = residual + act(z)          (kEpiBf16, kEpiF32)
+//   g = x Wg^T, u = x Wu^T;  out = act(g) u               (kEpiGated, w_gu = [Wg; Wu])
+//
+// and, without bias, activation and residual, the two products of their
+// backward pass.  An operand is K-major (the contraction contiguous: x and the
+// weights of a forward) or MN-major (its other dimension contiguous: the
+// weights in da = dz w, both operands in dw = dz^T a), so no transpose is
+// ever stored.  bf16 operands, fp32 accumulation.
+//
+// Bound: the tensor cores (2 M N K flops; a 256-wide tile reads 1/128 byte of
+// L2 a flop), or for short contractions the epilogue's stores.
+//
+// One cluster of CG CTAs (an SM pair with CG = 2) per 128 CG x 256 tile,
+// persistent over the tiles in groups of `group_m` row blocks, so that the
+// CTAs at work share operands in L2.  With CG = 2 an MMA is M256 N256 K16
+// over both SMs' tensor cores: each CTA holds its 128 rows of A and half of B,
+// so a CTA's shared memory feeds half as many B bytes.
+//   warps 0-7   epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
+//               columns 128 (w / 4) .. (gated: 64 gate columns and their 64 up
+//               columns).  Values pass through a 4 KB staging buffer a warp
+//               (rows of 128 bytes, 16-byte parts XORed by the row): residual
+//               and outputs move between global memory and it in whole
+//               128-byte rows, 8 lanes a row.
+//   warp 8      TMA producer: per K block of 64 the A and B boxes into a ring.
+//   warp 9      TMEM allocator; MMA issuer (of the cluster's first CTA).
+// TMEM: two 256-column accumulators: the epilogue of one tile overlaps the
+// next one's main loop.
+//
+// kEpiF32: the tensor cores truncate as they add into fp32, which costs about
+// 1e-9 relative an added value (measured: 1e-6 for a contraction of 1000,
+// 9e-6 for 8192).  A result in bf16 does not see that; one in fp32 would, so
+// its accumulators sum 512 values each and the epilogue warps add them up in
+// registers, rounding to nearest.
+//
+// Rows past M and contraction past K are zero-filled by TMA on load; rows past
+// M and columns past N are not stored.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "linear_params.h"
+#include "ptx.cuh"
+
+#undef DA_BOUNDS_FILE
+#define DA_BOUNDS_FILE 12
+
+namespace da {
+
+// ----------------------------------------------------------------- SM pairs
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address, in the cluster's shared window, of what `p` is in CTA `rank`.
+__device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A load into this CTA's shared memory whose bytes count on the barrier at
+// cluster address `bar` (its own or the pair's other CTA's).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  if (!DA_TMA_OK(smem_u32(dst), c0, c1, 0, 0)) return;
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst, uint32_t ncols) {
+  if (CG == 1) {
+    tmem_alloc(dst, ncols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) {
+  if (CG == 1)
+    tmem_dealloc(taddr, ncols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on `bar` (with CG = 2: in both CTAs of the pair) when the MMAs issued so far have completed.
+template <int CG>
+__device__ __forceinline__ void tc_commit_cg(uint64_t* bar) {
+  if (CG == 1)
+    tc_commit_elect(bar);
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tmov.b16 m, 3;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void mma_cg(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  if (CG == 1) {
+    mma_ss_elect(d_tmem, a_desc, b_desc, idesc, accumulate);
+    return;
+  }
+  if (!DA_MMA_OK(d_tmem, idesc)) return;
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ----------------------------------------------------------------- layout
+template <int CG, bool A_MN, bool B_MN>
+struct LinearCfg {
+  static constexpr int BM = kLinBM, BN = kLinBN, BK = kLinBK;
+  static constexpr int BN_CTA = BN / CG;  // rows of B that a CTA holds
+  static constexpr int EPI_WARPS = 8, NTHREADS = (EPI_WARPS + 2) * 32;
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_BYTES = BN_CTA * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 48 KB, a pair's CTA 32 KB
+  static constexpr int STAGES = 196608 / STAGE_BYTES;    // 4, a pair 6
+  static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
+  static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * 4096;
+  static constexpr int NBARS = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], mma_done
+  static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t IDESC = idesc_bf16(BM * CG, BN, A_MN, B_MN);
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int& mb, int& nb) {
+  const int per_group = p.group_m * p.tiles_n;
+  const int g = t / per_group;
+  const int first = g * p.group_m;
+  const int gm = min(p.group_m, p.tiles_m - first);
+  const int r = t - g * per_group;
+  mb = first + r % gm;
+  nb = r / gm;
+}
+
+// ----------------------------------------------------------------- staging
+// 32 rows x 128 bytes between global memory (rows `ld` bytes apart, `rows` of
+// them and the first `bytes` bytes of each, a multiple of 16) and a warp's
+// staging buffer; lane = part lane % 8 of rows lane / 8 + 4 i.
+__device__ __forceinline__ void stage_load(uint4 (&r)[8], const uint8_t* src, long long ld, int rows, int bytes, int lane) {
+  const int part = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = (lane >> 3) + 4 * i;
+    r[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows && part * 16 < bytes) r[i] = *reinterpret_cast<const uint4*>(src + row * ld + part * 16);
+  }
+}
+__device__ __forceinline__ void stage_put(uint8_t* stg, const uint4 (&r)[8], int lane) {
+  const int part = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = (lane >> 3) + 4 * i;
+    *reinterpret_cast<uint4*>(stg + row * 128 + ((part ^ (row & 7)) << 4)) = r[i];
+  }
+}
+__device__ __forceinline__ void stage_store(const uint8_t* stg, uint8_t* dst, long long ld, int rows, int bytes, int lane) {
+  const int part = lane & 7;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = (lane >> 3) + 4 * i;
+    const uint4 v = *reinterpret_cast<const uint4*>(stg + row * 128 + ((part ^ (row & 7)) << 4));
+    if (row < rows && part * 16 < bytes && DA_BOUNDS(row < 32 && part < 8))
+      *reinterpret_cast<uint4*>(dst + row * ld + part * 16) = v;
+  }
+}
+// Part `q` (16 bytes) of this lane's own row.
+__device__ __forceinline__ uint4* stage_row(uint8_t* stg, int lane, int q) {
+  return reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// This lane's row of 64 values as bf16, through the staging buffer, to global memory.
+__device__ __forceinline__ void put_bf16_rows(uint8_t* stg, const float (&v)[64], __nv_bfloat16* dst, long long ld,
+                                              int rows, int cols, int lane) {
+  __syncwarp();  // (the buffer's earlier readers)
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *stage_row(stg, lane, q) = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+  __syncwarp();
+  stage_store(stg, reinterpret_cast<uint8_t*>(dst), ld * 2, rows, min(cols, 64) * 2, lane);
+}
+
+// 64 accumulator columns as floats.
+__device__ __forceinline__ void load_cols64(uint32_t taddr, float (&v)[64]) {
+  uint32_t a[32], b[32];
+  tmem_ld32(taddr, a);
+  tmem_ld32(taddr + 32, b);
+  tmem_ld_wait2(a, b);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    v[j] = __uint_as_float(a[j]);
+    v[32 + j] = __uint_as_float(b[j]);
+  }
+}
+
+// ----------------------------------------------------------------- epilogues
+// 64 columns from column c0 (global) of the warp's 32 rows from row r0:
+// `rows` rows and `cols` columns of them exist.  res: the residual's rows as stage_load read them.
+__device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[64], const uint4 (&res)[8], uint8_t* stg,
+                                              long long r0, int c0, int rows, int cols, int lane) {
+  if (p.bias) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      if (4 * q < cols) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + q);
+        v[4 * q] += b.x;
+        v[4 * q + 1] += b.y;
+        v[4 * q + 2] += b.z;
+        v[4 * q + 3] += b.w;
+      }
+  }
+  if (p.pre) put_bf16_rows(stg, v, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane);
+  if (p.act != DIFFATTN_ACT_NONE)
+    with_act(p.act, [&](auto tag) {
+#pragma unroll
+      for (int j = 0; j < 64; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+    });
+  if (p.residual) {
+    __syncwarp();
+    stage_put(stg, res, lane);
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint4 w = *stage_row(stg, lane, q);
+      v[8 * q] += bf16_lo(w.x);
+      v[8 * q + 1] += bf16_hi(w.x);
+      v[8 * q + 2] += bf16_lo(w.y);
+      v[8 * q + 3] += bf16_hi(w.y);
+      v[8 * q + 4] += bf16_lo(w.z);
+      v[8 * q + 5] += bf16_hi(w.z);
+      v[8 * q + 6] += bf16_lo(w.w);
+      v[8 * q + 7] += bf16_hi(w.w);
+    }
+  }
+  put_bf16_rows(stg, v, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
+}
+
+// The same in fp32: 32 columns (a 128-byte row).
+__device__ __forceinline__ void epilogue_f32(const LinearParams& p, float* v, uint8_t* stg, long long r0, int c0, int rows,
+                                             int cols, int lane) {
+  uint4 res[8];
+  if (p.residual)
+    stage_load(res, reinterpret_cast<const uint8_t*>(static_cast<const float*>(p.residual) + r0 * p.ldr + c0), p.ldr * 4,
+               rows, cols * 4, lane);
+  if (p.bias) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (4 * q < cols) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + q);
+        v[4 * q] += b.x;
+        v[4 * q + 1] += b.y;
+        v[4 * q + 2] += b.z;
+        v[4 * q + 3] += b.w;
+      }
+  }
+  if (p.pre) {  // 32 columns of bf16: 64 bytes a row
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *stage_row(stg, lane, q) = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                            pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+    __syncwarp();
+    stage_store(stg, reinterpret_cast<uint8_t*>(p.pre + r0 * p.ldp + c0), p.ldp * 2, rows, min(cols, 32) * 2, lane);
+  }
+  if (p.act != DIFFATTN_ACT_NONE)
+    with_act(p.act, [&](auto tag) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+    });
+  if (p.residual) {
+    __syncwarp();
+    stage_put(stg, res, lane);
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint4 w = *stage_row(stg, lane, q);
+      v[4 * q] += __uint_as_float(w.x);
+      v[4 * q + 1] += __uint_as_float(w.y);
+      v[4 * q + 2] += __uint_as_float(w.z);
+      v[4 * q + 3] += __uint_as_float(w.w);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *stage_row(stg, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                          __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+  __syncwarp();
+  stage_store(stg, reinterpret_cast<uint8_t*>(static_cast<float*>(p.out) + r0 * p.ldo + c0), p.ldo * 4, rows,
+              min(cols, 32) * 4, lane);
+}
+
+// ----------------------------------------------------------------- kernel
+template <int CG, bool A_MN, bool B_MN, int EPI>
+__global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
+    linear_kernel(const __grid_constant__ LinearParams p) {
+  using C = LinearCfg<CG, A_MN, B_MN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
+  uint64_t* full = bars;                   // [STAGES] A and B of a K block landed (in both CTAs)
+  uint64_t* empty = full + C::STAGES;      // [STAGES] the MMAs reading the slot completed
+  uint64_t* acc_full = empty + C::STAGES;  // [2] every MMA of the accumulator completed
+  uint64_t* acc_empty = acc_full + 2;      // [2] the epilogue (of both CTAs) has read the accumulator
+  uint64_t* mma_done = acc_empty + 2;      // every MMA issued completed (abort drain)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int kblocks = (p.K + C::BK - 1) / C::BK;
+  const int seg = EPI == kEpiF32 ? kLinSegBlocks : kblocks;  // K blocks an accumulator sums
+  const int cid = static_cast<int>(blockIdx.x) / CG, ncl = static_cast<int>(gridDim.x) / CG;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], CG * C::EPI_WARPS);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::EPI_WARPS + 1) tmem_alloc_cg<CG>(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const AbortState ab{abort_flag, p.status};
+
+  if (warp == C::EPI_WARPS) {
+    // ================================================================ producer
+    if (lane == 0) {
+      tma_prefetch_desc(&p.tm_a);
+      tma_prefetch_desc(&p.tm_b);
+      long long fill = 0;
+      bool ok = true;
+      for (int t = cid; ok && t < tiles; t += ncl) {
+        int mb, nb;
+        linear_tile(p, t, mb, nb);
+        const int m0 = (mb * CG + static_cast<int>(rank)) * C::BM;
+        // Rows of B: 256 columns of the tile; gated: 128 gate columns, and their up columns N rows further.
+        const int n0 = EPI == kEpiGated ? nb * (C::BN / 2) : nb * C::BN;
+        for (int kb = 0; kb < kblocks; ++kb, ++fill) {
+          const int s = static_cast<int>(fill % C::STAGES);
+          const long long use = fill / C::STAGES;
+          if (use > 0 && !mbar_wait(&empty[s], static_cast<uint32_t>(use - 1) & 1u, ab)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = smem + s * C::STAGE_BYTES;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE_BYTES);
+          const uint32_t bar = CG == 2 ? map_to_rank(&full[s], 0) : 0;
+          auto load = [&](uint8_t* to, const CUtensorMap* map, int c0, int c1) {
+            if (CG == 2)
+              tma_load_2d_pair(to, map, bar, c0, c1);
+            else
+              tma_load_2d(to, map, &full[s], c0, c1);
+          };
+          const int k0 = kb * C::BK;
+          if (!DA_BOUNDS(k0 < p.K)) continue;
+          // A box that starts past its tensor is filled with zeros, as one that ends past it.
+          if (A_MN) {
+            load(dst, &p.tm_a, m0, k0);
+            load(dst + 8192, &p.tm_a, m0 + 64, k0);
+          } else {
+            load(dst, &p.tm_a, k0, m0);
+          }
+#pragma unroll
+          for (int h = 0; h < C::BN_CTA / 128; ++h) {
+            const int part = CG == 2 ? static_cast<int>(rank) : h;  // which 128 of the tile's 256 B rows
+            const int nr = EPI == kEpiGated ? n0 + part * p.N : n0 + part * 128;
+            uint8_t* to = dst + C::A_BYTES + h * 16384;
+            if (B_MN) {
+              load(to, &p.tm_b, nr, k0);
+              load(to + 8192, &p.tm_b, nr + 64, k0);
+            } else {
+              load(to, &p.tm_b, k0, nr);
+            }
+          }
+        }
+      }
+      if (*ab.flag && rank == 0) {
+        // Aborted: the copies already issued land before the CTA exits.
+        for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); f < fill; ++f)
+          mbar_wait_drain(&full[f % C::STAGES], static_cast<uint32_t>(f / C::STAGES) & 1u, kWaitBudgetCycles);
+      }
+    }
+    __syncwarp();
+  } else if (warp == C::EPI_WARPS + 1) {
+    // ================================================================ MMA issuer
+    if (rank == 0) {
+      // K-major: 128-byte rows, 8-row groups 1024 bytes apart.  MN-major: boxes of 64 x 64 (8 KB), groups of
+      // eight k 1024 bytes apart inside one, the next 64 rows 8192 bytes further.
+      const uint64_t dA = sdesc_sw128(smem_u32(smem), A_MN ? 8192 : 16, 1024);
+      const uint64_t dB = sdesc_sw128(smem_u32(smem + C::A_BYTES), B_MN ? 8192 : 16, 1024);
+      constexpr int KA = A_MN ? 2048 : 32, KB = B_MN ? 2048 : 32;  // bytes from one K16 step to the next
+      auto waitp = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool r = __all_sync(0xffffffffu, mbar_wait(bar, parity, ab));
+        tc_fence_after();
+        return r;
+      };
+      long long fill = 0;
+      long long i = 0;  // accumulators of this cluster so far
+      bool ok = true;
+      for (int t = cid; ok && t < tiles; t += ncl) {
+        for (int kb = 0; ok && kb < kblocks; ++kb, ++fill) {
+          const int a = static_cast<int>(i & 1);
+          const bool first = kb % seg == 0;
+          // The epilogue of accumulator i - 2 has read these columns.
+          if (first && i >= 2 && !waitp(&acc_empty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+          const int s = static_cast<int>(fill % C::STAGES);
+          if (!waitp(&full[s], static_cast<uint32_t>(fill / C::STAGES) & 1u)) {
+            ok = false;
+            break;
+          }
+          const uint64_t so = static_cast<uint64_t>((s * C::STAGE_BYTES) >> 4);
+          const uint32_t dacc = tmem + static_cast<uint32_t>(a * C::BN);
+#pragma unroll
+          for (int k = 0; k < C::BK / 16; ++k)
+            mma_cg<CG>(dacc, dA + so + static_cast<uint64_t>((k * KA) >> 4), dB + so + static_cast<uint64_t>((k * KB) >> 4),
+                       C::IDESC, (!first || k > 0) ? 1u : 0u);
+          tc_commit_cg<CG>(&empty[s]);
+          if (kb % seg == seg - 1 || kb == kblocks - 1) {
+            tc_commit_cg<CG>(&acc_full[a]);
+            ++i;
+          }
+        }
+      }
+      tc_commit_cg<CG>(mma_done);
+      if (*ab.flag) mbar_wait_drain(mma_done, 0, kWaitBudgetCycles);
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ epilogue
+    const int wq = warp & 3, half = warp >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    uint8_t* stg = smem + C::OFF_STAGING + warp * 4096;
+    uint32_t empty0[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) empty0[a] = CG == 2 ? map_to_rank(&acc_empty[a], 0) : 0;
+    auto acc_wait = [&](long long i) -> bool {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, ab));
+      tc_fence_after();
+      return got;
+    };
+    auto acc_release = [&](long long i) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster(empty0[i & 1]);
+        else
+          mbar_arrive(&acc_empty[i & 1]);
+      }
+      __syncwarp();
+    };
+    long long i = 0;
+    bool ok = true;
+    for (int t = cid; ok && t < tiles; t += ncl) {
+      int mb, nb;
+      linear_tile(p, t, mb, nb);
+      const long long r0 = static_cast<long long>(mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
+      const int rows = static_cast<int>(min(32ll, static_cast<long long>(p.M) - r0));  // (<= 0: none)
+      if (EPI == kEpiGated) {
+        const int c0 = nb * (C::BN / 2) + half * 64, cols = p.N - c0;
+        if (!acc_wait(i)) break;
+        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 64);
+        float g[64], u[64];
+        load_cols64(acc, g);
+        load_cols64(acc + 128, u);
+        acc_release(i);
+        ++i;
+        if (rows <= 0 || cols <= 0) continue;
+        if (p.pre) {
+          put_bf16_rows(stg, g, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane);
+          put_bf16_rows(stg, u, p.pre + r0 * p.ldp + p.N + c0, p.ldp, rows, cols, lane);
+        }
+        with_act(p.act, [&](auto tag) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j) g[j] = act_of<decltype(tag)::value>(g[j]) * u[j];
+        });
+        put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
+      } else if (EPI == kEpiF32) {
+        const int c0 = nb * C::BN + half * 128, cols = p.N - c0;
+        float v[128];
+        for (int kb = 0; kb < kblocks; kb += seg, ++i) {
+          if (!acc_wait(i)) {
+            ok = false;
+            break;
+          }
+          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 128);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t r[32];
+            tmem_ld32(acc + 32 * q, r);
+            tmem_ld_wait(r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[32 * q + j] = kb == 0 ? __uint_as_float(r[j]) : v[32 * q + j] + __uint_as_float(r[j]);
+          }
+          acc_release(i);
+        }
+        if (!ok) break;
+        if (rows <= 0) continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (cols > 32 * q) epilogue_f32(p, v + 32 * q, stg, r0, c0 + 32 * q, rows, cols - 32 * q, lane);
+      } else {
+        const int c0 = nb * C::BN + half * 128, cols = p.N - c0;
+        uint4 res[8];
+        auto fetch = [&](int q) {
+          if (p.residual && rows > 0 && cols > 64 * q)
+            stage_load(res, reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.residual) + r0 * p.ldr + c0 + 64 * q),
+                       p.ldr * 2, rows, (cols - 64 * q) * 2, lane);
+        };
+        fetch(0);
+        if (!acc_wait(i)) break;
+        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 128);
+        float v[64];
+        load_cols64(acc, v);
+        if (rows > 0 && cols > 0) epilogue_bf16(p, v, res, stg, r0, c0, rows, cols, lane);
+        fetch(1);
+        load_cols64(acc + 64, v);
+        acc_release(i);
+        ++i;
+        if (rows > 0 && cols > 64) epilogue_bf16(p, v, res, stg, r0, c0 + 64, rows, cols - 64, lane);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();  // (no arrival or commit of the other CTA is on its way here any more)
+  if (warp == C::EPI_WARPS + 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace da

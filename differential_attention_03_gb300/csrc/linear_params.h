@@ -1,0 +1,36 @@
+// Parameter blocks of the product kernels (linear.cuh, linear_few.cuh) and of
+// the element-wise parts of their backward pass (act.cuh), shared by the
+// launchers and the host API.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace da {
+
+// What a product kernel does with its accumulator.
+constexpr int kEpiBf16 = 0;   // out = bf16(residual + act(z + bias)); pre = bf16(z + bias)
+constexpr int kEpiF32 = 1;    // the same with out and residual in fp32, sums of K segments added in registers
+constexpr int kEpiGated = 2;  // out = bf16(act(g) u); pre = [bf16(g) | bf16(u)]
+
+constexpr int kLinBM = 128;   // output rows of one CTA (TMEM lanes)
+constexpr int kLinBN = 256;   // accumulator columns of a tile
+constexpr int kLinBK = 64;    // contraction of a ring slot (one 128-byte row)
+constexpr int kLinSegBlocks = 8;  // K blocks (512 values) that one accumulator of kEpiF32 sums
+
+struct LinearParams {
+  CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
+  CUtensorMap tm_b;  // the same over B ({K, N} or {N, K})
+  const float* bias;     // [N] or nullptr
+  const void* residual;  // [M, N] in the output's type or nullptr
+  void* out;
+  __nv_bfloat16* pre;    // [M, N] (gated [M, 2 N]) or nullptr
+  long long ldr, ldo, ldp;
+  int M, N, K;           // gated: N = F
+  int act;
+  int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
+  int* status;
+};
+
+}  // namespace da

@@ -777,6 +777,121 @@ diffattn_status diffattn_v2_cache_keep(diffattn_cache_format fmt, int B, int A, 
                                        void* v_cache, float* k_scales, float* v_scales, const int* lens,
                                        const int* path, const int* nkeep, int* new_lens, void* stream);
 
+/* ------------------------------------------------------------------ the block around the attention layer
+ * A block of a transformer is x + attention(norm(x)), then the same around its
+ * feed-forward half.  The calls below are what stands around diffattn_layer_forward
+ * there: products with bias, activation and residual, the gated feed-forward
+ * product, the norms with a gate and a residual scale, and the backward passes.
+ * Matrices are row-major; a row stride (ld*) counts elements and is at least the
+ * row's width and a multiple of 8 (bf16) or 4 (fp32); bases are 16-byte aligned
+ * (else ERR_ALIGN); products' widths (N, K, D, F) are multiples of 8 (else ERR_SHAPE).
+ * An output may overlap nothing else of its call unless said otherwise (ERR_SHAPE);
+ * rows of two tensors that lie side by side in one buffer do not overlap.
+ * Each call is asynchronous on `stream` and allocates nothing.
+ */
+typedef enum {
+    DIFFATTN_ACT_NONE = 0,      /* z                                                            */
+    DIFFATTN_ACT_RELU = 1,      /* max(z, 0); slope 0 at 0                                      */
+    DIFFATTN_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution's integral             */
+    DIFFATTN_ACT_GELU_TANH = 3, /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3)))            */
+    DIFFATTN_ACT_SILU = 4       /* z / (1 + exp(-z))                                            */
+} diffattn_activation;
+
+/*
+ * z = a w^T + bias, out = residual + act(z): the projection GEMM with what
+ * follows it in its epilogue.
+ *   a [M, K] bf16 (row stride lda), w [N, K] bf16 contiguous, bias fp32 [N] or
+ *   NULL, out [M, N] of out_dt (bf16 or fp32; row stride ldo), residual [M, N]
+ *   of out_dt (row stride ldr) or NULL.  residual may be out (in place).
+ *   pre : bf16 [M, N] contiguous or NULL; z as diffattn_linear_backward needs it.
+ * Accumulation, bias, activation and residual in fp32, one rounding an output.
+ * M = 0 or N = 0 is a no-op.  out_dt not bf16 or fp32, an unknown activation -> ERR_DTYPE.
+ */
+diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long lda, const void* w, const float* bias,
+                                diffattn_activation act, const void* residual, long long ldr, diffattn_dtype out_dt,
+                                void* out, long long ldo, void* pre, void* stream);
+
+/*
+ * Its gradients, given dy [M, N] bf16 (row stride ldy), the gradient of out
+ * (which is also the residual's):  dz = dy act'(z),  da = dz w,  dw = dz^T a,
+ * dbias = sum over the rows of dz.
+ *   pre : z as the forward stored it (bf16); unused with DIFFATTN_ACT_NONE.
+ *   da [M, K] bf16, dw [N, K] of dw_dt (bf16 or fp32), dbias fp32 [N], contiguous;
+ *   any of them may be NULL (not wanted).
+ *   workspace : at least diffattn_linear_backward_workspace(M, N, K) bytes, 256-byte aligned.
+ * Behind an activation dz is rounded to bf16, the tensor cores' operand type,
+ * for da and dw; dbias sums it in fp32.  Sums repeat bit for bit.
+ */
+size_t diffattn_linear_backward_workspace(int M, int N, int K);
+diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, long long lda, const void* w, const void* dy,
+                                         long long ldy, const void* pre, diffattn_activation act, void* da, void* dw,
+                                         diffattn_dtype dw_dt, float* dbias, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * The gated feed-forward product: h = act(x Wg^T) * (x Wu^T), both products,
+ * the activation and their product in one kernel.
+ *   x [M, D] bf16 (row stride ldx), w_gu = [Wg; Wu] [2 F, D] bf16 contiguous,
+ *   h [M, F] bf16 (row stride ldh).
+ *   gu : bf16 [M, 2 F] contiguous or NULL; [x Wg^T | x Wu^T] for the backward pass.
+ * diffattn_linear is the product back to the model's width, with its residual.
+ */
+diffattn_status diffattn_gated_linear(int M, int D, int F, const void* x, long long ldx, const void* w_gu,
+                                      diffattn_activation act, void* h, long long ldh, void* gu, void* stream);
+
+/*
+ * Its gradients, given dh [M, F] bf16 (row stride ldh) and gu:
+ *   dg = dh u act'(g), du = dh act(g) (rounded to bf16), dx = [dg du] w_gu, dw = [dg du]^T x.
+ *   dx [M, D] bf16, dw [2 F, D] of dw_dt (bf16 or fp32), contiguous; either may be NULL.
+ *   workspace : at least diffattn_gated_linear_backward_workspace(M, D, F) bytes, 256-byte aligned.
+ */
+size_t diffattn_gated_linear_backward_workspace(int M, int D, int F);
+diffattn_status diffattn_gated_linear_backward(int M, int D, int F, const void* x, long long ldx, const void* w_gu,
+                                               const void* gu, const void* dh, long long ldh, diffattn_activation act,
+                                               void* dx, void* dw, diffattn_dtype dw_dt, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/*
+ * The norms after and before a block, with its gate and residual scale, in one
+ * pass over the rows:
+ *   p = post ? x / rms(x) * gamma_post : x        rms(x) = sqrt(mean x^2 + eps)
+ *   s = residual + scale * gate * p               (the residual stream behind the block)
+ *   y = s / rms(s) * gamma                        (the next block's input)
+ *   x, y [rows, D] of dt; residual, s [rows, D] of stream_dt, contiguous (16-byte
+ *   aligned).  (dt, stream_dt): both bf16, both fp32, or bf16 on an fp32 stream.
+ *   residual : NULL for none; may be s (in place).  s may be NULL (not wanted).
+ *   gate     : fp32 [gate_rows, D], row r of x under gate row r / (rows / gate_rows):
+ *              gate_rows = 1 one for all, the number of sequences, or rows; NULL: none.
+ *   gamma_post, gamma : fp32 [D], NULL for ones.  y : NULL: without the second norm.
+ *   eps <= 0 selects 1e-5.  D from 1 to 8192 (else ERR_UNSUPPORTED), any of them;
+ *   multiples of 8 are read 16 bytes at a time.
+ * rows not a multiple of gate_rows, neither s nor y wanted -> ERR_SHAPE.
+ */
+diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_dt, int rows, int D, const void* x,
+                                       const void* residual, const float* gate, int gate_rows, float scale, int post,
+                                       const float* gamma_post, const float* gamma, float eps, void* s, void* y,
+                                       void* stream);
+
+/*
+ * Its gradients, given dy (of dt, NULL: y was not used) and ds (of stream_dt, the
+ * gradient that reaches s from the blocks behind, NULL: none), from x, the stored
+ * s and the parameters:
+ *   dx of dt, dresidual of stream_dt, dgate fp32 [gate_rows, D], dgamma_post and
+ *   dgamma fp32 [D]; any of them may be NULL.  dresidual may be ds (in place).
+ *   Neither dy nor ds -> ERR_NULL; dgate without gate, dgamma_post without post,
+ *   dgamma without dy -> ERR_SHAPE.
+ *   workspace : at least diffattn_residual_norm_backward_workspace(rows, D, gate_rows)
+ *   bytes, 256-byte aligned (gate_rows 0 without a gate).
+ * Sums over the rows repeat bit for bit.
+ */
+size_t diffattn_residual_norm_backward_workspace(int rows, int D, int gate_rows);
+diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtype stream_dt, int rows, int D,
+                                                const void* x, const void* s, const void* dy, const void* ds,
+                                                const float* gate, int gate_rows, float scale, int post,
+                                                const float* gamma_post, const float* gamma, float eps, void* dx,
+                                                void* dresidual, float* dgate, float* dgamma_post, float* dgamma,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the library's device status
  * word on the current device.  Returns DIFFATTN_OK, DIFFATTN_ERR_TIMEOUT if a
