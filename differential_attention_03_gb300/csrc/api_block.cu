@@ -127,10 +127,16 @@ diffattn_status launch_product(const char* fn, Kind kind, da::LinearParams& p, i
   diffattn_status st = dh::status_address(&p.status);
   if (st != DIFFATTN_OK) return st;
   const int sms = sms_or_default();
-  const int cg = 1;
-  const int bm = da::kLinBM * cg, bn = kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
-  p.tiles_m = (p.M + bm - 1) / bm;
+  const int bn = kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
   p.tiles_n = (p.N + bn - 1) / bn;
+  // SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
+  auto rounds = [&](int c) {
+    const long long t = ((p.M + da::kLinBM * c - 1ll) / (da::kLinBM * c)) * p.tiles_n;
+    return static_cast<double>((t + sms / c - 1) / (sms / c));
+  };
+  const int cg = rounds(2) * 0.9 <= rounds(1) ? 2 : 1;
+  const int bm = da::kLinBM * cg;
+  p.tiles_m = (p.M + bm - 1) / bm;
   p.group_m = kGroupRows / bm;
   const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x7fffffffll - sms || static_cast<long long>(p.M) + 2 * da::kLinBM > 0x7fffffffll ||

@@ -414,6 +414,9 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
           }
         }
       }
+      // The commits of the last slots have arrived in this CTA (they come from the pair's first CTA).
+      for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); ok && f < fill; ++f)
+        ok = mbar_wait(&empty[f % C::STAGES], static_cast<uint32_t>(f / C::STAGES) & 1u, ab);
       if (*ab.flag && rank == 0) {
         // Aborted: the copies already issued land before the CTA exits.
         for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); f < fill; ++f)
@@ -464,8 +467,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
           }
         }
       }
-      tc_commit_cg<CG>(mma_done);
-      if (*ab.flag) mbar_wait_drain(mma_done, 0, kWaitBudgetCycles);
+      if (__any_sync(0xffffffffu, *ab.flag)) {
+        // Aborted: the MMAs already issued complete before TMEM is freed.
+        tc_commit_cg<CG>(mma_done);
+        mbar_wait_drain(mma_done, 0, kWaitBudgetCycles);
+      }
     }
     __syncwarp();
   } else {
