@@ -122,30 +122,81 @@ enum class Kind { kForward, kGated, kDgrad, kWgrad };
 
 constexpr int kGroupRows = 2048;  // rows of a group of the tile walk
 
-// Tiles, status word and launch of a product whose operands and epilogue are in p.
-diffattn_status launch_product(const char* fn, Kind kind, da::LinearParams& p, int epi, cudaStream_t s) {
+// A product: out [M, N] over a contraction of K.  x: the token rows [M, K] (wgrad: [K, M]); w: [N, K] (gated [2 N, K];
+// dgrad and wgrad [K, N]), rows ldx and ldw apart.
+struct Product {
+  Kind kind;
+  int epi;
+  const void* x;
+  const void* w;
+  long long ldx, ldw;
+};
+
+// How the products for few tokens lay their work out, or nt = 0: linear_kernel's tiles suit it better.
+struct FewPlan {
+  int nt, cs;
+  long long tiles;
+};
+
+FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
+  FewPlan f = {0, 1, 0};
+  if (q.kind == Kind::kWgrad) return f;
+  const int ft = q.kind == Kind::kGated ? 64 : 128;
+  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
+  if (p.M > 128) return f;
+  f.nt = nt;
+  f.tiles = ((p.M + nt - 1ll) / nt) * ((p.N + ft - 1ll) / ft);
+  const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
+  while (f.cs < 8 && f.tiles * f.cs * 2 <= 2ll * sms && kblocks >= 4 * f.cs) f.cs *= 2;
+  return f;
+}
+
+// Descriptors, tiles, status word and launch of a product whose sizes and epilogue are in p.
+diffattn_status launch_product(const char* fn, const Product& q, da::LinearParams& p, cudaStream_t s) {
   diffattn_status st = dh::status_address(&p.status);
   if (st != DIFFATTN_OK) return st;
   const int sms = sms_or_default();
-  const int bn = kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
-  p.tiles_n = (p.N + bn - 1) / bn;
-  // SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
-  auto rounds = [&](int c) {
-    const long long t = ((p.M + da::kLinBM * c - 1ll) / (da::kLinBM * c)) * p.tiles_n;
-    return static_cast<double>((t + sms / c - 1) / (sms / c));
-  };
-  const int cg = rounds(2) * 0.9 <= rounds(1) ? 2 : 1;
-  const int bm = da::kLinBM * cg;
-  p.tiles_m = (p.M + bm - 1) / bm;
-  p.group_m = kGroupRows / bm;
-  const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-  if (tiles > 0x7fffffffll - sms || static_cast<long long>(p.M) + 2 * da::kLinBM > 0x7fffffffll ||
-      2ll * p.N + 2 * da::kLinBN > 0x7fffffffll || static_cast<long long>(p.K) + da::kLinBK > 0x7fffffffll)
+  if (static_cast<long long>(p.M) + 2 * da::kLinBM > 0x7fffffffll || 2ll * p.N + 2 * da::kLinBN > 0x7fffffffll ||
+      static_cast<long long>(p.K) + da::kLinBK > 0x7fffffffll)
     return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
-  const int grid = static_cast<int>(std::min<long long>(tiles, sms / cg)) * cg;
-  const cudaError_t e = kind == Kind::kDgrad   ? da::launch_linear_dgrad(p, cg, grid, s)
-                        : kind == Kind::kWgrad ? da::launch_linear_wgrad(p, epi, cg, grid, s)
-                                               : da::launch_linear_fwd(p, epi, cg, grid, s);
+  const bool x_mn = q.kind == Kind::kWgrad, w_mn = x_mn || q.kind == Kind::kDgrad;
+  const long long wrows = q.kind == Kind::kGated ? 2ll * p.N : p.N;
+  auto map_w = [&](CUtensorMap* m, int box) {
+    return w_mn ? map_rows(m, q.w, p.K, p.N, q.ldw, 64) : map_rows(m, q.w, wrows, p.K, q.ldw, box);
+  };
+  auto map_x = [&](CUtensorMap* m, int box) {
+    return x_mn ? map_rows(m, q.x, p.K, p.M, q.ldx, 64) : map_rows(m, q.x, p.M, p.K, q.ldx, box);
+  };
+  cudaError_t e;
+  const FewPlan f = few_plan(q, p, sms);
+  if (f.nt) {
+    p.cs = f.cs;
+    p.tiles_n = (p.N + (q.kind == Kind::kGated ? 63 : 127)) / (q.kind == Kind::kGated ? 64 : 128);
+    if ((st = map_w(&p.tm_a, q.kind == Kind::kGated ? 64 : 128)) != DIFFATTN_OK) return st;
+    if ((st = map_x(&p.tm_b, f.nt)) != DIFFATTN_OK) return st;
+    if (f.tiles * f.cs > 0x7fffffffll) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+    e = da::launch_linear_few(p, q.epi, w_mn, f.nt, static_cast<int>(f.tiles * f.cs), s);
+  } else {
+    const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
+    p.tiles_n = (p.N + bn - 1) / bn;
+    // SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
+    auto rounds = [&](int c) {
+      const long long t = ((p.M + da::kLinBM * c - 1ll) / (da::kLinBM * c)) * p.tiles_n;
+      return static_cast<double>((t + sms / c - 1) / (sms / c));
+    };
+    const int cg = rounds(2) * 0.9 <= rounds(1) ? 2 : 1;
+    const int bm = da::kLinBM * cg;
+    p.tiles_m = (p.M + bm - 1) / bm;
+    p.group_m = kGroupRows / bm;
+    const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
+    if (tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+    if ((st = map_x(&p.tm_a, 128)) != DIFFATTN_OK) return st;
+    if ((st = map_w(&p.tm_b, 128)) != DIFFATTN_OK) return st;
+    const int grid = static_cast<int>(std::min<long long>(tiles, sms / cg)) * cg;
+    e = q.kind == Kind::kDgrad   ? da::launch_linear_dgrad(p, cg, grid, s)
+        : q.kind == Kind::kWgrad ? da::launch_linear_wgrad(p, q.epi, cg, grid, s)
+                                 : da::launch_linear_fwd(p, q.epi, cg, grid, s);
+  }
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);
   return DIFFATTN_OK;
@@ -156,12 +207,9 @@ diffattn_status dgrad(const char* fn, int M, int N, int C, const void* dz, long 
                       cudaStream_t s) {
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
-  diffattn_status st;
-  if ((st = map_rows(&p.tm_a, dz, M, C, ldz, 128)) != DIFFATTN_OK) return st;
-  if ((st = map_rows(&p.tm_b, w, C, N, N, 64)) != DIFFATTN_OK) return st;
   p.M = M, p.N = N, p.K = C;
   p.out = out, p.ldo = N;
-  return launch_product(fn, Kind::kDgrad, p, da::kEpiBf16, s);
+  return launch_product(fn, Product{Kind::kDgrad, da::kEpiBf16, dz, w, ldz, N}, p, s);
 }
 
 // out [M, N] = dz^T a with dz [C, M] and a [C, N].
@@ -169,12 +217,9 @@ diffattn_status wgrad(const char* fn, int M, int N, int C, const void* dz, long 
                       void* out, diffattn_dtype dt, cudaStream_t s) {
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
-  diffattn_status st;
-  if ((st = map_rows(&p.tm_a, dz, C, M, ldz, 64)) != DIFFATTN_OK) return st;
-  if ((st = map_rows(&p.tm_b, a, C, N, lda, 64)) != DIFFATTN_OK) return st;
   p.M = M, p.N = N, p.K = C;
   p.out = out, p.ldo = N;
-  return launch_product(fn, Kind::kWgrad, p, dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16, s);
+  return launch_product(fn, Product{Kind::kWgrad, dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16, dz, a, ldz, lda}, p, s);
 }
 
 // Row chunks of the element-wise kernels: some eight CTAs an SM, at least 32 rows each.
@@ -239,17 +284,14 @@ diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long ld
   }
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
-  if ((st = map_rows(&p.tm_a, a, M, K, lda, 128)) != DIFFATTN_OK) return st;
-  if ((st = map_rows(&p.tm_b, w, N, K, K, 128)) != DIFFATTN_OK) return st;
   p.bias = bias;
   p.residual = residual;
   p.out = out;
   p.pre = static_cast<__nv_bfloat16*>(pre);
   p.ldr = ldr, p.ldo = ldo, p.ldp = N;
   p.M = M, p.N = N, p.K = K, p.act = act;
-  if ((st = launch_product(fn, Kind::kForward, p, out_dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16,
-                           static_cast<cudaStream_t>(stream))) != DIFFATTN_OK)
-    return st;
+  const Product q = {Kind::kForward, out_dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16, a, w, lda, K};
+  if ((st = launch_product(fn, q, p, static_cast<cudaStream_t>(stream))) != DIFFATTN_OK) return st;
   return dh::success();
 }
 
@@ -344,13 +386,12 @@ diffattn_status diffattn_gated_linear(int M, int D, int F, const void* x, long l
   }
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
-  if ((st = map_rows(&p.tm_a, x, M, D, ldx, 128)) != DIFFATTN_OK) return st;
-  if ((st = map_rows(&p.tm_b, w_gu, 2ll * F, D, D, 128)) != DIFFATTN_OK) return st;
   p.out = h;
   p.pre = static_cast<__nv_bfloat16*>(gu);
   p.ldo = ldh, p.ldp = 2ll * F;
   p.M = M, p.N = F, p.K = D, p.act = act;
-  if ((st = launch_product(fn, Kind::kGated, p, da::kEpiGated, static_cast<cudaStream_t>(stream))) != DIFFATTN_OK) return st;
+  const Product q = {Kind::kGated, da::kEpiGated, x, w_gu, ldx, D};
+  if ((st = launch_product(fn, q, p, static_cast<cudaStream_t>(stream))) != DIFFATTN_OK) return st;
   return dh::success();
 }
 

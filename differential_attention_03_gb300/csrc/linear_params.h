@@ -30,6 +30,7 @@ struct LinearParams {
   int M, N, K;           // gated: N = F
   int act;
   int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
+  int cs;                         // linear_few: CTAs that share a tile's contraction
   int* status;
 };
 
