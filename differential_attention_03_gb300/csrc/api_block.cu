@@ -132,6 +132,18 @@ struct Product {
   long long ldx, ldw;
 };
 
+// Rounds of linear_kernel's tiles over the SMs, in clusters of cg.
+long long tile_rounds(const Product& q, const da::LinearParams& p, int sms, int cg) {
+  const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
+  const long long t = ((p.M + da::kLinBM * cg - 1ll) / (da::kLinBM * cg)) * ((p.N + bn - 1ll) / bn);
+  return (t + sms / cg - 1) / (sms / cg);
+}
+
+// SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
+int best_pair(const Product& q, const da::LinearParams& p, int sms) {
+  return tile_rounds(q, p, sms, 2) * 0.9 <= tile_rounds(q, p, sms, 1) ? 2 : 1;
+}
+
 // How the products for few tokens lay their work out, or nt = 0: linear_kernel's tiles suit it better.
 struct FewPlan {
   int nt, cs;
@@ -143,11 +155,16 @@ FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
   if (q.kind == Kind::kWgrad) return f;
   const int ft = q.kind == Kind::kGated ? 64 : 128;
   const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  if (p.M > 128) return f;
-  f.nt = nt;
-  f.tiles = ((p.M + nt - 1ll) / nt) * ((p.N + ft - 1ll) / ft);
+  const int slots = (nt == 128 ? 1 : 2) * sms;  // CTAs that run at once
   const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
-  while (f.cs < 8 && f.tiles * f.cs * 2 <= 2ll * sms && kblocks >= 4 * f.cs) f.cs *= 2;
+  f.tiles = ((p.M + nt - 1ll) / nt) * ((p.N + ft - 1ll) / ft);
+  while (f.cs < 8 && f.tiles * f.cs * 2 <= slots && kblocks >= 4 * f.cs) f.cs *= 2;
+  if (p.M > 128) {
+    const double few = static_cast<double>((f.tiles * f.cs + slots - 1) / slots) * ((kblocks + f.cs - 1) / f.cs) * 0.20;
+    const double tiles = static_cast<double>(tile_rounds(q, p, sms, best_pair(q, p, sms))) * kblocks * 0.28;
+    if (few > tiles) return f;
+  }
+  f.nt = nt;
   return f;
 }
 
@@ -179,12 +196,7 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
   } else {
     const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
     p.tiles_n = (p.N + bn - 1) / bn;
-    // SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
-    auto rounds = [&](int c) {
-      const long long t = ((p.M + da::kLinBM * c - 1ll) / (da::kLinBM * c)) * p.tiles_n;
-      return static_cast<double>((t + sms / c - 1) / (sms / c));
-    };
-    const int cg = rounds(2) * 0.9 <= rounds(1) ? 2 : 1;
+    const int cg = best_pair(q, p, sms);
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
