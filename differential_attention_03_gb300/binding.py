@@ -1309,38 +1309,59 @@ def _rows(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
 
 
-def _count(shape) -> int:
-    n = 1
-    for k in shape:
-        n *= k
-    return n
+def _here(dev) -> int:
+    """The raw current stream of the current device, which has to be `dev`."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _product(x, w, name, wname):
+    """Of rows x [..., K] under weights w [n, K]: device, n, K, the leading shape, the number of rows, the row stride."""
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if w.dim() != 2 or x.dim() < 1:
+        raise ValueError(f"{name} must be [..., K] and {wname} [n, K]")
+    dev = x.get_device()
+    n, K = w.shape
+    lead = x.shape[:-1]
+    if x.dtype == torch.bfloat16 and x.shape[-1] == K and x.is_contiguous():
+        ld = K
+    else:
+        ld = _rows(x, name, torch.bfloat16, lead + (K,), dev)
+    _on(w, wname, torch.bfloat16, w.shape, dev)
+    return dev, n, K, lead, lead.numel(), ld
 
 
 def _linear(a, w, bias, act, residual, dtype, out, pre, stream):
-    dev = _current(a, "a")
-    if w.dim() != 2 or a.dim() < 1:
-        raise ValueError("a must be [..., K] and w [N, K]")
-    N, K = w.shape
-    lead = a.shape[:-1]
+    dev, N, K, lead, M, lda = _product(a, w, "a", "w")
+    raw = _here(dev) if stream is None else _stream(stream)
     shape = lead + (N,)
-    M = _count(lead)
-    lda = _rows(a, "a", torch.bfloat16, lead + (K,), dev)
-    _on(w, "w", torch.bfloat16, w.shape, dev)
+    ldo = ldr = N
     if out is None:
-        out = _empty(shape, dtype or torch.bfloat16, a.device, stream)
-    elif dtype is not None and out.dtype != dtype:
-        raise ValueError(f"out must be {dtype}, got {out.dtype}")
-    dt = _dt(out)
-    ldo = _rows(out, "out", out.dtype, shape, dev)
-    ldr = 0
+        dtype = dtype or torch.bfloat16
+        out = _empty(shape, dtype, a.device, stream)
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out must be {dtype}, got {out.dtype}")
+        dtype = out.dtype
+        ldo = _rows(out, "out", dtype, shape, dev)
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        code = _act_code(act)
     if bias is not None:
         _on(bias, "bias", torch.float32, (N,), dev)
+        bias = bias.data_ptr()
     if residual is not None:
-        ldr = _rows(residual, "residual", out.dtype, shape, dev)
+        ldr = _rows(residual, "residual", dtype, shape, dev)
+        residual = residual.data_ptr()
     if pre is not None:
         _on(pre, "pre", torch.bfloat16, shape, dev)
-    _check(lib().diffattn_linear(M, N, K, a.data_ptr(), lda, w.data_ptr(), _addr(bias), _act_code(act), _addr(residual),
-                                 ldr, dt, out.data_ptr(), ldo, _addr(pre), _stream(stream)))
+        pre = pre.data_ptr()
+    st = lib().diffattn_linear(M, N, K, a.data_ptr(), lda, w.data_ptr(), bias, code, residual, ldr,
+                               BF16 if dtype is torch.bfloat16 else _dt(out), out.data_ptr(), ldo, pre, raw)
+    if st:
+        _check(st)
     return out
 
 
@@ -1397,15 +1418,9 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     Behind an activation the products take dy act'(pre) rounded to bf16.  out: None or a dict of tensors to
     write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K) bytes.
     """
-    dev = _current(a, "a")
-    if w.dim() != 2 or a.dim() < 1:
-        raise ValueError("a must be [..., K] and w [N, K]")
-    N, K = w.shape
-    lead = a.shape[:-1]
+    dev, N, K, lead, M, lda = _product(a, w, "a", "w")
+    raw = _here(dev) if stream is None else _stream(stream)
     shape = lead + (N,)
-    M = _count(lead)
-    lda = _rows(a, "a", torch.bfloat16, lead + (K,), dev)
-    _on(w, "w", torch.bfloat16, w.shape, dev)
     ldy = _rows(dy, "dy", torch.bfloat16, shape, dev)
     code = _act_code(act)
     if code:
@@ -1424,25 +1439,29 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     _check(lib().diffattn_linear_backward(M, N, K, a.data_ptr(), lda, w.data_ptr(), dy.data_ptr(), ldy,
                                           _addr(pre) if code else None, code, _addr(r.get("da")), _addr(r.get("dw")),
                                           _dt(r["dw"]) if dw else F32, _addr(r.get("dbias")), _addr(ws),
-                                          0 if ws is None else ws.nbytes, _stream(stream)))
+                                          0 if ws is None else ws.nbytes, raw))
     return r
 
 
 def _gated(x, w_gu, act, out, gu, stream):
-    dev = _current(x, "x")
-    if w_gu.dim() != 2 or w_gu.shape[0] % 2 or x.dim() < 1:
-        raise ValueError("x must be [..., D] and w_gu [2 F, D]")
-    F, D = w_gu.shape[0] // 2, w_gu.shape[1]
-    lead = x.shape[:-1]
-    ldx = _rows(x, "x", torch.bfloat16, lead + (D,), dev)
-    _on(w_gu, "w_gu", torch.bfloat16, w_gu.shape, dev)
+    dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
+    raw = _here(dev) if stream is None else _stream(stream)
+    if F2 % 2:
+        raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
+    ldh = F = F2 // 2
     if out is None:
         out = _empty(lead + (F,), torch.bfloat16, x.device, stream)
-    ldh = _rows(out, "out", torch.bfloat16, lead + (F,), dev)
+    else:
+        ldh = _rows(out, "out", torch.bfloat16, lead + (F,), dev)
     if gu is not None:
-        _on(gu, "gu", torch.bfloat16, lead + (2 * F,), dev)
-    _check(lib().diffattn_gated_linear(_count(lead), D, F, x.data_ptr(), ldx, w_gu.data_ptr(), _act_code(act),
-                                       out.data_ptr(), ldh, _addr(gu), _stream(stream)))
+        _on(gu, "gu", torch.bfloat16, lead + (F2,), dev)
+        gu = gu.data_ptr()
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        code = _act_code(act)
+    st = lib().diffattn_gated_linear(M, D, F, x.data_ptr(), ldx, w_gu.data_ptr(), code, out.data_ptr(), ldh, gu, raw)
+    if st:
+        _check(st)
     return out
 
 
@@ -1474,14 +1493,11 @@ def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, d
     the gradients of gu rounded to bf16.  out: None or a dict of tensors to write to; workspace: None or a
     tensor of gated_linear_backward_workspace_bytes(M, D, F) bytes.
     """
-    dev = _current(x, "x")
-    if w_gu.dim() != 2 or w_gu.shape[0] % 2 or x.dim() < 1:
-        raise ValueError("x must be [..., D] and w_gu [2 F, D]")
-    F, D = w_gu.shape[0] // 2, w_gu.shape[1]
-    lead = x.shape[:-1]
-    M = _count(lead)
-    ldx = _rows(x, "x", torch.bfloat16, lead + (D,), dev)
-    _on(w_gu, "w_gu", torch.bfloat16, w_gu.shape, dev)
+    dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
+    raw = _here(dev) if stream is None else _stream(stream)
+    if F2 % 2:
+        raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
+    F = F2 // 2
     _on(gu, "gu", torch.bfloat16, lead + (2 * F,), dev)
     ldh = _rows(dh, "dh", torch.bfloat16, lead + (F,), dev)
     _known(out, ("dx", "dw"))
@@ -1494,7 +1510,7 @@ def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, d
     _check(lib().diffattn_gated_linear_backward(M, D, F, x.data_ptr(), ldx, w_gu.data_ptr(), gu.data_ptr(),
                                                 dh.data_ptr(), ldh, _act_code(act), _addr(r.get("dx")), _addr(r.get("dw")),
                                                 _dt(r["dw"]) if dw else F32, _addr(ws), 0 if ws is None else ws.nbytes,
-                                                _stream(stream)))
+                                                raw))
     return r
 
 
@@ -1506,7 +1522,7 @@ def _gate_rows(gate, x, dev) -> int:
     if gate.dim() == 1:
         n = 1
     elif gate.shape == x.shape:
-        n = _count(x.shape[:-1])
+        n = x.shape[:-1].numel()
     elif gate.dim() == 2:
         n = gate.shape[0]
     else:
@@ -1515,16 +1531,22 @@ def _gate_rows(gate, x, dev) -> int:
     return n
 
 
-def _norm_args(x, stream_dtype, gate, gamma_post, post, gamma):
-    dev = _current(x, "x")
-    D = x.shape[-1]
-    _on(x, "x", x.dtype, x.shape, dev)
-    for name, g in (("gamma_post", gamma_post), ("gamma", gamma)):
-        if g is not None:
-            _on(g, name, torch.float32, (D,), dev)
-    dt = _dt(x)
-    return dev, D, _count(x.shape[:-1]), dt, BF16 if stream_dtype == torch.bfloat16 else F32, _gate_rows(gate, x, dev), (
-        gamma_post is not None if post is None else bool(post))
+def _norm_args(x, stream_dtype, gate, gamma_post, gamma):
+    """Device, width, rows, the types' codes, gate rows."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    dev, shape, dt = x.get_device(), x.shape, x.dtype
+    if not x.is_contiguous():
+        _on(x, "x", dt, shape, dev)
+    D = shape[-1]
+    if gamma_post is not None:
+        _on(gamma_post, "gamma_post", torch.float32, (D,), dev)
+    if gamma is not None:
+        _on(gamma, "gamma", torch.float32, (D,), dev)
+    if stream_dtype is not torch.bfloat16 and stream_dtype is not torch.float32:
+        raise ValueError(f"unsupported dtype {stream_dtype} (bf16 or fp32)")
+    return (dev, D, shape[:-1].numel(), BF16 if dt is torch.bfloat16 else _dt(x),
+            BF16 if stream_dtype is torch.bfloat16 else F32, 0 if gate is None else _gate_rows(gate, x, dev))
 
 
 def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=None, post=None, gamma=None,
@@ -1539,25 +1561,34 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     itself.  Returns (y, s); y is None without the second norm.
     """
     sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or x.dtype)
-    dev, D, rows, dt, sd, gate_rows, post = _norm_args(x, sdt, gate, gamma_post, post, gamma)
-    if sdt not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {sdt} (bf16 or fp32)")
+    dev, D, rows, dt, sd, gate_rows = _norm_args(x, sdt, gate, gamma_post, gamma)
+    raw = _here(dev) if stream is None else _stream(stream)
+    shape = x.shape
     if residual is not None:
-        _on(residual, "residual", sdt, x.shape, dev)
-    if out is None:
-        out = _empty(x.shape, sdt, x.device, stream)
+        _on(residual, "residual", sdt, shape, dev)
+        residual_at = residual.data_ptr()
     else:
-        _on(out, "out", sdt, x.shape, dev)
+        residual_at = None
+    if out is None:
+        out = _like(residual if residual is not None else x, stream) if residual is not None or sdt is x.dtype else _empty(
+            shape, sdt, x.device, stream)
+    else:
+        _on(out, "out", sdt, shape, dev)
     if not norm:
         if y is not None or gamma is not None:
             raise ValueError("y and gamma belong to the second norm")
-    elif y is None:
-        y = _like(x, stream)
+        y_at = None
     else:
-        _on(y, "y", x.dtype, x.shape, dev)
-    _check(lib().diffattn_residual_norm(dt, sd, rows, D, x.data_ptr(), _addr(residual), _addr(gate), gate_rows, scale,
-                                        1 if post else 0, _addr(gamma_post), _addr(gamma), eps, out.data_ptr(), _addr(y),
-                                        _stream(stream)))
+        if y is None:
+            y = _like(x, stream)
+        else:
+            _on(y, "y", x.dtype, shape, dev)
+        y_at = y.data_ptr()
+    st = lib().diffattn_residual_norm(dt, sd, rows, D, x.data_ptr(), residual_at, _addr(gate), gate_rows, scale,
+                                      1 if (gamma_post is not None if post is None else post) else 0, _addr(gamma_post),
+                                      _addr(gamma), eps, out.data_ptr(), y_at, raw)
+    if st:
+        _check(st)
     return y, out
 
 
@@ -1573,9 +1604,9 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
     dgamma (with dy), fp32.  out: None or a dict of tensors to write to (dresidual may be ds); workspace:
     None or a tensor of residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
     """
-    dev, D, rows, dt, sd, gate_rows, post = _norm_args(x, s.dtype, gate, gamma_post, post, gamma)
-    if s.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {s.dtype} (bf16 or fp32)")
+    dev, D, rows, dt, sd, gate_rows = _norm_args(x, s.dtype, gate, gamma_post, gamma)
+    raw = _here(dev) if stream is None else _stream(stream)
+    post = gamma_post is not None if post is None else bool(post)
     _on(s, "s", s.dtype, x.shape, dev)
     if dy is not None:
         _on(dy, "dy", x.dtype, x.shape, dev)
@@ -1595,7 +1626,7 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
                                                  _addr(gate), gate_rows, scale, 1 if post else 0, _addr(gamma_post),
                                                  _addr(gamma), eps, r["dx"].data_ptr(), r["dresidual"].data_ptr(),
                                                  _addr(r.get("dgate")), _addr(r.get("dgamma_post")), _addr(r.get("dgamma")),
-                                                 _addr(ws), 0 if ws is None else ws.nbytes, _stream(stream)))
+                                                 _addr(ws), 0 if ws is None else ws.nbytes, raw))
     return r
 
 

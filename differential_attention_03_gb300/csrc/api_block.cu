@@ -144,28 +144,50 @@ int best_pair(const Product& q, const da::LinearParams& p, int sms) {
   return tile_rounds(q, p, sms, 2) * 0.9 <= tile_rounds(q, p, sms, 1) ? 2 : 1;
 }
 
-// How the products for few tokens lay their work out, or nt = 0: linear_kernel's tiles suit it better.
+// How the products for few tokens lay their work out; nt = 0: linear_kernel's tiles suit it better.
 struct FewPlan {
-  int nt, cs;
+  int nt, width, cs, lg, stages, off_bars, smem;
   long long tiles;
 };
 
+// Estimates in us, above what every product costs, fitted to a sweep of widths and clusters over fourteen shapes from
+// 1 x 1024 x 1024 to 777 x 1024 x 1024 and 16 x 8192 x 8192 on a GB300 (the choice is within 5 % of the best width and
+// cluster on average, 20 % at worst): HBM 5.1 MB a us together with an SM's own stream (230 KB a us, at least 0.064 us
+// a K block; several token tiles, which L2 feeds, 115 KB a us), what a cluster's CTAs hand each other (72 KB a us),
+// and the epilogue.  linear_kernel: 0.26 us a K block and round, 2.6 us more.
 FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
-  FewPlan f = {0, 1, 0};
-  if (q.kind == Kind::kWgrad) return f;
-  const int ft = q.kind == Kind::kGated ? 64 : 128;
-  const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-  const int slots = (nt == 128 ? 1 : 2) * sms;  // CTAs that run at once
+  FewPlan best = {};
+  if (q.kind == Kind::kWgrad) return best;
+  const int sides = q.kind == Kind::kGated ? 2 : 1;
+  const int nt = p.M >= 128 ? 128 : (p.M + 15) / 16 * 16;
+  const long long ttiles = (p.M + nt - 1ll) / nt;
   const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
-  f.tiles = ((p.M + nt - 1ll) / nt) * ((p.N + ft - 1ll) / ft);
-  while (f.cs < 8 && f.tiles * f.cs * 2 <= slots && kblocks >= 4 * f.cs) f.cs *= 2;
-  if (p.M > 128) {
-    const double few = static_cast<double>((f.tiles * f.cs + slots - 1) / slots) * ((kblocks + f.cs - 1) / f.cs) * 0.20;
-    const double tiles = static_cast<double>(tile_rounds(q, p, sms, best_pair(q, p, sms))) * kblocks * 0.28;
-    if (few > tiles) return f;
+  const int step = q.kind == Kind::kDgrad ? 64 : sides == 2 ? 8 : 16, most = 256 / sides;
+  const double hbm = 2.0 * sides * p.N * p.K / 5.1e6, draw = ttiles > 1 ? 115e3 : 230e3;
+  double least = p.M > 128 ? tile_rounds(q, p, sms, best_pair(q, p, sms)) * kblocks * 0.26 + 2.6 : 1e30;
+  if (ttiles * p.N > 0x7fffffffll) return best;
+  for (int cs = 1; cs <= 8 && cs <= kblocks; cs *= 2) {
+    const int nkb = (kblocks + cs - 1) / cs;
+    for (int width = step; width <= most && width < p.N + step; width += step) {
+      const int wrows = width * sides, lg = (width / 8 + cs - 1) / cs;
+      const long long tiles = ttiles * ((p.N + width - 1) / width);
+      const double rounds = static_cast<double>((tiles * cs + sms - 1) / sms);
+      const double stream = rounds * nkb * std::max((wrows + nt) * 128.0 / draw, 0.064);
+      const double end = (cs > 1 ? 0.12 + nt * wrows * (4.0 / 72e3) : 0.0) + std::min(p.M, nt) * lg * sides * 0.001 + wrows * 0.005;
+      const double cost = std::sqrt(stream * stream + hbm * hbm) + rounds * end;
+      if (cost >= least) continue;
+      // ring, partial sums (and, behind the last slot's token rows, what an MMA of 128 rows reads), barriers
+      const int stage = (wrows + nt) * 128, part = std::max(cs * nt * (lg * sides * 8 + 4) * 4, (128 - nt) * 128);
+      const int budget = (rounds > 1 ? 113 * 1024 : da::kFewMaxSmem) - 1024 - part - 512;
+      const int stages = std::min({nkb, budget / stage, 24});
+      if (stages < 1 || (stages < 3 && stages < nkb)) continue;
+      least = cost;
+      best.nt = nt, best.width = width, best.cs = cs, best.lg = lg, best.stages = stages, best.tiles = tiles;
+      best.off_bars = stages * stage + part;
+      best.smem = best.off_bars + (2 * stages + 1) * 8 + 16 + 1024;
+    }
   }
-  f.nt = nt;
-  return f;
+  return best;
 }
 
 // Descriptors, tiles, status word and launch of a product whose sizes and epilogue are in p.
@@ -187,12 +209,12 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
   cudaError_t e;
   const FewPlan f = few_plan(q, p, sms);
   if (f.nt) {
-    p.cs = f.cs;
-    p.tiles_n = (p.N + (q.kind == Kind::kGated ? 63 : 127)) / (q.kind == Kind::kGated ? 64 : 128);
-    if ((st = map_w(&p.tm_a, q.kind == Kind::kGated ? 64 : 128)) != DIFFATTN_OK) return st;
+    p.nt = f.nt, p.width = f.width, p.cs = f.cs, p.lg = f.lg, p.stages = f.stages, p.off_bars = f.off_bars;
+    p.tiles_n = (p.N + f.width - 1) / f.width;
+    if ((st = map_w(&p.tm_a, f.width)) != DIFFATTN_OK) return st;
     if ((st = map_x(&p.tm_b, f.nt)) != DIFFATTN_OK) return st;
     if (f.tiles * f.cs > 0x7fffffffll) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
-    e = da::launch_linear_few(p, q.epi, w_mn, f.nt, static_cast<int>(f.tiles * f.cs), s);
+    e = da::launch_linear_few(p, q.epi, w_mn, static_cast<int>(f.tiles * f.cs), f.smem, s);
   } else {
     const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
     p.tiles_n = (p.N + bn - 1) / bn;

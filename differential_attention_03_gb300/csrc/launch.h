@@ -73,9 +73,8 @@ cudaError_t launch_linear_fwd(const LinearParams& p, int epi, int cg, int grid, 
 // da = dz w (the weights MN-major) and dw = dz^T a (both operands MN-major).
 cudaError_t launch_linear_dgrad(const LinearParams& p, int cg, int grid, cudaStream_t s);
 cudaError_t launch_linear_wgrad(const LinearParams& p, int epi, int cg, int grid, cudaStream_t s);
-// The same for few tokens: tm_a over the features (w_mn: [K, N]), tm_b over the tokens, nt token columns a tile
-// (16, 32, 64 or 128), clusters of p.cs CTAs.
-cudaError_t launch_linear_few(const LinearParams& p, int epi, bool w_mn, int nt, int grid, cudaStream_t s);
+// The same for few tokens: tm_a over the features (w_mn: [K, N]), tm_b over the tokens, clusters of p.cs CTAs.
+cudaError_t launch_linear_few(const LinearParams& p, int epi, bool w_mn, int grid, int smem_bytes, cudaStream_t s);
 // The element-wise part of their backward pass, and the sums over partial rows.
 cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s);
 cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s);

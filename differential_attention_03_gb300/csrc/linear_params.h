@@ -19,6 +19,8 @@ constexpr int kLinBN = 256;   // accumulator columns of a tile
 constexpr int kLinBK = 64;    // contraction of a ring slot (one 128-byte row)
 constexpr int kLinSegBlocks = 8;  // K blocks (512 values) that one accumulator of kEpiF32 sums
 
+constexpr int kFewMaxSmem = 232448;
+
 struct LinearParams {
   CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
   CUtensorMap tm_b;  // the same over B ({K, N} or {N, K})
@@ -30,7 +32,9 @@ struct LinearParams {
   int M, N, K;           // gated: N = F
   int act;
   int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
-  int cs;                         // linear_few: CTAs that share a tile's contraction
+  // linear_few: features (gated: gate features) and token rows of a tile, CTAs that share its contraction, groups of
+  // eight features that each of them finishes, ring slots, and where the barriers lie in shared memory
+  int width, nt, cs, lg, stages, off_bars;
   int* status;
 };
 
