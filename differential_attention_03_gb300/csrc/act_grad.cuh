@@ -82,25 +82,26 @@ __global__ void __launch_bounds__(kActGradThreads) act_grad_kernel(const ActGrad
   }
 }
 
-// 32 columns a CTA; its eight warps take every eighth partial row, then add up in order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const SumParts p) {
-  __shared__ float sums[8][32];
+// 32 columns a CTA; its 32 warps take every 32nd partial row, then add up in order.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const SumParts p) {
+  __shared__ float sums[32][33];
   const int k = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long col = static_cast<long long>(blockIdx.x) * 32 + lane;
   if (static_cast<long long>(blockIdx.x) * 32 >= p.width[k]) return;
+  grid_dep_wait();
   float t = 0.f;
   if (col < p.width[k]) {
 #pragma unroll 4
-    for (int c = warp; c < p.count[k]; c += 8) t += p.part[k][c * p.width[k] + col];
+    for (int c = warp; c < p.count[k]; c += 32) t += p.part[k][c * p.width[k] + col];
   }
   sums[warp][lane] = t;
   __syncthreads();
-  if (warp == 0 && col < p.width[k]) {
-    t = 0.f;
+  // (transposed: warp w adds up column w by shuffles, in a fixed order)
+  t = sums[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += sums[w][lane];
-    DA_STORE(p.dst[k], col, p.width[k], t);
-  }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const long long out = static_cast<long long>(blockIdx.x) * 32 + warp;
+  if (lane == 0 && out < p.width[k]) DA_STORE(p.dst[k], out, p.width[k], t);
 }
 
 }  // namespace da

@@ -488,16 +488,40 @@ diffattn_status diffattn_gated_linear_backward(int M, int D, int F, const void* 
 // ----------------------------------------------------------------- norms
 namespace {
 
-// How a row of D elements is laid over threads: 16-byte vectors (8 elements) where rows allow it.  A warp a row up
-// to 256 elements; above, a CTA a row, a vector a thread up to 4096 elements and two above.
-da::NormShape norm_shape(int D, bool vec) {
+// How a row of D elements is laid over threads: 16-byte vectors (8 elements) where rows allow it.  A power of two of
+// lanes up to 256 elements; above, a CTA a row, 8 elements a thread up to 4096 and 16 above.
+da::NormShape norm_shape(int D) {
+  const bool vec = D % 8 == 0;
+  const int per = D > 4096 ? 16 : 8;  // elements a thread
   da::NormShape h;
   h.vec = vec ? 8 : 1;
-  const int per = vec ? (D > 4096 ? 16 : 8) : (D > 4096 ? 16 : 8);  // elements a thread
-  h.warp = D <= 256;
   h.nv = per / h.vec;
-  h.threads = h.warp ? 256 : std::max(64, (((D + per - 1) / per) + 31) / 32 * 32);
+  h.lanes = 32;
+  if (D <= 256) {
+    h.layout = vec ? da::kSubWarp : da::kPlainWarp;
+    h.threads = 256;
+    if (vec)
+      for (h.lanes = 4; h.lanes * 8 < D;) h.lanes *= 2;
+  } else {
+    h.layout = vec ? da::kRing : da::kPlain;
+    h.threads = ((D + per - 1) / per + 31) / 32 * 32;
+  }
   return h;
+}
+
+int norm_workers(const da::NormShape& h) { return h.layout == da::kRing || h.layout == da::kPlain ? 1 : h.threads / h.lanes; }
+
+// Ring slots and dynamic shared memory where rows take `slot` bytes, for up to `ctas` CTAs an SM: some 128 KB an SM on
+// its way.  Returns how many CTAs an SM then holds.
+int norm_ring(const da::NormShape& h, long long slot, int ctas, int* stages, int* smem) {
+  *stages = 0;
+  *smem = 0;
+  if (h.layout != da::kRing) return ctas;
+  while (ctas > 1 && slot > da::kNormMaxSmem / ctas - 1152) --ctas;
+  const long long room = da::kNormMaxSmem / ctas - 1152;
+  *stages = static_cast<int>(std::max(1ll, std::min({8ll, room / slot, std::max(2ll, (128ll * 1024 / ctas) / slot)})));
+  *smem = static_cast<int>(128 + *stages * slot);
+  return ctas;
 }
 
 diffattn_status norm_common(const char* fn, int dt, int sdt, int rows, int D, const float* gate, int gate_rows) {
@@ -510,29 +534,29 @@ diffattn_status norm_common(const char* fn, int dt, int sdt, int rows, int D, co
   return DIFFATTN_OK;
 }
 
-// Workers and pieces of the backward pass.  A piece is a run of rows that share a gate row; a worker takes a
-// contiguous range of pieces and keeps its sums over them.
+// Pieces of the backward pass: runs of rows that are summed over together.  A CTA takes neighbouring pieces.
 struct NormPlan {
   long long groups, group_rows, chunk_rows, pieces;
-  int chunks;
-  int grid;
-  long long workers;
+  int chunks, grid;
 };
 
-constexpr int kNormCtas = 152 * 2;  // backward: about two CTAs an SM (eight workers each where a warp takes a row)
+// CTAs an SM of the backward kernel: 512 threads together (128 registers each), eight CTAs at most.
+int norm_grad_per_sm(const da::NormShape& h) { return std::max(1, std::min(8, 512 / h.threads)); }
 
 NormPlan norm_plan(int rows, int D, int gate_rows) {
   NormPlan n;
-  const long long per_cta = D <= 256 ? 8 : 1;
-  n.groups = gate_rows > 0 ? gate_rows : 1;
-  n.group_rows = std::max<long long>(1, rows / n.groups);
-  const long long want = std::max<long long>(1, std::min<long long>(rows, kNormCtas * per_cta));
-  const long long chunks = n.groups >= want ? 1 : std::min(n.group_rows, (want + n.groups - 1) / n.groups);
+  const da::NormShape h = norm_shape(D);
+  const int workers = norm_workers(h);
+  n.groups = gate_rows > 0 && gate_rows < rows ? gate_rows : 1;
+  n.group_rows = rows / n.groups;
+  const long long want = std::max<long long>(1, std::min<long long>((rows + workers - 1) / workers, 152 * norm_grad_per_sm(h)));
+  // A piece a CTA where groups are few; several smaller pieces a CTA where whole groups would leave CTAs unequal.
+  const long long pieces = 2 * n.groups <= want ? want / n.groups : n.groups < 4 * want ? (4 * want + n.groups - 1) / n.groups : 1;
+  const long long chunks = std::max(1ll, std::min(pieces, (n.group_rows + workers - 1) / workers));
   n.chunk_rows = (n.group_rows + chunks - 1) / chunks;
   n.chunks = static_cast<int>((n.group_rows + n.chunk_rows - 1) / n.chunk_rows);
   n.pieces = n.groups * n.chunks;
-  n.grid = static_cast<int>((std::min(n.pieces, want) + per_cta - 1) / per_cta);
-  n.workers = n.grid * per_cta;
+  n.grid = static_cast<int>(std::min(n.pieces, want));
   return n;
 }
 
@@ -568,16 +592,21 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
   p.x = x, p.residual = residual, p.gate = gate, p.gamma_post = gamma_post, p.gamma = gamma;
   p.s_out = s_out, p.y_out = y;
   p.rows = rows, p.D = D;
+  p.gate_rows = gate ? gate_rows : 0;
   p.groups = gate ? gate_rows : 1;
   p.group_rows = rows / p.groups;
   p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
   p.post = post ? 1 : 0, p.norm = y ? 1 : 0;
-  const da::NormShape h = norm_shape(D, D % 8 == 0);
-  const long long ctas = h.warp ? (rows + 7ll) / 8 : rows;
-  // As many CTAs as an SM holds at once (2048 threads, 16 of the narrow ones); each walks its rows.
-  const int per_sm = std::max(1, std::min(16, 2048 / h.threads));
-  const int grid = static_cast<int>(std::min<long long>(ctas, static_cast<long long>(sms_or_default()) * per_sm));
-  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, false, grid,
+  if ((st = dh::status_address(&p.status)) != DIFFATTN_OK) return st;
+  const da::NormShape h = norm_shape(D);
+  const int workers = norm_workers(h);
+  p.lanes = h.lanes;
+  // As many CTAs as an SM holds at once (up to 64 registers a thread); each walks its rows.
+  int smem;
+  const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)),
+                               std::max(1, std::min(16, 1024 / h.threads)), &p.stages, &smem);
+  const int grid = static_cast<int>(std::min<long long>((rows + workers - 1ll) / workers, static_cast<long long>(sms_or_default()) * per_sm));
+  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, false, grid, smem,
                                                  static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);
@@ -587,7 +616,7 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
 size_t diffattn_residual_norm_backward_workspace(int rows, int D, int gate_rows) {
   if (rows < 1 || D < 1 || gate_rows < 0) return 0;
   const NormPlan n = norm_plan(rows, D, gate_rows);
-  return 2 * round256(static_cast<size_t>(n.workers) * D * 4) +
+  return 2 * round256(static_cast<size_t>(n.grid) * D * 4) +
          (gate_rows > 0 && n.chunks > 1 ? round256(static_cast<size_t>(n.pieces) * D * 4) : 0);
 }
 
@@ -632,7 +661,7 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
     if ((st = disjoint(fn, wr, 6, rd, 7)) != DIFFATTN_OK) return st;
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t part = round256(static_cast<size_t>(n.workers) * D * 4);
+  const size_t part = round256(static_cast<size_t>(n.grid) * D * 4);
   da::NormParams p;
   memset(&p, 0, sizeof(p));
   p.x = x, p.s = s_in, p.dy = dy, p.ds = ds, p.gate = gate, p.gamma_post = gamma_post, p.gamma = gamma;
@@ -640,12 +669,21 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
   p.part_gamma = dgamma ? reinterpret_cast<float*>(ws) : nullptr;
   p.part_post = dgamma_post ? reinterpret_cast<float*>(ws + part) : nullptr;
   p.part_gate = !dgate ? nullptr : n.chunks > 1 ? reinterpret_cast<float*>(ws + 2 * part) : dgate;
-  p.rows = rows, p.group_rows = n.group_rows, p.groups = n.groups, p.chunk_rows = n.chunk_rows, p.pieces = n.pieces;
+  const bool row_gate = gate && gate_rows == rows;
+  if (row_gate) p.part_gate = dgate;
+  p.rows = rows, p.gate_rows = gate ? gate_rows : 0;
+  p.group_rows = n.group_rows, p.groups = n.groups, p.chunk_rows = n.chunk_rows, p.pieces = n.pieces;
   p.chunks = n.chunks, p.D = D;
   p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
   p.post = post ? 1 : 0, p.norm = dy ? 1 : 0;
-  cudaError_t e = da::launch_residual_norm(p, norm_shape(D, D % 8 == 0), dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, true,
-                                           n.grid, s);
+  if ((st = dh::status_address(&p.status)) != DIFFATTN_OK) return st;
+  const da::NormShape h = norm_shape(D);
+  p.lanes = h.lanes;
+  int smem;
+  norm_ring(h, D * ((dy ? xe + se : 0) + (ds ? se : 0) + (post || dgate ? xe : 0) + (row_gate ? 4 : 0)),
+            norm_grad_per_sm(h), &p.stages, &smem);
+  if (h.layout == da::kSubWarp || h.layout == da::kPlainWarp) smem = norm_workers(h) * D * 4;  // sums over the CTA's workers
+  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, true, n.grid, smem, s);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);
   da::SumParts q;
@@ -655,9 +693,9 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
     q.part[k] = from, q.dst[k] = to, q.width[k] = width, q.count[k] = static_cast<int>(count);
     ++k;
   };
-  if (dgamma) add(p.part_gamma, dgamma, D, n.workers);
-  if (dgamma_post) add(p.part_post, dgamma_post, D, n.workers);
-  if (dgate && n.chunks > 1) add(p.part_gate, dgate, static_cast<long long>(n.groups) * D, n.chunks);
+  if (dgamma) add(p.part_gamma, dgamma, D, n.grid);
+  if (dgamma_post) add(p.part_post, dgamma_post, D, n.grid);
+  if (dgate && !row_gate && n.chunks > 1) add(p.part_gate, dgate, static_cast<long long>(n.groups) * D, n.chunks);
   if (k > 0 && (st = sum_parts(fn, q, s)) != DIFFATTN_OK) return st;
   return dh::success();
 }

@@ -9,6 +9,9 @@
 namespace da {
 
 constexpr int kNormMaxD = 8192;
+constexpr int kNormMaxSmem = 200 * 1024;
+// Layouts of a row (residual_norm.cuh).
+enum NormLayout { kSubWarp, kRing, kPlain, kPlainWarp };
 
 struct ActGradParams {
   const __nv_bfloat16* dy;   // [M, N] (gated: dh [M, N])
@@ -32,27 +35,28 @@ struct NormParams {
   const void* residual;  // [rows, D] or nullptr (forward)
   const void* s;         // the stored sum (backward)
   const void *dy, *ds;   // gradients of y and s, either may be nullptr (backward)
-  const float* gate;     // [groups, D] or nullptr
+  const float* gate;     // [gate_rows, D] or nullptr
   const float *gamma_post, *gamma;  // [D] or nullptr: ones
   void *s_out, *y_out;              // forward; either may be nullptr
   void *dx, *dresidual;             // backward; either may be nullptr
-  float *part_gamma, *part_post;    // [workers][D] or nullptr
-  float* part_gate;                 // [chunks][groups][D], or dgate itself with one chunk; nullptr: not wanted
-  long long rows;
-  long long group_rows;  // rows that share a row of `gate`
-  long long groups;
-  long long chunk_rows;  // rows of a worker's piece of a group (backward)
-  long long pieces;      // groups * chunks (backward)
+  float *part_gamma, *part_post;    // [CTAs][D] or nullptr
+  float* part_gate;                 // [chunks][groups][D]; dgate itself with one chunk, or a gate a row; nullptr: not wanted
+  long long rows, gate_rows;
+  // Rows that share a gate row (forward).  Backward: groups of rows that are summed over together (with a gate a row: all
+  // rows are one group), in `chunks` pieces of chunk_rows rows; pieces = groups * chunks.
+  long long groups, group_rows, chunk_rows, pieces;
   int chunks;
   int D;
+  int lanes;   // lanes that share a row (kSubWarp, kPlainWarp)
+  int stages;  // rows on their way (kRing)
   float scale, eps;
-  int post, norm;        // whether x is normed, whether y is wanted or given
+  int post, norm;  // whether x is normed, whether y is wanted or given
+  int* status;
 };
 
-// How a row is laid over threads: `nv` vectors of `vec` elements each; warp: a warp a row.
+// How a row is laid over threads: `nv` vectors of `vec` elements a thread; layout: NormLayout.
 struct NormShape {
-  int vec, nv, threads;
-  bool warp;
+  int vec, nv, threads, layout, lanes;
 };
 
 }  // namespace da

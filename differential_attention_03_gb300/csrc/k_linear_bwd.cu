@@ -44,8 +44,16 @@ cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s) {
   for (; n < 3 && p.count[n] > 0; ++n)
     if (p.width[n] > widest) widest = p.width[n];
   if (n == 0) return cudaSuccess;
-  sum_parts_kernel<<<dim3(static_cast<unsigned>((widest + 31) / 32), n), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((widest + 31) / 32), n);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sum_parts_kernel, p);
 }
 
 }  // namespace da

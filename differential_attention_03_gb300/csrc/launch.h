@@ -79,7 +79,7 @@ cudaError_t launch_linear_few(const LinearParams& p, int epi, bool w_mn, int gri
 cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s);
 cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s);
 // The norms around a block, forward or backward.
-cudaError_t launch_residual_norm(const NormParams& p, const NormShape& h, bool x_f32, bool s_f32, bool grad, int grid,
+cudaError_t launch_residual_norm(const NormParams& p, const NormShape& h, bool x_f32, bool s_f32, bool grad, int grid, int smem,
                                  cudaStream_t s);
 cudaError_t launch_wait_selftest(unsigned long long budget_cycles, int* status, cudaStream_t s);
 
