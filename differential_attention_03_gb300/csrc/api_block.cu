@@ -488,14 +488,15 @@ diffattn_status diffattn_gated_linear_backward(int M, int D, int F, const void* 
 // ----------------------------------------------------------------- norms
 namespace {
 
-// How a row of D elements is laid over threads: 16-byte vectors (8 elements) where rows allow it.  A power of two of
-// lanes up to 256 elements; above, a CTA a row, 8 elements a thread up to 4096 and 16 above.
-da::NormShape norm_shape(int D) {
-  const bool vec = D % 8 == 0;
-  const int per = D > 4096 ? 16 : 8;  // elements a thread
+// How a row of D elements is laid over threads.  Rows of 16-byte multiples: vectors of 8 elements, a power of two of
+// lanes up to 256 elements, above a CTA a row with one or two vectors a thread: forward two above 512 elements;
+// backward one (of two rows at once) up to 4096, as 512 threads are the most.  Other rows: 8 single elements a thread
+// (backward above 4096: 16).
+da::NormShape norm_shape(int D, bool grad) {
   da::NormShape h;
+  const bool vec = D % 8 == 0;
   h.vec = vec ? 8 : 1;
-  h.nv = per / h.vec;
+  h.nv = vec ? (D > (grad ? 4096 : 512) ? 2 : 1) : (grad && D > 4096 ? 16 : 8);
   h.lanes = 32;
   if (D <= 256) {
     h.layout = vec ? da::kSubWarp : da::kPlainWarp;
@@ -503,23 +504,25 @@ da::NormShape norm_shape(int D) {
     if (vec)
       for (h.lanes = 4; h.lanes * 8 < D;) h.lanes *= 2;
   } else {
+    const int per = h.vec * h.nv;
     h.layout = vec ? da::kRing : da::kPlain;
     h.threads = ((D + per - 1) / per + 31) / 32 * 32;
   }
   return h;
 }
 
-int norm_workers(const da::NormShape& h) { return h.layout == da::kRing || h.layout == da::kPlain ? 1 : h.threads / h.lanes; }
+bool norm_row_cta(const da::NormShape& h) { return h.layout == da::kRing || h.layout == da::kPlain; }
+int norm_workers(const da::NormShape& h) { return norm_row_cta(h) ? 1 : h.threads / h.lanes; }
 
-// Ring slots and dynamic shared memory where rows take `slot` bytes, for up to `ctas` CTAs an SM: some 128 KB an SM on
-// its way.  Returns how many CTAs an SM then holds.
-int norm_ring(const da::NormShape& h, long long slot, int ctas, int* stages, int* smem) {
+// Ring slots and dynamic shared memory where rows take `slot` bytes (and a CTA `extra` more), for up to `ctas` CTAs an
+// SM: some 128 KB an SM on its way.  Returns how many CTAs an SM then holds.
+int norm_ring(const da::NormShape& h, long long slot, long long extra, int ctas, int* stages, int* smem) {
   *stages = 0;
   *smem = 0;
   if (h.layout != da::kRing) return ctas;
-  while (ctas > 1 && slot > da::kNormMaxSmem / ctas - 1152) --ctas;
-  const long long room = da::kNormMaxSmem / ctas - 1152;
-  *stages = static_cast<int>(std::max(1ll, std::min({8ll, room / slot, std::max(2ll, (128ll * 1024 / ctas) / slot)})));
+  while (ctas > 1 && slot + extra > da::kNormMaxSmem / ctas - 1152) --ctas;
+  const long long room = da::kNormMaxSmem / ctas - 1152 - extra;
+  *stages = static_cast<int>(std::max(1ll, std::min({static_cast<long long>(da::kNormMaxStages), room / slot, std::max(4ll, (128ll * 1024 / ctas) / slot)})));
   *smem = static_cast<int>(128 + *stages * slot);
   return ctas;
 }
@@ -545,7 +548,7 @@ int norm_grad_per_sm(const da::NormShape& h) { return std::max(1, std::min(8, 51
 
 NormPlan norm_plan(int rows, int D, int gate_rows) {
   NormPlan n;
-  const da::NormShape h = norm_shape(D);
+  const da::NormShape h = norm_shape(D, true);
   const int workers = norm_workers(h);
   n.groups = gate_rows > 0 && gate_rows < rows ? gate_rows : 1;
   n.group_rows = rows / n.groups;
@@ -598,13 +601,13 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
   p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
   p.post = post ? 1 : 0, p.norm = y ? 1 : 0;
   if ((st = dh::status_address(&p.status)) != DIFFATTN_OK) return st;
-  const da::NormShape h = norm_shape(D);
+  const da::NormShape h = norm_shape(D, false);
   const int workers = norm_workers(h);
   p.lanes = h.lanes;
-  // As many CTAs as an SM holds at once (up to 64 registers a thread); each walks its rows.
+  // As many CTAs as an SM holds at once (64 registers a thread; the ring kernel 128); each walks its rows.
   int smem;
-  const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)),
-                               std::max(1, std::min(16, 1024 / h.threads)), &p.stages, &smem);
+  const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)), 0,
+                               std::max(1, std::min(16, (h.layout == da::kRing ? 512 : 1024) / h.threads)), &p.stages, &smem);
   const int grid = static_cast<int>(std::min<long long>((rows + workers - 1ll) / workers, static_cast<long long>(sms_or_default()) * per_sm));
   const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, false, grid, smem,
                                                  static_cast<cudaStream_t>(stream));
@@ -677,12 +680,15 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
   p.scale = scale, p.eps = eps > 0.f ? eps : 1e-5f;
   p.post = post ? 1 : 0, p.norm = dy ? 1 : 0;
   if ((st = dh::status_address(&p.status)) != DIFFATTN_OK) return st;
-  const da::NormShape h = norm_shape(D);
+  const da::NormShape h = norm_shape(D, true);
   p.lanes = h.lanes;
   int smem;
-  norm_ring(h, D * ((dy ? xe + se : 0) + (ds ? se : 0) + (post || dgate ? xe : 0) + (row_gate ? 4 : 0)),
+  norm_ring(h, D * ((dy ? xe + se : 0) + (ds ? se : 0) + (post || dgate ? xe : 0) + (row_gate ? 4 : 0)), 4ll * D,
             norm_grad_per_sm(h), &p.stages, &smem);
-  if (h.layout == da::kSubWarp || h.layout == da::kPlainWarp) smem = norm_workers(h) * D * 4;  // sums over the CTA's workers
+  // Behind the ring: sums for dgamma_post.  Rows of warps: two such arrays a worker (those sums, and room to join them).
+  if (!norm_row_cta(h)) smem = norm_workers(h) * D * 4;
+  p.off_post = smem;
+  smem += norm_workers(h) * D * 4;
   const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, true, n.grid, smem, s);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);

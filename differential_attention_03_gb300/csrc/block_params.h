@@ -10,6 +10,7 @@ namespace da {
 
 constexpr int kNormMaxD = 8192;
 constexpr int kNormMaxSmem = 200 * 1024;
+constexpr int kNormMaxStages = 8;
 // Layouts of a row (residual_norm.cuh).
 enum NormLayout { kSubWarp, kRing, kPlain, kPlainWarp };
 
@@ -49,6 +50,7 @@ struct NormParams {
   int D;
   int lanes;   // lanes that share a row (kSubWarp, kPlainWarp)
   int stages;  // rows on their way (kRing)
+  int off_post;  // where the sums for dgamma_post lie in shared memory (backward): D floats, or D a worker of the CTA
   float scale, eps;
   int post, norm;  // whether x is normed, whether y is wanted or given
   int* status;

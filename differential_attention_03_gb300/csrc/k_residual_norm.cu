@@ -6,8 +6,12 @@ namespace da {
 
 namespace {
 
-template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
-cudaError_t launch_as(const NormParams& p, bool grad, int grid, int threads, int smem, cudaStream_t s) {
+template <class Kernel>
+cudaError_t launch_kernel(Kernel kernel, const NormParams& p, int grid, int threads, int smem, cudaStream_t s) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -18,25 +22,27 @@ cudaError_t launch_as(const NormParams& p, bool grad, int grid, int threads, int
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto kernel) {
-    if (LAYOUT == kRing) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-  };
-  return grad ? go(residual_norm_grad_kernel<TX, TS, VEC, NV, LAYOUT>) : go(residual_norm_kernel<TX, TS, VEC, NV, LAYOUT>);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <typename TX, typename TS>
 cudaError_t launch_types(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s) {
+  auto go = [&](auto kernel) { return launch_kernel(kernel, p, grid, h.threads, smem, s); };
+  if (grad) switch (h.layout) {
+      case kSubWarp: return go(residual_norm_grad_kernel<TX, TS, 8, 1, kSubWarp>);
+      case kPlainWarp: return go(residual_norm_grad_kernel<TX, TS, 1, 8, kPlainWarp>);
+      case kPlain:
+        return h.nv == 8 ? go(residual_norm_grad_kernel<TX, TS, 1, 8, kPlain>) : go(residual_norm_grad_kernel<TX, TS, 1, 16, kPlain>);
+      default:
+        if (h.nv == 2) return go(residual_norm_grad_kernel<TX, TS, 8, 2, kRing>);
+        if (!p.norm || p.stages < 2) return go(residual_norm_grad_kernel<TX, TS, 8, 1, kRing>);
+        return p.post ? go(residual_norm_grad_pairs_kernel<TX, TS, true>) : go(residual_norm_grad_pairs_kernel<TX, TS, false>);
+    }
   switch (h.layout) {
-    case kSubWarp: return launch_as<TX, TS, 8, 1, kSubWarp>(p, grad, grid, h.threads, smem, s);
-    case kPlainWarp: return launch_as<TX, TS, 1, 8, kPlainWarp>(p, grad, grid, h.threads, smem, s);
-    case kPlain: return h.nv == 8 ? launch_as<TX, TS, 1, 8, kPlain>(p, grad, grid, h.threads, smem, s)
-                                  : launch_as<TX, TS, 1, 16, kPlain>(p, grad, grid, h.threads, smem, s);
-    default: return h.nv == 1 ? launch_as<TX, TS, 8, 1, kRing>(p, grad, grid, h.threads, smem, s)
-                              : launch_as<TX, TS, 8, 2, kRing>(p, grad, grid, h.threads, smem, s);
+    case kSubWarp: return go(residual_norm_kernel<TX, TS, 8, 1, kSubWarp>);
+    case kPlainWarp: return go(residual_norm_kernel<TX, TS, 1, 8, kPlainWarp>);
+    case kPlain: return go(residual_norm_kernel<TX, TS, 1, 8, kPlain>);
+    default: return h.nv == 1 ? go(residual_norm_kernel<TX, TS, 8, 1, kRing>) : go(residual_norm_kernel<TX, TS, 8, 2, kRing>);
   }
 }
 

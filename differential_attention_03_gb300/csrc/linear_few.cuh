@@ -1,0 +1,314 @@
+// The products of linear.cuh for few tokens (sm_103a): the weights stream
+// through once, so HBM (or L2) bounds them, not the tensor cores.
+//
+// A CTA owns `width` features (the MMA's columns; gated: width gate rows and
+// their up rows) of up to 128 tokens (its rows; only p.nt of them are loaded, and
+// rows past them multiply what lies behind in shared memory into accumulator
+// rows that nothing reads).  A cluster of cs CTAs shares the contraction of
+// one tile.  The host picks width and cs so that one round of CTAs covers the
+// SMs evenly, whatever the model's width.
+//   warps 0-7   accumulators (thread = token, half of the columns a warp) as
+//               fp32 to the CTA of the cluster that finishes the feature (lg
+//               groups of eight features each), through distributed shared
+//               memory, 16 bytes a store; after one cluster barrier all warps
+//               sum what came, in the order of the ranks, and do the epilogue.
+//   warp 8      TMA producer: its first loads are under way before the CTA's
+//               other warps have their barriers and TMEM.
+//   warp 9      TMEM allocator and MMA issuer.
+// A programmatic dependent launch: the CTAs come up while the kernel before
+// them ends, and wait for its end before they touch global memory.
+// Results repeat bit for bit (no atomics).  kEpiF32 sums K segments in
+// accumulators of their own, for the tensor cores' truncation (see linear.cuh).
+#pragma once
+
+#include "linear.cuh"
+#include "vec8.cuh"
+
+#undef DA_BOUNDS_FILE
+#define DA_BOUNDS_FILE 15
+
+namespace da {
+
+constexpr int kFewEpiWarps = 8;
+constexpr int kFewThreads = (kFewEpiWarps + 2) * 32;
+
+__device__ __forceinline__ void store_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+template <bool W_MN, int EPI>
+__global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid_constant__ LinearParams p) {
+  constexpr int SIDES = EPI == kEpiGated ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- shared memory: ring of [weights | tokens], partial sums, barriers
+  const int wrows = p.width * SIDES;
+  const uint32_t w_bytes = static_cast<uint32_t>(wrows) * 128u, stage_bytes = w_bytes + static_cast<uint32_t>(p.nt) * 128u;
+  const int stages = p.stages;
+  float* part = reinterpret_cast<float*>(smem + stages * stage_bytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.off_bars);
+  uint64_t* full = bars;
+  uint64_t* empty = full + stages;
+  uint64_t* done = empty + stages;  // every MMA completed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1) + 1;
+
+  // ---- work of this CTA: features, tokens, and its share of the contraction
+  const int cs = p.cs, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / cs;
+  const int f0 = (tile % p.tiles_n) * p.width, t0 = (tile / p.tiles_n) * p.nt;
+  const int kblocks = (p.K + kLinBK - 1) / kLinBK;
+  // K blocks rank, rank + cs, ...: what a cluster reads at one time lies together in the weights' rows.
+  const int nkb = (kblocks - rank + cs - 1) / cs;  // >= 1
+  const int most = 256 / wrows;                    // accumulators that fit (two CTAs share an SM's 512 columns)
+  const int seg = EPI == kEpiF32 ? (nkb + most - 1) / most : nkb;  // K blocks an accumulator sums
+  const int segs = (nkb + seg - 1) / seg;
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < static_cast<uint32_t>(segs * wrows)) tmem_cols *= 2;
+
+  if (cs > 1) cluster_arrive();  // (waited for below: every CTA of the cluster has started)
+  int fill = 0, slot = 0;
+  uint32_t phase = 0;
+  auto load = [&]() {
+    const int k0 = (rank + fill * cs) * kLinBK;
+    uint8_t* dst = smem + slot * stage_bytes;
+    uint64_t* bar = &full[slot];
+    mbar_arrive_expect_tx(bar, stage_bytes);
+    ++fill;
+    if (++slot == stages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    if (!DA_BOUNDS(k0 < p.K && f0 < p.N && t0 < p.M)) return;
+    if (W_MN) {
+      for (int j = 0; j < wrows; j += 64) tma_load_2d(dst + j * 128, &p.tm_a, bar, f0 + j, k0);
+    } else {
+      tma_load_2d(dst, &p.tm_a, bar, k0, f0);
+      if (EPI == kEpiGated) tma_load_2d(dst + p.width * 128, &p.tm_a, bar, k0, p.N + f0);
+    }
+    tma_load_2d(dst + w_bytes, &p.tm_b, bar, k0, t0);
+  };
+  if (warp == kFewEpiWarps) {
+    if (lane == 0) {
+      for (int s = 0; s < stages; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+      }
+      mbar_init(done, 1);
+      *abort_flag = 0;
+      fence_mbar_init();
+      grid_dep_wait();
+      const int first = min(nkb, stages);
+      while (fill < first) load();
+    }
+    __syncwarp();
+  } else if (warp == kFewEpiWarps + 1) {
+    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_launch_dependents();  // (every CTA has its TMEM by the time the next kernel's come up)
+  const uint32_t tmem = *tmem_slot;
+  const AbortState ab{abort_flag, p.status};
+
+  if (warp == kFewEpiWarps) {
+    // ================================================================ producer
+    if (lane == 0) {
+      while (fill < nkb) {
+        if (!mbar_wait(&empty[slot], phase ^ 1u, ab)) break;
+        load();
+      }
+      if (*ab.flag)  // aborted: the copies already issued land before the CTA exits
+        for (int f = max(0, fill - stages); f < fill; ++f)
+          mbar_wait_drain(&full[f % stages], static_cast<uint32_t>(f / stages) & 1u, kWaitBudgetCycles);
+    }
+    __syncwarp();
+  } else if (warp == kFewEpiWarps + 1) {
+    // ================================================================ MMA issuer
+    const uint64_t dX = sdesc_sw128(smem_u32(smem + w_bytes), 16, 1024);
+    const uint64_t dW = sdesc_sw128(smem_u32(smem), W_MN ? 8192 : 16, 1024);
+    constexpr int KW = W_MN ? 2048 : 32;
+    const uint32_t idesc = idesc_bf16(128, 0, false, W_MN) | (static_cast<uint32_t>(wrows >> 3) << 17);
+    int s = 0, in_seg = 0;
+    uint32_t ph = 0, dacc = tmem;
+    for (int kb = 0; kb < nkb; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, ab))) break;
+      tc_fence_after();
+      const uint64_t so = static_cast<uint64_t>((s * stage_bytes) >> 4);
+#pragma unroll
+      for (int k = 0; k < kLinBK / 16; ++k)
+        mma_ss_elect(dacc, dX + so + static_cast<uint64_t>((k * 32) >> 4), dW + so + static_cast<uint64_t>((k * KW) >> 4), idesc,
+                     (in_seg > 0 || k > 0) ? 1u : 0u);
+      tc_commit_elect(&empty[s]);
+      if (++s == stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+      if (++in_seg == seg) {
+        in_seg = 0;
+        dacc += static_cast<uint32_t>(wrows);
+      }
+    }
+    tc_commit_elect(done);
+    if (__any_sync(0xffffffffu, *ab.flag)) mbar_wait_drain(done, 0, kWaitBudgetCycles);
+    __syncwarp();
+  }
+
+  // ---- partial sums: [rank][token][lg groups][side][8], rows 16 bytes longer than their values (banks)
+  const int groups = p.width >> 3, lg = p.lg;  // rank r finishes groups r lg .. of every token
+  const int row_floats = lg * SIDES * 8 + 4;
+  const int mt = min(p.nt, p.M - t0);
+  const int wq = (warp & 3) * 32;  // first accumulator row of this warp
+  const bool go = warp < kFewEpiWarps && __all_sync(0xffffffffu, mbar_wait(done, 0, ab));
+  if (cs > 1) cluster_wait();
+  if (go && wq < mt) {
+    // ================================================================ accumulators to the CTAs that finish them
+    tc_fence_after();
+    const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 16);
+    const int row = wq + lane;
+    const uint32_t mine = smem_u32(part + (rank * p.nt + row) * row_floats);
+    // groups of eight columns of this half of the warps: pairs [first, last) of 16 columns
+    const int pairs = wrows >> 4, first = warp < 4 ? 0 : (pairs + 1) >> 1, last = warp < 4 ? (pairs + 1) >> 1 : pairs;
+    int side = 0, g = 2 * first;
+    if (SIDES == 2 && g >= groups) side = 1, g -= groups;
+    int owner = g / lg, local = g - owner * lg;
+    auto put = [&](const uint32_t* r) {
+      uint32_t to = mine + static_cast<uint32_t>((local * SIDES + side) * 32);
+      if (cs > 1) {
+        asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(owner));
+        store_cluster_f4(to, __uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]), __uint_as_float(r[3]));
+        store_cluster_f4(to + 16, __uint_as_float(r[4]), __uint_as_float(r[5]), __uint_as_float(r[6]), __uint_as_float(r[7]));
+      } else {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+      }
+    };
+    auto next = [&]() {
+      ++g;
+      if (++local == lg) {
+        local = 0;
+        ++owner;
+      }
+      if (SIDES == 2 && g == groups) side = 1, g = 0, owner = 0, local = 0;
+    };
+    auto add_segments = [&](int c, uint32_t (&a)[16]) {
+      for (int q = 1; q < segs; ++q) {
+        uint32_t z[16];
+        tmem_ld16(tl + static_cast<uint32_t>(q * wrows + c), z);
+        tmem_ld_wait16x2(a, z);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(z[j]));
+      }
+    };
+    for (int h = first; h < last; h += 2) {  // 32 columns a wait
+      uint32_t a[16], b[16] = {};
+      tmem_ld16(tl + static_cast<uint32_t>(16 * h), a);
+      if (h + 1 < last) tmem_ld16(tl + static_cast<uint32_t>(16 * h + 16), b);
+      tmem_ld_wait16x2(a, b);
+      if (EPI == kEpiF32) {
+        add_segments(16 * h, a);
+        if (h + 1 < last) add_segments(16 * h + 16, b);
+      }
+      auto two = [&](const uint32_t* r) {
+        if (row < mt) put(r);
+        next();
+        if (row < mt) put(r + 8);
+        next();
+      };
+      two(a);
+      if (h + 1 < last) two(b);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (cs > 1) {
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  grid_dep_wait();
+
+  // ================================================================ sum over the cluster, epilogue: eight features an item
+  {
+    const int ng = max(0, min(lg, groups - rank * lg));  // groups of this CTA
+    const int items = mt * ng;
+    const uint32_t over = 0xffffffffu / static_cast<uint32_t>(max(1, ng)) + 1u;  // i / ng by its high product (i < 2^16)
+    auto sum8 = [&](int t, int g, int side, float (&v)[8]) {
+      const float* at = part + t * row_floats + (g * SIDES + side) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < cs; ++c, at += p.nt * row_floats) {
+        const float4 a = *reinterpret_cast<const float4*>(at), b = *reinterpret_cast<const float4*>(at + 4);
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+      }
+    };
+    for (int i = threadIdx.x; i < items; i += kFewThreads) {
+      const int t = ng == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), over)), g = i - t * ng;
+      const int col = f0 + (rank * lg + g) * 8;
+      const long long row = t0 + t;
+      if (col >= p.N || !DA_BOUNDS_V(row < p.M && col + 8 <= p.N, col)) continue;
+      float v[8];
+      sum8(t, g, 0, v);
+      if (EPI == kEpiGated) {
+        float u[8];
+        sum8(t, g, 1, u);
+        if (p.pre) {
+          __nv_bfloat16* pre = p.pre + row * p.ldp + col;
+          *reinterpret_cast<uint4*>(pre) = pack8(v);
+          *reinterpret_cast<uint4*>(pre + p.N) = pack8(u);
+        }
+        with_act(p.act, [&](auto tag) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = act_of<decltype(tag)::value>(v[j]) * u[j];
+        });
+      } else {
+        if (p.bias) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + col)), b = __ldg(reinterpret_cast<const float4*>(p.bias + col) + 1);
+          v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+          v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        }
+        if (p.pre) *reinterpret_cast<uint4*>(p.pre + row * p.ldp + col) = pack8(v);
+        if (p.act != DIFFATTN_ACT_NONE)
+          with_act(p.act, [&](auto tag) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+          });
+        if (p.residual) {
+          float r[8];
+          if (EPI == kEpiF32) {
+            const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + row * p.ldr + col);
+            const float4 a = at[0], b = at[1];
+            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+          } else {
+            unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.ldr + col), r);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += r[j];
+        }
+      }
+      if (EPI == kEpiF32) {
+        float4* at = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.ldo + col);
+        at[0] = make_float4(v[0], v[1], v[2], v[3]);
+        at[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.ldo + col) = pack8(v);
+      }
+    }
+  }
+
+  if (warp == kFewEpiWarps + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tmem_cols);
+  }
+}
+
+}  // namespace da
