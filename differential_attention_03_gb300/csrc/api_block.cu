@@ -132,14 +132,25 @@ struct Product {
   long long ldx, ldw;
 };
 
-// Rounds of linear_kernel's tiles over the SMs, in clusters of cg.
-long long tile_rounds(const Product& q, const da::LinearParams& p, int sms, int cg) {
+// linear_kernel's tiles in clusters of cg CTAs.
+long long tile_count(const Product& q, const da::LinearParams& p, int cg) {
   const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
-  const long long t = ((p.M + da::kLinBM * cg - 1ll) / (da::kLinBM * cg)) * ((p.N + bn - 1ll) / bn);
-  return (t + sms / cg - 1) / (sms / cg);
+  return ((p.M + da::kLinBM * cg - 1ll) / (da::kLinBM * cg)) * ((p.N + bn - 1ll) / bn);
 }
 
-// SM pairs, unless single SMs take clearly fewer rounds (few row blocks, or a last round that pairs leave emptier).
+// Tiles before the ones that come in halves: those of whole rounds, if half of the clusters or fewer have work after them.
+long long full_tiles(long long tiles, long long clusters) {
+  const long long rest = tiles % clusters;
+  return 2 * rest <= clusters ? tiles - rest : tiles;
+}
+
+// Rounds of tiles over the SMs.  A half tile takes some 0.55 of a tile (it reads the same rows of A).
+double tile_rounds(const Product& q, const da::LinearParams& p, int sms, int cg) {
+  const long long tiles = tile_count(q, p, cg), clusters = sms / cg, full = full_tiles(tiles, clusters);
+  return static_cast<double>((full + clusters - 1) / clusters) + (full < tiles ? 0.55 : 0.0);
+}
+
+// SM pairs, unless single SMs take clearly less (few row blocks, or a last round that pairs leave emptier).
 int best_pair(const Product& q, const da::LinearParams& p, int sms) {
   return tile_rounds(q, p, sms, 2) * 0.9 <= tile_rounds(q, p, sms, 1) ? 2 : 1;
 }
@@ -222,11 +233,12 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
-    const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    if (tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+    const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
+    if (2 * tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+    p.full = static_cast<int>(full_tiles(tiles, clusters));
     if ((st = map_x(&p.tm_a, 128)) != DIFFATTN_OK) return st;
-    if ((st = map_w(&p.tm_b, 128)) != DIFFATTN_OK) return st;
-    const int grid = static_cast<int>(std::min<long long>(tiles, sms / cg)) * cg;
+    if ((st = map_w(&p.tm_b, 64)) != DIFFATTN_OK) return st;
+    const int grid = static_cast<int>(std::min(p.full + 2 * (tiles - p.full), clusters)) * cg;
     e = q.kind == Kind::kDgrad   ? da::launch_linear_dgrad(p, cg, grid, s)
         : q.kind == Kind::kWgrad ? da::launch_linear_wgrad(p, q.epi, cg, grid, s)
                                  : da::launch_linear_fwd(p, q.epi, cg, grid, s);

@@ -14,7 +14,8 @@
 //
 // One cluster of CG CTAs (an SM pair with CG = 2) per 128 CG x 256 tile,
 // persistent over the tiles in groups of `group_m` row blocks, so that the
-// CTAs at work share operands in L2.  With CG = 2 an MMA is M256 N256 K16
+// CTAs at work share operands in L2; a last round that would leave half of the
+// clusters without work takes 128 CG x 128 tiles instead.  With CG = 2 an MMA is M256 N256 K16
 // over both SMs' tensor cores: each CTA holds its 128 rows of A and half of B,
 // so a CTA's shared memory feeds half as many B bytes.
 //   warps 0-7   epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
@@ -142,18 +143,33 @@ struct LinearCfg {
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t IDESC = idesc_bf16(BM * CG, BN, A_MN, B_MN);
+  static constexpr uint32_t IDESC = idesc_bf16(BM * CG, BN, A_MN, B_MN), IDESC_HALF = idesc_bf16(BM * CG, BN / 2, A_MN, B_MN);
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ void linear_tile(const LinearParams& p, int t, int& mb, int& nb) {
+// What a cluster computes at step t of the persistent walk: rows from m (of CTA 0), accumulator columns from n0 (gated:
+// gate columns), 256 or 128 accumulator columns.
+struct LinTile {
+  int mb, n0, cols;
+};
+
+// Tile t -> row block and column block, row blocks in groups of group_m.  From p.full on tiles come in halves: the last
+// round, where it has work for no more than half of the clusters.
+template <int EPI>
+__device__ __forceinline__ LinTile linear_tile(const LinearParams& p, int t) {
+  const bool half = t >= p.full;
+  const int tile = half ? p.full + ((t - p.full) >> 1) : t;
   const int per_group = p.group_m * p.tiles_n;
-  const int g = t / per_group;
+  const int g = tile / per_group;
   const int first = g * p.group_m;
   const int gm = min(p.group_m, p.tiles_m - first);
-  const int r = t - g * per_group;
-  mb = first + r % gm;
-  nb = r / gm;
+  const int r = tile - g * per_group;
+  constexpr int BN = EPI == kEpiGated ? kLinBN / 2 : kLinBN;
+  LinTile x;
+  x.mb = first + r % gm;
+  x.n0 = (r / gm) * BN + (half ? ((t - p.full) & 1) * (BN / 2) : 0);
+  x.cols = half ? kLinBN / 2 : kLinBN;
+  return x;
 }
 
 // ----------------------------------------------------------------- staging
@@ -336,7 +352,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int steps = p.full + 2 * (p.tiles_m * p.tiles_n - p.full);
   const int kblocks = (p.K + C::BK - 1) / C::BK;
   const int seg = EPI == kEpiF32 ? kLinSegBlocks : kblocks;  // K blocks an accumulator sums
   const int cid = static_cast<int>(blockIdx.x) / CG, ncl = static_cast<int>(gridDim.x) / CG;
@@ -369,12 +385,12 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
       tma_prefetch_desc(&p.tm_b);
       long long fill = 0;
       bool ok = true;
-      for (int t = cid; ok && t < tiles; t += ncl) {
-        int mb, nb;
-        linear_tile(p, t, mb, nb);
-        const int m0 = (mb * CG + static_cast<int>(rank)) * C::BM;
-        // Rows of B: 256 columns of the tile; gated: 128 gate columns, and their up columns N rows further.
-        const int n0 = EPI == kEpiGated ? nb * (C::BN / 2) : nb * C::BN;
+      for (int t = cid; ok && t < steps; t += ncl) {
+        const LinTile x = linear_tile<EPI>(p, t);
+        if (x.n0 >= p.N) continue;
+        const int m0 = (x.mb * CG + static_cast<int>(rank)) * C::BM;
+        const int part = x.cols / CG;  // rows of B that this CTA loads: gate columns and, N rows further, up columns if gated
+        const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(part) * 128u;
         for (int kb = 0; kb < kblocks; ++kb, ++fill) {
           const int s = static_cast<int>(fill % C::STAGES);
           const long long use = fill / C::STAGES;
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
             break;
           }
           uint8_t* dst = smem + s * C::STAGE_BYTES;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * C::STAGE_BYTES);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * bytes);
           const uint32_t bar = CG == 2 ? map_to_rank(&full[s], 0) : 0;
           auto load = [&](uint8_t* to, const CUtensorMap* map, int c0, int c1) {
             if (CG == 2)
@@ -401,16 +417,15 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
             load(dst, &p.tm_a, k0, m0);
           }
 #pragma unroll
-          for (int h = 0; h < C::BN_CTA / 128; ++h) {
-            const int part = CG == 2 ? static_cast<int>(rank) : h;  // which 128 of the tile's 256 B rows
-            const int nr = EPI == kEpiGated ? n0 + part * p.N : n0 + part * 128;
-            uint8_t* to = dst + C::A_BYTES + h * 16384;
-            if (B_MN) {
-              load(to, &p.tm_b, nr, k0);
-              load(to + 8192, &p.tm_b, nr + 64, k0);
-            } else {
-              load(to, &p.tm_b, k0, nr);
-            }
+          for (int h = 0; h < C::BN_CTA / 64; ++h) {
+            if (64 * h >= part) break;
+            const int b = static_cast<int>(rank) * part + 64 * h;  // accumulator column of the box's first row
+            // gated: the first half of the columns are gate rows, the second half their up rows
+            const int nr = EPI == kEpiGated ? x.n0 + (2 * b < x.cols ? b : p.N + b - x.cols / 2) : x.n0 + b;
+            if (B_MN)
+              load(dst + C::A_BYTES + h * 8192, &p.tm_b, nr, k0);
+            else
+              load(dst + C::A_BYTES + h * 8192, &p.tm_b, k0, nr);
           }
         }
       }
@@ -440,7 +455,10 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
       long long fill = 0;
       long long i = 0;  // accumulators of this cluster so far
       bool ok = true;
-      for (int t = cid; ok && t < tiles; t += ncl) {
+      for (int t = cid; ok && t < steps; t += ncl) {
+        const LinTile x = linear_tile<EPI>(p, t);
+        if (x.n0 >= p.N) continue;
+        const uint32_t idesc = x.cols == C::BN ? C::IDESC : C::IDESC_HALF;
         for (int kb = 0; ok && kb < kblocks; ++kb, ++fill) {
           const int a = static_cast<int>(i & 1);
           const bool first = kb % seg == 0;
@@ -459,7 +477,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
 #pragma unroll
           for (int k = 0; k < C::BK / 16; ++k)
             mma_cg<CG>(dacc, dA + so + static_cast<uint64_t>((k * KA) >> 4), dB + so + static_cast<uint64_t>((k * KB) >> 4),
-                       C::IDESC, (!first || k > 0) ? 1u : 0u);
+                       idesc, (!first || k > 0) ? 1u : 0u);
           tc_commit_cg<CG>(&empty[s]);
           if (kb % seg == seg - 1 || kb == kblocks - 1) {
             tc_commit_cg<CG>(&acc_full[a]);
@@ -500,18 +518,20 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
     };
     long long i = 0;
     bool ok = true;
-    for (int t = cid; ok && t < tiles; t += ncl) {
-      int mb, nb;
-      linear_tile(p, t, mb, nb);
-      const long long r0 = static_cast<long long>(mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
+    for (int t = cid; ok && t < steps; t += ncl) {
+      const LinTile x = linear_tile<EPI>(p, t);
+      if (x.n0 >= p.N) continue;
+      const long long r0 = static_cast<long long>(x.mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
       const int rows = static_cast<int>(min(32ll, static_cast<long long>(p.M) - r0));  // (<= 0: none)
+      const int width = x.cols >> 1;  // accumulator columns of this half of the warps
       if (EPI == kEpiGated) {
-        const int c0 = nb * (C::BN / 2) + half * 64, cols = p.N - c0;
+        // gate columns and their up columns, 64 each; of a half tile 32 (what lies beyond is loaded and not used)
+        const int off = half * (width >> 1), c0 = x.n0 + off, cols = min(width >> 1, p.N - c0);
         if (!acc_wait(i)) break;
-        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 64);
+        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + off);
         float g[64], u[64];
         load_cols64(acc, g);
-        load_cols64(acc + 128, u);
+        load_cols64(acc + static_cast<uint32_t>(width), u);
         acc_release(i);
         ++i;
         if (rows <= 0 || cols <= 0) continue;
@@ -525,16 +545,17 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         });
         put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
       } else if (EPI == kEpiF32) {
-        const int c0 = nb * C::BN + half * 128, cols = p.N - c0;
+        const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         float v[128];
         for (int kb = 0; kb < kblocks; kb += seg, ++i) {
           if (!acc_wait(i)) {
             ok = false;
             break;
           }
-          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 128);
+          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * width);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            if (32 * q >= width) break;
             uint32_t r[32];
             tmem_ld32(acc + 32 * q, r);
             tmem_ld_wait(r);
@@ -549,7 +570,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         for (int q = 0; q < 4; ++q)
           if (cols > 32 * q) epilogue_f32(p, v + 32 * q, stg, r0, c0 + 32 * q, rows, cols - 32 * q, lane);
       } else {
-        const int c0 = nb * C::BN + half * 128, cols = p.N - c0;
+        const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         uint4 res[8];
         auto fetch = [&](int q) {
           if (p.residual && rows > 0 && cols > 64 * q)
@@ -558,15 +579,18 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         };
         fetch(0);
         if (!acc_wait(i)) break;
-        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * 128);
+        const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * width);
         float v[64];
         load_cols64(acc, v);
+        if (width == 64) acc_release(i);
         if (rows > 0 && cols > 0) epilogue_bf16(p, v, res, stg, r0, c0, rows, cols, lane);
-        fetch(1);
-        load_cols64(acc + 64, v);
-        acc_release(i);
+        if (width > 64) {
+          fetch(1);
+          load_cols64(acc + 64, v);
+          acc_release(i);
+          if (rows > 0 && cols > 64) epilogue_bf16(p, v, res, stg, r0, c0 + 64, rows, cols - 64, lane);
+        }
         ++i;
-        if (rows > 0 && cols > 64) epilogue_bf16(p, v, res, stg, r0, c0 + 64, rows, cols - 64, lane);
       }
     }
   }

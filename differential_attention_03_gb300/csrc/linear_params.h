@@ -23,7 +23,7 @@ constexpr int kFewMaxSmem = 232448;
 
 struct LinearParams {
   CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
-  CUtensorMap tm_b;  // the same over B ({K, N} or {N, K})
+  CUtensorMap tm_b;  // over B ({K, N} or {N, K}), box {64, 64}; linear_few: the tokens, box {64, nt}
   const float* bias;     // [N] or nullptr
   const void* residual;  // [M, N] in the output's type or nullptr
   void* out;
@@ -32,6 +32,7 @@ struct LinearParams {
   int M, N, K;           // gated: N = F
   int act;
   int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
+  int full;                       // tiles before the ones that come in halves
   // linear_few: features (gated: gate features) and token rows of a tile, CTAs that share its contraction, groups of
   // eight features that each of them finishes, ring slots, and where the barriers lie in shared memory
   int width, nt, cs, lg, stages, off_bars;
