@@ -12,61 +12,104 @@
 
 namespace da {
 
-// 1 / (1 + e^-z): e^-z = inf for z below -88 gives 0, as it should.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
+// Two values at a time: sums and products of pairs are one instruction each.
+__device__ __forceinline__ uint64_t pair_of(float x) { return f2pack(x, x); }
+template <class F>
+__device__ __forceinline__ uint64_t each(uint64_t x, F&& f) {
+  float lo, hi;
+  f2unpack(x, lo, hi);
+  return f2pack(f(lo), f(hi));
+}
+
+// 1 / (1 + 2^-t): 2^-t = inf gives 0, as it should.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t t) {
+  return each(t, [](float x) { return rcp_fast(1.f + ex2(-x)); });
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC0 = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kGeluC1 = 0.044715f;
 
 // Phi(z), and e = exp(-z^2 / 2), by the rational approximation of erfc in Abramowitz and Stegun 7.1.26 (absolute error
-// 1.5e-7; the tail below zero keeps its size, as nothing is subtracted from 1 there).  One exponential and one
-// reciprocal: a kernel whose epilogue called erff was bound by it (8002 x 8192 x 2048, bias, stored z: 193 us; 177 so).
-__device__ __forceinline__ float normal_integral(float z, float& e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, 1.f + 0.3275911f * x);
-  e = ex2(-0.72134752044448170f * z * z);  // (log2(e) / 2)
-  const float tail = 0.5f * e * t *
-                     (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
-  return z < 0.f ? tail : 1.f - tail;
+// 1.5e-7).  One exponential and one reciprocal: a kernel whose epilogue called erff was bound by it (8002 x 8192 x 2048,
+// bias, stored z: 193 us; 174 so).
+__device__ __forceinline__ uint64_t normal_integral2(uint64_t z, uint64_t& e) {
+  e = each(mul2(mul2(z, z), pair_of(-0.5f * kLog2e)), [](float x) { return ex2(x); });
+  const uint64_t a = each(z, [](float x) { return fabsf(x); });
+  const uint64_t t = each(fma2(a, pair_of(0.3275911f * 0.70710678118654752f), pair_of(1.f)), [](float x) { return rcp_fast(x); });
+  uint64_t q = fma2(t, pair_of(0.5f * 1.061405429f), pair_of(0.5f * -1.453152027f));
+  q = fma2(t, q, pair_of(0.5f * 1.421413741f));
+  q = fma2(t, q, pair_of(0.5f * -0.284496736f));
+  q = fma2(t, q, pair_of(0.5f * 0.254829592f));
+  // the upper tail Phi(-|z|) is q t e; Phi = 1/2 +- (1/2 - tail)
+  const uint64_t h = fma2(mul2(q, t), mul2(e, pair_of(-1.f)), pair_of(0.5f));
+  const uint64_t sign = z & 0x8000000080000000ull;
+  return add2(h ^ sign, pair_of(0.5f));
 }
 
+// act(z) of a pair.
 template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-  if (ACT == DIFFATTN_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+__device__ __forceinline__ uint64_t act_of2(uint64_t z) {
+  if (ACT == DIFFATTN_ACT_RELU) return each(z, [](float x) { return x > 0.f ? x : (x != x ? x : 0.f); });
   if (ACT == DIFFATTN_ACT_GELU) {
-    float e;
-    return z * normal_integral(z, e);
+    uint64_t e;
+    return mul2(z, normal_integral2(z, e));
   }
-  if (ACT == DIFFATTN_ACT_GELU_TANH) return z * sigmoid(2.f * kGeluC0 * (z + kGeluC1 * z * z * z));
-  if (ACT == DIFFATTN_ACT_SILU) return z * sigmoid(z);
+  if (ACT == DIFFATTN_ACT_GELU_TANH) {
+    const uint64_t w = fma2(mul2(z, z), pair_of(2.f * kLog2e * kGeluC0 * kGeluC1), pair_of(2.f * kLog2e * kGeluC0));
+    return mul2(z, sigmoid2(mul2(z, w)));
+  }
+  if (ACT == DIFFATTN_ACT_SILU) return mul2(z, sigmoid2(mul2(z, pair_of(kLog2e))));
   return z;
 }
 
-// act'(z), and act(z) beside it.
+// act'(z) of a pair, and act(z) beside it.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z, float& value) {
+__device__ __forceinline__ uint64_t act_slope2(uint64_t z, uint64_t& value) {
   if (ACT == DIFFATTN_ACT_RELU) {
-    value = z > 0.f ? z : (z != z ? z : 0.f);
-    return z > 0.f ? 1.f : (z != z ? z : 0.f);
+    value = act_of2<ACT>(z);
+    return each(z, [](float x) { return x > 0.f ? 1.f : (x != x ? x : 0.f); });
   }
   if (ACT == DIFFATTN_ACT_GELU) {
-    float e;
-    const float phi = normal_integral(z, e);
-    value = z * phi;
-    return phi + z * e * 0.39894228040143268f;
+    uint64_t e;
+    const uint64_t phi = normal_integral2(z, e);
+    value = mul2(z, phi);
+    return fma2(mul2(z, e), pair_of(0.39894228040143268f), phi);
   }
   if (ACT == DIFFATTN_ACT_GELU_TANH) {
-    const float s = sigmoid(2.f * kGeluC0 * (z + kGeluC1 * z * z * z));
-    value = z * s;
-    return s + z * s * (1.f - s) * 2.f * kGeluC0 * (1.f + 3.f * kGeluC1 * z * z);
+    const uint64_t zz = mul2(z, z);
+    const uint64_t w = fma2(zz, pair_of(2.f * kLog2e * kGeluC0 * kGeluC1), pair_of(2.f * kLog2e * kGeluC0));
+    const uint64_t s = sigmoid2(mul2(z, w));
+    value = mul2(z, s);
+    // s + value (1 - s) 2 c0 (1 + 3 c1 z^2)
+    const uint64_t rest = fma2(s, mul2(value, pair_of(-1.f)), value);
+    return fma2(rest, fma2(zz, pair_of(6.f * kGeluC0 * kGeluC1), pair_of(2.f * kGeluC0)), s);
   }
   if (ACT == DIFFATTN_ACT_SILU) {
-    const float s = sigmoid(z);
-    value = z * s;
-    return s * (1.f + z * (1.f - s));
+    const uint64_t s = sigmoid2(mul2(z, pair_of(kLog2e)));
+    value = mul2(z, s);
+    return add2(s, fma2(s, mul2(value, pair_of(-1.f)), value));
   }
   value = z;
-  return 1.f;
+  return pair_of(1.f);
+}
+
+// v[0 .. N) = act(v); v = act(v) u.
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float* v) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) f2unpack(act_of2<ACT>(f2pack(v[j], v[j + 1])), v[j], v[j + 1]);
+}
+template <int ACT, int N>
+__device__ __forceinline__ void act_times(float* v, const float* u) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) f2unpack(mul2(act_of2<ACT>(f2pack(v[j], v[j + 1])), f2pack(u[j], u[j + 1])), v[j], v[j + 1]);
 }
 
 // f(integral_constant) for the activation `act`: one branch around a loop, none inside it.

@@ -15,7 +15,6 @@
 #include "act.cuh"
 #include "block_params.h"
 #include "ptx.cuh"
-#include "vec8.cuh"
 
 #undef DA_BOUNDS_FILE
 #define DA_BOUNDS_FILE 13
@@ -24,6 +23,23 @@ namespace da {
 
 constexpr int kActGradThreads = 256;
 
+// Eight bf16 values as pairs in fp32, and back.
+__device__ __forceinline__ void pairs_of(const uint4& w, uint64_t (&v)[4]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = f2pack(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 rounded(const uint64_t (&v)[4]) {
+  uint32_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float lo, hi;
+    f2unpack(v[j], lo, hi);
+    x[j] = pack_bf16x2(lo, hi);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
 template <bool kGated, int ACT>
 __global__ void __launch_bounds__(kActGradThreads) act_grad_kernel(const ActGradParams p) {
   __shared__ float sums[kGated ? 1 : 8][kGated ? 1 : 256];
@@ -31,46 +47,57 @@ __global__ void __launch_bounds__(kActGradThreads) act_grad_kernel(const ActGrad
   const int col = blockIdx.x * 256 + lane * 8;
   const int per = (p.M + p.chunks - 1) / p.chunks;
   const int r0 = blockIdx.y * per, r1 = min(p.M, r0 + per);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  uint64_t acc[4] = {0, 0, 0, 0};
+  constexpr int IN = kGated ? 3 : ACT != DIFFATTN_ACT_NONE ? 2 : 1, RR = kGated ? 2 : 4;  // rows on their way at once
   if (col < p.N) {
-#pragma unroll 2
-    for (int r = r0 + warp; r < r1; r += 8) {
-      float dy[8];
-      unpack8(*reinterpret_cast<const uint4*>(p.dy + r * p.ldy + col), dy);
-      if (kGated) {
-        float g[8], u[8], dg[8], du[8];
-        unpack8(*reinterpret_cast<const uint4*>(p.pre + r * p.ldp + col), g);
-        unpack8(*reinterpret_cast<const uint4*>(p.pre + r * p.ldp + p.N + col), u);
+    for (int r = r0 + warp; r < r1; r += 8 * RR) {
+      uint4 in[RR][IN];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float value;
-          const float slope = act_slope<ACT>(g[j], value);
-          dg[j] = dy[j] * u[j] * slope;
-          du[j] = dy[j] * value;
-        }
-        if (DA_BOUNDS_V(r < p.M && col + 8 <= p.N, r)) {
-          *reinterpret_cast<uint4*>(p.dz + r * p.ldz + col) = pack8(dg);
-          *reinterpret_cast<uint4*>(p.dz + r * p.ldz + p.N + col) = pack8(du);
-        }
-      } else {
-        if (ACT != DIFFATTN_ACT_NONE) {
-          float z[8];
-          unpack8(*reinterpret_cast<const uint4*>(p.pre + r * p.ldp + col), z);
+      for (int k = 0; k < RR; ++k) {
+        const long long row = min(r + 8 * k, r1 - 1);  // (past the chunk: its last row again, which is not used)
+        in[k][0] = *reinterpret_cast<const uint4*>(p.dy + row * p.ldy + col);
+        if (IN > 1) in[k][IN > 1 ? 1 : 0] = *reinterpret_cast<const uint4*>(p.pre + row * p.ldp + col);
+        if (IN > 2) in[k][IN > 2 ? 2 : 0] = *reinterpret_cast<const uint4*>(p.pre + row * p.ldp + p.N + col);
+      }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float value;
-            dy[j] *= act_slope<ACT>(z[j], value);
+      for (int k = 0; k < RR; ++k) {
+        const int row = r + 8 * k;
+        if (row >= r1) break;
+        uint64_t dy[4];
+        pairs_of(in[k][0], dy);
+        if (kGated) {
+          uint64_t g[4], u[4], value;
+          pairs_of(in[k][IN > 1 ? 1 : 0], g);
+          pairs_of(in[k][IN > 2 ? 2 : 0], u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t slope = act_slope2<ACT>(g[j], value);
+            g[j] = mul2(mul2(dy[j], u[j]), slope);
+            u[j] = mul2(dy[j], value);
           }
-          if (DA_BOUNDS_V(r < p.M && col + 8 <= p.N, r)) *reinterpret_cast<uint4*>(p.dz + r * p.ldz + col) = pack8(dy);
-        }
+          if (DA_BOUNDS_V(row < p.M && col + 8 <= p.N, row)) {
+            *reinterpret_cast<uint4*>(p.dz + row * p.ldz + col) = rounded(g);
+            *reinterpret_cast<uint4*>(p.dz + row * p.ldz + p.N + col) = rounded(u);
+          }
+        } else {
+          if (ACT != DIFFATTN_ACT_NONE) {
+            uint64_t z[4], value;
+            pairs_of(in[k][IN > 1 ? 1 : 0], z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] += dy[j];
+            for (int j = 0; j < 4; ++j) dy[j] = mul2(dy[j], act_slope2<ACT>(z[j], value));
+            if (DA_BOUNDS_V(row < p.M && col + 8 <= p.N, row)) *reinterpret_cast<uint4*>(p.dz + row * p.ldz + col) = rounded(dy);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = add2(acc[j], dy[j]);
+        }
       }
     }
   }
   if (!kGated && p.part) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[warp][lane * 8 + j] = acc[j];
+    for (int j = 0; j < 4; ++j) f2unpack(acc[j], sums[warp][lane * 8 + 2 * j], sums[warp][lane * 8 + 2 * j + 1]);
     __syncthreads();
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (c < p.N) {

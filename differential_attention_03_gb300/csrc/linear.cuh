@@ -255,8 +255,7 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
   if (p.pre) put_bf16_rows(stg, v, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane);
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
-#pragma unroll
-      for (int j = 0; j < 64; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+      act_all<decltype(tag)::value, 64>(v);
     });
   if (p.residual) {
     __syncwarp();
@@ -307,8 +306,7 @@ __device__ __forceinline__ void epilogue_f32(const LinearParams& p, float* v, ui
   }
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+      act_all<decltype(tag)::value, 32>(v);
     });
   if (p.residual) {
     __syncwarp();
@@ -540,8 +538,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
           put_bf16_rows(stg, u, p.pre + r0 * p.ldp + p.N + c0, p.ldp, rows, cols, lane);
         }
         with_act(p.act, [&](auto tag) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) g[j] = act_of<decltype(tag)::value>(g[j]) * u[j];
+          act_times<decltype(tag)::value, 64>(g, u);
         });
         put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
       } else if (EPI == kEpiF32) {

@@ -267,8 +267,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
           *reinterpret_cast<uint4*>(pre + p.N) = pack8(u);
         }
         with_act(p.act, [&](auto tag) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = act_of<decltype(tag)::value>(v[j]) * u[j];
+          act_times<decltype(tag)::value, 8>(v, u);
         });
       } else {
         if (p.bias) {
@@ -279,8 +278,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         if (p.pre) *reinterpret_cast<uint4*>(p.pre + row * p.ldp + col) = pack8(v);
         if (p.act != DIFFATTN_ACT_NONE)
           with_act(p.act, [&](auto tag) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = act_of<decltype(tag)::value>(v[j]);
+            act_all<decltype(tag)::value, 8>(v);
           });
         if (p.residual) {
           float r[8];
