@@ -233,6 +233,8 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
+    p.wide = p.N % 16 == 0 && p.ldo % 16 == 0 && p.ldr % 16 == 0 && p.ldp % 16 == 0 && aligned(p.out, 32) &&
+             aligned(p.residual, 32) && aligned(p.pre, 32);
     const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
     if (2 * tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
     p.full = static_cast<int>(full_tiles(tiles, clusters));

@@ -20,14 +20,16 @@
 // so a CTA's shared memory feeds half as many B bytes.
 //   warps 0-7   epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
 //               columns 128 (w / 4) .. (gated: 64 gate columns and their 64 up
-//               columns).  Values pass through a 4 KB staging buffer a warp
-//               (rows of 128 bytes, 16-byte parts XORed by the row): residual
-//               and outputs move between global memory and it in whole
-//               128-byte rows, 8 lanes a row.
+//               columns).  A lane's row moves between registers and global
+//               memory in 32-byte sectors; in fp32, or where rows are not
+//               multiples of 32 bytes, through a 4 KB staging buffer a warp
+//               (rows of 128 bytes, 16-byte parts XORed by the row), 8 lanes a
+//               128-byte row.
 //   warp 8      TMA producer: per K block of 64 the A and B boxes into a ring.
 //   warp 9      TMEM allocator; MMA issuer (of the cluster's first CTA).
 // TMEM: two 256-column accumulators: the epilogue of one tile overlaps the
-// next one's main loop.
+// next one's main loop.  A programmatic dependent launch: barriers and TMEM are
+// set up while the kernel before ends.
 //
 // kEpiF32: the tensor cores truncate as they add into fp32, which costs about
 // 1e-9 relative an added value (measured: 1e-6 for a contraction of 1000,
@@ -211,14 +213,40 @@ __device__ __forceinline__ uint4* stage_row(uint8_t* stg, int lane, int q) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// This lane's row of 64 values as bf16, through the staging buffer, to global memory.
+// 32 bytes of a lane, to or from global memory (32-byte aligned).
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 pack8_at(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// This lane's row of 64 values as bf16 to global memory.  wide (rows of 32-byte multiples): whole 32-byte sectors from
+// each lane, which leaves shared memory to the MMAs (8002 x 8192 x 2048, gelu, stored z: 637 cycles a K block through
+// the staging buffer); else through that buffer, 8 lanes a 128-byte row.
 __device__ __forceinline__ void put_bf16_rows(uint8_t* stg, const float (&v)[64], __nv_bfloat16* dst, long long ld,
-                                              int rows, int cols, int lane) {
+                                              int rows, int cols, int lane, bool wide) {
+  if (wide) {
+    if (lane < rows && DA_BOUNDS(cols > 0)) {
+      __nv_bfloat16* at = dst + lane * ld;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (16 * q < cols) store32(at + 16 * q, pack8_at(v + 16 * q), pack8_at(v + 16 * q + 8));
+    }
+    return;
+  }
   __syncwarp();  // (the buffer's earlier readers)
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    *stage_row(stg, lane, q) = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+  for (int q = 0; q < 8; ++q) *stage_row(stg, lane, q) = pack8_at(v + 8 * q);
   __syncwarp();
   stage_store(stg, reinterpret_cast<uint8_t*>(dst), ld * 2, rows, min(cols, 64) * 2, lane);
 }
@@ -252,18 +280,20 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
         v[4 * q + 3] += b.w;
       }
   }
-  if (p.pre) put_bf16_rows(stg, v, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane);
+  if (p.pre) put_bf16_rows(stg, v, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane, p.wide);
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
       act_all<decltype(tag)::value, 64>(v);
     });
   if (p.residual) {
-    __syncwarp();
-    stage_put(stg, res, lane);
-    __syncwarp();
+    if (!p.wide) {
+      __syncwarp();
+      stage_put(stg, res, lane);
+      __syncwarp();
+    }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const uint4 w = *stage_row(stg, lane, q);
+      const uint4 w = p.wide ? res[q] : *stage_row(stg, lane, q);
       v[8 * q] += bf16_lo(w.x);
       v[8 * q + 1] += bf16_hi(w.x);
       v[8 * q + 2] += bf16_lo(w.y);
@@ -274,7 +304,7 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
       v[8 * q + 7] += bf16_hi(w.w);
     }
   }
-  put_bf16_rows(stg, v, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
+  put_bf16_rows(stg, v, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
 }
 
 // The same in fp32: 32 columns (a 128-byte row).
@@ -373,6 +403,8 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
+  grid_dep_wait();
+  grid_dep_launch_dependents();  // (every CTA at work has its TMEM by now)
   const uint32_t tmem = *tmem_slot;
   const AbortState ab{abort_flag, p.status};
 
@@ -534,13 +566,13 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         ++i;
         if (rows <= 0 || cols <= 0) continue;
         if (p.pre) {
-          put_bf16_rows(stg, g, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane);
-          put_bf16_rows(stg, u, p.pre + r0 * p.ldp + p.N + c0, p.ldp, rows, cols, lane);
+          put_bf16_rows(stg, g, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane, p.wide);
+          put_bf16_rows(stg, u, p.pre + r0 * p.ldp + p.N + c0, p.ldp, rows, cols, lane, p.wide);
         }
         with_act(p.act, [&](auto tag) {
           act_times<decltype(tag)::value, 64>(g, u);
         });
-        put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane);
+        put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
       } else if (EPI == kEpiF32) {
         const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         float v[128];
@@ -570,9 +602,16 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         uint4 res[8];
         auto fetch = [&](int q) {
-          if (p.residual && rows > 0 && cols > 64 * q)
+          if (!p.residual || rows <= 0 || cols <= 64 * q) return;
+          if (p.wide) {  // this lane's own row
+            const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(p.residual) + (r0 + lane) * p.ldr + c0 + 64 * q;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (lane < rows && 64 * q + 16 * h < cols) load32(at + 16 * h, res[2 * h], res[2 * h + 1]);
+          } else {
             stage_load(res, reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.residual) + r0 * p.ldr + c0 + 64 * q),
                        p.ldr * 2, rows, (cols - 64 * q) * 2, lane);
+          }
         };
         fetch(0);
         if (!acc_wait(i)) break;
