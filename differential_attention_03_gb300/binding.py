@@ -1382,6 +1382,7 @@ def linear_train(a, w, bias=None, act: str = "none", residual=None, dtype=None, 
     return _linear(a, w, bias, act, residual, dtype, out, pre, stream), pre
 
 
+@functools.lru_cache(maxsize=1024)
 def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib().diffattn_linear_backward_workspace(M, N, K))
 
@@ -1394,19 +1395,32 @@ def _workspace(workspace, need, dev, like, stream):
     return workspace
 
 
-def _grad(out, name, shape, dtype, dev, like, stream):
-    """A gradient's tensor: the caller's, or a new one."""
-    t = (out or {}).get(name)
-    if t is None:
-        return _empty(shape, dtype, like.device, stream)
-    _on(t, name, dtype, shape, dev)
-    return t
+def _grads(out, wanted, dev, device, stream) -> dict:
+    """Tensors for the gradients `wanted` ((name, shape, dtype), ...): the caller's in the dict `out`, or new ones."""
+    r = {}
+    if out is None:
+        if stream is None:
+            for name, shape, dtype in wanted:
+                r[name] = torch.empty(shape, dtype=dtype, device=device)
+            return r
+        out = {}
+    known = [name for name, _, _ in wanted]
+    for k in out:
+        if k not in known:
+            raise ValueError(f"out may hold {known} here, got {k!r}")
+    for name, shape, dtype in wanted:
+        t = out.get(name)
+        if t is None:
+            t = _empty(shape, dtype, device, stream)
+        else:
+            _on(t, name, dtype, shape, dev)
+        r[name] = t
+    return r
 
 
-def _known(out, names):
-    for k in out or ():
-        if k not in names:
-            raise ValueError(f"out may hold {names}, got {k!r}")
+def _at(r, name):
+    t = r.get(name)
+    return None if t is None else t.data_ptr()
 
 
 def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, da: bool = True, dw: bool = True,
@@ -1427,18 +1441,19 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
         if pre is None:
             raise ValueError("pre is needed behind an activation")
         _on(pre, "pre", torch.bfloat16, shape, dev)
-    _known(out, ("da", "dw", "dbias"))
-    r = {}
+    want = []
     if da:
-        r["da"] = _grad(out, "da", a.shape, torch.bfloat16, dev, a, stream)
+        want.append(("da", a.shape, torch.bfloat16))
     if dw:
-        r["dw"] = _grad(out, "dw", w.shape, dw_dtype, dev, a, stream)
+        want.append(("dw", w.shape, dw_dtype))
     if bias:
-        r["dbias"] = _grad(out, "dbias", (N,), torch.float32, dev, a, stream)
-    ws = _workspace(workspace, linear_backward_workspace_bytes(M, N, K), dev, a, stream)
+        want.append(("dbias", (N,), torch.float32))
+    r = _grads(out, want, dev, a.device, stream)
+    need = linear_backward_workspace_bytes(M, N, K) if code or bias else 0
+    ws = _workspace(workspace, need, dev, a, stream)
     _check(lib().diffattn_linear_backward(M, N, K, a.data_ptr(), lda, w.data_ptr(), dy.data_ptr(), ldy,
-                                          _addr(pre) if code else None, code, _addr(r.get("da")), _addr(r.get("dw")),
-                                          _dt(r["dw"]) if dw else F32, _addr(r.get("dbias")), _addr(ws),
+                                          pre.data_ptr() if code else None, code, _at(r, "da"), _at(r, "dw"),
+                                          _dt(r["dw"]) if dw else F32, _at(r, "dbias"), _addr(ws),
                                           0 if ws is None else ws.nbytes, raw))
     return r
 
@@ -1481,6 +1496,7 @@ def gated_linear_train(x, w_gu, act: str = "silu", out=None, gu=None, stream=Non
     return _gated(x, w_gu, act, out, gu, stream), gu
 
 
+@functools.lru_cache(maxsize=1024)
 def gated_linear_backward_workspace_bytes(M: int, D: int, F: int) -> int:
     return int(lib().diffattn_gated_linear_backward_workspace(M, D, F))
 
@@ -1500,15 +1516,15 @@ def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, d
     F = F2 // 2
     _on(gu, "gu", torch.bfloat16, lead + (2 * F,), dev)
     ldh = _rows(dh, "dh", torch.bfloat16, lead + (F,), dev)
-    _known(out, ("dx", "dw"))
-    r = {}
+    want = []
     if dx:
-        r["dx"] = _grad(out, "dx", x.shape, torch.bfloat16, dev, x, stream)
+        want.append(("dx", x.shape, torch.bfloat16))
     if dw:
-        r["dw"] = _grad(out, "dw", w_gu.shape, dw_dtype, dev, x, stream)
+        want.append(("dw", w_gu.shape, dw_dtype))
+    r = _grads(out, want, dev, x.device, stream)
     ws = _workspace(workspace, gated_linear_backward_workspace_bytes(M, D, F), dev, x, stream)
     _check(lib().diffattn_gated_linear_backward(M, D, F, x.data_ptr(), ldx, w_gu.data_ptr(), gu.data_ptr(),
-                                                dh.data_ptr(), ldh, _act_code(act), _addr(r.get("dx")), _addr(r.get("dw")),
+                                                dh.data_ptr(), ldh, _act_code(act), _at(r, "dx"), _at(r, "dw"),
                                                 _dt(r["dw"]) if dw else F32, _addr(ws), 0 if ws is None else ws.nbytes,
                                                 raw))
     return r
@@ -1592,6 +1608,7 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     return y, out
 
 
+@functools.lru_cache(maxsize=1024)
 def residual_norm_backward_workspace_bytes(rows: int, D: int, gate_rows: int = 0) -> int:
     return int(lib().diffattn_residual_norm_backward_workspace(rows, D, gate_rows))
 
@@ -1612,20 +1629,19 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
         _on(dy, "dy", x.dtype, x.shape, dev)
     if ds is not None:
         _on(ds, "ds", s.dtype, x.shape, dev)
-    _known(out, ("dx", "dresidual", "dgate", "dgamma_post", "dgamma"))
-    r = {"dx": _grad(out, "dx", x.shape, x.dtype, dev, x, stream),
-         "dresidual": _grad(out, "dresidual", x.shape, s.dtype, dev, x, stream)}
+    want = [("dx", x.shape, x.dtype), ("dresidual", x.shape, s.dtype)]
     if gate is not None:
-        r["dgate"] = _grad(out, "dgate", gate.shape, torch.float32, dev, x, stream)
+        want.append(("dgate", gate.shape, torch.float32))
     if post:
-        r["dgamma_post"] = _grad(out, "dgamma_post", (D,), torch.float32, dev, x, stream)
+        want.append(("dgamma_post", (D,), torch.float32))
     if dy is not None:
-        r["dgamma"] = _grad(out, "dgamma", (D,), torch.float32, dev, x, stream)
+        want.append(("dgamma", (D,), torch.float32))
+    r = _grads(out, want, dev, x.device, stream)
     ws = _workspace(workspace, residual_norm_backward_workspace_bytes(rows, D, gate_rows), dev, x, stream)
     _check(lib().diffattn_residual_norm_backward(dt, sd, rows, D, x.data_ptr(), s.data_ptr(), _addr(dy), _addr(ds),
                                                  _addr(gate), gate_rows, scale, 1 if post else 0, _addr(gamma_post),
                                                  _addr(gamma), eps, r["dx"].data_ptr(), r["dresidual"].data_ptr(),
-                                                 _addr(r.get("dgate")), _addr(r.get("dgamma_post")), _addr(r.get("dgamma")),
+                                                 _at(r, "dgate"), _at(r, "dgamma_post"), _at(r, "dgamma"),
                                                  _addr(ws), 0 if ws is None else ws.nbytes, raw))
     return r
 

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdint>
@@ -144,15 +145,34 @@ long long full_tiles(long long tiles, long long clusters) {
   return 2 * rest <= clusters ? tiles - rest : tiles;
 }
 
-// Rounds of tiles over the SMs.  A half tile takes some 0.55 of a tile (it reads the same rows of A).
+// Rounds of tiles over the SMs.  A half tile takes 0.75 of a tile: what an SM draws from L2 (some 115 KB a us) bounds
+// both, and it draws the same rows of A.
 double tile_rounds(const Product& q, const da::LinearParams& p, int sms, int cg) {
   const long long tiles = tile_count(q, p, cg), clusters = sms / cg, full = full_tiles(tiles, clusters);
-  return static_cast<double>((full + clusters - 1) / clusters) + (full < tiles ? 0.55 : 0.0);
+  return static_cast<double>((full + clusters - 1) / clusters) + (full < tiles ? 0.75 : 0.0);
 }
 
 // SM pairs, unless single SMs take clearly less (few row blocks, or a last round that pairs leave emptier).
 int best_pair(const Product& q, const da::LinearParams& p, int sms) {
   return tile_rounds(q, p, sms, 2) * 0.9 <= tile_rounds(q, p, sms, 1) ? 2 : 1;
+}
+
+// Clusters of cs CTAs of linear_few_kernel, one CTA an SM, that run at once: clusters of 4 and 8 do not fill every SM.
+int cluster_slots(int cs, int sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][4];
+  int dev = 0;
+  if (cs <= 2 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return std::max(1, sms / cs);
+  std::atomic<int>& slot = known[dev][cs == 4 ? 2 : 3];
+  int n = slot.load();
+  if (n == 0) {
+    if (da::linear_few_clusters(cs, &n) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = std::max(1, sms / cs);
+    }
+    slot.store(n);
+  }
+  return n;
 }
 
 // How the products for few tokens lay their work out; nt = 0: linear_kernel's tiles suit it better.
@@ -164,8 +184,8 @@ struct FewPlan {
 // Estimates in us, above what every product costs, fitted to a sweep of widths and clusters over fourteen shapes from
 // 1 x 1024 x 1024 to 777 x 1024 x 1024 and 16 x 8192 x 8192 on a GB300 (the choice is within 5 % of the best width and
 // cluster on average, 20 % at worst): HBM 5.1 MB a us together with an SM's own stream (230 KB a us, at least 0.064 us
-// a K block; several token tiles, which L2 feeds, 115 KB a us), what a cluster's CTAs hand each other (72 KB a us),
-// and the epilogue.  linear_kernel: 0.26 us a K block and round, 2.6 us more.
+// a K block; several token tiles, which L2 feeds, 115 KB a us), what a cluster's CTAs hand each other (40 KB a us),
+// and the epilogue.  linear_kernel: 0.28 us a K block and round, 2.6 us more.
 FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
   FewPlan best = {};
   if (q.kind == Kind::kWgrad) return best;
@@ -175,16 +195,17 @@ FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
   const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
   const int step = q.kind == Kind::kDgrad ? 64 : sides == 2 ? 8 : 16, most = 256 / sides;
   const double hbm = 2.0 * sides * p.N * p.K / 5.1e6, draw = ttiles > 1 ? 115e3 : 230e3;
-  double least = p.M > 128 ? tile_rounds(q, p, sms, best_pair(q, p, sms)) * kblocks * 0.26 + 2.6 : 1e30;
+  double least = p.M > 128 ? tile_rounds(q, p, sms, best_pair(q, p, sms)) * kblocks * 0.28 + 2.6 : 1e30;
   if (ttiles * p.N > 0x7fffffffll) return best;
   for (int cs = 1; cs <= 8 && cs <= kblocks; cs *= 2) {
+    const int at_once = cluster_slots(cs, sms);
     const int nkb = (kblocks + cs - 1) / cs;
     for (int width = step; width <= most && width < p.N + step; width += step) {
       const int wrows = width * sides, lg = (width / 8 + cs - 1) / cs;
       const long long tiles = ttiles * ((p.N + width - 1) / width);
-      const double rounds = static_cast<double>((tiles * cs + sms - 1) / sms);
+      const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
       const double stream = rounds * nkb * std::max((wrows + nt) * 128.0 / draw, 0.064);
-      const double end = (cs > 1 ? 0.12 + nt * wrows * (4.0 / 72e3) : 0.0) + std::min(p.M, nt) * lg * sides * 0.001 + wrows * 0.005;
+      const double end = (cs > 1 ? 0.2 + nt * wrows * (4.0 / 40e3) * (cs - 1) / cs : 0.0) + std::min(p.M, nt) * lg * sides * 0.001 + wrows * 0.005;
       const double cost = std::sqrt(stream * stream + hbm * hbm) + rounds * end;
       if (cost >= least) continue;
       // ring, partial sums (and, behind the last slot's token rows, what an MMA of 128 rows reads), barriers

@@ -29,6 +29,23 @@ cudaError_t launch_few_as(const LinearParams& p, int grid, int smem_bytes, cudaS
 
 }  // namespace
 
+cudaError_t linear_few_clusters(int cs, int* n) {
+  auto kernel = linear_few_kernel<false, kEpiBf16>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewMaxSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+}
+
 cudaError_t launch_linear_few(const LinearParams& p, int epi, bool w_mn, int grid, int smem_bytes, cudaStream_t s) {
   if (w_mn) return launch_few_as<true, kEpiBf16>(p, grid, smem_bytes, s);
   switch (epi) {

@@ -75,6 +75,8 @@ cudaError_t launch_linear_dgrad(const LinearParams& p, int cg, int grid, cudaStr
 cudaError_t launch_linear_wgrad(const LinearParams& p, int epi, int cg, int grid, cudaStream_t s);
 // The same for few tokens: tm_a over the features (w_mn: [K, N]), tm_b over the tokens, clusters of p.cs CTAs.
 cudaError_t launch_linear_few(const LinearParams& p, int epi, bool w_mn, int grid, int smem_bytes, cudaStream_t s);
+// How many clusters of cs CTAs with an SM's whole shared memory each run at once.
+cudaError_t linear_few_clusters(int cs, int* n);
 // The element-wise part of their backward pass, and the sums over partial rows.
 cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s);
 cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s);
