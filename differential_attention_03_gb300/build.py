@@ -30,7 +30,7 @@ SOURCES = ["api.cu", "k_simt.cu", "k_twopass_v1_d128.cu", "k_onepass_v1_d64.cu",
            "k_decode.cu", "k_backward.cu", "k_gemm.cu",
            "k_twopass_v1_d128_f8.cu", "k_onepass_v2_d128_f8.cu", "k_onepass_v1_d64_f8.cu", "k_onepass_save.cu", "k_bwd_tc.cu",
            "api_cache.cu", "k_cache.cu", "k_tree_v1_d64.cu", "k_tree_v1_d128.cu", "k_tree_v2_d128.cu",
-           "api_block.cu", "k_linear_fwd.cu", "k_linear_bwd.cu", "k_linear_few.cu", "k_residual_norm.cu"]
+           "api_block.cu", "k_linear_fwd.cu", "k_linear_bwd.cu", "k_linear_few.cu", "k_norm_bf16.cu", "k_norm_mixed.cu", "k_norm_f32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -525,22 +525,22 @@ namespace {
 
 // How a row of D elements is laid over threads.  Rows of 16-byte multiples: vectors of 8 elements, a power of two of
 // lanes up to 256 elements, above a CTA a row with one or two vectors a thread: forward two above 512 elements;
-// backward one (of two rows at once) up to 4096, as 512 threads are the most.  Other rows: 8 single elements a thread
-// (backward above 4096: 16).
+// backward one (of two rows at once) up to 4096, as 512 threads are the most.  Other rows: 8 elements a thread, in pairs
+// where the width is even (backward above 4096: 16).
 da::NormShape norm_shape(int D, bool grad) {
   da::NormShape h;
-  const bool vec = D % 8 == 0;
-  h.vec = vec ? 8 : 1;
-  h.nv = vec ? (D > (grad ? 4096 : 512) ? 2 : 1) : (grad && D > 4096 ? 16 : 8);
+  h.vec = D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1;
+  const int per = h.vec == 8 ? (D > (grad ? 4096 : 512) ? 16 : 8) : grad && D > 4096 ? 16 : 8;  // elements a thread
+  h.nv = per / h.vec;
   h.lanes = 32;
   if (D <= 256) {
-    h.layout = vec ? da::kSubWarp : da::kPlainWarp;
+    h.layout = h.vec == 8 ? da::kSubWarp : da::kPlainWarp;
     h.threads = 256;
-    if (vec)
+    h.nv = 8 / h.vec;
+    if (h.vec == 8)
       for (h.lanes = 4; h.lanes * 8 < D;) h.lanes *= 2;
   } else {
-    const int per = h.vec * h.nv;
-    h.layout = vec ? da::kRing : da::kPlain;
+    h.layout = h.vec == 8 ? da::kRing : da::kPlain;
     h.threads = ((D + per - 1) / per + 31) / 32 * 32;
   }
   return h;
@@ -570,6 +570,12 @@ diffattn_status norm_common(const char* fn, int dt, int sdt, int rows, int D, co
   if (gate && (gate_rows < 1 || rows % gate_rows != 0))
     return fail(DIFFATTN_ERR_SHAPE, "%s: rows (%d) must be a multiple of gate_rows (%d)", fn, rows, gate_rows);
   return DIFFATTN_OK;
+}
+
+cudaError_t launch_norm(const da::NormParams& p, const da::NormShape& h, int dt, int sdt, bool grad, int grid, int smem,
+                        cudaStream_t s) {
+  if (dt == DIFFATTN_F32) return da::launch_norm_f32(p, h, grad, grid, smem, s);
+  return sdt == DIFFATTN_F32 ? da::launch_norm_mixed(p, h, grad, grid, smem, s) : da::launch_norm_bf16(p, h, grad, grid, smem, s);
 }
 
 // Pieces of the backward pass: runs of rows that are summed over together.  A CTA takes neighbouring pieces.
@@ -644,8 +650,7 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
   const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)), 0,
                                std::max(1, std::min(16, (h.layout == da::kRing ? 512 : 1024) / h.threads)), &p.stages, &smem);
   const int grid = static_cast<int>(std::min<long long>((rows + workers - 1ll) / workers, static_cast<long long>(sms_or_default()) * per_sm));
-  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, false, grid, smem,
-                                                 static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_norm(p, h, dt, stream_dt, false, grid, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);
   return dh::success();
@@ -724,7 +729,7 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
   if (!norm_row_cta(h)) smem = norm_workers(h) * D * 4;
   p.off_post = smem;
   smem += norm_workers(h) * D * 4;
-  const cudaError_t e = da::launch_residual_norm(p, h, dt == DIFFATTN_F32, stream_dt == DIFFATTN_F32, true, n.grid, smem, s);
+  const cudaError_t e = launch_norm(p, h, dt, stream_dt, true, n.grid, smem, s);
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);
   da::SumParts q;

@@ -80,9 +80,10 @@ cudaError_t linear_few_clusters(int cs, int* n);
 // The element-wise part of their backward pass, and the sums over partial rows.
 cudaError_t launch_act_grad(const ActGradParams& p, bool gated, cudaStream_t s);
 cudaError_t launch_sum_parts(const SumParts& p, cudaStream_t s);
-// The norms around a block, forward or backward.
-cudaError_t launch_residual_norm(const NormParams& p, const NormShape& h, bool x_f32, bool s_f32, bool grad, int grid, int smem,
-                                 cudaStream_t s);
+// The norms around a block, forward or backward: bf16, bf16 on an fp32 stream, fp32.
+cudaError_t launch_norm_bf16(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s);
+cudaError_t launch_norm_mixed(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s);
+cudaError_t launch_norm_f32(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s);
 cudaError_t launch_wait_selftest(unsigned long long budget_cycles, int* status, cudaStream_t s);
 
 }  // namespace da

@@ -1,10 +1,11 @@
-// Launchers of the norms around a block.  Programmatic dependents: their CTAs come up while the kernel before them ends.
+// One pair of types of the norms around a block: a translation unit each, so that they compile in parallel.
+// Programmatic dependents: their CTAs come up while the kernel before them ends.
+#pragma once
+
 #include "launch.h"
 #include "residual_norm.cuh"
 
 namespace da {
-
-namespace {
 
 template <class Kernel>
 cudaError_t launch_kernel(Kernel kernel, const NormParams& p, int grid, int threads, int smem, cudaStream_t s) {
@@ -26,12 +27,14 @@ cudaError_t launch_kernel(Kernel kernel, const NormParams& p, int grid, int thre
 }
 
 template <typename TX, typename TS>
-cudaError_t launch_types(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s) {
+cudaError_t launch_norm_types(const NormParams& p, const NormShape& h, bool grad, int grid, int smem, cudaStream_t s) {
   auto go = [&](auto kernel) { return launch_kernel(kernel, p, grid, h.threads, smem, s); };
   if (grad) switch (h.layout) {
       case kSubWarp: return go(residual_norm_grad_kernel<TX, TS, 8, 1, kSubWarp>);
-      case kPlainWarp: return go(residual_norm_grad_kernel<TX, TS, 1, 8, kPlainWarp>);
+      case kPlainWarp:
+        return h.vec == 2 ? go(residual_norm_grad_kernel<TX, TS, 2, 4, kPlainWarp>) : go(residual_norm_grad_kernel<TX, TS, 1, 8, kPlainWarp>);
       case kPlain:
+        if (h.vec == 2) return h.nv == 4 ? go(residual_norm_grad_kernel<TX, TS, 2, 4, kPlain>) : go(residual_norm_grad_kernel<TX, TS, 2, 8, kPlain>);
         return h.nv == 8 ? go(residual_norm_grad_kernel<TX, TS, 1, 8, kPlain>) : go(residual_norm_grad_kernel<TX, TS, 1, 16, kPlain>);
       default:
         if (h.nv == 2) return go(residual_norm_grad_kernel<TX, TS, 8, 2, kRing>);
@@ -40,19 +43,10 @@ cudaError_t launch_types(const NormParams& p, const NormShape& h, bool grad, int
     }
   switch (h.layout) {
     case kSubWarp: return go(residual_norm_kernel<TX, TS, 8, 1, kSubWarp>);
-    case kPlainWarp: return go(residual_norm_kernel<TX, TS, 1, 8, kPlainWarp>);
-    case kPlain: return go(residual_norm_kernel<TX, TS, 1, 8, kPlain>);
+    case kPlainWarp: return h.vec == 2 ? go(residual_norm_kernel<TX, TS, 2, 4, kPlainWarp>) : go(residual_norm_kernel<TX, TS, 1, 8, kPlainWarp>);
+    case kPlain: return h.vec == 2 ? go(residual_norm_kernel<TX, TS, 2, 4, kPlain>) : go(residual_norm_kernel<TX, TS, 1, 8, kPlain>);
     default: return h.nv == 1 ? go(residual_norm_kernel<TX, TS, 8, 1, kRing>) : go(residual_norm_kernel<TX, TS, 8, 2, kRing>);
   }
-}
-
-}  // namespace
-
-cudaError_t launch_residual_norm(const NormParams& p, const NormShape& h, bool x_f32, bool s_f32, bool grad, int grid, int smem,
-                                 cudaStream_t s) {
-  if (x_f32) return launch_types<float, float>(p, h, grad, grid, smem, s);
-  if (s_f32) return launch_types<__nv_bfloat16, float>(p, h, grad, grid, smem, s);
-  return launch_types<__nv_bfloat16, __nv_bfloat16>(p, h, grad, grid, smem, s);
 }
 
 }  // namespace da

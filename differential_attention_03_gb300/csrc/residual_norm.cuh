@@ -20,7 +20,7 @@
 //             warp of its own for them would take a quarter of the registers
 //             from the others: 17 warps an SM instead of 16).
 //   kPlain    rows of any other width: a CTA (up to 256 elements: a warp) a
-//             row, single elements, plain loads.
+//             row, two or single elements at a time, plain loads.
 // Backward: a CTA takes neighbouring rows and a thread keeps its columns over
 // all of them, so the sums over rows stay in registers; each CTA writes them
 // once (for a gate shared by a group of rows: once a group, or once a chunk of
@@ -76,6 +76,32 @@ struct Row {
     for (int j = 1; j < N; ++j) t = fma2(v[j], o.v[j], t);
     float lo, hi;
     f2unpack(t, lo, hi);
+    return lo + hi;
+  }
+  __device__ __forceinline__ float square() const { return dot(*this); }
+  static __device__ __forceinline__ uint64_t mul(uint64_t a, uint64_t b) { return mul2(a, b); }
+  static __device__ __forceinline__ uint64_t fma(uint64_t a, uint64_t b, uint64_t c) { return fma2(a, b, c); }
+  static __device__ __forceinline__ uint64_t all(float x) { return f2pack(x, x); }
+};
+template <>
+struct Row<2> {
+  static constexpr int N = 1;
+  uint64_t v[1];
+  __device__ __forceinline__ void fill(float x) { v[0] = f2pack(x, x); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = f2pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  __device__ __forceinline__ void load(const float* p) { v[0] = *reinterpret_cast<const uint64_t*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+    float lo, hi;
+    f2unpack(v[0], lo, hi);
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(lo, hi);
+  }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<uint64_t*>(p) = v[0]; }
+  __device__ __forceinline__ float dot(const Row& o) const {
+    float lo, hi;
+    f2unpack(mul2(v[0], o.v[0]), lo, hi);
     return lo + hi;
   }
   __device__ __forceinline__ float square() const { return dot(*this); }
@@ -224,7 +250,8 @@ struct RowRing {
 
 // NV vectors of VEC elements a thread; thread t of a row's nt holds vectors t, t + nt, ...
 template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
-__global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 1024 : 256) residual_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 1024 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 4)
+    residual_norm_kernel(const NormParams p) {
   using R = Row<VEC>;
   __shared__ __align__(16) float buf[256];
   extern __shared__ __align__(128) uint8_t smem[];
@@ -380,7 +407,8 @@ __device__ __forceinline__ void write_columns(const RowTeam<LAYOUT>& team, const
 }
 
 template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
-__global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormParams p) {
+__global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 2)
+    residual_norm_grad_kernel(const NormParams p) {
   using R = Row<VEC>;
   __shared__ __align__(16) float buf[256];
   extern __shared__ __align__(128) uint8_t smem[];
@@ -410,12 +438,14 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormParam
   if (LAYOUT == kRing && threadIdx.x == 0) ring.start(piece_row(first), end, 1);
   if (RowTeam<LAYOUT>::kCta) __syncthreads();
   grid_dep_launch_dependents();
-  constexpr int RR = 1;
-  // Of a row's values only t is held across the reductions; s, dy and x are read from the slot again, the parameters
-  // from L1.
+  // kHold: a row's values and the parameters of a thread's columns stay in registers, every load of a row issued at its
+  // start.  Rows of the ring (16 elements a thread here): only t is held across the reductions; s, dy and x are read from
+  // the slot again, the parameters from L1.
   // dga: sums of dy n.  u: sums of t xh over a piece (with a gate a row: of t gate xh), of which gamma_post times is the
   // gate's gradient and the gate times gamma_post's; the latter's sums over pieces are in shared memory.
-  R dga[NV], u[NV];
+  constexpr bool kHold = LAYOUT != kRing;
+  constexpr int NH = kHold ? NV : 1;
+  R dga[NV], u[NV], kept_ga[NH], kept_c[NH];
   float* post_sums = reinterpret_cast<float*>(smem + p.off_post) + (RowTeam<LAYOUT>::kCta ? 0 : team.worker * p.D);
   auto column = [&](const float* from, int i) -> R {
     R w;
@@ -429,6 +459,7 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormParam
     dga[i].fill(0.f);
     u[i].fill(0.f);
     if (p.part_post && c < p.D) u[i].store(post_sums + c);
+    if (kHold && c < p.D) kept_ga[kHold ? i : 0] = column(p.gamma, i);
   }
   const auto scale = R::all(p.scale);
 
@@ -445,147 +476,156 @@ __global__ void __launch_bounds__(512) residual_norm_grad_kernel(const NormParam
       }
       return w;
     };
-    auto gamma_of = [&](int i) -> R { return column(p.gamma, i); };
-    auto c_of = combined;
-    long long at0 = (row0 + team.worker) * p.D;
-    for (long long head = row0; head < row1; head += RR * team.workers, at0 += static_cast<long long>(RR * team.workers) * p.D) {
-      R tt[RR][NV];  // t = the gradient of s, then that of gate p
-      const uint8_t* slot[RR];
-      bool live[RR];
-      float sums[2 * RR];
+    if (kHold) {
 #pragma unroll
-      for (int k = 0; k < RR; ++k) {
-        live[k] = head + team.worker + k < row1;
-        slot[k] = LAYOUT == kRing ? (k == 0 || live[k] ? ring.take(k) : smem) : nullptr;
-        sums[2 * k] = sums[2 * k + 1] = 0.f;
+      for (int i = 0; i < NV; ++i)
+        if ((t + i * nt) * VEC < p.D) kept_c[kHold ? i : 0] = combined(i);
+    }
+    auto gamma_of = [&](int i) -> R { return kHold ? kept_ga[kHold ? i : 0] : column(p.gamma, i); };
+    auto c_of = [&](int i) -> R { return kHold ? kept_c[kHold ? i : 0] : combined(i); };
+    long long at = (row0 + team.worker) * p.D;
+    for (long long head = row0; head < row1; head += team.workers, at += static_cast<long long>(team.workers) * p.D) {
+      const long long row = head + team.worker;
+      const bool live = RowTeam<LAYOUT>::kCta || row < row1;
+      auto mine = [&](int i) { return (t + i * nt) * VEC < p.D && live; };  // whether this thread has vector i
+      const uint8_t* slot = LAYOUT == kRing ? ring.take() : nullptr;
+      const TS* s_row = LAYOUT == kRing ? reinterpret_cast<const TS*>(slot) : static_cast<const TS*>(p.s) + at;
+      const TX* dy_row = LAYOUT == kRing ? reinterpret_cast<const TX*>(slot + ring.off[1]) : static_cast<const TX*>(p.dy) + at;
+      const TS* ds_row = LAYOUT == kRing ? reinterpret_cast<const TS*>(slot + ring.off[2]) : static_cast<const TS*>(p.ds) + at;
+      const TX* x_row = LAYOUT == kRing ? reinterpret_cast<const TX*>(slot + ring.off[3]) : static_cast<const TX*>(p.x) + at;
+      const float* gate_row = LAYOUT == kRing ? reinterpret_cast<const float*>(slot + ring.off[4]) : p.gate + at;
+      R tt[NV];  // t = the gradient of s, then that of gate p
+      R held_s[NH], held_dy[NH], held_x[NH], held_g[NH];
+      if (kHold) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (t + i * nt) * VEC, h = kHold ? i : 0;
+          if (!mine(i)) continue;
+          tt[i].fill(0.f);
+          held_x[h].fill(0.f);
+          if (p.norm) {
+            held_s[h].load(s_row + c);
+            held_dy[h].load(dy_row + c);
+          }
+          if (has_ds) tt[i].load(ds_row + c);
+          if (need_x) held_x[h].load(x_row + c);
+          if (row_gate) held_g[h].load(gate_row + c);
+        }
       }
-      auto mine = [&](int k, int i) { return (t + i * nt) * VEC < p.D && live[k]; };  // whether this thread has vector i
-      auto s_row = [&](int k) { return LAYOUT == kRing ? reinterpret_cast<const TS*>(slot[k]) : static_cast<const TS*>(p.s) + at0 + k * p.D; };
-      auto dy_row = [&](int k) {
-        return LAYOUT == kRing ? reinterpret_cast<const TX*>(slot[k] + ring.off[1]) : static_cast<const TX*>(p.dy) + at0 + k * p.D;
+      auto s_of = [&](int i) -> R {
+        if (kHold) return held_s[kHold ? i : 0];
+        R w;
+        w.load(s_row + (t + i * nt) * VEC);
+        return w;
       };
-      auto ds_row = [&](int k) {
-        return LAYOUT == kRing ? reinterpret_cast<const TS*>(slot[k] + ring.off[2]) : static_cast<const TS*>(p.ds) + at0 + k * p.D;
+      auto dy_of = [&](int i) -> R {
+        if (kHold) return held_dy[kHold ? i : 0];
+        R w;
+        w.load(dy_row + (t + i * nt) * VEC);
+        return w;
       };
-      auto x_row = [&](int k) {
-        return LAYOUT == kRing ? reinterpret_cast<const TX*>(slot[k] + ring.off[3]) : static_cast<const TX*>(p.x) + at0 + k * p.D;
+      auto x_of = [&](int i) -> R {
+        if (kHold) return held_x[kHold ? i : 0];
+        R w;
+        w.fill(0.f);
+        if (need_x) w.load(x_row + (t + i * nt) * VEC);
+        return w;
       };
-      auto gate_row = [&](int k) {
-        return LAYOUT == kRing ? reinterpret_cast<const float*>(slot[k] + ring.off[4]) : p.gate + at0 + k * p.D;
+      auto gate_of = [&](int i) -> R {
+        if (kHold) return held_g[kHold ? i : 0];
+        R w;
+        w.load(gate_row + (t + i * nt) * VEC);
+        return w;
       };
+      float sums[2] = {0.f, 0.f}, r = 0.f, mean = 0.f;  // one over rms(s); minus the mean of dn n, over rms(s)
       if (p.norm) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (t + i * nt) * VEC;
-          R ga;
-          if (c < p.D) ga = gamma_of(i);
+          if (!mine(i)) continue;
+          const R ga = gamma_of(i), sv = s_of(i);
+          R dn = dy_of(i);
 #pragma unroll
-          for (int k = 0; k < RR; ++k) {
-            if (!mine(k, i)) continue;
-            R sv, dn;
-            sv.load(s_row(k) + c);
-            dn.load(dy_row(k) + c);
-#pragma unroll
-            for (int j = 0; j < R::N; ++j) dn.v[j] = R::mul(dn.v[j], ga.v[j]);
-            sums[2 * k] += sv.square();
-            sums[2 * k + 1] += sv.dot(dn);
-          }
+          for (int j = 0; j < R::N; ++j) dn.v[j] = R::mul(dn.v[j], ga.v[j]);
+          sums[0] += sv.square();
+          sums[1] += sv.dot(dn);
         }
         team.sums(sums);
+        r = rsqrtf(sums[0] * inv_d + p.eps);
+        mean = -sums[1] * r * r * inv_d;
       }
-      float r[RR], mean[RR];  // one over rms(s); minus the mean of dn n, over rms(s)
-#pragma unroll
-      for (int k = 0; k < RR; ++k) {
-        r[k] = p.norm ? rsqrtf(sums[2 * k] * inv_d + p.eps) : 0.f;
-        mean[k] = p.norm ? -sums[2 * k + 1] * r[k] * r[k] * inv_d : 0.f;
-        sums[2 * k] = sums[2 * k + 1] = 0.f;
-      }
+      sums[0] = sums[1] = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (t + i * nt) * VEC;
-        if (c >= p.D) continue;
-        R ga, cv;
-        if (p.norm) ga = gamma_of(i);
-        if (p.post) cv = c_of(i);
-#pragma unroll
-        for (int k = 0; k < RR; ++k) {
-          if (!mine(k, i)) continue;
-          R& tk = tt[k][i];
+        if (!mine(i)) continue;
+        R& tk = tt[i];
+        if (!kHold) {
           tk.fill(0.f);
-          if (has_ds) tk.load(ds_row(k) + c);
-          if (p.norm) {
-            const auto rs = R::all(r[k]), m = R::all(mean[k]);
-            R sv, dn;
-            sv.load(s_row(k) + c);
-            dn.load(dy_row(k) + c);
-#pragma unroll
-            for (int j = 0; j < R::N; ++j) {
-              const auto n = R::mul(sv.v[j], rs);
-              dga[i].v[j] = R::fma(dn.v[j], n, dga[i].v[j]);
-              tk.v[j] = R::fma(R::mul(dn.v[j], ga.v[j]), rs, R::fma(n, m, tk.v[j]));
-            }
-          }
-          if (p.dresidual && DA_BOUNDS_V(head + team.worker + k < p.rows && c + VEC <= p.D, head))
-            tk.store(static_cast<TS*>(p.dresidual) + at0 + k * p.D + c);
-#pragma unroll
-          for (int j = 0; j < R::N; ++j) tk.v[j] = R::mul(tk.v[j], scale);
-          if (p.post) {
-            R xv, d;
-            xv.load(x_row(k) + c);
-#pragma unroll
-            for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(tk.v[j], cv.v[j]);
-            if (row_gate) {
-              R gv;
-              gv.load(gate_row(k) + c);
-#pragma unroll
-              for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(d.v[j], gv.v[j]);
-            }
-            sums[2 * k] += xv.square();
-            sums[2 * k + 1] += xv.dot(d);
-          }
+          if (has_ds) tk.load(ds_row + c);
         }
-      }
-      if (p.post) team.sums(sums);
-#pragma unroll
-      for (int k = 0; k < RR; ++k) {
-        r[k] = p.post ? rsqrtf(sums[2 * k] * inv_d + p.eps) : 1.f;       // one over rms(x)
-        mean[k] = p.post ? -sums[2 * k + 1] * r[k] * r[k] * inv_d : 0.f;  // minus the mean, over rms(x)
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * nt) * VEC;
-        if (c >= p.D) continue;
-        const R cv = c_of(i);
-#pragma unroll
-        for (int k = 0; k < RR; ++k) {
-          if (!mine(k, i)) continue;
-          const auto rx = R::all(r[k]), m = R::all(mean[k]);
-          R out, xh, gv;
-          xh.fill(0.f);
-          if (need_x) xh.load(x_row(k) + c);
-          if (row_gate) gv.load(gate_row(k) + c);
+        if (p.norm) {
+          const auto rs = R::all(r), m = R::all(mean);
+          const R ga = gamma_of(i), sv = s_of(i), dn = dy_of(i);
 #pragma unroll
           for (int j = 0; j < R::N; ++j) {
-            // (without the norm rx = 1, m = 0, and c is the gate alone)
-            xh.v[j] = R::mul(xh.v[j], rx);
-            const auto dp = row_gate ? R::mul(tt[k][i].v[j], gv.v[j]) : tt[k][i].v[j];
-            u[i].v[j] = R::fma(dp, xh.v[j], u[i].v[j]);
-            out.v[j] = R::fma(R::mul(dp, cv.v[j]), rx, R::mul(xh.v[j], m));
+            const auto n = R::mul(sv.v[j], rs);
+            dga[i].v[j] = R::fma(dn.v[j], n, dga[i].v[j]);
+            tk.v[j] = R::fma(R::mul(dn.v[j], ga.v[j]), rs, R::fma(n, m, tk.v[j]));
           }
-          const bool in = DA_BOUNDS_V(head + team.worker + k < p.rows && c + VEC <= p.D, head);
-          if (p.dx && in) out.store(static_cast<TX*>(p.dx) + at0 + k * p.D + c);
-          if (row_gate && p.part_gate && in) {
+        }
+        if (p.dresidual && DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row)) tk.store(static_cast<TS*>(p.dresidual) + at + c);
 #pragma unroll
-            for (int j = 0; j < R::N; ++j) xh.v[j] = R::mul(R::mul(tt[k][i].v[j], xh.v[j]), cv.v[j]);
-            xh.store(p.part_gate + at0 + k * p.D + c);
+        for (int j = 0; j < R::N; ++j) tk.v[j] = R::mul(tk.v[j], scale);
+        if (p.post) {
+          const R cv = c_of(i), xv = x_of(i);
+          R d;
+#pragma unroll
+          for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(tk.v[j], cv.v[j]);
+          if (row_gate) {
+            const R gv = gate_of(i);
+#pragma unroll
+            for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(d.v[j], gv.v[j]);
           }
+          sums[0] += xv.square();
+          sums[1] += xv.dot(d);
+        }
+      }
+      r = 1.f, mean = 0.f;
+      if (p.post) {
+        team.sums(sums);
+        r = rsqrtf(sums[0] * inv_d + p.eps);  // one over rms(x)
+        mean = -sums[1] * r * r * inv_d;      // minus the mean, over rms(x)
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * nt) * VEC;
+        if (!mine(i)) continue;
+        const auto rx = R::all(r), m = R::all(mean);
+        const R cv = c_of(i);
+        R out, xh = x_of(i), dp = tt[i];
+        if (row_gate) {
+          const R gv = gate_of(i);
+#pragma unroll
+          for (int j = 0; j < R::N; ++j) dp.v[j] = R::mul(dp.v[j], gv.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < R::N; ++j) {
+          // (without the norm rx = 1, m = 0, and c is the gate alone)
+          xh.v[j] = R::mul(xh.v[j], rx);
+          u[i].v[j] = R::fma(dp.v[j], xh.v[j], u[i].v[j]);
+          out.v[j] = R::fma(R::mul(dp.v[j], cv.v[j]), rx, R::mul(xh.v[j], m));
+        }
+        const bool in = DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row);
+        if (p.dx && in) out.store(static_cast<TX*>(p.dx) + at + c);
+        if (row_gate && p.part_gate && in) {
+#pragma unroll
+          for (int j = 0; j < R::N; ++j) xh.v[j] = R::mul(R::mul(tt[i].v[j], xh.v[j]), cv.v[j]);
+          xh.store(p.part_gate + at + c);
         }
       }
       if (LAYOUT == kRing) {
-        __syncthreads();  // (every thread has read the slots)
-#pragma unroll
-        for (int k = 0; k < RR; ++k)
-          if (live[k]) ring.refill(head + k + p.stages, end);
+        __syncthreads();  // (every thread has read the slot)
+        ring.refill(row + p.stages, end);
       }
     }
     if (p.part_post) {
