@@ -83,7 +83,8 @@ __device__ __forceinline__ uint64_t act_slope2(uint64_t z, uint64_t& value) {
     return fma2(mul2(z, e), pair_of(0.39894228040143268f), phi);
   }
   if (ACT == DIFFATTN_ACT_GELU_TANH) {
-    const uint64_t zz = mul2(z, z);
+    // (a z beyond 1e4 has a slope of 0 or 1 either way; its square would not always be finite)
+    const uint64_t zz = each(mul2(z, z), [](float x) { return fminf(x, 1e8f); });
     const uint64_t w = fma2(zz, pair_of(2.f * kLog2e * kGeluC0 * kGeluC1), pair_of(2.f * kLog2e * kGeluC0));
     const uint64_t s = sigmoid2(mul2(z, w));
     value = mul2(z, s);

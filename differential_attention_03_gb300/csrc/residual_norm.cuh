@@ -248,6 +248,16 @@ struct RowRing {
   }
 };
 
+// Rows whose sum of squares leaves fp32's range (elements above 1e17) are summed again scaled by this power of two.
+constexpr float kSmall = 8.271806125530277e-25f;  // 2^-80
+__device__ __forceinline__ bool overflowed(float q) { return q > 3.4028234e38f; }
+template <int VEC>
+__device__ __forceinline__ Row<VEC> scaled(Row<VEC> r, float k) {
+#pragma unroll
+  for (int j = 0; j < Row<VEC>::N; ++j) r.v[j] = Row<VEC>::mul(r.v[j], Row<VEC>::all(k));
+  return r;
+}
+
 // NV vectors of VEC elements a thread; thread t of a row's nt holds vectors t, t + nt, ...
 template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
 __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 1024 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 4)
@@ -331,17 +341,30 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
         if (row_gate) w[i].load(g_row + c);
       }
     }
-    float m = p.scale;
-    if (p.post) {
+    // one over rms(v)
+    auto inverse_rms = [&](auto&& have) {
       float q[1] = {0.f};
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (mine(i)) q[0] += v[i].square();
+        if (have(i)) q[0] += v[i].square();
       team.sums(q);
-      m *= rsqrtf(q[0] * inv_d + p.eps);
+      float r = rsqrtf(q[0] * inv_d + p.eps);
+      const bool over = overflowed(q[0]);
+      if (RowTeam<LAYOUT>::kCta ? over : __any_sync(0xffffffffu, over)) {
+        q[0] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (have(i)) q[0] += scaled(v[i], kSmall).square();
+        team.sums(q);
+        if (over) r = rsqrtf(q[0] * inv_d) * kSmall;
+      }
+      return r;
+    };
+    float m = p.scale;
+    if (p.post) {
+      m *= inverse_rms(mine);
       if (LAYOUT == kRing) ring.refill(row + p.stages * step, p.rows);
     }
-    float q[1] = {0.f};
     const auto mm = R::all(m);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -358,7 +381,6 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
       }
 #pragma unroll
       for (int j = 0; j < R::N; ++j) v[i].v[j] = R::fma(R::mul(v[i].v[j], k.v[j]), mm, r[i].v[j]);
-      q[0] += v[i].square();
       if (p.s_out && DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row)) v[i].store(static_cast<TS*>(p.s_out) + at + c);
     }
     if (!p.norm) {
@@ -368,8 +390,7 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
       }
       continue;
     }
-    team.sums(q);
-    const auto rs = R::all(rsqrtf(q[0] * inv_d + p.eps));
+    const auto rs = R::all(inverse_rms(mine));
     if (LAYOUT == kRing && !p.post) ring.refill(row + p.stages * step, p.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -537,23 +558,40 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
         w.load(gate_row + (t + i * nt) * VEC);
         return w;
       };
-      float sums[2] = {0.f, 0.f}, r = 0.f, mean = 0.f;  // one over rms(s); minus the mean of dn n, over rms(s)
-      if (p.norm) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (!mine(i)) continue;
-          const R ga = gamma_of(i), sv = s_of(i);
-          R dn = dy_of(i);
-#pragma unroll
-          for (int j = 0; j < R::N; ++j) dn.v[j] = R::mul(dn.v[j], ga.v[j]);
-          sums[0] += sv.square();
-          sums[1] += sv.dot(dn);
-        }
+      float r = 0.f, mean = 0.f;  // one over rms(s); minus the mean of dn n, over rms(s)
+      // From partial(k, sums), which adds this thread's share of the sums of (k v)^2 and of d (k v): one over rms(v), and
+      // minus the mean of d v / rms(v), over rms(v).
+      auto statistics = [&](auto&& partial) {
+        float sums[2] = {0.f, 0.f};
+        partial(1.f, sums);
         team.sums(sums);
         r = rsqrtf(sums[0] * inv_d + p.eps);
-        mean = -sums[1] * r * r * inv_d;
-      }
-      sums[0] = sums[1] = 0.f;
+        mean = -(sums[1] * r * inv_d) * r;
+        const bool over = overflowed(sums[0]);
+        if (RowTeam<LAYOUT>::kCta ? over : __any_sync(0xffffffffu, over)) {
+          sums[0] = sums[1] = 0.f;
+          partial(kSmall, sums);
+          team.sums(sums);
+          if (over) {
+            const float q = rsqrtf(sums[0] * inv_d);
+            r = q * kSmall;
+            mean = -(sums[1] * q * inv_d) * r;
+          }
+        }
+      };
+      if (p.norm)
+        statistics([&](float k, float (&sums)[2]) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (!mine(i)) continue;
+            const R ga = gamma_of(i), sv = scaled(s_of(i), k);
+            R dn = dy_of(i);
+#pragma unroll
+            for (int j = 0; j < R::N; ++j) dn.v[j] = R::mul(dn.v[j], ga.v[j]);
+            sums[0] += sv.square();
+            sums[1] += sv.dot(dn);
+          }
+        });
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (t + i * nt) * VEC;
@@ -576,26 +614,26 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
         if (p.dresidual && DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row)) tk.store(static_cast<TS*>(p.dresidual) + at + c);
 #pragma unroll
         for (int j = 0; j < R::N; ++j) tk.v[j] = R::mul(tk.v[j], scale);
-        if (p.post) {
-          const R cv = c_of(i), xv = x_of(i);
-          R d;
-#pragma unroll
-          for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(tk.v[j], cv.v[j]);
-          if (row_gate) {
-            const R gv = gate_of(i);
-#pragma unroll
-            for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(d.v[j], gv.v[j]);
-          }
-          sums[0] += xv.square();
-          sums[1] += xv.dot(d);
-        }
       }
       r = 1.f, mean = 0.f;
-      if (p.post) {
-        team.sums(sums);
-        r = rsqrtf(sums[0] * inv_d + p.eps);  // one over rms(x)
-        mean = -sums[1] * r * r * inv_d;      // minus the mean, over rms(x)
-      }
+      if (p.post)  // of x
+        statistics([&](float k, float (&sums)[2]) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (!mine(i)) continue;
+            const R cv = c_of(i), xv = scaled(x_of(i), k);
+            R d;
+#pragma unroll
+            for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(tt[i].v[j], cv.v[j]);
+            if (row_gate) {
+              const R gv = gate_of(i);
+#pragma unroll
+              for (int j = 0; j < R::N; ++j) d.v[j] = R::mul(d.v[j], gv.v[j]);
+            }
+            sums[0] += xv.square();
+            sums[1] += xv.dot(d);
+          }
+        });
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (t + i * nt) * VEC;
@@ -772,25 +810,58 @@ __global__ void __launch_bounds__(512) residual_norm_grad_pairs_kernel(const Nor
       constexpr int RR = decltype(count)::value;
       R tt[RR];
       uint32_t slot[RR];
-      float q[2], dot[2];
-      q[1] = dot[1] = 0.f;
+      float q[2], dot[2], r[2], mean[2];
+      // From partial(k, f, q, dot), this thread's share of the sums of (f v)^2 and of d (f v) of row k: one over rms(v), and
+      // minus the mean of d v / rms(v), over rms(v).
+      auto statistics = [&](auto&& partial, float* at) {
+        q[1] = dot[1] = 0.f;
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          partial(k, 1.f, q[k], dot[k]);
+          if (!mine) q[k] = dot[k] = 0.f;
+        }
+        float4 sums = cta_sum4(q[0], dot[0], q[1], dot[1], at);
+        q[0] = sums.x, dot[0] = sums.y, q[1] = sums.z, dot[1] = sums.w;
+        const bool over = overflowed(q[0]) || overflowed(q[1]);
+#pragma unroll
+        for (int k = 0; k < RR; ++k) {
+          r[k] = rsqrtf(q[k] * inv_d + p.eps);
+          mean[k] = -(dot[k] * r[k] * inv_d) * r[k];
+        }
+        if (over) {  // (the same for every thread)
+          __syncthreads();
+          float w[2] = {0.f, 0.f}, e[2] = {0.f, 0.f};
+          for (int k = 0; k < RR; ++k) {
+            partial(k, kSmall, w[k], e[k]);
+            if (!mine) w[k] = e[k] = 0.f;
+          }
+          sums = cta_sum4(w[0], e[0], w[1], e[1], at);
+          w[0] = sums.x, e[0] = sums.y, w[1] = sums.z, e[1] = sums.w;
+          for (int k = 0; k < RR; ++k)
+            if (overflowed(q[k])) {
+              const float s = rsqrtf(w[k] * inv_d);
+              r[k] = s * kSmall;
+              mean[k] = -(e[k] * s * inv_d) * r[k];
+            }
+        }
+      };
+#pragma unroll
+      for (int k = 0; k < RR; ++k) slot[k] = base + ring.take_slot(k) * ring.slot_bytes;
+      statistics(
+          [&](int k, float f, float& square, float& dots) {
+            R sv, dn;
+            load_shared8<TS>(sv, slot[k] + o_s);
+            load_shared8<TX>(dn, slot[k] + o_dy);
+            if (f != 1.f) sv = scaled(sv, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dn.v[j] = mul2(dn.v[j], ga.v[j]);
+            square = sv.square();
+            dots = sv.dot(dn);
+          },
+          buf);
 #pragma unroll
       for (int k = 0; k < RR; ++k) {
-        slot[k] = base + ring.take_slot(k) * ring.slot_bytes;
-        R sv, dn;
-        load_shared8<TS>(sv, slot[k] + o_s);
-        load_shared8<TX>(dn, slot[k] + o_dy);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dn.v[j] = mul2(dn.v[j], ga.v[j]);
-        q[k] = mine ? sv.square() : 0.f;
-        dot[k] = mine ? sv.dot(dn) : 0.f;
-      }
-      float4 sums = cta_sum4(q[0], dot[0], q[1], dot[1], buf);
-      q[0] = sums.x, dot[0] = sums.y, q[1] = sums.z, dot[1] = sums.w;
-#pragma unroll
-      for (int k = 0; k < RR; ++k) {
-        const float r = rsqrtf(q[k] * inv_d + p.eps);
-        const auto rs = R::all(r), m = R::all(-dot[k] * r * r * inv_d);
+        const auto rs = R::all(r[k]), m = R::all(mean[k]);
         R sv, dn;
         tt[k].fill(0.f);
         if (has_ds) load_shared8<TS>(tt[k], slot[k] + o_ds);
@@ -805,29 +876,28 @@ __global__ void __launch_bounds__(512) residual_norm_grad_pairs_kernel(const Nor
         if (p.dresidual && mine && DA_BOUNDS_V(row + k < p.rows && c + 8 <= p.D, row)) tt[k].store(static_cast<TS*>(p.dresidual) + at + k * p.D);
 #pragma unroll
         for (int j = 0; j < 4; ++j) tt[k].v[j] = mul2(tt[k].v[j], scale);
-        if (POST) {
-          R xv, d;
-          load_shared8<TX>(xv, slot[k] + o_x);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d.v[j] = mul2(tt[k].v[j], cv.v[j]);
-          if (row_gate) {
-            R gr;
-            load_shared8<float>(gr, slot[k] + o_g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d.v[j] = mul2(d.v[j], gr.v[j]);
-          }
-          q[k] = mine ? xv.square() : 0.f;
-          dot[k] = mine ? xv.dot(d) : 0.f;
-        }
       }
-      if (POST) {
-        sums = cta_sum4(q[0], dot[0], q[1], dot[1], buf + 64);
-        q[0] = sums.x, dot[0] = sums.y, q[1] = sums.z, dot[1] = sums.w;
-      }
+      if (POST)  // of x
+        statistics(
+            [&](int k, float f, float& square, float& dots) {
+              R xv, d;
+              load_shared8<TX>(xv, slot[k] + o_x);
+              if (f != 1.f) xv = scaled(xv, f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) d.v[j] = mul2(tt[k].v[j], cv.v[j]);
+              if (row_gate) {
+                R gr;
+                load_shared8<float>(gr, slot[k] + o_g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d.v[j] = mul2(d.v[j], gr.v[j]);
+              }
+              square = xv.square();
+              dots = xv.dot(d);
+            },
+            buf + 64);
 #pragma unroll
       for (int k = 0; k < RR; ++k) {
-        const float r = POST ? rsqrtf(q[k] * inv_d + p.eps) : 1.f;
-        const auto rx = R::all(r), m = R::all(POST ? -dot[k] * r * r * inv_d : 0.f);
+        const auto rx = R::all(POST ? r[k] : 1.f), m = R::all(POST ? mean[k] : 0.f);
         R xh, out;
         xh.fill(0.f);
         if (need_x) load_shared8<TX>(xh, slot[k] + o_x);
