@@ -1309,40 +1309,44 @@ def _rows(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
 
 
+_bf16, _f32 = torch.bfloat16, torch.float32
+
+
 def _here(dev) -> int:
     """The raw current stream of the current device, which has to be `dev`."""
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors are on device {dev}, the current device is cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _product(x, w, name, wname):
     """Of rows x [..., K] under weights w [n, K]: device, n, K, the leading shape, the number of rows, the row stride."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if w.dim() != 2 or x.dim() < 1:
-        raise ValueError(f"{name} must be [..., K] and {wname} [n, K]")
     dev = x.get_device()
-    n, K = w.shape
-    lead = x.shape[:-1]
-    if x.dtype == torch.bfloat16 and x.shape[-1] == K and x.is_contiguous():
-        ld = K
-    else:
-        ld = _rows(x, name, torch.bfloat16, lead + (K,), dev)
-    _on(w, wname, torch.bfloat16, w.shape, dev)
-    return dev, n, K, lead, lead.numel(), ld
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, wshape = x.shape, w.shape
+    if len(wshape) != 2 or not shape:
+        raise ValueError(f"{name} must be [..., K] and {wname} [n, K]")
+    n, K = wshape
+    if w.dtype is not _bf16 or w.get_device() != dev or not w.is_contiguous():
+        _on(w, wname, _bf16, wshape, dev)
+    lead = shape[:-1]
+    if x.dtype is _bf16 and shape[-1] == K and x.is_contiguous():
+        return dev, n, K, lead, lead.numel(), K
+    return dev, n, K, lead, lead.numel(), _rows(x, name, _bf16, lead + (K,), dev)
 
 
 def _linear(a, w, bias, act, residual, dtype, out, pre, stream):
     dev, N, K, lead, M, lda = _product(a, w, "a", "w")
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     shape = lead + (N,)
     ldo = ldr = N
     if out is None:
-        dtype = dtype or torch.bfloat16
-        out = _empty(shape, dtype, a.device, stream)
+        if dtype is None:
+            dtype = _bf16
+        out = torch.empty(shape, dtype=dtype, device=a.device) if stream is None else _empty(shape, dtype, a.device, stream)
     else:
-        if dtype is not None and out.dtype != dtype:
+        if dtype is not None and out.dtype is not dtype:
             raise ValueError(f"out must be {dtype}, got {out.dtype}")
         dtype = out.dtype
         ldo = _rows(out, "out", dtype, shape, dev)
@@ -1350,16 +1354,17 @@ def _linear(a, w, bias, act, residual, dtype, out, pre, stream):
     if code is None:
         code = _act_code(act)
     if bias is not None:
-        _on(bias, "bias", torch.float32, (N,), dev)
+        _on(bias, "bias", _f32, (N,), dev)
         bias = bias.data_ptr()
     if residual is not None:
-        ldr = _rows(residual, "residual", dtype, shape, dev)
+        if residual.dtype is not dtype or residual.shape != shape or residual.get_device() != dev or not residual.is_contiguous():
+            ldr = _rows(residual, "residual", dtype, shape, dev)
         residual = residual.data_ptr()
     if pre is not None:
-        _on(pre, "pre", torch.bfloat16, shape, dev)
+        _on(pre, "pre", _bf16, shape, dev)
         pre = pre.data_ptr()
     st = lib().diffattn_linear(M, N, K, a.data_ptr(), lda, w.data_ptr(), bias, code, residual, ldr,
-                               BF16 if dtype is torch.bfloat16 else _dt(out), out.data_ptr(), ldo, pre, raw)
+                               BF16 if dtype is _bf16 else _dt(out), out.data_ptr(), ldo, pre, raw)
     if st:
         _check(st)
     return out
@@ -1397,13 +1402,10 @@ def _workspace(workspace, need, dev, like, stream):
 
 def _grads(out, wanted, dev, device, stream) -> dict:
     """Tensors for the gradients `wanted` ((name, shape, dtype), ...): the caller's in the dict `out`, or new ones."""
-    r = {}
-    if out is None:
-        if stream is None:
-            for name, shape, dtype in wanted:
-                r[name] = torch.empty(shape, dtype=dtype, device=device)
-            return r
-        out = {}
+    if out is None and stream is None:
+        empty = torch.empty
+        return {name: empty(shape, dtype=dtype, device=device) for name, shape, dtype in wanted}
+    r, out = {}, out or {}
     known = [name for name, _, _ in wanted]
     for k in out:
         if k not in known:
@@ -1433,7 +1435,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K) bytes.
     """
     dev, N, K, lead, M, lda = _product(a, w, "a", "w")
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     shape = lead + (N,)
     ldy = _rows(dy, "dy", torch.bfloat16, shape, dev)
     code = _act_code(act)
@@ -1460,7 +1462,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
 
 def _gated(x, w_gu, act, out, gu, stream):
     dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     if F2 % 2:
         raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
     ldh = F = F2 // 2
@@ -1510,7 +1512,7 @@ def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, d
     tensor of gated_linear_backward_workspace_bytes(M, D, F) bytes.
     """
     dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     if F2 % 2:
         raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
     F = F2 // 2
@@ -1549,20 +1551,20 @@ def _gate_rows(gate, x, dev) -> int:
 
 def _norm_args(x, stream_dtype, gate, gamma_post, gamma):
     """Device, width, rows, the types' codes, gate rows."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
     dev, shape, dt = x.get_device(), x.shape, x.dtype
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
     if not x.is_contiguous():
         _on(x, "x", dt, shape, dev)
     D = shape[-1]
     if gamma_post is not None:
-        _on(gamma_post, "gamma_post", torch.float32, (D,), dev)
+        _on(gamma_post, "gamma_post", _f32, (D,), dev)
     if gamma is not None:
-        _on(gamma, "gamma", torch.float32, (D,), dev)
-    if stream_dtype is not torch.bfloat16 and stream_dtype is not torch.float32:
+        _on(gamma, "gamma", _f32, (D,), dev)
+    if stream_dtype is not _bf16 and stream_dtype is not _f32:
         raise ValueError(f"unsupported dtype {stream_dtype} (bf16 or fp32)")
-    return (dev, D, shape[:-1].numel(), BF16 if dt is torch.bfloat16 else _dt(x),
-            BF16 if stream_dtype is torch.bfloat16 else F32, 0 if gate is None else _gate_rows(gate, x, dev))
+    return (dev, D, shape[:-1].numel(), BF16 if dt is _bf16 else _dt(x), BF16 if stream_dtype is _bf16 else F32,
+            0 if gate is None else _gate_rows(gate, x, dev))
 
 
 def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=None, post=None, gamma=None,
@@ -1576,9 +1578,10 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     stream_dtype: the type of s where there is no residual (default x's).  out: s, which may be residual
     itself.  Returns (y, s); y is None without the second norm.
     """
-    sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or x.dtype)
+    xdt = x.dtype
+    sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or xdt)
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, sdt, gate, gamma_post, gamma)
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     shape = x.shape
     if residual is not None:
         _on(residual, "residual", sdt, shape, dev)
@@ -1586,8 +1589,10 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     else:
         residual_at = None
     if out is None:
-        out = _like(residual if residual is not None else x, stream) if residual is not None or sdt is x.dtype else _empty(
-            shape, sdt, x.device, stream)
+        if sdt is xdt and stream is None:
+            out = torch.empty_like(x)
+        else:
+            out = _empty(shape, sdt, x.device, stream)
     else:
         _on(out, "out", sdt, shape, dev)
     if not norm:
@@ -1598,7 +1603,7 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
         if y is None:
             y = _like(x, stream)
         else:
-            _on(y, "y", x.dtype, shape, dev)
+            _on(y, "y", xdt, shape, dev)
         y_at = y.data_ptr()
     st = lib().diffattn_residual_norm(dt, sd, rows, D, x.data_ptr(), residual_at, _addr(gate), gate_rows, scale,
                                       1 if (gamma_post is not None if post is None else post) else 0, _addr(gamma_post),
@@ -1622,7 +1627,7 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
     None or a tensor of residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
     """
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, s.dtype, gate, gamma_post, gamma)
-    raw = _here(dev) if stream is None else _stream(stream)
+    raw = _here(dev) if stream is None else stream.cuda_stream
     post = gamma_post is not None if post is None else bool(post)
     _on(s, "s", s.dtype, x.shape, dev)
     if dy is not None:

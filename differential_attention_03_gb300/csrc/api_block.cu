@@ -186,7 +186,7 @@ struct FewPlan {
 // cluster on average, 20 % at worst): HBM 5.1 MB a us together with an SM's own stream (230 KB a us, at least 0.064 us
 // a K block; several token tiles, which L2 feeds, 115 KB a us), what a cluster's CTAs hand each other (40 KB a us),
 // and the epilogue.  linear_kernel: 0.28 us a K block and round, 2.6 us more.
-FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
+FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms) {
   FewPlan best = {};
   if (q.kind == Kind::kWgrad) return best;
   const int sides = q.kind == Kind::kGated ? 2 : 1;
@@ -220,6 +220,23 @@ FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
     }
   }
   return best;
+}
+
+// The plans of the sizes that this thread asked for last.
+FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
+  struct Known {
+    int kind, M, N, K, sms;
+    FewPlan plan;
+  };
+  constexpr unsigned kEntries = 64;
+  static thread_local Known known[kEntries];  // (sms = 0: none yet)
+  const int kind = static_cast<int>(q.kind);
+  const unsigned h = static_cast<unsigned>(p.M) * 2654435761u ^ static_cast<unsigned>(p.N) * 40503u ^ static_cast<unsigned>(p.K) * 9973u ^
+                     static_cast<unsigned>(kind) * 131u;
+  Known& k = known[(h >> 7) % kEntries];
+  if (k.sms != sms || k.kind != kind || k.M != p.M || k.N != p.N || k.K != p.K)
+    k = Known{kind, p.M, p.N, p.K, sms, make_few_plan(q, p, sms)};
+  return k.plan;
 }
 
 // Descriptors, tiles, status word and launch of a product whose sizes and epilogue are in p.
