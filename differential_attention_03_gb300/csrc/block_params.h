@@ -9,7 +9,7 @@
 namespace da {
 
 constexpr int kNormMaxD = 8192;
-constexpr int kNormMaxSmem = 200 * 1024;
+constexpr int kNormMaxSmem = 224 * 1024;
 constexpr int kNormMaxStages = 8;
 // Layouts of a row (residual_norm.cuh).
 enum NormLayout { kSubWarp, kRing, kPlain, kPlainWarp };
