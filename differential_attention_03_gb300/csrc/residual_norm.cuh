@@ -341,12 +341,9 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
         if (row_gate) w[i].load(g_row + c);
       }
     }
-    // one over rms(v)
-    auto inverse_rms = [&](auto&& have) {
-      float q[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (have(i)) q[0] += v[i].square();
+    // One over rms(v), from this thread's share of the sum of squares.
+    auto inverse_rms = [&](float share) {
+      float q[1] = {share};
       team.sums(q);
       float r = rsqrtf(q[0] * inv_d + p.eps);
       const bool over = overflowed(q[0]);
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
         q[0] = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (have(i)) q[0] += scaled(v[i], kSmall).square();
+          if (mine(i)) q[0] += scaled(v[i], kSmall).square();
         team.sums(q);
         if (over) r = rsqrtf(q[0] * inv_d) * kSmall;
       }
@@ -362,9 +359,14 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
     };
     float m = p.scale;
     if (p.post) {
-      m *= inverse_rms(mine);
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (mine(i)) q += v[i].square();
+      m *= inverse_rms(q);
       if (LAYOUT == kRing) ring.refill(row + p.stages * step, p.rows);
     }
+    float q = 0.f;
     const auto mm = R::all(m);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -381,6 +383,7 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
       }
 #pragma unroll
       for (int j = 0; j < R::N; ++j) v[i].v[j] = R::fma(R::mul(v[i].v[j], k.v[j]), mm, r[i].v[j]);
+      q += v[i].square();
       if (p.s_out && DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row)) v[i].store(static_cast<TS*>(p.s_out) + at + c);
     }
     if (!p.norm) {
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 102
       }
       continue;
     }
-    const auto rs = R::all(inverse_rms(mine));
+    const auto rs = R::all(inverse_rms(q));
     if (LAYOUT == kRing && !p.post) ring.refill(row + p.stages * step, p.rows);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
