@@ -44,7 +44,9 @@ cudaError_t launch_norm_types(const NormParams& p, const NormShape& h, bool grad
   switch (h.layout) {
     case kSubWarp: return go(residual_norm_kernel<TX, TS, 8, 1, kSubWarp>);
     case kPlainWarp: return h.vec == 2 ? go(residual_norm_kernel<TX, TS, 2, 4, kPlainWarp>) : go(residual_norm_kernel<TX, TS, 1, 8, kPlainWarp>);
-    case kPlain: return h.vec == 2 ? go(residual_norm_kernel<TX, TS, 2, 4, kPlain>) : go(residual_norm_kernel<TX, TS, 1, 8, kPlain>);
+    case kPlain:
+      if (h.vec == 2) return h.nv == 4 ? go(residual_norm_kernel<TX, TS, 2, 4, kPlain>) : go(residual_norm_kernel<TX, TS, 2, 8, kPlain>);
+      return h.nv == 8 ? go(residual_norm_kernel<TX, TS, 1, 8, kPlain>) : go(residual_norm_kernel<TX, TS, 1, 16, kPlain>);
     default: return h.nv == 1 ? go(residual_norm_kernel<TX, TS, 8, 1, kRing>) : go(residual_norm_kernel<TX, TS, 8, 2, kRing>);
   }
 }

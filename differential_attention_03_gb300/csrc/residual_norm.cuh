@@ -260,7 +260,7 @@ __device__ __forceinline__ Row<VEC> scaled(Row<VEC> r, float k) {
 
 // NV vectors of VEC elements a thread; thread t of a row's nt holds vectors t, t + nt, ...
 template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
-__global__ void __launch_bounds__(LAYOUT == kRing ? 512 : LAYOUT == kPlain ? 1024 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 4)
+__global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 4)
     residual_norm_kernel(const NormParams p) {
   using R = Row<VEC>;
   __shared__ __align__(16) float buf[256];
