@@ -271,7 +271,8 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
-    p.wide = p.N % 16 == 0 && p.ldo % 16 == 0 && p.ldr % 16 == 0 && p.ldp % 16 == 0 && aligned(p.out, 32) &&
+    const int sector = q.epi == da::kEpiF32 ? 8 : 16;  // elements of 32 bytes (pre, in bf16, is written 16 bytes at a time beside fp32)
+    p.wide = p.N % sector == 0 && p.ldo % sector == 0 && p.ldr % sector == 0 && p.ldp % sector == 0 && aligned(p.out, 32) &&
              aligned(p.residual, 32) && aligned(p.pre, 32);
     const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
     if (2 * tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);

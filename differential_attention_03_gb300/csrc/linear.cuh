@@ -18,15 +18,15 @@
 // clusters without work takes 128 CG x 128 tiles instead.  With CG = 2 an MMA is M256 N256 K16
 // over both SMs' tensor cores: each CTA holds its 128 rows of A and half of B,
 // so a CTA's shared memory feeds half as many B bytes.
-//   warps 0-7   epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
+//   warps 0-7   (kEpiF32: 16 warps, 64 columns each) epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
 //               columns 128 (w / 4) .. (gated: 64 gate columns and their 64 up
 //               columns).  A lane's row moves between registers and global
-//               memory in 32-byte sectors; in fp32, or where rows are not
-//               multiples of 32 bytes, through a 4 KB staging buffer a warp
+//               memory in 32-byte sectors; in bf16 whose rows are not multiples
+//               of 32 bytes through a 4 KB staging buffer a warp
 //               (rows of 128 bytes, 16-byte parts XORed by the row), 8 lanes a
 //               128-byte row.
-//   warp 8      TMA producer: per K block of 64 the A and B boxes into a ring.
-//   warp 9      TMEM allocator; MMA issuer (of the cluster's first CTA).
+//   then        TMA producer: per K block of 64 the A and B boxes into a ring.
+//   last warp   TMEM allocator; MMA issuer (of the cluster's first CTA).
 // TMEM: two 256-column accumulators: the epilogue of one tile overlaps the
 // next one's main loop.  A programmatic dependent launch: barriers and TMEM are
 // set up while the kernel before ends.
@@ -130,17 +130,20 @@ __device__ __forceinline__ void mma_cg(uint32_t d_tmem, uint64_t a_desc, uint64_
 }
 
 // ----------------------------------------------------------------- layout
-template <int CG, bool A_MN, bool B_MN>
+// Epilogue warps: kEpiF32 holds sums in registers, 64 columns a thread (128 would spill: a warp may have 168).
+__host__ __device__ constexpr int linear_epi_warps(int epi) { return epi == kEpiF32 ? 16 : 8; }
+
+template <int CG, bool A_MN, bool B_MN, int EPI>
 struct LinearCfg {
   static constexpr int BM = kLinBM, BN = kLinBN, BK = kLinBK;
   static constexpr int BN_CTA = BN / CG;  // rows of B that a CTA holds
-  static constexpr int EPI_WARPS = 8, NTHREADS = (EPI_WARPS + 2) * 32;
+  static constexpr int EPI_WARPS = linear_epi_warps(EPI), NTHREADS = (EPI_WARPS + 2) * 32;
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = BN_CTA * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 48 KB, a pair's CTA 32 KB
   static constexpr int STAGES = 196608 / STAGE_BYTES;    // 4, a pair 6
   static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * 4096;
+  static constexpr int OFF_BARS = OFF_STAGING + (EPI == kEpiF32 ? 0 : EPI_WARPS * 4096);
   static constexpr int NBARS = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], mma_done
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
@@ -251,6 +254,14 @@ __device__ __forceinline__ void put_bf16_rows(uint8_t* stg, const float (&v)[64]
   stage_store(stg, reinterpret_cast<uint8_t*>(dst), ld * 2, rows, min(cols, 64) * 2, lane);
 }
 
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]),
+                 "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
+               :
+               : "memory");
+}
+
 // 64 accumulator columns as floats.
 __device__ __forceinline__ void load_cols64(uint32_t taddr, float (&v)[64]) {
   uint32_t a[32], b[32];
@@ -307,65 +318,48 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
   put_bf16_rows(stg, v, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
 }
 
-// The same in fp32: 32 columns (a 128-byte row).
-__device__ __forceinline__ void epilogue_f32(const LinearParams& p, float* v, uint8_t* stg, long long r0, int c0, int rows,
-                                             int cols, int lane) {
-  uint4 res[8];
-  if (p.residual)
-    stage_load(res, reinterpret_cast<const uint8_t*>(static_cast<const float*>(p.residual) + r0 * p.ldr + c0), p.ldr * 4,
-               rows, cols * 4, lane);
-  if (p.bias) {
+// The same in fp32: 64 columns of this lane's row from registers, 32 bytes at a time (16 where rows are not multiples of
+// that).
+__device__ __forceinline__ void epilogue_f32(const LinearParams& p, float (&v)[64], long long row, int c0, int cols) {
+  float* out = static_cast<float*>(p.out) + row * p.ldo + c0;
+  const float* res = static_cast<const float*>(p.residual) + row * p.ldr + c0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (4 * q < cols) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + q);
-        v[4 * q] += b.x;
-        v[4 * q + 1] += b.y;
-        v[4 * q + 2] += b.z;
-        v[4 * q + 3] += b.w;
-      }
-  }
-  if (p.pre) {  // 32 columns of bf16: 64 bytes a row
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *stage_row(stg, lane, q) = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                            pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-    __syncwarp();
-    stage_store(stg, reinterpret_cast<uint8_t*>(p.pre + r0 * p.ldp + c0), p.ldp * 2, rows, min(cols, 32) * 2, lane);
-  }
-  if (p.act != DIFFATTN_ACT_NONE)
-    with_act(p.act, [&](auto tag) {
-      act_all<decltype(tag)::value, 32>(v);
-    });
-  if (p.residual) {
-    __syncwarp();
-    stage_put(stg, res, lane);
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint4 w = *stage_row(stg, lane, q);
-      v[4 * q] += __uint_as_float(w.x);
-      v[4 * q + 1] += __uint_as_float(w.y);
-      v[4 * q + 2] += __uint_as_float(w.z);
-      v[4 * q + 3] += __uint_as_float(w.w);
+  for (int q = 0; q < 8; ++q) {
+    if (8 * q >= cols) break;
+    float* w = v + 8 * q;
+    if (p.bias) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + 2 * q), b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + 2 * q + 1);
+      w[0] += a.x, w[1] += a.y, w[2] += a.z, w[3] += a.w;
+      w[4] += b.x, w[5] += b.y, w[6] += b.z, w[7] += b.w;
+    }
+    if (p.pre) *reinterpret_cast<uint4*>(p.pre + row * p.ldp + c0 + 8 * q) = pack8_at(w);
+    if (p.act != DIFFATTN_ACT_NONE) with_act(p.act, [&](auto tag) { act_all<decltype(tag)::value, 8>(w); });
+    if (p.residual) {
+      uint4 a, b;
+      if (p.wide)
+        load32(res + 8 * q, a, b);
+      else
+        a = reinterpret_cast<const uint4*>(res + 8 * q)[0], b = reinterpret_cast<const uint4*>(res + 8 * q)[1];
+      w[0] += __uint_as_float(a.x), w[1] += __uint_as_float(a.y), w[2] += __uint_as_float(a.z), w[3] += __uint_as_float(a.w);
+      w[4] += __uint_as_float(b.x), w[5] += __uint_as_float(b.y), w[6] += __uint_as_float(b.z), w[7] += __uint_as_float(b.w);
+    }
+    const uint4 a = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3]));
+    const uint4 b = make_uint4(__float_as_uint(w[4]), __float_as_uint(w[5]), __float_as_uint(w[6]), __float_as_uint(w[7]));
+    if (!DA_BOUNDS_V(row < p.M && c0 + 8 * q + 8 <= p.N, row)) continue;
+    if (p.wide) {
+      store32(out + 8 * q, a, b);
+    } else {
+      reinterpret_cast<uint4*>(out + 8 * q)[0] = a;
+      reinterpret_cast<uint4*>(out + 8 * q)[1] = b;
     }
   }
-  __syncwarp();
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    *stage_row(stg, lane, q) = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                                          __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-  __syncwarp();
-  stage_store(stg, reinterpret_cast<uint8_t*>(static_cast<float*>(p.out) + r0 * p.ldo + c0), p.ldo * 4, rows,
-              min(cols, 32) * 4, lane);
 }
 
 // ----------------------------------------------------------------- kernel
 template <int CG, bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
+__global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
     linear_kernel(const __grid_constant__ LinearParams p) {
-  using C = LinearCfg<CG, A_MN, B_MN>;
+  using C = LinearCfg<CG, A_MN, B_MN, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -524,7 +518,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
     __syncwarp();
   } else {
     // ================================================================ epilogue
-    const int wq = warp & 3, half = warp >> 2;
+    const int wq = warp & 3, half = warp >> 2;  // (kEpiF32: quarter)
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     uint8_t* stg = smem + C::OFF_STAGING + warp * 4096;
     uint32_t empty0[2];
@@ -574,30 +568,28 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN>::NTHREADS, 1)
         });
         put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
       } else if (EPI == kEpiF32) {
-        const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
-        float v[128];
+        const int mine = x.cols >> 2;  // columns of this quarter of the warps
+        const int c0 = x.n0 + half * mine, cols = min(mine, p.N - c0);
+        float v[64];
         for (int kb = 0; kb < kblocks; kb += seg, ++i) {
           if (!acc_wait(i)) {
             ok = false;
             break;
           }
-          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * width);
+          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * mine);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (32 * q >= width) break;
-            uint32_t r[32];
-            tmem_ld32(acc + 32 * q, r);
-            tmem_ld_wait(r);
+            if (16 * q >= mine) break;
+            uint32_t r[16];
+            tmem_ld16(acc + 16 * q, r);
+            tmem_ld_wait16(r);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[32 * q + j] = kb == 0 ? __uint_as_float(r[j]) : v[32 * q + j] + __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) v[16 * q + j] = kb == 0 ? __uint_as_float(r[j]) : v[16 * q + j] + __uint_as_float(r[j]);
           }
           acc_release(i);
         }
         if (!ok) break;
-        if (rows <= 0) continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (cols > 32 * q) epilogue_f32(p, v + 32 * q, stg, r0, c0 + 32 * q, rows, cols - 32 * q, lane);
+        if (lane < rows && cols > 0) epilogue_f32(p, v, r0 + lane, c0, cols);
       } else {
         const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         uint4 res[8];

@@ -8,7 +8,7 @@ namespace da {
 
 template <int CG, bool A_MN, bool B_MN, int EPI>
 cudaError_t launch_linear_cg(const LinearParams& p, int grid, cudaStream_t s) {
-  using C = LinearCfg<CG, A_MN, B_MN>;
+  using C = LinearCfg<CG, A_MN, B_MN, EPI>;
   auto kernel = linear_kernel<CG, A_MN, B_MN, EPI>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;

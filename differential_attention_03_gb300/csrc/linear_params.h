@@ -31,7 +31,7 @@ struct LinearParams {
   long long ldr, ldo, ldp;
   int M, N, K;           // gated: N = F
   int act;
-  int wide;  // residual, out and pre: bases and rows of bf16 in multiples of 32 bytes
+  int wide;  // residual and out (in bf16 also pre): bases and rows in multiples of 32 bytes
   int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
   int full;                       // tiles before the ones that come in halves
   // linear_few: features (gated: gate features) and token rows of a tile, CTAs that share its contraction, groups of
