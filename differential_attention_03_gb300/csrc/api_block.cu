@@ -119,6 +119,24 @@ diffattn_status map_rows(CUtensorMap* m, const void* base, long long rows, long 
   return DIFFATTN_OK;
 }
 
+// 3-D map for stores of 32 rows x 128 bytes (swizzled) into rows of `sides` parts of `cols` columns; what lies past an
+// edge is dropped.
+diffattn_status map_out(CUtensorMap* m, void* base, long long rows, int sides, long long cols, long long ld, bool f32) {
+  dh::EncodeTiled enc;
+  diffattn_status s = dh::encoder(&enc);
+  if (s != DIFFATTN_OK) return s;
+  const cuuint64_t es = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(sides), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * es, static_cast<cuuint64_t>(ld) * es};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, 1, 32};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DIFFATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return DIFFATTN_OK;
+}
+
 enum class Kind { kForward, kGated, kDgrad, kWgrad };
 
 constexpr int kGroupRows = 2048;  // rows of a group of the tile walk
@@ -271,14 +289,13 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
-    const int sector = q.epi == da::kEpiF32 ? 8 : 16;  // elements of 32 bytes (pre, in bf16, is written 16 bytes at a time beside fp32)
-    p.wide = p.N % sector == 0 && p.ldo % sector == 0 && p.ldr % sector == 0 && p.ldp % sector == 0 && aligned(p.out, 32) &&
-             aligned(p.residual, 32) && aligned(p.pre, 32);
     const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
     if (2 * tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
     p.full = static_cast<int>(full_tiles(tiles, clusters));
     if ((st = map_x(&p.tm_a, 128)) != DIFFATTN_OK) return st;
     if ((st = map_w(&p.tm_b, 64)) != DIFFATTN_OK) return st;
+    if ((st = map_out(&p.tm_out, p.out, p.M, 1, p.N, p.ldo, q.epi == da::kEpiF32)) != DIFFATTN_OK) return st;
+    if (p.pre && (st = map_out(&p.tm_pre, p.pre, p.M, q.kind == Kind::kGated ? 2 : 1, p.N, p.ldp, false)) != DIFFATTN_OK) return st;
     const int grid = static_cast<int>(std::min(p.full + 2 * (tiles - p.full), clusters)) * cg;
     e = q.kind == Kind::kDgrad   ? da::launch_linear_dgrad(p, cg, grid, s)
         : q.kind == Kind::kWgrad ? da::launch_linear_wgrad(p, q.epi, cg, grid, s)

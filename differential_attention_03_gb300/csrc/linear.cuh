@@ -20,11 +20,8 @@
 // so a CTA's shared memory feeds half as many B bytes.
 //   warps 0-7   (kEpiF32: 16 warps, 64 columns each) epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
 //               columns 128 (w / 4) .. (gated: 64 gate columns and their 64 up
-//               columns).  A lane's row moves between registers and global
-//               memory in 32-byte sectors; in bf16 whose rows are not multiples
-//               of 32 bytes through a 4 KB staging buffer a warp
-//               (rows of 128 bytes, 16-byte parts XORed by the row), 8 lanes a
-//               128-byte row.
+//               columns).  32 rows of 128 bytes at a time leave through a
+//               4 KB staging buffer a warp (128-byte swizzle) by TMA.
 //   then        TMA producer: per K block of 64 the A and B boxes into a ring.
 //   last warp   TMEM allocator; MMA issuer (of the cluster's first CTA).
 // TMEM: two 256-column accumulators: the epilogue of one tile overlaps the
@@ -141,9 +138,9 @@ struct LinearCfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = BN_CTA * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 48 KB, a pair's CTA 32 KB
-  static constexpr int STAGES = 196608 / STAGE_BYTES;    // 4, a pair 6
+  static constexpr int STAGES = (229376 - EPI_WARPS * 4096) / STAGE_BYTES;  // 4, a pair 6; kEpiF32: 3 and 5
   static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
-  static constexpr int OFF_BARS = OFF_STAGING + (EPI == kEpiF32 ? 0 : EPI_WARPS * 4096);
+  static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * 4096;
   static constexpr int NBARS = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], mma_done
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
@@ -178,9 +175,13 @@ __device__ __forceinline__ LinTile linear_tile(const LinearParams& p, int t) {
 }
 
 // ----------------------------------------------------------------- staging
-// 32 rows x 128 bytes between global memory (rows `ld` bytes apart, `rows` of
-// them and the first `bytes` bytes of each, a multiple of 16) and a warp's
-// staging buffer; lane = part lane % 8 of rows lane / 8 + 4 i.
+// A warp's staging buffer: 32 rows x 128 bytes, 16-byte parts XORed by the row (the 128-byte swizzle of a tensor map).
+// Part `q` of a row:
+__device__ __forceinline__ uint4* stage_at(uint8_t* stg, int row, int q) {
+  return reinterpret_cast<uint4*>(stg + row * 128 + ((q ^ (row & 7)) << 4));
+}
+// Global rows (`ld` bytes apart, `rows` of them and the first `bytes` bytes of each, a multiple of 16) to registers, 8
+// lanes a row (lane = part lane % 8 of rows lane / 8 + 4 i), and from there into the buffer.
 __device__ __forceinline__ void stage_load(uint4 (&r)[8], const uint8_t* src, long long ld, int rows, int bytes, int lane) {
   const int part = lane & 7;
 #pragma unroll
@@ -191,67 +192,59 @@ __device__ __forceinline__ void stage_load(uint4 (&r)[8], const uint8_t* src, lo
   }
 }
 __device__ __forceinline__ void stage_put(uint8_t* stg, const uint4 (&r)[8], int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) *stage_at(stg, (lane >> 3) + 4 * i, lane & 7) = r[i];
+}
+// The same without registers between; stage_copied: it has landed.
+__device__ __forceinline__ void stage_copy(uint8_t* stg, const uint8_t* src, long long ld, int rows, int bytes, int lane) {
   const int part = lane & 7;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = (lane >> 3) + 4 * i;
-    *reinterpret_cast<uint4*>(stg + row * 128 + ((part ^ (row & 7)) << 4)) = r[i];
+    if (row < rows && part * 16 < bytes && DA_BOUNDS(row < 32))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(stage_at(stg, row, part))), "l"(src + row * ld + part * 16)
+                   : "memory");
   }
 }
-__device__ __forceinline__ void stage_store(const uint8_t* stg, uint8_t* dst, long long ld, int rows, int bytes, int lane) {
-  const int part = lane & 7;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = (lane >> 3) + 4 * i;
-    const uint4 v = *reinterpret_cast<const uint4*>(stg + row * 128 + ((part ^ (row & 7)) << 4));
-    if (row < rows && part * 16 < bytes && DA_BOUNDS(row < 32 && part < 8))
-      *reinterpret_cast<uint4*>(dst + row * ld + part * 16) = v;
-  }
+__device__ __forceinline__ void stage_copied() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 }
-// Part `q` (16 bytes) of this lane's own row.
-__device__ __forceinline__ uint4* stage_row(uint8_t* stg, int lane, int q) {
-  return reinterpret_cast<uint4*>(stg + lane * 128 + ((q ^ (lane & 7)) << 4));
+// Until the stores sent from the buffer have read it.
+__device__ __forceinline__ void stage_free(int lane) {
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+}
+// The buffer to columns from c0 of side c1, rows from r0: the tensor map drops what lies past its edges.
+__device__ __forceinline__ void stage_send(const CUtensorMap* map, uint8_t* stg, int c0, int c1, int r0, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (DA_TMA_OK(smem_u32(stg), c0, c1, r0, 0))
+      asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(smem_u32(stg)), "r"(c0), "r"(c1), "r"(r0)
+                   : "memory");
+    bulk_commit_group();
+  }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 32 bytes of a lane, to or from global memory (32-byte aligned).
-__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
-               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-               : "memory");
-}
-__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-               : "l"(p)
-               : "memory");
-}
-
 __device__ __forceinline__ uint4 pack8_at(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// This lane's row of 64 values as bf16 to global memory.  wide (rows of 32-byte multiples): whole 32-byte sectors from
-// each lane, which leaves shared memory to the MMAs (8002 x 8192 x 2048, gelu, stored z: 637 cycles a K block through
-// the staging buffer); else through that buffer, 8 lanes a 128-byte row.
-__device__ __forceinline__ void put_bf16_rows(uint8_t* stg, const float (&v)[64], __nv_bfloat16* dst, long long ld,
-                                              int rows, int cols, int lane, bool wide) {
-  if (wide) {
-    if (lane < rows && DA_BOUNDS(cols > 0)) {
-      __nv_bfloat16* at = dst + lane * ld;
+// This lane's row of 64 values as bf16, from column c0 of a side.  Whole lines leave by TMA: with 32-byte sectors straight
+// from each lane a CTA's 64 KB took 5200 cycles (8192 x 8192 x 64: 47.6 us, in fp32 83.4; 34.5 and 50.2 so).  A second
+// buffer a warp in place of a ring slot: no faster.
+__device__ __forceinline__ void put_bf16_rows(uint8_t* stg, const float (&v)[64], const CUtensorMap* map, int c0, int side, int r0,
+                                              int lane) {
+  stage_free(lane);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (16 * q < cols) store32(at + 16 * q, pack8_at(v + 16 * q), pack8_at(v + 16 * q + 8));
-    }
-    return;
-  }
-  __syncwarp();  // (the buffer's earlier readers)
-#pragma unroll
-  for (int q = 0; q < 8; ++q) *stage_row(stg, lane, q) = pack8_at(v + 8 * q);
-  __syncwarp();
-  stage_store(stg, reinterpret_cast<uint8_t*>(dst), ld * 2, rows, min(cols, 64) * 2, lane);
+  for (int q = 0; q < 8; ++q) *stage_at(stg, lane, q) = pack8_at(v + 8 * q);
+  stage_send(map, stg, c0, side, r0, lane);
 }
 
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&a)[16]) {
@@ -276,35 +269,36 @@ __device__ __forceinline__ void load_cols64(uint32_t taddr, float (&v)[64]) {
 }
 
 // ----------------------------------------------------------------- epilogues
-// 64 columns from column c0 (global) of the warp's 32 rows from row r0:
-// `rows` rows and `cols` columns of them exist.  res: the residual's rows as stage_load read them.
-__device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[64], const uint4 (&res)[8], uint8_t* stg,
-                                              long long r0, int c0, int rows, int cols, int lane) {
-  if (p.bias) {
+template <int N>
+__device__ __forceinline__ void add_bias(float* v, const float* bias, int cols) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (4 * q < cols) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + q);
-        v[4 * q] += b.x;
-        v[4 * q + 1] += b.y;
-        v[4 * q + 2] += b.z;
-        v[4 * q + 3] += b.w;
-      }
-  }
-  if (p.pre) put_bf16_rows(stg, v, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane, p.wide);
+  for (int q = 0; q < N / 4; ++q)
+    if (4 * q < cols) {
+      const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + q);
+      v[4 * q] += b.x;
+      v[4 * q + 1] += b.y;
+      v[4 * q + 2] += b.z;
+      v[4 * q + 3] += b.w;
+    }
+}
+
+// 64 columns from column c0 (global) of the warp's 32 rows from row r0, `cols` columns of which exist.  res: the
+// residual's rows as stage_load read them.
+__device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[64], const uint4 (&res)[8], uint8_t* stg,
+                                              int r0, int c0, int cols, int lane) {
+  if (p.bias) add_bias<64>(v, p.bias + c0, cols);
+  if (p.pre) put_bf16_rows(stg, v, &p.tm_pre, c0, 0, r0, lane);
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
       act_all<decltype(tag)::value, 64>(v);
     });
   if (p.residual) {
-    if (!p.wide) {
-      __syncwarp();
-      stage_put(stg, res, lane);
-      __syncwarp();
-    }
+    stage_free(lane);
+    stage_put(stg, res, lane);
+    __syncwarp();
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const uint4 w = p.wide ? res[q] : *stage_row(stg, lane, q);
+      const uint4 w = *stage_at(stg, lane, q);
       v[8 * q] += bf16_lo(w.x);
       v[8 * q + 1] += bf16_hi(w.x);
       v[8 * q + 2] += bf16_lo(w.y);
@@ -315,43 +309,46 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
       v[8 * q + 7] += bf16_hi(w.w);
     }
   }
-  put_bf16_rows(stg, v, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
+  put_bf16_rows(stg, v, &p.tm_out, c0, 0, r0, lane);
 }
 
-// The same in fp32: 64 columns of this lane's row from registers, 32 bytes at a time (16 where rows are not multiples of
-// that).
-__device__ __forceinline__ void epilogue_f32(const LinearParams& p, float (&v)[64], long long row, int c0, int cols) {
-  float* out = static_cast<float*>(p.out) + row * p.ldo + c0;
-  const float* res = static_cast<const float*>(p.residual) + row * p.ldr + c0;
+// Columns c0 .. c0 + 32 of an fp32 residual into the staging buffer.
+__device__ __forceinline__ void fetch_f32(const LinearParams& p, uint8_t* stg, int r0, int c0, int rows, int cols, int lane) {
+  stage_free(lane);
+  stage_copy(stg, reinterpret_cast<const uint8_t*>(static_cast<const float*>(p.residual) + r0 * p.ldr + c0), p.ldr * 4, rows, cols * 4, lane);
+}
+
+// The same in fp32, 32 columns at a time; `rows` rows exist.  The first columns of a residual are on their way, unless
+// the stored z needs the buffer first.
+__device__ __forceinline__ void epilogue_f32(const LinearParams& p, float (&v)[64], uint8_t* stg, int r0, int c0, int rows,
+                                             int cols, int lane) {
+  if (p.bias) add_bias<64>(v, p.bias + c0, cols);
+  if (p.pre) put_bf16_rows(stg, v, &p.tm_pre, c0, 0, r0, lane);
+  if (p.act != DIFFATTN_ACT_NONE)
+    with_act(p.act, [&](auto tag) {
+      act_all<decltype(tag)::value, 64>(v);
+    });
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    if (8 * q >= cols) break;
-    float* w = v + 8 * q;
-    if (p.bias) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + 2 * q), b = __ldg(reinterpret_cast<const float4*>(p.bias + c0) + 2 * q + 1);
-      w[0] += a.x, w[1] += a.y, w[2] += a.z, w[3] += a.w;
-      w[4] += b.x, w[5] += b.y, w[6] += b.z, w[7] += b.w;
-    }
-    if (p.pre) *reinterpret_cast<uint4*>(p.pre + row * p.ldp + c0 + 8 * q) = pack8_at(w);
-    if (p.act != DIFFATTN_ACT_NONE) with_act(p.act, [&](auto tag) { act_all<decltype(tag)::value, 8>(w); });
+  for (int h = 0; h < 2; ++h) {
+    if (32 * h >= cols) break;
     if (p.residual) {
-      uint4 a, b;
-      if (p.wide)
-        load32(res + 8 * q, a, b);
-      else
-        a = reinterpret_cast<const uint4*>(res + 8 * q)[0], b = reinterpret_cast<const uint4*>(res + 8 * q)[1];
-      w[0] += __uint_as_float(a.x), w[1] += __uint_as_float(a.y), w[2] += __uint_as_float(a.z), w[3] += __uint_as_float(a.w);
-      w[4] += __uint_as_float(b.x), w[5] += __uint_as_float(b.y), w[6] += __uint_as_float(b.z), w[7] += __uint_as_float(b.w);
-    }
-    const uint4 a = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]), __float_as_uint(w[3]));
-    const uint4 b = make_uint4(__float_as_uint(w[4]), __float_as_uint(w[5]), __float_as_uint(w[6]), __float_as_uint(w[7]));
-    if (!DA_BOUNDS_V(row < p.M && c0 + 8 * q + 8 <= p.N, row)) continue;
-    if (p.wide) {
-      store32(out + 8 * q, a, b);
+      if (h > 0 || p.pre) fetch_f32(p, stg, r0, c0 + 32 * h, rows, cols - 32 * h, lane);
+      stage_copied();
     } else {
-      reinterpret_cast<uint4*>(out + 8 * q)[0] = a;
-      reinterpret_cast<uint4*>(out + 8 * q)[1] = b;
+      stage_free(lane);
     }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float4* at = reinterpret_cast<float4*>(stage_at(stg, lane, q));
+      const float* w = v + 32 * h + 4 * q;
+      float4 x = make_float4(w[0], w[1], w[2], w[3]);
+      if (p.residual) {
+        const float4 y = *at;
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      *at = x;
+    }
+    stage_send(&p.tm_out, stg, c0 + 32 * h, 0, r0, lane);
   }
 }
 
@@ -521,9 +518,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
     const int wq = warp & 3, half = warp >> 2;  // (kEpiF32: quarter)
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     uint8_t* stg = smem + C::OFF_STAGING + warp * 4096;
-    uint32_t empty0[2];
-#pragma unroll
-    for (int a = 0; a < 2; ++a) empty0[a] = CG == 2 ? map_to_rank(&acc_empty[a], 0) : 0;
+    const uint32_t empty0 = CG == 2 ? map_to_rank(&acc_empty[0], 0) : 0;
     auto acc_wait = [&](long long i) -> bool {
       const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, ab));
       tc_fence_after();
@@ -534,7 +529,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if (CG == 2)
-          mbar_arrive_cluster(empty0[i & 1]);
+          mbar_arrive_cluster(empty0 + static_cast<uint32_t>(i & 1) * 8u);
         else
           mbar_arrive(&acc_empty[i & 1]);
       }
@@ -545,65 +540,61 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
     for (int t = cid; ok && t < steps; t += ncl) {
       const LinTile x = linear_tile<EPI>(p, t);
       if (x.n0 >= p.N) continue;
-      const long long r0 = static_cast<long long>(x.mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
-      const int rows = static_cast<int>(min(32ll, static_cast<long long>(p.M) - r0));  // (<= 0: none)
-      const int width = x.cols >> 1;  // accumulator columns of this half of the warps
+      const int r0 = (x.mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
+      const int rows = min(32, p.M - r0);  // (<= 0: none)
       if (EPI == kEpiGated) {
-        // gate columns and their up columns, 64 each; of a half tile 32 (what lies beyond is loaded and not used)
-        const int off = half * (width >> 1), c0 = x.n0 + off, cols = min(width >> 1, p.N - c0);
+        // 64 gate columns and their up columns (a half tile has no more than 64)
+        const int off = half * 64, width = x.cols >> 1, c0 = x.n0 + off, cols = off < width ? p.N - c0 : 0;
         if (!acc_wait(i)) break;
         const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + off);
         float g[64], u[64];
-        load_cols64(acc, g);
-        load_cols64(acc + static_cast<uint32_t>(width), u);
+        if (off < width) {
+          load_cols64(acc, g);
+          load_cols64(acc + static_cast<uint32_t>(width), u);
+        }
         acc_release(i);
         ++i;
         if (rows <= 0 || cols <= 0) continue;
         if (p.pre) {
-          put_bf16_rows(stg, g, p.pre + r0 * p.ldp + c0, p.ldp, rows, cols, lane, p.wide);
-          put_bf16_rows(stg, u, p.pre + r0 * p.ldp + p.N + c0, p.ldp, rows, cols, lane, p.wide);
+          put_bf16_rows(stg, g, &p.tm_pre, c0, 0, r0, lane);
+          put_bf16_rows(stg, u, &p.tm_pre, c0, 1, r0, lane);
         }
         with_act(p.act, [&](auto tag) {
           act_times<decltype(tag)::value, 64>(g, u);
         });
-        put_bf16_rows(stg, g, static_cast<__nv_bfloat16*>(p.out) + r0 * p.ldo + c0, p.ldo, rows, cols, lane, p.wide);
+        put_bf16_rows(stg, g, &p.tm_out, c0, 0, r0, lane);
       } else if (EPI == kEpiF32) {
-        const int mine = x.cols >> 2;  // columns of this quarter of the warps
-        const int c0 = x.n0 + half * mine, cols = min(mine, p.N - c0);
+        const int off = half * 64, c0 = x.n0 + off, cols = off < x.cols ? p.N - c0 : 0;
+        if (p.residual && !p.pre && rows > 0 && cols > 0) fetch_f32(p, stg, r0, c0, rows, cols, lane);
         float v[64];
         for (int kb = 0; kb < kblocks; kb += seg, ++i) {
           if (!acc_wait(i)) {
             ok = false;
             break;
           }
-          const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + half * mine);
+          if (off < x.cols) {
+            const uint32_t acc = tl + static_cast<uint32_t>((i & 1) * C::BN + off);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if (16 * q >= mine) break;
-            uint32_t r[16];
-            tmem_ld16(acc + 16 * q, r);
-            tmem_ld_wait16(r);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t r[16];
+              tmem_ld16(acc + 16 * q, r);
+              tmem_ld_wait16(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[16 * q + j] = kb == 0 ? __uint_as_float(r[j]) : v[16 * q + j] + __uint_as_float(r[j]);
+              for (int j = 0; j < 16; ++j) v[16 * q + j] = kb == 0 ? __uint_as_float(r[j]) : v[16 * q + j] + __uint_as_float(r[j]);
+            }
           }
           acc_release(i);
         }
         if (!ok) break;
-        if (lane < rows && cols > 0) epilogue_f32(p, v, r0 + lane, c0, cols);
+        if (rows > 0 && cols > 0) epilogue_f32(p, v, stg, r0, c0, rows, cols, lane);
       } else {
+        const int width = x.cols >> 1;  // accumulator columns of this half of the warps
         const int c0 = x.n0 + half * width, cols = min(width, p.N - c0);
         uint4 res[8];
         auto fetch = [&](int q) {
-          if (!p.residual || rows <= 0 || cols <= 64 * q) return;
-          if (p.wide) {  // this lane's own row
-            const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(p.residual) + (r0 + lane) * p.ldr + c0 + 64 * q;
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-              if (lane < rows && 64 * q + 16 * h < cols) load32(at + 16 * h, res[2 * h], res[2 * h + 1]);
-          } else {
+          if (p.residual && rows > 0 && cols > 64 * q)
             stage_load(res, reinterpret_cast<const uint8_t*>(static_cast<const __nv_bfloat16*>(p.residual) + r0 * p.ldr + c0 + 64 * q),
                        p.ldr * 2, rows, (cols - 64 * q) * 2, lane);
-          }
         };
         fetch(0);
         if (!acc_wait(i)) break;
@@ -611,16 +602,18 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
         float v[64];
         load_cols64(acc, v);
         if (width == 64) acc_release(i);
-        if (rows > 0 && cols > 0) epilogue_bf16(p, v, res, stg, r0, c0, rows, cols, lane);
+        if (rows > 0 && cols > 0) epilogue_bf16(p, v, res, stg, r0, c0, cols, lane);
         if (width > 64) {
-          fetch(1);
+          fetch(1);  // (earlier it costs registers that the activations need: 4096 x 4096 x 512, gelu, stored z: 36 for 31 us)
           load_cols64(acc + 64, v);
           acc_release(i);
-          if (rows > 0 && cols > 64) epilogue_bf16(p, v, res, stg, r0, c0 + 64, rows, cols - 64, lane);
+          if (rows > 0 && cols > 64) epilogue_bf16(p, v, res, stg, r0, c0 + 64, cols - 64, lane);
         }
         ++i;
       }
     }
+    if (lane == 0) bulk_wait_all();  // (the staging buffer lives until its stores are done, aborted or not)
+    __syncwarp();
   }
 
   tc_fence_before();

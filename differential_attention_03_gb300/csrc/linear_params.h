@@ -24,6 +24,7 @@ constexpr int kFewMaxSmem = 232448;
 struct LinearParams {
   CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
   CUtensorMap tm_b;  // over B ({K, N} or {N, K}), box {64, 64}; linear_few: the tokens, box {64, nt}
+  CUtensorMap tm_out, tm_pre;  // linear_kernel: {N, sides, M} box {128 bytes, 1, 32}; pre has two sides if gated
   const float* bias;     // [N] or nullptr
   const void* residual;  // [M, N] in the output's type or nullptr
   void* out;
@@ -31,7 +32,6 @@ struct LinearParams {
   long long ldr, ldo, ldp;
   int M, N, K;           // gated: N = F
   int act;
-  int wide;  // residual and out (in bf16 also pre): bases and rows in multiples of 32 bytes
   int tiles_m, tiles_n, group_m;  // tiles_m in units of a cluster's rows
   int full;                       // tiles before the ones that come in halves
   // linear_few: features (gated: gate features) and token rows of a tile, CTAs that share its contraction, groups of
