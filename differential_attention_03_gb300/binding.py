@@ -1312,11 +1312,15 @@ def _rows(t, name, dtype, shape, dev):
 _bf16, _f32 = torch.bfloat16, torch.float32
 
 
-def _here(dev) -> int:
-    """The raw current stream of the current device, which has to be `dev`."""
+def _here(dev, stream) -> int:
+    """The raw stream `stream` (None: the current one) of the current device, which has to be `dev`."""
     if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors are on device {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(dev)
+        raise ValueError(f"tensors are on device {dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"tensors are on device {dev}, the stream is on device {stream.device_index}")
+    return stream.cuda_stream
 
 
 def _product(x, w, name, wname):
@@ -1328,17 +1332,20 @@ def _product(x, w, name, wname):
     if len(wshape) != 2 or not shape:
         raise ValueError(f"{name} must be [..., K] and {wname} [n, K]")
     n, K = wshape
+    lead = shape[:-1]
+    M = lead.numel()
+    if (M | n | K) >> 31:
+        raise ValueError(f"{name} {tuple(shape)} and {wname} {tuple(wshape)}: sizes are below 2^31")
     if w.dtype is not _bf16 or w.get_device() != dev or not w.is_contiguous():
         _on(w, wname, _bf16, wshape, dev)
-    lead = shape[:-1]
     if x.dtype is _bf16 and shape[-1] == K and x.is_contiguous():
-        return dev, n, K, lead, lead.numel(), K
-    return dev, n, K, lead, lead.numel(), _rows(x, name, _bf16, lead + (K,), dev)
+        return dev, n, K, lead, M, K
+    return dev, n, K, lead, M, _rows(x, name, _bf16, lead + (K,), dev)
 
 
 def _linear(a, w, bias, act, residual, dtype, out, pre, stream):
     dev, N, K, lead, M, lda = _product(a, w, "a", "w")
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     shape = lead + (N,)
     ldo = ldr = N
     if out is None:
@@ -1435,7 +1442,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K) bytes.
     """
     dev, N, K, lead, M, lda = _product(a, w, "a", "w")
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     shape = lead + (N,)
     ldy = _rows(dy, "dy", torch.bfloat16, shape, dev)
     code = _act_code(act)
@@ -1462,7 +1469,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
 
 def _gated(x, w_gu, act, out, gu, stream):
     dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     if F2 % 2:
         raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
     ldh = F = F2 // 2
@@ -1512,7 +1519,7 @@ def gated_linear_backward(x, w_gu, gu, dh, act: str = "silu", dx: bool = True, d
     tensor of gated_linear_backward_workspace_bytes(M, D, F) bytes.
     """
     dev, F2, D, lead, M, ldx = _product(x, w_gu, "x", "w_gu")
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     if F2 % 2:
         raise ValueError(f"w_gu must be [2 F, D], got {tuple(w_gu.shape)}")
     F = F2 // 2
@@ -1554,16 +1561,20 @@ def _norm_args(x, stream_dtype, gate, gamma_post, gamma):
     dev, shape, dt = x.get_device(), x.shape, x.dtype
     if dev < 0:
         raise ValueError("x must be a CUDA tensor")
+    if not shape:
+        raise ValueError("x must be [..., D]")
+    D, rows = shape[-1], shape[:-1].numel()
+    if (D | rows) >> 31:
+        raise ValueError(f"x {tuple(shape)}: sizes are below 2^31")
     if not x.is_contiguous():
         _on(x, "x", dt, shape, dev)
-    D = shape[-1]
     if gamma_post is not None:
         _on(gamma_post, "gamma_post", _f32, (D,), dev)
     if gamma is not None:
         _on(gamma, "gamma", _f32, (D,), dev)
     if stream_dtype is not _bf16 and stream_dtype is not _f32:
         raise ValueError(f"unsupported dtype {stream_dtype} (bf16 or fp32)")
-    return (dev, D, shape[:-1].numel(), BF16 if dt is _bf16 else _dt(x), BF16 if stream_dtype is _bf16 else F32,
+    return (dev, D, rows, BF16 if dt is _bf16 else _dt(x), BF16 if stream_dtype is _bf16 else F32,
             0 if gate is None else _gate_rows(gate, x, dev))
 
 
@@ -1581,7 +1592,7 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     xdt = x.dtype
     sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or xdt)
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, sdt, gate, gamma_post, gamma)
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     shape = x.shape
     if residual is not None:
         _on(residual, "residual", sdt, shape, dev)
@@ -1627,7 +1638,7 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
     None or a tensor of residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
     """
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, s.dtype, gate, gamma_post, gamma)
-    raw = _here(dev) if stream is None else stream.cuda_stream
+    raw = _here(dev, stream)
     post = gamma_post is not None if post is None else bool(post)
     _on(s, "s", s.dtype, x.shape, dev)
     if dy is not None:

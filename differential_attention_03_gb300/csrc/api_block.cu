@@ -127,7 +127,7 @@ diffattn_status map_out(CUtensorMap* m, void* base, long long rows, int sides, l
   if (s != DIFFATTN_OK) return s;
   const cuuint64_t es = f32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(sides), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * es, static_cast<cuuint64_t>(ld) * es};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sides > 1 ? cols : ld) * es, static_cast<cuuint64_t>(ld) * es};
   const cuuint32_t box[3] = {f32 ? 32u : 64u, 1, 32};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
@@ -326,6 +326,9 @@ diffattn_status wgrad(const char* fn, int M, int N, int C, const void* dz, long 
   return launch_product(fn, Product{Kind::kWgrad, dt == DIFFATTN_F32 ? da::kEpiF32 : da::kEpiBf16, dz, a, ldz, lda}, p, s);
 }
 
+// Sizes of a backward pass whose kernels' 32-bit indexes (a step past the last row, chunk or column block) do not overflow.
+bool too_large(int M, int N, int K) { return M > 0x7ffe0000 || N > 0x3fff0000 || K > 0x3fff0000; }
+
 // Row chunks of the element-wise kernels: some eight CTAs an SM, at least 32 rows each.
 int act_grad_chunks(int M, int N) {
   const long long across = (N + 255) / 256;
@@ -414,6 +417,7 @@ diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, lon
     return fail(DIFFATTN_ERR_SHAPE, "%s: N and K must be multiples of 8 (16-byte rows; got N=%d K=%d)", fn, N, K);
   if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
   if (bad_dtype(dw_dt)) return fail(DIFFATTN_ERR_DTYPE, "%s: dw must be bf16 or fp32", fn);
+  if (too_large(M, N, K)) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t wes = dtype_bytes(dw_dt);
   diffattn_status st;
@@ -514,7 +518,7 @@ diffattn_status diffattn_gated_linear_backward(int M, int D, int F, const void* 
     return fail(DIFFATTN_ERR_SHAPE, "%s: D and F must be multiples of 8 (16-byte rows; got D=%d F=%d)", fn, D, F);
   if (bad_act(act)) return fail(DIFFATTN_ERR_DTYPE, "%s: unknown activation %d", fn, (int)act);
   if (bad_dtype(dw_dt)) return fail(DIFFATTN_ERR_DTYPE, "%s: dw must be bf16 or fp32", fn);
-  if (F > 0x3fffffff) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+  if (too_large(M, F, D)) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t wes = dtype_bytes(dw_dt);
   diffattn_status st;

@@ -785,6 +785,7 @@ diffattn_status diffattn_v2_cache_keep(diffattn_cache_format fmt, int B, int A, 
  * Matrices are row-major; a row stride (ld*) counts elements and is at least the
  * row's width and a multiple of 8 (bf16) or 4 (fp32); bases are 16-byte aligned
  * (else ERR_ALIGN); products' widths (N, K, D, F) are multiples of 8 (else ERR_SHAPE).
+ * Sizes whose indexes would not fit 32 bits (rows from 2^31 - 2^17, widths from 2^30 - 2^16 on) are ERR_SHAPE at the latest.
  * An output may overlap nothing else of its call unless said otherwise (ERR_SHAPE);
  * rows of two tensors that lie side by side in one buffer do not overlap.
  * Each call is asynchronous on `stream` and allocates nothing.

@@ -151,6 +151,14 @@ def test_norm_backward_refuses(L):
     assert _norm_bwd(L, dx=None, dr=None, dg=None, dgp=None, dga=None) == da.OK
 
 
+def test_backward_passes_refuse_sizes_whose_indexes_would_overflow(L):
+    for kw in (dict(M=0x7ffffff0, N=8, K=8, ldy=8, dx=None, dw=None), dict(M=1, N=0x7ffffff8, K=8, ldy=0x7ffffff8, dx=None, dw=None),
+               dict(M=1, N=8, K=0x7ffffff8, ldy=8, lda=0x7ffffff8)):
+        assert _linear_bwd(L, **kw) == da.ERR_SHAPE and b"too large" in L.diffattn_last_error(), kw
+    for kw in (dict(M=0x7ffffff0, F=8, D=8, ldh=8), dict(M=1, F=0x3ffffff8, D=8, ldh=0x3ffffff8), dict(M=1, F=8, D=0x7ffffff8, ldx=0x7ffffff8, ldh=8)):
+        assert _gated_bwd(L, **kw) == da.ERR_SHAPE and b"too large" in L.diffattn_last_error(), kw
+
+
 def test_workspace_sizes(L):
     for bad in ((0, 8, 8), (8, 0, 8), (-1, 8, 8)):
         assert L.diffattn_linear_backward_workspace(*bad) == 0 and L.diffattn_gated_linear_backward_workspace(*bad) == 0

@@ -60,6 +60,43 @@ def test_poisoned_neighbours_are_not_seen(M, K):
     da.device_status()
 
 
+@pytest.mark.parametrize("M", [1, 100, 129, 300, 1000])
+@pytest.mark.parametrize("N", [8, 72, 200, 456])
+def test_what_lies_around_an_output_stays(M, N):
+    """Outputs, stored z and gradients that end inside a tile, in the middle of a tensor of sevens: the values are those
+    of the same call into tensors of its own (an fp32 output's sums go by segments, so its z is not a bf16 output's)."""
+    rnd = _rnd(7 * M + N)
+    K = 520  # (a short contraction, and one above 512 values)
+    a, w, gu_w = rnd(M, K), rnd(N, K), rnd(2 * N, K)
+    for dt in (BF, F32):
+        wide = torch.full((M + 3, N + 128), 7.0, device="cuda", dtype=dt)
+        pool = torch.full((M + 3, N), 7.0, device="cuda", dtype=BF)
+        out = wide[1:M + 1, 64:64 + N]
+        y, pre = da.linear_train(a, w, act="silu", out=out, pre=pool[:M], dtype=dt)
+        alone = da.linear_train(a, w, act="silu", dtype=dt)
+        assert torch.equal(out, alone[0]) and torch.equal(pre, alone[1])
+        wide[1:M + 1, 64:64 + N] = 7
+        assert (wide == 7).all() and (pool[M:] == 7).all()
+    wide = torch.full((M + 3, N + 128), 7.0, device="cuda", dtype=BF)
+    pool = torch.full((M + 3, 2 * N), 7.0, device="cuda", dtype=BF)
+    out = wide[1:M + 1, 64:64 + N]
+    h, gu = da.gated_linear_train(a, gu_w, out=out, gu=pool[:M])
+    alone = da.gated_linear_train(a, gu_w)
+    assert torch.equal(out, alone[0]) and torch.equal(gu, alone[1])
+    wide[1:M + 1, 64:64 + N] = 7
+    assert (wide == 7).all() and (pool[M:] == 7).all()
+    dy = rnd(M, N)
+    for dt in (BF, F32):
+        flat = torch.full((N * K + 64,), 7.0, device="cuda", dtype=dt)
+        rows = torch.full((M * K + 64,), 7.0, device="cuda", dtype=BF)
+        out = {"dw": flat[:N * K].view(N, K), "da": rows[:M * K].view(M, K)}
+        got = da.linear_backward(a, w, dy, out=out, dw_dtype=dt)
+        want = da.linear_backward(a, w, dy, dw_dtype=dt)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        assert (flat[N * K:] == 7).all() and (rows[M * K:] == 7).all()
+    da.device_status()
+
+
 @pytest.mark.parametrize("M", [3, 60, 128, 300])
 def test_a_rows_nan_stays_in_its_row(M):
     rnd = _rnd(M)
@@ -381,3 +418,33 @@ def test_a_training_step_in_a_graph_beside_an_eager_one():
     for o, r, q in zip(outs, ref, again):
         assert torch.equal(o, r) and torch.equal(q, r)
     da.device_status()
+
+
+# ----------------------------------------------------------------------------- sizes and devices that are refused
+def test_sizes_past_31_bits_are_refused():
+    """Expanded views: nothing of this size is allocated."""
+    big = 2**32 + 8
+    x, w = torch.empty(1, 8, device="cuda", dtype=BF), torch.empty(16, 8, device="cuda", dtype=BF)
+    tall = x.expand(big, 8)
+    for f in (lambda: da.linear(tall, w), lambda: da.linear(x, w[:1].expand(big, 8)), lambda: da.gated_linear(tall, w),
+              lambda: da.linear(x[:, :1].expand(1, big), w[:, :1].expand(16, big)),
+              lambda: da.linear_backward(tall, w, x), lambda: da.gated_linear_backward(tall, w, w, x),
+              lambda: da.residual_norm(tall), lambda: da.residual_norm(x[:, :1].expand(1, big)),
+              lambda: da.residual_norm_backward(tall, tall, tall), lambda: da.linear(tall.view(big // 8, 8, 8), w)):
+        with pytest.raises(ValueError, match=r"sizes are below 2\^31"):
+            f()
+
+
+def test_another_device_than_the_current_one_is_refused(monkeypatch):
+    x, w = torch.zeros(4, 8, device="cuda", dtype=BF), torch.zeros(16, 8, device="cuda", dtype=BF)
+    stream = torch.cuda.current_stream()
+    other = type("Stream", (), {"device_index": x.get_device() + 1, "cuda_stream": 0})()
+    with pytest.raises(ValueError, match="the stream is on device"):
+        da.linear(x, w, out=torch.empty(4, 16, device="cuda", dtype=BF), stream=other)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: x.get_device() + 1)
+    for s in (None, stream):
+        for f in (lambda: da.linear(x, w, stream=s), lambda: da.gated_linear(x, w, stream=s), lambda: da.residual_norm(x, stream=s),
+                  lambda: da.linear_backward(x, w, x.new_zeros(4, 16), stream=s), lambda: da.residual_norm_backward(x, x, x, stream=s),
+                  lambda: da.gated_linear_backward(x, w, x.new_zeros(4, 16), x, stream=s)):
+            with pytest.raises(ValueError, match="the current device is"):
+                f()
