@@ -67,6 +67,13 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// One lane of a warp that is whole here (the same one each time).  Roles run by a whole warp with one lane issuing keep
+// their addresses in uniform registers, where TMA and MMA want them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e)::"memory");
+  return e != 0;
+}
 // A load into this CTA's shared memory whose bytes count on the barrier at
 // cluster address `bar` (its own or the pair's other CTA's).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
@@ -96,33 +103,20 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) 
   else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives on `bar` (with CG = 2: in both CTAs of the pair) when the MMAs issued so far have completed.
-template <int CG>
-__device__ __forceinline__ void tc_commit_cg(uint64_t* bar) {
-  if (CG == 1)
-    tc_commit_elect(bar);
-  else
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\tmov.b16 m, 3;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void mma_cg(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  if (CG == 1) {
-    mma_ss_elect(d_tmem, a_desc, b_desc, idesc, accumulate);
-    return;
-  }
+// Of a pair, from one lane: `commit` arrives on `bar` in both CTAs when the MMAs that the lane issued have completed.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   if (!DA_MMA_OK(d_tmem, idesc)) return;
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -394,6 +388,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
   __syncthreads();
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
+  LinTile x = linear_tile<EPI>(p, cid);
+  if (warp == C::EPI_WARPS && elect_one()) {
+    tma_prefetch_desc(&p.tm_a);
+    tma_prefetch_desc(&p.tm_b);
+  }
   grid_dep_wait();
   grid_dep_launch_dependents();  // (every CTA at work has its TMEM by now)
   const uint32_t tmem = *tmem_slot;
@@ -401,35 +400,33 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
 
   if (warp == C::EPI_WARPS) {
     // ================================================================ producer
-    if (lane == 0) {
-      tma_prefetch_desc(&p.tm_a);
-      tma_prefetch_desc(&p.tm_b);
-      long long fill = 0;
-      bool ok = true;
-      for (int t = cid; ok && t < steps; t += ncl) {
-        const LinTile x = linear_tile<EPI>(p, t);
-        if (x.n0 >= p.N) continue;
-        const int m0 = (x.mb * CG + static_cast<int>(rank)) * C::BM;
-        const int part = x.cols / CG;  // rows of B that this CTA loads: gate columns and, N rows further, up columns if gated
-        const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(part) * 128u;
-        for (int kb = 0; kb < kblocks; ++kb, ++fill) {
-          const int s = static_cast<int>(fill % C::STAGES);
-          const long long use = fill / C::STAGES;
-          if (use > 0 && !mbar_wait(&empty[s], static_cast<uint32_t>(use - 1) & 1u, ab)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = smem + s * C::STAGE_BYTES;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CG * bytes);
-          const uint32_t bar = CG == 2 ? map_to_rank(&full[s], 0) : 0;
+    // (Loops of one lane alone, its ring slots divided out of a 64-bit count, took 470 to 600 cycles a K block, more than
+    // the MMAs of a half tile or of a single SM: 300 x 2048 x 8192 41.9 us on single SMs, 33 so.)
+    int slot = 0;
+    uint32_t phase = 1;  // of `empty`; a slot's first use waits for nothing
+    long long fill = 0;
+    bool ok = true;
+    for (int t = cid; ok && t < steps; t += ncl, x = linear_tile<EPI>(p, t)) {
+      if (x.n0 >= p.N) continue;
+      const int m0 = (x.mb * CG + static_cast<int>(rank)) * C::BM;
+      const int part = x.cols / CG;  // rows of B that this CTA loads: gate columns and, N rows further, up columns if gated
+      const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(part) * 128u;
+      for (int kb = 0; kb < kblocks; ++kb, ++fill) {
+        if (fill >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, ab))) {
+          ok = false;
+          break;
+        }
+        uint8_t* dst = smem + slot * C::STAGE_BYTES;
+        const uint32_t bar = CG == 2 ? map_to_rank(&full[slot], 0) : 0;
+        const int k0 = kb * C::BK;
+        if (elect_one() && DA_BOUNDS(k0 < p.K)) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], CG * bytes);
           auto load = [&](uint8_t* to, const CUtensorMap* map, int c0, int c1) {
             if (CG == 2)
               tma_load_2d_pair(to, map, bar, c0, c1);
             else
-              tma_load_2d(to, map, &full[s], c0, c1);
+              tma_load_2d(to, map, &full[slot], c0, c1);
           };
-          const int k0 = kb * C::BK;
-          if (!DA_BOUNDS(k0 < p.K)) continue;
           // A box that starts past its tensor is filled with zeros, as one that ends past it.
           if (A_MN) {
             load(dst, &p.tm_a, m0, k0);
@@ -449,7 +446,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
               load(dst + C::A_BYTES + h * 8192, &p.tm_b, k0, nr);
           }
         }
+        __syncwarp();
+        if (++slot == C::STAGES) slot = 0, phase ^= 1u;
       }
+    }
+    if (lane == 0) {
       // The commits of the last slots have arrived in this CTA (they come from the pair's first CTA).
       for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); ok && f < fill; ++f)
         ok = mbar_wait(&empty[f % C::STAGES], static_cast<uint32_t>(f / C::STAGES) & 1u, ab);
@@ -473,42 +474,60 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
         tc_fence_after();
         return r;
       };
-      long long fill = 0;
+      int s = 0;
+      uint32_t phase = 0;
       long long i = 0;  // accumulators of this cluster so far
       bool ok = true;
-      for (int t = cid; ok && t < steps; t += ncl) {
-        const LinTile x = linear_tile<EPI>(p, t);
-        if (x.n0 >= p.N) continue;
+      for (int t = cid; ok && t < steps; t += ncl, x = linear_tile<EPI>(p, t)) {
+          if (x.n0 >= p.N) continue;
         const uint32_t idesc = x.cols == C::BN ? C::IDESC : C::IDESC_HALF;
-        for (int kb = 0; ok && kb < kblocks; ++kb, ++fill) {
+        for (int kb = 0, j = 0; ok && kb < kblocks; ++kb) {  // j: K blocks in the accumulator
           const int a = static_cast<int>(i & 1);
-          const bool first = kb % seg == 0;
+          const bool first = j == 0;
           // The epilogue of accumulator i - 2 has read these columns.
           if (first && i >= 2 && !waitp(&acc_empty[a], static_cast<uint32_t>((i >> 1) - 1) & 1u)) {
             ok = false;
             break;
           }
-          const int s = static_cast<int>(fill % C::STAGES);
-          if (!waitp(&full[s], static_cast<uint32_t>(fill / C::STAGES) & 1u)) {
+          if (!waitp(&full[s], phase)) {
             ok = false;
             break;
           }
           const uint64_t so = static_cast<uint64_t>((s * C::STAGE_BYTES) >> 4);
           const uint32_t dacc = tmem + static_cast<uint32_t>(a * C::BN);
+          const bool last = ++j == seg || kb == kblocks - 1;
+          auto a_at = [&](int k) { return dA + so + static_cast<uint64_t>((k * KA) >> 4); };
+          auto b_at = [&](int k) { return dB + so + static_cast<uint64_t>((k * KB) >> 4); };
+          // (One lane for a whole block, or one elected for each instruction: half tiles of pairs 30.5 and 33.5 us, single
+          // SMs 38.5 and 32.9, 300 x 2048 x 8192.)
+          if (CG == 2) {
+            if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < C::BK / 16; ++k)
-            mma_cg<CG>(dacc, dA + so + static_cast<uint64_t>((k * KA) >> 4), dB + so + static_cast<uint64_t>((k * KB) >> 4),
-                       idesc, (!first || k > 0) ? 1u : 0u);
-          tc_commit_cg<CG>(&empty[s]);
-          if (kb % seg == seg - 1 || kb == kblocks - 1) {
-            tc_commit_cg<CG>(&acc_full[a]);
+              for (int k = 0; k < C::BK / 16; ++k) mma_pair(dacc, a_at(k), b_at(k), idesc, (!first || k > 0) ? 1u : 0u);
+              tc_commit_pair(&empty[s]);
+              if (last) tc_commit_pair(&acc_full[a]);
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int k = 0; k < C::BK / 16; ++k) mma_ss_elect(dacc, a_at(k), b_at(k), idesc, (!first || k > 0) ? 1u : 0u);
+            tc_commit_elect(&empty[s]);
+            if (last) tc_commit_elect(&acc_full[a]);
+          }
+          if (++s == C::STAGES) s = 0, phase ^= 1u;
+          if (last) {
             ++i;
+            j = 0;
           }
         }
       }
       if (__any_sync(0xffffffffu, *ab.flag)) {
         // Aborted: the MMAs already issued complete before TMEM is freed.
-        tc_commit_cg<CG>(mma_done);
+        if (CG == 1)
+          tc_commit_elect(mma_done);
+        else if (elect_one())
+          tc_commit_pair(mma_done);
+        __syncwarp();
         mbar_wait_drain(mma_done, 0, kWaitBudgetCycles);
       }
     }
@@ -537,8 +556,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
     };
     long long i = 0;
     bool ok = true;
-    for (int t = cid; ok && t < steps; t += ncl) {
-      const LinTile x = linear_tile<EPI>(p, t);
+    for (int t = cid; ok && t < steps; t += ncl, x = linear_tile<EPI>(p, t)) {
       if (x.n0 >= p.N) continue;
       const int r0 = (x.mb * CG + static_cast<int>(rank)) * C::BM + wq * 32;
       const int rows = min(32, p.M - r0);  // (<= 0: none)
@@ -612,7 +630,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
         ++i;
       }
     }
-    if (lane == 0) bulk_wait_all();  // (the staging buffer lives until its stores are done, aborted or not)
+    if (lane == 0) bulk_wait_read_all();  // (the staging buffer lives until its stores have read it, aborted or not)
     __syncwarp();
   }
 
