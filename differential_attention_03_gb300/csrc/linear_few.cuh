@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   constexpr int SIDES = EPI == kEpiGated ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform to the compiler too)
 
   // ---- shared memory: ring of [weights | tokens], partial sums, barriers
   const int wrows = p.width * SIDES;
@@ -77,20 +77,22 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     const int k0 = (rank + fill * cs) * kLinBK;
     uint8_t* dst = smem + slot * stage_bytes;
     uint64_t* bar = &full[slot];
-    mbar_arrive_expect_tx(bar, stage_bytes);
     ++fill;
     if (++slot == stages) {
       slot = 0;
       phase ^= 1u;
     }
-    if (!DA_BOUNDS(k0 < p.K && f0 < p.N && t0 < p.M)) return;
-    if (W_MN) {
-      for (int j = 0; j < wrows; j += 64) tma_load_2d(dst + j * 128, &p.tm_a, bar, f0 + j, k0);
-    } else {
-      tma_load_2d(dst, &p.tm_a, bar, k0, f0);
-      if (EPI == kEpiGated) tma_load_2d(dst + p.width * 128, &p.tm_a, bar, k0, p.N + f0);
+    if (elect_one() && DA_BOUNDS(k0 < p.K && f0 < p.N && t0 < p.M)) {
+      mbar_arrive_expect_tx(bar, stage_bytes);
+      if (W_MN) {
+        for (int j = 0; j < wrows; j += 64) tma_load_2d(dst + j * 128, &p.tm_a, bar, f0 + j, k0);
+      } else {
+        tma_load_2d(dst, &p.tm_a, bar, k0, f0);
+        if (EPI == kEpiGated) tma_load_2d(dst + p.width * 128, &p.tm_a, bar, k0, p.N + f0);
+      }
+      tma_load_2d(dst + w_bytes, &p.tm_b, bar, k0, t0);
     }
-    tma_load_2d(dst + w_bytes, &p.tm_b, bar, k0, t0);
+    __syncwarp();
   };
   if (warp == kFewEpiWarps) {
     if (lane == 0) {
@@ -101,11 +103,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
       mbar_init(done, 1);
       *abort_flag = 0;
       fence_mbar_init();
-      grid_dep_wait();
-      const int first = min(nkb, stages);
-      while (fill < first) load();
     }
     __syncwarp();
+    grid_dep_wait();
+    const int first = min(nkb, stages);
+    while (fill < first) load();
   } else if (warp == kFewEpiWarps + 1) {
     tmem_alloc(tmem_slot, tmem_cols);
     tmem_relinquish();
@@ -119,11 +121,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
 
   if (warp == kFewEpiWarps) {
     // ================================================================ producer
+    while (fill < nkb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, ab))) break;
+      load();
+    }
     if (lane == 0) {
-      while (fill < nkb) {
-        if (!mbar_wait(&empty[slot], phase ^ 1u, ab)) break;
-        load();
-      }
       if (*ab.flag)  // aborted: the copies already issued land before the CTA exits
         for (int f = max(0, fill - stages); f < fill; ++f)
           mbar_wait_drain(&full[f % stages], static_cast<uint32_t>(f / stages) & 1u, kWaitBudgetCycles);
@@ -136,9 +138,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     constexpr int KW = W_MN ? 2048 : 32;
     const uint32_t idesc = idesc_bf16(128, 0, false, W_MN) | (static_cast<uint32_t>(wrows >> 3) << 17);
     int s = 0, in_seg = 0;
+    bool landed = false;
     uint32_t ph = 0, dacc = tmem;
     for (int kb = 0; kb < nkb; ++kb) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, ab))) break;
+      if (!__all_sync(0xffffffffu, landed) && !__all_sync(0xffffffffu, mbar_wait(&full[s], ph, ab))) break;
+      const int next = s + 1 == stages ? 0 : s + 1;
+      landed = mbar_test(&full[next], next ? ph : ph ^ 1u);  // (known by the time that these MMAs are issued)
       tc_fence_after();
       const uint64_t so = static_cast<uint64_t>((s * stage_bytes) >> 4);
 #pragma unroll
@@ -146,10 +151,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         mma_ss_elect(dacc, dX + so + static_cast<uint64_t>((k * 32) >> 4), dW + so + static_cast<uint64_t>((k * KW) >> 4), idesc,
                      (in_seg > 0 || k > 0) ? 1u : 0u);
       tc_commit_elect(&empty[s]);
-      if (++s == stages) {
-        s = 0;
-        ph ^= 1u;
-      }
+      s = next;
+      if (s == 0) ph ^= 1u;
       if (++in_seg == seg) {
         in_seg = 0;
         dacc += static_cast<uint32_t>(wrows);
