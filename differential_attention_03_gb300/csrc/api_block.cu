@@ -163,16 +163,40 @@ long long full_tiles(long long tiles, long long clusters) {
   return 2 * rest <= clusters ? tiles - rest : tiles;
 }
 
-// Rounds of tiles over the SMs.  A half tile takes 0.75 of a tile: what an SM draws from L2 (some 115 KB a us) bounds
-// both, and it draws the same rows of A.
-double tile_rounds(const Product& q, const da::LinearParams& p, int sms, int cg) {
-  const long long tiles = tile_count(q, p, cg), clusters = sms / cg, full = full_tiles(tiles, clusters);
-  return static_cast<double>((full + clusters - 1) / clusters) + (full < tiles ? 0.75 : 0.0);
-}
+// How linear_kernel's tiles are laid out: SM pairs or single SMs, tiles before the ones that come in halves, and an
+// estimate of the time.
+struct TilePlan {
+  int cg;
+  long long full;
+  double cost;
+};
 
-// SM pairs, unless single SMs take clearly less (few row blocks, or a last round that pairs leave emptier).
-int best_pair(const Product& q, const da::LinearParams& p, int sms) {
-  return tile_rounds(q, p, sms, 2) * 0.9 <= tile_rounds(q, p, sms, 1) ? 2 : 1;
+// Estimates in us, fitted to whole and half tiles on pairs and single SMs over 64 products from 160 x 1024 x 512 to
+// 1000 x 2048 x 8192 and 16384 x 512 x 512 with inputs beyond L2 on a GB300 (the choice takes 0.7 % more than the best of
+// the four on average, 11 % at worst): a K block takes so long, or what the CTAs of its round draw from L2 at 16.8 MB a
+// us; a tile at least its epilogue; beside them what a call costs.  (Pairs throughout, halves in the last round alone:
+// 777 x 1024 x 1024 8.9 us, 2048 x 1024 x 1024 9.0, 4096 x 256 x 256 5.6; single SMs' halves 5.7, 5.9 and 3.4.)
+TilePlan make_tile_plan(const Product& q, const da::LinearParams& p, int sms) {
+  static const double block[2][2] = {{0.323, 0.269}, {0.263, 0.178}}, call[2][2] = {{3.4, 2.8}, {5.4, 4.2}};
+  static const double least[2] = {1.7, 1.2};  // [whole, half]
+  const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
+  TilePlan best = {};
+  for (int cg = 1; cg <= 2; ++cg) {
+    const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
+    auto rounds = [&](long long n, int half) {
+      const double bytes = (da::kLinBM + da::kLinBN / cg / (half ? 2 : 1)) * da::kLinBK * 2.0;
+      auto round = [&](long long at_work) {
+        return std::max(kblocks * std::max(block[cg - 1][half], bytes * at_work * cg / 16.8e6), least[half]);
+      };
+      return n / clusters * round(clusters) + (n % clusters ? round(n % clusters) : 0.0);
+    };
+    for (int half = 0; half <= 1; ++half) {
+      const long long full = half ? 0 : full_tiles(tiles, clusters);
+      const double cost = call[cg - 1][half] + rounds(full, 0) + rounds(2 * (tiles - full), 1);
+      if (best.cg == 0 || cost < best.cost) best = TilePlan{cg, full, cost};
+    }
+  }
+  return best;
 }
 
 // Clusters of cs CTAs of linear_few_kernel, one CTA an SM, that run at once: clusters of 4 and 8 do not fill every SM.
@@ -199,12 +223,12 @@ struct FewPlan {
   long long tiles;
 };
 
-// Estimates in us, above what every product costs, fitted to a sweep of widths and clusters over fourteen shapes from
-// 1 x 1024 x 1024 to 777 x 1024 x 1024 and 16 x 8192 x 8192 on a GB300 (the choice is within 5 % of the best width and
-// cluster on average, 20 % at worst): HBM 5.1 MB a us together with an SM's own stream (230 KB a us, at least 0.064 us
-// a K block; several token tiles, which L2 feeds, 115 KB a us), what a cluster's CTAs hand each other (40 KB a us),
-// and the epilogue.  linear_kernel: 0.28 us a K block and round, 2.6 us more.
-FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms) {
+// Estimates in us, fitted to a sweep of widths and clusters over 54 products from 1 x 1024 x 1024 to 2048 x 1024 x 1024
+// and 16 x 8192 x 8192, weights beyond L2, on a GB300 (the choice takes 0.6 % more than the best width and cluster on
+// average, 7 % at worst; between it and linear_kernel's tiles 1.4 % and 13 %): HBM 6.1 MB a us together with an SM's own
+// stream (167 KB a us, dgrad's boxes 143; at least 0.105 us a K block; all together 32 MB a us), what a cluster's CTAs
+// hand each other (12.7 KB a us), the epilogue, and what a call costs.
+FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms, double least) {
   FewPlan best = {};
   if (q.kind == Kind::kWgrad) return best;
   const int sides = q.kind == Kind::kGated ? 2 : 1;
@@ -212,8 +236,7 @@ FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms) {
   const long long ttiles = (p.M + nt - 1ll) / nt;
   const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
   const int step = q.kind == Kind::kDgrad ? 64 : sides == 2 ? 8 : 16, most = 256 / sides;
-  const double hbm = 2.0 * sides * p.N * p.K / 5.1e6, draw = ttiles > 1 ? 115e3 : 230e3;
-  double least = p.M > 128 ? tile_rounds(q, p, sms, best_pair(q, p, sms)) * kblocks * 0.28 + 2.6 : 1e30;
+  const double hbm = 2.0 * sides * p.N * p.K / 6.1e6, draw = q.kind == Kind::kDgrad ? 143e3 : 167e3;
   if (ttiles * p.N > 0x7fffffffll) return best;
   for (int cs = 1; cs <= 8 && cs <= kblocks; cs *= 2) {
     const int at_once = cluster_slots(cs, sms);
@@ -222,9 +245,9 @@ FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms) {
       const int wrows = width * sides, lg = (width / 8 + cs - 1) / cs;
       const long long tiles = ttiles * ((p.N + width - 1) / width);
       const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
-      const double stream = rounds * nkb * std::max((wrows + nt) * 128.0 / draw, 0.064);
-      const double end = (cs > 1 ? 0.2 + nt * wrows * (4.0 / 40e3) * (cs - 1) / cs : 0.0) + std::min(p.M, nt) * lg * sides * 0.001 + wrows * 0.005;
-      const double cost = std::sqrt(stream * stream + hbm * hbm) + rounds * end;
+      const double stream = rounds * nkb * std::max({(wrows + nt) * 128.0 / draw, (wrows + nt) * 128.0 * std::min<long long>(tiles, at_once) * cs / 32e6, 0.105});
+      const double end = (cs > 1 ? 0.28 + nt * wrows * (4.0 / 12.7e3) * (cs - 1) / cs : 0.0) + std::min(p.M, nt) * lg * sides * 0.001 + wrows * 0.0031;
+      const double cost = 1.8 + std::sqrt(stream * stream + hbm * hbm) + rounds * end + (rounds - 1) * 0.4;
       if (cost >= least) continue;
       // ring, partial sums (and, behind the last slot's token rows, what an MMA of 128 rows reads), barriers
       const int stage = (wrows + nt) * 128, part = std::max(cs * nt * (lg * sides * 8 + 4) * 4, (128 - nt) * 128);
@@ -240,11 +263,16 @@ FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms) {
   return best;
 }
 
+struct Plan {
+  FewPlan few;
+  TilePlan tile;
+};
+
 // The plans of the sizes that this thread asked for last.
-FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
+Plan product_plan(const Product& q, const da::LinearParams& p, int sms) {
   struct Known {
     int kind, M, N, K, sms;
-    FewPlan plan;
+    Plan plan;
   };
   constexpr unsigned kEntries = 64;
   static thread_local Known known[kEntries];  // (sms = 0: none yet)
@@ -252,8 +280,10 @@ FewPlan few_plan(const Product& q, const da::LinearParams& p, int sms) {
   const unsigned h = static_cast<unsigned>(p.M) * 2654435761u ^ static_cast<unsigned>(p.N) * 40503u ^ static_cast<unsigned>(p.K) * 9973u ^
                      static_cast<unsigned>(kind) * 131u;
   Known& k = known[(h >> 7) % kEntries];
-  if (k.sms != sms || k.kind != kind || k.M != p.M || k.N != p.N || k.K != p.K)
-    k = Known{kind, p.M, p.N, p.K, sms, make_few_plan(q, p, sms)};
+  if (k.sms != sms || k.kind != kind || k.M != p.M || k.N != p.N || k.K != p.K) {
+    const TilePlan t = make_tile_plan(q, p, sms);
+    k = Known{kind, p.M, p.N, p.K, sms, {make_few_plan(q, p, sms, p.M > 128 ? t.cost : 1e30), t}};
+  }
   return k.plan;
 }
 
@@ -274,7 +304,8 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
     return x_mn ? map_rows(m, q.x, p.K, p.M, q.ldx, 64) : map_rows(m, q.x, p.M, p.K, q.ldx, box);
   };
   cudaError_t e;
-  const FewPlan f = few_plan(q, p, sms);
+  const Plan plan = product_plan(q, p, sms);
+  const FewPlan& f = plan.few;
   if (f.nt) {
     p.nt = f.nt, p.width = f.width, p.cs = f.cs, p.lg = f.lg, p.stages = f.stages, p.off_bars = f.off_bars;
     p.tiles_n = (p.N + f.width - 1) / f.width;
@@ -285,13 +316,13 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
   } else {
     const int bn = q.kind == Kind::kGated ? da::kLinBN / 2 : da::kLinBN;
     p.tiles_n = (p.N + bn - 1) / bn;
-    const int cg = best_pair(q, p, sms);
+    const int cg = plan.tile.cg;
     const int bm = da::kLinBM * cg;
     p.tiles_m = (p.M + bm - 1) / bm;
     p.group_m = kGroupRows / bm;
     const long long tiles = tile_count(q, p, cg), clusters = sms / cg;
     if (2 * tiles > 0x7fffffffll - sms) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
-    p.full = static_cast<int>(full_tiles(tiles, clusters));
+    p.full = static_cast<int>(plan.tile.full);
     if ((st = map_x(&p.tm_a, 128)) != DIFFATTN_OK) return st;
     if ((st = map_w(&p.tm_b, 64)) != DIFFATTN_OK) return st;
     if ((st = map_out(&p.tm_out, p.out, p.M, 1, p.N, p.ldo, q.epi == da::kEpiF32)) != DIFFATTN_OK) return st;
