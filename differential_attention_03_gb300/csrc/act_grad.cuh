@@ -5,7 +5,8 @@
 //   dbias[j] = sum over the rows of dz, in fp32 before dz is rounded
 //
 // dz (and [dg | du]) leave in bf16, the operand type of the products that
-// follow.  HBM-bound: 6 bytes a value of z (gated 10).  A warp owns 256
+// follow.  HBM-bound: 6 bytes a value of z (gated 10); 8192 x 8192, gelu, with
+// dbias 67 us (6.0 TB/s), 8192 x 2 x 5464 97 (4.6; what lies in L2 aside).  A warp owns 256
 // neighbouring columns (16 bytes a lane and tensor) and every eighth row of
 // its CTA's chunk; the column sums stay in registers, are joined over the CTA's
 // warps in shared memory and over the chunks by sum_parts_kernel, both in a

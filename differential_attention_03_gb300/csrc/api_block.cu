@@ -597,12 +597,13 @@ namespace {
 
 // How a row of D elements is laid over threads.  Rows of 16-byte multiples: vectors of 8 elements, a power of two of
 // lanes up to 256 elements, above a CTA a row with one or two vectors a thread: forward two above 512 elements;
-// backward one (of two rows at once) up to 4096, as 512 threads are the most.  Other rows: as many elements a thread, in
-// pairs where the width is even.
+// backward one (of two rows at once) up to 4096, as 512 threads are the most.  Other rows: eight elements a thread up to
+// 4096, sixteen above, in pairs where the width is even (sixteen forward too: 16760 x 1001 150 us, with eight and twice
+// the warps 103).
 da::NormShape norm_shape(int D, bool grad) {
   da::NormShape h;
   h.vec = D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1;
-  const int per = D > (grad ? 4096 : 512) ? 16 : 8;  // elements a thread
+  const int per = D > (grad || h.vec < 8 ? 4096 : 512) ? 16 : 8;  // elements a thread
   h.nv = per / h.vec;
   h.lanes = 32;
   if (D <= 256) {
@@ -717,10 +718,12 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
   const da::NormShape h = norm_shape(D, false);
   const int workers = norm_workers(h);
   p.lanes = h.lanes;
-  // As many CTAs as an SM holds at once (64 registers a thread; a CTA a row 112); each walks its rows.
+  // As many CTAs as an SM holds at once, by its registers, which warps take in fours; each walks its rows.  (A CTA more
+  // than fit and it runs alone behind the others: 16777 x 1000 37 us, not 25.)
+  const int fit = h.layout != da::kRing ? 1024 : h.nv == 1 ? 640 : 512;  // threads: at 64, 96 and 116 registers
   int smem;
   const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)), 0,
-                               std::max(1, std::min(16, (norm_row_cta(h) ? 576 : 1024) / h.threads)), &p.stages, &smem);
+                               std::max(1, std::min(16, fit / h.threads)), &p.stages, &smem);
   const int grid = static_cast<int>(std::min<long long>((rows + workers - 1ll) / workers, static_cast<long long>(sms_or_default()) * per_sm));
   const cudaError_t e = launch_norm(p, h, dt, stream_dt, false, grid, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);

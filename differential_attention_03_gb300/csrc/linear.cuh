@@ -10,18 +10,24 @@
 // ever stored.  bf16 operands, fp32 accumulation.
 //
 // Bound: the tensor cores (2 M N K flops; a 256-wide tile reads 1/128 byte of
-// L2 a flop), or for short contractions the epilogue's stores.
+// L2 a flop), or for short contractions the epilogue's stores.  8002 x 8192 x
+// 2048: 139 to 142 us, 1.9 PFLOP/s; 510 to 520 cycles a K block, 512 of them MMAs.
+// 8192 x 8192 x 64: 24 us, 5.6 TB/s of stores.
 //
 // One cluster of CG CTAs (an SM pair with CG = 2) per 128 CG x 256 tile,
 // persistent over the tiles in groups of `group_m` row blocks, so that the
-// CTAs at work share operands in L2; a last round that would leave half of the
-// clusters without work takes 128 CG x 128 tiles instead.  With CG = 2 an MMA is M256 N256 K16
-// over both SMs' tensor cores: each CTA holds its 128 rows of A and half of B,
-// so a CTA's shared memory feeds half as many B bytes.
+// CTAs at work share operands in L2.  From tile p.full on tiles are halves, of
+// 128 CG x 128: a last round that would leave half of the clusters without
+// work, or all of a small product (the host's choice, as is CG).  With CG = 2
+// an MMA is M256 N256 K16 over both SMs' tensor cores: each CTA holds its 128
+// rows of A and half of B, so a CTA's shared memory feeds half as many B bytes
+// (8002 x 4096 x 2 x 10928, gated: 945 us on single SMs, 885 on pairs, at the time).
 //   warps 0-7   (kEpiF32: 16 warps, 64 columns each) epilogue: warp w reads lanes 32 (w % 4) .. of the accumulator,
 //               columns 128 (w / 4) .. (gated: 64 gate columns and their 64 up
 //               columns).  32 rows of 128 bytes at a time leave through a
-//               4 KB staging buffer a warp (128-byte swizzle) by TMA.
+//               4 KB staging buffer a warp (128-byte swizzle) by TMA.  (16
+//               warps in bf16 too: 4096 x 4096 x 512 with gelu and stored z 26
+//               for 29 us, but 8192 x 1024 x 1024 18.4 for 15.3.)
 //   then        TMA producer: per K block of 64 the A and B boxes into a ring.
 //   last warp   TMEM allocator; MMA issuer (of the cluster's first CTA).
 // TMEM: two 256-column accumulators: the epilogue of one tile overlaps the
@@ -393,8 +399,9 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
 
   if (warp == C::EPI_WARPS) {
     // ================================================================ producer
-    // (Loops of one lane alone, its ring slots divided out of a 64-bit count, took 470 to 600 cycles a K block, more than
-    // the MMAs of a half tile or of a single SM: 300 x 2048 x 8192 41.9 us on single SMs, 33 so.)
+    // (The whole warp, one lane issuing: loops of one lane alone, ring slots divided out of a 64-bit count and a warp
+    // index that the compiler took for divergent cost 470 to 600 cycles a K block, whatever its size; half tiles of
+    // 300 x 2048 x 8192 took 41.9 us on single SMs and 38.9 on pairs, now 23.9 and 21.8, 300 and 270 cycles.)
     int slot = 0;
     uint32_t phase = 1;  // of `empty`; a slot's first use waits for nothing
     long long fill = 0;
@@ -491,8 +498,8 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
           const bool last = ++j == seg || kb == kblocks - 1;
           auto a_at = [&](int k) { return dA + so + static_cast<uint64_t>((k * KA) >> 4); };
           auto b_at = [&](int k) { return dB + so + static_cast<uint64_t>((k * KB) >> 4); };
-          // (One lane for a whole block, or one elected for each instruction: half tiles of pairs 30.5 and 33.5 us, single
-          // SMs 38.5 and 32.9, 300 x 2048 x 8192.)
+          // (One lane for a whole block suits pairs, one elected for each instruction single SMs: half tiles of
+          // 300 x 2048 x 8192 30.5 us against 33.5, and 23.9 against 29.0.)
           if (CG == 2) {
             if (elect_one()) {
 #pragma unroll

@@ -25,6 +25,10 @@
 // all of them, so the sums over rows stay in registers; each CTA writes them
 // once (for a gate shared by a group of rows: once a group, or once a chunk of
 // a large group), and sum_parts_kernel joins the CTAs in a fixed order.
+// 8002 x 4096 on an fp32 stream, both norms, a gate a sequence: 65 us forward
+// (6.0 TB/s); 16384 x 2048 in bf16, a gate, both norms: 73 us backward (5.5 TB/s).
+// 16777 x 1000 in bf16, the same: 25 us (5.4 TB/s), 43 backward; of odd width,
+// 16760 x 1001: 103 and 197 us, bound by instructions on single elements.
 #pragma once
 
 #include "act.cuh"
@@ -260,7 +264,7 @@ __device__ __forceinline__ Row<VEC> scaled(Row<VEC> r, float k) {
 
 // NV vectors of VEC elements a thread; thread t of a row's nt holds vectors t, t + nt, ...
 template <typename TX, typename TS, int VEC, int NV, int LAYOUT>
-__global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 256, LAYOUT == kRing || LAYOUT == kPlain ? 1 : 4)
+__global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 256, LAYOUT == kRing ? 1 : LAYOUT == kPlain ? 2 : 4)
     residual_norm_kernel(const NormParams p) {
   using R = Row<VEC>;
   __shared__ __align__(16) float buf[256];
@@ -711,7 +715,7 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
 // residual_norm_grad_kernel's work for rows of 16-byte multiples up to 4096 with dy given, which is bound by
 // instructions (16384 x 2048 took 496 a warp and row, 104 us): two rows at once, whose four sums share one butterfly and
 // one barrier, and whose parameters stay in registers; no branch in a row depends on the thread (threads past the row
-// compute its first columns again and count for nothing).
+// compute its first columns again and count for nothing): 73 us.
 
 // Sums of four values over the warp: lane l gets that of value (l >> 3) & 3.
 __device__ __forceinline__ float warp_sum4(float a, float b, float c, float d) {
