@@ -157,7 +157,7 @@ __device__ __forceinline__ LinTile linear_tile(const LinearParams& p, int t) {
   const int per_group = p.group_m * p.tiles_n;
   const int g = tile / per_group;
   const int first = g * p.group_m;
-  const int gm = min(p.group_m, p.tiles_m - first);
+  const int gm = max(1, min(p.group_m, p.tiles_m - first));  // (a step past the last one is not used)
   const int r = tile - g * per_group;
   constexpr int BN = EPI == kEpiGated ? kLinBN / 2 : kLinBN;
   LinTile x;
