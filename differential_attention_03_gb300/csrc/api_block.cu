@@ -798,9 +798,14 @@ diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtyp
   const da::NormShape h = norm_shape(D, true);
   p.lanes = h.lanes;
   int smem;
-  norm_ring(h, D * ((dy ? xe + se : 0) + (ds ? se : 0) + (post || dgate ? xe : 0) + (row_gate ? 4 : 0)), 4ll * D,
-            norm_grad_per_sm(h), &p.stages, &smem);
-  // Behind the ring: sums for dgamma_post.  Rows of warps: two such arrays a worker (those sums, and room to join them).
+  const long long slot = D * ((dy ? xe + se : 0) + (ds ? se : 0) + (post || dgate ? xe : 0) + (row_gate ? 4 : 0));
+  // gamma_post times the gate in shared memory too, where that leaves two slots.
+  const bool combined = h.layout == da::kRing && h.nv == 2 && (gamma_post || (gate && !row_gate)) && 2 * slot + 8ll * D <= da::kNormMaxSmem - 1152;
+  norm_ring(h, slot, (combined ? 8ll : 4ll) * D, norm_grad_per_sm(h), &p.stages, &smem);
+  // Behind the ring: gamma_post times the gate, and sums for dgamma_post.  Rows of warps: two such arrays a worker (those
+  // sums, and room to join them).
+  p.off_combined = combined ? smem : -1;
+  if (combined) smem += 4 * D;
   if (!norm_row_cta(h)) smem = norm_workers(h) * D * 4;
   p.off_post = smem;
   smem += norm_workers(h) * D * 4;

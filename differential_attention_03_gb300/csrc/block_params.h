@@ -50,6 +50,7 @@ struct NormParams {
   int D;
   int lanes;   // lanes that share a row (kSubWarp, kPlainWarp)
   int stages;  // rows on their way (kRing)
+  int off_combined;  // where gamma_post times the gate lies in shared memory (backward, kRing of 16 elements a thread; -1: nowhere)
   int off_post;  // where the sums for dgamma_post lie in shared memory (backward): D floats, or D a worker of the CTA
   float scale, eps;
   int post, norm;  // whether x is normed, whether y is wanted or given

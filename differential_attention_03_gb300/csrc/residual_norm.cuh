@@ -468,13 +468,15 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
   grid_dep_launch_dependents();
   // kHold: a row's values and the parameters of a thread's columns stay in registers, every load of a row issued at its
   // start.  Rows of the ring (16 elements a thread here): only t is held across the reductions; s, dy and x are read from
-  // the slot again, the parameters from L1.
+  // the slot again, gamma from L1, and gamma_post with the group's gate from shared memory where it has room (all three
+  // from L1, which they overfill: 2730 x 6144 in bf16 100 us, 78 so; 4088 x 4104 on an fp32 stream 140 and 110).
   // dga: sums of dy n.  u: sums of t xh over a piece (with a gate a row: of t gate xh), of which gamma_post times is the
   // gate's gradient and the gate times gamma_post's; the latter's sums over pieces are in shared memory.
   constexpr bool kHold = LAYOUT != kRing;
   constexpr int NH = kHold ? NV : 1;
   R dga[NV], u[NV], kept_ga[NH], kept_c[NH];
   float* post_sums = reinterpret_cast<float*>(smem + p.off_post) + (RowTeam<LAYOUT>::kCta ? 0 : team.worker * p.D);
+  float* combined_row = reinterpret_cast<float*>(smem + p.off_combined);  // (a thread's own columns)
   auto column = [&](const float* from, int i) -> R {
     R w;
     w.fill(1.f);
@@ -508,9 +510,19 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if ((t + i * nt) * VEC < p.D) kept_c[kHold ? i : 0] = combined(i);
+    } else if (p.off_combined >= 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((t + i * nt) * VEC < p.D) combined(i).store(combined_row + (t + i * nt) * VEC);
     }
     auto gamma_of = [&](int i) -> R { return kHold ? kept_ga[kHold ? i : 0] : column(p.gamma, i); };
-    auto c_of = [&](int i) -> R { return kHold ? kept_c[kHold ? i : 0] : combined(i); };
+    auto c_of = [&](int i) -> R {
+      if (kHold) return kept_c[kHold ? i : 0];
+      if (p.off_combined < 0) return combined(i);
+      R w;
+      w.load(combined_row + (t + i * nt) * VEC);
+      return w;
+    };
     long long at = (row0 + team.worker) * p.D;
     for (long long head = row0; head < row1; head += team.workers, at += static_cast<long long>(team.workers) * p.D) {
       const long long row = head + team.worker;

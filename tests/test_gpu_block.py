@@ -286,7 +286,9 @@ def _check_norm(x, res, gate, gp, ga, scale, y, s):
     e = 2.0 ** -17 * (part + (0 if R is None else np.abs(R)))
     _within(s, rs, e + _half(s.dtype) * (np.abs(rs) + e) + 1e-37, "s")
     if y is not None:
-        f = np.abs(ry) / np.maximum(np.abs(rs), 1e-30)  # y per s
+        # y per s: y = s gamma / rms(s).  (Not |y| / |s|: where scale x cancels the residual exactly in 64 bits, as 0.7 * 10 - 7
+        # does, that is 0, but scale is a float, and 0.7f * 10 - 7 = -1.2e-7, within e.)
+        f = np.abs(1.0 if ga is None else _f64(ga)) / np.sqrt((rs * rs).mean(-1, keepdims=True) + 1e-5)
         ey = f * e + 2.0 ** -17 * np.abs(ry) + np.abs(ry) * np.sqrt((e * e).mean(-1, keepdims=True) / ((rs * rs).mean(-1, keepdims=True) + 1e-5))
         _within(y, ry, ey + _half(y.dtype) * (np.abs(ry) + ey) + 1e-37, "y")
 
@@ -352,6 +354,20 @@ def _check_norm_backward(x, s, dy, ds, gate, gp, ga, scale, got, post=None):
         G = gate.size // X.shape[1]
         e = (rows * 2.0 ** -24 + 3 * rel) * (scale * T * P).reshape(G, rows // G, -1).sum(1)
         _within(got["dgate"], ref["dgate"], e + 1e-37, "dgate")
+
+
+@pytest.mark.parametrize("rows,D,G", [(400, 4104, 4), (310, 5120, 155), (170, 6144, 1), (160, 8192, 80), (500, 4104, 500), (4000, 1000, 8),
+                                      (2700, 1152, 0), (2000, 1001, 2), (900, 2050, 0)])
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("post", [False, True])
+def test_norm_more_rows_than_workers(rows, D, G, types, post):
+    """Several rows a CTA, and of the backward pass several groups of rows."""
+    x, res, gate, gp, ga, dy, ds = _norm_inputs(rows, D, types, post, G, rows + 3 * D)
+    y, s = da.residual_norm(x, res, gate=gate, scale=0.7, gamma_post=gp, gamma=ga)
+    _check_norm(x, res, gate, gp, ga, 0.7, y, s)
+    got = da.residual_norm_backward(x, s, dy, ds, gate=gate, scale=0.7, gamma_post=gp, gamma=ga)
+    da.device_status()
+    _check_norm_backward(x, s, dy, ds, gate, gp, ga, 0.7, got)
 
 
 @pytest.mark.parametrize("D", [72, 300, 1000])
