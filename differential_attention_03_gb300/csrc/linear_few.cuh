@@ -170,6 +170,29 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   const int row_floats = lg * SIDES * 8 + 4;
   const int mt = min(p.nt, p.M - t0);
   const int wq = (warp & 3) * 32;  // first accumulator row of this warp
+  // ---- what this CTA finishes: items of eight features of a token, i / ng by its high product (i < 2^16); the bias and
+  // the residual of a thread's first item are on their way while the accumulators come
+  const int ng = max(0, min(lg, groups - rank * lg));  // groups of this CTA
+  const int items = mt * ng;
+  const uint32_t over = 0xffffffffu / static_cast<uint32_t>(max(1, ng)) + 1u;
+  auto token_of = [&](int i) { return ng == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), over)); };
+  float4 bias[2];
+  uint4 res[2];
+  auto fetch = [&](int i) {
+    const int t = token_of(i), col = f0 + (rank * lg + i - t * ng) * 8;
+    if (EPI == kEpiGated || i >= items || col >= p.N) return;
+    if (p.bias) {
+      bias[0] = __ldg(reinterpret_cast<const float4*>(p.bias + col));
+      bias[1] = __ldg(reinterpret_cast<const float4*>(p.bias + col) + 1);
+    }
+    if (p.residual) {
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) + ((t0 + t) * p.ldr + col) * (EPI == kEpiF32 ? 4 : 2));
+      res[0] = at[0];
+      if (EPI == kEpiF32) res[1] = at[1];
+    }
+  };
+  grid_dep_wait();
+  fetch(threadIdx.x);
   const bool go = warp < kFewEpiWarps && __all_sync(0xffffffffu, mbar_wait(done, 0, ab));
   if (cs > 1) cluster_wait();
   if (go && wq < mt) {
@@ -238,13 +261,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   } else {
     __syncthreads();
   }
-  grid_dep_wait();
 
   // ================================================================ sum over the cluster, epilogue: eight features an item
   {
-    const int ng = max(0, min(lg, groups - rank * lg));  // groups of this CTA
-    const int items = mt * ng;
-    const uint32_t over = 0xffffffffu / static_cast<uint32_t>(max(1, ng)) + 1u;  // i / ng by its high product (i < 2^16)
     auto sum8 = [&](int t, int g, int side, float (&v)[8]) {
       const float* at = part + t * row_floats + (g * SIDES + side) * 8;
 #pragma unroll
@@ -257,10 +276,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
       }
     };
     for (int i = threadIdx.x; i < items; i += kFewThreads) {
-      const int t = ng == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), over)), g = i - t * ng;
+      const int t = token_of(i), g = i - t * ng;
       const int col = f0 + (rank * lg + g) * 8;
       const long long row = t0 + t;
       if (col >= p.N || !DA_BOUNDS_V(row < p.M && col + 8 <= p.N, col)) continue;
+      if (i >= kFewThreads) fetch(i);
       float v[8];
       sum8(t, g, 0, v);
       if (EPI == kEpiGated) {
@@ -276,7 +296,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         });
       } else {
         if (p.bias) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(p.bias + col)), b = __ldg(reinterpret_cast<const float4*>(p.bias + col) + 1);
+          const float4 a = bias[0], b = bias[1];
           v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
           v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
         }
@@ -288,11 +308,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         if (p.residual) {
           float r[8];
           if (EPI == kEpiF32) {
-            const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + row * p.ldr + col);
-            const float4 a = at[0], b = at[1];
-            r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+            r[0] = __uint_as_float(res[0].x), r[1] = __uint_as_float(res[0].y), r[2] = __uint_as_float(res[0].z), r[3] = __uint_as_float(res[0].w);
+            r[4] = __uint_as_float(res[1].x), r[5] = __uint_as_float(res[1].y), r[6] = __uint_as_float(res[1].z), r[7] = __uint_as_float(res[1].w);
           } else {
-            unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.residual) + row * p.ldr + col), r);
+            unpack8(res[0], r);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += r[j];
