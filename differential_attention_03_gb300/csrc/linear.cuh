@@ -132,9 +132,12 @@ struct LinearCfg {
   static constexpr int B_BYTES = BN_CTA * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 48 KB, a pair's CTA 32 KB
   static constexpr int STAGES = (229376 - EPI_WARPS * 4096) / STAGE_BYTES;  // 4, a pair 6; kEpiF32: 3 and 5
+  // Where every tile is a half, its smaller slots: 6 and 8, kEpiF32 4 and 6.
+  static constexpr int HALF_BYTES = A_BYTES + B_BYTES / 2;
+  static constexpr int HALF_STAGES = STAGES * STAGE_BYTES / HALF_BYTES;
   static constexpr int OFF_STAGING = STAGES * STAGE_BYTES;
   static constexpr int OFF_BARS = OFF_STAGING + EPI_WARPS * 4096;
-  static constexpr int NBARS = 2 * STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], mma_done
+  static constexpr int NBARS = 2 * HALF_STAGES + 5;  // full, empty, acc_full[2], acc_empty[2], mma_done
   static constexpr int OFF_MISC = OFF_BARS + NBARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment slack
   static constexpr uint32_t TMEM_COLS = 512;
@@ -357,8 +360,8 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
   uint64_t* full = bars;                   // [STAGES] A and B of a K block landed (in both CTAs)
-  uint64_t* empty = full + C::STAGES;      // [STAGES] the MMAs reading the slot completed
-  uint64_t* acc_full = empty + C::STAGES;  // [2] every MMA of the accumulator completed
+  uint64_t* empty = full + C::HALF_STAGES;      // [STAGES] the MMAs reading the slot completed
+  uint64_t* acc_full = empty + C::HALF_STAGES;  // [2] every MMA of the accumulator completed
   uint64_t* acc_empty = acc_full + 2;      // [2] the epilogue (of both CTAs) has read the accumulator
   uint64_t* mma_done = acc_empty + 2;      // every MMA issued completed (abort drain)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -367,10 +370,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
   const int steps = p.full + 2 * (p.tiles_m * p.tiles_n - p.full);
   const int kblocks = (p.K + C::BK - 1) / C::BK;
   const int seg = EPI == kEpiF32 ? kLinSegBlocks : kblocks;  // K blocks an accumulator sums
+  const int stages = p.full > 0 ? C::STAGES : C::HALF_STAGES, stage_bytes = p.full > 0 ? C::STAGE_BYTES : C::HALF_BYTES;
   const int cid = static_cast<int>(blockIdx.x) / CG, ncl = static_cast<int>(gridDim.x) / CG;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -412,11 +416,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
       const int part = x.cols / CG;  // rows of B that this CTA loads: gate columns and, N rows further, up columns if gated
       const uint32_t bytes = C::A_BYTES + static_cast<uint32_t>(part) * 128u;
       for (int kb = 0; kb < kblocks; ++kb, ++fill) {
-        if (fill >= C::STAGES && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, ab))) {
+        if (fill >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase, ab))) {
           ok = false;
           break;
         }
-        uint8_t* dst = smem + slot * C::STAGE_BYTES;
+        uint8_t* dst = smem + slot * stage_bytes;
         const uint32_t bar = CG == 2 ? map_to_rank(&full[slot], 0) : 0;
         const int k0 = kb * C::BK;
         if (elect_one() && DA_BOUNDS(k0 < p.K)) {
@@ -447,17 +451,17 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
           }
         }
         __syncwarp();
-        if (++slot == C::STAGES) slot = 0, phase ^= 1u;
+        if (++slot == stages) slot = 0, phase ^= 1u;
       }
     }
     if (lane == 0) {
       // The commits of the last slots have arrived in this CTA (they come from the pair's first CTA).
-      for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); ok && f < fill; ++f)
-        ok = mbar_wait(&empty[f % C::STAGES], static_cast<uint32_t>(f / C::STAGES) & 1u, ab);
+      for (long long f = (fill > stages ? fill - stages : 0); ok && f < fill; ++f)
+        ok = mbar_wait(&empty[f % stages], static_cast<uint32_t>(f / stages) & 1u, ab);
       if (*ab.flag && rank == 0) {
         // Aborted: the copies already issued land before the CTA exits.
-        for (long long f = (fill > C::STAGES ? fill - C::STAGES : 0); f < fill; ++f)
-          mbar_wait_drain(&full[f % C::STAGES], static_cast<uint32_t>(f / C::STAGES) & 1u, kWaitBudgetCycles);
+        for (long long f = (fill > stages ? fill - stages : 0); f < fill; ++f)
+          mbar_wait_drain(&full[f % stages], static_cast<uint32_t>(f / stages) & 1u, kWaitBudgetCycles);
       }
     }
     __syncwarp();
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
             ok = false;
             break;
           }
-          const uint64_t so = static_cast<uint64_t>((s * C::STAGE_BYTES) >> 4);
+          const uint64_t so = static_cast<uint64_t>((s * stage_bytes) >> 4);
           const uint32_t dacc = tmem + static_cast<uint32_t>(a * C::BN);
           const bool last = ++j == seg || kb == kblocks - 1;
           auto a_at = [&](int k) { return dA + so + static_cast<uint64_t>((k * KA) >> 4); };
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
             tc_commit_elect(&empty[s]);
             if (last) tc_commit_elect(&acc_full[a]);
           }
-          if (++s == C::STAGES) s = 0, phase ^= 1u;
+          if (++s == stages) s = 0, phase ^= 1u;
           if (last) {
             ++i;
             j = 0;
