@@ -172,13 +172,13 @@ struct TilePlan {
 };
 
 // Estimates in us, fitted to whole and half tiles on pairs and single SMs over 64 products from 160 x 1024 x 512 to
-// 1000 x 2048 x 8192 and 16384 x 512 x 512 with inputs beyond L2 on a GB300 (the choice takes 0.7 % more than the best of
-// the four on average, 11 % at worst): a K block takes so long, or what the CTAs of its round draw from L2 at 16.8 MB a
+// 1000 x 2048 x 8192 and 16384 x 512 x 512 with inputs beyond L2 on a GB300 (the choice takes 0.3 % more than the best of
+// the four on average, 3 % at worst): a K block takes so long, or what the CTAs of its round draw from L2 at 20 MB a
 // us; a tile at least its epilogue; beside them what a call costs.  (Pairs throughout, halves in the last round alone:
-// 777 x 1024 x 1024 8.9 us, 2048 x 1024 x 1024 9.0, 4096 x 256 x 256 5.6; single SMs' halves 5.7, 5.9 and 3.4.)
+// 777 x 1024 x 1024 8.9 us, 2048 x 1024 x 1024 9.0, 4096 x 256 x 256 5.6; single SMs' halves 5.5, 5.7 and 3.4.)
 TilePlan make_tile_plan(const Product& q, const da::LinearParams& p, int sms) {
-  static const double block[2][2] = {{0.323, 0.269}, {0.263, 0.178}}, call[2][2] = {{3.4, 2.8}, {5.4, 4.2}};
-  static const double least[2] = {1.7, 1.2};  // [whole, half]
+  static const double block[2][2] = {{0.318, 0.191}, {0.261, 0.145}}, call[2][2] = {{3.7, 2.75}, {5.55, 4.8}};
+  static const double least[2] = {1.35, 0.57};  // [whole, half]
   const int kblocks = (p.K + da::kLinBK - 1) / da::kLinBK;
   TilePlan best = {};
   for (int cg = 1; cg <= 2; ++cg) {
@@ -186,7 +186,7 @@ TilePlan make_tile_plan(const Product& q, const da::LinearParams& p, int sms) {
     auto rounds = [&](long long n, int half) {
       const double bytes = (da::kLinBM + da::kLinBN / cg / (half ? 2 : 1)) * da::kLinBK * 2.0;
       auto round = [&](long long at_work) {
-        return std::max(kblocks * std::max(block[cg - 1][half], bytes * at_work * cg / 16.8e6), least[half]);
+        return std::max(kblocks * std::max(block[cg - 1][half], bytes * at_work * cg / 20e6), least[half]);
       };
       return n / clusters * round(clusters) + (n % clusters ? round(n % clusters) : 0.0);
     };
@@ -225,7 +225,7 @@ struct FewPlan {
 
 // Estimates in us, fitted to a sweep of widths and clusters over 54 products from 1 x 1024 x 1024 to 2048 x 1024 x 1024
 // and 16 x 8192 x 8192, weights beyond L2, on a GB300 (the choice takes 0.6 % more than the best width and cluster on
-// average, 7 % at worst; between it and linear_kernel's tiles 1.4 % and 13 %): HBM 6.1 MB a us together with an SM's own
+// average, 7 % at worst; between it and linear_kernel's tiles 0.7 % and 7 %): HBM 6.1 MB a us together with an SM's own
 // stream (167 KB a us, dgrad's boxes 143; at least 0.105 us a K block; all together 32 MB a us), what a cluster's CTAs
 // hand each other (12.7 KB a us), the epilogue, and what a call costs.
 FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms, double least) {

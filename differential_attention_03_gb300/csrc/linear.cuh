@@ -359,11 +359,11 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);
-  uint64_t* full = bars;                   // [STAGES] A and B of a K block landed (in both CTAs)
-  uint64_t* empty = full + C::HALF_STAGES;      // [STAGES] the MMAs reading the slot completed
+  uint64_t* full = bars;                        // [stages] A and B of a K block landed (in both CTAs)
+  uint64_t* empty = full + C::HALF_STAGES;      // [stages] the MMAs reading the slot completed
   uint64_t* acc_full = empty + C::HALF_STAGES;  // [2] every MMA of the accumulator completed
-  uint64_t* acc_empty = acc_full + 2;      // [2] the epilogue (of both CTAs) has read the accumulator
-  uint64_t* mma_done = acc_empty + 2;      // every MMA issued completed (abort drain)
+  uint64_t* acc_empty = acc_full + 2;           // [2] the epilogue (of both CTAs) has read the accumulator
+  uint64_t* mma_done = acc_empty + 2;           // every MMA issued completed (abort drain)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
 
