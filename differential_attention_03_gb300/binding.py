@@ -176,6 +176,8 @@ def lib() -> ctypes.CDLL:
             L.diffattn_debug_bounds_selftest.restype = i
             L.diffattn_debug_item_plan.argtypes = [i, ll, i, i, i, i, ll, vp, vp]
             L.diffattn_debug_item_plan.restype = i
+            L.diffattn_debug_product_plan.argtypes = [i, i, i, i, vp]
+            L.diffattn_debug_product_plan.restype = i
             L.diffattn_last_error.argtypes = []
             L.diffattn_last_error.restype = ctypes.c_char_p
             L.diffattn_debug_wait_timeout.argtypes = [ll, vp]
@@ -1681,6 +1683,24 @@ def debug_item_plan(grid: int, units: int, nqt: int, qt0: int, n: int, causal: b
     cnt = lib().diffattn_debug_item_plan(grid, units, nqt, qt0, n, 1 if causal else 0, kv_unit_bytes,
                                          first.ctypes.data_as(ctypes.c_void_p), items.ctypes.data_as(ctypes.c_void_p))
     return None if cnt == 0 else (first, items)
+
+
+PRODUCTS = {"linear": 0, "gated": 1, "da": 2, "dw": 3}
+
+
+def debug_product_plan(kind: str, M: int, N: int, K: int) -> dict:
+    """How a product [M, N] over a contraction of K would run (host only).
+
+    kind: "linear", "gated" (N = F, K = D), "da" (dx too) or "dw".  Returns a dict: kernel ("few" or "tiles") and
+    its layout; segment: the values of K that one accumulator of an fp32 output sums.
+    """
+    plan = (ctypes.c_int * 6)()
+    form = lib().diffattn_debug_product_plan(PRODUCTS[kind], M, N, K, plan)
+    if form == 1:
+        return dict(kernel="few", cluster=plan[0], width=plan[1], tokens=plan[2], stages=plan[4], segment=plan[5])
+    if form == 2:
+        return dict(kernel="tiles", cluster=plan[0], whole=plan[1], halved=plan[2], segment=plan[5])
+    raise ValueError(f"no product {kind} of {M} x {N} x {K}")
 
 
 def device_status(stream=None) -> int:

@@ -393,6 +393,24 @@ size_t dtype_bytes(int dt) { return dt == DIFFATTN_F32 ? 4 : 2; }
 
 extern "C" {
 
+int diffattn_debug_product_plan(int kind, int M, int N, int K, int* plan) {
+  if (kind < 0 || kind > 3 || M < 1 || N < 1 || K < 1 || !plan) return 0;
+  da::LinearParams p;
+  memset(&p, 0, sizeof(p));
+  p.M = M, p.N = N, p.K = K;
+  const Product q = {static_cast<Kind>(kind), da::kEpiBf16, nullptr, nullptr, 0, 0};
+  const Plan x = product_plan(q, p, sms_or_default());
+  const int cg = x.tile.cg;
+  if (x.few.nt) {
+    const int row[6] = {x.few.cs, x.few.width, x.few.nt, x.few.lg, x.few.stages, da::few_segment(K, x.few.cs, x.few.width * (q.kind == Kind::kGated ? 2 : 1)) * da::kLinBK};
+    memcpy(plan, row, sizeof(row));
+    return 1;
+  }
+  const int row[6] = {cg, static_cast<int>(x.tile.full), static_cast<int>(tile_count(q, p, cg) - x.tile.full), 0, 0, da::kLinSegBlocks * da::kLinBK};
+  memcpy(plan, row, sizeof(row));
+  return 2;
+}
+
 diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long lda, const void* w, const float* bias,
                                 diffattn_activation act, const void* residual, long long ldr, diffattn_dtype out_dt,
                                 void* out, long long ldo, void* pre, void* stream) {

@@ -66,8 +66,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   const int kblocks = (p.K + kLinBK - 1) / kLinBK;
   // K blocks rank, rank + cs, ...: what a cluster reads at one time lies together in the weights' rows.
   const int nkb = (kblocks - rank + cs - 1) / cs;  // >= 1
-  const int most = 256 / wrows;                    // accumulators that fit (two CTAs share an SM's 512 columns)
-  const int seg = EPI == kEpiF32 ? (nkb + most - 1) / most : nkb;  // K blocks an accumulator sums
+  const int seg = EPI == kEpiF32 ? few_segment_blocks(nkb, wrows) : nkb;  // K blocks an accumulator sums
   const int segs = (nkb + seg - 1) / seg;
   uint32_t tmem_cols = 32;
   while (tmem_cols < static_cast<uint32_t>(segs * wrows)) tmem_cols *= 2;

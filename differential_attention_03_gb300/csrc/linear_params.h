@@ -21,6 +21,16 @@ constexpr int kLinSegBlocks = 8;  // K blocks (512 values) that one accumulator 
 
 constexpr int kFewMaxSmem = 232448;
 
+// linear_few_kernel with fp32 outputs: K blocks that one accumulator of `wrows` columns sums, in the CTA of a cluster of cs
+// with the most of them.  A CTA has 256 columns of tensor memory (two CTAs share an SM's 512).
+__host__ __device__ inline int few_segment_blocks(int blocks, int wrows) {
+  const int most = 256 / wrows;
+  return (blocks + most - 1) / most;
+}
+inline int few_segment(int K, int cs, int wrows) {
+  return few_segment_blocks(((K + kLinBK - 1) / kLinBK + cs - 1) / cs, wrows);
+}
+
 struct LinearParams {
   CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
   CUtensorMap tm_b;  // over B ({K, N} or {N, K}), box {64, 64}; linear_few: the tokens, box {64, nt}

@@ -941,6 +941,19 @@ int diffattn_debug_item_plan(int grid, long long units, int nqt, int qt0, int n,
                              long long kv_unit_bytes, unsigned short* first, unsigned short* items);
 
 /*
+ * Host only (nothing launched): how a product out [M, N] over a contraction of K
+ * would run, for the tests.  kind 0: diffattn_linear (M, N, K), 1:
+ * diffattn_gated_linear (M, F, D), 2: da or dx of a backward pass (M, K, N; gated
+ * M, D, 2 F), 3: dw (N, K, M; gated 2 F, D, M).
+ * Returns 1 for the kernel for few tokens (plan: CTAs of a cluster, features of a
+ * tile, tokens of a tile, groups of eight features that a CTA finishes, ring
+ * slots, values of K in one accumulator of an fp32 output), 2 for the tiles
+ * (plan: SMs of a cluster, whole tiles, tiles that come in halves, 0, 0, values of
+ * K in one accumulator of an fp32 output), 0 for bad arguments.
+ */
+int diffattn_debug_product_plan(int kind, int M, int N, int K, int* plan);
+
+/*
  * Diagnostics: launches one CTA whose thread waits on an mbarrier that nothing
  * arrives on, with a budget of about `budget_ns` nanoseconds (1 .. 1e9; the
  * kernel counts 2 SM clock cycles per nanosecond).  The wait
