@@ -176,7 +176,7 @@ def lib() -> ctypes.CDLL:
             L.diffattn_debug_bounds_selftest.restype = i
             L.diffattn_debug_item_plan.argtypes = [i, ll, i, i, i, i, ll, vp, vp]
             L.diffattn_debug_item_plan.restype = i
-            L.diffattn_debug_product_plan.argtypes = [i, i, i, i, vp]
+            L.diffattn_debug_product_plan.argtypes = [i, i, i, i, i, vp]
             L.diffattn_debug_product_plan.restype = i
             L.diffattn_last_error.argtypes = []
             L.diffattn_last_error.restype = ctypes.c_char_p
@@ -1688,14 +1688,14 @@ def debug_item_plan(grid: int, units: int, nqt: int, qt0: int, n: int, causal: b
 PRODUCTS = {"linear": 0, "gated": 1, "da": 2, "dw": 3}
 
 
-def debug_product_plan(kind: str, M: int, N: int, K: int) -> dict:
+def debug_product_plan(kind: str, M: int, N: int, K: int, f32: bool = False) -> dict:
     """How a product [M, N] over a contraction of K would run (host only).
 
     kind: "linear", "gated" (N = F, K = D), "da" (dx too) or "dw".  Returns a dict: kernel ("few" or "tiles") and
-    its layout; segment: the values of K that one accumulator of an fp32 output sums.
+    its layout; segment: the values of K that one accumulator sums (f32: of an fp32 output).
     """
     plan = (ctypes.c_int * 6)()
-    form = lib().diffattn_debug_product_plan(PRODUCTS[kind], M, N, K, plan)
+    form = lib().diffattn_debug_product_plan(PRODUCTS[kind], M, N, K, 1 if f32 else 0, plan)
     if form == 1:
         return dict(kernel="few", cluster=plan[0], width=plan[1], tokens=plan[2], stages=plan[4], segment=plan[5])
     if form == 2:

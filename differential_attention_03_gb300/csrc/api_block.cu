@@ -219,7 +219,7 @@ int cluster_slots(int cs, int sms) {
 
 // How the products for few tokens lay their work out; nt = 0: linear_kernel's tiles suit it better.
 struct FewPlan {
-  int nt, width, cs, lg, stages, off_bars, smem;
+  int nt, width, cs, lg, stages, off_bars, turns, smem;
   long long tiles;
 };
 
@@ -243,6 +243,9 @@ FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms, doub
     const int nkb = (kblocks + cs - 1) / cs;
     for (int width = step; width <= most && width < p.N + step; width += step) {
       const int wrows = width * sides, lg = (width / 8 + cs - 1) / cs;
+      // fp32 outputs: segments of kLinSegBlocks, more than tensor memory has accumulators for, take turns in them.
+      const bool turns = q.epi == da::kEpiF32 && da::few_segment_blocks(nkb, wrows) > da::kLinSegBlocks;
+      if (turns && da::few_turns(wrows) == 0) continue;
       const long long tiles = ttiles * ((p.N + width - 1) / width);
       const double rounds = static_cast<double>((tiles + at_once - 1) / at_once);
       const double stream = rounds * nkb * std::max({(wrows + nt) * 128.0 / draw, (wrows + nt) * 128.0 * std::min<long long>(tiles, at_once) * cs / 32e6, 0.105});
@@ -257,7 +260,8 @@ FewPlan make_few_plan(const Product& q, const da::LinearParams& p, int sms, doub
       least = cost;
       best.nt = nt, best.width = width, best.cs = cs, best.lg = lg, best.stages = stages, best.tiles = tiles;
       best.off_bars = stages * stage + part;
-      best.smem = best.off_bars + (2 * stages + 1) * 8 + 16 + 1024;
+      best.turns = turns ? 1 : 0;
+      best.smem = best.off_bars + (2 * stages + 5) * 8 + 16 + 1024;
     }
   }
   return best;
@@ -271,18 +275,18 @@ struct Plan {
 // The plans of the sizes that this thread asked for last.
 Plan product_plan(const Product& q, const da::LinearParams& p, int sms) {
   struct Known {
-    int kind, M, N, K, sms;
+    int kind, epi, M, N, K, sms;
     Plan plan;
   };
   constexpr unsigned kEntries = 64;
   static thread_local Known known[kEntries];  // (sms = 0: none yet)
   const int kind = static_cast<int>(q.kind);
   const unsigned h = static_cast<unsigned>(p.M) * 2654435761u ^ static_cast<unsigned>(p.N) * 40503u ^ static_cast<unsigned>(p.K) * 9973u ^
-                     static_cast<unsigned>(kind) * 131u;
+                     static_cast<unsigned>(4 * kind + q.epi) * 131u;
   Known& k = known[(h >> 7) % kEntries];
-  if (k.sms != sms || k.kind != kind || k.M != p.M || k.N != p.N || k.K != p.K) {
+  if (k.sms != sms || k.kind != kind || k.epi != q.epi || k.M != p.M || k.N != p.N || k.K != p.K) {
     const TilePlan t = make_tile_plan(q, p, sms);
-    k = Known{kind, p.M, p.N, p.K, sms, {make_few_plan(q, p, sms, p.M > 128 ? t.cost : 1e30), t}};
+    k = Known{kind, q.epi, p.M, p.N, p.K, sms, {make_few_plan(q, p, sms, p.M > 128 ? t.cost : 1e30), t}};
   }
   return k.plan;
 }
@@ -307,7 +311,7 @@ diffattn_status launch_product(const char* fn, const Product& q, da::LinearParam
   const Plan plan = product_plan(q, p, sms);
   const FewPlan& f = plan.few;
   if (f.nt) {
-    p.nt = f.nt, p.width = f.width, p.cs = f.cs, p.lg = f.lg, p.stages = f.stages, p.off_bars = f.off_bars;
+    p.nt = f.nt, p.width = f.width, p.cs = f.cs, p.lg = f.lg, p.stages = f.stages, p.off_bars = f.off_bars, p.turns = f.turns;
     p.tiles_n = (p.N + f.width - 1) / f.width;
     if ((st = map_w(&p.tm_a, f.width)) != DIFFATTN_OK) return st;
     if ((st = map_x(&p.tm_b, f.nt)) != DIFFATTN_OK) return st;
@@ -393,20 +397,24 @@ size_t dtype_bytes(int dt) { return dt == DIFFATTN_F32 ? 4 : 2; }
 
 extern "C" {
 
-int diffattn_debug_product_plan(int kind, int M, int N, int K, int* plan) {
+int diffattn_debug_product_plan(int kind, int M, int N, int K, int f32, int* plan) {
   if (kind < 0 || kind > 3 || M < 1 || N < 1 || K < 1 || !plan) return 0;
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
   p.M = M, p.N = N, p.K = K;
-  const Product q = {static_cast<Kind>(kind), da::kEpiBf16, nullptr, nullptr, 0, 0};
+  const bool gated = static_cast<Kind>(kind) == Kind::kGated;
+  const Product q = {static_cast<Kind>(kind), gated ? da::kEpiGated : f32 ? da::kEpiF32 : da::kEpiBf16, nullptr, nullptr, 0, 0};
   const Plan x = product_plan(q, p, sms_or_default());
   const int cg = x.tile.cg;
   if (x.few.nt) {
-    const int row[6] = {x.few.cs, x.few.width, x.few.nt, x.few.lg, x.few.stages, da::few_segment(K, x.few.cs, x.few.width * (q.kind == Kind::kGated ? 2 : 1)) * da::kLinBK};
+    const int blocks = ((K + da::kLinBK - 1) / da::kLinBK + x.few.cs - 1) / x.few.cs;
+    const int seg = !f32 ? blocks : x.few.turns ? da::kLinSegBlocks : da::few_segment_blocks(blocks, x.few.width);
+    const int row[6] = {x.few.cs, x.few.width, x.few.nt, x.few.lg, x.few.stages, seg * da::kLinBK};
     memcpy(plan, row, sizeof(row));
     return 1;
   }
-  const int row[6] = {cg, static_cast<int>(x.tile.full), static_cast<int>(tile_count(q, p, cg) - x.tile.full), 0, 0, da::kLinSegBlocks * da::kLinBK};
+  const int row[6] = {cg, static_cast<int>(x.tile.full), static_cast<int>(tile_count(q, p, cg) - x.tile.full), 0, 0,
+                      f32 ? da::kLinSegBlocks * da::kLinBK : (K + da::kLinBK - 1) / da::kLinBK * da::kLinBK};
   memcpy(plan, row, sizeof(row));
   return 2;
 }

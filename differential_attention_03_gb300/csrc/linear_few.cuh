@@ -19,8 +19,14 @@
 //   warp 9      TMEM allocator and MMA issuer.
 // A programmatic dependent launch: the CTAs come up while the kernel before
 // them ends, and wait for its end before they touch global memory.
-// Results repeat bit for bit (no atomics).  kEpiF32 sums K segments in
-// accumulators of their own, for the tensor cores' truncation (see linear.cuh).
+// Results repeat bit for bit (no atomics).
+//
+// kEpiF32 sums segments of 512 values of K at most, for the tensor cores'
+// truncation (see linear.cuh): in accumulators of their own, where tensor memory
+// has room for all of them, else taking turns in one or two.  Warps 0-7 then add
+// each segment into running sums, in tensor memory too, while the next one's MMAs
+// run: 1 x 32768 x 8192 79 us (all 8192 values in one accumulator, which is off
+// by 3e-5, 79), 48 x 8192 x 8192 24.6 (24.0).
 #pragma once
 
 #include "linear.cuh"
@@ -56,8 +62,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   uint64_t* full = bars;
   uint64_t* empty = full + stages;
   uint64_t* done = empty + stages;  // every MMA completed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(done + 1) + 1;
+  uint64_t* acc_full = done + 1;       // [2] segments taking turns: the accumulator's MMAs completed
+  uint64_t* acc_empty = acc_full + 2;  // [2] ... it has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   // ---- work of this CTA: features, tokens, and its share of the contraction
   const int cs = p.cs, rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -66,10 +74,12 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
   const int kblocks = (p.K + kLinBK - 1) / kLinBK;
   // K blocks rank, rank + cs, ...: what a cluster reads at one time lies together in the weights' rows.
   const int nkb = (kblocks - rank + cs - 1) / cs;  // >= 1
-  const int seg = EPI == kEpiF32 ? few_segment_blocks(nkb, wrows) : nkb;  // K blocks an accumulator sums
+  const bool turns = EPI == kEpiF32 && p.turns;
+  const int seg = EPI != kEpiF32 ? nkb : turns ? kLinSegBlocks : few_segment_blocks(nkb, wrows);  // K blocks of a segment
   const int segs = (nkb + seg - 1) / seg;
+  const int accs = turns ? few_turns(wrows) : segs;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < static_cast<uint32_t>(segs * wrows)) tmem_cols *= 2;
+  while (tmem_cols < static_cast<uint32_t>((accs + (turns ? 1 : 0)) * wrows)) tmem_cols *= 2;
 
   if (cs > 1) cluster_arrive();  // (waited for below: every CTA of the cluster has started)
   int fill = 0, slot = 0;
@@ -102,6 +112,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         mbar_init(&empty[s], 1);
       }
       mbar_init(done, 1);
+      for (int a = 0; a < 2; ++a) {
+        mbar_init(&acc_full[a], 1);
+        mbar_init(&acc_empty[a], kFewEpiWarps);
+      }
       *abort_flag = 0;
       fence_mbar_init();
     }
@@ -138,11 +152,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     const uint64_t dW = sdesc_sw128(smem_u32(smem), W_MN ? 8192 : 16, 1024);
     constexpr int KW = W_MN ? 2048 : 32;
     const uint32_t idesc = idesc_bf16(128, 0, false, W_MN) | (static_cast<uint32_t>(wrows >> 3) << 17);
-    int s = 0, in_seg = 0;
+    int s = 0;
     bool landed = false;
-    uint32_t ph = 0, dacc = tmem;
-    for (int kb = 0; kb < nkb; ++kb) {
-      if (!__all_sync(0xffffffffu, landed) && !__all_sync(0xffffffffu, mbar_wait(&full[s], ph, ab))) break;
+    uint32_t ph = 0;
+    auto block = [&](uint32_t dacc, bool more) {  // one K block; more: onto what the accumulator holds
+      if (!__all_sync(0xffffffffu, landed) && !__all_sync(0xffffffffu, mbar_wait(&full[s], ph, ab))) return false;
       const int next = s + 1 == stages ? 0 : s + 1;
       landed = mbar_test(&full[next], next ? ph : ph ^ 1u);  // (known by the time that these MMAs are issued)
       tc_fence_after();
@@ -150,13 +164,32 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
 #pragma unroll
       for (int k = 0; k < kLinBK / 16; ++k)
         mma_ss_elect(dacc, dX + so + static_cast<uint64_t>((k * 32) >> 4), dW + so + static_cast<uint64_t>((k * KW) >> 4), idesc,
-                     (in_seg > 0 || k > 0) ? 1u : 0u);
+                     (more || k > 0) ? 1u : 0u);
       tc_commit_elect(&empty[s]);
       s = next;
       if (s == 0) ph ^= 1u;
-      if (++in_seg == seg) {
-        in_seg = 0;
-        dacc += static_cast<uint32_t>(wrows);
+      return true;
+    };
+    if (turns) {
+      bool ok = true;
+      int acc = 0;
+      uint32_t acc_ph = 1;  // (an accumulator's first segment waits for nothing)
+      for (int kb = 0; ok && kb < nkb; kb += seg) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_empty[acc], acc_ph, ab))) break;
+        const int to = min(seg, nkb - kb);
+        for (int i = 0; ok && i < to; ++i) ok = block(tmem + static_cast<uint32_t>(acc * wrows), i > 0);
+        tc_commit_elect(&acc_full[acc]);
+        if (++acc == accs) acc = 0, acc_ph ^= 1u;
+      }
+    } else {
+      int in_seg = 0;
+      uint32_t dacc = tmem;
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!block(dacc, in_seg > 0)) break;
+        if (++in_seg == seg) {
+          in_seg = 0;
+          dacc += static_cast<uint32_t>(wrows);
+        }
       }
     }
     tc_commit_elect(done);
@@ -191,17 +224,41 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     }
   };
   grid_dep_wait();
+  // groups of sixteen columns that a thread of warps 0-7 reads of its row: [first, last)
+  const int pairs = wrows >> 4, first = warp < 4 ? 0 : (pairs + 1) >> 1, last = warp < 4 ? (pairs + 1) >> 1 : pairs;
+  const int row = wq + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 16);
+  const uint32_t running = static_cast<uint32_t>(accs * wrows);  // columns of the running sums, behind the accumulators
+  if (turns && warp < kFewEpiWarps) {
+    int acc = 0;
+    uint32_t ph = 0;
+    for (int j = 0; j < segs; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], ph, ab))) break;
+      tc_fence_after();
+      for (int h = first; wq < mt && h < last; ++h) {
+        uint32_t a[16], b[16] = {};
+        tmem_ld16(tl + static_cast<uint32_t>(acc * wrows + 16 * h), a);
+        if (j > 0) tmem_ld16(tl + running + static_cast<uint32_t>(16 * h), b);
+        tmem_ld_wait16x2(a, b);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) + __uint_as_float(b[k]));
+        tmem_st16(tl + running + static_cast<uint32_t>(16 * h), a);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      if (++acc == accs) acc = 0, ph ^= 1u;
+    }
+  }
   fetch(threadIdx.x);
   const bool go = warp < kFewEpiWarps && __all_sync(0xffffffffu, mbar_wait(done, 0, ab));
   if (cs > 1) cluster_wait();
   if (go && wq < mt) {
     // ================================================================ accumulators to the CTAs that finish them
     tc_fence_after();
-    const uint32_t tl = tmem + (static_cast<uint32_t>(wq) << 16);
-    const int row = wq + lane;
     const uint32_t mine = smem_u32(part + (rank * p.nt + row) * row_floats);
-    // groups of eight columns of this half of the warps: pairs [first, last) of 16 columns
-    const int pairs = wrows >> 4, first = warp < 4 ? 0 : (pairs + 1) >> 1, last = warp < 4 ? (pairs + 1) >> 1 : pairs;
+    // groups of eight columns of this half of the warps
     int side = 0, g = 2 * first;
     if (SIDES == 2 && g >= groups) side = 1, g -= groups;
     int owner = g / lg, local = g - owner * lg;
@@ -233,15 +290,15 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         for (int j = 0; j < 16; ++j) a[j] = __float_as_uint(__uint_as_float(a[j]) + __uint_as_float(z[j]));
       }
     };
-    for (int h = first; h < last; h += 2) {  // 32 columns a wait
+    constexpr int STEP = EPI == kEpiF32 ? 1 : 2;  // 16 or 32 columns a wait (an fp32 residual's registers leave no room for 32)
+    const uint32_t from = turns ? tl + running : tl;
+    for (int h = first; h < last; h += STEP) {
       uint32_t a[16], b[16] = {};
-      tmem_ld16(tl + static_cast<uint32_t>(16 * h), a);
-      if (h + 1 < last) tmem_ld16(tl + static_cast<uint32_t>(16 * h + 16), b);
+      tmem_ld16(from + static_cast<uint32_t>(16 * h), a);
+      const bool more = STEP == 2 && h + 1 < last;
+      if (more) tmem_ld16(from + static_cast<uint32_t>(16 * h + 16), b);
       tmem_ld_wait16x2(a, b);
-      if (EPI == kEpiF32) {
-        add_segments(16 * h, a);
-        if (h + 1 < last) add_segments(16 * h + 16, b);
-      }
+      if (EPI == kEpiF32 && !turns) add_segments(16 * h, a);
       auto two = [&](const uint32_t* r) {
         if (row < mt) put(r);
         next();
@@ -249,7 +306,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         next();
       };
       two(a);
-      if (h + 1 < last) two(b);
+      if (more) two(b);
     }
   }
   tc_fence_before();

@@ -21,15 +21,14 @@ constexpr int kLinSegBlocks = 8;  // K blocks (512 values) that one accumulator 
 
 constexpr int kFewMaxSmem = 232448;
 
-// linear_few_kernel with fp32 outputs: K blocks that one accumulator of `wrows` columns sums, in the CTA of a cluster of cs
-// with the most of them.  A CTA has 256 columns of tensor memory (two CTAs share an SM's 512).
+// linear_few_kernel with fp32 outputs: K blocks that an accumulator of `wrows` columns sums where each segment has its own.
+// A CTA has 256 columns of tensor memory (two CTAs share an SM's 512).
 __host__ __device__ inline int few_segment_blocks(int blocks, int wrows) {
   const int most = 256 / wrows;
   return (blocks + most - 1) / most;
 }
-inline int few_segment(int K, int cs, int wrows) {
-  return few_segment_blocks(((K + kLinBK - 1) / kLinBK + cs - 1) / cs, wrows);
-}
+// Accumulators that segments of kLinSegBlocks take turns in, beside one accumulator's columns of running sums; 0: no room.
+__host__ __device__ inline int few_turns(int wrows) { return 3 * wrows <= 256 ? 2 : 2 * wrows <= 256 ? 1 : 0; }
 
 struct LinearParams {
   CUtensorMap tm_a;  // K-major: {K, M} box {64, 128}; MN-major: {M, K} box {64, 64}; 128-byte swizzle
@@ -47,6 +46,7 @@ struct LinearParams {
   // linear_few: features (gated: gate features) and token rows of a tile, CTAs that share its contraction, groups of
   // eight features that each of them finishes, ring slots, and where the barriers lie in shared memory
   int width, nt, cs, lg, stages, off_bars;
+  int turns;  // ... whether segments of kLinSegBlocks take turns in its accumulators (few_turns)
   int* status;
 };
 

@@ -945,13 +945,14 @@ int diffattn_debug_item_plan(int grid, long long units, int nqt, int qt0, int n,
  * would run, for the tests.  kind 0: diffattn_linear (M, N, K), 1:
  * diffattn_gated_linear (M, F, D), 2: da or dx of a backward pass (M, K, N; gated
  * M, D, 2 F), 3: dw (N, K, M; gated 2 F, D, M).
+ * f32: an fp32 output.
  * Returns 1 for the kernel for few tokens (plan: CTAs of a cluster, features of a
  * tile, tokens of a tile, groups of eight features that a CTA finishes, ring
- * slots, values of K in one accumulator of an fp32 output), 2 for the tiles
- * (plan: SMs of a cluster, whole tiles, tiles that come in halves, 0, 0, values of
- * K in one accumulator of an fp32 output), 0 for bad arguments.
+ * slots, values of K in one accumulator), 2 for the tiles (plan: SMs of a cluster,
+ * whole tiles, tiles that come in halves, 0, 0, values of K in one accumulator),
+ * 0 for bad arguments.
  */
-int diffattn_debug_product_plan(int kind, int M, int N, int K, int* plan);
+int diffattn_debug_product_plan(int kind, int M, int N, int K, int f32, int* plan);
 
 /*
  * Diagnostics: launches one CTA whose thread waits on an mbarrier that nothing

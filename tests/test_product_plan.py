@@ -41,3 +41,16 @@ def test_bad_sizes_have_no_plan():
     for sizes in ((0, 8, 8), (8, 0, 8), (8, 8, 0), (-1, 8, 8)):
         with pytest.raises(ValueError):
             da.debug_product_plan("linear", *sizes)
+
+
+def test_fp32_outputs_sum_512_values_in_an_accumulator():
+    """The tensor cores cut off as they add: 1e-9 relative a value, whatever the kernel and its layout."""
+    for M in (1, 2, 16, 17, 48, 100, 128, 129, 200, 256, 300, 512, 777, 2050):
+        for N in (8, 72, 512, 1000, 2048, 4096, 8192, 32768, 128256):
+            for K in (8, 72, 512, 520, 1000, 2048, 4096, 5472, 8192, 16384, 32768, 65536, 1048576):
+                p = da.debug_product_plan("linear", M, N, K, f32=True)
+                assert p["segment"] <= 512, (M, N, K, p)
+                if p["kernel"] == "few":
+                    assert p["width"] <= 256 and p["stages"] >= 1
+    assert da.debug_product_plan("dw", 264, 256, 8192, f32=True)["segment"] <= 512
+    assert da.debug_product_plan("linear", 1, 2048, 8192)["segment"] > 512  # (a bf16 output does not see it)
