@@ -270,7 +270,7 @@ __device__ __forceinline__ void add_bias(float* v, const float* bias, int cols) 
 #pragma unroll
   for (int q = 0; q < N / 4; ++q)
     if (4 * q < cols) {
-      const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + q);
+      const float4 b = reinterpret_cast<const float4*>(bias)[q];
       v[4 * q] += b.x;
       v[4 * q + 1] += b.y;
       v[4 * q + 2] += b.z;

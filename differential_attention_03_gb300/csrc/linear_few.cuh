@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     const int t = token_of(i), col = f0 + (rank * lg + i - t * ng) * 8;
     if (EPI == kEpiGated || i >= items || col >= p.N) return;
     if (p.bias) {
-      bias[0] = __ldg(reinterpret_cast<const float4*>(p.bias + col));
-      bias[1] = __ldg(reinterpret_cast<const float4*>(p.bias + col) + 1);
+      bias[0] = reinterpret_cast<const float4*>(p.bias + col)[0];
+      bias[1] = reinterpret_cast<const float4*>(p.bias + col)[1];
     }
     if (p.residual) {
       const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.residual) + ((t0 + t) * p.ldr + col) * (EPI == kEpiF32 ? 4 : 2));
