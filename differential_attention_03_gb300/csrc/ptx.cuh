@@ -472,6 +472,10 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // memory operations are visible.  grid_dep_launch_dependents() lets the next
 // such kernel be scheduled once every CTA of this grid has issued it (or
 // exited); it does not relax that wait.
+// A kernel that takes tensor memory issues it only when the CTA holds it: a
+// dependent may take its own before it waits, and one that got an SM's columns
+// ahead of the kernel it waits for would leave both waiting, with no time limit
+// on either (tcgen05.alloc, griddepcontrol.wait).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -163,7 +163,6 @@ template <int D, bool V2, int TP>
 __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeColsCfg<D, V2, TP>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NC = C::NC, COLS = C::COLS;
-  grid_dep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,6 +221,7 @@ __global__ void __launch_bounds__(640, 1) tree_cols_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch_dependents();  // (every CTA holds its tensor memory: ptx.cuh)
   const uint32_t tmem = *tmem_slot;
   const int count = start[3];
   const AbortState ab{abort_flag, p.status};

@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   using C = TreeRowsCfg<D, V2, FMT>;
   constexpr int DV = C::DV, BN = C::BN, NK = C::NK, NV = C::NV, NS = C::NS;
   static_assert(!SPLIT || FMT == kCacheFp8k, "only 8-bit keys with bf16 values stand twice");
-  grid_dep_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -207,6 +206,7 @@ __global__ void __launch_bounds__(640, 1) tree_rows_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch_dependents();  // (every CTA holds its tensor memory: ptx.cuh)
   const uint32_t tmem = *tmem_slot;
   const int count = start[3];
   const AbortState ab{abort_flag, p.status};

@@ -80,3 +80,39 @@ def test_weights_rows_and_residuals_of_the_product_before(M):
         for p, q in zip(one, two):
             assert torch.equal(p, q), i
     da.device_status()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("T", [1, 16])
+def test_products_behind_a_tree_decode(T, fmt):
+    """The attention of a serving step, W^O with the residual, the gated half, and the next step's attention behind it."""
+    rnd = _rnd(T)
+    B, n, H, d = 2, 640, 4, 64
+    D = 2 * H * d
+    cache = da.cache_v1(B, n, H, d, fmt)
+    lens = torch.full((B,), 600, device="cuda", dtype=torch.int32)
+    da.cache_append(cache, rnd(B, 600, H, d), rnd(B, 600, H, d), rnd(B, 600, H, 2 * d), lens=torch.zeros_like(lens))
+    lam = torch.full((1,), 0.3, device="cuda")
+    wo, wg, wd, wq = rnd(D, D, std=D ** -0.5), rnd(2 * 680, D, std=D ** -0.5), rnd(D, 680, std=680 ** -0.5), rnd(2 * H * d, D, std=D ** -0.5)
+    q0, x0 = rnd(B, T, 2, H, d), rnd(B, T, D)
+
+    def step(q, x, sync):
+        outs = []
+
+        def keep(t):
+            outs.append(t)
+            if sync:
+                torch.cuda.synchronize()
+            return t
+        for _ in range(4):
+            o = keep(da.tree_decode(q[:, :, 0].contiguous(), q[:, :, 1].contiguous(), cache, lam, 0.8, lens=lens))
+            x = keep(da.linear(o.view(B, T, D), wo, residual=x))
+            h = keep(da.gated_linear(x, wg))
+            x = keep(da.linear(h, wd, residual=x))
+            q = keep(da.linear(x, wq)).view(B, T, 2, H, d)
+        return outs
+    want = step(q0, x0, True)
+    for _ in range(5):
+        for i, (a, b) in enumerate(zip(step(q0, x0, False), want)):
+            assert torch.equal(a, b), i
+    da.device_status()

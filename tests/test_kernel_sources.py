@@ -23,3 +23,20 @@ def test_dependents_load_nothing_as_invariant(path):
     code = _code(path)
     for word in ("__ldg", "__restrict__", ".nc."):
         assert word not in code, (os.path.basename(path), word)
+
+
+KERNEL = re.compile(r"__global__.*?\n}\n", re.S)
+
+
+@pytest.mark.parametrize("path", [h for h in HEADERS if "tmem_alloc" in _code(h) and os.path.basename(h) != "ptx.cuh"],
+                         ids=os.path.basename)
+def test_dependents_start_when_tensor_memory_is_held(path):
+    """A kernel lets its dependents start only when its CTAs hold their tensor memory: a dependent takes its own before it
+    waits, and neither tcgen05.alloc nor griddepcontrol.wait has a time limit."""
+    kernels = [k for k in KERNEL.findall(_code(path)) if "tmem_alloc" in k]
+    assert kernels
+    for k in kernels:
+        if "grid_dep_launch_dependents()" in k:
+            taken = max(m.start() for m in re.finditer("tmem_alloc", k))
+            held = k.index("__syncthreads()", taken)
+            assert k.index("grid_dep_launch_dependents()") > held, os.path.basename(path)
