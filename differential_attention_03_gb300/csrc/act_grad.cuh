@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kActGradThreads) act_grad_kernel(const ActGrad
           pairs_of(in[k][IN > 2 ? 2 : 0], u);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint64_t slope = act_slope2<ACT>(g[j], value);
+            const uint64_t slope = act_slope2<ACT, false>(g[j], value);
             g[j] = mul2(mul2(dy[j], u[j]), slope);
             u[j] = mul2(dy[j], value);
           }
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kActGradThreads) act_grad_kernel(const ActGrad
             uint64_t z[4], value;
             pairs_of(in[k][IN > 1 ? 1 : 0], z);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dy[j] = mul2(dy[j], act_slope2<ACT>(z[j], value));
+            for (int j = 0; j < 4; ++j) dy[j] = mul2(dy[j], act_slope2<ACT, true>(z[j], value));
             if (DA_BOUNDS_V(row < p.M && col + 8 <= p.N, row)) *reinterpret_cast<uint4*>(p.dz + row * p.ldz + col) = rounded(dy);
           }
 #pragma unroll

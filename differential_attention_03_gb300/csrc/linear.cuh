@@ -286,7 +286,7 @@ __device__ __forceinline__ void epilogue_bf16(const LinearParams& p, float (&v)[
   if (p.pre) put_bf16_rows(stg, v, &p.tm_pre, c0, 0, r0, lane);
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
-      act_all<decltype(tag)::value, 64>(v);
+      act_all<decltype(tag)::value, 64, false>(v);
     });
   if (p.residual) {
     stage_free(lane);
@@ -322,7 +322,7 @@ __device__ __forceinline__ void epilogue_f32(const LinearParams& p, float (&v)[6
   if (p.pre) put_bf16_rows(stg, v, &p.tm_pre, c0, 0, r0, lane);
   if (p.act != DIFFATTN_ACT_NONE)
     with_act(p.act, [&](auto tag) {
-      act_all<decltype(tag)::value, 64>(v);
+      act_all<decltype(tag)::value, 64, true>(v);
     });
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
         if (p.pre) *reinterpret_cast<uint4*>(p.pre + row * p.ldp + col) = pack8(v);
         if (p.act != DIFFATTN_ACT_NONE)
           with_act(p.act, [&](auto tag) {
-            act_all<decltype(tag)::value, 8>(v);
+            act_all<decltype(tag)::value, 8, EPI == kEpiF32>(v);
           });
         if (p.residual) {
           float r[8];
