@@ -18,7 +18,7 @@
 #include "ptx.cuh"
 
 #undef DA_BOUNDS_FILE
-#define DA_BOUNDS_FILE 13
+#define DA_BOUNDS_FILE 17
 
 namespace da {
 

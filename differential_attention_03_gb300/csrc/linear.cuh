@@ -51,7 +51,7 @@
 #include "ptx.cuh"
 
 #undef DA_BOUNDS_FILE
-#define DA_BOUNDS_FILE 12
+#define DA_BOUNDS_FILE 16
 
 namespace da {
 

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
       landed = mbar_test(&full[next], next ? ph : ph ^ 1u);  // (known by the time that these MMAs are issued)
       tc_fence_after();
       const uint64_t so = static_cast<uint64_t>((s * stage_bytes) >> 4);
+      if (!DA_BOUNDS_V(dacc - tmem + static_cast<uint32_t>(wrows) <= tmem_cols, dacc)) return false;
 #pragma unroll
       for (int k = 0; k < kLinBK / 16; ++k)
         mma_ss_elect(dacc, dX + so + static_cast<uint64_t>((k * 32) >> 4), dW + so + static_cast<uint64_t>((k * KW) >> 4), idesc,
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
       if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[acc], ph, ab))) break;
       tc_fence_after();
       for (int h = first; wq < mt && h < last; ++h) {
+        if (!DA_BOUNDS_V(running + static_cast<uint32_t>(16 * h + 16) <= tmem_cols, h)) break;
         uint32_t a[16], b[16] = {};
         tmem_ld16(tl + static_cast<uint32_t>(acc * wrows + 16 * h), a);
         if (j > 0) tmem_ld16(tl + running + static_cast<uint32_t>(16 * h), b);
@@ -283,6 +285,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     };
     auto add_segments = [&](int c, uint32_t (&a)[16]) {
       for (int q = 1; q < segs; ++q) {
+        if (!DA_BOUNDS_V(static_cast<uint32_t>(q * wrows + c + 16) <= tmem_cols, q)) break;
         uint32_t z[16];
         tmem_ld16(tl + static_cast<uint32_t>(q * wrows + c), z);
         tmem_ld_wait16x2(a, z);
@@ -293,6 +296,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     constexpr int STEP = EPI == kEpiF32 ? 1 : 2;  // 16 or 32 columns a wait (an fp32 residual's registers leave no room for 32)
     const uint32_t from = turns ? tl + running : tl;
     for (int h = first; h < last; h += STEP) {
+      if (!DA_BOUNDS_V(from - tl + static_cast<uint32_t>(16 * min(h + STEP, last)) <= tmem_cols, h)) break;
       uint32_t a[16], b[16] = {};
       tmem_ld16(from + static_cast<uint32_t>(16 * h), a);
       const bool more = STEP == 2 && h + 1 < last;

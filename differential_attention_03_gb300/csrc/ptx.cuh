@@ -134,8 +134,8 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
 
 // Bounds-check build: a 32x32b tensor-memory access of `ncols` columns at
 // `taddr` must address this warp's quarter of the lanes (warp w of a
-// warpgroup: lanes 32 (w % 4) ..) and stay inside the 512 columns that every
-// kernel of this library allocates.
+// warpgroup: lanes 32 (w % 4) ..) and stay inside the 512 columns there are.
+// (linear_few_kernel, the one that allocates fewer, checks its own besides.)
 #define DA_TMEM_OK(taddr, ncols)                                                       \
   DA_BOUNDS_V(((taddr) >> 16) == 32u * ((threadIdx.x >> 5) & 3u) &&                  \
                   ((taddr) & 0xffffu) + static_cast<uint32_t>(ncols) <= 512u, (taddr))

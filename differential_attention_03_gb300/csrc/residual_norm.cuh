@@ -37,7 +37,7 @@
 #include "vec8.cuh"
 
 #undef DA_BOUNDS_FILE
-#define DA_BOUNDS_FILE 14
+#define DA_BOUNDS_FILE 18
 
 namespace da {
 

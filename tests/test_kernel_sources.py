@@ -40,3 +40,13 @@ def test_dependents_start_when_tensor_memory_is_held(path):
             taken = max(m.start() for m in re.finditer("tmem_alloc", k))
             held = k.index("__syncthreads()", taken)
             assert k.index("grid_dep_launch_dependents()") > held, os.path.basename(path)
+
+
+def test_bounds_sites_name_one_file():
+    """A failed check reports DA_BOUNDS_FILE * 100000 + line: every file has a number of its own."""
+    of = {}
+    for path in HEADERS:
+        for n in re.findall(r"#define DA_BOUNDS_FILE (\d+)", _code(path)):
+            if n != "0":
+                of.setdefault(int(n), []).append(os.path.basename(path))
+    assert of and all(len(files) == 1 for files in of.values()), of
