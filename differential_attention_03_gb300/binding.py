@@ -154,6 +154,8 @@ def lib() -> ctypes.CDLL:
             L.diffattn_linear.restype = i
             L.diffattn_linear_backward_workspace.argtypes = [i, i, i]
             L.diffattn_linear_backward_workspace.restype = sz
+            L.diffattn_linear_backward_workspace_for.argtypes = [i, i, i, i, i]
+            L.diffattn_linear_backward_workspace_for.restype = sz
             L.diffattn_linear_backward.argtypes = [i, i, i, vp, ll, vp, vp, ll, vp, i, vp, vp, i, vp, vp, sz, vp]
             L.diffattn_linear_backward.restype = i
             L.diffattn_gated_linear.argtypes = [i, i, i, vp, ll, vp, i, vp, ll, vp, vp]
@@ -1397,8 +1399,11 @@ def linear_train(a, w, bias=None, act: str = "none", residual=None, dtype=None, 
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(lib().diffattn_linear_backward_workspace(M, N, K))
+def linear_backward_workspace_bytes(M: int, N: int, K: int, act: str | None = None, bias: bool = True) -> int:
+    """Workspace of linear_backward; act=None: enough for any activation.  Without one only the bias gradient needs any."""
+    if act is None:
+        return int(lib().diffattn_linear_backward_workspace(M, N, K))
+    return int(lib().diffattn_linear_backward_workspace_for(M, N, K, _act_code(act), 1 if bias else 0))
 
 
 def _workspace(workspace, need, dev, like, stream):
@@ -1441,7 +1446,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     pre: what linear_train kept (not needed without an activation).  Returns a dict of da (bf16, like a), dw
     [N, K] (dw_dtype: fp32 or bf16) and, with bias, dbias (fp32 [N]); da=False / dw=False leave one out.
     Behind an activation the products take dy act'(pre) rounded to bf16.  out: None or a dict of tensors to
-    write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K) bytes.
+    write to; workspace: None or a tensor of linear_backward_workspace_bytes(M, N, K, act, bias) bytes.
     """
     dev, N, K, lead, M, lda = _product(a, w, "a", "w")
     raw = _here(dev, stream)
@@ -1460,7 +1465,7 @@ def linear_backward(a, w, dy, pre=None, act: str = "none", bias: bool = False, d
     if bias:
         want.append(("dbias", (N,), torch.float32))
     r = _grads(out, want, dev, a.device, stream)
-    need = linear_backward_workspace_bytes(M, N, K) if code or bias else 0
+    need = linear_backward_workspace_bytes(M, N, K, act, bool(bias)) if code or bias else 0
     ws = _workspace(workspace, need, dev, a, stream)
     _check(lib().diffattn_linear_backward(M, N, K, a.data_ptr(), lda, w.data_ptr(), dy.data_ptr(), ldy,
                                           pre.data_ptr() if code else None, code, _at(r, "da"), _at(r, "dw"),

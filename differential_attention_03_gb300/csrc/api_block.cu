@@ -371,6 +371,16 @@ int act_grad_chunks(int M, int N) {
   return static_cast<int>(std::max(1ll, std::min({want, most, 65535ll})));
 }
 
+// Row chunks of the bias gradient.  Up to 64 rows are one chunk, whose column sums need no second kernel (64 x 8192, gelu:
+// 5.9 us; 3.9 so; 128 x 1024 3.9, so 6.2).
+int bias_chunks(int M, int N) { return M <= 64 ? 1 : act_grad_chunks(M, N); }
+
+// Workspace of diffattn_linear_backward: the bias gradient's partial sums, then dz.
+size_t bias_parts_bytes(int M, int N) { return round256(static_cast<size_t>(bias_chunks(M, N)) * N * 4); }
+size_t linear_workspace(int M, int N, bool bent, bool dbias) {
+  return (dbias && bias_chunks(M, N) > 1 ? bias_parts_bytes(M, N) : 0) + (bent ? round256(static_cast<size_t>(M) * N * 2) : 0);
+}
+
 diffattn_status act_grad(const char* fn, const da::ActGradParams& p, bool gated, cudaStream_t s) {
   const cudaError_t e = da::launch_act_grad(p, gated, s);
   if (e != cudaSuccess) return cuda_fail(e, fn);
@@ -460,8 +470,12 @@ diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long ld
 }
 
 size_t diffattn_linear_backward_workspace(int M, int N, int K) {
-  if (M < 1 || N < 1 || K < 1) return 0;
-  return round256(static_cast<size_t>(M) * N * 2) + round256(static_cast<size_t>(act_grad_chunks(M, N)) * N * 4);
+  return diffattn_linear_backward_workspace_for(M, N, K, DIFFATTN_ACT_RELU, 1);
+}
+
+size_t diffattn_linear_backward_workspace_for(int M, int N, int K, diffattn_activation act, int dbias) {
+  if (M < 1 || N < 1 || K < 1 || bad_act(act)) return 0;
+  return linear_workspace(M, N, act != DIFFATTN_ACT_NONE, dbias != 0);
 }
 
 diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, long long lda, const void* w, const void* dy,
@@ -493,7 +507,7 @@ diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, lon
   if (da_ && (st = check_rows(fn, "w", w, K, K, 2)) != DIFFATTN_OK) return st;
   if ((st = check_rows(fn, "dy", dy, N, ldy, 2)) != DIFFATTN_OK) return st;
   if (bent && (st = check_rows(fn, "pre", pre, N, N, 2)) != DIFFATTN_OK) return st;
-  const size_t need = (bent || dbias) ? diffattn_linear_backward_workspace(M, N, K) : 0;
+  const size_t need = linear_workspace(M, N, bent, dbias != nullptr);
   if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != DIFFATTN_OK) return st;
   {
     const long long n = N, k = K;
@@ -511,12 +525,11 @@ diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, lon
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.dy = static_cast<const __nv_bfloat16*>(dy);
     p.pre = static_cast<const __nv_bfloat16*>(pre);
-    p.dz = reinterpret_cast<__nv_bfloat16*>(ws);
     p.ldy = ldy, p.ldp = N, p.ldz = N;
-    // Up to 64 rows are one chunk, whose column sums need no second kernel (64 x 8192, gelu: 5.9 us; 3.9 so; 128 x 1024
-    // 3.9, so 6.2).
-    p.M = M, p.N = N, p.act = act, p.chunks = dbias && M <= 64 ? 1 : act_grad_chunks(M, N);
-    p.part = !dbias || p.chunks == 1 ? dbias : reinterpret_cast<float*>(ws + round256(static_cast<size_t>(M) * N * 2));
+    p.M = M, p.N = N, p.act = act, p.chunks = dbias ? bias_chunks(M, N) : act_grad_chunks(M, N);
+    p.part = dbias;
+    if (dbias && p.chunks > 1) p.part = reinterpret_cast<float*>(ws), ws += bias_parts_bytes(M, N);
+    p.dz = bent ? reinterpret_cast<__nv_bfloat16*>(ws) : nullptr;
     if ((st = act_grad(fn, p, false, s)) != DIFFATTN_OK) return st;
     if (dbias && p.chunks > 1) {
       da::SumParts q;
@@ -524,7 +537,7 @@ diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, lon
       q.part[0] = p.part, q.dst[0] = dbias, q.width[0] = N, q.count[0] = p.chunks;
       if ((st = sum_parts(fn, q, s)) != DIFFATTN_OK) return st;
     }
-    if (bent) dz = ws, ldz = N;
+    if (bent) dz = p.dz, ldz = N;
   }
   if (da_ && (st = dgrad(fn, M, K, N, dz, ldz, w, da_, s)) != DIFFATTN_OK) return st;
   if (dw && (st = wgrad(fn, N, K, M, dz, ldz, a, lda, dw, dw_dt, s)) != DIFFATTN_OK) return st;
@@ -761,7 +774,7 @@ size_t diffattn_residual_norm_backward_workspace(int rows, int D, int gate_rows)
   if (rows < 1 || D < 1 || gate_rows < 0) return 0;
   const NormPlan n = norm_plan(rows, D, gate_rows);
   return 2 * round256(static_cast<size_t>(n.grid) * D * 4) +
-         (gate_rows > 0 && n.chunks > 1 ? round256(static_cast<size_t>(n.pieces) * D * 4) : 0);
+         (gate_rows > 0 && gate_rows < rows && n.chunks > 1 ? round256(static_cast<size_t>(n.pieces) * D * 4) : 0);
 }
 
 diffattn_status diffattn_residual_norm_backward(diffattn_dtype dt, diffattn_dtype stream_dt, int rows, int D,

@@ -819,11 +819,14 @@ diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long ld
  *   pre : z as the forward stored it (bf16); unused with DIFFATTN_ACT_NONE.
  *   da [M, K] bf16, dw [N, K] of dw_dt (bf16 or fp32), dbias fp32 [N], contiguous;
  *   any of them may be NULL (not wanted).
- *   workspace : at least diffattn_linear_backward_workspace(M, N, K) bytes, 256-byte aligned.
+ *   workspace : at least diffattn_linear_backward_workspace_for(M, N, K, act, dbias wanted)
+ *   bytes, 256-byte aligned (0: it may be NULL); without an activation there is no dz
+ *   to hold.  diffattn_linear_backward_workspace(M, N, K) bytes serve every call.
  * Behind an activation dz is rounded to bf16, the tensor cores' operand type,
  * for da and dw; dbias sums it in fp32.  Sums repeat bit for bit.
  */
 size_t diffattn_linear_backward_workspace(int M, int N, int K);
+size_t diffattn_linear_backward_workspace_for(int M, int N, int K, diffattn_activation act, int dbias);
 diffattn_status diffattn_linear_backward(int M, int N, int K, const void* a, long long lda, const void* w, const void* dy,
                                          long long ldy, const void* pre, diffattn_activation act, void* da, void* dw,
                                          diffattn_dtype dw_dt, float* dbias, void* workspace, size_t workspace_bytes,

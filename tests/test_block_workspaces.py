@@ -1,0 +1,57 @@
+"""Workspaces of the block's backward passes hold what a kernel writes there and nothing else (host only: every call below
+is refused for a later fault, so that nothing is launched)."""
+
+import pytest
+
+from differential_attention_03_gb300 import binding as da
+from .test_block_refusals import AT, WS, _linear_bwd, _norm_bwd, _off
+from .test_block_refusals import L  # noqa: F401  (the fixture)
+
+ACT = {"none": 0, "silu": 4}
+
+
+def _overlaps(L, status):
+    return status == da.ERR_SHAPE and b"overlap" in L.diffattn_last_error()
+
+
+@pytest.mark.parametrize("M,N,K", [(8192, 8192, 64), (65, 8, 8), (1000, 1304, 1000), (64, 512, 64), (1, 8, 8)])
+def test_sizes(L, M, N, K):  # noqa: F811
+    f = L.diffattn_linear_backward_workspace_for
+    every = L.diffattn_linear_backward_workspace(M, N, K)
+    dz = -(-M * N * 2 // 256) * 256
+    assert f(M, N, K, 0, 0) == 0
+    assert f(M, N, K, 4, 0) == dz
+    sums = f(M, N, K, 0, 1)  # partial column sums, of 32 rows or more each; up to 64 rows go straight to the gradient
+    assert sums == 0 if M <= 64 else 4 * N <= sums <= 4 * N * -(-M // 32) + 256
+    assert f(M, N, K, 4, 1) == dz + sums == every
+    assert f(M, N, K, 9, 1) == f(0, N, K, 0, 1) == 0
+    assert da.linear_backward_workspace_bytes(M, N, K) == every
+    assert da.linear_backward_workspace_bytes(M, N, K, "none", False) == 0
+    assert da.linear_backward_workspace_bytes(M, N, K, "none", True) == sums
+    assert da.linear_backward_workspace_bytes(M, N, K, "gelu", False) == dz
+
+
+def test_linear_backward_takes_what_it_needs(L):  # noqa: F811
+    f = L.diffattn_linear_backward_workspace_for
+    late = dict(dx=AT[2])  # (da over dy: found behind the workspace)
+    # up to 64 rows without an activation: none at all
+    assert _overlaps(L, _linear_bwd(L, M=64, act=0, pre=None, ws=None, room=0, **late))
+    for M, act, db in ((100, 0, AT[6]), (100, 4, AT[6]), (100, 4, None), (64, 4, AT[6])):
+        need = f(M, 256, 128, act, 1 if db else 0)
+        assert need > 0
+        assert _overlaps(L, _linear_bwd(L, M=M, act=act, db=db, room=need, **late))
+        assert _linear_bwd(L, M=M, act=act, db=db, room=need - 1, **late) == da.ERR_SHAPE and b"workspace" in L.diffattn_last_error()
+        assert _linear_bwd(L, M=M, act=act, db=db, ws=None, **late) == da.ERR_NULL
+        # no output may lie in what is used of it, and what lies behind is free
+        assert _overlaps(L, _linear_bwd(L, M=M, act=act, db=db, dx=_off(WS, need - 256)))
+
+
+def test_norm_backward_with_a_gate_a_row_needs_no_partial_gates(L):  # noqa: F811
+    f = L.diffattn_residual_norm_backward_workspace
+    for rows, D in ((700, 128), (1500, 512), (5000, 2048), (37, 33)):
+        assert f(rows, D, rows) == f(rows, D, 0)
+        assert f(rows, D, 1) >= f(rows, D, 0)
+    need = f(12, 256, 12)
+    late = dict(G=12, dx=AT[2])
+    assert _overlaps(L, _norm_bwd(L, room=need, **late))
+    assert _norm_bwd(L, room=need - 1, **late) == da.ERR_SHAPE and b"workspace" in L.diffattn_last_error()
