@@ -705,7 +705,7 @@ NormPlan norm_plan(int rows, int D, int gate_rows) {
   const int workers = norm_workers(h);
   n.groups = gate_rows > 0 && gate_rows < rows ? gate_rows : 1;
   n.group_rows = rows / n.groups;
-  const long long want = std::max<long long>(1, std::min<long long>((rows + workers - 1) / workers, 152 * norm_grad_per_sm(h)));
+  const long long want = std::max<long long>(1, std::min<long long>((rows + workers - 1ll) / workers, 152 * norm_grad_per_sm(h)));
   // A piece a CTA where groups are few; several smaller pieces a CTA where whole groups would leave CTAs unequal.
   const long long pieces = 2 * n.groups <= want ? want / n.groups : n.groups < 4 * want ? (4 * want + n.groups - 1) / n.groups : 1;
   const long long chunks = std::max(1ll, std::min(pieces, (n.group_rows + workers - 1) / workers));

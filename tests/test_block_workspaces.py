@@ -55,3 +55,10 @@ def test_norm_backward_with_a_gate_a_row_needs_no_partial_gates(L):  # noqa: F81
     late = dict(G=12, dx=AT[2])
     assert _overlaps(L, _norm_bwd(L, room=need, **late))
     assert _norm_bwd(L, room=need - 1, **late) == da.ERR_SHAPE and b"workspace" in L.diffattn_last_error()
+
+
+def test_norm_backward_spreads_the_most_rows_over_the_card(L):  # noqa: F811
+    """Sums of as many CTAs for 2^31 - 1 rows as for a million: the count of rows does not overflow on the way."""
+    f = L.diffattn_residual_norm_backward_workspace
+    for D in (1, 8, 33, 256, 512, 2048):
+        assert f(0x7fffffff, D, 0) == f(1 << 20, D, 0)
