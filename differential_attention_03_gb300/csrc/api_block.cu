@@ -291,14 +291,17 @@ Plan product_plan(const Product& q, const da::LinearParams& p, int sms) {
   return k.plan;
 }
 
+// Sizes of a product whose indexes, to the end of the last tile, do not fit 31 bits.
+bool past_31_bits(int M, int N, int K) {
+  return M + 2ll * da::kLinBM > 0x7fffffffll || 2ll * N + 2 * da::kLinBN > 0x7fffffffll || static_cast<long long>(K) + da::kLinBK > 0x7fffffffll;
+}
+
 // Descriptors, tiles, status word and launch of a product whose sizes and epilogue are in p.
 diffattn_status launch_product(const char* fn, const Product& q, da::LinearParams& p, cudaStream_t s) {
   diffattn_status st = dh::status_address(&p.status);
   if (st != DIFFATTN_OK) return st;
   const int sms = sms_or_default();
-  if (static_cast<long long>(p.M) + 2 * da::kLinBM > 0x7fffffffll || 2ll * p.N + 2 * da::kLinBN > 0x7fffffffll ||
-      static_cast<long long>(p.K) + da::kLinBK > 0x7fffffffll)
-    return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
+  if (past_31_bits(p.M, p.N, p.K)) return fail(DIFFATTN_ERR_SHAPE, "%s: too large", fn);
   const bool x_mn = q.kind == Kind::kWgrad, w_mn = x_mn || q.kind == Kind::kDgrad;
   const long long wrows = q.kind == Kind::kGated ? 2ll * p.N : p.N;
   auto map_w = [&](CUtensorMap* m, int box) {
@@ -366,8 +369,8 @@ bool too_large(int M, int N, int K) { return M > 0x7ffe0000 || N > 0x3fff0000 ||
 
 // Row chunks of the element-wise kernels: some eight CTAs an SM, at least 32 rows each.
 int act_grad_chunks(int M, int N) {
-  const long long across = (N + 255) / 256;
-  const long long want = (152 * 8 + across - 1) / across, most = (M + 31) / 32;
+  const long long across = (N + 255ll) / 256;
+  const long long want = (152 * 8 + across - 1) / across, most = (M + 31ll) / 32;
   return static_cast<int>(std::max(1ll, std::min({want, most, 65535ll})));
 }
 
@@ -408,7 +411,7 @@ size_t dtype_bytes(int dt) { return dt == DIFFATTN_F32 ? 4 : 2; }
 extern "C" {
 
 int diffattn_debug_product_plan(int kind, int M, int N, int K, int f32, int* plan) {
-  if (kind < 0 || kind > 3 || M < 1 || N < 1 || K < 1 || !plan) return 0;
+  if (kind < 0 || kind > 3 || M < 1 || N < 1 || K < 1 || !plan || past_31_bits(M, N, K)) return 0;
   da::LinearParams p;
   memset(&p, 0, sizeof(p));
   p.M = M, p.N = N, p.K = K;
@@ -705,7 +708,7 @@ NormPlan norm_plan(int rows, int D, int gate_rows) {
   const int workers = norm_workers(h);
   n.groups = gate_rows > 0 && gate_rows < rows ? gate_rows : 1;
   n.group_rows = rows / n.groups;
-  const long long want = std::max<long long>(1, std::min<long long>((rows + workers - 1ll) / workers, 152 * norm_grad_per_sm(h)));
+  const long long want = std::max<long long>(1, std::min<long long>((rows - 1ll + workers) / workers, 152 * norm_grad_per_sm(h)));
   // A piece a CTA where groups are few; several smaller pieces a CTA where whole groups would leave CTAs unequal.
   const long long pieces = 2 * n.groups <= want ? want / n.groups : n.groups < 4 * want ? (4 * want + n.groups - 1) / n.groups : 1;
   const long long chunks = std::max(1ll, std::min(pieces, (n.group_rows + workers - 1) / workers));
@@ -763,7 +766,7 @@ diffattn_status diffattn_residual_norm(diffattn_dtype dt, diffattn_dtype stream_
   int smem;
   const int per_sm = norm_ring(h, D * (xe + (residual ? se : 0) + (gate && p.group_rows == 1 ? 4 : 0)), 0,
                                std::max(1, std::min(16, fit / h.threads)), &p.stages, &smem);
-  const int grid = static_cast<int>(std::min<long long>((rows + workers - 1ll) / workers, static_cast<long long>(sms_or_default()) * per_sm));
+  const int grid = static_cast<int>(std::min<long long>((rows - 1ll + workers) / workers, static_cast<long long>(sms_or_default()) * per_sm));
   const cudaError_t e = launch_norm(p, h, dt, stream_dt, false, grid, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn);
   dh::count_launches(1);

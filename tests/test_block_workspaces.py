@@ -62,3 +62,14 @@ def test_norm_backward_spreads_the_most_rows_over_the_card(L):  # noqa: F811
     f = L.diffattn_residual_norm_backward_workspace
     for D in (1, 8, 33, 256, 512, 2048):
         assert f(0x7fffffff, D, 0) == f(1 << 20, D, 0)
+
+
+def test_sizes_near_2_to_the_31(L):  # noqa: F811
+    """Column sums of the most rows: as many chunks as any other long tensor's.  Plans of sizes past 31 bits are refused."""
+    f = L.diffattn_linear_backward_workspace_for
+    assert f(0x7fffffff, 264, 8, 0, 1) == f(1 << 20, 264, 8, 0, 1)
+    assert f(100, 0x7ffffff8, 8, 0, 1) == 0  # (so many columns that one chunk fills the card: straight to the gradient)
+    for sizes in ((0x7fffffff, 8, 8), (8, 0x7ffffff8, 8), (8, 8, 0x7ffffff8)):
+        with pytest.raises(ValueError):
+            da.debug_product_plan("linear", *sizes)
+    assert da.debug_product_plan("linear", 0x7fff0000, 8, 8)["kernel"] in ("few", "tiles")
