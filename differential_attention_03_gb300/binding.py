@@ -1593,11 +1593,13 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     s = residual + scale * gate * p, y = s / rms(s) * gamma, over the last dimension (1 to 8192).
     x: [..., D] bf16 or fp32; residual: like x, or fp32 beside a bf16 x; gate: fp32 [D], like x, or
     [G, D] where G divides x's rows (G sequences: each its own row); gammas: fp32 [D] or None (ones).  norm=False: without the second norm.
-    stream_dtype: the type of s where there is no residual (default x's).  out: s, which may be residual
+    stream_dtype: the type of s (default the residual's or out's, else x's).  out: s, which may be residual
     itself.  Returns (y, s); y is None without the second norm.
     """
     xdt = x.dtype
     sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or xdt)
+    if stream_dtype is not None and stream_dtype is not sdt:
+        raise ValueError(f"stream_dtype is {stream_dtype}, the {'residual' if residual is not None else 'out'} given is {sdt}")
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, sdt, gate, gamma_post, gamma)
     raw = _here(dev, stream)
     shape = x.shape
