@@ -1557,6 +1557,8 @@ def _gate_rows(gate, x, dev) -> int:
         n = x.shape[:-1].numel()
     elif gate.dim() == 2:
         n = gate.shape[0]
+        if n == 0 and x.shape[:-1].numel() > 0:
+            raise ValueError(f"gate has no rows, x {tuple(x.shape)} has")
     else:
         raise ValueError(f"gate must be [D], [G, D] or like x {tuple(x.shape)}, got {tuple(gate.shape)}")
     _on(gate, "gate", torch.float32, gate.shape[:-1] + (D,), dev)
