@@ -1641,12 +1641,14 @@ def residual_norm_backward_workspace_bytes(rows: int, D: int, gate_rows: int = 0
 
 
 def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0, gamma_post=None, post=None, gamma=None,
-                           eps: float = 1e-5, out=None, workspace=None, stream=None) -> dict:
+                           eps: float = 1e-5, out=None, workspace=None, stream=None, dx: bool = True, dresidual: bool = True,
+                           dgate: bool = True, dgammas: bool = True) -> dict:
     """Gradients of residual_norm from x, the s it returned, dy (like y) and ds (like s; either may be None).
 
     Returns a dict of dx, dresidual (like s), and of those that apply: dgate (like gate), dgamma_post (post),
-    dgamma (with dy), fp32.  out: None or a dict of tensors to write to (dresidual may be ds); workspace:
-    None or a tensor of residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
+    dgamma (with dy), fp32; dx=False, dresidual=False, dgate=False and dgammas=False leave theirs out.  out:
+    None or a dict of tensors to write to (dresidual may be ds); workspace: None or a tensor of
+    residual_norm_backward_workspace_bytes(rows, D, gate rows) bytes.
     """
     dev, D, rows, dt, sd, gate_rows = _norm_args(x, s.dtype, gate, gamma_post, gamma)
     raw = _here(dev, stream)
@@ -1656,18 +1658,22 @@ def residual_norm_backward(x, s, dy=None, ds=None, gate=None, scale: float = 1.0
         _on(dy, "dy", x.dtype, x.shape, dev)
     if ds is not None:
         _on(ds, "ds", s.dtype, x.shape, dev)
-    want = [("dx", x.shape, x.dtype), ("dresidual", x.shape, s.dtype)]
-    if gate is not None:
+    want = []
+    if dx:
+        want.append(("dx", x.shape, x.dtype))
+    if dresidual:
+        want.append(("dresidual", x.shape, s.dtype))
+    if gate is not None and dgate:
         want.append(("dgate", gate.shape, torch.float32))
-    if post:
+    if post and dgammas:
         want.append(("dgamma_post", (D,), torch.float32))
-    if dy is not None:
+    if dy is not None and dgammas:
         want.append(("dgamma", (D,), torch.float32))
     r = _grads(out, want, dev, x.device, stream)
     ws = _workspace(workspace, residual_norm_backward_workspace_bytes(rows, D, gate_rows), dev, x, stream)
     _check(lib().diffattn_residual_norm_backward(dt, sd, rows, D, x.data_ptr(), s.data_ptr(), _addr(dy), _addr(ds),
                                                  _addr(gate), gate_rows, scale, 1 if post else 0, _addr(gamma_post),
-                                                 _addr(gamma), eps, r["dx"].data_ptr(), r["dresidual"].data_ptr(),
+                                                 _addr(gamma), eps, _at(r, "dx"), _at(r, "dresidual"),
                                                  _at(r, "dgate"), _at(r, "dgamma_post"), _at(r, "dgamma"),
                                                  _addr(ws), 0 if ws is None else ws.nbytes, raw))
     return r
