@@ -116,3 +116,38 @@ def test_products_behind_a_tree_decode(T, fmt):
         for i, (a, b) in enumerate(zip(step(q0, x0, False), want)):
             assert torch.equal(a, b), i
     da.device_status()
+
+
+def test_two_streams_at_once():
+    """Products for few tokens (clusters, tensor memory shared by two CTAs of an SM), tiles, norms and gradients of two streams
+    beside each other: each gives what it gives alone."""
+    sides = []
+    for k, M in ((0, 24), (1, 130)):
+        rnd = _rnd(k)
+        D, F = 1024, 2056
+        x, w, wg, wd, bias = rnd(M, D), rnd(D, D, std=D ** -0.5), rnd(2 * F, D, std=D ** -0.5), rnd(D, F, std=F ** -0.5), rnd(D, dtype=F32)
+        big, wide = rnd(1300, D), rnd(2312, D, std=D ** -0.5)
+
+        def work(s, x=x, w=w, wg=wg, wd=wd, bias=bias, big=big, wide=wide):
+            y, r = da.residual_norm(x, stream=s)
+            a = da.linear(y, w, bias=bias, act="gelu", residual=r, stream=s)
+            f = da.linear(a, wide, dtype=F32, stream=s)
+            h, gu = da.gated_linear_train(a, wg, stream=s)
+            o = da.linear(h, wd, residual=a, stream=s)
+            b = da.linear(big, wide, act="silu", stream=s)
+            g = da.gated_linear_backward(a, wg, gu, h, stream=s)
+            n = da.residual_norm_backward(x, r, o, a, stream=s)
+            return [y, r, a, f, h, o, b, *g.values(), *n.values()]
+        want = work(None)
+        torch.cuda.synchronize()
+        sides.append((torch.cuda.Stream(), work, want))
+    outs = [[], []]
+    for _ in range(30):
+        for k, (s, work, _) in enumerate(sides):
+            outs[k].append(work(s))
+    torch.cuda.synchronize()
+    for k, (_, _, want) in enumerate(sides):
+        for got in outs[k]:
+            for i, (p, q) in enumerate(zip(got, want)):
+                assert torch.equal(p, q), (k, i)
+    da.device_status()
