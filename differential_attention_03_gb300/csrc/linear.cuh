@@ -119,6 +119,10 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// The limit of a wait for an accumulator of `blocks` K blocks: a wait's own, and 4096 cycles a block (they take 270 to 450;
+// from some 5 million blocks on, a weight gradient over 300 million rows, the contraction alone would pass the limit).
+__device__ __forceinline__ uint64_t blocks_budget(int blocks) { return kWaitBudgetCycles + static_cast<uint64_t>(blocks) * 4096u; }
+
 // ----------------------------------------------------------------- layout
 // Epilogue warps: kEpiF32 holds sums in registers, 64 columns a thread (128 would spill: a warp may have 168).
 __host__ __device__ constexpr int linear_epi_warps(int epi) { return epi == kEpiF32 ? 16 : 8; }
@@ -542,8 +546,9 @@ __global__ void __launch_bounds__(LinearCfg<CG, A_MN, B_MN, EPI>::NTHREADS, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     uint8_t* stg = smem + C::OFF_STAGING + warp * 4096;
     const uint32_t empty0 = CG == 2 ? map_to_rank(&acc_empty[0], 0) : 0;
+    const uint64_t wait_budget = EPI == kEpiF32 ? kWaitBudgetCycles : blocks_budget(kblocks);
     auto acc_wait = [&](long long i) -> bool {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, ab));
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, ab, wait_budget));
       tc_fence_after();
       return got;
     };

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) linear_few_kernel(const __grid
     }
   }
   fetch(threadIdx.x);
-  const bool go = warp < kFewEpiWarps && __all_sync(0xffffffffu, mbar_wait(done, 0, ab));
+  const bool go = warp < kFewEpiWarps && __all_sync(0xffffffffu, mbar_wait(done, 0, ab, blocks_budget(nkb)));
   if (cs > 1) cluster_wait();
   if (go && wq < mt) {
     // ================================================================ accumulators to the CTAs that finish them
