@@ -6,7 +6,7 @@
 //
 // dz (and [dg | du]) leave in bf16, the operand type of the products that
 // follow.  HBM-bound: 6 bytes a value of z (gated 10); 8192 x 8192, gelu, with
-// dbias 67 us (6.0 TB/s), 8192 x 2 x 5464 97 (4.6; what lies in L2 aside).  A warp owns 256
+// dbias 69 us (5.8 TB/s; silu 67), 8192 x 2 x 5464 97 (4.6; what lies in L2 aside).  A warp owns 256
 // neighbouring columns (16 bytes a lane and tensor) and every eighth row of
 // its CTA's chunk; the column sums stay in registers, are joined over the CTA's
 // warps in shared memory and over the chunks by sum_parts_kernel, both in a

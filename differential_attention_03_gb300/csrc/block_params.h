@@ -23,7 +23,8 @@ struct ActGradParams {
   int M, N, act, chunks;     // chunks: of rows (gridDim.y)
 };
 
-// dst[j] = sum_c part[c][j] in the order of c, for up to three tensors at once.
+// dst[j] = sum_c part[c][j] for up to three tensors at once, in a fixed order: every 32nd row by one warp, these 32 sums in
+// a butterfly.
 struct SumParts {
   const float* part[3];
   float* dst[3];

@@ -1,7 +1,8 @@
 // The products of linear.cuh for few tokens (sm_103a): the weights stream
-// through once, so HBM (or L2) bounds them, not the tensor cores.  Weights from
-// HBM: 1 x 2048 x 2048 4.5 us (two of them the call's), 1 x 8192 x 2048 9.0,
-// 16 x 8192 x 8192 26.8 (5.0 TB/s), 48 x 2048 x 2 x 5464 10.7, 512 x 2048 x 2048 8.2.
+// through once, so HBM (or L2) bounds them, not the tensor cores.  Replayed from a
+// graph, weights from HBM: 1 x 2048 x 2048 4.5 us (two of them the call's; from L2
+// 3.6 to 4.0), 1 x 8192 x 2048 8.8, 16 x 8192 x 8192 22.9 (5.9 TB/s), 48 x 2048 x 2
+// x 5464 10.2 to 11.0 (from L2 7.4 to 9.2), 512 x 2048 x 2048 8.0.
 //
 // A CTA owns `width` features (the MMA's columns; gated: width gate rows and
 // their up rows) of up to 128 tokens (its rows; only p.nt of them are loaded, and
@@ -25,8 +26,11 @@
 // truncation (see linear.cuh): in accumulators of their own, where tensor memory
 // has room for all of them, else taking turns in one or two.  Warps 0-7 then add
 // each segment into running sums, in tensor memory too, while the next one's MMAs
-// run: 1 x 32768 x 8192 79 us (all 8192 values in one accumulator, which is off
-// by 3e-5, 79), 48 x 8192 x 8192 24.6 (24.0).
+// run: 1 x 32768 x 8192 81.5 us (bf16 out 80.5), 48 x 8192 x 8192 24.9 (23.3), 256 x
+// 4096 x 16384 42.6 (37.5).  With all 8192 values in one accumulator results were
+// off by 3e-5.  Not kept: narrower features in place of turns (88.9 and 29.7 us of
+// the first two), running sums in shared memory (83.6 and 24.6, but the ring lost
+// slots to them: 52.9 of the third).
 #pragma once
 
 #include "linear.cuh"

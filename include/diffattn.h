@@ -806,6 +806,9 @@ typedef enum {
  *   of out_dt (row stride ldr) or NULL.  residual may be out (in place).
  *   pre : bf16 [M, N] contiguous or NULL; z as diffattn_linear_backward needs it.
  * Accumulation, bias, activation and residual in fp32, one rounding an output.
+ * An fp32 output sums 512 values of K in a tensor-core accumulator at most (they
+ * cut off as they add: 1e-9 relative a value) and those sums to nearest, whatever
+ * the sizes; a bf16 output all of K in one.
  * M = 0 or N = 0 is a no-op.  out_dt not bf16 or fp32, an unknown activation -> ERR_DTYPE.
  */
 diffattn_status diffattn_linear(int M, int N, int K, const void* a, long long lda, const void* w, const float* bias,
