@@ -381,12 +381,15 @@ __global__ void __launch_bounds__(LAYOUT == kRing || LAYOUT == kPlain ? 512 : 25
         k = kept[kKeep ? i : 0];
       else
         column(c, k, group);
+      // (normed before gamma and the gate, which may take a large element past fp32)
+#pragma unroll
+      for (int j = 0; j < R::N; ++j) v[i].v[j] = R::mul(v[i].v[j], mm);
       if (row_gate) {
 #pragma unroll
         for (int j = 0; j < R::N; ++j) v[i].v[j] = R::mul(v[i].v[j], w[i].v[j]);
       }
 #pragma unroll
-      for (int j = 0; j < R::N; ++j) v[i].v[j] = R::fma(R::mul(v[i].v[j], k.v[j]), mm, r[i].v[j]);
+      for (int j = 0; j < R::N; ++j) v[i].v[j] = R::fma(v[i].v[j], k.v[j], r[i].v[j]);
       q += v[i].square();
       if (p.s_out && DA_BOUNDS_V(row < p.rows && c + VEC <= p.D, row)) v[i].store(static_cast<TS*>(p.s_out) + at + c);
     }

@@ -71,3 +71,24 @@ def test_gradients_of_rows_of_large_elements(D, types, gates, post):
     # the rows' own gradients are not lost beside zeros
     assert float(got["dx"][2::7].abs().float().mean()) > 0.05 and float(got["dresidual"][5::7].abs().float().mean()) > 0.05
     da.device_status()
+
+
+@pytest.mark.parametrize("D", WIDTHS)
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("gates", [0, 1, ROWS])
+def test_elements_near_the_types_largest(D, types, gates):
+    """Elements of 2.5e38 are normed before gamma and the gate, above one here, multiply them."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    dt, sdt = TYPES[types]
+    x = (2.5e38 * (1 - 0.2 * torch.rand(ROWS, D, generator=g, device="cuda"))).to(dt)
+    x[::3] = torch.randn(x[::3].shape, generator=g, device="cuda").to(dt)
+    gate = None if gates == 0 else 2 + torch.rand(gates, D, generator=g, device="cuda")
+    gp, ga = (3 + torch.rand(D, generator=g, device="cuda") for _ in range(2))
+    res = torch.randn(ROWS, D, generator=g, device="cuda").to(sdt)
+    y, s = da.residual_norm(x, res, gate=gate, scale=0.5, gamma_post=gp, gamma=ga)
+    assert torch.isfinite(y).all() and torch.isfinite(s).all()
+    _check_norm(x, res, gate, gp, ga, 0.5, y, s)
+    got = da.residual_norm_backward(x, s, res.to(dt), res, gate=gate, scale=0.5, gamma_post=gp, gamma=ga)
+    assert all(torch.isfinite(t).all() for t in got.values())
+    _check_norm_backward(x, s, res.to(dt), res, gate, gp, ga, 0.5, got)
+    da.device_status()
