@@ -1596,7 +1596,7 @@ def residual_norm(x, residual=None, gate=None, scale: float = 1.0, gamma_post=No
     x: [..., D] bf16 or fp32; residual: like x, or fp32 beside a bf16 x; gate: fp32 [D], like x, or
     [G, D] where G divides x's rows (G sequences: each its own row); gammas: fp32 [D] or None (ones).  norm=False: without the second norm.
     stream_dtype: the type of s (default the residual's or out's, else x's).  out: s, which may be residual
-    itself.  Returns (y, s); y is None without the second norm.
+    itself.  eps of 0 or less selects 1e-5.  Returns (y, s); y is None without the second norm.
     """
     xdt = x.dtype
     sdt = residual.dtype if residual is not None else out.dtype if out is not None else (stream_dtype or xdt)
